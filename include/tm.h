@@ -65,7 +65,8 @@ typedef enum tm_status {
     TM_ERR_BROKEN_PROMISE = 4,   /* TM_ALIGNED while M % TM != 0 or N % TN != 0 */
     TM_ERR_CUDA = 5,             /* a CUDA runtime call or kernel launch failed */
     TM_ERR_WORKSPACE = 6,        /* workspace NULL, too small or misaligned (colsum: 16 bytes, gemm: 1024) */
-    TM_ERR_TIMEOUT = 7           /* a bounded device-side wait gave up (reported by tm_check) */
+    TM_ERR_TIMEOUT = 7,          /* a bounded device-side wait gave up (reported by tm_check) */
+    TM_ERR_INDEX = 8             /* a page, slot or length read on the device is out of range (reported by tm_check) */
 } tm_status;
 
 /* A cudaStream_t, passed as an opaque pointer; NULL = legacy default stream. */
@@ -409,10 +410,217 @@ tm_status tm_gemm(const float *A, int64_t lda, const float *B, int64_t ldb, floa
                   int32_t TK, uint32_t flags, void *workspace, size_t ws_bytes, tm_stream_t stream);
 
 /*
+ * Operators of a transformer block, around its matrix products
+ * ------------------------------------------------------------
+ * Elements.  Tensors are fp32, fp16 or bf16 (TM_F32, TM_F16, TM_BF16; one type
+ *           for all activations of a call), passed as void*.  All sums, norms
+ *           and softmax statistics are fp32; an output is rounded once, to
+ *           nearest.  Strides count elements.  16-byte aligned tensors whose
+ *           strides are whole 16-byte vectors take vector accesses, others
+ *           single elements: the results are the same.
+ * Flags.    TM_PDL everywhere; the others are named at each entry point.
+ * Device data.  Positions, slots, page tables and lengths are read on the
+ *           device.  One that is out of range is never followed: the work it
+ *           names is left out (or, for a page of the attention, taken from
+ *           page 0) and the next tm_check returns TM_ERR_INDEX.
+ */
+#define TM_F32 0
+#define TM_F16 1
+#define TM_BF16 2
+#define TM_E4M3 3 /* 8-bit floats, 4 exponent and 3 mantissa bits, largest 448 (outputs only) */
+
+/*
+ * tm_rmsnorm -- root-mean-square norm of each row, after an optional addition:
+ *   h = x + r,   y_j = h_j * w_j / sqrt(mean_j h_j^2 + eps).
+ *   X, ldx     device input [M, N] of xtype
+ *   R, ldr     the residual stream, or NULL
+ *   H, ldh     output h (rounded to xtype; the statistics use it unrounded), or
+ *              NULL.  H may be X or R (same ld): the addition in place
+ *   W          N weights of wtype (xtype or TM_F32), or NULL for ones
+ *   Y, ldy     output, of ytype: xtype (may be X or R, same ld) or TM_E4M3
+ *   scales     TM_E4M3 only (else NULL): fp32, what a code of 1 stands for.
+ *              group == 0: one a row, [M]; group 32, 64 or 128: one for each
+ *              run of that many columns (the last may be short),
+ *              [M, ceil(N / group)].  scale = max|y| / 448 over its values (1
+ *              where they are all 0), code = y * (448 / max|y|) rounded to
+ *              nearest even
+ *   rstd       output [M] fp32, 1 / sqrt(mean h^2 + eps), for the gradient, or NULL
+ * N <= 32768.  Overlaps other than those named are refused.
+ * Errors: INVALID_ARG (also eps < 0 or NaN, scales without TM_E4M3 or missing
+ *         with it), UNSUPPORTED_TILE (group, N), MISALIGNED (a pointer not
+ *         aligned to its element), CUDA.
+ */
+tm_status tm_rmsnorm(const void *X, int64_t ldx, const void *R, int64_t ldr, void *H, int64_t ldh, const void *W,
+                     int64_t M, int64_t N, float eps, void *Y, int64_t ldy, float *scales, float *rstd,
+                     int32_t xtype, int32_t wtype, int32_t ytype, int32_t group, uint32_t flags,
+                     tm_stream_t stream);
+
+/*
+ * tm_rmsnorm_bwd -- the gradient of tm_rmsnorm.  With n = h * rstd:
+ *   DX = rstd * (dy * w - n * mean_j(dy * w * n)) + DR,   DW = sum over rows of dy * n.
+ * DX is the gradient of x and of r alike.
+ *   DY, lddy   gradient of y [M, N] of xtype
+ *   H, ldh     the forward pass's h (X itself where nothing was added)
+ *   W, rstd    as in the forward pass
+ *   DR, lddr   gradient that reaches h from the residual stream, or NULL
+ *   DX, lddx   output [M, N]; may be DY, H or DR (same ld)
+ *   DW         output [N] of wtype, or NULL; M == 0 gives zeros
+ *   workspace, ws_bytes   with DW: tm_rmsnorm_bwd_workspace_bytes(M, N) bytes,
+ *              16-byte aligned; in use until the call's kernels finish
+ * The rows' shares of DW are added in a fixed order.
+ * Errors: as tm_rmsnorm, and WORKSPACE.
+ */
+size_t tm_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t N);
+tm_status tm_rmsnorm_bwd(const void *DY, int64_t lddy, const void *H, int64_t ldh, const void *W, const float *rstd,
+                         const void *DR, int64_t lddr, void *DX, int64_t lddx, void *DW, int64_t M, int64_t N,
+                         int32_t xtype, int32_t wtype, void *workspace, size_t ws_bytes, uint32_t flags,
+                         tm_stream_t stream);
+
+/*
+ * Rotary positions.  A head's first `rot` dims form rot/2 pairs; pair i of a
+ * token at position p is turned by the angle p * f_i:
+ *   (a, b) -> gain * (a cos - b sin, a sin + b cos).
+ * The half layout pairs dims (i, i + rot/2), TM_ROPE_INTERLEAVED (2i, 2i + 1).
+ * f_i is given as turns a position in units of 2^-64: the fraction of a turn,
+ * p * turns_i mod 2^64, is then exact at any position, positive or negative.
+ *
+ * tm_rope_turns -- fills the HOST array turns[rot/2] (64-bit unsigned values)
+ * for f_i = base^(-2i/rot) radians, scaled for contexts longer than the
+ * `orig` positions a model was trained on:
+ *   TM_ROPE_PLAIN    f_i
+ *   TM_ROPE_LINEAR   f_i / factor
+ *   TM_ROPE_BASE     base * factor^(rot / (rot - 2)) in the place of base
+ *   TM_ROPE_BY_TURNS by the turns n_i = orig * f_i / 2pi that pair i makes
+ *                    within orig positions: f_i / factor below `low` turns, f_i
+ *                    above `high`, and between them the mean of both weighted
+ *                    by (n_i - low) / (high - low)
+ *   TM_ROPE_BY_DIM   the same two ends, weighted linearly in the pair's index
+ *                    between the (real) indices at which n_i = high and n_i = low,
+ *                    rounded down and up to whole ones
+ * Host only.  Errors: INVALID_ARG (rot odd or < 2, base <= 1, factor < 1, and
+ * for the last two orig <= 0 or not 0 < low < high), and TM_ROPE_BASE with rot 2.
+ */
+#define TM_ROPE_PLAIN 0
+#define TM_ROPE_LINEAR 1
+#define TM_ROPE_BASE 2
+#define TM_ROPE_BY_TURNS 3
+#define TM_ROPE_BY_DIM 4
+#define TM_ROPE_INTERLEAVED 0x400u
+#define TM_ROPE_INVERSE 0x800u
+tm_status tm_rope_turns(uint64_t *turns, int32_t rot, float base, int32_t scaling, float factor, float low, float high,
+                        int64_t orig);
+
+/*
+ * tm_rope -- rotate the heads of T tokens; dims from `rot` on are copied.
+ *   X, Y       [T, H, D]: token t's head h starts at X + t*xs_tok + h*xs_head,
+ *              its dims are contiguous.  Y may be X (same strides).  Queries and
+ *              keys of one projection are one call, with H their heads together
+ *   pos        device [T] int64     turns   device [rot/2] uint64
+ *   rot        even, 0 .. D         gain    factor on the rotated dims
+ *   flags      TM_ROPE_INTERLEAVED; TM_ROPE_INVERSE turns back: with the same
+ *              gain it is the gradient of the forward call
+ * Strides are >= 0, and no two heads of Y overlap (the caller's promise).
+ * Errors: INVALID_ARG, UNSUPPORTED_TILE (D > 1024), MISALIGNED, CUDA.
+ */
+tm_status tm_rope(const void *X, int64_t xs_tok, int64_t xs_head, void *Y, int64_t ys_tok, int64_t ys_head,
+                  const int64_t *pos, const uint64_t *turns, int64_t T, int32_t H, int32_t D, int32_t rot, float gain,
+                  int32_t xtype, uint32_t flags, tm_stream_t stream);
+
+/*
+ * A paged cache of keys and values in 4 bits.  A vector of D values (one token,
+ * one KV head) is held as
+ *   low = fp16(min),  step = fp16((max - min) / 15),  code = round((x - low) / step) in 0 .. 15,
+ * and stands for low + code * step (roundings to nearest even, min and
+ * (max - min) / 15 by way of fp32, both clamped to fp16's range; step 0 gives
+ * codes 0).  A vector with a NaN, an infinity or a spread beyond fp32's range is
+ * held as NaN.  The codes are
+ * those of this formula on the exactly rotated values: where fp32 cannot decide
+ * a rounding, the kernel decides it in fp64.
+ *
+ * The pool is `pages` pages of `page` tokens (a multiple of 16), each
+ * tm_kv4_page_bytes(Hkv, D, page) bytes: [Hkv][page / 16] blocks of 16 tokens,
+ * 16 * (D + 8) bytes each:
+ *   K codes    [16 tokens][D / 2 bytes], dims in order, the even one in the low nibble
+ *   V codes    [8 token pairs][8 slices][2 tokens][D / 16 bytes]: slice r holds dims r*D/8 ..
+ *   K scales   [16] (step, low) fp16     V scales  [16] (step, low) fp16
+ * Slot s of the pool is token s % page of page s / page.  The pool is 16-byte
+ * aligned; its contents need no clearing.  D is 64, 128 or 256.
+ */
+size_t tm_kv4_page_bytes(int32_t Hkv, int32_t D, int32_t page);
+
+/*
+ * tm_kv4_append -- write T new tokens to the cache, rotating on the way: keys
+ * are rotated (as tm_rope) and then held, values held as they are, and queries,
+ * if given, rotated into QO, in one launch.
+ *   Q, QO      [T, Hq, D] as in tm_rope (QO may be Q, same strides); Hq == 0 for none
+ *   K, V       [T, Hkv, D]
+ *   pos, turns, rot, gain   as tm_rope; rot a multiple of 16 (0: no rotation,
+ *              pos and turns may be NULL)
+ *   slots      device [T] int64: where each token goes.  -1: nowhere (padding of
+ *              a captured batch; its query is rotated all the same).  Two tokens
+ *              of one call must not share a slot
+ *   flags      TM_ROPE_INTERLEAVED
+ * Errors: INVALID_ARG, UNSUPPORTED_TILE (D, rot, page), MISALIGNED, CUDA;
+ *         INDEX through tm_check for a slot outside the pool (not written).
+ */
+tm_status tm_kv4_append(const void *Q, int64_t qs_tok, int64_t qs_head, void *QO, int64_t qos_tok, int64_t qos_head,
+                        int32_t Hq, const void *K, int64_t ks_tok, int64_t ks_head, const void *V, int64_t vs_tok,
+                        int64_t vs_head, const int64_t *pos, const uint64_t *turns, const int64_t *slots, void *pool,
+                        int64_t pages, int32_t page, int64_t T, int32_t Hkv, int32_t D, int32_t rot, float gain,
+                        int32_t xtype, uint32_t flags, tm_stream_t stream);
+
+/*
+ * tm_kv4_gather -- read tokens back: K[t], V[t] = what slot slots[t] stands for,
+ * rounded to xtype (zeros for slot -1, and for one outside the pool, which
+ * tm_check reports as INDEX).  K or V may be NULL.
+ * Errors: INVALID_ARG, UNSUPPORTED_TILE, MISALIGNED, CUDA.
+ */
+tm_status tm_kv4_gather(const void *pool, int64_t pages, int32_t page, const int64_t *slots, void *K, int64_t ks_tok,
+                        int64_t ks_head, void *V, int64_t vs_tok, int64_t vs_head, int64_t T, int32_t Hkv, int32_t D,
+                        int32_t xtype, uint32_t flags, tm_stream_t stream);
+
+/*
+ * tm_kv4_attention -- attention of new queries over the cache:
+ *   o = softmax_j(scale * q . k_j + mask) v,   lse = log sum_j exp(scale * q . k_j + mask).
+ * Sequence b has lens[b] tokens in the cache (its newest queries' own keys among
+ * them), token j in page table[b*ldt + j / page]; its queries are rows
+ * qstart[b] .. qstart[b+1] - 1 of Q, at positions lens[b] - n .. lens[b] - 1 (n
+ * their count).  A query at position p sees keys j <= p, with window > 0 only
+ * j > p - window, with TM_ATTN_FULL every key (window 0).  A query that sees
+ * none gets o = 0 and lse = -inf.  Query head h reads KV head h / (Hq / Hkv).
+ *   Q, O       [Tq, Hq, D] as in tm_rope; O does not overlap Q
+ *   lse        [Tq, Hq] fp32, or NULL
+ *   pool, pages, page   the cache
+ *   table, ldt device int32 [B, ldt]; lens device int32 [B], each at most max_len
+ *   qstart     device int32 [B + 1], non-decreasing from 0 to Tq, or NULL: one
+ *              query a sequence (Tq == B)
+ *   max_q      no sequence has more queries (the grid is sized by it)
+ *   max_len    no sequence has more tokens; table rows hold its pages.  It sets how
+ *              the work is split, so a close bound is faster
+ *   workspace  tm_kv4_attention_workspace_bytes(...) bytes, 16-byte aligned, in
+ *              use until the call's kernels finish
+ * Products run on the codes in fp16 on the tensor cores (fp32 queries as two
+ * fp16 parts), sums in fp32; splits of a sequence are joined in a fixed order.
+ * Errors: INVALID_ARG, UNSUPPORTED_TILE (D, page), MISALIGNED, WORKSPACE, CUDA;
+ *         INDEX (a page outside the pool, a length beyond max_len, a count beyond
+ *         max_q or Tq) and TIMEOUT through tm_check.
+ */
+#define TM_ATTN_FULL 0x1000u
+size_t tm_kv4_attention_workspace_bytes(int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_t Hq, int32_t Hkv,
+                                        int32_t D);
+tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_head, void *O, int64_t os_tok, int64_t os_head,
+                           float *lse, const void *pool, int64_t pages, int32_t page, const int32_t *table,
+                           int64_t ldt, const int32_t *lens, const int32_t *qstart, int32_t B, int64_t Tq,
+                           int32_t max_q, int64_t max_len, int32_t Hq, int32_t Hkv, int32_t D, float scale,
+                           int32_t window, int32_t xtype, void *workspace, size_t ws_bytes, uint32_t flags,
+                           tm_stream_t stream);
+
+/*
  * tm_check -- synchronize `stream`, then read and clear this device's status
  * word.  Returns TM_ERR_BROKEN_PROMISE if a kernel's entry check found the
  * aligned promise broken (that kernel stored nothing), TM_ERR_MISALIGNED if it
  * found a misaligned pointer or ld, TM_ERR_TIMEOUT if a bounded wait gave up,
+ * TM_ERR_INDEX if a kernel met a page, slot or length out of range,
  * TM_ERR_CUDA if the stream reports a CUDA error, else TM_OK.
  */
 tm_status tm_check(tm_stream_t stream);

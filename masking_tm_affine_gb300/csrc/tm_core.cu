@@ -163,6 +163,7 @@ extern "C" const char *tm_status_string(tm_status st)
     case TM_ERR_CUDA: return "TM_ERR_CUDA: CUDA runtime error";
     case TM_ERR_WORKSPACE: return "TM_ERR_WORKSPACE: workspace missing, too small or misaligned";
     case TM_ERR_TIMEOUT: return "TM_ERR_TIMEOUT: a bounded device wait gave up";
+    case TM_ERR_INDEX: return "TM_ERR_INDEX: a page, slot or length read on the device is out of range";
     }
     return "TM_ERR_UNKNOWN";
 }
@@ -190,6 +191,7 @@ extern "C" tm_status tm_check(tm_stream_t stream)
     if (word & kStatusBrokenPromise) return TM_ERR_BROKEN_PROMISE;
     if (word & kStatusMisaligned) return TM_ERR_MISALIGNED;
     if (word & kStatusTimeout) return TM_ERR_TIMEOUT;
+    if (word & kStatusIndex) return TM_ERR_INDEX;
     return TM_OK;
 }
 

@@ -18,6 +18,7 @@ enum : unsigned {
     kStatusBrokenPromise = 1u,  // aligned path entered with M % TM or N % TN != 0
     kStatusMisaligned = 2u,     // aligned path entered with a pointer or ld off the vector grid
     kStatusTimeout = 4u,        // a bounded wait gave up
+    kStatusIndex = 8u,          // a page, slot or length from device memory is out of range
 };
 
 struct u32x4 {

@@ -1,0 +1,907 @@
+// tm_kv4_attn.cu -- attention over the 4-bit paged cache.
+//
+//   s_tj = scale q_t . k_j,  o_t = sum_j softmax(s_t)_j v_j,   k_j = lowK_j + stepK_j ck_j,  v_j = lowV_j + stepV_j cv_j
+//
+// The codes are never turned into values: with integer codes c in 0 .. 15,
+//   s_tj = scale (stepK_j (q_t . ck_j) + lowK_j sum(q_t))
+//   o_t  = sum_j (p_tj stepV_j) cv_j + sum_j p_tj lowV_j
+// so the products run on codes and the scales meet one value per (query, token).
+//
+// Decode is bound by HBM (D + 8 bytes a token and KV head against 4 D flops for
+// each of its query heads); what it must not do is spend more than about three
+// instructions a code.  A K nibble becomes half of an fp16 pair by one AND: the
+// bits 0x000c read as fp16 are the subnormal c 2^-24, 0x00c0 is c 2^-20, both
+// exact.  Eight codes of a 32-bit word are four pairs for four ANDs and a shift;
+// the factor 16 between even and odd nibbles is folded into q (K) and into the
+// output (V).  V's codes (and K's with fp32 tensors) take one subtraction a pair
+// more and go in as c - 8: a sum of positive codes over many tokens is 10 to 1000
+// times what is left of it in the output, and the tensor cores, which align a
+// step's products to the largest exponent (a subnormal counting as 2^-14) and cut
+// what lies below fp32's last place, would leave that many times their own error.
+//
+// Products are mma.sync m16n8k16 with tokens (or dims) as the 16 rows and up to
+// NT x 8 query rows (queries x the heads that share a KV head) as columns, so
+// one query token's group of 8 heads fills a tile and the accumulators are small:
+//   S^T [16 tokens, 8 rows] += K codes [16 tokens, 16 dims] . Q^T [16 dims, 8 rows]
+//   O^T [16 dims, 8 rows]   += V codes^T [16 dims, 16 tokens] . P^T [16 tokens, 8 rows]
+// A lane's K operand for all D/16 steps is D/8 contiguous bytes of two tokens;
+// V is laid out in token pairs so that two byte permutes pair the tokens; P^T is
+// the first product's accumulator, transposed by movmatrix in registers.
+//
+// A block is one (sequence, KV head, row tile, split of the tokens).  Each of its
+// four warps streams its own tiles of 32 tokens through a private ring of bulk
+// copies (one or two per tile: a cache block is contiguous), so no barrier is in
+// the loop; each keeps its own running maximum, sum and output, joined at the
+// end in shared memory, and splits by a second launch.
+//
+// P stepV is rounded to fp16 for the second product: scaled by 2^E so that the
+// largest step seen lies in [2^14, 2^15), it is off by at most 2^-11 of itself,
+// errors that the sum over tokens averages below the output's own rounding.  With
+// fp32 tensors q and P stepV go in as two fp16 parts each (22 bits).
+#include "tm_host.h"
+
+#include "tm_elem.cuh"
+#include "tm_kv4.cuh"
+
+namespace libtm {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kTile = 32;    // tokens a warp takes at a time: two cache blocks
+constexpr int kMaxSplits = 256;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2eF = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 half2_at(const uint8_t *p)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(p));
+}
+
+// The codes of two nibbles 16 bits apart as an fp16 pair, from the low nibble
+// position (even dims of a word) or the next one (odd dims).
+// Plain: the bits as they are, subnormal fp16: c 2^-24, or c 2^-20.
+__device__ __forceinline__ uint32_t plain_even(uint32_t x) { return x & 0x000f000fu; }
+__device__ __forceinline__ uint32_t plain_odd(uint32_t x) { return x & 0x00f000f0u; }
+
+// Centred: c - 8, or 16 (c - 8), normal numbers: the nibble joins the low bits of
+// 1024 and the subtraction is exact.
+__device__ __forceinline__ uint32_t centred(uint32_t x, uint16_t middle)
+{
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), __halves2half2(__ushort_as_half(middle), __ushort_as_half(middle)));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t centred_even(uint32_t x) { return centred((x & 0x000f000fu) | 0x64006400u, 0x6408); }  // 1032
+__device__ __forceinline__ uint32_t centred_odd(uint32_t x) { return centred((x & 0x00f000f0u) | 0x64006400u, 0x6480); }   // 1152
+
+struct AttnArgs {
+    const void *Q;
+    void *O;
+    float *lse;
+    const uint8_t *pool;
+    const int32_t *table, *lens, *qstart;
+    float *part;  // splits > 1: [splits][Tq * Hq][D] outputs, then [splits][Tq * Hq][2] (maximum, sum)
+    int64_t qs_tok, qs_head, os_tok, os_head, pages, page_bytes, ldt, Tq, max_len;
+    int page, B, Hq, Hkv, G, window, full, vec, row_tiles, splits, chunk;  // chunk: tokens a split
+    int max_q;
+    float scale;
+    unsigned *status;
+};
+
+// What a sequence's queries are: their first row of Q, their count and the
+// cache's length, checked against the call's bounds.
+struct Seq {
+    int64_t q0;
+    int n, len;
+};
+
+__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b, bool report)
+{
+    Seq s;
+    int64_t q1;
+    if (a.qstart) {
+        s.q0 = a.qstart[b];
+        q1 = a.qstart[b + 1];
+    } else {
+        s.q0 = b;
+        q1 = b + 1;
+    }
+    s.len = a.lens[b];
+    if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || q1 - s.q0 > a.max_q || s.len < 0 || s.len > a.max_len) {
+        if (report) atomicOr(a.status, kStatusIndex);
+        s.n = 0;
+        s.len = 0;
+        return s;
+    }
+    s.n = (int)(q1 - s.q0);
+    return s;
+}
+
+template <int D>
+__host__ __device__ constexpr int stage_bytes()
+{
+    return 2 * kv4_block_bytes(D);
+}
+
+// Stages of the copy ring: enough bytes in flight (about 16 KB a warp), and four
+// blocks of four warps in an SM's 227 KB.
+template <int D>
+__host__ __device__ constexpr int ring_stages()
+{
+    return D == 64 ? 5 : D == 128 ? 3 : 2;
+}
+
+template <int D>
+__host__ __device__ constexpr int attn_smem()
+{
+    return kWarps * ring_stages<D>() * stage_bytes<D>() + 128;
+}
+
+// T: element type.  NT: column tiles of 8 query rows.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_constant__ AttnArgs a)
+{
+    constexpr bool SPLIT = sizeof(T) == 4;     // two fp16 parts
+    constexpr int PARTS = SPLIT ? 2 : 1;
+    constexpr int KS = D / 16;                 // steps of the first product = row tiles of the second
+    constexpr int LD = D / 4;                  // dims of a row that a lane holds for the first product
+    constexpr int STAGES = ring_stages<D>();
+    constexpr int SB = stage_bytes<D>(), BB = kv4_block_bytes(D);
+    constexpr int ROWS = 8 * NT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kWarps][STAGES];
+
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
+    // blockIdx.x = ((b * Hkv + h) * row_tiles + tile) * splits + split
+    int u = blockIdx.x;
+    const int split = u % a.splits;
+    u /= a.splits;
+    const int tile = u % a.row_tiles;
+    u /= a.row_tiles;
+    const int kvh = u % a.Hkv, b = u / a.Hkv;
+    const Seq seq = sequence(a, b, threadIdx.x == 0 && kvh == 0 && tile == 0 && split == 0);
+    const int rows = min(ROWS, seq.n * a.G - tile * ROWS);
+    if (rows <= 0) {
+        pdl_wait();
+        return;
+    }
+
+    // The tokens this row tile sees: [begin, end), and of those this split's.
+    const int t_first = tile * ROWS / a.G, t_last = (tile * ROWS + rows - 1) / a.G;
+    auto upper = [&](int t) { return a.full ? seq.len : min(seq.len, max(0, seq.len - seq.n + t + 1)); };
+    auto lower = [&](int t) { return a.window > 0 ? max(0, seq.len - seq.n + t + 1 - a.window) : 0; };
+    const int begin = lower(t_first) / kTile * kTile, end = upper(t_last);
+    const int c0 = begin + split * a.chunk, c1 = min(end, c0 + a.chunk);
+    const int tiles = c1 > c0 ? (c1 - c0 + kTile - 1) / kTile : 0;
+    if (a.splits > 1 && tiles == 0) {  // the join counts a row's splits the same way
+        pdl_wait();
+        return;
+    }
+
+    // ---- the copy ring: this warp's tiles are warp, warp + 4, ... of the split
+    uint8_t *ring = smem + warp * (STAGES * SB);
+    const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(&bars[warp][0]);
+    if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_s + 8 * s) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncwarp();
+    const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+    const int32_t *trow = a.table + (int64_t)b * a.ldt;
+    const uint64_t policy = l2_evict_first_policy();
+    // Page numbers of this warp's tiles i .. i + 31 sit one a lane (two blocks of a
+    // tile can lie in two pages).
+    int page0 = 0, page1 = 0;
+    auto fetch_pages = [&](int i0) {
+        const int i = i0 + lane;
+        page0 = page1 = 0;
+        if (i < mine) {
+            const int tok = c0 + (warp + i * kWarps) * kTile;
+            page0 = trow[tok / a.page];
+            page1 = tok + 16 < end ? trow[(tok + 16) / a.page] : page0;
+            if (page0 < 0 || page0 >= a.pages || page1 < 0 || page1 >= a.pages) {
+                atomicOr(a.status, kStatusIndex);
+                page0 = page0 < 0 || page0 >= a.pages ? 0 : page0;
+                page1 = page1 < 0 || page1 >= a.pages ? 0 : page1;
+            }
+        }
+    };
+    auto issue = [&](int i) {  // every lane calls it; lane 0 copies
+        if ((i & 31) == 0) fetch_pages(i);
+        const int p0 = __shfl_sync(0xffffffffu, page0, i & 31), p1 = __shfl_sync(0xffffffffu, page1, i & 31);
+        if (lane == 0) {
+            const int tok = c0 + (warp + i * kWarps) * kTile, s = i % STAGES;
+            const bool two = tok + 16 < end;
+            const uint32_t dst = ring_s + s * SB, bar = bar_s + 8 * s;
+            const int64_t head = (int64_t)kvh * (a.page / 16);
+            const int blk0 = tok % a.page / 16, blk1 = (tok + 16) % a.page / 16;
+            const uint8_t *s0 = a.pool + p0 * a.page_bytes + (head + blk0) * BB;
+            const uint8_t *s1 = a.pool + p1 * a.page_bytes + (head + blk1) * BB;
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(two ? 2 * BB : BB)
+                         : "memory");
+            const bool joined = two && s1 == s0 + BB;
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
+                "%4;" ::"r"(dst), "l"(s0), "r"(joined ? 2 * BB : BB), "r"(bar), "l"(policy)
+                : "memory");
+            if (two && !joined)
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
+                    "[%3], %4;" ::"r"(dst + BB), "l"(s1), "r"(BB), "r"(bar), "l"(policy)
+                    : "memory");
+        }
+    };
+    int issued = 0;
+    for (; issued < STAGES && issued < mine; ++issued) issue(issued);
+
+    // ---- queries: lane (g, j) holds dims j D/4 .. of row g of each column tile, as the
+    // second operand of the first product.  Scaled by a power of two common to all
+    // rows, so that the largest lies in [2^14, 2^15): bf16's eight bits, and fp16's
+    // eleven down to 2^-28 of the largest, are kept whole.
+    uint32_t qf[PARTS][NT][KS][2];
+    float qsum[NT];
+    float top = 0.0f;
+    auto row_ptr = [&](int row) {
+        const int t = row / a.G, hh = row - t * a.G;
+        return reinterpret_cast<const T *>(a.Q) + (seq.q0 + t) * a.qs_tok + (int64_t)(kvh * a.G + hh) * a.qs_head;
+    };
+    auto load_q8 = [&](int nt, int w, float (&f)[8]) {
+        const int row = tile * ROWS + nt * 8 + g;
+        if (nt * 8 + g < rows) {
+            const T *p = row_ptr(row) + j * LD + 8 * w;
+            if (a.vec) {
+                Vec<T, 8> v = *reinterpret_cast<const Vec<T, 8> *>(p);
+                widen(v, f);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = to_f(p[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+        }
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int w = 0; w < LD / 8; ++w) {
+            float f[8];
+            load_q8(nt, w, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+        }
+    top = lanes_max(top, 32);
+    // 2^qe: exponent of the largest, kept where 2^(14 - qe) and its inverse are normal
+    int qe = (int)(__float_as_uint(top) >> 23) - 127;
+    qe = max(-100, min(qe, 127));
+    const float up = ldexpf(1.0f, 14 - qe);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < LD / 8; ++w) {
+            float f[8];
+            load_q8(nt, w, f);
+            // word w of a lane's codes: pairs (0,4), (1,5)/16 in step 2w and (2,6), (3,7)/16 in step 2w + 1
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[e] *= up;
+                sum += f[e];
+                if (e & 1) f[e] *= 0.0625f;
+            }
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr) {
+                const uint32_t hi = pack_half2(f[pr], f[pr + 4]);
+                qf[0][nt][2 * w + (pr >> 1)][pr & 1] = hi;
+                if constexpr (SPLIT) {
+                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                    qf[PARTS - 1][nt][2 * w + (pr >> 1)][pr & 1] =
+                        pack_half2((f[pr] - h.x) * 2048.0f, (f[pr + 4] - h.y) * 2048.0f);
+                }
+            }
+        }
+        qsum[nt] = lanes_sum(sum, 4);
+    }
+    // logits in base 2 are (acc stepK + lowK qsum) * unit, acc in units of 2^-24 where codes are subnormal
+    const float unit = a.scale * kLog2eF * ldexpf(1.0f, qe - 14);
+    float qs[NT][2];  // of this lane's accumulator columns, rows 2j and 2j + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        qs[nt][0] = __shfl_sync(0xffffffffu, qsum[nt], 8 * j) * unit;
+        qs[nt][1] = __shfl_sync(0xffffffffu, qsum[nt], 8 * j + 4) * unit;
+    }
+    const float kunit = SPLIT ? unit : unit * 0x1p24f;
+
+    // ---- running state: per column (2j, 2j + 1 of each tile); the maximum is the
+    // warp's, the sums are this lane's share (its tokens)
+    float o[KS][NT][4], m[NT][2], l[NT][2], lowsum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[k][nt][e] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            m[nt][c] = -INFINITY;
+            l[nt][c] = lowsum[nt][c] = 0.0f;
+        }
+    }
+    float vcap = 0.0f, vscale = 1.0f;  // largest stepV is below vcap; vscale = 2^E
+    int vexp = 0;
+    bool alive = true;
+
+    // Where every row of the tile sees every token: [safe0, safe1).
+    const int safe0 = lower(t_last), safe1 = upper(t_first);
+
+    for (int i = 0; i < mine; ++i) {
+        const int s = i % STAGES, tok0 = c0 + (warp + i * kWarps) * kTile;
+        if (!mbar_wait_bounded(bar_s + 8 * s, (i / STAGES) & 1)) {
+            alive = false;
+            break;
+        }
+        const uint8_t *st = ring + s * SB;
+        const bool masked = tok0 < safe0 || tok0 + kTile > safe1;
+        float y[2][NT][4];
+        float2 vp[2][2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint8_t *blk = st + q * BB;
+            // first product
+            float acc[PARTS][NT][4];
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[p][nt][e] = 0.0f;
+            uint32_t k0[LD / 8], k1[LD / 8];
+            const uint8_t *kr = blk + g * (D / 2) + j * (D / 8);
+            if constexpr (D == 64) {
+                *reinterpret_cast<uint2 *>(k0) = *reinterpret_cast<const uint2 *>(kr);
+                *reinterpret_cast<uint2 *>(k1) = *reinterpret_cast<const uint2 *>(kr + 8 * (D / 2));
+            } else {
+#pragma unroll
+                for (int x = 0; x < LD / 32; ++x) {
+                    reinterpret_cast<uint4 *>(k0)[x] = reinterpret_cast<const uint4 *>(kr)[x];
+                    reinterpret_cast<uint4 *>(k1)[x] = reinterpret_cast<const uint4 *>(kr + 8 * (D / 2))[x];
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < LD / 8; ++w) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint32_t x0 = hf ? k0[w] >> 8 : k0[w], x1 = hf ? k1[w] >> 8 : k1[w];
+                    const uint32_t a0 = SPLIT ? centred_even(x0) : plain_even(x0);
+                    const uint32_t a1 = SPLIT ? centred_even(x1) : plain_even(x1);
+                    const uint32_t a2 = SPLIT ? centred_odd(x0) : plain_odd(x0);
+                    const uint32_t a3 = SPLIT ? centred_odd(x1) : plain_odd(x1);
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816(acc[p][nt], a0, a1, a2, a3, qf[p][nt][2 * w + hf][0], qf[p][nt][2 * w + hf][1]);
+                }
+            }
+            // logits: this lane's tokens g and g + 8
+            float2 kp0 = half2_at(blk + kv4_ks_off(D) + 4 * g), kp1 = half2_at(blk + kv4_ks_off(D) + 4 * (g + 8));
+            vp[q][0] = half2_at(blk + kv4_vs_off(D) + 4 * g);
+            vp[q][1] = half2_at(blk + kv4_vs_off(D) + 4 * (g + 8));
+            // centred codes count from low + 8 step
+            if constexpr (SPLIT) {
+                kp0.y = fmaf(8.0f, kp0.x, kp0.y);
+                kp1.y = fmaf(8.0f, kp1.x, kp1.y);
+            }
+            vp[q][0].y = fmaf(8.0f, vp[q][0].x, vp[q][0].y);
+            vp[q][1].y = fmaf(8.0f, vp[q][1].x, vp[q][1].y);
+            const float ks0 = kp0.x * kunit, ks1 = kp1.x * kunit;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float d = acc[0][nt][e];
+                    if constexpr (SPLIT) d = fmaf(acc[PARTS - 1][nt][e], 1.0f / 2048.0f, d);
+                    y[q][nt][e] = fmaf(d, e < 2 ? ks0 : ks1, (e < 2 ? kp0.y : kp1.y) * qs[nt][e & 1]);
+                }
+        }
+        if (masked) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int t = (tile * ROWS + nt * 8 + 2 * j + c) / a.G;
+                    const int hi = upper(t), lo = lower(t);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int tok = tok0 + 16 * q + 8 * r + g;
+                            if (tok < lo || tok >= hi) y[q][nt][2 * r + c] = -INFINITY;
+                        }
+                }
+            // a token past the end has no scales (its bytes are whatever the page or the ring held)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    if (tok0 + 16 * q + 8 * r + g >= end) vp[q][r] = make_float2(0.0f, 0.0f);
+        }
+        // A token held as NaN makes the rows that see it NaN, and no others: its scales
+        // leave the sums (0 * NaN is not 0) and a NaN joins what is added to each output.
+        const float steps = (vp[0][0].x + vp[0][1].x) + (vp[1][0].x + vp[1][1].x);
+        if (__any_sync(0xffffffffu, !(steps < INFINITY))) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    if (!(vp[q][r].x < INFINITY)) {
+                        vp[q][r] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (y[q][nt][2 * r + c] != -INFINITY) lowsum[nt][c] = NAN;
+                    }
+        }
+        // a new maximum, or a larger step: move the running state (rare after the first tiles)
+        bool grow = false;
+        float vmax = fmaxf(fmaxf(vp[0][0].x, vp[0][1].x), fmaxf(vp[1][0].x, vp[1][1].x));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float t = fmaxf(fmaxf(y[0][nt][c], y[0][nt][2 + c]), fmaxf(y[1][nt][c], y[1][nt][2 + c]));
+                grow = grow || t > m[nt][c];
+            }
+        if (__any_sync(0xffffffffu, grow || vmax >= vcap)) {
+            vmax = lanes_max(vmax, 32);
+            float move = 1.0f;
+            if (vmax >= vcap && vmax > 0.0f) {
+                const int e = (int)(__float_as_uint(vmax) >> 23) - 127;  // 2^e <= vmax < 2^(e+1)
+                move = vcap > 0.0f ? ldexpf(1.0f, vexp - e) : 1.0f;
+                vexp = e;
+                vcap = ldexpf(1.0f, e + 1);
+                vscale = ldexpf(1.0f, 14 - e);
+            } else if (vcap == 0.0f) {
+                vcap = 0x1p-30f;  // only zero steps so far
+                vexp = -31;
+                vscale = 0x1p45f;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float t = fmaxf(fmaxf(y[0][nt][c], y[0][nt][2 + c]), fmaxf(y[1][nt][c], y[1][nt][2 + c]));
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+                    const float mn = fmaxf(m[nt][c], t);
+                    const float f = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - mn);
+                    m[nt][c] = mn;
+                    l[nt][c] *= f;
+                    lowsum[nt][c] *= f;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        o[k][nt][c] *= f * move;
+                        o[k][nt][2 + c] *= f * move;
+                    }
+                }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint8_t *blk = st + q * BB;
+            uint32_t pb[PARTS][NT][2];
+            const float vs0 = vp[q][0].x * vscale, vs1 = vp[q][1].x * vscale;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float mm = m[nt][e & 1];
+                    const float p = ex2(y[q][nt][e] - (mm == -INFINITY ? 0.0f : mm));
+                    l[nt][e & 1] += p;
+                    lowsum[nt][e & 1] = fmaf(p, e < 2 ? vp[q][0].y : vp[q][1].y, lowsum[nt][e & 1]);
+                    w[e] = p * (e < 2 ? vs0 : vs1);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t hi = pack_half2(w[2 * r], w[2 * r + 1]);
+                    pb[0][nt][r] = transpose8x8(hi);
+                    if constexpr (SPLIT) {
+                        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                        // the rest, below 2^4 against a largest of 2^15: down to 2^-24, 2^-39 of it
+                        pb[PARTS - 1][nt][r] = transpose8x8(pack_half2(w[2 * r] - h.x, w[2 * r + 1] - h.y));
+                    }
+                }
+            }
+            // second product: pairs j and j + 4 of tokens, slice g of dims
+            constexpr int VW = D / 128 > 0 ? D / 64 : 1;  // words of 8 dims a token has in a slice: 1, 2, 4
+            uint32_t v0[2 * VW], v1[2 * VW];  // [token parity][word]
+            const uint8_t *vr = blk + kv4_v_off(D) + j * D + g * (D / 8);
+            if constexpr (D == 64) {
+                *reinterpret_cast<uint2 *>(v0) = *reinterpret_cast<const uint2 *>(vr);
+                *reinterpret_cast<uint2 *>(v1) = *reinterpret_cast<const uint2 *>(vr + 4 * D);
+            } else {
+#pragma unroll
+                for (int x = 0; x < VW / 2; ++x) {
+                    reinterpret_cast<uint4 *>(v0)[x] = reinterpret_cast<const uint4 *>(vr)[x];
+                    reinterpret_cast<uint4 *>(v1)[x] = reinterpret_cast<const uint4 *>(vr + 4 * D)[x];
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+#pragma unroll
+                for (int pr = 0; pr < 2; ++pr) {
+                    const uint32_t sel = pr ? 0x7632u : 0x5410u;  // (even, odd) token: low or high 16 bits
+                    const uint32_t e0 = __byte_perm(v0[w], v0[VW + w], sel), e1 = __byte_perm(v1[w], v1[VW + w], sel);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t x0 = hf ? e0 >> 8 : e0, x1 = hf ? e1 >> 8 : e1;
+                        const uint32_t a0 = centred_even(x0), a1 = centred_odd(x0);
+                        const uint32_t a2 = centred_even(x1), a3 = centred_odd(x1);
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(o[4 * w + 2 * pr + hf][nt], a0, a1, a2, a3, pb[p][nt][0], pb[p][nt][1]);
+                    }
+                }
+        }
+        __syncwarp();  // every lane has read the stage
+        if (issued < mine) issue(issued++);
+    }
+    if (!alive) {
+        // let what is in flight land before the block's shared memory goes
+        if (lane == 0) atomicOr(a.status, kStatusTimeout);
+        for (int i = max(0, issued - STAGES); i < issued; ++i)
+            mbar_wait_bounded(bar_s + 8 * (i % STAGES), (i / STAGES) & 1);
+    }
+    pdl_wait();
+    if (!__syncthreads_and(alive)) return;
+
+    // ---- join the warps.  o: dims 2k of slice g in elements 0, 1 and 2k + 1 in 2, 3,
+    // in units of 2^E (16 times that for the odd ones)
+    const float even = ldexpf(1.0f, vexp - 14), odd = even * 0.0625f;
+    float *stat = reinterpret_cast<float *>(smem);            // [kWarps][ROWS][2]: maximum, sum
+    float *buf = stat + kWarps * ROWS * 2;                    // [kWarps][ROWS][D / PASS]
+    constexpr int kRoom = kWarps * STAGES * SB - kWarps * ROWS * 8;
+    constexpr int kNeed = kWarps * ROWS * D * 4;
+    constexpr int PASS = kNeed <= kRoom ? 1 : kNeed <= 2 * kRoom ? 2 : 4;  // parts of the dims joined at a time
+    static_assert(kNeed <= 4 * kRoom, "join buffer");
+    constexpr int KP = KS / PASS, DP = D / PASS;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+                l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+                lowsum[nt][c] += __shfl_xor_sync(0xffffffffu, lowsum[nt][c], x);
+            }
+            if (g == 0) {
+                float *q = stat + (warp * ROWS + nt * 8 + 2 * j + c) * 2;
+                q[0] = m[nt][c];
+                q[1] = l[nt][c];
+            }
+        }
+    const int64_t all_rows = a.Tq * a.Hq;
+#pragma unroll
+    for (int ps = 0; ps < PASS; ++ps) {
+        if (ps > 0) __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                // this lane's 2 KP dims of this part: 2 KP g .. of it
+                float *q = buf + ((warp * ROWS + nt * 8 + 2 * j + c) * 8 + g) * (2 * KP);
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    q[2 * k] = fmaf(o[ps * KP + k][nt][c], even, lowsum[nt][c]);
+                    q[2 * k + 1] = fmaf(o[ps * KP + k][nt][2 + c], odd, lowsum[nt][c]);
+                }
+            }
+        __syncthreads();
+        for (int x = threadIdx.x; x < rows * (DP / 2); x += kWarps * 32) {
+            const int row = x / (DP / 2), d2 = x % (DP / 2) * 2;
+            float mm = -INFINITY, ll = 0.0f, v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[(w * ROWS + row) * 2]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = stat[(w * ROWS + row) * 2];
+                // (a warp that saw nothing: m = -inf, sum and output 0; a NaN sum stays a NaN)
+                const float f = mw == -INFINITY ? 1.0f : ex2(mw - mm);
+                const float2 v = *reinterpret_cast<const float2 *>(buf + (w * ROWS + row) * DP + d2);
+                ll = fmaf(stat[(w * ROWS + row) * 2 + 1], f, ll);
+                v0 = fmaf(v.x, f, v0);
+                v1 = fmaf(v.y, f, v1);
+            }
+            // dims of this part: 2 KP of every slice of 2 KS
+            const int d = d2 / (2 * KP) * (2 * KS) + ps * 2 * KP + d2 % (2 * KP);
+            const int full_row = tile * ROWS + row, t = full_row / a.G, hq = kvh * a.G + full_row - t * a.G;
+            const int64_t q = (seq.q0 + t) * a.Hq + hq;
+            if (a.splits > 1) {
+                *reinterpret_cast<float2 *>(a.part + ((int64_t)split * all_rows + q) * D + d) = make_float2(v0, v1);
+                if (d == 0)
+                    *reinterpret_cast<float2 *>(a.part + (int64_t)a.splits * all_rows * D +
+                                                ((int64_t)split * all_rows + q) * 2) = make_float2(mm, ll);
+            } else {
+                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+                T *out = reinterpret_cast<T *>(a.O) + (seq.q0 + t) * a.os_tok + hq * a.os_head + d;
+                if (a.vec) {
+                    Vec<T, 2> v;
+                    v.v[0] = from_f<T>(v0 * inv);
+                    v.v[1] = from_f<T>(v1 * inv);
+                    store_vec(out, v);
+                } else {
+                    out[0] = from_f<T>(v0 * inv);
+                    out[1] = from_f<T>(v1 * inv);
+                }
+                if (d == 0 && a.lse) a.lse[q] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            }
+        }
+    }
+}
+
+// Joins the splits of one (query, head) a warp, in order.  Splits that a
+// sequence does not reach were not written: each row's count is recomputed.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ AttnArgs a, int rows_of_tile)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), all_rows = a.Tq * a.Hq;
+    if (r >= all_rows) return;
+    const int64_t q = r / a.Hq;
+    const int hq = (int)(r - q * a.Hq);
+    // the sequence of query q: the last b with qstart[b] <= q
+    int b = (int)q;
+    if (a.qstart) {
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.qstart[mid] <= q) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+    }
+    const Seq seq = sequence(a, b, false);
+    int n = 0;
+    if (q >= seq.q0 && q < seq.q0 + seq.n) {
+        const int row = (int)(q - seq.q0) * a.G + hq % a.G, tile = row / rows_of_tile;
+        const int first = tile * rows_of_tile / a.G;
+        const int last = min(tile * rows_of_tile + rows_of_tile, seq.n * a.G) - 1;
+        const int t_last = last / a.G;
+        const int begin = a.window > 0 ? max(0, seq.len - seq.n + first + 1 - a.window) / kTile * kTile : 0;
+        const int end = a.full ? seq.len : min(seq.len, max(0, seq.len - seq.n + t_last + 1));
+        n = end > begin ? min(a.splits, (end - begin + a.chunk - 1) / a.chunk) : 0;
+    } else {
+        return;  // not a query of any sequence
+    }
+    const float *stat = a.part + (int64_t)a.splits * all_rows * D;
+    float mm = -INFINITY;
+    for (int s = lane; s < n; s += 32) mm = fmaxf(mm, stat[((int64_t)s * all_rows + r) * 2]);
+    mm = lanes_max(mm, 32);
+    float ll = 0.0f, v[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) v[e] = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+        const float2 ms = *reinterpret_cast<const float2 *>(stat + ((int64_t)s * all_rows + r) * 2);
+        const float f = ms.x == -INFINITY ? 1.0f : ex2(ms.x - mm);
+        const float *p = a.part + ((int64_t)s * all_rows + r) * D + lane * (D / 32);
+        ll = fmaf(ms.y, f, ll);
+#pragma unroll
+        for (int e = 0; e < D / 32; e += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(p + e);
+            v[e] = fmaf(x.x, f, v[e]);
+            v[e + 1] = fmaf(x.y, f, v[e + 1]);
+        }
+    }
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    T *out = reinterpret_cast<T *>(a.O) + q * a.os_tok + hq * a.os_head + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) out[e] = from_f<T>(v[e] * inv);
+    if (lane == 0 && a.lse) a.lse[r] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+}
+
+// Column tiles for a sequence's rows (its queries x the heads of a group).
+// fp32 needs twice the registers for q, D = 256 twice those for the output.
+int pick_nt(int64_t rows, int D, bool f32)
+{
+    const int most = D == 256 || f32 ? 1 : 2;
+    int nt = 1;
+    while (nt < most && nt * 8 < rows) nt *= 2;
+    return nt;
+}
+
+struct AttnPlan {
+    int nt, row_tiles, splits, chunk;
+};
+
+// Splits: enough blocks for a few rounds of every SM's four, in chunks of at
+// least 256 tokens (a block's start and end cost about as much as 100).
+// Uses nothing but the arguments, so the workspace can be sized without a device.
+AttnPlan attn_plan(int32_t B, int32_t max_q, int64_t max_len, int32_t Hq, int32_t Hkv, int32_t D, bool f32, bool window)
+{
+    AttnPlan p;
+    const int64_t rows = (int64_t)max_q * (Hq / Hkv);
+    p.nt = pick_nt(rows, D, f32);
+    p.row_tiles = (int)((rows + p.nt * 8 - 1) / (p.nt * 8));
+    const int64_t items = (int64_t)B * Hkv * p.row_tiles;
+    const int64_t slots = 152 * 4 * 3;
+    int64_t splits = items > 0 ? (slots + items - 1) / items : 1;
+    const int64_t most = (max_len + 255) / 256;
+    if (splits > most) splits = most;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    if (splits < 1) splits = 1;
+    const int64_t range = max_len + (window ? kTile - 1 : 0);  // a window's first tile is rounded down
+    int64_t chunk = (range + splits - 1) / splits;
+    const int64_t unit = kTile * kWarps;
+    chunk = (chunk + unit - 1) / unit * unit;
+    if (chunk < unit) chunk = unit;
+    p.chunk = (int)chunk;
+    p.splits = (int)((range + chunk - 1) / chunk);
+    if (p.splits < 1) p.splits = 1;
+    return p;
+}
+
+template <typename T, int D>
+tm_status launch_attn(const AttnArgs &a, const AttnPlan &p, cudaStream_t s, bool pdl)
+{
+    const void *k = (const void *)kv4_attn_kernel<T, D, 1>;
+    if constexpr (D != 256 && sizeof(T) == 2) {
+        if (p.nt == 2) k = (const void *)kv4_attn_kernel<T, D, 2>;
+    }
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D>()) != cudaSuccess) {
+        cudaGetLastError();
+        return TM_ERR_CUDA;
+    }
+    void *args[] = {(void *)&a};
+    const int64_t blocks = (int64_t)a.B * a.Hkv * p.row_tiles * p.splits;
+    tm_status st = launch_kernel(k, dim3((unsigned)blocks), dim3(kWarps * 32), args, attn_smem<D>(), s, pdl);
+    if (st != TM_OK || p.splits == 1) return st;
+    int rows_of_tile = p.nt * 8;
+    void *jargs[] = {(void *)&a, &rows_of_tile};
+    return launch_dependent((const void *)kv4_join_kernel<T, D>, dim3((unsigned)((a.Tq * a.Hq + 3) / 4)), dim3(128),
+                            jargs, 0, s);
+}
+
+template <typename T>
+tm_status launch_attn(int D, const AttnArgs &a, const AttnPlan &p, cudaStream_t s, bool pdl)
+{
+    return D == 64 ? launch_attn<T, 64>(a, p, s, pdl)
+           : D == 128 ? launch_attn<T, 128>(a, p, s, pdl) : launch_attn<T, 256>(a, p, s, pdl);
+}
+
+bool attn_shape_ok(int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_t Hq, int32_t Hkv)
+{
+    return B >= 0 && Tq >= 0 && max_q >= 0 && max_len >= 0 && max_len <= (1 << 30) && Hkv > 0 && Hq > 0 &&
+           Hq % Hkv == 0 && Hq <= 65536 && Tq <= INT32_MAX && max_q <= (1 << 24) / (Hq / Hkv);
+}
+
+}  // namespace
+}  // namespace libtm
+
+using namespace libtm;
+
+extern "C" size_t tm_kv4_attention_workspace_bytes(int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_t Hq,
+                                                   int32_t Hkv, int32_t D)
+{
+    if (!attn_shape_ok(B, Tq, max_q, max_len, Hq, Hkv) || !kv4_head_ok(D) || B == 0 || Tq == 0) return 0;
+    size_t most = 0;
+    for (int i = 0; i < 4; ++i) {  // any element type, with or without a window
+        const AttnPlan p = attn_plan(B, max_q, max_len, Hq, Hkv, D, (i & 1) != 0, (i & 2) != 0);
+        const size_t n = p.splits > 1 ? (size_t)p.splits * (size_t)Tq * Hq * (D + 2) * sizeof(float) : 0;
+        most = n > most ? n : most;
+    }
+    return most;
+}
+
+extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_head, void *O, int64_t os_tok,
+                                      int64_t os_head, float *lse, const void *pool, int64_t pages, int32_t page,
+                                      const int32_t *table, int64_t ldt, const int32_t *lens, const int32_t *qstart,
+                                      int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_t Hq, int32_t Hkv,
+                                      int32_t D, float scale, int32_t window, int32_t xtype, void *workspace,
+                                      size_t ws_bytes, uint32_t flags, tm_stream_t stream)
+{
+    const int e = elem_bytes(xtype);
+    if (e == 0 || (flags & ~(TM_ATTN_FULL | TM_PDL))) return TM_ERR_INVALID_ARG;
+    if (!attn_shape_ok(B, Tq, max_q, max_len, Hq, Hkv) || window < 0) return TM_ERR_INVALID_ARG;
+    if ((flags & TM_ATTN_FULL) && window > 0) return TM_ERR_INVALID_ARG;
+    if (!kv4_head_ok(D) || page <= 0 || page % 16 != 0) return TM_ERR_UNSUPPORTED_TILE;
+    const Heads q = {Q, qs_tok, qs_head}, o = {O, os_tok, os_head};
+    if (!heads_ok(q, Tq, Hq, D) || !heads_ok(o, Tq, Hq, D)) return TM_ERR_INVALID_ARG;
+    if (!kv4_pool_ok(pool, pages, page, Hkv, D)) return TM_ERR_INVALID_ARG;
+    if (B == 0 || Tq == 0) return TM_OK;
+    if (max_q < 1 || lens == nullptr || (qstart == nullptr && Tq != B)) return TM_ERR_INVALID_ARG;
+    if (ldt < (max_len + page - 1) / page || (max_len > 0 && (table == nullptr || pages == 0)) || ldt > INT64_MAX / 8 / B)
+        return TM_ERR_INVALID_ARG;
+    if (!aligned_to(Q, e) || !aligned_to(O, e) || !aligned_to(pool, 16) || !aligned_to(lse, 4) || !aligned_to(table, 4) ||
+        !aligned_to(lens, 4) || !aligned_to(qstart, 4))
+        return TM_ERR_MISALIGNED;
+    const AttnPlan p = attn_plan(B, max_q, max_len, Hq, Hkv, D, e == 4, window > 0);
+    const size_t need = p.splits > 1 ? (size_t)p.splits * (size_t)Tq * Hq * (D + 2) * sizeof(float) : 0;
+    if (need > 0 && (workspace == nullptr || ws_bytes < need || !aligned_to(workspace, 16))) return TM_ERR_WORKSPACE;
+    const int64_t pb = (int64_t)tm_kv4_page_bytes(Hkv, D, page);
+    const Span so = heads_span(o, Tq, Hq, D, e), sl = span_of(lse, Tq * Hq, lse ? 1 : 0, Tq * Hq, 4),
+               sw = need ? span_of(workspace, (int64_t)need, 1, (int64_t)need, 1) : Span{0, 0};
+    const Span ins[] = {heads_span(q, Tq, Hq, D, e), span_of(pool, pages * pb, 1, pages * pb, 1),
+                        span_of(table, ldt, B, ldt, 4), span_of(lens, B, 1, B, 4), span_of(qstart, B + 1, 1, B + 1, 4)};
+    for (const Span &s : ins)
+        if (meets(so, s) || meets(sl, s) || meets(sw, s)) return TM_ERR_INVALID_ARG;
+    if (meets(so, sl) || meets(so, sw) || meets(sl, sw)) return TM_ERR_INVALID_ARG;
+    const int64_t blocks = (int64_t)B * Hkv * p.row_tiles;
+    if (blocks > INT32_MAX / p.splits || Tq * Hq > INT32_MAX) return TM_ERR_INVALID_ARG;
+    const DevInfo *dev;
+    tm_status st = device_info(&dev);
+    if (st != TM_OK) return st;
+    AttnArgs a = {};
+    a.Q = Q;
+    a.O = O;
+    a.lse = lse;
+    a.pool = reinterpret_cast<const uint8_t *>(pool);
+    a.table = table;
+    a.lens = lens;
+    a.qstart = qstart;
+    a.part = reinterpret_cast<float *>(workspace);
+    a.qs_tok = qs_tok;
+    a.qs_head = qs_head;
+    a.os_tok = os_tok;
+    a.os_head = os_head;
+    a.pages = pages;
+    a.page_bytes = pb;
+    a.ldt = ldt;
+    a.Tq = Tq;
+    a.max_len = max_len;
+    a.page = page;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.window = window;
+    a.full = (flags & TM_ATTN_FULL) ? 1 : 0;
+    a.vec = heads_vec(q, e) && heads_vec(o, e) ? 1 : 0;
+    a.row_tiles = p.row_tiles;
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.max_q = max_q;
+    a.scale = scale;
+    a.status = dev->status;
+    cudaStream_t s = as_stream(stream);
+    const bool pdl = (flags & TM_PDL) != 0;
+    return xtype == TM_F32   ? launch_attn<float>(D, a, p, s, pdl)
+           : xtype == TM_F16 ? launch_attn<__half>(D, a, p, s, pdl)
+                             : launch_attn<__nv_bfloat16>(D, a, p, s, pdl);
+}

@@ -1,0 +1,601 @@
+// tm_norm.cu -- root-mean-square norm of rows, with the residual's addition
+// before it and an optional 8-bit output with scales, and its gradient.
+//
+//   h = x + r,   s = 1 / sqrt(mean_j h_j^2 + eps),   y_j = h_j s w_j
+//   e4m3 output: scale_g = max_{j in g} |y_j| / 448, code_j = e4m3(y_j / scale_g)
+//
+//   n = h s,  c = mean_j dy_j w_j n_j
+//   dx_j = s (dy_j w_j - n_j c) + dr_j,   dw_j = sum_rows dy_j n_j
+//
+// Both are bound by HBM (about 5 and 10 flops per element of 4 to 8 bytes
+// moved), so a row is read once and lives in registers between its statistics
+// and its output: L lanes share it (a power of two, 8 lanes up to a block of
+// 1024), each holding K vectors of EW elements.  Lane l's k-th vector is
+// (w K + k) 32 + l of the row (w the warp within the row): every access of a
+// warp is one run of 512 bytes, and a scale group of 32, 64 or 128 columns is a
+// run of lanes of one warp (or, with single elements, of one lane's registers).
+// All sums are fp32, in a fixed order.
+#include "tm_host.h"
+
+#include <cuda_fp8.h>
+
+#include "tm_elem.cuh"
+
+namespace libtm {
+namespace {
+
+constexpr int kMaxCols = 32768;  // what a block of 1024 lanes holds in registers
+
+// Largest block an instance is launched with (see pick_lanes).
+template <int EW, int K>
+constexpr int kMostLanes = (EW == 1 ? K > 8 : K > 4) ? 1024 : 512;
+
+// Sum over the L lanes of a row.  L > 32: through shared memory, warps added
+// in order, one barrier per call (the caller alternates between two buffers,
+// so a second call cannot overwrite what a slow warp still reads).
+__device__ __forceinline__ float row_sum(float x, int L, float *buf)
+{
+    x = lanes_sum(x, L < 32 ? L : 32);
+    if (L > 32) {
+        const int warp = threadIdx.x >> 5, W = L >> 5, base = warp / W * W;
+        if ((threadIdx.x & 31) == 0) buf[warp] = x;
+        __syncthreads();
+        x = buf[base];
+        for (int w = 1; w < W; ++w) x += buf[base + w];
+    }
+    return x;
+}
+
+__device__ __forceinline__ float row_max(float x, int L, float *buf)
+{
+    x = lanes_max(x, L < 32 ? L : 32);
+    if (L > 32) {
+        const int warp = threadIdx.x >> 5, W = L >> 5, base = warp / W * W;
+        if ((threadIdx.x & 31) == 0) buf[warp] = x;
+        __syncthreads();
+        x = buf[base];
+        for (int w = 1; w < W; ++w) x = fmaxf(x, buf[base + w]);
+    }
+    return x;
+}
+
+// Index of a lane's k-th vector in its row (in vectors).
+template <int K>
+__device__ __forceinline__ int vec_index(int ln, int k, int L)
+{
+    return L < 32 ? k * L + ln : ((ln >> 5) * K + k) * 32 + (ln & 31);
+}
+
+template <typename T, int EW>
+__device__ __forceinline__ void load_weight(const void *W, int wf32, int64_t j, float (&w)[EW])
+{
+    if (W == nullptr) {
+#pragma unroll
+        for (int e = 0; e < EW; ++e) w[e] = 1.0f;
+    } else if (wf32) {
+        const float *p = reinterpret_cast<const float *>(W) + j;
+#pragma unroll
+        for (int e = 0; e < EW; ++e) w[e] = __ldg(p + e);
+    } else {
+        const T *p = reinterpret_cast<const T *>(W) + j;
+        const Vec<T, EW> r = *reinterpret_cast<const Vec<T, EW> *>(p);
+        widen(r, w);
+    }
+}
+
+template <int EW>
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&y)[EW])
+{
+    if constexpr (EW == 1) {
+        *p = __nv_cvt_float_to_fp8(y[0], __NV_SATFINITE, __NV_E4M3);
+    } else {
+        uint16_t c[EW / 2];
+#pragma unroll
+        for (int e = 0; e < EW / 2; ++e)
+            c[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e], y[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
+        if constexpr (EW == 8)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+        else
+            *reinterpret_cast<uint32_t *>(p) = c[0] | (uint32_t)c[1] << 16;
+    }
+}
+
+struct NormArgs {
+    const void *X, *R, *W;
+    void *H, *Y;
+    float *scales, *rstd;
+    int64_t ldx, ldr, ldh, ldy, M;
+    int N, L, group, wf32;
+    float eps;
+};
+
+// One block per blockDim.x / L rows.
+template <typename T, int EW, int K, bool E4M3>
+__global__ void __launch_bounds__(kMostLanes<EW, K>) rmsnorm_kernel(const __grid_constant__ NormArgs a)
+{
+    __shared__ float buf[2][32];
+    pdl_trigger();
+    const int L = a.L, ln = threadIdx.x & (L - 1);
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / L) + threadIdx.x / L;
+    const bool live = row < a.M;
+    const T *x = reinterpret_cast<const T *>(a.X) + row * a.ldx;
+    const T *r = reinterpret_cast<const T *>(a.R) + row * a.ldr;
+    Vec<T, EW> vx[K], vr[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = vec_index<K>(ln, k, L) * EW;
+        if (live && j < a.N) {
+            load_vec(x + j, vx[k]);
+            if (a.R) load_vec(r + j, vr[k]);
+        }
+    }
+    float h[K][EW], ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = vec_index<K>(ln, k, L) * EW;
+        if (live && j < a.N) {
+            widen(vx[k], h[k]);
+            if (a.R) {
+                float f[EW];
+                widen(vr[k], f);
+#pragma unroll
+                for (int e = 0; e < EW; ++e) h[k][e] += f[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < EW; ++e) h[k][e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < EW; ++e) ss = fmaf(h[k][e], h[k][e], ss);
+    }
+    const float s = rsqrtf(row_sum(ss, L, buf[0]) / (float)a.N + a.eps);
+    pdl_wait();  // loads may run ahead of the kernel before, stores may not
+    if (live && a.rstd && ln == 0) a.rstd[row] = s;
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = vec_index<K>(ln, k, L) * EW;
+        if (live && j < a.N) {
+            if (a.H) {
+                Vec<T, EW> o;
+                narrow(h[k], o);
+                store_vec(reinterpret_cast<T *>(a.H) + row * a.ldh + j, o);
+            }
+            float w[EW];
+            load_weight<T, EW>(a.W, a.wf32, j, w);
+#pragma unroll
+            for (int e = 0; e < EW; ++e) h[k][e] = h[k][e] * s * w[e];
+            if constexpr (!E4M3) {
+                Vec<T, EW> o;
+                narrow(h[k], o);
+                store_vec(reinterpret_cast<T *>(a.Y) + row * a.ldy + j, o);
+            }
+        }
+        if constexpr (E4M3) {
+#pragma unroll
+            for (int e = 0; e < EW; ++e) top = fmaxf(top, fabsf(h[k][e]));
+        }
+    }
+    if constexpr (E4M3) {
+        uint8_t *y = reinterpret_cast<uint8_t *>(a.Y) + row * a.ldy;
+        if (a.group == 0) {
+            top = row_max(top, L, buf[1]);
+            const float inv = top > 0.0f ? 448.0f / top : 1.0f;
+            if (live && ln == 0) a.scales[row] = top > 0.0f ? top / 448.0f : 1.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int j = vec_index<K>(ln, k, L) * EW;
+                if (live && j < a.N) {
+#pragma unroll
+                    for (int e = 0; e < EW; ++e) h[k][e] *= inv;
+                    store_e4m3<EW>(y + j, h[k]);
+                }
+            }
+        } else {
+            // group columns = lanes x EW (EW > 1), or 32 lanes x kk registers (EW = 1)
+            const int ng = (a.N + a.group - 1) / a.group;
+            constexpr int KK = EW > 1 ? 1 : K;
+            const int per = EW > 1 ? 1 : a.group / 32;  // consecutive k of one group
+            const int lanes = EW > 1 ? a.group / EW : 32;
+            float m[KK];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float t = 0.0f;
+#pragma unroll
+                for (int e = 0; e < EW; ++e) t = fmaxf(t, fabsf(h[k][e]));
+                if constexpr (EW > 1) {
+                    t = lanes_max(t, lanes);
+                    const int j = vec_index<K>(ln, k, L) * EW;
+                    if (live && j < a.N) {
+                        const float inv = t > 0.0f ? 448.0f / t : 1.0f;
+                        if ((threadIdx.x & (lanes - 1)) == 0)
+                            a.scales[row * ng + j / a.group] = t > 0.0f ? t / 448.0f : 1.0f;
+#pragma unroll
+                        for (int e = 0; e < EW; ++e) h[k][e] *= inv;
+                        store_e4m3<EW>(y + j, h[k]);
+                    }
+                } else {
+                    m[k] = lanes_max(t, 32);
+                }
+            }
+            if constexpr (EW == 1) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    float t = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < K; ++q)
+                        if (q / per == k / per) t = fmaxf(t, m[q]);
+                    const int j = vec_index<K>(ln, k, L);
+                    if (live && j < a.N) {
+                        if (j % a.group == 0) a.scales[row * ng + j / a.group] = t > 0.0f ? t / 448.0f : 1.0f;
+                        const float v[1] = {h[k][0] * (t > 0.0f ? 448.0f / t : 1.0f)};
+                        store_e4m3<1>(y + j, v);
+                    }
+                }
+            }
+        }
+    }
+}
+
+struct NormBwdArgs {
+    const void *DY, *H, *W, *DR;
+    const float *rstd;
+    void *DX;
+    float *part;  // [gridDim.x, N]: each block's share of dw
+    int64_t lddy, ldh, lddr, lddx, M;
+    int N, L, wf32;
+};
+
+// A block walks rows blockIdx.x, + gridDim.x, ... in each of its blockDim.x / L
+// slots, adding dy n into its own columns' dw: in registers, or for rows of
+// 1024 lanes (64 registers each) in its own words of shared memory.  At the end the slots' sums meet in shared memory and one row of
+// partials goes out; a second launch adds the blocks' rows in order.
+template <typename T, int EW, int K>
+__global__ void __launch_bounds__(kMostLanes<EW, K>) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdArgs a)
+{
+    constexpr bool kRegs = kMostLanes<EW, K> == 512;
+    extern __shared__ float acc[];  // [N] floats, zeroed here
+    __shared__ float buf[2][32];
+    pdl_trigger();
+    const int L = a.L, ln = threadIdx.x & (L - 1), slots = blockDim.x / L, slot = threadIdx.x / L;
+    for (int j = threadIdx.x; j < a.N; j += blockDim.x) acc[j] = 0.0f;
+    float dw[kRegs ? K : 1][EW];
+#pragma unroll
+    for (int k = 0; k < (kRegs ? K : 1); ++k)
+#pragma unroll
+        for (int e = 0; e < EW; ++e) dw[k][e] = 0.0f;
+    __syncthreads();
+    bool wrote = false;
+    int turn = 0;
+    // the same number of steps for every slot: row_sum holds a barrier
+    for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < a.M; r0 += (int64_t)gridDim.x * slots, turn ^= 1) {
+        const int64_t row = r0 + slot;
+        const bool live = row < a.M;
+        const T *dy = reinterpret_cast<const T *>(a.DY) + row * a.lddy;
+        const T *h = reinterpret_cast<const T *>(a.H) + row * a.ldh;
+        const T *dr = reinterpret_cast<const T *>(a.DR) + row * a.lddr;
+        Vec<T, EW> vy[K], vh[K], vr[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = vec_index<K>(ln, k, L) * EW;
+            if (live && j < a.N) {
+                load_vec(dy + j, vy[k]);
+                load_vec(h + j, vh[k]);
+                if (a.DR) load_vec(dr + j, vr[k]);
+            }
+        }
+        const float s = live ? a.rstd[row] : 0.0f;
+        float c = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = vec_index<K>(ln, k, L) * EW;
+            if (live && j < a.N) {
+                float fy[EW], fh[EW], w[EW];
+                widen(vy[k], fy);
+                widen(vh[k], fh);
+                load_weight<T, EW>(a.W, a.wf32, j, w);
+#pragma unroll
+                for (int e = 0; e < EW; ++e) {
+                    const float n = fh[e] * s;
+                    c = fmaf(fy[e] * w[e], n, c);
+                    if constexpr (kRegs)
+                        dw[k][e] = fmaf(fy[e], n, dw[k][e]);
+                    else
+                        acc[j + e] = fmaf(fy[e], n, acc[j + e]);  // one slot: L is the whole block
+                }
+            }
+        }
+        c = row_sum(c, L, buf[turn]) / (float)a.N;
+        if (!wrote) pdl_wait();
+        wrote = true;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = vec_index<K>(ln, k, L) * EW;
+            if (live && j < a.N) {
+                float fy[EW], fh[EW], w[EW], o[EW];
+                widen(vy[k], fy);
+                widen(vh[k], fh);
+                load_weight<T, EW>(a.W, a.wf32, j, w);
+#pragma unroll
+                for (int e = 0; e < EW; ++e) o[e] = s * (fy[e] * w[e] - fh[e] * s * c);
+                if (a.DR) {
+                    float fr[EW];
+                    widen(vr[k], fr);
+#pragma unroll
+                    for (int e = 0; e < EW; ++e) o[e] += fr[e];
+                }
+                Vec<T, EW> v;
+                narrow(o, v);
+                store_vec(reinterpret_cast<T *>(a.DX) + row * a.lddx + j, v);
+            }
+        }
+    }
+    if (!wrote) pdl_wait();
+    if (a.part == nullptr) return;
+    float *out = a.part + (int64_t)blockIdx.x * a.N;
+    if constexpr (kRegs) {
+        for (int q = 0; q < slots; ++q) {
+            if (slot == q) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int j = vec_index<K>(ln, k, L) * EW;
+                    if (j < a.N) {
+#pragma unroll
+                        for (int e = 0; e < EW; ++e) acc[j + e] += dw[k][e];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    } else {
+        __syncthreads();
+    }
+    for (int j = threadIdx.x; j < a.N; j += blockDim.x) out[j] = acc[j];
+}
+
+// dw[j] = sum over the P blocks' partial rows: 32 columns x 8 lanes a block,
+// each lane every 8th row in order, then the 8 lanes in order.
+template <typename TW>
+__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float *__restrict__ part, TW *__restrict__ dw, int P,
+                                                         int N)
+{
+    __shared__ float s[8][33];
+    pdl_trigger();
+    pdl_wait();
+    const int col = threadIdx.x & 31, ln = threadIdx.x >> 5;
+    const int j = blockIdx.x * 32 + col;
+    float t = 0.0f;
+    if (j < N) {
+#pragma unroll 8
+        for (int p = ln; p < P; p += 8) t += __ldcg(part + (int64_t)p * N + j);
+    }
+    s[ln][col] = t;
+    __syncthreads();
+    if (ln == 0 && j < N) {
+#pragma unroll
+        for (int q = 1; q < 8; ++q) t += s[q][col];
+        dw[j] = from_f<TW>(t);
+    }
+}
+
+// Lanes a row (L) and vectors a lane (K) for nv vectors: about `want` vectors
+// a lane, at least `least` lanes.  Up to 512 lanes of 1, 2 or 4 vectors (8
+// single elements); rows beyond that take 1024 lanes and the instance with the
+// most vectors a lane (8, or 32 single elements), whose registers are scarce.
+void pick_lanes(int64_t nv, int want, int least, bool single, int *L, int *K)
+{
+    const int most = single ? 8 : 4;
+    int l = least;
+    while (l < 512 && (int64_t)l * want < nv) l *= 2;
+    if ((int64_t)l * most < nv) {
+        *L = 1024;
+        *K = single ? 32 : 8;
+        return;
+    }
+    int k = single ? 8 : 1;
+    while ((int64_t)l * k < nv) k *= 2;
+    *L = l;
+    *K = k;
+}
+
+template <typename T, int EW, bool E4M3>
+const void *norm_kernel(int K)
+{
+    if constexpr (EW == 1) return K <= 8 ? (const void *)rmsnorm_kernel<T, 1, 8, E4M3> : (const void *)rmsnorm_kernel<T, 1, 32, E4M3>;
+    switch (K) {
+    case 1: return (const void *)rmsnorm_kernel<T, EW, 1, E4M3>;
+    case 2: return (const void *)rmsnorm_kernel<T, EW, 2, E4M3>;
+    case 4: return (const void *)rmsnorm_kernel<T, EW, 4, E4M3>;
+    default: return (const void *)rmsnorm_kernel<T, EW, 8, E4M3>;
+    }
+}
+
+template <typename T, int EW>
+const void *norm_bwd_kernel(int K)
+{
+    if constexpr (EW == 1) return K <= 8 ? (const void *)rmsnorm_bwd_kernel<T, 1, 8> : (const void *)rmsnorm_bwd_kernel<T, 1, 32>;
+    switch (K) {
+    case 1: return (const void *)rmsnorm_bwd_kernel<T, EW, 1>;
+    case 2: return (const void *)rmsnorm_bwd_kernel<T, EW, 2>;
+    case 4: return (const void *)rmsnorm_bwd_kernel<T, EW, 4>;
+    default: return (const void *)rmsnorm_bwd_kernel<T, EW, 8>;
+    }
+}
+
+constexpr int64_t kBwdBlocks = 608;  // dw partial rows at most: 152 SMs x 4 blocks
+
+struct BwdPlan {
+    int L, K, threads;
+    int64_t blocks;
+};
+
+BwdPlan bwd_plan(int64_t M, int64_t N, int EW)
+{
+    BwdPlan p;
+    const int64_t nv = (N + EW - 1) / EW;
+    pick_lanes(nv, EW == 1 ? 8 : 16 / EW, EW == 1 ? 32 : 8, EW == 1, &p.L, &p.K);
+    p.threads = p.L < 256 ? 256 : p.L;
+    const int64_t per = p.threads / p.L;
+    p.blocks = (M + per - 1) / per;
+    if (p.blocks > kBwdBlocks) p.blocks = kBwdBlocks;
+    return p;
+}
+
+bool type_ok(int32_t t) { return elem_bytes(t) != 0; }
+
+}  // namespace
+}  // namespace libtm
+
+using namespace libtm;
+
+extern "C" tm_status tm_rmsnorm(const void *X, int64_t ldx, const void *R, int64_t ldr, void *H, int64_t ldh,
+                                const void *W, int64_t M, int64_t N, float eps, void *Y, int64_t ldy, float *scales,
+                                float *rstd, int32_t xtype, int32_t wtype, int32_t ytype, int32_t group,
+                                uint32_t flags, tm_stream_t stream)
+{
+    const bool e4 = ytype == TM_E4M3;
+    if (!type_ok(xtype) || (wtype != xtype && wtype != TM_F32) || (!e4 && ytype != xtype)) return TM_ERR_INVALID_ARG;
+    if (flags & ~TM_PDL) return TM_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f)) return TM_ERR_INVALID_ARG;
+    if (!valid_rows(X, ldx, M, N) || !valid_rows(Y, ldy, M, N)) return TM_ERR_INVALID_ARG;
+    if (R != nullptr && !valid_rows(R, ldr, M, N)) return TM_ERR_INVALID_ARG;
+    if (H != nullptr && !valid_rows(H, ldh, M, N)) return TM_ERR_INVALID_ARG;
+    if (group != 0 && (!e4 || (group != 32 && group != 64 && group != 128))) return TM_ERR_UNSUPPORTED_TILE;
+    if (N > kMaxCols) return TM_ERR_UNSUPPORTED_TILE;
+    if (e4 ? (M > 0 && N > 0 && scales == nullptr) : scales != nullptr) return TM_ERR_INVALID_ARG;
+    const int e = elem_bytes(xtype), we = elem_bytes(wtype);
+    if (!aligned_to(X, e) || !aligned_to(R, e) || !aligned_to(H, e) || !aligned_to(W, we) || !aligned_to(scales, 4) ||
+        !aligned_to(rstd, 4) || (!e4 && !aligned_to(Y, e)))
+        return TM_ERR_MISALIGNED;
+    if (M == 0 || N == 0) return TM_OK;
+    const Span sx = span_of(X, ldx, M, N, e), sr = span_of(R, ldr, M, N, e), sh = span_of(H, ldh, M, N, e);
+    const Span sy = span_of(Y, ldy, M, N, e4 ? 1 : e), sw = span_of(W, N, W ? 1 : 0, N, we);
+    const int64_t ng = group ? (N + group - 1) / group : 1;
+    const Span ss = span_of(scales, ng, scales ? M : 0, ng, 4), sd = span_of(rstd, 1, rstd ? M : 0, 1, 4);
+    // In place: H or Y may be X or R exactly (same base, same ld, same type);
+    // every other overlap of an output with anything is refused.
+    auto clash = [&](const void *o, int64_t ldo, const Span &so, bool same_type, const void *p, int64_t ldp,
+                     const Span &sp) { return meets(so, sp) && !(same_type && o == p && ldo == ldp); };
+    if (clash(H, ldh, sh, true, X, ldx, sx) || clash(H, ldh, sh, true, R, ldr, sr) ||
+        clash(Y, ldy, sy, !e4, X, ldx, sx) || clash(Y, ldy, sy, !e4, R, ldr, sr))
+        return TM_ERR_INVALID_ARG;
+    const Span outs[] = {sh, sy, ss, sd};
+    for (int i = 0; i < 4; ++i) {
+        if (meets(outs[i], sw)) return TM_ERR_INVALID_ARG;
+        if (i >= 2 && (meets(outs[i], sx) || meets(outs[i], sr))) return TM_ERR_INVALID_ARG;
+        for (int k = 0; k < i; ++k)
+            if (meets(outs[i], outs[k])) return TM_ERR_INVALID_ARG;
+    }
+
+    const int EWv = 16 / e;
+    const bool vec = N % EWv == 0 && ldx % EWv == 0 && aligned_to(X, 16) &&
+                     (!R || (ldr % EWv == 0 && aligned_to(R, 16))) && (!H || (ldh % EWv == 0 && aligned_to(H, 16))) &&
+                     ldy % EWv == 0 && aligned_to(Y, e4 ? EWv : 16) && (!W || wtype == TM_F32 || aligned_to(W, 16));
+    const int EW = vec ? EWv : 1;
+    const int64_t nv = (N + EW - 1) / EW;
+    int L, K;
+    if (vec) {
+        // few rows: one vector a lane, the shortest chain; many: four, so that
+        // each lane has that many loads in flight
+        pick_lanes(nv, M <= 304 ? 1 : 4, group ? 32 : 8, false, &L, &K);
+    } else {
+        pick_lanes(nv, 8, 32, true, &L, &K);
+    }
+    const int threads = L < 128 ? 128 : L;
+    const int64_t rows = threads / L, blocks = (M + rows - 1) / rows;
+    if (blocks > INT32_MAX) return TM_ERR_INVALID_ARG;
+    const DevInfo *dev;
+    tm_status st = device_info(&dev);
+    if (st != TM_OK) return st;
+    NormArgs a = {X, R, W, H, Y, scales, rstd, ldx, ldr, ldh, ldy, M, (int)N, L, group, wtype == TM_F32, eps};
+    const void *k = nullptr;
+#define PICK(T, EV)                                                                             \
+    k = vec ? (e4 ? norm_kernel<T, EV, true>(K) : norm_kernel<T, EV, false>(K))                 \
+            : (e4 ? norm_kernel<T, 1, true>(K) : norm_kernel<T, 1, false>(K))
+    if (xtype == TM_F32) {
+        PICK(float, 4);
+    } else if (xtype == TM_F16) {
+        PICK(__half, 8);
+    } else {
+        PICK(__nv_bfloat16, 8);
+    }
+#undef PICK
+    void *args[] = {&a};
+    return launch_kernel(k, dim3((unsigned)blocks), dim3(threads), args, 0, as_stream(stream), (flags & TM_PDL) != 0);
+}
+
+extern "C" size_t tm_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t N)
+{
+    if (M <= 0 || N <= 0 || N > kMaxCols) return 0;
+    return (size_t)(M < kBwdBlocks ? M : kBwdBlocks) * (size_t)N * sizeof(float);
+}
+
+extern "C" tm_status tm_rmsnorm_bwd(const void *DY, int64_t lddy, const void *H, int64_t ldh, const void *W,
+                                    const float *rstd, const void *DR, int64_t lddr, void *DX, int64_t lddx, void *DW,
+                                    int64_t M, int64_t N, int32_t xtype, int32_t wtype, void *workspace,
+                                    size_t ws_bytes, uint32_t flags, tm_stream_t stream)
+{
+    if (!type_ok(xtype) || (wtype != xtype && wtype != TM_F32)) return TM_ERR_INVALID_ARG;
+    if (flags & ~TM_PDL) return TM_ERR_INVALID_ARG;
+    if (!valid_rows(DY, lddy, M, N) || !valid_rows(H, ldh, M, N) || !valid_rows(DX, lddx, M, N))
+        return TM_ERR_INVALID_ARG;
+    if (DR != nullptr && !valid_rows(DR, lddr, M, N)) return TM_ERR_INVALID_ARG;
+    if (M > 0 && N > 0 && rstd == nullptr) return TM_ERR_INVALID_ARG;
+    if (N > kMaxCols) return TM_ERR_UNSUPPORTED_TILE;
+    const int e = elem_bytes(xtype), we = elem_bytes(wtype);
+    if (!aligned_to(DY, e) || !aligned_to(H, e) || !aligned_to(DR, e) || !aligned_to(DX, e) || !aligned_to(W, we) ||
+        !aligned_to(DW, we) || !aligned_to(rstd, 4))
+        return TM_ERR_MISALIGNED;
+    if (N == 0) return TM_OK;
+    const size_t need = tm_rmsnorm_bwd_workspace_bytes(M, N);
+    if (DW != nullptr && M > 0 && (workspace == nullptr || ws_bytes < need || !aligned_to(workspace, 16)))
+        return TM_ERR_WORKSPACE;
+    const Span sy = span_of(DY, lddy, M, N, e), sh = span_of(H, ldh, M, N, e), sr = span_of(DR, lddr, M, N, e);
+    const Span sx = span_of(DX, lddx, M, N, e), sw = span_of(W, N, W ? 1 : 0, N, we);
+    const Span sdw = span_of(DW, N, DW ? 1 : 0, N, we), sd = span_of(rstd, 1, M, 1, 4);
+    const Span sws = DW && M > 0 ? span_of(workspace, (int64_t)need, 1, (int64_t)need, 1) : Span{0, 0};
+    auto clash = [&](const void *p, int64_t ldp, const Span &sp) { return meets(sx, sp) && !(DX == p && lddx == ldp); };
+    if (clash(DY, lddy, sy) || clash(H, ldh, sh) || clash(DR, lddr, sr)) return TM_ERR_INVALID_ARG;
+    const Span ins[] = {sy, sh, sr, sw, sd};
+    for (const Span &s : ins)
+        if (meets(s, sdw) || meets(s, sws)) return TM_ERR_INVALID_ARG;
+    if (meets(sx, sw) || meets(sx, sd) || meets(sx, sdw) || meets(sx, sws) || meets(sdw, sws)) return TM_ERR_INVALID_ARG;
+    if (M == 0 && DW == nullptr) return TM_OK;
+
+    const int EWv = 16 / e;
+    const bool vec = N % EWv == 0 && lddy % EWv == 0 && aligned_to(DY, 16) && ldh % EWv == 0 && aligned_to(H, 16) &&
+                     lddx % EWv == 0 && aligned_to(DX, 16) && (!DR || (lddr % EWv == 0 && aligned_to(DR, 16))) &&
+                     (!W || wtype == TM_F32 || aligned_to(W, 16));
+    const BwdPlan p = bwd_plan(M, N, vec ? EWv : 1);
+    const DevInfo *dev;
+    tm_status st = device_info(&dev);
+    if (st != TM_OK) return st;
+    cudaStream_t s = as_stream(stream);
+    if (M > 0) {
+        NormBwdArgs a = {DY, H, W, DR, rstd, DX, DW ? reinterpret_cast<float *>(workspace) : nullptr,
+                         lddy, ldh, lddr, lddx, M, (int)N, p.L, wtype == TM_F32};
+        const void *k = xtype == TM_F32   ? (vec ? norm_bwd_kernel<float, 4>(p.K) : norm_bwd_kernel<float, 1>(p.K))
+                        : xtype == TM_F16 ? (vec ? norm_bwd_kernel<__half, 8>(p.K) : norm_bwd_kernel<__half, 1>(p.K))
+                                          : (vec ? norm_bwd_kernel<__nv_bfloat16, 8>(p.K)
+                                                 : norm_bwd_kernel<__nv_bfloat16, 1>(p.K));
+        const size_t smem = (size_t)N * sizeof(float);
+        if (smem > 40 * 1024 &&
+            cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+            cudaGetLastError();
+            return TM_ERR_CUDA;
+        }
+        void *args[] = {&a};
+        st = launch_kernel(k, dim3((unsigned)p.blocks), dim3(p.threads), args, smem, s, (flags & TM_PDL) != 0);
+        if (st != TM_OK) return st;
+    }
+    if (DW != nullptr) {
+        const float *part = reinterpret_cast<const float *>(workspace);
+        int P = M > 0 ? (int)p.blocks : 0, n = (int)N;
+        void *args[] = {&part, &DW, &P, &n};
+        const void *k = wtype == TM_F32   ? (const void *)rmsnorm_dw_kernel<float>
+                        : wtype == TM_F16 ? (const void *)rmsnorm_dw_kernel<__half>
+                                          : (const void *)rmsnorm_dw_kernel<__nv_bfloat16>;
+        return launch_dependent(k, dim3((unsigned)((N + 31) / 32)), dim3(256), args, 0, s);
+    }
+    return TM_OK;
+}

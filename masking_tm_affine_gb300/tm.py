@@ -26,6 +26,7 @@ TM_ERR_BROKEN_PROMISE = 4
 TM_ERR_CUDA = 5
 TM_ERR_WORKSPACE = 6
 TM_ERR_TIMEOUT = 7
+TM_ERR_INDEX = 8
 
 # flags
 TM_ALIGNED = 0x1
@@ -72,6 +73,20 @@ SIGNATURES = {
     "tm_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "tm_gemm": (_st, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _f32, _f32, _i32, _i32, _i32, _u32,
                       _vp, _sz, _vp]),
+    "tm_rmsnorm": (_st, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _vp, _i64, _vp, _vp, _i32, _i32, _i32,
+                         _i32, _u32, _vp]),
+    "tm_rmsnorm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "tm_rmsnorm_bwd": (_st, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _sz,
+                             _u32, _vp]),
+    "tm_rope_turns": (_st, [_vp, _i32, _f32, _i32, _f32, _f32, _f32, _i64]),
+    "tm_rope": (_st, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _f32, _i32, _u32, _vp]),
+    "tm_kv4_page_bytes": (_sz, [_i32, _i32, _i32]),
+    "tm_kv4_append": (_st, [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                            _i64, _i32, _i64, _i32, _i32, _i32, _f32, _i32, _u32, _vp]),
+    "tm_kv4_gather": (_st, [_vp, _i64, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _u32, _vp]),
+    "tm_kv4_attention_workspace_bytes": (_sz, [_i32, _i64, _i32, _i64, _i32, _i32, _i32]),
+    "tm_kv4_attention": (_st, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _i64,
+                               _i32, _i64, _i32, _i32, _i32, _f32, _i32, _i32, _vp, _sz, _u32, _vp]),
     "tm_check": (_st, [_vp]),
     "tm_tile_walk_probe": (_st, [_i64, _i32, _vp, _vp]),
     "tm_scale2d_unchecked": (_st, [_vp, _i64, _vp, _i64, _i64, _i64, _f32, _i32, _i32, _vp]),
@@ -232,6 +247,90 @@ def tm_gemm(A, lda: int, B, ldb: int, C, ldc: int, M: int, N: int, K: int, alpha
     TM = 256 runs CTA pairs (the default, fastest); TM = 128 single CTAs."""
     _ok(load().tm_gemm(_ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, M, N, K, alpha, beta, TM, TN, TK, flags,
                        _ptr(workspace), ws_bytes, _stream(stream)), "tm_gemm")
+
+
+# Operators of a transformer block: element types, layouts and flags (include/tm.h)
+TM_F32 = 0
+TM_F16 = 1
+TM_BF16 = 2
+TM_E4M3 = 3
+TM_ROPE_PLAIN = 0
+TM_ROPE_LINEAR = 1
+TM_ROPE_BASE = 2
+TM_ROPE_BY_TURNS = 3
+TM_ROPE_BY_DIM = 4
+TM_ROPE_INTERLEAVED = 0x400
+TM_ROPE_INVERSE = 0x800
+TM_ATTN_FULL = 0x1000
+
+
+def tm_rmsnorm(X, ldx: int, R, ldr: int, H, ldh: int, W, M: int, N: int, eps: float, Y, ldy: int, scales=None,
+               rstd=None, xtype: int = TM_F32, wtype: int = TM_F32, ytype: int = TM_F32, group: int = 0,
+               flags: int = 0, stream=None) -> None:
+    """y = (x + r) * w / rms(x + r); with ytype TM_E4M3 in 8 bits, a scale a row or a group of columns."""
+    _ok(load().tm_rmsnorm(_ptr(X), ldx, _ptr(R), ldr, _ptr(H), ldh, _ptr(W), M, N, eps, _ptr(Y), ldy, _ptr(scales),
+                          _ptr(rstd), xtype, wtype, ytype, group, flags, _stream(stream)), "tm_rmsnorm")
+
+
+def tm_rmsnorm_bwd_workspace_bytes(M: int, N: int) -> int:
+    return int(load().tm_rmsnorm_bwd_workspace_bytes(M, N))
+
+
+def tm_rmsnorm_bwd(DY, lddy: int, H, ldh: int, W, rstd, DR, lddr: int, DX, lddx: int, DW, M: int, N: int,
+                   xtype: int = TM_F32, wtype: int = TM_F32, workspace=None, ws_bytes: int = 0, flags: int = 0,
+                   stream=None) -> None:
+    _ok(load().tm_rmsnorm_bwd(_ptr(DY), lddy, _ptr(H), ldh, _ptr(W), _ptr(rstd), _ptr(DR), lddr, _ptr(DX), lddx,
+                              _ptr(DW), M, N, xtype, wtype, _ptr(workspace), ws_bytes, flags, _stream(stream)),
+        "tm_rmsnorm_bwd")
+
+
+def tm_rope_turns(rot: int, base: float, scaling: int = TM_ROPE_PLAIN, factor: float = 1.0, low: float = 0.0,
+                  high: float = 0.0, orig: int = 0):
+    """The rot/2 frequencies tm_rope and tm_kv4_append take, as a host ctypes array of unsigned 64-bit values
+    (``numpy.ctypeslib.as_array(t).view("int64")`` makes it an array to copy to the device)."""
+    arr = (ctypes.c_uint64 * max(rot // 2, 1))()
+    _ok(load().tm_rope_turns(ctypes.cast(arr, ctypes.c_void_p), rot, base, scaling, factor, low, high, orig),
+        "tm_rope_turns")
+    return arr
+
+
+def tm_rope(X, xs_tok: int, xs_head: int, Y, ys_tok: int, ys_head: int, pos, turns, T: int, H: int, D: int, rot: int,
+            gain: float = 1.0, xtype: int = TM_F32, flags: int = 0, stream=None) -> None:
+    _ok(load().tm_rope(_ptr(X), xs_tok, xs_head, _ptr(Y), ys_tok, ys_head, _ptr(pos), _ptr(turns), T, H, D, rot, gain,
+                       xtype, flags, _stream(stream)), "tm_rope")
+
+
+def tm_kv4_page_bytes(Hkv: int, D: int, page: int) -> int:
+    return int(load().tm_kv4_page_bytes(Hkv, D, page))
+
+
+def tm_kv4_append(Q, qs_tok: int, qs_head: int, QO, qos_tok: int, qos_head: int, Hq: int, K, ks_tok: int, ks_head: int,
+                  V, vs_tok: int, vs_head: int, pos, turns, slots, pool, pages: int, page: int, T: int, Hkv: int,
+                  D: int, rot: int, gain: float = 1.0, xtype: int = TM_F32, flags: int = 0, stream=None) -> None:
+    """Rotate q into QO and k into the 4-bit cache, v as it is, in one launch."""
+    _ok(load().tm_kv4_append(_ptr(Q), qs_tok, qs_head, _ptr(QO), qos_tok, qos_head, Hq, _ptr(K), ks_tok, ks_head,
+                             _ptr(V), vs_tok, vs_head, _ptr(pos), _ptr(turns), _ptr(slots), _ptr(pool), pages, page, T,
+                             Hkv, D, rot, gain, xtype, flags, _stream(stream)), "tm_kv4_append")
+
+
+def tm_kv4_gather(pool, pages: int, page: int, slots, K, ks_tok: int, ks_head: int, V, vs_tok: int, vs_head: int,
+                  T: int, Hkv: int, D: int, xtype: int = TM_F32, flags: int = 0, stream=None) -> None:
+    _ok(load().tm_kv4_gather(_ptr(pool), pages, page, _ptr(slots), _ptr(K), ks_tok, ks_head, _ptr(V), vs_tok, vs_head,
+                             T, Hkv, D, xtype, flags, _stream(stream)), "tm_kv4_gather")
+
+
+def tm_kv4_attention_workspace_bytes(B: int, Tq: int, max_q: int, max_len: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().tm_kv4_attention_workspace_bytes(B, Tq, max_q, max_len, Hq, Hkv, D))
+
+
+def tm_kv4_attention(Q, qs_tok: int, qs_head: int, O, os_tok: int, os_head: int, lse, pool, pages: int, page: int,
+                     table, ldt: int, lens, qstart, B: int, Tq: int, max_q: int, max_len: int, Hq: int, Hkv: int,
+                     D: int, scale: float, window: int = 0, xtype: int = TM_F32, workspace=None, ws_bytes: int = 0,
+                     flags: int = 0, stream=None) -> None:
+    """Attention of each sequence's newest queries over its pages of the 4-bit cache."""
+    _ok(load().tm_kv4_attention(_ptr(Q), qs_tok, qs_head, _ptr(O), os_tok, os_head, _ptr(lse), _ptr(pool), pages, page,
+                                _ptr(table), ldt, _ptr(lens), _ptr(qstart), B, Tq, max_q, max_len, Hq, Hkv, D, scale,
+                                window, xtype, _ptr(workspace), ws_bytes, flags, _stream(stream)), "tm_kv4_attention")
 
 
 def tm_check(stream=None) -> None:
