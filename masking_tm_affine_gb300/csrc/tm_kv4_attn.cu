@@ -28,11 +28,16 @@
 // V is laid out in token pairs so that two byte permutes pair the tokens; P^T is
 // the first product's accumulator, transposed by movmatrix in registers.
 //
-// A block is one (sequence, KV head, row tile, split of the tokens).  Each of its
-// four warps streams its own tiles of 32 tokens through a private ring of bulk
-// copies (one or two per tile: a cache block is contiguous), so no barrier is in
-// the loop; each keeps its own running maximum, sum and output, joined at the
-// end in shared memory, and splits by a second launch.
+// Work.  An item is a (sequence, KV head, row tile); its tokens are cut into units of
+// 256.  The launch has as many blocks as the GPU holds at once, and each takes an
+// equal run of the concatenated units of all items, whatever the lengths: lengths
+// live on the device, so every block adds them up itself (one load and a scan).  A
+// block's run is a few segments of items; a segment that is a whole item writes its
+// output, the others write partial outputs that a second launch joins in order.
+// Each of a block's four warps streams its own tiles of 32 tokens through a private
+// ring of bulk copies (a cache block is contiguous: one or two copies a tile), so no
+// barrier is in the loop; each keeps its own running maximum, sum and output, joined
+// in shared memory at a segment's end.
 //
 // P stepV is rounded to fp16 for the second product: scaled by 2^E so that the
 // largest step seen lies in [2^14, 2^15), it is off by at most 2^-11 of itself,
@@ -48,7 +53,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTile = 32;    // tokens a warp takes at a time: two cache blocks
-constexpr int kMaxSplits = 256;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2eF = 1.4426950408889634f;
 
@@ -102,17 +106,22 @@ __device__ __forceinline__ uint32_t centred(uint32_t x, uint16_t middle)
 __device__ __forceinline__ uint32_t centred_even(uint32_t x) { return centred((x & 0x000f000fu) | 0x64006400u, 0x6408); }  // 1032
 __device__ __forceinline__ uint32_t centred_odd(uint32_t x) { return centred((x & 0x00f000f0u) | 0x64006400u, 0x6480); }   // 1152
 
+constexpr int kUnit = 256;             // tokens: two tiles a warp
+static_assert(kUnit % (kWarps * kTile) == 0, "a unit is whole tiles of every warp");
+constexpr int kMostBlocks = 608;       // 152 SMs x 4: what the workspace is sized for
+
 struct AttnArgs {
     const void *Q;
     void *O;
     float *lse;
     const uint8_t *pool;
     const int32_t *table, *lens, *qstart;
-    float *part;  // splits > 1: [splits][Tq * Hq][D] outputs, then [splits][Tq * Hq][2] (maximum, sum)
+    float *part;      // [2 gridDim.x] slots of [ROWS][D] outputs and [ROWS][2] (maximum, sum)
+    int64_t *prefix;  // [B]: units before each sequence, for the join; then the share of a block
     int64_t qs_tok, qs_head, os_tok, os_head, pages, page_bytes, ldt, Tq, max_len;
-    int page, B, Hq, Hkv, G, window, full, vec, row_tiles, splits, chunk;  // chunk: tokens a split
-    int max_q;
+    int B, Hq, Hkv, G, window, full, vec, max_q, blocks_per_page;
     float scale;
+    FastDiv by_page, by_group;  // cache blocks of a page, heads of a group
     unsigned *status;
 };
 
@@ -145,6 +154,34 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b, bool report)
     return s;
 }
 
+// Keys a query at place t of its sequence sees: [lower, upper).
+__device__ __forceinline__ int upper(const AttnArgs &a, const Seq &s, int t)
+{
+    return a.full ? s.len : min(s.len, max(0, s.len - s.n + t + 1));
+}
+__device__ __forceinline__ int lower(const AttnArgs &a, const Seq &s, int t)
+{
+    return a.window > 0 ? max(0, s.len - s.n + t + 1 - a.window) : 0;
+}
+
+// Row tiles of a sequence, and the units each of its items counts (one at
+// least: an item that sees nothing still has its zeros to write).  With a
+// window every row tile counts as many units as the widest could need.
+struct Load {
+    int tiles, units;
+    __device__ __forceinline__ int64_t total(int Hkv) const { return (int64_t)tiles * units * Hkv; }
+};
+
+__device__ __forceinline__ Load load_of(const AttnArgs &a, const Seq &s, int rows_of_tile)
+{
+    Load l;
+    l.tiles = (s.n * a.G + rows_of_tile - 1) / rows_of_tile;
+    int range = s.len;
+    if (a.window > 0) range = min(range, a.window + rows_of_tile / a.G + 1 + kTile);
+    l.units = max(1, (range + kUnit - 1) / kUnit);
+    return l;
+}
+
 template <int D>
 __host__ __device__ constexpr int stage_bytes()
 {
@@ -165,9 +202,18 @@ __host__ __device__ constexpr int attn_smem()
     return kWarps * ring_stages<D>() * stage_bytes<D>() + 128;
 }
 
+// Blocks an SM holds, by registers (the instances with 16 column rows or two fp16
+// parts need more) and shared memory.
+template <typename T, int D, int NT>
+__host__ __device__ constexpr int blocks_per_sm()
+{
+    return NT > 1 ? 2 : sizeof(T) == 4 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : D == 256 ? 3 : 4;
+}
+
 // T: element type.  NT: column tiles of 8 query rows.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_constant__ AttnArgs a)
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
+    kv4_attn_kernel(const __grid_constant__ AttnArgs a)
 {
     constexpr bool SPLIT = sizeof(T) == 4;     // two fp16 parts
     constexpr int PARTS = SPLIT ? 2 : 1;
@@ -178,36 +224,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_cons
     constexpr int ROWS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps][STAGES];
+    __shared__ int64_t scan[kWarps + 1], found_base;
+    __shared__ int found_b;
 
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
-    // blockIdx.x = ((b * Hkv + h) * row_tiles + tile) * splits + split
-    int u = blockIdx.x;
-    const int split = u % a.splits;
-    u /= a.splits;
-    const int tile = u % a.row_tiles;
-    u /= a.row_tiles;
-    const int kvh = u % a.Hkv, b = u / a.Hkv;
-    const Seq seq = sequence(a, b, threadIdx.x == 0 && kvh == 0 && tile == 0 && split == 0);
-    const int rows = min(ROWS, seq.n * a.G - tile * ROWS);
-    if (rows <= 0) {
-        pdl_wait();
-        return;
-    }
-
-    // The tokens this row tile sees: [begin, end), and of those this split's.
-    const int t_first = tile * ROWS / a.G, t_last = (tile * ROWS + rows - 1) / a.G;
-    auto upper = [&](int t) { return a.full ? seq.len : min(seq.len, max(0, seq.len - seq.n + t + 1)); };
-    auto lower = [&](int t) { return a.window > 0 ? max(0, seq.len - seq.n + t + 1 - a.window) : 0; };
-    const int begin = lower(t_first) / kTile * kTile, end = upper(t_last);
-    const int c0 = begin + split * a.chunk, c1 = min(end, c0 + a.chunk);
-    const int tiles = c1 > c0 ? (c1 - c0 + kTile - 1) / kTile : 0;
-    if (a.splits > 1 && tiles == 0) {  // the join counts a row's splits the same way
-        pdl_wait();
-        return;
-    }
-
-    // ---- the copy ring: this warp's tiles are warp, warp + 4, ... of the split
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
     uint8_t *ring = smem + warp * (STAGES * SB);
     const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(&bars[warp][0]);
     if (lane == 0) {
@@ -217,54 +238,144 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_cons
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    __syncwarp();
-    const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-    const int32_t *trow = a.table + (int64_t)b * a.ldt;
-    const uint64_t policy = l2_evict_first_policy();
-    // Page numbers of this warp's tiles i .. i + 31 sit one a lane (two blocks of a
-    // tile can lie in two pages).
-    int page0 = 0, page1 = 0;
-    auto fetch_pages = [&](int i0) {
-        const int i = i0 + lane;
-        page0 = page1 = 0;
-        if (i < mine) {
-            const int tok = c0 + (warp + i * kWarps) * kTile;
-            page0 = trow[tok / a.page];
-            page1 = tok + 16 < end ? trow[(tok + 16) / a.page] : page0;
-            if (page0 < 0 || page0 >= a.pages || page1 < 0 || page1 >= a.pages) {
-                atomicOr(a.status, kStatusIndex);
-                page0 = page0 < 0 || page0 >= a.pages ? 0 : page0;
-                page1 = page1 < 0 || page1 >= a.pages ? 0 : page1;
+
+    // ---- this block's run of units: [pos, stop)
+    int64_t pos, stop, base = 0;
+    int b = 0;
+    {
+        // sum over the sequences of threads before this one, and all
+        auto scan_of = [&](int64_t x, int64_t &before) -> int64_t {
+            int64_t inc = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            __syncthreads();  // the last use of scan[]
+            if (lane == 31) scan[warp] = inc;
+            __syncthreads();
+            int64_t head = 0, all = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) head += scan[w];
+                all += scan[w];
+            }
+            before = head + inc - x;
+            return all;
+        };
+        int64_t mine = 0, before, all = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
+            const bool in = b0 + tid < a.B;
+            mine = 0;
+            if (in) mine = load_of(a, sequence(a, b0 + tid, blockIdx.x == 0), ROWS).total(a.Hkv);
+            const int64_t sum = scan_of(mine, before);
+            if (in && blockIdx.x == 0 && a.prefix) {
+                if (b0 == 0) pdl_wait();
+                a.prefix[b0 + tid] = all + before;
+            }
+            all += sum;
+        }
+        const int64_t share = (all + gridDim.x - 1) / gridDim.x;
+        if (blockIdx.x == 0 && tid == 0 && a.prefix) a.prefix[a.B] = share;
+        pos = share * blockIdx.x;
+        stop = min(all, pos + share);
+        if (pos >= stop) {
+            pdl_wait();
+            return;
+        }
+        const bool once = a.B <= kWarps * 32;  // one round: mine and before still hold
+        int64_t sofar = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
+            if (!once) {
+                mine = b0 + tid < a.B ? load_of(a, sequence(a, b0 + tid, false), ROWS).total(a.Hkv) : 0;
+                const int64_t sum = scan_of(mine, before);
+                before += sofar;
+                sofar += sum;
+            }
+            if (pos >= before && pos < before + mine) {
+                found_b = b0 + tid;
+                found_base = before;
             }
         }
-    };
-    auto issue = [&](int i) {  // every lane calls it; lane 0 copies
-        if ((i & 31) == 0) fetch_pages(i);
-        const int p0 = __shfl_sync(0xffffffffu, page0, i & 31), p1 = __shfl_sync(0xffffffffu, page1, i & 31);
-        if (lane == 0) {
-            const int tok = c0 + (warp + i * kWarps) * kTile, s = i % STAGES;
-            const bool two = tok + 16 < end;
-            const uint32_t dst = ring_s + s * SB, bar = bar_s + 8 * s;
-            const int64_t head = (int64_t)kvh * (a.page / 16);
-            const int blk0 = tok % a.page / 16, blk1 = (tok + 16) % a.page / 16;
-            const uint8_t *s0 = a.pool + p0 * a.page_bytes + (head + blk0) * BB;
-            const uint8_t *s1 = a.pool + p1 * a.page_bytes + (head + blk1) * BB;
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(two ? 2 * BB : BB)
-                         : "memory");
-            const bool joined = two && s1 == s0 + BB;
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
-                "%4;" ::"r"(dst), "l"(s0), "r"(joined ? 2 * BB : BB), "r"(bar), "l"(policy)
-                : "memory");
-            if (two && !joined)
+        __syncthreads();
+        b = found_b;
+        base = found_base;
+    }
+    const uint64_t policy = l2_evict_first_policy();
+    int stage = 0;       // of the next tile to read, in this warp's ring
+    uint32_t phase = 0;  // and its parity
+    int fill = 0;        // stage of the next tile to copy
+    bool alive = true;
+
+    while (pos < stop) {
+        // ---- the segment: units [unit0, unit0 + count) of an item
+        Seq seq = sequence(a, b, false);
+        Load load = load_of(a, seq, ROWS);
+        while (pos >= base + load.total(a.Hkv)) {
+            base += load.total(a.Hkv);
+            seq = sequence(a, ++b, false);
+            load = load_of(a, seq, ROWS);
+        }
+        const int64_t item = (pos - base) / load.units;
+        const int unit0 = (int)(pos - base - item * load.units);
+        const int kvh = (int)(item / load.tiles), tile = (int)(item - (int64_t)kvh * load.tiles);
+        const int count = (int)min((int64_t)(load.units - unit0), stop - pos);
+        const bool whole = count == load.units;
+        pos += count;
+        const int rows = min(ROWS, seq.n * a.G - tile * ROWS);
+        const int t_first = (int)fdiv(tile * ROWS, a.by_group), t_last = (int)fdiv(tile * ROWS + rows - 1, a.by_group);
+        const int begin = lower(a, seq, t_first) / kTile * kTile, end = upper(a, seq, t_last);
+        const int c0 = min(end, begin + unit0 * kUnit);
+        const int c1 = unit0 + count == load.units ? end : min(end, c0 + count * kUnit);
+        // Where every row of the tile sees every token: [safe0, safe1).
+        const int safe0 = lower(a, seq, t_last), safe1 = upper(a, seq, t_first);
+
+        // ---- the copies: this warp's tiles are warp, warp + 4, ... of the segment.  Of each
+        // 32 tiles a lane works out one's source (two blocks, which can lie in two
+        // pages) and copies it when its turn comes.
+        const int tiles = (c1 - c0 + kTile - 1) / kTile;
+        const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+        const int32_t *trow = a.table + (int64_t)b * a.ldt;
+        const uint8_t *src0 = nullptr, *src1 = nullptr;
+        int blocks = 0;  // of this lane's tile: 1, 2, or 3 for two that are adjacent
+        auto find = [&](int i) {
+            if (i < mine) {
+                const int blk = (c0 + (warp + i * kWarps) * kTile) / kBlockTokens;
+                const int e0 = (int)fdiv(blk, a.by_page), in0 = blk - e0 * a.blocks_per_page;
+                const bool two = (blk + 1) * kBlockTokens < end, next = in0 + 1 == a.blocks_per_page;
+                int p0 = trow[e0], p1 = two && next ? trow[e0 + 1] : p0;
+                if (p0 < 0 || p0 >= a.pages || p1 < 0 || p1 >= a.pages) {
+                    atomicOr(a.status, kStatusIndex);
+                    p0 = p0 < 0 || p0 >= a.pages ? 0 : p0;
+                    p1 = p1 < 0 || p1 >= a.pages ? 0 : p1;
+                }
+                const uint8_t *head = a.pool + (int64_t)kvh * a.blocks_per_page * BB;
+                src0 = head + p0 * a.page_bytes + (int64_t)in0 * BB;
+                src1 = next ? head + p1 * a.page_bytes : src0 + BB;
+                blocks = !two ? 1 : next ? 2 : 3;
+            }
+        };
+        auto issue = [&](int i) {
+            if ((i & 31) == 0) find(i + lane);
+            if (lane == (i & 31)) {
+                const uint32_t dst = ring_s + fill * SB, bar = bar_s + 8 * fill;
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                             "r"(blocks == 1 ? BB : 2 * BB)
+                             : "memory");
                 asm volatile(
                     "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                    "[%3], %4;" ::"r"(dst + BB), "l"(s1), "r"(BB), "r"(bar), "l"(policy)
+                    "[%3], %4;" ::"r"(dst), "l"(src0), "r"(blocks == 3 ? 2 * BB : BB), "r"(bar), "l"(policy)
                     : "memory");
-        }
-    };
-    int issued = 0;
-    for (; issued < STAGES && issued < mine; ++issued) issue(issued);
+                if (blocks == 2)
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], "
+                        "%2, [%3], %4;" ::"r"(dst + BB), "l"(src1), "r"(BB), "r"(bar), "l"(policy)
+                        : "memory");
+            }
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+        };
+        int issued = 0;
+        for (; issued < STAGES && issued < mine; ++issued) issue(issued);
 
     // ---- queries: lane (g, j) holds dims j D/4 .. of row g of each column tile, as the
     // second operand of the first product.  Scaled by a power of two common to all
@@ -274,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_cons
     float qsum[NT];
     float top = 0.0f;
     auto row_ptr = [&](int row) {
-        const int t = row / a.G, hh = row - t * a.G;
+        const int t = (int)fdiv(row, a.by_group), hh = row - t * a.G;
         return reinterpret_cast<const T *>(a.Q) + (seq.q0 + t) * a.qs_tok + (int64_t)(kvh * a.G + hh) * a.qs_head;
     };
     auto load_q8 = [&](int nt, int w, float (&f)[8]) {
@@ -361,18 +472,13 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_cons
     }
     float vcap = 0.0f, vscale = 1.0f;  // largest stepV is below vcap; vscale = 2^E
     int vexp = 0;
-    bool alive = true;
-
-    // Where every row of the tile sees every token: [safe0, safe1).
-    const int safe0 = lower(t_last), safe1 = upper(t_first);
-
     for (int i = 0; i < mine; ++i) {
-        const int s = i % STAGES, tok0 = c0 + (warp + i * kWarps) * kTile;
-        if (!mbar_wait_bounded(bar_s + 8 * s, (i / STAGES) & 1)) {
+        const int tok0 = c0 + (warp + i * kWarps) * kTile;
+        if (!mbar_wait_bounded(bar_s + 8 * stage, phase)) {
             alive = false;
             break;
         }
-        const uint8_t *st = ring + s * SB;
+        const uint8_t *st = ring + stage * SB;
         const bool masked = tok0 < safe0 || tok0 + kTile > safe1;
         float y[2][NT][4];
         float2 vp[2][2];
@@ -441,8 +547,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_cons
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int t = (tile * ROWS + nt * 8 + 2 * j + c) / a.G;
-                    const int hi = upper(t), lo = lower(t);
+                    const int t = (int)fdiv(tile * ROWS + nt * 8 + 2 * j + c, a.by_group);
+                    const int hi = upper(a, seq, t), lo = lower(a, seq, t);
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -580,12 +686,22 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_cons
         }
         __syncwarp();  // every lane has read the stage
         if (issued < mine) issue(issued++);
+        if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+        }
     }
     if (!alive) {
-        // let what is in flight land before the block's shared memory goes
+        // let what is in flight land before the block's shared memory goes: the
+        // stages from the one that did not come
         if (lane == 0) atomicOr(a.status, kStatusTimeout);
-        for (int i = max(0, issued - STAGES); i < issued; ++i)
-            mbar_wait_bounded(bar_s + 8 * (i % STAGES), (i / STAGES) & 1);
+        do {
+            mbar_wait_bounded(bar_s + 8 * stage, phase);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+        } while (stage != fill);
     }
     pdl_wait();
     if (!__syncthreads_and(alive)) return;
@@ -649,14 +765,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_cons
             }
             // dims of this part: 2 KP of every slice of 2 KS
             const int d = d2 / (2 * KP) * (2 * KS) + ps * 2 * KP + d2 % (2 * KP);
-            const int full_row = tile * ROWS + row, t = full_row / a.G, hq = kvh * a.G + full_row - t * a.G;
-            const int64_t q = (seq.q0 + t) * a.Hq + hq;
-            if (a.splits > 1) {
-                *reinterpret_cast<float2 *>(a.part + ((int64_t)split * all_rows + q) * D + d) = make_float2(v0, v1);
-                if (d == 0)
-                    *reinterpret_cast<float2 *>(a.part + (int64_t)a.splits * all_rows * D +
-                                                ((int64_t)split * all_rows + q) * 2) = make_float2(mm, ll);
+            if (!whole) {
+                // the first segment of a block starts inside an item or is slot 1's like any other
+                float *slot = a.part + (2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0)) * (ROWS * (D + 2));
+                *reinterpret_cast<float2 *>(slot + row * D + d) = make_float2(v0, v1);
+                if (d == 0) *reinterpret_cast<float2 *>(slot + ROWS * D + row * 2) = make_float2(mm, ll);
             } else {
+                const int full_row = tile * ROWS + row, t = (int)fdiv(full_row, a.by_group);
+                const int hq = kvh * a.G + full_row - t * a.G;
+                const int64_t q = (seq.q0 + t) * a.Hq + hq;
                 const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
                 T *out = reinterpret_cast<T *>(a.O) + (seq.q0 + t) * a.os_tok + hq * a.os_head + d;
                 if (a.vec) {
@@ -672,137 +789,132 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const __grid_cons
             }
         }
     }
+    // the ring takes copies again: after every thread's last look at the join's buffers
+    __syncthreads();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
 }
 
-// Joins the splits of one (query, head) a warp, in order.  Splits that a
-// sequence does not reach were not written: each row's count is recomputed.
+// Joins the partial outputs of an item's rows: 8 warps, W of them a row (1 or 8), each
+// every W-th partial, a lane D/32 dims; then a row's warps in order.  Items with few
+// partials (many items) take a warp a row, few items with many partials all eight.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ AttnArgs a, int rows_of_tile)
+__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ AttnArgs a, int rows_of_tile, int row_tiles,
+                                                       int W)
 {
+    constexpr int E = D / 32;
+    __shared__ float sums[8][D], stat[8];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), all_rows = a.Tq * a.Hq;
-    if (r >= all_rows) return;
-    const int64_t q = r / a.Hq;
-    const int hq = (int)(r - q * a.Hq);
-    // the sequence of query q: the last b with qstart[b] <= q
-    int b = (int)q;
-    if (a.qstart) {
-        int lo = 0, hi = a.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.qstart[mid] <= q) lo = mid; else hi = mid - 1;
-        }
-        b = lo;
-    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows_here = 8 / W, sub = warp % W;
+    // blockIdx.x = ((b * Hkv + kvh) * row_tiles + tile) * (rows_of_tile / rows_here) + part
+    const int parts = rows_of_tile / rows_here;
+    unsigned u = blockIdx.x;
+    const int row = (int)(u % parts) * rows_here + warp / W;
+    u /= parts;
+    const int tile = (int)(u % row_tiles);
+    u /= row_tiles;
+    const int b = (int)(u / a.Hkv), kvh = (int)(u - b * a.Hkv);
     const Seq seq = sequence(a, b, false);
-    int n = 0;
-    if (q >= seq.q0 && q < seq.q0 + seq.n) {
-        const int row = (int)(q - seq.q0) * a.G + hq % a.G, tile = row / rows_of_tile;
-        const int first = tile * rows_of_tile / a.G;
-        const int last = min(tile * rows_of_tile + rows_of_tile, seq.n * a.G) - 1;
-        const int t_last = last / a.G;
-        const int begin = a.window > 0 ? max(0, seq.len - seq.n + first + 1 - a.window) / kTile * kTile : 0;
-        const int end = a.full ? seq.len : min(seq.len, max(0, seq.len - seq.n + t_last + 1));
-        n = end > begin ? min(a.splits, (end - begin + a.chunk - 1) / a.chunk) : 0;
-    } else {
-        return;  // not a query of any sequence
-    }
-    const float *stat = a.part + (int64_t)a.splits * all_rows * D;
+    const Load load = load_of(a, seq, rows_of_tile);
+    if (tile >= load.tiles) return;
+    const int64_t share = a.prefix[a.B], first = a.prefix[b] + ((int64_t)kvh * load.tiles + tile) * load.units;
+    const int64_t c0 = first / share;
+    const int n = (int)((first + load.units - 1) / share - c0) + 1;
+    if (n == 1) return;  // one block had the whole item and wrote its output
+    const int stride = rows_of_tile * (D + 2);
+    const float *item = a.part + 2 * c0 * stride;
+    // partial p: the item's first block holds it in its slot 1, the others in slot 0
+    auto slot = [&](int p) { return item + (int64_t)(p == 0 ? 1 : 2 * p) * stride; };
     float mm = -INFINITY;
-    for (int s = lane; s < n; s += 32) mm = fmaxf(mm, stat[((int64_t)s * all_rows + r) * 2]);
+    for (int p = lane; p < n; p += 32) mm = fmaxf(mm, slot(p)[rows_of_tile * D + row * 2]);
     mm = lanes_max(mm, 32);
-    float ll = 0.0f, v[D / 32];
+    float ll = 0.0f, v[E];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) v[e] = 0.0f;
+    for (int e = 0; e < E; ++e) v[e] = 0.0f;
 #pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-        const float2 ms = *reinterpret_cast<const float2 *>(stat + ((int64_t)s * all_rows + r) * 2);
-        const float f = ms.x == -INFINITY ? 1.0f : ex2(ms.x - mm);
-        const float *p = a.part + ((int64_t)s * all_rows + r) * D + lane * (D / 32);
+    for (int p = sub; p < n; p += W) {
+        const float *q = slot(p);
+        const float2 ms = *reinterpret_cast<const float2 *>(q + rows_of_tile * D + row * 2);
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<float2 *>(x + e) = *reinterpret_cast<const float2 *>(q + row * D + lane * E + e);
+        const float f = ms.x == -INFINITY ? 1.0f : ex2(ms.x - mm);  // a share that saw nothing holds zeros
         ll = fmaf(ms.y, f, ll);
 #pragma unroll
-        for (int e = 0; e < D / 32; e += 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(p + e);
-            v[e] = fmaf(x.x, f, v[e]);
-            v[e + 1] = fmaf(x.y, f, v[e + 1]);
+        for (int e = 0; e < E; ++e) v[e] = fmaf(x[e], f, v[e]);
+    }
+    if (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = v[e];
+        if (lane == 0) stat[warp] = ll;
+        __syncthreads();
+        if (sub != 0) return;
+        for (int w = 1; w < W; ++w) {
+            ll += stat[warp + w];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] += sums[warp + w][lane * E + e];
         }
     }
+    if (tile * rows_of_tile + row >= seq.n * a.G) return;
+    const int full_row = tile * rows_of_tile + row, t = (int)fdiv(full_row, a.by_group);
+    const int hq = kvh * a.G + full_row - t * a.G;
+    const int64_t q = (seq.q0 + t) * a.Hq + hq;
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-    T *out = reinterpret_cast<T *>(a.O) + q * a.os_tok + hq * a.os_head + lane * (D / 32);
+    T *out = reinterpret_cast<T *>(a.O) + (seq.q0 + t) * a.os_tok + hq * a.os_head + lane * E;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) out[e] = from_f<T>(v[e] * inv);
-    if (lane == 0 && a.lse) a.lse[r] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    for (int e = 0; e < E; ++e) out[e] = from_f<T>(v[e] * inv);
+    if (lane == 0 && a.lse) a.lse[q] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
 // Column tiles for a sequence's rows (its queries x the heads of a group).
 // fp32 needs twice the registers for q, D = 256 twice those for the output.
 int pick_nt(int64_t rows, int D, bool f32)
 {
-    const int most = D == 256 || f32 ? 1 : 2;
-    int nt = 1;
-    while (nt < most && nt * 8 < rows) nt *= 2;
-    return nt;
+    return rows > 8 && D != 256 && !f32 ? 2 : 1;
 }
 
-struct AttnPlan {
-    int nt, row_tiles, splits, chunk;
-};
-
-// Splits: enough blocks for a few rounds of every SM's four, in chunks of at
-// least 256 tokens (a block's start and end cost about as much as 100).
-// Uses nothing but the arguments, so the workspace can be sized without a device.
-AttnPlan attn_plan(int32_t B, int32_t max_q, int64_t max_len, int32_t Hq, int32_t Hkv, int32_t D, bool f32, bool window)
+// Floats of the partial slots and the prefix of the sequences (as 64-bit words),
+// for any element type.
+size_t attn_workspace(int32_t B, int32_t max_q, int32_t Hq, int32_t Hkv, int32_t D)
 {
-    AttnPlan p;
     const int64_t rows = (int64_t)max_q * (Hq / Hkv);
-    p.nt = pick_nt(rows, D, f32);
-    p.row_tiles = (int)((rows + p.nt * 8 - 1) / (p.nt * 8));
-    const int64_t items = (int64_t)B * Hkv * p.row_tiles;
-    const int64_t slots = 152 * 4 * 3;
-    int64_t splits = items > 0 ? (slots + items - 1) / items : 1;
-    const int64_t most = (max_len + 255) / 256;
-    if (splits > most) splits = most;
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    if (splits < 1) splits = 1;
-    const int64_t range = max_len + (window ? kTile - 1 : 0);  // a window's first tile is rounded down
-    int64_t chunk = (range + splits - 1) / splits;
-    const int64_t unit = kTile * kWarps;
-    chunk = (chunk + unit - 1) / unit * unit;
-    if (chunk < unit) chunk = unit;
-    p.chunk = (int)chunk;
-    p.splits = (int)((range + chunk - 1) / chunk);
-    if (p.splits < 1) p.splits = 1;
-    return p;
+    const size_t slots = 2 * kMostBlocks * (size_t)(rows > 8 ? 16 : 8) * (D + 2) * sizeof(float);
+    return slots + (size_t)(B + 1) * sizeof(int64_t);
 }
 
-template <typename T, int D>
-tm_status launch_attn(const AttnArgs &a, const AttnPlan &p, cudaStream_t s, bool pdl)
+template <typename T, int D, int NT>
+tm_status launch_attn(AttnArgs &a, int sms, int row_tiles, bool join, cudaStream_t s, bool pdl)
 {
-    const void *k = (const void *)kv4_attn_kernel<T, D, 1>;
-    if constexpr (D != 256 && sizeof(T) == 2) {
-        if (p.nt == 2) k = (const void *)kv4_attn_kernel<T, D, 2>;
-    }
+    const void *k = (const void *)kv4_attn_kernel<T, D, NT>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D>()) != cudaSuccess) {
         cudaGetLastError();
         return TM_ERR_CUDA;
     }
+    int64_t blocks = (int64_t)sms * blocks_per_sm<T, D, NT>();
+    if (blocks > kMostBlocks) blocks = kMostBlocks;
     void *args[] = {(void *)&a};
-    const int64_t blocks = (int64_t)a.B * a.Hkv * p.row_tiles * p.splits;
     tm_status st = launch_kernel(k, dim3((unsigned)blocks), dim3(kWarps * 32), args, attn_smem<D>(), s, pdl);
-    if (st != TM_OK || p.splits == 1) return st;
-    int rows_of_tile = p.nt * 8;
-    void *jargs[] = {(void *)&a, &rows_of_tile};
-    return launch_dependent((const void *)kv4_join_kernel<T, D>, dim3((unsigned)((a.Tq * a.Hq + 3) / 4)), dim3(128),
-                            jargs, 0, s);
+    if (st != TM_OK || !join) return st;
+    const int64_t items = (int64_t)a.B * a.Hkv * row_tiles;
+    int rows_of_tile = NT * 8, W = items >= sms ? 1 : 8;
+    void *jargs[] = {(void *)&a, &rows_of_tile, &row_tiles, &W};
+    return launch_dependent((const void *)kv4_join_kernel<T, D>, dim3((unsigned)(items * rows_of_tile / (8 / W))),
+                            dim3(256), jargs, 0, s);
 }
 
 template <typename T>
-tm_status launch_attn(int D, const AttnArgs &a, const AttnPlan &p, cudaStream_t s, bool pdl)
+tm_status launch_attn(int D, int nt, AttnArgs &a, int sms, int row_tiles, bool join, cudaStream_t s, bool pdl)
 {
-    return D == 64 ? launch_attn<T, 64>(a, p, s, pdl)
-           : D == 128 ? launch_attn<T, 128>(a, p, s, pdl) : launch_attn<T, 256>(a, p, s, pdl);
+    if constexpr (sizeof(T) == 2) {
+        if (nt == 2)
+            return D == 64 ? launch_attn<T, 64, 2>(a, sms, row_tiles, join, s, pdl)
+                           : launch_attn<T, 128, 2>(a, sms, row_tiles, join, s, pdl);
+    }
+    return D == 64    ? launch_attn<T, 64, 1>(a, sms, row_tiles, join, s, pdl)
+           : D == 128 ? launch_attn<T, 128, 1>(a, sms, row_tiles, join, s, pdl)
+                      : launch_attn<T, 256, 1>(a, sms, row_tiles, join, s, pdl);
 }
 
 bool attn_shape_ok(int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_t Hq, int32_t Hkv)
@@ -819,14 +931,8 @@ using namespace libtm;
 extern "C" size_t tm_kv4_attention_workspace_bytes(int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_t Hq,
                                                    int32_t Hkv, int32_t D)
 {
-    if (!attn_shape_ok(B, Tq, max_q, max_len, Hq, Hkv) || !kv4_head_ok(D) || B == 0 || Tq == 0) return 0;
-    size_t most = 0;
-    for (int i = 0; i < 4; ++i) {  // any element type, with or without a window
-        const AttnPlan p = attn_plan(B, max_q, max_len, Hq, Hkv, D, (i & 1) != 0, (i & 2) != 0);
-        const size_t n = p.splits > 1 ? (size_t)p.splits * (size_t)Tq * Hq * (D + 2) * sizeof(float) : 0;
-        most = n > most ? n : most;
-    }
-    return most;
+    if (!attn_shape_ok(B, Tq, max_q, max_len, Hq, Hkv) || !kv4_head_ok(D) || B == 0 || Tq == 0 || max_q == 0) return 0;
+    return max_len <= kUnit ? 0 : attn_workspace(B, max_q, Hq, Hkv, D);
 }
 
 extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_head, void *O, int64_t os_tok,
@@ -851,8 +957,9 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     if (!aligned_to(Q, e) || !aligned_to(O, e) || !aligned_to(pool, 16) || !aligned_to(lse, 4) || !aligned_to(table, 4) ||
         !aligned_to(lens, 4) || !aligned_to(qstart, 4))
         return TM_ERR_MISALIGNED;
-    const AttnPlan p = attn_plan(B, max_q, max_len, Hq, Hkv, D, e == 4, window > 0);
-    const size_t need = p.splits > 1 ? (size_t)p.splits * (size_t)Tq * Hq * (D + 2) * sizeof(float) : 0;
+    // one unit an item at most: every item is one block's, nothing to join
+    const bool join = max_len > kUnit;
+    const size_t need = join ? attn_workspace(B, max_q, Hq, Hkv, D) : 0;
     if (need > 0 && (workspace == nullptr || ws_bytes < need || !aligned_to(workspace, 16))) return TM_ERR_WORKSPACE;
     const int64_t pb = (int64_t)tm_kv4_page_bytes(Hkv, D, page);
     const Span so = heads_span(o, Tq, Hq, D, e), sl = span_of(lse, Tq * Hq, lse ? 1 : 0, Tq * Hq, 4),
@@ -862,8 +969,9 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     for (const Span &s : ins)
         if (meets(so, s) || meets(sl, s) || meets(sw, s)) return TM_ERR_INVALID_ARG;
     if (meets(so, sl) || meets(so, sw) || meets(sl, sw)) return TM_ERR_INVALID_ARG;
-    const int64_t blocks = (int64_t)B * Hkv * p.row_tiles;
-    if (blocks > INT32_MAX / p.splits || Tq * Hq > INT32_MAX) return TM_ERR_INVALID_ARG;
+    const int nt = pick_nt((int64_t)max_q * (Hq / Hkv), D, e == 4);
+    const int64_t row_tiles = ((int64_t)max_q * (Hq / Hkv) + nt * 8 - 1) / (nt * 8);
+    if (row_tiles > INT32_MAX / 16 / ((int64_t)B * Hkv)) return TM_ERR_INVALID_ARG;
     const DevInfo *dev;
     tm_status st = device_info(&dev);
     if (st != TM_OK) return st;
@@ -876,6 +984,7 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.lens = lens;
     a.qstart = qstart;
     a.part = reinterpret_cast<float *>(workspace);
+    a.prefix = join ? reinterpret_cast<int64_t *>(a.part + 2 * (size_t)kMostBlocks * nt * 8 * (D + 2)) : nullptr;
     a.qs_tok = qs_tok;
     a.qs_head = qs_head;
     a.os_tok = os_tok;
@@ -885,7 +994,6 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.ldt = ldt;
     a.Tq = Tq;
     a.max_len = max_len;
-    a.page = page;
     a.B = B;
     a.Hq = Hq;
     a.Hkv = Hkv;
@@ -893,15 +1001,15 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.window = window;
     a.full = (flags & TM_ATTN_FULL) ? 1 : 0;
     a.vec = heads_vec(q, e) && heads_vec(o, e) ? 1 : 0;
-    a.row_tiles = p.row_tiles;
-    a.splits = p.splits;
-    a.chunk = p.chunk;
+    a.blocks_per_page = page / 16;
+    a.by_page = make_fastdiv((uint32_t)a.blocks_per_page);
+    a.by_group = make_fastdiv((uint32_t)a.G);
     a.max_q = max_q;
     a.scale = scale;
     a.status = dev->status;
     cudaStream_t s = as_stream(stream);
     const bool pdl = (flags & TM_PDL) != 0;
-    return xtype == TM_F32   ? launch_attn<float>(D, a, p, s, pdl)
-           : xtype == TM_F16 ? launch_attn<__half>(D, a, p, s, pdl)
-                             : launch_attn<__nv_bfloat16>(D, a, p, s, pdl);
+    return xtype == TM_F32   ? launch_attn<float>(D, nt, a, dev->sms, (int)row_tiles, join, s, pdl)
+           : xtype == TM_F16 ? launch_attn<__half>(D, nt, a, dev->sms, (int)row_tiles, join, s, pdl)
+                             : launch_attn<__nv_bfloat16>(D, nt, a, dev->sms, (int)row_tiles, join, s, pdl);
 }

@@ -159,5 +159,5 @@ def test_sizes():
     assert tm.tm_kv4_page_bytes(8, 96, 64) == tm.tm_kv4_page_bytes(0, 64, 16) == tm.tm_kv4_page_bytes(1, 64, 8) == 0
     f = tm.tm_kv4_attention_workspace_bytes
     assert f(64, 64, 1, 100, 32, 8, 128) == 0                       # one split: nothing to join
-    assert f(1, 1, 1, 131072, 64, 8, 128) % (64 * 130 * 4) == 0 < f(1, 1, 1, 131072, 64, 8, 128)
+    assert 0 < f(1, 1, 1, 131072, 64, 8, 128) < 32 << 20             # a slot or two a block, whatever the length
     assert f(0, 0, 1, 100, 4, 2, 64) == f(1, 1, 1, 100, 4, 3, 64) == f(1, 1, 1, 100, 4, 2, 80) == 0
