@@ -39,10 +39,10 @@
 // barrier is in the loop; each keeps its own running maximum, sum and output, joined
 // in shared memory at a segment's end.
 //
-// P stepV is rounded to fp16 for the second product: scaled by 2^E so that the
-// largest step seen lies in [2^14, 2^15), it is off by at most 2^-11 of itself,
-// errors that the sum over tokens averages below the output's own rounding.  With
-// fp32 tensors q and P stepV go in as two fp16 parts each (22 bits).
+// P stepV is rounded to fp16 for the second product, scaled by a 2^E that keeps the
+// largest of them in range: off by at most 2^-11 of itself, errors that the sum over
+// tokens averages below the output's own rounding.  With fp32 tensors q and P stepV
+// go in as two fp16 parts each (22 bits).
 #include "tm_host.h"
 
 #include "tm_elem.cuh"
@@ -53,6 +53,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTile = 32;    // tokens a warp takes at a time: two cache blocks
+// p goes up to 2^kSlack, p stepV 2^E up to 2^kSlack 2^(kStepBits + 3) <= 2^15
+constexpr int kSlack = 8, kStepBits = 4;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2eF = 1.4426950408889634f;
 
@@ -66,8 +68,7 @@ __device__ __forceinline__ float ex2(float x)
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -75,7 +76,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
@@ -117,7 +118,7 @@ struct AttnArgs {
     const uint8_t *pool;
     const int32_t *table, *lens, *qstart;
     float *part;      // [2 gridDim.x] slots of [ROWS][D] outputs and [ROWS][2] (maximum, sum)
-    int64_t *prefix;  // [B]: units before each sequence, for the join; then the share of a block
+    int *prefix;      // [B]: units before each sequence, for the join; then the share of a block
     int64_t qs_tok, qs_head, os_tok, os_head, pages, page_bytes, ldt, Tq, max_len;
     int B, Hq, Hkv, G, window, full, vec, max_q, blocks_per_page;
     float scale;
@@ -169,7 +170,7 @@ __device__ __forceinline__ int lower(const AttnArgs &a, const Seq &s, int t)
 // window every row tile counts as many units as the widest could need.
 struct Load {
     int tiles, units;
-    __device__ __forceinline__ int64_t total(int Hkv) const { return (int64_t)tiles * units * Hkv; }
+    __device__ __forceinline__ int total(int Hkv) const { return tiles * units * Hkv; }  // the host bounds the sum
 };
 
 __device__ __forceinline__ Load load_of(const AttnArgs &a, const Seq &s, int rows_of_tile)
@@ -224,8 +225,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
     constexpr int ROWS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps][STAGES];
-    __shared__ int64_t scan[kWarps + 1], found_base;
-    __shared__ int found_b;
+    __shared__ int scan[kWarps], found_b, found_base;
 
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
@@ -240,21 +240,21 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
     }
 
     // ---- this block's run of units: [pos, stop)
-    int64_t pos, stop, base = 0;
+    int pos, stop, base = 0;
     int b = 0;
     {
         // sum over the sequences of threads before this one, and all
-        auto scan_of = [&](int64_t x, int64_t &before) -> int64_t {
-            int64_t inc = x;
+        auto scan_of = [&](int x, int &before) -> int {
+            int inc = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += y;
             }
             __syncthreads();  // the last use of scan[]
             if (lane == 31) scan[warp] = inc;
             __syncthreads();
-            int64_t head = 0, all = 0;
+            int head = 0, all = 0;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 if (w < warp) head += scan[w];
@@ -263,32 +263,32 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
             before = head + inc - x;
             return all;
         };
-        int64_t mine = 0, before, all = 0;
+        int mine = 0, before, all = 0;
         for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
             const bool in = b0 + tid < a.B;
             mine = 0;
             if (in) mine = load_of(a, sequence(a, b0 + tid, blockIdx.x == 0), ROWS).total(a.Hkv);
-            const int64_t sum = scan_of(mine, before);
+            const int sum = scan_of(mine, before);
             if (in && blockIdx.x == 0 && a.prefix) {
                 if (b0 == 0) pdl_wait();
                 a.prefix[b0 + tid] = all + before;
             }
             all += sum;
         }
-        const int64_t share = (all + gridDim.x - 1) / gridDim.x;
+        const int share = (all + (int)gridDim.x - 1) / (int)gridDim.x;
         if (blockIdx.x == 0 && tid == 0 && a.prefix) a.prefix[a.B] = share;
-        pos = share * blockIdx.x;
+        pos = min(share * (int)blockIdx.x, all);
         stop = min(all, pos + share);
         if (pos >= stop) {
             pdl_wait();
             return;
         }
         const bool once = a.B <= kWarps * 32;  // one round: mine and before still hold
-        int64_t sofar = 0;
+        int sofar = 0;
         for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
             if (!once) {
                 mine = b0 + tid < a.B ? load_of(a, sequence(a, b0 + tid, false), ROWS).total(a.Hkv) : 0;
-                const int64_t sum = scan_of(mine, before);
+                const int sum = scan_of(mine, before);
                 before += sofar;
                 sofar += sum;
             }
@@ -316,10 +316,9 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
             seq = sequence(a, ++b, false);
             load = load_of(a, seq, ROWS);
         }
-        const int64_t item = (pos - base) / load.units;
-        const int unit0 = (int)(pos - base - item * load.units);
-        const int kvh = (int)(item / load.tiles), tile = (int)(item - (int64_t)kvh * load.tiles);
-        const int count = (int)min((int64_t)(load.units - unit0), stop - pos);
+        const int item = (pos - base) / load.units, unit0 = pos - base - item * load.units;
+        const int kvh = item / load.tiles, tile = item - kvh * load.tiles;
+        const int count = min(load.units - unit0, stop - pos);
         const bool whole = count == load.units;
         pos += count;
         const int rows = min(ROWS, seq.n * a.G - tile * ROWS);
@@ -482,65 +481,74 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         const bool masked = tok0 < safe0 || tok0 + kTile > safe1;
         float y[2][NT][4];
         float2 vp[2][2];
+        // first product, both blocks at once, the dims in two chains: four independent
+        // accumulators hide the latency of a chain
+        {
+            float acc[2][PARTS][NT][2][4];
+            uint32_t k0[2][LD / 8], k1[2][LD / 8];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint8_t *blk = st + q * BB;
-            // first product
-            float acc[PARTS][NT][4];
+            for (int q = 0; q < 2; ++q) {
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p)
+                for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[q][p][nt][0][e] = acc[q][p][nt][1][e] = 0.0f;
+                const uint8_t *kr = st + q * BB + g * (D / 2) + j * (D / 8);
+                if constexpr (D == 64) {
+                    *reinterpret_cast<uint2 *>(k0[q]) = *reinterpret_cast<const uint2 *>(kr);
+                    *reinterpret_cast<uint2 *>(k1[q]) = *reinterpret_cast<const uint2 *>(kr + 8 * (D / 2));
+                } else {
+#pragma unroll
+                    for (int x = 0; x < LD / 32; ++x) {
+                        reinterpret_cast<uint4 *>(k0[q])[x] = reinterpret_cast<const uint4 *>(kr)[x];
+                        reinterpret_cast<uint4 *>(k1[q])[x] = reinterpret_cast<const uint4 *>(kr + 8 * (D / 2))[x];
+                    }
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < LD / 8; ++w)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t x0 = hf ? k0[q][w] >> 8 : k0[q][w], x1 = hf ? k1[q][w] >> 8 : k1[q][w];
+                        const uint32_t a0 = SPLIT ? centred_even(x0) : plain_even(x0);
+                        const uint32_t a1 = SPLIT ? centred_even(x1) : plain_even(x1);
+                        const uint32_t a2 = SPLIT ? centred_odd(x0) : plain_odd(x0);
+                        const uint32_t a3 = SPLIT ? centred_odd(x1) : plain_odd(x1);
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(acc[q][p][nt][hf], a0, a1, a2, a3, qf[p][nt][2 * w + hf][0],
+                                         qf[p][nt][2 * w + hf][1]);
+                    }
+            // logits: this lane's tokens g and g + 8
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint8_t *blk = st + q * BB;
+                float2 kp0 = half2_at(blk + kv4_ks_off(D) + 4 * g), kp1 = half2_at(blk + kv4_ks_off(D) + 4 * (g + 8));
+                vp[q][0] = half2_at(blk + kv4_vs_off(D) + 4 * g);
+                vp[q][1] = half2_at(blk + kv4_vs_off(D) + 4 * (g + 8));
+                // centred codes count from low + 8 step
+                if constexpr (SPLIT) {
+                    kp0.y = fmaf(8.0f, kp0.x, kp0.y);
+                    kp1.y = fmaf(8.0f, kp1.x, kp1.y);
+                }
+                vp[q][0].y = fmaf(8.0f, vp[q][0].x, vp[q][0].y);
+                vp[q][1].y = fmaf(8.0f, vp[q][1].x, vp[q][1].y);
+                const float ks0 = kp0.x * kunit, ks1 = kp1.x * kunit;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[p][nt][e] = 0.0f;
-            uint32_t k0[LD / 8], k1[LD / 8];
-            const uint8_t *kr = blk + g * (D / 2) + j * (D / 8);
-            if constexpr (D == 64) {
-                *reinterpret_cast<uint2 *>(k0) = *reinterpret_cast<const uint2 *>(kr);
-                *reinterpret_cast<uint2 *>(k1) = *reinterpret_cast<const uint2 *>(kr + 8 * (D / 2));
-            } else {
-#pragma unroll
-                for (int x = 0; x < LD / 32; ++x) {
-                    reinterpret_cast<uint4 *>(k0)[x] = reinterpret_cast<const uint4 *>(kr)[x];
-                    reinterpret_cast<uint4 *>(k1)[x] = reinterpret_cast<const uint4 *>(kr + 8 * (D / 2))[x];
-                }
+                    for (int e = 0; e < 4; ++e) {
+                        float d = acc[q][0][nt][0][e] + acc[q][0][nt][1][e];
+                        if constexpr (SPLIT)
+                            d = fmaf(acc[q][PARTS - 1][nt][0][e] + acc[q][PARTS - 1][nt][1][e], 1.0f / 2048.0f, d);
+                        y[q][nt][e] = fmaf(d, e < 2 ? ks0 : ks1, (e < 2 ? kp0.y : kp1.y) * qs[nt][e & 1]);
+                    }
             }
-#pragma unroll
-            for (int w = 0; w < LD / 8; ++w) {
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t x0 = hf ? k0[w] >> 8 : k0[w], x1 = hf ? k1[w] >> 8 : k1[w];
-                    const uint32_t a0 = SPLIT ? centred_even(x0) : plain_even(x0);
-                    const uint32_t a1 = SPLIT ? centred_even(x1) : plain_even(x1);
-                    const uint32_t a2 = SPLIT ? centred_odd(x0) : plain_odd(x0);
-                    const uint32_t a3 = SPLIT ? centred_odd(x1) : plain_odd(x1);
-#pragma unroll
-                    for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816(acc[p][nt], a0, a1, a2, a3, qf[p][nt][2 * w + hf][0], qf[p][nt][2 * w + hf][1]);
-                }
-            }
-            // logits: this lane's tokens g and g + 8
-            float2 kp0 = half2_at(blk + kv4_ks_off(D) + 4 * g), kp1 = half2_at(blk + kv4_ks_off(D) + 4 * (g + 8));
-            vp[q][0] = half2_at(blk + kv4_vs_off(D) + 4 * g);
-            vp[q][1] = half2_at(blk + kv4_vs_off(D) + 4 * (g + 8));
-            // centred codes count from low + 8 step
-            if constexpr (SPLIT) {
-                kp0.y = fmaf(8.0f, kp0.x, kp0.y);
-                kp1.y = fmaf(8.0f, kp1.x, kp1.y);
-            }
-            vp[q][0].y = fmaf(8.0f, vp[q][0].x, vp[q][0].y);
-            vp[q][1].y = fmaf(8.0f, vp[q][1].x, vp[q][1].y);
-            const float ks0 = kp0.x * kunit, ks1 = kp1.x * kunit;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float d = acc[0][nt][e];
-                    if constexpr (SPLIT) d = fmaf(acc[PARTS - 1][nt][e], 1.0f / 2048.0f, d);
-                    y[q][nt][e] = fmaf(d, e < 2 ? ks0 : ks1, (e < 2 ? kp0.y : kp1.y) * qs[nt][e & 1]);
-                }
         }
         if (masked) {
 #pragma unroll
@@ -581,7 +589,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
                                 if (y[q][nt][2 * r + c] != -INFINITY) lowsum[nt][c] = NAN;
                     }
         }
-        // a new maximum, or a larger step: move the running state (rare after the first tiles)
+        // The reference m moves only where a logit passes it by 2^kSlack, and the steps' cap
+        // only past three times a power of two: moving the running state costs half a
+        // tile's work, and following every new maximum of eight rows did so in two
+        // tiles of three (attn of 131071 tokens: 44 against 33 us).
         bool grow = false;
         float vmax = fmaxf(fmaxf(vp[0][0].x, vp[0][1].x), fmaxf(vp[1][0].x, vp[1][1].x));
 #pragma unroll
@@ -589,7 +600,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const float t = fmaxf(fmaxf(y[0][nt][c], y[0][nt][2 + c]), fmaxf(y[1][nt][c], y[1][nt][2 + c]));
-                grow = grow || t > m[nt][c];
+                grow = grow || t > m[nt][c] + kSlack;
             }
         if (__any_sync(0xffffffffu, grow || vmax >= vcap)) {
             vmax = lanes_max(vmax, 32);
@@ -598,12 +609,12 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
                 const int e = (int)(__float_as_uint(vmax) >> 23) - 127;  // 2^e <= vmax < 2^(e+1)
                 move = vcap > 0.0f ? ldexpf(1.0f, vexp - e) : 1.0f;
                 vexp = e;
-                vcap = ldexpf(1.0f, e + 1);
-                vscale = ldexpf(1.0f, 14 - e);
+                vcap = ldexpf(1.0f, e + 3);
+                vscale = ldexpf(1.0f, kStepBits - e);
             } else if (vcap == 0.0f) {
                 vcap = 0x1p-30f;  // only zero steps so far
-                vexp = -31;
-                vscale = 0x1p45f;
+                vexp = -33;
+                vscale = ldexpf(1.0f, kStepBits + 33);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -646,7 +657,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
                     pb[0][nt][r] = transpose8x8(hi);
                     if constexpr (SPLIT) {
                         const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                        // the rest, below 2^4 against a largest of 2^15: down to 2^-24, 2^-39 of it
+                        // the rest, below 2^4 against a largest of 2^15
                         pb[PARTS - 1][nt][r] = transpose8x8(pack_half2(w[2 * r] - h.x, w[2 * r + 1] - h.y));
                     }
                 }
@@ -708,7 +719,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 
     // ---- join the warps.  o: dims 2k of slice g in elements 0, 1 and 2k + 1 in 2, 3,
     // in units of 2^E (16 times that for the odd ones)
-    const float even = ldexpf(1.0f, vexp - 14), odd = even * 0.0625f;
+    const float even = ldexpf(1.0f, vexp - kStepBits), odd = even * 0.0625f;
     float *stat = reinterpret_cast<float *>(smem);            // [kWarps][ROWS][2]: maximum, sum
     float *buf = stat + kWarps * ROWS * 2;                    // [kWarps][ROWS][D / PASS]
     constexpr int kRoom = kWarps * STAGES * SB - kWarps * ROWS * 8;
@@ -818,12 +829,11 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ A
     const Seq seq = sequence(a, b, false);
     const Load load = load_of(a, seq, rows_of_tile);
     if (tile >= load.tiles) return;
-    const int64_t share = a.prefix[a.B], first = a.prefix[b] + ((int64_t)kvh * load.tiles + tile) * load.units;
-    const int64_t c0 = first / share;
-    const int n = (int)((first + load.units - 1) / share - c0) + 1;
+    const int share = a.prefix[a.B], first = a.prefix[b] + (kvh * load.tiles + tile) * load.units;
+    const int c0 = first / share, n = (first + load.units - 1) / share - c0 + 1;
     if (n == 1) return;  // one block had the whole item and wrote its output
     const int stride = rows_of_tile * (D + 2);
-    const float *item = a.part + 2 * c0 * stride;
+    const float *item = a.part + (int64_t)2 * c0 * stride;
     // partial p: the item's first block holds it in its slot 1, the others in slot 0
     auto slot = [&](int p) { return item + (int64_t)(p == 0 ? 1 : 2 * p) * stride; };
     float mm = -INFINITY;
@@ -875,13 +885,12 @@ int pick_nt(int64_t rows, int D, bool f32)
     return rows > 8 && D != 256 && !f32 ? 2 : 1;
 }
 
-// Floats of the partial slots and the prefix of the sequences (as 64-bit words),
-// for any element type.
+// Bytes of the partial slots and of the sequences' prefix, for any element type.
 size_t attn_workspace(int32_t B, int32_t max_q, int32_t Hq, int32_t Hkv, int32_t D)
 {
     const int64_t rows = (int64_t)max_q * (Hq / Hkv);
     const size_t slots = 2 * kMostBlocks * (size_t)(rows > 8 ? 16 : 8) * (D + 2) * sizeof(float);
-    return slots + (size_t)(B + 1) * sizeof(int64_t);
+    return slots + ((size_t)B + 1) * sizeof(int);
 }
 
 template <typename T, int D, int NT>
@@ -971,7 +980,10 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     if (meets(so, sl) || meets(so, sw) || meets(sl, sw)) return TM_ERR_INVALID_ARG;
     const int nt = pick_nt((int64_t)max_q * (Hq / Hkv), D, e == 4);
     const int64_t row_tiles = ((int64_t)max_q * (Hq / Hkv) + nt * 8 - 1) / (nt * 8);
-    if (row_tiles > INT32_MAX / 16 / ((int64_t)B * Hkv)) return TM_ERR_INVALID_ARG;
+    // the units of all items, and the join's grid, fit 31 bits (with room for a block's share)
+    if (row_tiles > (1 << 30) / 16 / ((int64_t)B * Hkv) ||
+        (max_len / kUnit + 2) > (1 << 30) / ((int64_t)B * Hkv * row_tiles))
+        return TM_ERR_INVALID_ARG;
     const DevInfo *dev;
     tm_status st = device_info(&dev);
     if (st != TM_OK) return st;
@@ -984,7 +996,7 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.lens = lens;
     a.qstart = qstart;
     a.part = reinterpret_cast<float *>(workspace);
-    a.prefix = join ? reinterpret_cast<int64_t *>(a.part + 2 * (size_t)kMostBlocks * nt * 8 * (D + 2)) : nullptr;
+    a.prefix = join ? reinterpret_cast<int *>(a.part + 2 * (size_t)kMostBlocks * nt * 8 * (D + 2)) : nullptr;
     a.qs_tok = qs_tok;
     a.qs_head = qs_head;
     a.os_tok = os_tok;

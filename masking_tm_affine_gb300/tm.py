@@ -110,6 +110,8 @@ class TmError(RuntimeError):
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libtm.so (once) and attach the signatures; raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -135,8 +137,9 @@ def _ptr(x) -> int | None:
 def _stream(s) -> int | None:
     if s is None:
         torch = sys.modules.get("torch")
-        if torch is not None and torch.cuda.is_available() and torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
+        if torch is not None and torch.cuda.is_initialized():
+            # what torch.cuda.current_stream().cuda_stream reads, without building a Stream object (3.8 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return None
     if isinstance(s, int):
         return s
