@@ -43,6 +43,8 @@
 // largest of them in range: off by at most 2^-11 of itself, errors that the sum over
 // tokens averages below the output's own rounding.  With fp32 tensors q and P stepV
 // go in as two fp16 parts each (22 bits).
+#include <atomic>
+
 #include "tm_host.h"
 
 #include "tm_elem.cuh"
@@ -98,14 +100,16 @@ __device__ __forceinline__ uint32_t plain_even(uint32_t x) { return x & 0x000f00
 __device__ __forceinline__ uint32_t plain_odd(uint32_t x) { return x & 0x00f000f0u; }
 
 // Centred: c - 8, or 16 (c - 8), normal numbers: the nibble joins the low bits of
-// 1024 and the subtraction is exact.
+// 1024 and the subtraction is exact.  `bias` holds 1024 twice and comes from the
+// launch's arguments: as a constant it would share the one immediate an instruction
+// has with the mask, and cost an instruction more for each pair.
 __device__ __forceinline__ uint32_t centred(uint32_t x, uint16_t middle)
 {
     const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), __halves2half2(__ushort_as_half(middle), __ushort_as_half(middle)));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t centred_even(uint32_t x) { return centred((x & 0x000f000fu) | 0x64006400u, 0x6408); }  // 1032
-__device__ __forceinline__ uint32_t centred_odd(uint32_t x) { return centred((x & 0x00f000f0u) | 0x64006400u, 0x6480); }   // 1152
+__device__ __forceinline__ uint32_t centred_even(uint32_t x, uint32_t bias) { return centred((x & 0x000f000fu) | bias, 0x6408); }  // 1032
+__device__ __forceinline__ uint32_t centred_odd(uint32_t x, uint32_t bias) { return centred((x & 0x00f000f0u) | bias, 0x6480); }   // 1152
 
 constexpr int kUnit = 256;             // tokens: two tiles a warp
 static_assert(kUnit % (kWarps * kTile) == 0, "a unit is whole tiles of every warp");
@@ -118,9 +122,10 @@ struct AttnArgs {
     const uint8_t *pool;
     const int32_t *table, *lens, *qstart;
     float *part;      // [2 gridDim.x] slots of [ROWS][D] outputs and [ROWS][2] (maximum, sum)
-    int *prefix;      // [B]: units before each sequence, for the join; then the share of a block
+    int2 *job;        // [B][Hkv][row_tiles]: the first block an item lies in, and how many; or NULL
     int64_t qs_tok, qs_head, os_tok, os_head, pages, page_bytes, ldt, Tq, max_len;
-    int B, Hq, Hkv, G, window, full, vec, max_q, blocks_per_page;
+    int B, Hq, Hkv, G, window, full, vec, max_q, blocks_per_page, row_tiles;
+    uint32_t bias;  // 1024 in both halves of an fp16 pair
     float scale;
     FastDiv by_page, by_group;  // cache blocks of a page, heads of a group
     unsigned *status;
@@ -129,14 +134,13 @@ struct AttnArgs {
 // What a sequence's queries are: their first row of Q, their count and the
 // cache's length, checked against the call's bounds.
 struct Seq {
-    int64_t q0;
-    int n, len;
+    int q0, n, len;
 };
 
 __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b, bool report)
 {
     Seq s;
-    int64_t q1;
+    int q1;
     if (a.qstart) {
         s.q0 = a.qstart[b];
         q1 = a.qstart[b + 1];
@@ -151,7 +155,7 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b, bool report)
         s.len = 0;
         return s;
     }
-    s.n = (int)(q1 - s.q0);
+    s.n = q1 - s.q0;
     return s;
 }
 
@@ -225,7 +229,6 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
     constexpr int ROWS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps][STAGES];
-    __shared__ int scan[kWarps], found_b, found_base;
 
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
@@ -239,69 +242,54 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
 
-    // ---- this block's run of units: [pos, stop)
-    int pos, stop, base = 0;
-    int b = 0;
+    // ---- this block's run of units: [pos, stop), starting in sequence b, whose units
+    // start at base.  Every warp adds the sequences up for itself, 32 at a time.
+    int pos, stop, share, base = 0, b = 0;
+    Seq seq;
+    Load load;
     {
-        // sum over the sequences of threads before this one, and all
-        auto scan_of = [&](int x, int &before) -> int {
-            int inc = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            __syncthreads();  // the last use of scan[]
-            if (lane == 31) scan[warp] = inc;
-            __syncthreads();
-            int head = 0, all = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) head += scan[w];
-                all += scan[w];
-            }
-            before = head + inc - x;
-            return all;
+        auto lane_load = [&](int i, bool report, Seq &q) {
+            q = {0, 0, 0};
+            if (i < a.B) q = sequence(a, i, report);
+            return load_of(a, q, ROWS).total(a.Hkv);
         };
-        int mine = 0, before, all = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
-            const bool in = b0 + tid < a.B;
-            mine = 0;
-            if (in) mine = load_of(a, sequence(a, b0 + tid, blockIdx.x == 0), ROWS).total(a.Hkv);
-            const int sum = scan_of(mine, before);
-            if (in && blockIdx.x == 0 && a.prefix) {
-                if (b0 == 0) pdl_wait();
-                a.prefix[b0 + tid] = all + before;
-            }
-            all += sum;
-        }
-        const int share = (all + (int)gridDim.x - 1) / (int)gridDim.x;
-        if (blockIdx.x == 0 && tid == 0 && a.prefix) a.prefix[a.B] = share;
+        int all = 0, mine = 0;
+        Seq q;
+        for (int b0 = 0; b0 < a.B; b0 += 32) all += mine = lane_load(b0 + lane, blockIdx.x == 0 && warp == 0, q);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        share = (all + (int)gridDim.x - 1) / (int)gridDim.x;
         pos = min(share * (int)blockIdx.x, all);
         stop = min(all, pos + share);
         if (pos >= stop) {
             pdl_wait();
             return;
         }
-        const bool once = a.B <= kWarps * 32;  // one round: mine and before still hold
-        int sofar = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
-            if (!once) {
-                mine = b0 + tid < a.B ? load_of(a, sequence(a, b0 + tid, false), ROWS).total(a.Hkv) : 0;
-                const int sum = scan_of(mine, before);
-                before += sofar;
-                sofar += sum;
+        int before = 0;
+        for (;; b += 32) {
+            if (a.B > 32) mine = lane_load(b + lane, false, q);
+            int inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
             }
-            if (pos >= before && pos < before + mine) {
-                found_b = b0 + tid;
-                found_base = before;
+            const int sum = __shfl_sync(0xffffffffu, inc, 31);
+            if (pos < before + sum) {
+                const int at = __ffs(__ballot_sync(0xffffffffu, pos < before + inc)) - 1;
+                b += at;
+                base = before + __shfl_sync(0xffffffffu, inc - mine, at);
+                seq.q0 = __shfl_sync(0xffffffffu, q.q0, at);
+                seq.n = __shfl_sync(0xffffffffu, q.n, at);
+                seq.len = __shfl_sync(0xffffffffu, q.len, at);
+                break;
             }
+            before += sum;
         }
-        __syncthreads();
-        b = found_b;
-        base = found_base;
+        load = load_of(a, seq, ROWS);
     }
     const uint64_t policy = l2_evict_first_policy();
+    const uint32_t bias = a.bias;
     int stage = 0;       // of the next tile to read, in this warp's ring
     uint32_t phase = 0;  // and its parity
     int fill = 0;        // stage of the next tile to copy
@@ -309,8 +297,6 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 
     while (pos < stop) {
         // ---- the segment: units [unit0, unit0 + count) of an item
-        Seq seq = sequence(a, b, false);
-        Load load = load_of(a, seq, ROWS);
         while (pos >= base + load.total(a.Hkv)) {
             base += load.total(a.Hkv);
             seq = sequence(a, ++b, false);
@@ -320,6 +306,12 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         const int kvh = item / load.tiles, tile = item - kvh * load.tiles;
         const int count = min(load.units - unit0, stop - pos);
         const bool whole = count == load.units;
+        // the blocks an item lies in, noted for the join by the block that ends it
+        if (a.job && unit0 + count == load.units && tid == 0) {
+            const int first = pos - unit0, c0 = first / share;
+            pdl_wait();
+            a.job[((int64_t)b * a.Hkv + kvh) * a.row_tiles + tile] = make_int2(c0, (int)blockIdx.x - c0 + 1);
+        }
         pos += count;
         const int rows = min(ROWS, seq.n * a.G - tile * ROWS);
         const int t_first = (int)fdiv(tile * ROWS, a.by_group), t_last = (int)fdiv(tile * ROWS + rows - 1, a.by_group);
@@ -328,6 +320,27 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         const int c1 = unit0 + count == load.units ? end : min(end, c0 + count * kUnit);
         // Where every row of the tile sees every token: [safe0, safe1).
         const int safe0 = lower(a, seq, t_last), safe1 = upper(a, seq, t_first);
+
+        // ---- this lane's queries, asked for before the copies' page numbers
+        Vec<T, 8> raw[NT][LD / 8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = tile * ROWS + nt * 8 + g, t = (int)fdiv(row, a.by_group), hh = row - t * a.G;
+            const T *p = reinterpret_cast<const T *>(a.Q) + (int64_t)(seq.q0 + t) * a.qs_tok +
+                         (int64_t)(kvh * a.G + hh) * a.qs_head + j * LD;
+#pragma unroll
+            for (int w = 0; w < LD / 8; ++w) {
+                if (nt * 8 + g >= rows) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) raw[nt][w].v[e] = from_f<T>(0.0f);
+                } else if (a.vec) {
+                    load_vec(p + 8 * w, raw[nt][w]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) raw[nt][w].v[e] = p[8 * w + e];
+                }
+            }
+        }
 
         // ---- the copies: this warp's tiles are warp, warp + 4, ... of the segment.  Of each
         // 32 tiles a lane works out one's source (two blocks, which can lie in two
@@ -383,35 +396,12 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
     uint32_t qf[PARTS][NT][KS][2];
     float qsum[NT];
     float top = 0.0f;
-    auto row_ptr = [&](int row) {
-        const int t = (int)fdiv(row, a.by_group), hh = row - t * a.G;
-        return reinterpret_cast<const T *>(a.Q) + (seq.q0 + t) * a.qs_tok + (int64_t)(kvh * a.G + hh) * a.qs_head;
-    };
-    auto load_q8 = [&](int nt, int w, float (&f)[8]) {
-        const int row = tile * ROWS + nt * 8 + g;
-        if (nt * 8 + g < rows) {
-            const T *p = row_ptr(row) + j * LD + 8 * w;
-            if (a.vec) {
-                Vec<T, 8> v = *reinterpret_cast<const Vec<T, 8> *>(p);
-                widen(v, f);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = to_f(p[e]);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-        }
-    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int w = 0; w < LD / 8; ++w) {
-            float f[8];
-            load_q8(nt, w, f);
+        for (int w = 0; w < LD / 8; ++w)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-        }
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(raw[nt][w].v[e])));
     top = lanes_max(top, 32);
     // 2^qe: exponent of the largest, kept where 2^(14 - qe) and its inverse are normal
     int qe = (int)(__float_as_uint(top) >> 23) - 127;
@@ -423,7 +413,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 #pragma unroll
         for (int w = 0; w < LD / 8; ++w) {
             float f[8];
-            load_q8(nt, w, f);
+            widen(raw[nt][w], f);
             // word w of a lane's codes: pairs (0,4), (1,5)/16 in step 2w and (2,6), (3,7)/16 in step 2w + 1
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -513,10 +503,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const uint32_t x0 = hf ? k0[q][w] >> 8 : k0[q][w], x1 = hf ? k1[q][w] >> 8 : k1[q][w];
-                        const uint32_t a0 = SPLIT ? centred_even(x0) : plain_even(x0);
-                        const uint32_t a1 = SPLIT ? centred_even(x1) : plain_even(x1);
-                        const uint32_t a2 = SPLIT ? centred_odd(x0) : plain_odd(x0);
-                        const uint32_t a3 = SPLIT ? centred_odd(x1) : plain_odd(x1);
+                        const uint32_t a0 = SPLIT ? centred_even(x0, bias) : plain_even(x0);
+                        const uint32_t a1 = SPLIT ? centred_even(x1, bias) : plain_even(x1);
+                        const uint32_t a2 = SPLIT ? centred_odd(x0, bias) : plain_odd(x0);
+                        const uint32_t a3 = SPLIT ? centred_odd(x1, bias) : plain_odd(x1);
 #pragma unroll
                         for (int p = 0; p < PARTS; ++p)
 #pragma unroll
@@ -685,8 +675,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         const uint32_t x0 = hf ? e0 >> 8 : e0, x1 = hf ? e1 >> 8 : e1;
-                        const uint32_t a0 = centred_even(x0), a1 = centred_odd(x0);
-                        const uint32_t a2 = centred_even(x1), a3 = centred_odd(x1);
+                        const uint32_t a0 = centred_even(x0, bias), a1 = centred_odd(x0, bias);
+                        const uint32_t a2 = centred_even(x1, bias), a3 = centred_odd(x1, bias);
 #pragma unroll
                         for (int p = 0; p < PARTS; ++p)
 #pragma unroll
@@ -784,9 +774,9 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
             } else {
                 const int full_row = tile * ROWS + row, t = (int)fdiv(full_row, a.by_group);
                 const int hq = kvh * a.G + full_row - t * a.G;
-                const int64_t q = (seq.q0 + t) * a.Hq + hq;
+                const int64_t q = (int64_t)(seq.q0 + t) * a.Hq + hq;
                 const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-                T *out = reinterpret_cast<T *>(a.O) + (seq.q0 + t) * a.os_tok + hq * a.os_head + d;
+                T *out = reinterpret_cast<T *>(a.O) + (int64_t)(seq.q0 + t) * a.os_tok + hq * a.os_head + d;
                 if (a.vec) {
                     Vec<T, 2> v;
                     v.v[0] = from_f<T>(v0 * inv);
@@ -807,72 +797,95 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 }
 
 // Joins the partial outputs of an item's rows: 8 warps, W of them a row (1 or 8), each
-// every W-th partial, a lane D/32 dims; then a row's warps in order.  Items with few
-// partials (many items) take a warp a row, few items with many partials all eight.
+// every W-th partial with a running maximum of its own, a lane D/32 dims; then a row's
+// warps in order.  Items with few partials (many items) take a warp a row, few items
+// with many partials all eight.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ AttnArgs a, int rows_of_tile, int row_tiles,
-                                                       int W)
+__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ AttnArgs a, int rows_of_tile, int W)
 {
-    constexpr int E = D / 32;
-    __shared__ float sums[8][D], stat[8];
+    constexpr int E = D / 32, U = D == 256 ? 4 : 8;  // partials in flight
+    __shared__ float sums[8][D], stat[8][2];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows_here = 8 / W, sub = warp % W;
     // blockIdx.x = ((b * Hkv + kvh) * row_tiles + tile) * (rows_of_tile / rows_here) + part
-    const int parts = rows_of_tile / rows_here;
-    unsigned u = blockIdx.x;
-    const int row = (int)(u % parts) * rows_here + warp / W;
-    u /= parts;
-    const int tile = (int)(u % row_tiles);
-    u /= row_tiles;
-    const int b = (int)(u / a.Hkv), kvh = (int)(u - b * a.Hkv);
+    const unsigned parts = rows_of_tile / rows_here, item = blockIdx.x / parts;
+    const int row = (int)(blockIdx.x - item * parts) * rows_here + warp / W;
+    const int2 job = a.job[item];
+    const unsigned bh = item / a.row_tiles;
+    const int tile = (int)(item - bh * a.row_tiles), b = (int)(bh / a.Hkv), kvh = (int)(bh - b * a.Hkv);
     const Seq seq = sequence(a, b, false);
-    const Load load = load_of(a, seq, rows_of_tile);
-    if (tile >= load.tiles) return;
-    const int share = a.prefix[a.B], first = a.prefix[b] + (kvh * load.tiles + tile) * load.units;
-    const int c0 = first / share, n = (first + load.units - 1) / share - c0 + 1;
+    if (tile * rows_of_tile >= seq.n * a.G) return;  // not an item: its job was not noted
+    const int n = job.y;
     if (n == 1) return;  // one block had the whole item and wrote its output
     const int stride = rows_of_tile * (D + 2);
-    const float *item = a.part + (int64_t)2 * c0 * stride;
     // partial p: the item's first block holds it in its slot 1, the others in slot 0
-    auto slot = [&](int p) { return item + (int64_t)(p == 0 ? 1 : 2 * p) * stride; };
-    float mm = -INFINITY;
-    for (int p = lane; p < n; p += 32) mm = fmaxf(mm, slot(p)[rows_of_tile * D + row * 2]);
-    mm = lanes_max(mm, 32);
-    float ll = 0.0f, v[E];
+    const float *first = a.part + (int64_t)2 * job.x * stride;
+    float mm = -INFINITY, ll = 0.0f, v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = 0.0f;
-#pragma unroll 4
-    for (int p = sub; p < n; p += W) {
-        const float *q = slot(p);
-        const float2 ms = *reinterpret_cast<const float2 *>(q + rows_of_tile * D + row * 2);
-        float x[E];
+    for (int p0 = sub; p0 < n; p0 += U * W) {
+        float x[U][E];
+        float2 ms[U];
+        float top = mm;
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<float2 *>(x + e) = *reinterpret_cast<const float2 *>(q + row * D + lane * E + e);
-        const float f = ms.x == -INFINITY ? 1.0f : ex2(ms.x - mm);  // a share that saw nothing holds zeros
-        ll = fmaf(ms.y, f, ll);
+        for (int u = 0; u < U; ++u) {
+            const int p = p0 + u * W;
+            ms[u] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = fmaf(x[e], f, v[e]);
+            for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
+            if (p < n) {
+                const float *q = first + (int64_t)(p == 0 ? 1 : 2 * p) * stride;
+                ms[u] = *reinterpret_cast<const float2 *>(q + rows_of_tile * D + row * 2);
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    *reinterpret_cast<float2 *>(x[u] + e) = *reinterpret_cast<const float2 *>(q + row * D + lane * E + e);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, ms[u].x);
+        const float f0 = mm == -INFINITY ? 1.0f : ex2(mm - top);
+        ll *= f0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= f0;
+        mm = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = ms[u].x == -INFINITY ? 1.0f : ex2(ms[u].x - mm);  // a share that saw nothing holds zeros
+            ll = fmaf(ms[u].y, f, ll);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = fmaf(x[u][e], f, v[e]);
+        }
     }
     if (W > 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = v[e];
-        if (lane == 0) stat[warp] = ll;
+        if (lane == 0) {
+            stat[warp][0] = mm;
+            stat[warp][1] = ll;
+        }
         __syncthreads();
         if (sub != 0) return;
-        for (int w = 1; w < W; ++w) {
-            ll += stat[warp + w];
+        float top = mm;
+        for (int w = 1; w < W; ++w) top = fmaxf(top, stat[warp + w][0]);
+        const float f0 = mm == -INFINITY ? 1.0f : ex2(mm - top);
+        ll *= f0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] += sums[warp + w][lane * E + e];
+        for (int e = 0; e < E; ++e) v[e] *= f0;
+        for (int w = 1; w < W; ++w) {
+            const float mw = stat[warp + w][0], f = mw == -INFINITY ? 1.0f : ex2(mw - top);
+            ll = fmaf(stat[warp + w][1], f, ll);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = fmaf(sums[warp + w][lane * E + e], f, v[e]);
         }
+        mm = top;
     }
-    if (tile * rows_of_tile + row >= seq.n * a.G) return;
-    const int full_row = tile * rows_of_tile + row, t = (int)fdiv(full_row, a.by_group);
-    const int hq = kvh * a.G + full_row - t * a.G;
-    const int64_t q = (seq.q0 + t) * a.Hq + hq;
+    const int full_row = tile * rows_of_tile + row;
+    if (full_row >= seq.n * a.G) return;
+    const int t = (int)fdiv(full_row, a.by_group), hq = kvh * a.G + full_row - t * a.G;
+    const int64_t q = (int64_t)(seq.q0 + t) * a.Hq + hq;
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-    T *out = reinterpret_cast<T *>(a.O) + (seq.q0 + t) * a.os_tok + hq * a.os_head + lane * E;
+    T *out = reinterpret_cast<T *>(a.O) + (int64_t)(seq.q0 + t) * a.os_tok + hq * a.os_head + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) out[e] = from_f<T>(v[e] * inv);
     if (lane == 0 && a.lse) a.lse[q] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
@@ -885,45 +898,49 @@ int pick_nt(int64_t rows, int D, bool f32)
     return rows > 8 && D != 256 && !f32 ? 2 : 1;
 }
 
-// Bytes of the partial slots and of the sequences' prefix, for any element type.
+// Bytes of the partial slots and of the items' jobs, for any element type.
 size_t attn_workspace(int32_t B, int32_t max_q, int32_t Hq, int32_t Hkv, int32_t D)
 {
     const int64_t rows = (int64_t)max_q * (Hq / Hkv);
     const size_t slots = 2 * kMostBlocks * (size_t)(rows > 8 ? 16 : 8) * (D + 2) * sizeof(float);
-    return slots + ((size_t)B + 1) * sizeof(int);
+    return slots + (size_t)B * Hkv * ((size_t)rows + 7) / 8 * sizeof(int2);
 }
 
 template <typename T, int D, int NT>
-tm_status launch_attn(AttnArgs &a, int sms, int row_tiles, bool join, cudaStream_t s, bool pdl)
+tm_status launch_attn(AttnArgs &a, int dev, int sms, bool join, cudaStream_t s, bool pdl)
 {
     const void *k = (const void *)kv4_attn_kernel<T, D, NT>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D>()) != cudaSuccess) {
-        cudaGetLastError();
-        return TM_ERR_CUDA;
+    static std::atomic<bool> ready[kMaxDevices];  // once a device
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D>()) != cudaSuccess) {
+            cudaGetLastError();
+            return TM_ERR_CUDA;
+        }
+        ready[dev].store(true, std::memory_order_release);
     }
     int64_t blocks = (int64_t)sms * blocks_per_sm<T, D, NT>();
     if (blocks > kMostBlocks) blocks = kMostBlocks;
     void *args[] = {(void *)&a};
     tm_status st = launch_kernel(k, dim3((unsigned)blocks), dim3(kWarps * 32), args, attn_smem<D>(), s, pdl);
     if (st != TM_OK || !join) return st;
-    const int64_t items = (int64_t)a.B * a.Hkv * row_tiles;
+    const int64_t items = (int64_t)a.B * a.Hkv * a.row_tiles;
     int rows_of_tile = NT * 8, W = items >= sms ? 1 : 8;
-    void *jargs[] = {(void *)&a, &rows_of_tile, &row_tiles, &W};
+    void *jargs[] = {(void *)&a, &rows_of_tile, &W};
     return launch_dependent((const void *)kv4_join_kernel<T, D>, dim3((unsigned)(items * rows_of_tile / (8 / W))),
                             dim3(256), jargs, 0, s);
 }
 
 template <typename T>
-tm_status launch_attn(int D, int nt, AttnArgs &a, int sms, int row_tiles, bool join, cudaStream_t s, bool pdl)
+tm_status launch_attn(int D, int nt, AttnArgs &a, int dev, int sms, bool join, cudaStream_t s, bool pdl)
 {
     if constexpr (sizeof(T) == 2) {
         if (nt == 2)
-            return D == 64 ? launch_attn<T, 64, 2>(a, sms, row_tiles, join, s, pdl)
-                           : launch_attn<T, 128, 2>(a, sms, row_tiles, join, s, pdl);
+            return D == 64 ? launch_attn<T, 64, 2>(a, dev, sms, join, s, pdl)
+                           : launch_attn<T, 128, 2>(a, dev, sms, join, s, pdl);
     }
-    return D == 64    ? launch_attn<T, 64, 1>(a, sms, row_tiles, join, s, pdl)
-           : D == 128 ? launch_attn<T, 128, 1>(a, sms, row_tiles, join, s, pdl)
-                      : launch_attn<T, 256, 1>(a, sms, row_tiles, join, s, pdl);
+    return D == 64    ? launch_attn<T, 64, 1>(a, dev, sms, join, s, pdl)
+           : D == 128 ? launch_attn<T, 128, 1>(a, dev, sms, join, s, pdl)
+                      : launch_attn<T, 256, 1>(a, dev, sms, join, s, pdl);
 }
 
 bool attn_shape_ok(int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_t Hq, int32_t Hkv)
@@ -996,7 +1013,7 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.lens = lens;
     a.qstart = qstart;
     a.part = reinterpret_cast<float *>(workspace);
-    a.prefix = join ? reinterpret_cast<int *>(a.part + 2 * (size_t)kMostBlocks * nt * 8 * (D + 2)) : nullptr;
+    a.job = join ? reinterpret_cast<int2 *>(a.part + 2 * (size_t)kMostBlocks * nt * 8 * (D + 2)) : nullptr;
     a.qs_tok = qs_tok;
     a.qs_head = qs_head;
     a.os_tok = os_tok;
@@ -1017,11 +1034,18 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.by_page = make_fastdiv((uint32_t)a.blocks_per_page);
     a.by_group = make_fastdiv((uint32_t)a.G);
     a.max_q = max_q;
+    a.row_tiles = (int)row_tiles;
+    a.bias = 0x64006400u;
     a.scale = scale;
     a.status = dev->status;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) {
+        cudaGetLastError();
+        return TM_ERR_CUDA;
+    }
     cudaStream_t s = as_stream(stream);
     const bool pdl = (flags & TM_PDL) != 0;
-    return xtype == TM_F32   ? launch_attn<float>(D, nt, a, dev->sms, (int)row_tiles, join, s, pdl)
-           : xtype == TM_F16 ? launch_attn<__half>(D, nt, a, dev->sms, (int)row_tiles, join, s, pdl)
-                             : launch_attn<__nv_bfloat16>(D, nt, a, dev->sms, (int)row_tiles, join, s, pdl);
+    return xtype == TM_F32   ? launch_attn<float>(D, nt, a, device, dev->sms, join, s, pdl)
+           : xtype == TM_F16 ? launch_attn<__half>(D, nt, a, device, dev->sms, join, s, pdl)
+                             : launch_attn<__nv_bfloat16>(D, nt, a, device, dev->sms, join, s, pdl);
 }
