@@ -2,18 +2,21 @@
 //
 // Append: rotate q and k, hold k and v as codes (see tm.h for the format).
 // Bound by HBM: q is read and written, k and v read, their (D + 8) / 2 bytes a
-// vector written.  A block takes one token: its rot/2 sines and cosines go to
-// shared memory once, then every group of D/16 lanes takes a head, 16 values a
-// lane as two runs of 8 (the halves of 8 pairs), so a run's codes are one
-// 32-bit store and a vector's minimum and maximum are two or three shuffles.
+// vector written.  A warp takes a token and a run of its heads; its rot/2 sines
+// and cosines are computed once (two a lane) and passed through shared memory, so
+// no block-wide barrier is needed.  A group of D/16 lanes takes a head, 16 values
+// a lane as two runs of 8 (the halves of 8 pairs, whose sines and cosines stay in
+// registers over the heads): a run's codes are one 32-bit store and a vector's
+// minimum and maximum two or three shuffles.  The next heads' values are loaded
+// before the present ones are worked on.
 //
 // Exact codes.  fp32 leaves a rotated value off by up to about 2^-22 of its
 // pair's size, which moves a code only where (x - low) / step is that close to
 // a half, and step or low only where they are that close to a midpoint of two
-// fp16 numbers.  Those cases are found by bounds on the fp32 error (about one
-// value in 10^5 and one vector in 300) and decided by the same formula in fp64,
-// on the lanes concerned alone: fp64 runs at 1/64 of the fp32 rate here, and
-// deciding every value in it would take longer than the whole launch.
+// fp16 numbers.  One bound a vector finds those cases (a few vectors in a
+// thousand); they go through a second routine that decides the values concerned,
+// and only those, by the same formula in fp64: fp64 runs at 1/64 of the fp32 rate
+// here, and deciding every value in it would take longer than the whole launch.
 #include "tm_host.h"
 
 #include "tm_kv4.cuh"
@@ -29,8 +32,8 @@ struct AppendArgs {
     const int64_t *pos, *slots;
     const uint64_t *turns;
     uint8_t *pool;
-    int64_t slots_in_pool, page_bytes;
-    int page, Hq, Hkv, rot;
+    int64_t slots_in_pool, page_bytes, T;
+    int page, Hq, Hkv, rot, split;
     float gain;
     unsigned *status;
 };
@@ -65,161 +68,181 @@ __device__ __forceinline__ void store8(T *p, const float (&f)[8])
 __device__ __forceinline__ __half held_half(float x) { return __float2half_rn(fminf(fmaxf(x, -65504.0f), 65504.0f)); }
 __device__ __forceinline__ __half held_half_d(double x) { return held_half((float)x); }
 
-// One element of a rotated pair in fp64: a cos - b sin (first) or a sin + b cos.
-__device__ __noinline__ double exact_rotated(float a, float b, int64_t fraction, float gain, bool first)
+// Value i (0 .. 15) of a lane in fp64, from the tensor.
+template <typename T, bool INTER>
+__device__ __noinline__ double exact_value(const T *p, int o0, int o1, bool turn, int64_t pos, const uint64_t *turns,
+                                           float gain, int i)
 {
+    if (!turn) return (double)to_f(i < 8 ? p[o0 + i] : p[o1 + i - 8]);
+    const int pair = INTER ? i / 2 : i % 8;
+    const bool first = INTER ? i % 2 == 0 : i < 8;
+    const float a = to_f(INTER ? (pair < 4 ? p[o0 + 2 * pair] : p[o1 + 2 * pair - 8]) : p[o0 + pair]);
+    const float b = to_f(INTER ? (pair < 4 ? p[o0 + 2 * pair + 1] : p[o1 + 2 * pair - 7]) : p[o1 + pair]);
     double s, c;
-    sincospi((double)fraction * 0x1p-63, &s, &c);
+    sincospi((double)turn_fraction(pos, turns[pair]) * 0x1p-63, &s, &c);
     const double r = first ? (double)a * c - (double)b * s : (double)a * s + (double)b * c;
     return r * (double)gain;
 }
 
-__device__ __noinline__ int exact_code(double x, float low, float step)
+__device__ __forceinline__ int exact_code(double x, float low, float step)
 {
     const double t = rint((x - (double)low) / (double)step);
     return (int)fmin(fmax(t, 0.0), 15.0);
 }
 
-// A vector's 16 values in one lane: the fp32 values, the error each may have,
-// and what computes value i in fp64.
-template <int LANES, typename Exact>
-__device__ __forceinline__ void hold_vector(const float (&x)[2][8], const float (&err)[2][8], Exact exact,
-                                            uint32_t (&word)[2], __half2 &params)
+// Bounds of a vector's fp32 errors: `err` is how far any of its values may be
+// off.  Of the step and the low:
+struct Doubt {
+    float step, low;
+};
+__device__ __forceinline__ Doubt doubt_of(float err, float s, float lo)
 {
-    const unsigned lane = threadIdx.x & 31;
-    const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (lane / LANES * LANES);
-    // minimum and maximum, how far each may be off, and whether all are finite
-    float lo = INFINITY, hi = -INFINITY, worst = 0.0f, size = 0.0f;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            lo = fminf(lo, x[u][e]);
-            hi = fmaxf(hi, x[u][e]);
-            worst = fmaxf(worst, err[u][e]);
-            size += fabsf(x[u][e]);
-        }
-    const bool bad = __any_sync(mask, !(size < INFINITY));
-    lo = -lanes_max(-lo, LANES, mask);
-    hi = lanes_max(hi, LANES, mask);
-    worst = lanes_max(worst, LANES, mask);
-    if (bad || !(hi - lo < INFINITY)) {
-        word[0] = word[1] = 0;
-        params = __halves2half2(__ushort_as_half(0x7fff), __ushort_as_half(0x7fff));
-        return;
-    }
-    const float s = (hi - lo) * (1.0f / 15.0f);
-    const float es = worst * (2.0f / 15.0f) + s * 0x1p-21f, el = worst + fabsf(lo) * 0x1p-23f;
-    __half step = held_half(s), low = held_half(lo);
-    const bool unsure = __half_as_ushort(held_half(s - es)) != __half_as_ushort(held_half(s + es)) ||
-                        __half_as_ushort(held_half(lo - el)) != __half_as_ushort(held_half(lo + el));
-    if (unsure) {  // the same for every lane of the vector
-        // the values that may be the extremes, in fp64
-        double dlo = INFINITY, dhi = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (x[u][e] - err[u][e] <= lo + worst || x[u][e] + err[u][e] >= hi - worst) {
-                    const double d = exact(u, e);
-                    dlo = fmin(dlo, d);
-                    dhi = fmax(dhi, d);
-                }
-            }
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) {
-            dlo = fmin(dlo, __shfl_xor_sync(mask, dlo, o));
-            dhi = fmax(dhi, __shfl_xor_sync(mask, dhi, o));
-        }
-        step = held_half_d((dhi - dlo) / 15.0);
-        low = held_half_d(dlo);
-    }
-    const float fs = __half2float(step), fl = __half2float(low);
-    const float inv = fs > 0.0f ? 1.0f / fs : 0.0f;
-    word[0] = word[1] = 0;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = x[u][e] - fl, t = d * inv;
-            const float r = rintf(t);
-            // the value's error, the difference's rounding and the product's
-            const float et = (err[u][e] + fabsf(d) * 0x1p-23f) * inv + fabsf(t) * 0x1p-22f;
-            int c = (int)fminf(fmaxf(r, 0.0f), 15.0f);
-            if (fs > 0.0f && fabsf(t - r) + et >= 0.5f && t > -1.0f && t < 16.0f) c = exact_code(exact(u, e), fl, fs);
-            word[u] |= (uint32_t)c << (4 * e);
-        }
-    params = __halves2half2(step, low);
+    return {err * (2.0f / 15.0f) + s * 0x1p-21f, err + fabsf(lo) * 0x1p-23f};
 }
 
+// The slow path: two words of codes and (step, low), whatever is in doubt in fp64.
+// Called by all D/16 lanes of a vector; lo, hi: its fp32 minimum and maximum.
 template <typename T, int D, bool VEC, bool INTER>
-__global__ void __launch_bounds__(512) kv4_append_kernel(const __grid_constant__ AppendArgs a)
+__device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool turn, int64_t pos, const uint64_t *turns,
+                                           float gain, const float2 *table, float lo, float hi, float err)
 {
     constexpr int LANES = D / 16;
-    __shared__ float2 cs[D / 2];
+    const unsigned lane = threadIdx.x & 31, mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (lane / LANES * LANES);
+    float x[2][8];
+    float2 cs[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = turn ? table[e] : make_float2(1.0f, 0.0f);
+    load8<T, VEC>(p + o0, x[0]);
+    load8<T, VEC>(p + o1, x[1]);
+    if (turn) rotate_pairs<8, INTER>(x[0], x[1], cs);
+    uint32_t extreme = 0;  // the values that may be the minimum or the maximum
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (x[i / 8][i % 8] <= lo + 2 * err || x[i / 8][i % 8] >= hi - 2 * err) extreme |= 1u << i;
+    double dlo = INFINITY, dhi = -INFINITY;
+    for (; extreme; extreme &= extreme - 1) {
+        const double d = exact_value<T, INTER>(p, o0, o1, turn, pos, turns, gain, __ffs(extreme) - 1);
+        dlo = fmin(dlo, d);
+        dhi = fmax(dhi, d);
+    }
+    __syncwarp(mask);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        dlo = fmin(dlo, __shfl_xor_sync(mask, dlo, o));
+        dhi = fmax(dhi, __shfl_xor_sync(mask, dhi, o));
+    }
+    const __half step = held_half_d((dhi - dlo) / 15.0), low = held_half_d(dlo);
+    const float fs = __half2float(step), fl = __half2float(low);
+    const float inv = fs > 0.0f ? 1.0f / fs : 0.0f;
+    uint32_t word[2] = {0, 0}, close = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float d = x[i / 8][i % 8] - fl, t = d * inv, r = rintf(t);
+        // the value's error, the difference's rounding and the product's
+        const float et = (err + fabsf(d) * 0x1p-23f) * inv + fabsf(t) * 0x1p-22f;
+        if (fs > 0.0f && fabsf(t - r) + et >= 0.5f && t > -1.0f && t < 16.0f) close |= 1u << i;
+        word[i / 8] |= (uint32_t)fminf(fmaxf(r, 0.0f), 15.0f) << (i % 8 * 4);
+    }
+    for (; close; close &= close - 1) {
+        const int i = __ffs(close) - 1, sh = i % 8 * 4;
+        const uint32_t c = (uint32_t)exact_code(exact_value<T, INTER>(p, o0, o1, turn, pos, turns, gain, i), fl, fs) << sh;
+        if (i < 8)
+            word[0] = (word[0] & ~(15u << sh)) | c;
+        else
+            word[1] = (word[1] & ~(15u << sh)) | c;
+    }
+    const __half2 params = __halves2half2(step, low);
+    return make_uint3(word[0], word[1], *reinterpret_cast<const uint32_t *>(&params));
+}
+
+constexpr int kAppendWarps = 4;
+
+// One warp a task: token task / split, heads [part, part + 1) / split of its
+// passes of 512 / D heads.
+template <typename T, int D, bool VEC, bool INTER>
+__global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const __grid_constant__ AppendArgs a)
+{
+    constexpr int LANES = D / 16, PER = 32 / LANES;  // lanes a head, heads a pass
+    __shared__ float2 table[kAppendWarps][D / 2];
     pdl_trigger();
-    const int64_t t = blockIdx.x;
-    const int64_t slot = a.slots[t];
-    const int64_t pos = a.rot > 0 ? a.pos[t] : 0;
-    for (int i = threadIdx.x; i < a.rot / 2; i += blockDim.x) cs[i] = pair_rotation(pos, a.turns[i], a.gain, 1.0f);
-    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ln = lane % LANES;
+    const int64_t task = (int64_t)blockIdx.x * kAppendWarps + warp;
+    if (task >= a.T * a.split) {
+        pdl_wait();
+        return;
+    }
+    const int64_t t = task / a.split;
+    const int part = (int)(task - t * a.split);
+    const int heads = a.Hq + 2 * a.Hkv, passes = (heads + PER - 1) / PER;
+    const int pass0 = passes * part / a.split, pass1 = passes * (part + 1) / a.split;
+
+    const int half = a.rot / 2;
+    const bool turned = ln < a.rot / 16;  // this lane's 16 dims are 8 pairs
+    const int q0 = !turned || INTER ? 16 * ln : 8 * ln, q1 = !turned || INTER ? q0 + 8 : q0 + half;
+    // where this lane's head of a pass is read; nullptr past the last
+    auto head_ptr = [&](int h) -> const T * {
+        if (h >= heads) return nullptr;
+        if (h < a.Hq) return reinterpret_cast<const T *>(a.Q) + t * a.qs_tok + h * a.qs_head;
+        if (h < a.Hq + a.Hkv) return reinterpret_cast<const T *>(a.K) + t * a.ks_tok + (h - a.Hq) * a.ks_head;
+        return reinterpret_cast<const T *>(a.V) + t * a.vs_tok + (h - a.Hq - a.Hkv) * a.vs_head;
+    };
+    Vec<T, 8> n0, n1;
+    auto fetch = [&](int pass) {
+        const int h = pass * PER + lane / LANES;
+        const T *p = pass < pass1 ? head_ptr(h) : nullptr;
+        if (p == nullptr) return;
+        const bool v = h >= a.Hq + a.Hkv;
+        const T *p0 = p + (v ? 16 * ln : q0), *p1 = p + (v ? 16 * ln + 8 : q1);
+        if constexpr (VEC) {
+            load_vec(p0, n0);
+            load_vec(p1, n1);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                n0.v[e] = p0[e];
+                n1.v[e] = p1[e];
+            }
+        }
+    };
+    fetch(pass0);
+    const int64_t slot = a.slots[t], pos = a.rot > 0 ? a.pos[t] : 0;
+    for (int i = lane; i < half; i += 32) table[warp][i] = pair_rotation(pos, a.turns[i], a.gain, 1.0f);
+    __syncwarp();
+    float2 cs[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = turned ? table[warp][8 * ln + e] : make_float2(1.0f, 0.0f);
+
     const bool held = slot >= 0 && slot < a.slots_in_pool;
-    if (!held && slot != -1 && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusIndex);
+    if (!held && slot != -1 && lane == 0 && part == 0) atomicOr(a.status, kStatusIndex);
     uint8_t *block = nullptr;  // of KV head 0
     int r = 0;
     if (held) {
-        const int64_t pg = slot / a.page;
+        const int64_t pg = slot <= INT32_MAX ? (int64_t)((uint32_t)slot / (uint32_t)a.page) : slot / a.page;
         const int at = (int)(slot - pg * a.page);
         block = a.pool + pg * a.page_bytes + (int64_t)(at / 16) * kv4_block_bytes(D);
         r = at % 16;
     }
-    const int ln = threadIdx.x % LANES, half = a.rot / 2;
-    const bool turned = ln < a.rot / 16;  // this lane's 16 dims are 8 pairs
-    const int d0 = !turned || INTER ? 16 * ln : 8 * ln, d1 = !turned || INTER ? d0 + 8 : d0 + half;
-    const int heads = a.Hq + 2 * a.Hkv, slots = blockDim.x / LANES;
-    bool waited = false;
-    for (int h = blockIdx.y * slots + threadIdx.x / LANES; h < heads; h += gridDim.y * slots) {
-        const T *p;
-        const bool q = h < a.Hq, k = !q && h < a.Hq + a.Hkv;
-        if (q)
-            p = reinterpret_cast<const T *>(a.Q) + t * a.qs_tok + h * a.qs_head;
-        else if (k)
-            p = reinterpret_cast<const T *>(a.K) + t * a.ks_tok + (h - a.Hq) * a.ks_head;
-        else
-            p = reinterpret_cast<const T *>(a.V) + t * a.vs_tok + (h - a.Hq - a.Hkv) * a.vs_head;
-        const bool turn = turned && (q || k);
-        const int o0 = q || k ? d0 : 16 * ln, o1 = q || k ? d1 : 16 * ln + 8;
+    const int64_t head_bytes = (int64_t)(a.page / 16) * kv4_block_bytes(D);
+    pdl_wait();
+    for (int pass = pass0; pass < pass1; ++pass) {
         float x[2][8];
-        load8<T, VEC>(p + o0, x[0]);
-        load8<T, VEC>(p + o1, x[1]);
-        float in[2][8], err[2][8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            in[0][e] = x[0][e];
-            in[1][e] = x[1][e];
-            err[0][e] = err[1][e] = 0.0f;
-        }
+        widen(n0, x[0]);
+        widen(n1, x[1]);
+        fetch(pass + 1);
+        const int h = pass * PER + lane / LANES;
+        if (h >= heads) break;  // the last pass: whole groups of lanes leave
+        const bool q = h < a.Hq, k = !q && h < a.Hq + a.Hkv, turn = turned && (q || k);
+        const int o0 = q || k ? q0 : 16 * ln, o1 = q || k ? q1 : 16 * ln + 8;
+        float size = 0.0f;  // the largest |a| + |b| of a pair, for the error of a rotation
         if (turn) {
-            float2 rot8[8];
+            if (!q) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) rot8[e] = cs[8 * ln + e];
-            rotate_pairs<8, INTER>(x[0], x[1], rot8);
-            // |cos|, |sin| are off by at most 2.1e-7 (the argument's rounding
-            // pi 2^-25, sincospif's last place, the gain's rounding), the products
-            // and the sum add 2^-23 of |a| + |b|: 3.3e-7 in all, below 1.5 * 2^-22
-            const float ge = fabsf(a.gain) * 0x1.8p-22f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if constexpr (INTER) {
-                    err[e / 4][e % 4 * 2] = err[e / 4][e % 4 * 2 + 1] =
-                        (fabsf(in[e / 4][e % 4 * 2]) + fabsf(in[e / 4][e % 4 * 2 + 1])) * ge;
-                } else {
-                    err[0][e] = err[1][e] = (fabsf(in[0][e]) + fabsf(in[1][e])) * ge;
-                }
+                for (int e = 0; e < 8; ++e)
+                    size = fmaxf(size, INTER ? fabsf(x[e / 4][e % 4 * 2]) + fabsf(x[e / 4][e % 4 * 2 + 1])
+                                             : fabsf(x[0][e]) + fabsf(x[1][e]));
             }
+            rotate_pairs<8, INTER>(x[0], x[1], cs);
         }
-        if (!waited) pdl_wait();
-        waited = true;
         if (q) {
             T *o = reinterpret_cast<T *>(a.QO) + t * a.qos_tok + h * a.qos_head;
             store8<T, VEC>(o + o0, x[0]);
@@ -227,40 +250,68 @@ __global__ void __launch_bounds__(512) kv4_append_kernel(const __grid_constant__
             continue;
         }
         if (!held) continue;
-        auto exact = [&](int u, int e) -> double {
-            if (!turn) return (double)in[u][e];
-            float pa, pb;
-            int pair;
-            bool first;
-            if constexpr (INTER) {
-                pair = 4 * u + e / 2;
-                first = e % 2 == 0;
-                pa = in[u][e / 2 * 2];
-                pb = in[u][e / 2 * 2 + 1];
-            } else {
-                pair = e;
-                first = u == 0;
-                pa = in[0][e];
-                pb = in[1][e];
-            }
-            return exact_rotated(pa, pb, turn_fraction(pos, a.turns[8 * ln + pair]), a.gain, first);
-        };
+        const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (lane / LANES * LANES);
+        float lo = INFINITY, hi = -INFINITY, finite = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            lo = fminf(lo, x[i / 8][i % 8]);
+            hi = fmaxf(hi, x[i / 8][i % 8]);
+            finite = fmaf(x[i / 8][i % 8], 0.0f, finite);  // 0, or a NaN
+        }
+        // |cos|, |sin| are off by at most 2.1e-7 (the argument's rounding pi 2^-25,
+        // sincospif's last place, the gain's rounding), the products and the sum add
+        // 2^-23 of |a| + |b|: 3.3e-7 in all, below 1.5 * 2^-22
+        float err = size * fabsf(a.gain) * 0x1.8p-22f;
+        const bool bad = __any_sync(mask, finite != 0.0f);
+        lo = -lanes_max(-lo, LANES, mask);
+        hi = lanes_max(hi, LANES, mask);
+        err = lanes_max(err, LANES, mask);
         uint32_t word[2];
         __half2 params;
-        hold_vector<LANES>(x, err, exact, word, params);
-        const int kvh = k ? h - a.Hq : h - a.Hq - a.Hkv;
-        uint8_t *b = block + (int64_t)kvh * (a.page / 16) * kv4_block_bytes(D);
-        if (k) {
-            *reinterpret_cast<uint32_t *>(b + kv4_k_word(D, r, o0)) = word[0];
-            *reinterpret_cast<uint32_t *>(b + kv4_k_word(D, r, o1)) = word[1];
-            if (ln == 0) *reinterpret_cast<__half2 *>(b + kv4_ks_off(D) + 4 * r) = params;
+        if (bad || !(hi - lo < INFINITY)) {
+            word[0] = word[1] = 0;
+            params = __halves2half2(__ushort_as_half(0x7fff), __ushort_as_half(0x7fff));
         } else {
-            *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, o0)) = word[0];
-            *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, o1)) = word[1];
-            if (ln == 0) *reinterpret_cast<__half2 *>(b + kv4_vs_off(D) + 4 * r) = params;
+            const float s = (hi - lo) * (1.0f / 15.0f);
+            const Doubt u = doubt_of(err, s, lo);
+            const __half step = held_half(s), low = held_half(lo);
+            bool unsure = __half_as_ushort(held_half(s - u.step)) != __half_as_ushort(held_half(s + u.step)) ||
+                          __half_as_ushort(held_half(lo - u.low)) != __half_as_ushort(held_half(lo + u.low));
+            const float fs = __half2float(step), fl = __half2float(low);
+            const float inv = fs > 0.0f ? 1.0f / fs : 0.0f;
+            // t = (x - low) / step as 15 times a value cut to [0, 1]; adding 1.5 * 2^23
+            // rounds it to a whole number, in the low bits of the sum
+            const float m15 = inv * (1.0f / 15.0f), c15 = -fl * m15, magic = 12582912.0f;
+            float off = 0.0f;  // the largest distance from a whole number
+            word[0] = word[1] = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float t15 = __saturatef(fmaf(x[i / 8][i % 8], m15, c15));
+                const float sum = fmaf(t15, 15.0f, magic), whole = sum - magic;
+                off = fmaxf(off, fabsf(fmaf(t15, 15.0f, -whole)));
+                word[i / 8] += __float_as_uint(sum) << (i % 8 * 4);
+            }
+            word[0] -= 0x4b400000u * 0x11111111u;
+            word[1] -= 0x4b400000u * 0x11111111u;
+            params = __halves2half2(step, low);
+            // the values' error, three roundings of t up to 15, and those of low / step
+            const float et = (err + fabsf(fl) * 0x1p-22f) * inv + 15.0f * 0x1p-22f;
+            unsure = unsure || off + et >= 0.5f;
+            if (__any_sync(mask, unsure)) {
+                const uint3 w = hold_exactly<T, D, VEC, INTER>(head_ptr(h), o0, o1, turn, pos, a.turns + 8 * ln, a.gain,
+                                                               &table[warp][turn ? 8 * ln : 0], lo, hi, err);
+                word[0] = w.x;
+                word[1] = w.y;
+                params = *reinterpret_cast<const __half2 *>(&w.z);
+            }
         }
+        const int kvh = k ? h - a.Hq : h - a.Hq - a.Hkv;
+        uint8_t *b = block + kvh * head_bytes;
+        const int w0 = k ? kv4_k_word(D, r, o0) : kv4_v_word(D, r, o0), w1 = k ? kv4_k_word(D, r, o1) : kv4_v_word(D, r, o1);
+        *reinterpret_cast<uint32_t *>(b + w0) = word[0];
+        *reinterpret_cast<uint32_t *>(b + w1) = word[1];
+        if (ln == 0) *reinterpret_cast<__half2 *>(b + (k ? kv4_ks_off(D) : kv4_vs_off(D)) + 4 * r) = params;
     }
-    if (!waited) pdl_wait();
 }
 
 struct GatherArgs {
@@ -291,7 +342,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
         uint32_t kw[2] = {0, 0}, vw[2] = {0, 0};
         float2 kp = {0.0f, 0.0f}, vp = {0.0f, 0.0f};
         if (held) {
-            const int64_t pg = slot / a.page;
+            const int64_t pg = slot <= INT32_MAX ? (int64_t)((uint32_t)slot / (uint32_t)a.page) : slot / a.page;
             const int at = (int)(slot - pg * a.page), r = at % 16;
             const uint8_t *b = a.pool + pg * a.page_bytes + ((int64_t)h * (a.page / 16) + at / 16) * kv4_block_bytes(D);
 #pragma unroll
@@ -400,24 +451,20 @@ extern "C" tm_status tm_kv4_append(const void *Q, int64_t qs_tok, int64_t qs_hea
     const DevInfo *dev;
     tm_status st = device_info(&dev);
     if (st != TM_OK) return st;
+    // Tasks: about two rounds of the warps the GPU holds, each at least one pass of heads.
+    const int64_t passes = ((int64_t)Hq + 2 * Hkv + 512 / D - 1) / (512 / D), want = 40LL * dev->sms;
+    int64_t split = (want + T - 1) / T;
+    if (split > passes) split = passes;
     AppendArgs a = {Q, K, V, QO, qs_tok, qs_head, qos_tok, qos_head, ks_tok, ks_head, vs_tok, vs_head, pos, slots, turns,
-                    reinterpret_cast<uint8_t *>(pool), pages * page, pb, page, Hq, Hkv, rot, gain, dev->status};
-    const int lanes = D / 16;
-    const int heads = Hq + 2 * Hkv;
-    int threads = (heads * lanes + 31) / 32 * 32;
-    threads = threads > 512 ? 512 : threads;
-    // few tokens: heads split over blocks, each of at least a warp's heads
-    int split = 1;
-    while (threads > 64 && T * split * 2 <= dev->sms) {
-        split *= 2;
-        threads = (threads / 2 + 31) / 32 * 32;
-    }
+                    reinterpret_cast<uint8_t *>(pool), pages * page, pb, T, page, Hq, Hkv, rot, (int)split, gain,
+                    dev->status};
+    const int64_t blocks = (T * split + kAppendWarps - 1) / kAppendWarps;
     const bool inter = (flags & TM_ROPE_INTERLEAVED) != 0;
     const void *kern = xtype == TM_F32   ? append_kernel<float>(D, vec, inter)
                        : xtype == TM_F16 ? append_kernel<__half>(D, vec, inter)
                                          : append_kernel<__nv_bfloat16>(D, vec, inter);
     void *args[] = {&a};
-    return launch_kernel(kern, dim3((unsigned)T, (unsigned)split), dim3((unsigned)threads), args, 0, as_stream(stream),
+    return launch_kernel(kern, dim3((unsigned)blocks), dim3(kAppendWarps * 32), args, 0, as_stream(stream),
                          (flags & TM_PDL) != 0);
 }
 
