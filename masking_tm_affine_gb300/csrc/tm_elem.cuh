@@ -7,6 +7,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "tm_device.cuh"
 
 namespace libtm {
@@ -83,11 +85,37 @@ __device__ __forceinline__ void widen(const Vec<T, W> &r, float (&f)[W])
     for (int e = 0; e < W; ++e) f[e] = to_f(r.v[e]);
 }
 
+// Rounded to nearest, two values an instruction.
 template <typename T, int W>
 __device__ __forceinline__ void narrow(const float (&f)[W], Vec<T, W> &r)
 {
+    if constexpr (sizeof(T) == 2 && W % 2 == 0) {
+        uint32_t *u = reinterpret_cast<uint32_t *>(&r);
 #pragma unroll
-    for (int e = 0; e < W; ++e) r.v[e] = from_f<T>(f[e]);
+        for (int e = 0; e < W / 2; ++e) {
+            if constexpr (std::is_same<T, __half>::value)
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u[e]) : "f"(f[2 * e + 1]), "f"(f[2 * e]));
+            else
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[e]) : "f"(f[2 * e + 1]), "f"(f[2 * e]));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) r.v[e] = from_f<T>(f[e]);
+    }
+}
+
+// 2^x, good to two places; 1 / x likewise, for x whose reciprocal is a normal number.
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // Maximum over the `lanes` (a power of two) consecutive lanes that share a row.

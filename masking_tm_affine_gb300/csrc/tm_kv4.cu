@@ -14,8 +14,9 @@
 // pair's size, which moves a code only where (x - low) / step is that close to
 // a half, and step or low only where they are that close to a midpoint of two
 // fp16 numbers.  One bound a vector finds those cases (a few vectors in a
-// thousand); they go through a second routine that decides the values concerned,
-// and only those, by the same formula in fp64: fp64 runs at 1/64 of the fp32 rate
+// thousand); after its heads a warp goes through those again, in a second routine
+// (out of the loop, whose registers a call in it would spill) that decides the values
+// concerned, and only those, by the same formula in fp64: fp64 runs at 1/64 of the fp32 rate
 // here, and deciding every value in it would take longer than the whole launch.
 #include "tm_host.h"
 
@@ -68,6 +69,65 @@ __device__ __forceinline__ void store8(T *p, const float (&f)[8])
 __device__ __forceinline__ __half held_half(float x) { return __float2half_rn(fminf(fmaxf(x, -65504.0f), 65504.0f)); }
 __device__ __forceinline__ __half held_half_d(double x) { return held_half((float)x); }
 
+// Largest and smallest of three, NaN if any is.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ void extremes(const float (&x)[2][8], float &lo, float &hi)
+{
+    lo = hi = x[0][0];
+#pragma unroll
+    for (int i = 1; i < 15; i += 2) {
+        lo = min3(lo, x[i / 8][i % 8], x[(i + 1) / 8][(i + 1) % 8]);
+        hi = max3(hi, x[i / 8][i % 8], x[(i + 1) / 8][(i + 1) % 8]);
+    }
+    lo = min3(lo, x[1][7], x[1][7]);
+    hi = max3(hi, x[1][7], x[1][7]);
+}
+
+// Of the vector that LANES lanes hold.
+template <int LANES>
+__device__ __forceinline__ void vector_extremes(const float (&x)[2][8], unsigned mask, float &lo, float &hi)
+{
+    extremes(x, lo, hi);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        const float l = __shfl_xor_sync(mask, lo, o), h = __shfl_xor_sync(mask, hi, o);
+        lo = min3(lo, l, l);
+        hi = max3(hi, h, h);
+    }
+}
+
+// How far a rotated value may be off in fp32.  |cos|, |sin| are off by at most
+// 2.1e-7 (the argument's rounding pi 2^-25, sincospif's last place, the gain's
+// rounding), the products and the sum add 2^-23 of |a| + |b|: 3.3e-7 in all, below
+// 1.5 * 2^-22, and gain (|a| + |b|) is at most twice the larger of the vector's
+// rotated extremes.
+__device__ __forceinline__ float vector_error(bool turn, float lo, float hi)
+{
+    return turn ? fmaxf(fabsf(lo), fabsf(hi)) * 0x1.82p-21f : 0.0f;
+}
+
+// Bounds of a vector's fp32 errors: `err` is how far any of its values may be
+// off.  Of the step and the low:
+struct Doubt {
+    float step, low;
+};
+__device__ __forceinline__ Doubt doubt_of(float err, float s, float lo)
+{
+    return {err * (2.0f / 15.0f) + s * 0x1p-21f, err + fabsf(lo) * 0x1p-23f};
+}
+
 // Value i (0 .. 15) of a lane in fp64, from the tensor.
 template <typename T, bool INTER>
 __device__ __noinline__ double exact_value(const T *p, int o0, int o1, bool turn, int64_t pos, const uint64_t *turns,
@@ -90,21 +150,11 @@ __device__ __forceinline__ int exact_code(double x, float low, float step)
     return (int)fmin(fmax(t, 0.0), 15.0);
 }
 
-// Bounds of a vector's fp32 errors: `err` is how far any of its values may be
-// off.  Of the step and the low:
-struct Doubt {
-    float step, low;
-};
-__device__ __forceinline__ Doubt doubt_of(float err, float s, float lo)
-{
-    return {err * (2.0f / 15.0f) + s * 0x1p-21f, err + fabsf(lo) * 0x1p-23f};
-}
-
 // The slow path: two words of codes and (step, low), whatever is in doubt in fp64.
-// Called by all D/16 lanes of a vector; lo, hi: its fp32 minimum and maximum.
+// Called by all D/16 lanes of a vector without NaN or infinity.
 template <typename T, int D, bool VEC, bool INTER>
-__device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool turn, int64_t pos, const uint64_t *turns,
-                                           float gain, const float2 *table, float lo, float hi, float err)
+__device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool rotated, bool turn, int64_t pos, const uint64_t *turns,
+                                           float gain, const float2 *table)
 {
     constexpr int LANES = D / 16;
     const unsigned lane = threadIdx.x & 31, mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (lane / LANES * LANES);
@@ -115,6 +165,9 @@ __device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool turn
     load8<T, VEC>(p + o0, x[0]);
     load8<T, VEC>(p + o1, x[1]);
     if (turn) rotate_pairs<8, INTER>(x[0], x[1], cs);
+    float lo, hi;
+    vector_extremes<LANES>(x, mask, lo, hi);
+    const float err = vector_error(rotated, lo, hi);
     uint32_t extreme = 0;  // the values that may be the minimum or the maximum
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -173,38 +226,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
     }
     const int64_t t = task / a.split;
     const int part = (int)(task - t * a.split);
-    const int heads = a.Hq + 2 * a.Hkv, passes = (heads + PER - 1) / PER;
+    // passes over the query heads, then the key heads, then the value heads
+    const int nq = (a.Hq + PER - 1) / PER, nk = (a.Hkv + PER - 1) / PER, passes = nq + 2 * nk;
     const int pass0 = passes * part / a.split, pass1 = passes * (part + 1) / a.split;
 
     const int half = a.rot / 2;
     const bool turned = ln < a.rot / 16;  // this lane's 16 dims are 8 pairs
     const int q0 = !turned || INTER ? 16 * ln : 8 * ln, q1 = !turned || INTER ? q0 + 8 : q0 + half;
-    // where this lane's head of a pass is read; nullptr past the last
-    auto head_ptr = [&](int h) -> const T * {
-        if (h >= heads) return nullptr;
-        if (h < a.Hq) return reinterpret_cast<const T *>(a.Q) + t * a.qs_tok + h * a.qs_head;
-        if (h < a.Hq + a.Hkv) return reinterpret_cast<const T *>(a.K) + t * a.ks_tok + (h - a.Hq) * a.ks_head;
-        return reinterpret_cast<const T *>(a.V) + t * a.vs_tok + (h - a.Hq - a.Hkv) * a.vs_head;
-    };
-    Vec<T, 8> n0, n1;
-    auto fetch = [&](int pass) {
-        const int h = pass * PER + lane / LANES;
-        const T *p = pass < pass1 ? head_ptr(h) : nullptr;
-        if (p == nullptr) return;
-        const bool v = h >= a.Hq + a.Hkv;
-        const T *p0 = p + (v ? 16 * ln : q0), *p1 = p + (v ? 16 * ln + 8 : q1);
-        if constexpr (VEC) {
-            load_vec(p0, n0);
-            load_vec(p1, n1);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                n0.v[e] = p0[e];
-                n1.v[e] = p1[e];
-            }
-        }
-    };
-    fetch(pass0);
     const int64_t slot = a.slots[t], pos = a.rot > 0 ? a.pos[t] : 0;
     for (int i = lane; i < half; i += 32) table[warp][i] = pair_rotation(pos, a.turns[i], a.gain, 1.0f);
     __syncwarp();
@@ -224,61 +252,67 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
     }
     const int64_t head_bytes = (int64_t)(a.page / 16) * kv4_block_bytes(D);
     pdl_wait();
-    for (int pass = pass0; pass < pass1; ++pass) {
-        float x[2][8];
-        widen(n0, x[0]);
-        widen(n1, x[1]);
-        fetch(pass + 1);
-        const int h = pass * PER + lane / LANES;
-        if (h >= heads) break;  // the last pass: whole groups of lanes leave
-        const bool q = h < a.Hq, k = !q && h < a.Hq + a.Hkv, turn = turned && (q || k);
-        const int o0 = q || k ? q0 : 16 * ln, o1 = q || k ? q1 : 16 * ln + 8;
-        float size = 0.0f;  // the largest |a| + |b| of a pair, for the error of a rotation
-        if (turn) {
-            if (!q) {
+
+    // Passes [p0, p1) of one tensor of H heads; every lane has its two runs in hand
+    // one pass ahead.
+    auto walk = [&](const T *base, int64_t tok, int64_t head, int H, int p0, int p1, int o0, int o1, auto work) {
+        if (p0 >= p1) return;
+        const int h0 = p0 * PER + lane / LANES;
+        const T *p = base + t * tok + h0 * head;
+        Vec<T, 8> n0, n1;
+        auto fetch = [&](int h) {
+            if (h >= H) return;
+            if constexpr (VEC) {
+                load_vec(p + o0, n0);
+                load_vec(p + o1, n1);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    size = fmaxf(size, INTER ? fabsf(x[e / 4][e % 4 * 2]) + fabsf(x[e / 4][e % 4 * 2 + 1])
-                                             : fabsf(x[0][e]) + fabsf(x[1][e]));
+                for (int e = 0; e < 8; ++e) {
+                    n0.v[e] = p[o0 + e];
+                    n1.v[e] = p[o1 + e];
+                }
             }
-            rotate_pairs<8, INTER>(x[0], x[1], cs);
+        };
+        fetch(h0);
+        for (int h = h0, i = p0; i < p1; ++i, h += PER) {
+            float x[2][8];
+            widen(n0, x[0]);
+            widen(n1, x[1]);
+            p += PER * head;
+            if (i + 1 < p1) fetch(h + PER);
+            if (h < H) work(h, x);  // whole groups of lanes
         }
-        if (q) {
-            T *o = reinterpret_cast<T *>(a.QO) + t * a.qos_tok + h * a.qos_head;
-            store8<T, VEC>(o + o0, x[0]);
-            store8<T, VEC>(o + o1, x[1]);
-            continue;
-        }
-        if (!held) continue;
-        const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (lane / LANES * LANES);
-        float lo = INFINITY, hi = -INFINITY, finite = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            lo = fminf(lo, x[i / 8][i % 8]);
-            hi = fmaxf(hi, x[i / 8][i % 8]);
-            finite = fmaf(x[i / 8][i % 8], 0.0f, finite);  // 0, or a NaN
-        }
-        // |cos|, |sin| are off by at most 2.1e-7 (the argument's rounding pi 2^-25,
-        // sincospif's last place, the gain's rounding), the products and the sum add
-        // 2^-23 of |a| + |b|: 3.3e-7 in all, below 1.5 * 2^-22
-        float err = size * fabsf(a.gain) * 0x1.8p-22f;
-        const bool bad = __any_sync(mask, finite != 0.0f);
-        lo = -lanes_max(-lo, LANES, mask);
-        hi = lanes_max(hi, LANES, mask);
-        err = lanes_max(err, LANES, mask);
+    };
+    walk(reinterpret_cast<const T *>(a.Q), a.qs_tok, a.qs_head, a.Hq, pass0, min(pass1, nq), q0, q1,
+         [&](int h, float (&x)[2][8]) {
+             if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
+             T *o = reinterpret_cast<T *>(a.QO) + t * a.qos_tok + h * a.qos_head;
+             store8<T, VEC>(o + q0, x[0]);
+             store8<T, VEC>(o + q1, x[1]);
+         });
+    if (!held) return;
+    // Hold a vector and store it at its words of a block, its (step, low) at `at`.
+    const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (lane / LANES * LANES);
+    // True if fp32 could not decide all of it.
+    auto hold = [&](float (&x)[2][8], bool turn, uint8_t *w0, uint8_t *w1, uint8_t *at) -> bool {
+        float lo, hi;
+        vector_extremes<LANES>(x, mask, lo, hi);  // NaN if any value is
+        const float err = vector_error(turn, lo, hi);
+        bool unsure = false;
         uint32_t word[2];
         __half2 params;
-        if (bad || !(hi - lo < INFINITY)) {
+        if (!(hi - lo < INFINITY)) {
             word[0] = word[1] = 0;
             params = __halves2half2(__ushort_as_half(0x7fff), __ushort_as_half(0x7fff));
         } else {
             const float s = (hi - lo) * (1.0f / 15.0f);
             const Doubt u = doubt_of(err, s, lo);
             const __half step = held_half(s), low = held_half(lo);
-            bool unsure = __half_as_ushort(held_half(s - u.step)) != __half_as_ushort(held_half(s + u.step)) ||
-                          __half_as_ushort(held_half(lo - u.low)) != __half_as_ushort(held_half(lo + u.low));
+            unsure = __half_as_ushort(held_half(s - u.step)) != __half_as_ushort(held_half(s + u.step)) ||
+                     __half_as_ushort(held_half(lo - u.low)) != __half_as_ushort(held_half(lo + u.low));
             const float fs = __half2float(step), fl = __half2float(low);
-            const float inv = fs > 0.0f ? 1.0f / fs : 0.0f;
+            // steps are 0 or at least 2^-24: the reciprocal is a normal number
+            const float inv = fs > 0.0f ? rcp(fs) : 0.0f;
             // t = (x - low) / step as 15 times a value cut to [0, 1]; adding 1.5 * 2^23
             // rounds it to a whole number, in the low bits of the sum
             const float m15 = inv * (1.0f / 15.0f), c15 = -fl * m15, magic = 12582912.0f;
@@ -294,23 +328,50 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
             word[0] -= 0x4b400000u * 0x11111111u;
             word[1] -= 0x4b400000u * 0x11111111u;
             params = __halves2half2(step, low);
-            // the values' error, three roundings of t up to 15, and those of low / step
-            const float et = (err + fabsf(fl) * 0x1p-22f) * inv + 15.0f * 0x1p-22f;
+            // the values' error, five roundings of t up to 15 (the reciprocal counts two),
+            // and those of low / step
+            const float et = (err + fabsf(fl) * 0x1p-21f) * inv + 15.0f * 0x1.4p-22f;
             unsure = unsure || off + et >= 0.5f;
-            if (__any_sync(mask, unsure)) {
-                const uint3 w = hold_exactly<T, D, VEC, INTER>(head_ptr(h), o0, o1, turn, pos, a.turns + 8 * ln, a.gain,
-                                                               &table[warp][turn ? 8 * ln : 0], lo, hi, err);
-                word[0] = w.x;
-                word[1] = w.y;
-                params = *reinterpret_cast<const __half2 *>(&w.z);
-            }
         }
-        const int kvh = k ? h - a.Hq : h - a.Hq - a.Hkv;
-        uint8_t *b = block + kvh * head_bytes;
-        const int w0 = k ? kv4_k_word(D, r, o0) : kv4_v_word(D, r, o0), w1 = k ? kv4_k_word(D, r, o1) : kv4_v_word(D, r, o1);
-        *reinterpret_cast<uint32_t *>(b + w0) = word[0];
-        *reinterpret_cast<uint32_t *>(b + w1) = word[1];
-        if (ln == 0) *reinterpret_cast<__half2 *>(b + (k ? kv4_ks_off(D) : kv4_vs_off(D)) + 4 * r) = params;
+        *reinterpret_cast<uint32_t *>(w0) = word[0];
+        *reinterpret_cast<uint32_t *>(w1) = word[1];
+        if (ln == 0) *reinterpret_cast<__half2 *>(at) = params;
+        return __any_sync(mask, unsure);
+    };
+    uint32_t again_k = 0, again_v = 0;  // passes to go through again, from the first of this task
+    const int k0 = max(pass0 - nq, 0), k1 = min(pass1 - nq, nk), v0 = max(pass0 - nq - nk, 0), v1 = pass1 - nq - nk;
+    walk(reinterpret_cast<const T *>(a.K), a.ks_tok, a.ks_head, a.Hkv, k0, k1, q0, q1,
+         [&](int h, float (&x)[2][8]) {
+             if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
+             uint8_t *b = block + h * head_bytes;
+             if (hold(x, a.rot > 0, b + kv4_k_word(D, r, q0), b + kv4_k_word(D, r, q1), b + kv4_ks_off(D) + 4 * r))
+                 again_k |= 1u << (h / PER - k0);
+         });
+    walk(reinterpret_cast<const T *>(a.V), a.vs_tok, a.vs_head, a.Hkv, v0, v1, 16 * ln, 16 * ln + 8,
+         [&](int h, float (&x)[2][8]) {
+             uint8_t *b = block + h * head_bytes;
+             if (hold(x, false, b + kv4_v_word(D, r, 16 * ln), b + kv4_v_word(D, r, 16 * ln + 8), b + kv4_vs_off(D) + 4 * r))
+                 again_v |= 1u << (h / PER - v0);
+         });
+    for (; again_k; again_k &= again_k - 1) {
+        const int h = (k0 + __ffs(again_k) - 1) * PER + lane / LANES;
+        const T *p = reinterpret_cast<const T *>(a.K) + t * a.ks_tok + h * a.ks_head;
+        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, q0, q1, a.rot > 0, turned, pos, a.turns + 8 * ln, a.gain,
+                                                       &table[warp][turned ? 8 * ln : 0]);
+        uint8_t *b = block + h * head_bytes;
+        *reinterpret_cast<uint32_t *>(b + kv4_k_word(D, r, q0)) = w.x;
+        *reinterpret_cast<uint32_t *>(b + kv4_k_word(D, r, q1)) = w.y;
+        if (ln == 0) *reinterpret_cast<uint32_t *>(b + kv4_ks_off(D) + 4 * r) = w.z;
+    }
+    for (; again_v; again_v &= again_v - 1) {
+        const int h = (v0 + __ffs(again_v) - 1) * PER + lane / LANES;
+        const T *p = reinterpret_cast<const T *>(a.V) + t * a.vs_tok + h * a.vs_head;
+        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, 16 * ln, 16 * ln + 8, false, false, pos, a.turns, a.gain,
+                                                       &table[warp][0]);
+        uint8_t *b = block + h * head_bytes;
+        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, 16 * ln)) = w.x;
+        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, 16 * ln + 8)) = w.y;
+        if (ln == 0) *reinterpret_cast<uint32_t *>(b + kv4_vs_off(D) + 4 * r) = w.z;
     }
 }
 
@@ -452,13 +513,15 @@ extern "C" tm_status tm_kv4_append(const void *Q, int64_t qs_tok, int64_t qs_hea
     tm_status st = device_info(&dev);
     if (st != TM_OK) return st;
     // Tasks: about two rounds of the warps the GPU holds, each at least one pass of heads.
-    const int64_t passes = ((int64_t)Hq + 2 * Hkv + 512 / D - 1) / (512 / D), want = 40LL * dev->sms;
+    const int64_t per = 512 / D, passes = (Hq + per - 1) / per + 2 * ((Hkv + per - 1) / per), want = 40LL * dev->sms;
     int64_t split = (want + T - 1) / T;
+    if (split * 32 < passes) split = (passes + 31) / 32;  // a task notes its passes in 32 bits
     if (split > passes) split = passes;
     AppendArgs a = {Q, K, V, QO, qs_tok, qs_head, qos_tok, qos_head, ks_tok, ks_head, vs_tok, vs_head, pos, slots, turns,
                     reinterpret_cast<uint8_t *>(pool), pages * page, pb, T, page, Hq, Hkv, rot, (int)split, gain,
                     dev->status};
     const int64_t blocks = (T * split + kAppendWarps - 1) / kAppendWarps;
+    if (blocks > INT32_MAX) return TM_ERR_INVALID_ARG;
     const bool inter = (flags & TM_ROPE_INTERLEAVED) != 0;
     const void *kern = xtype == TM_F32   ? append_kernel<float>(D, vec, inter)
                        : xtype == TM_F16 ? append_kernel<__half>(D, vec, inter)

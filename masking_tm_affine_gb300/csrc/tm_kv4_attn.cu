@@ -60,13 +60,6 @@ constexpr int kSlack = 8, kStepBits = 4;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2eF = 1.4426950408889634f;
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {

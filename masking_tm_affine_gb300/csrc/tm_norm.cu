@@ -26,9 +26,12 @@ namespace {
 
 constexpr int kMaxCols = 32768;  // what a block of 1024 lanes holds in registers
 
-// Largest block an instance is launched with (see pick_lanes).
+// Largest block an instance of the norm and of its gradient is launched with (see
+// pick_lanes).
 template <int EW, int K>
-constexpr int kMostLanes = (EW == 1 ? K > 8 : K > 4) ? 1024 : 512;
+constexpr int kNormLanes = (EW == 1 && K > 8) || (EW == 4 && K >= 4) ? 1024 : 512;
+template <int EW, int K>
+constexpr int kGradLanes = (EW == 1 && K > 8) || (EW == 4 && K > 4) ? 1024 : 512;
 
 // Sum over the L lanes of a row.  L > 32: through shared memory, warps added
 // in order, one barrier per call (the caller alternates between two buffers,
@@ -59,27 +62,48 @@ __device__ __forceinline__ float row_max(float x, int L, float *buf)
     return x;
 }
 
-// Index of a lane's k-th vector in its row (in vectors).
-template <int K>
-__device__ __forceinline__ int vec_index(int ln, int k, int L)
+// Columns of a lane's vectors: column0, + step, + 2 step, ...
+template <int EW, int K>
+__device__ __forceinline__ int first_column(int ln, int L)
 {
-    return L < 32 ? k * L + ln : ((ln >> 5) * K + k) * 32 + (ln & 31);
+    return (L < 32 ? ln : (ln >> 5) * K * 32 + (ln & 31)) * EW;
+}
+template <int EW>
+__device__ __forceinline__ int column_step(int L)
+{
+    return (L < 32 ? L : 32) * EW;
 }
 
-template <typename T, int EW>
-__device__ __forceinline__ void load_weight(const void *W, int wf32, int64_t j, float (&w)[EW])
+// A lane's vectors of a row, zeros past its end (n columns).
+template <typename T, int EW, int K>
+__device__ __forceinline__ void load_row(const T *p, int j0, int step, int n, Vec<T, EW> (&v)[K])
 {
-    if (W == nullptr) {
 #pragma unroll
-        for (int e = 0; e < EW; ++e) w[e] = 1.0f;
-    } else if (wf32) {
-        const float *p = reinterpret_cast<const float *>(W) + j;
+    for (int k = 0; k < K; ++k) {
+        const int j = j0 + k * step;
+        if (j < n) {
+            load_vec(p + j, v[k]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < EW; ++e) w[e] = __ldg(p + e);
-    } else {
-        const T *p = reinterpret_cast<const T *>(W) + j;
-        const Vec<T, EW> r = *reinterpret_cast<const Vec<T, EW> *>(p);
-        widen(r, w);
+            for (int e = 0; e < EW; ++e) v[k].v[e] = from_f<T>(0.0f);
+        }
+    }
+}
+
+// A lane's weights (every row reads the same: through L1), ones if there are none.
+template <typename WT, int EW, int K>
+__device__ __forceinline__ void load_weights(const void *W, int j0, int step, int n, Vec<WT, EW> (&v)[K])
+{
+    const WT *p = reinterpret_cast<const WT *>(W);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = j0 + k * step;
+        if (p != nullptr && j < n) {
+            v[k] = *reinterpret_cast<const Vec<WT, EW> *>(p + j);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EW; ++e) v[k].v[e] = from_f<WT>(1.0f);
+        }
     }
 }
 
@@ -105,134 +129,135 @@ struct NormArgs {
     void *H, *Y;
     float *scales, *rstd;
     int64_t ldx, ldr, ldh, ldy, M;
-    int N, L, group, wf32;
-    float eps;
+    int N, L, group, group_log;
+    float eps, inv_n;
 };
 
+// What maps a largest magnitude of `top` to 448, and what a code of 1 then
+// stands for.  The approximate reciprocal is good to two places; where it
+// would leave the normal numbers, a division.
+__device__ __forceinline__ float e4m3_factor(float top)
+{
+    if (top > 0x1p-100f && top < 0x1p100f) return 448.0f * rcp(top);
+    return top > 0.0f ? 448.0f / top : 1.0f;
+}
+__device__ __forceinline__ float e4m3_scale(float top) { return top > 0.0f ? top * (1.0f / 448.0f) : 1.0f; }
+
 // One block per blockDim.x / L rows.
-template <typename T, int EW, int K, bool E4M3>
-__global__ void __launch_bounds__(kMostLanes<EW, K>) rmsnorm_kernel(const __grid_constant__ NormArgs a)
+template <typename T, typename WT, int EW, int K, bool E4M3>
+__global__ void __launch_bounds__(kNormLanes<EW, K>) rmsnorm_kernel(const __grid_constant__ NormArgs a)
 {
     __shared__ float buf[2][32];
     pdl_trigger();
     const int L = a.L, ln = threadIdx.x & (L - 1);
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / L) + threadIdx.x / L;
-    const bool live = row < a.M;
-    const T *x = reinterpret_cast<const T *>(a.X) + row * a.ldx;
-    const T *r = reinterpret_cast<const T *>(a.R) + row * a.ldr;
-    Vec<T, EW> vx[K], vr[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int j = vec_index<K>(ln, k, L) * EW;
-        if (live && j < a.N) {
-            load_vec(x + j, vx[k]);
-            if (a.R) load_vec(r + j, vr[k]);
-        }
-    }
+    const int n = row < a.M ? a.N : 0;  // a row past the end has no columns
+    const int j0 = first_column<EW, K>(ln, L), step = column_step<EW>(L);
     float h[K][EW], ss = 0.0f;
+    {
+        Vec<T, EW> v[K], r[K];
+        load_row<T, EW, K>(reinterpret_cast<const T *>(a.X) + row * a.ldx, j0, step, n, v);
+        if (a.R) load_row<T, EW, K>(reinterpret_cast<const T *>(a.R) + row * a.ldr, j0, step, n, r);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int j = vec_index<K>(ln, k, L) * EW;
-        if (live && j < a.N) {
-            widen(vx[k], h[k]);
-            if (a.R) {
+        for (int k = 0; k < K; ++k) widen(v[k], h[k]);
+        if (a.R) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
                 float f[EW];
-                widen(vr[k], f);
+                widen(r[k], f);
 #pragma unroll
                 for (int e = 0; e < EW; ++e) h[k][e] += f[e];
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < EW; ++e) h[k][e] = 0.0f;
         }
+    }
+    Vec<WT, EW> w[K];
+    constexpr bool kEarly = K * EW * sizeof(WT) <= 64;  // weights asked for before the reduction: up to 16 registers
+    if constexpr (kEarly) load_weights<WT, EW, K>(a.W, j0, step, a.N, w);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < EW; ++e) ss = fmaf(h[k][e], h[k][e], ss);
-    }
-    const float s = rsqrtf(row_sum(ss, L, buf[0]) / (float)a.N + a.eps);
+    const float s = rsqrtf(fmaf(row_sum(ss, L, buf[0]), a.inv_n, a.eps));
     pdl_wait();  // loads may run ahead of the kernel before, stores may not
-    if (live && a.rstd && ln == 0) a.rstd[row] = s;
-    float top = 0.0f;
+    if (n && a.rstd && ln == 0) a.rstd[row] = s;
+    if (a.H) {
+        T *out = reinterpret_cast<T *>(a.H) + row * a.ldh;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            Vec<T, EW> o;
+            narrow(h[k], o);
+            if (j0 + k * step < n) store_vec(out + j0 + k * step, o);
+        }
+    }
+    if constexpr (!kEarly) load_weights<WT, EW, K>(a.W, j0, step, a.N, w);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int j = vec_index<K>(ln, k, L) * EW;
-        if (live && j < a.N) {
-            if (a.H) {
-                Vec<T, EW> o;
-                narrow(h[k], o);
-                store_vec(reinterpret_cast<T *>(a.H) + row * a.ldh + j, o);
-            }
-            float w[EW];
-            load_weight<T, EW>(a.W, a.wf32, j, w);
+        float f[EW];
+        widen(w[k], f);
 #pragma unroll
-            for (int e = 0; e < EW; ++e) h[k][e] = h[k][e] * s * w[e];
-            if constexpr (!E4M3) {
-                Vec<T, EW> o;
-                narrow(h[k], o);
-                store_vec(reinterpret_cast<T *>(a.Y) + row * a.ldy + j, o);
-            }
-        }
-        if constexpr (E4M3) {
-#pragma unroll
-            for (int e = 0; e < EW; ++e) top = fmaxf(top, fabsf(h[k][e]));
-        }
+        for (int e = 0; e < EW; ++e) h[k][e] = h[k][e] * s * f[e];
     }
-    if constexpr (E4M3) {
-        uint8_t *y = reinterpret_cast<uint8_t *>(a.Y) + row * a.ldy;
+    if constexpr (!E4M3) {
+        T *out = reinterpret_cast<T *>(a.Y) + row * a.ldy;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            Vec<T, EW> o;
+            narrow(h[k], o);
+            if (j0 + k * step < n) store_vec(out + j0 + k * step, o);
+        }
+    } else {
+        uint8_t *out = reinterpret_cast<uint8_t *>(a.Y) + row * a.ldy;
+        float top[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            top[k] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < EW; ++e) top[k] = fmaxf(top[k], fabsf(h[k][e]));
+        }
         if (a.group == 0) {
-            top = row_max(top, L, buf[1]);
-            const float inv = top > 0.0f ? 448.0f / top : 1.0f;
-            if (live && ln == 0) a.scales[row] = top > 0.0f ? top / 448.0f : 1.0f;
+            float t = 0.0f;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int j = vec_index<K>(ln, k, L) * EW;
-                if (live && j < a.N) {
+            for (int k = 0; k < K; ++k) t = fmaxf(t, top[k]);
+            t = row_max(t, L, buf[1]);
+            if (n && ln == 0) a.scales[row] = e4m3_scale(t);
+            const float f = e4m3_factor(t);
 #pragma unroll
-                    for (int e = 0; e < EW; ++e) h[k][e] *= inv;
-                    store_e4m3<EW>(y + j, h[k]);
-                }
-            }
+            for (int k = 0; k < K; ++k) top[k] = f;
         } else {
-            // group columns = lanes x EW (EW > 1), or 32 lanes x kk registers (EW = 1)
-            const int ng = (a.N + a.group - 1) / a.group;
-            constexpr int KK = EW > 1 ? 1 : K;
-            const int per = EW > 1 ? 1 : a.group / 32;  // consecutive k of one group
-            const int lanes = EW > 1 ? a.group / EW : 32;
-            float m[KK];
+            // a group is group / EW lanes of one k (EW > 1), or all 32 lanes of group / 32
+            // consecutive k (EW = 1)
+            const int64_t ng = (a.N + a.group - 1) >> a.group_log;
+            float *scales = a.scales + row * ng;
+            if constexpr (EW > 1) {
+                const int lanes = a.group / EW;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float t = 0.0f;
-#pragma unroll
-                for (int e = 0; e < EW; ++e) t = fmaxf(t, fabsf(h[k][e]));
-                if constexpr (EW > 1) {
-                    t = lanes_max(t, lanes);
-                    const int j = vec_index<K>(ln, k, L) * EW;
-                    if (live && j < a.N) {
-                        const float inv = t > 0.0f ? 448.0f / t : 1.0f;
-                        if ((threadIdx.x & (lanes - 1)) == 0)
-                            a.scales[row * ng + j / a.group] = t > 0.0f ? t / 448.0f : 1.0f;
-#pragma unroll
-                        for (int e = 0; e < EW; ++e) h[k][e] *= inv;
-                        store_e4m3<EW>(y + j, h[k]);
-                    }
-                } else {
-                    m[k] = lanes_max(t, 32);
+                for (int k = 0; k < K; ++k) {
+                    top[k] = lanes_max(top[k], lanes);
+                    const int j = j0 + k * step;
+                    if (j < n && (ln & (lanes - 1)) == 0) scales[j >> a.group_log] = e4m3_scale(top[k]);
+                    top[k] = e4m3_factor(top[k]);
                 }
-            }
-            if constexpr (EW == 1) {
+            } else {
+                float m[K];
+#pragma unroll
+                for (int k = 0; k < K; ++k) m[k] = lanes_max(top[k], 32);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     float t = 0.0f;
 #pragma unroll
                     for (int q = 0; q < K; ++q)
-                        if (q / per == k / per) t = fmaxf(t, m[q]);
-                    const int j = vec_index<K>(ln, k, L);
-                    if (live && j < a.N) {
-                        if (j % a.group == 0) a.scales[row * ng + j / a.group] = t > 0.0f ? t / 448.0f : 1.0f;
-                        const float v[1] = {h[k][0] * (t > 0.0f ? 448.0f / t : 1.0f)};
-                        store_e4m3<1>(y + j, v);
-                    }
+                        if (q >> (a.group_log - 5) == k >> (a.group_log - 5)) t = fmaxf(t, m[q]);
+                    const int j = j0 + k * step;
+                    if (j < n && (j & (a.group - 1)) == 0) scales[j >> a.group_log] = e4m3_scale(t);
+                    top[k] = e4m3_factor(t);
                 }
             }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int e = 0; e < EW; ++e) h[k][e] *= top[k];
+            if (j0 + k * step < n) store_e4m3<EW>(out + j0 + k * step, h[k]);
         }
     }
 }
@@ -243,91 +268,94 @@ struct NormBwdArgs {
     void *DX;
     float *part;  // [gridDim.x, N]: each block's share of dw
     int64_t lddy, ldh, lddr, lddx, M;
-    int N, L, wf32;
+    int N, L;
+    float inv_n;
 };
 
 // A block walks rows blockIdx.x, + gridDim.x, ... in each of its blockDim.x / L
-// slots, adding dy n into its own columns' dw: in registers, or for rows of
-// 1024 lanes (64 registers each) in its own words of shared memory.  At the end the slots' sums meet in shared memory and one row of
-// partials goes out; a second launch adds the blocks' rows in order.
-template <typename T, int EW, int K>
-__global__ void __launch_bounds__(kMostLanes<EW, K>) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdArgs a)
+// slots, adding dy n into its own columns' dw: in registers, or for the
+// longest rows (a lane's share would not fit) in its own words of shared memory.  Its weights
+// stay in registers.  At the end the slots' sums meet in shared memory and one row
+// of partials goes out; a second launch adds the blocks' rows in order.
+template <typename T, typename WT, int EW, int K>
+__global__ void __launch_bounds__(kGradLanes<EW, K>) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdArgs a)
 {
-    constexpr bool kRegs = kMostLanes<EW, K> == 512;
+    constexpr bool kRegs = EW == 1 ? K <= 8 : K <= 4;  // beyond, a row is the whole block's
     extern __shared__ float acc[];  // [N] floats, zeroed here
     __shared__ float buf[2][32];
     pdl_trigger();
     const int L = a.L, ln = threadIdx.x & (L - 1), slots = blockDim.x / L, slot = threadIdx.x / L;
+    const int j0 = first_column<EW, K>(ln, L), step = column_step<EW>(L);
     for (int j = threadIdx.x; j < a.N; j += blockDim.x) acc[j] = 0.0f;
     float dw[kRegs ? K : 1][EW];
 #pragma unroll
     for (int k = 0; k < (kRegs ? K : 1); ++k)
 #pragma unroll
         for (int e = 0; e < EW; ++e) dw[k][e] = 0.0f;
+    Vec<WT, EW> w[kRegs ? K : 1];
+    if constexpr (kRegs) load_weights<WT, EW, K>(a.W, j0, step, a.N, w);
     __syncthreads();
     bool wrote = false;
     int turn = 0;
     // the same number of steps for every slot: row_sum holds a barrier
     for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < a.M; r0 += (int64_t)gridDim.x * slots, turn ^= 1) {
         const int64_t row = r0 + slot;
-        const bool live = row < a.M;
-        const T *dy = reinterpret_cast<const T *>(a.DY) + row * a.lddy;
-        const T *h = reinterpret_cast<const T *>(a.H) + row * a.ldh;
-        const T *dr = reinterpret_cast<const T *>(a.DR) + row * a.lddr;
+        const int n = row < a.M ? a.N : 0;
         Vec<T, EW> vy[K], vh[K], vr[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int j = vec_index<K>(ln, k, L) * EW;
-            if (live && j < a.N) {
-                load_vec(dy + j, vy[k]);
-                load_vec(h + j, vh[k]);
-                if (a.DR) load_vec(dr + j, vr[k]);
-            }
-        }
-        const float s = live ? a.rstd[row] : 0.0f;
+        load_row<T, EW, K>(reinterpret_cast<const T *>(a.DY) + row * a.lddy, j0, step, n, vy);
+        load_row<T, EW, K>(reinterpret_cast<const T *>(a.H) + row * a.ldh, j0, step, n, vh);
+        if (a.DR) load_row<T, EW, K>(reinterpret_cast<const T *>(a.DR) + row * a.lddr, j0, step, n, vr);
+        const float s = n ? a.rstd[row] : 0.0f;
         float c = 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int j = vec_index<K>(ln, k, L) * EW;
-            if (live && j < a.N) {
-                float fy[EW], fh[EW], w[EW];
-                widen(vy[k], fy);
-                widen(vh[k], fh);
-                load_weight<T, EW>(a.W, a.wf32, j, w);
+            float fy[EW], fh[EW], fw[EW];
+            widen(vy[k], fy);
+            widen(vh[k], fh);
+            if constexpr (kRegs) {
+                widen(w[k], fw);
+            } else {
+                Vec<WT, EW> one[1];
+                load_weights<WT, EW, 1>(a.W, j0 + k * step, 0, a.N, one);
+                widen(one[0], fw);
+            }
 #pragma unroll
-                for (int e = 0; e < EW; ++e) {
-                    const float n = fh[e] * s;
-                    c = fmaf(fy[e] * w[e], n, c);
-                    if constexpr (kRegs)
-                        dw[k][e] = fmaf(fy[e], n, dw[k][e]);
-                    else
-                        acc[j + e] = fmaf(fy[e], n, acc[j + e]);  // one slot: L is the whole block
-                }
+            for (int e = 0; e < EW; ++e) {
+                const float m = fh[e] * s, p = fy[e] * m;
+                c = fmaf(p, fw[e], c);
+                if constexpr (kRegs)
+                    dw[k][e] += p;
+                else if (j0 + k * step < n)
+                    acc[j0 + k * step + e] += p;  // one slot: L is the whole block
             }
         }
-        c = row_sum(c, L, buf[turn]) / (float)a.N;
+        c = row_sum(c, L, buf[turn]) * a.inv_n * s;
         if (!wrote) pdl_wait();
         wrote = true;
+        T *out = reinterpret_cast<T *>(a.DX) + row * a.lddx;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int j = vec_index<K>(ln, k, L) * EW;
-            if (live && j < a.N) {
-                float fy[EW], fh[EW], w[EW], o[EW];
-                widen(vy[k], fy);
-                widen(vh[k], fh);
-                load_weight<T, EW>(a.W, a.wf32, j, w);
-#pragma unroll
-                for (int e = 0; e < EW; ++e) o[e] = s * (fy[e] * w[e] - fh[e] * s * c);
-                if (a.DR) {
-                    float fr[EW];
-                    widen(vr[k], fr);
-#pragma unroll
-                    for (int e = 0; e < EW; ++e) o[e] += fr[e];
-                }
-                Vec<T, EW> v;
-                narrow(o, v);
-                store_vec(reinterpret_cast<T *>(a.DX) + row * a.lddx + j, v);
+            float fy[EW], fh[EW], fw[EW], o[EW];
+            widen(vy[k], fy);
+            widen(vh[k], fh);
+            if constexpr (kRegs) {
+                widen(w[k], fw);
+            } else {
+                Vec<WT, EW> one[1];
+                load_weights<WT, EW, 1>(a.W, j0 + k * step, 0, a.N, one);
+                widen(one[0], fw);
             }
+#pragma unroll
+            for (int e = 0; e < EW; ++e) o[e] = s * fmaf(fy[e], fw[e], -(fh[e] * c));
+            if (a.DR) {
+                float fr[EW];
+                widen(vr[k], fr);
+#pragma unroll
+                for (int e = 0; e < EW; ++e) o[e] += fr[e];
+            }
+            Vec<T, EW> v;
+            narrow(o, v);
+            if (j0 + k * step < n) store_vec(out + j0 + k * step, v);
         }
     }
     if (!wrote) pdl_wait();
@@ -338,7 +366,7 @@ __global__ void __launch_bounds__(kMostLanes<EW, K>) rmsnorm_bwd_kernel(const __
             if (slot == q) {
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const int j = vec_index<K>(ln, k, L) * EW;
+                    const int j = j0 + k * step;
                     if (j < a.N) {
 #pragma unroll
                         for (int e = 0; e < EW; ++e) acc[j + e] += dw[k][e];
@@ -353,73 +381,99 @@ __global__ void __launch_bounds__(kMostLanes<EW, K>) rmsnorm_bwd_kernel(const __
     for (int j = threadIdx.x; j < a.N; j += blockDim.x) out[j] = acc[j];
 }
 
-// dw[j] = sum over the P blocks' partial rows: 32 columns x 8 lanes a block,
-// each lane every 8th row in order, then the 8 lanes in order.
-template <typename TW>
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float *__restrict__ part, TW *__restrict__ dw, int P,
-                                                         int N)
+// dw[j] = sum over the P blocks' partial rows: 16 columns x 32 lanes a block (64
+// bytes a row of partials; few columns, so that enough blocks run), each lane every
+// 32nd row in order with 8 loads in flight, then the lanes in order.
+constexpr int kDwCols = 16;
+template <typename WT>
+__global__ void __launch_bounds__(512) rmsnorm_dw_kernel(const float *__restrict__ part, WT *__restrict__ dw, int P, int N)
 {
-    __shared__ float s[8][33];
+    __shared__ float s[32][kDwCols + 1];
     pdl_trigger();
     pdl_wait();
-    const int col = threadIdx.x & 31, ln = threadIdx.x >> 5;
-    const int j = blockIdx.x * 32 + col;
+    const int col = threadIdx.x % kDwCols, ln = threadIdx.x / kDwCols;
+    const int j = blockIdx.x * kDwCols + col;
     float t = 0.0f;
     if (j < N) {
-#pragma unroll 8
-        for (int p = ln; p < P; p += 8) t += __ldcg(part + (int64_t)p * N + j);
+        int p = ln;
+        for (; p + 7 * 32 < P; p += 8 * 32) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = __ldcg(part + (int64_t)(p + 32 * u) * N + j);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) t += v[u];
+        }
+        float v[7];
+#pragma unroll
+        for (int u = 0; u < 7; ++u) v[u] = p + 32 * u < P ? __ldcg(part + (int64_t)(p + 32 * u) * N + j) : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 7; ++u) t += v[u];
     }
     s[ln][col] = t;
     __syncthreads();
     if (ln == 0 && j < N) {
 #pragma unroll
-        for (int q = 1; q < 8; ++q) t += s[q][col];
-        dw[j] = from_f<TW>(t);
+        for (int q = 1; q < 32; ++q) t += s[q][col];
+        dw[j] = from_f<WT>(t);
     }
 }
 
-// Lanes a row (L) and vectors a lane (K) for nv vectors: about `want` vectors
-// a lane, at least `least` lanes.  Up to 512 lanes of 1, 2 or 4 vectors (8
-// single elements); rows beyond that take 1024 lanes and the instance with the
-// most vectors a lane (8, or 32 single elements), whose registers are scarce.
-void pick_lanes(int64_t nv, int want, int least, bool single, int *L, int *K)
+// Lanes a row (L) and vectors of EW a lane (K) for nv vectors: about `want`
+// vectors a lane, at least `least` lanes.  Up to 512 lanes of 1, 2 or 4 vectors (8
+// single elements); rows beyond that take the instances with more vectors a lane
+// or 1024 lanes, whose registers are scarce.
+void pick_lanes(int64_t nv, int want, int least, int EW, bool grad, int *L, int *K)
 {
-    const int most = single ? 8 : 4;
+    const int most = EW == 1 ? 8 : 4;
     int l = least;
     while (l < 512 && (int64_t)l * want < nv) l *= 2;
     if ((int64_t)l * most < nv) {
-        *L = 1024;
-        *K = single ? 32 : 8;
+        *L = EW == 8 ? 512 : 1024;
+        *K = EW == 1 ? 32 : EW == 4 && !grad && nv <= 4096 ? 4 : 8;
         return;
     }
-    int k = single ? 8 : 1;
+    int k = EW == 1 ? 8 : 1;
     while ((int64_t)l * k < nv) k *= 2;
     *L = l;
     *K = k;
 }
 
-template <typename T, int EW, bool E4M3>
+template <typename T, typename WT, int EW, bool E4M3>
 const void *norm_kernel(int K)
 {
-    if constexpr (EW == 1) return K <= 8 ? (const void *)rmsnorm_kernel<T, 1, 8, E4M3> : (const void *)rmsnorm_kernel<T, 1, 32, E4M3>;
-    switch (K) {
-    case 1: return (const void *)rmsnorm_kernel<T, EW, 1, E4M3>;
-    case 2: return (const void *)rmsnorm_kernel<T, EW, 2, E4M3>;
-    case 4: return (const void *)rmsnorm_kernel<T, EW, 4, E4M3>;
-    default: return (const void *)rmsnorm_kernel<T, EW, 8, E4M3>;
-    }
+    if constexpr (EW == 1)
+        return K <= 8 ? (const void *)rmsnorm_kernel<T, WT, 1, 8, E4M3> : (const void *)rmsnorm_kernel<T, WT, 1, 32, E4M3>;
+    else
+        return K == 1   ? (const void *)rmsnorm_kernel<T, WT, EW, 1, E4M3>
+               : K == 2 ? (const void *)rmsnorm_kernel<T, WT, EW, 2, E4M3>
+               : K == 4 ? (const void *)rmsnorm_kernel<T, WT, EW, 4, E4M3>
+                        : (const void *)rmsnorm_kernel<T, WT, EW, 8, E4M3>;
 }
 
-template <typename T, int EW>
+template <typename T, typename WT, int EW>
 const void *norm_bwd_kernel(int K)
 {
-    if constexpr (EW == 1) return K <= 8 ? (const void *)rmsnorm_bwd_kernel<T, 1, 8> : (const void *)rmsnorm_bwd_kernel<T, 1, 32>;
-    switch (K) {
-    case 1: return (const void *)rmsnorm_bwd_kernel<T, EW, 1>;
-    case 2: return (const void *)rmsnorm_bwd_kernel<T, EW, 2>;
-    case 4: return (const void *)rmsnorm_bwd_kernel<T, EW, 4>;
-    default: return (const void *)rmsnorm_bwd_kernel<T, EW, 8>;
-    }
+    if constexpr (EW == 1)
+        return K <= 8 ? (const void *)rmsnorm_bwd_kernel<T, WT, 1, 8> : (const void *)rmsnorm_bwd_kernel<T, WT, 1, 32>;
+    else
+        return K == 1   ? (const void *)rmsnorm_bwd_kernel<T, WT, EW, 1>
+               : K == 2 ? (const void *)rmsnorm_bwd_kernel<T, WT, EW, 2>
+               : K == 4 ? (const void *)rmsnorm_bwd_kernel<T, WT, EW, 4>
+                        : (const void *)rmsnorm_bwd_kernel<T, WT, EW, 8>;
+}
+
+template <typename T, typename WT>
+const void *norm_pick(bool vec, bool e4, int K)
+{
+    constexpr int EW = 16 / sizeof(T);
+    if (vec) return e4 ? norm_kernel<T, WT, EW, true>(K) : norm_kernel<T, WT, EW, false>(K);
+    return e4 ? norm_kernel<T, WT, 1, true>(K) : norm_kernel<T, WT, 1, false>(K);
+}
+
+template <typename T, typename WT>
+const void *norm_bwd_pick(bool vec, int K)
+{
+    return vec ? norm_bwd_kernel<T, WT, 16 / sizeof(T)>(K) : norm_bwd_kernel<T, WT, 1>(K);
 }
 
 constexpr int64_t kBwdBlocks = 608;  // dw partial rows at most: 152 SMs x 4 blocks
@@ -433,7 +487,7 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int EW)
 {
     BwdPlan p;
     const int64_t nv = (N + EW - 1) / EW;
-    pick_lanes(nv, EW == 1 ? 8 : 16 / EW, EW == 1 ? 32 : 8, EW == 1, &p.L, &p.K);
+    pick_lanes(nv, EW == 1 ? 8 : 16 / EW, EW == 1 ? 32 : 8, EW, true, &p.L, &p.K);
     p.threads = p.L < 256 ? 256 : p.L;
     const int64_t per = p.threads / p.L;
     p.blocks = (M + per - 1) / per;
@@ -490,16 +544,16 @@ extern "C" tm_status tm_rmsnorm(const void *X, int64_t ldx, const void *R, int64
     const int EWv = 16 / e;
     const bool vec = N % EWv == 0 && ldx % EWv == 0 && aligned_to(X, 16) &&
                      (!R || (ldr % EWv == 0 && aligned_to(R, 16))) && (!H || (ldh % EWv == 0 && aligned_to(H, 16))) &&
-                     ldy % EWv == 0 && aligned_to(Y, e4 ? EWv : 16) && (!W || wtype == TM_F32 || aligned_to(W, 16));
+                     ldy % EWv == 0 && aligned_to(Y, e4 ? EWv : 16) && (!W || aligned_to(W, 16));
     const int EW = vec ? EWv : 1;
     const int64_t nv = (N + EW - 1) / EW;
     int L, K;
     if (vec) {
         // few rows: one vector a lane, the shortest chain; many: four, so that
         // each lane has that many loads in flight
-        pick_lanes(nv, M <= 304 ? 1 : 4, group ? 32 : 8, false, &L, &K);
+        pick_lanes(nv, M <= 304 ? 1 : 4, group ? 32 : 8, EW, false, &L, &K);
     } else {
-        pick_lanes(nv, 8, 32, true, &L, &K);
+        pick_lanes(nv, 8, 32, 1, false, &L, &K);
     }
     const int threads = L < 128 ? 128 : L;
     const int64_t rows = threads / L, blocks = (M + rows - 1) / rows;
@@ -507,19 +561,14 @@ extern "C" tm_status tm_rmsnorm(const void *X, int64_t ldx, const void *R, int64
     const DevInfo *dev;
     tm_status st = device_info(&dev);
     if (st != TM_OK) return st;
-    NormArgs a = {X, R, W, H, Y, scales, rstd, ldx, ldr, ldh, ldy, M, (int)N, L, group, wtype == TM_F32, eps};
-    const void *k = nullptr;
-#define PICK(T, EV)                                                                             \
-    k = vec ? (e4 ? norm_kernel<T, EV, true>(K) : norm_kernel<T, EV, false>(K))                 \
-            : (e4 ? norm_kernel<T, 1, true>(K) : norm_kernel<T, 1, false>(K))
-    if (xtype == TM_F32) {
-        PICK(float, 4);
-    } else if (xtype == TM_F16) {
-        PICK(__half, 8);
-    } else {
-        PICK(__nv_bfloat16, 8);
-    }
-#undef PICK
+    NormArgs a = {X, R, W, H, Y, scales, rstd, ldx, ldr, ldh, ldy, M, (int)N, L, group,
+                  group == 32 ? 5 : group == 64 ? 6 : 7, eps, 1.0f / (float)N};
+    const bool wf = wtype == TM_F32;
+    const void *k = xtype == TM_F32 ? norm_pick<float, float>(vec, e4, K)
+                    : xtype == TM_F16
+                        ? (wf ? norm_pick<__half, float>(vec, e4, K) : norm_pick<__half, __half>(vec, e4, K))
+                        : (wf ? norm_pick<__nv_bfloat16, float>(vec, e4, K)
+                              : norm_pick<__nv_bfloat16, __nv_bfloat16>(vec, e4, K));
     void *args[] = {&a};
     return launch_kernel(k, dim3((unsigned)blocks), dim3(threads), args, 0, as_stream(stream), (flags & TM_PDL) != 0);
 }
@@ -565,7 +614,7 @@ extern "C" tm_status tm_rmsnorm_bwd(const void *DY, int64_t lddy, const void *H,
     const int EWv = 16 / e;
     const bool vec = N % EWv == 0 && lddy % EWv == 0 && aligned_to(DY, 16) && ldh % EWv == 0 && aligned_to(H, 16) &&
                      lddx % EWv == 0 && aligned_to(DX, 16) && (!DR || (lddr % EWv == 0 && aligned_to(DR, 16))) &&
-                     (!W || wtype == TM_F32 || aligned_to(W, 16));
+                     (!W || aligned_to(W, 16));
     const BwdPlan p = bwd_plan(M, N, vec ? EWv : 1);
     const DevInfo *dev;
     tm_status st = device_info(&dev);
@@ -573,11 +622,13 @@ extern "C" tm_status tm_rmsnorm_bwd(const void *DY, int64_t lddy, const void *H,
     cudaStream_t s = as_stream(stream);
     if (M > 0) {
         NormBwdArgs a = {DY, H, W, DR, rstd, DX, DW ? reinterpret_cast<float *>(workspace) : nullptr,
-                         lddy, ldh, lddr, lddx, M, (int)N, p.L, wtype == TM_F32};
-        const void *k = xtype == TM_F32   ? (vec ? norm_bwd_kernel<float, 4>(p.K) : norm_bwd_kernel<float, 1>(p.K))
-                        : xtype == TM_F16 ? (vec ? norm_bwd_kernel<__half, 8>(p.K) : norm_bwd_kernel<__half, 1>(p.K))
-                                          : (vec ? norm_bwd_kernel<__nv_bfloat16, 8>(p.K)
-                                                 : norm_bwd_kernel<__nv_bfloat16, 1>(p.K));
+                         lddy, ldh, lddr, lddx, M, (int)N, p.L, 1.0f / (float)N};
+        const bool wf = wtype == TM_F32;
+        const void *k = xtype == TM_F32 ? norm_bwd_pick<float, float>(vec, p.K)
+                        : xtype == TM_F16
+                            ? (wf ? norm_bwd_pick<__half, float>(vec, p.K) : norm_bwd_pick<__half, __half>(vec, p.K))
+                            : (wf ? norm_bwd_pick<__nv_bfloat16, float>(vec, p.K)
+                                  : norm_bwd_pick<__nv_bfloat16, __nv_bfloat16>(vec, p.K));
         const size_t smem = (size_t)N * sizeof(float);
         if (smem > 40 * 1024 &&
             cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
@@ -595,7 +646,7 @@ extern "C" tm_status tm_rmsnorm_bwd(const void *DY, int64_t lddy, const void *H,
         const void *k = wtype == TM_F32   ? (const void *)rmsnorm_dw_kernel<float>
                         : wtype == TM_F16 ? (const void *)rmsnorm_dw_kernel<__half>
                                           : (const void *)rmsnorm_dw_kernel<__nv_bfloat16>;
-        return launch_dependent(k, dim3((unsigned)((N + 31) / 32)), dim3(256), args, 0, s);
+        return launch_dependent(k, dim3((unsigned)((N + kDwCols - 1) / kDwCols)), dim3(512), args, 0, s);
     }
     return TM_OK;
 }

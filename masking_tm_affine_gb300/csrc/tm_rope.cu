@@ -3,11 +3,13 @@
 //   (a, b) -> gain (a cos t - b sin t, a sin t + b cos t),  t = pos * f_i
 //
 // Bound by HBM: each element is read and written once, against three flops.
-// What could cost more is the sine and cosine (about 40 instructions a pair),
-// so a block takes a run of tokens, computes each token's rot/2 pairs once
-// into shared memory and then walks the tokens' heads with them: with 40 heads
-// of 128 that is half an instruction an element.  A lane moves two vectors of
-// P elements, the two halves of P pairs.
+// What could cost more is the sine and cosine (about 40 instructions a pair), so a
+// warp takes a token and a run of its heads, computes the token's rot/2 pairs once
+// (two or so a lane, exchanged through shared memory) and keeps the P pairs of its
+// own place in registers over the heads.  A lane moves two vectors of P elements,
+// the two halves of P pairs; rot/2P lanes take a head, as many heads as fit a warp
+// at a time.  (Tables read from shared memory for each head instead cost a four-way
+// bank conflict a read: 40 heads of 128, 8192 tokens, 30.9 against ROPEUS us.)
 #include <cmath>
 
 #include "tm_host.h"
@@ -17,6 +19,8 @@
 namespace libtm {
 namespace {
 
+constexpr int kRopeWarps = 4;
+
 struct RopeArgs {
     const void *X;
     void *Y;
@@ -24,62 +28,87 @@ struct RopeArgs {
     const int64_t *pos;
     const uint64_t *turns;
     int64_t T;
-    int H, D, rot, tokens;  // tokens per block
+    int H, D, rot, split, rest;  // rest: whether dims from rot on are copied
     float gain, sign;
-    FastDiv by_items, by_groups;  // items of a token; pair groups of a head
 };
 
-// Items of a token: H heads x (rot / 2P rotated groups + (D - rot) / P copied
-// vectors).  blockIdx.x walks token runs, blockIdx.y splits the items of a run
-// (few tokens, many heads).
+// One warp a task: token task / split, heads [part, part + 1) / split.
 template <typename T, int P, bool INTER>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a)
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeArgs a)
 {
-    extern __shared__ float2 cs[];  // [tokens][rot / 2]
+    constexpr int kChunk = 32 * P;  // pairs a warp holds at a time
+    __shared__ float2 table[kRopeWarps][kChunk];
     pdl_trigger();
-    const int half = a.rot / 2;
-    const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
-    const int n = (int)(a.T - t0 < a.tokens ? a.T - t0 : a.tokens);
-    for (int i = threadIdx.x; i < n * half; i += blockDim.x) {
-        const int t = i / half, q = i - t * half;
-        cs[i] = pair_rotation(a.pos[t0 + t], a.turns[q], a.gain, a.sign);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t task = (int64_t)blockIdx.x * kRopeWarps + warp;
+    if (task >= a.T * a.split) {
+        pdl_wait();
+        return;
     }
-    __syncthreads();
-    const int groups = half / P, per_head = groups + (a.D - a.rot) / P, items = a.H * per_head;
+    const int64_t t = task / a.split;
+    const int part = (int)(task - t * a.split);
+    const int h0 = (int)((int64_t)a.H * part / a.split), h1 = (int)((int64_t)a.H * (part + 1) / a.split);
+    const T *x = reinterpret_cast<const T *>(a.X) + t * a.xs_tok;
+    T *y = reinterpret_cast<T *>(a.Y) + t * a.ys_tok;
+    const int half = a.rot / 2, groups = half / P;
+    const int64_t pos = half ? a.pos[t] : 0;
     bool waited = false;
-    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < n * items; i += gridDim.y * blockDim.x) {
-        const int t = (int)fdiv((uint32_t)i, a.by_items), it = i - t * items;
-        const int h = (int)fdiv((uint32_t)it, a.by_groups), g = it - h * per_head;
-        const T *x = reinterpret_cast<const T *>(a.X) + (t0 + t) * a.xs_tok + h * a.xs_head;
-        T *y = reinterpret_cast<T *>(a.Y) + (t0 + t) * a.ys_tok + h * a.ys_head;
-        if (g < groups) {
-            const int o0 = INTER ? 2 * P * g : P * g, o1 = INTER ? o0 + P : o0 + half;
-            Vec<T, P> va, vb;
-            load_vec(x + o0, va);
-            load_vec(x + o1, vb);
-            float lo[P], hi[P];
-            float2 r[P];
+    for (int g0 = 0; g0 < groups; g0 += 32) {  // one round unless P is small and the head long
+        const int gn = min(32, groups - g0), per = 32 / gn;  // lanes a head, heads at a time
+        const int hl = lane / gn, gl = lane - hl * gn;
+        const bool in = hl < per;
+        const int i = P * (g0 + gl);  // this lane's first pair
+        const int o0 = INTER ? 2 * i : i, o1 = INTER ? o0 + P : o0 + half;
+        // the first heads' loads go out before the sines
+        constexpr int U = 4;
+        Vec<T, P> va[U], vb[U];
+        auto fetch = [&](int h) {
 #pragma unroll
-            for (int q = 0; q < P; ++q) r[q] = cs[t * half + P * g + q];
-            widen(va, lo);
-            widen(vb, hi);
-            rotate_pairs<P, INTER>(lo, hi, r);
-            narrow(lo, va);
-            narrow(hi, vb);
-            if (!waited) pdl_wait();
-            waited = true;
-            store_vec(y + o0, va);
-            store_vec(y + o1, vb);
-        } else {
-            const int o = a.rot + P * (g - groups);
-            Vec<T, P> v;
-            load_vec(x + o, v);
-            if (!waited) pdl_wait();
-            waited = true;
-            store_vec(y + o, v);
+            for (int u = 0; u < U; ++u) {
+                const int hh = h + u * per + hl;
+                if (in && hh < h1) {
+                    load_vec(x + hh * a.xs_head + o0, va[u]);
+                    load_vec(x + hh * a.xs_head + o1, vb[u]);
+                }
+            }
+        };
+        fetch(h0);
+        __syncwarp();
+        for (int q = lane; q < gn * P; q += 32) table[warp][q] = pair_rotation(pos, a.turns[P * g0 + q], a.gain, a.sign);
+        __syncwarp();
+        float2 cs[P];
+#pragma unroll
+        for (int q = 0; q < P; ++q) cs[q] = table[warp][P * gl + q];
+        if (!waited) pdl_wait();
+        waited = true;
+        for (int h = h0; h < h1; h += U * per) {
+            if (h > h0) fetch(h);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int hh = h + u * per + hl;
+                if (in && hh < h1) {
+                    float lo[P], hi[P];
+                    widen(va[u], lo);
+                    widen(vb[u], hi);
+                    rotate_pairs<P, INTER>(lo, hi, cs);
+                    narrow(lo, va[u]);
+                    narrow(hi, vb[u]);
+                    store_vec(y + hh * a.ys_head + o0, va[u]);
+                    store_vec(y + hh * a.ys_head + o1, vb[u]);
+                }
+            }
         }
     }
     if (!waited) pdl_wait();
+    if (a.rest) {
+        const int per = (a.D - a.rot) / P;
+        for (int i = lane; i < (h1 - h0) * per; i += 32) {
+            const int h = i / per, o = a.rot + P * (i - h * per);
+            Vec<T, P> v;
+            load_vec(x + (h0 + h) * a.xs_head + o, v);
+            store_vec(y + (h0 + h) * a.ys_head + o, v);
+        }
+    }
 }
 
 template <typename T, int P>
@@ -166,28 +195,21 @@ extern "C" tm_status tm_rope(const void *X, int64_t xs_tok, int64_t xs_head, voi
                           ys_head % p == 0);
     };
     while (!fits(P)) P /= 2;
-    const int per_head = rot / 2 / P + (D - rot) / P;
-    const int64_t items = (int64_t)H * per_head;
-    if (items > (1 << 24)) return TM_ERR_INVALID_ARG;
     const DevInfo *dev;
     tm_status st = device_info(&dev);
     if (st != TM_OK) return st;
-    // Tokens per block: enough items for several rounds of the block, while
-    // every SM keeps some blocks; few tokens split their items over blocks.
-    int tokens = 1;
-    while (tokens < 16 && tokens * rot <= 4096 && tokens * items < 2048 && T / (2 * tokens) >= 4LL * dev->sms) tokens *= 2;
-    const int64_t blocks = (T + tokens - 1) / tokens;
-    if (blocks > INT32_MAX) return TM_ERR_INVALID_ARG;
-    int64_t split = 1;
-    while (split < 64 && blocks * split < 2LL * dev->sms && split * 256 < tokens * items) split *= 2;
-    RopeArgs a = {X, Y, xs_tok, xs_head, ys_tok, ys_head, pos, turns, T, H, D, rot, tokens, gain,
-                  (flags & TM_ROPE_INVERSE) ? -1.0f : 1.0f, make_fastdiv((uint32_t)items),
-                  make_fastdiv((uint32_t)per_head)};
+    // Tasks: about two rounds of the warps the GPU holds, each of some heads.
+    int64_t split = (64LL * dev->sms + T - 1) / T;
+    if (split > H) split = H;
+    if (T > (int64_t)INT32_MAX * kRopeWarps / split) return TM_ERR_INVALID_ARG;
+    const int64_t blocks = (T * split + kRopeWarps - 1) / kRopeWarps;
+    RopeArgs a = {X, Y, xs_tok, xs_head, ys_tok, ys_head, pos, turns, T, H, D, rot, (int)split, X != Y && rot < D, gain,
+                  (flags & TM_ROPE_INVERSE) ? -1.0f : 1.0f};
     const bool inter = (flags & TM_ROPE_INTERLEAVED) != 0;
     const void *k = xtype == TM_F32   ? rope_width<float>(P, inter)
                     : xtype == TM_F16 ? rope_width<__half>(P, inter)
                                       : rope_width<__nv_bfloat16>(P, inter);
     void *args[] = {&a};
-    return launch_kernel(k, dim3((unsigned)blocks, (unsigned)split), dim3(256), args,
-                         (size_t)tokens * (rot / 2) * sizeof(float2), as_stream(stream), (flags & TM_PDL) != 0);
+    return launch_kernel(k, dim3((unsigned)blocks), dim3(kRopeWarps * 32), args, 0, as_stream(stream),
+                         (flags & TM_PDL) != 0);
 }

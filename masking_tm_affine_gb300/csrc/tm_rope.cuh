@@ -4,7 +4,8 @@
 // p * turns_i in wrapping 64-bit integers is the exact fraction of a turn at
 // position p (for |p| up to 2^63; the only error is turns_i's own rounding,
 // p * 2^-65 turns).  Read as a signed number it is the angle in units of
-// 2^-63 * pi within [-pi, pi), one rounding away from sincospif's argument.
+// 2^-63 * pi within [-pi, pi), and its upper half in units of 2^-31 * pi one
+// rounding away from sincospif's argument.
 // fp32 angles formed as p * f_i would be off by 0.03 radians at p = 2^20.
 #pragma once
 
@@ -21,7 +22,8 @@ __device__ __forceinline__ int64_t turn_fraction(int64_t pos, uint64_t turns)
 __device__ __forceinline__ float2 pair_rotation(int64_t pos, uint64_t turns, float gain, float sign)
 {
     float s, c;
-    sincospif((float)turn_fraction(pos, turns) * 0x1p-63f, &s, &c);
+    // the upper 32 bits are enough (2^-32 of a turn) and convert at full rate, 64 bits do not
+    sincospif((float)(int32_t)(turn_fraction(pos, turns) >> 32) * 0x1p-31f, &s, &c);
     return make_float2(c * gain, s * gain * sign);
 }
 
