@@ -33,49 +33,86 @@ struct alignas(W * sizeof(T) > 16 ? 16 : W * sizeof(T)) Vec {
     T v[W];
 };
 
-// Read-only data, each byte read once: past L1.
+// Read-only data, each byte read once: past L1.  Zeros where `ok` is false: a
+// predicate on the access itself, no branch around it (a warp's branches and the
+// moves that join their two sides cost the norms more than their arithmetic).
 template <typename T, int W>
-__device__ __forceinline__ void load_vec(const T *p, Vec<T, W> &r)
+__device__ __forceinline__ void load_vec_if(const T *p, bool ok, Vec<T, W> &r)
 {
     constexpr int B = W * sizeof(T);
     uint32_t *u = reinterpret_cast<uint32_t *>(&r);
     if constexpr (B % 16 == 0) {
 #pragma unroll
         for (int q = 0; q < B / 16; ++q)
-            asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(u[4 * q]), "=r"(u[4 * q + 1]), "=r"(u[4 * q + 2]), "=r"(u[4 * q + 3])
-                         : "l"(reinterpret_cast<const char *>(p) + 16 * q));
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                "@p ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n\t}"
+                : "=&r"(u[4 * q]), "=&r"(u[4 * q + 1]), "=&r"(u[4 * q + 2]), "=&r"(u[4 * q + 3])
+                : "l"(reinterpret_cast<const char *>(p) + 16 * q), "r"((uint32_t)ok));
     } else if constexpr (B == 8) {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "l"(p));
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+            "@p ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];\n\t}"
+            : "=&r"(u[0]), "=&r"(u[1])
+            : "l"(p), "r"((uint32_t)ok));
     } else if constexpr (B == 4) {
-        asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(u[0]) : "l"(p));
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+            "@p ld.global.nc.L1::no_allocate.b32 %0, [%1];\n\t}"
+            : "=&r"(u[0])
+            : "l"(p), "r"((uint32_t)ok));
     } else {
         static_assert(B == 2, "access width");
         uint16_t h;
-        asm volatile("ld.global.nc.L1::no_allocate.b16 %0, [%1];" : "=h"(h) : "l"(p));
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t"
+            "@p ld.global.nc.L1::no_allocate.b16 %0, [%1];\n\t}"
+            : "=&h"(h)
+            : "l"(p), "r"((uint32_t)ok));
         *reinterpret_cast<uint16_t *>(&r) = h;
     }
 }
 
 template <typename T, int W>
-__device__ __forceinline__ void store_vec(T *p, const Vec<T, W> &r)
+__device__ __forceinline__ void load_vec(const T *p, Vec<T, W> &r)
+{
+    load_vec_if(p, true, r);
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_vec_if(T *p, bool ok, const Vec<T, W> &r)
 {
     constexpr int B = W * sizeof(T);
     const uint32_t *u = reinterpret_cast<const uint32_t *>(&r);
     if constexpr (B % 16 == 0) {
 #pragma unroll
         for (int q = 0; q < B / 16; ++q)
-            asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(reinterpret_cast<char *>(p) + 16 * q),
-                         "r"(u[4 * q]), "r"(u[4 * q + 1]), "r"(u[4 * q + 2]), "r"(u[4 * q + 3])
-                         : "memory");
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1,%2,%3,%4};\n\t}" ::"l"(
+                    reinterpret_cast<char *>(p) + 16 * q),
+                "r"(u[4 * q]), "r"(u[4 * q + 1]), "r"(u[4 * q + 2]), "r"(u[4 * q + 3]), "r"((uint32_t)ok)
+                : "memory");
     } else if constexpr (B == 8) {
-        asm volatile("st.global.v2.b32 [%0], {%1,%2};" ::"l"(p), "r"(u[0]), "r"(u[1]) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p st.global.v2.b32 [%0], {%1,%2};\n\t}" ::"l"(p),
+                     "r"(u[0]), "r"(u[1]), "r"((uint32_t)ok)
+                     : "memory");
     } else if constexpr (B == 4) {
-        asm volatile("st.global.b32 [%0], %1;" ::"l"(p), "r"(u[0]) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(p),
+                     "r"(u[0]), "r"((uint32_t)ok)
+                     : "memory");
     } else {
         static_assert(B == 2, "access width");
-        asm volatile("st.global.b16 [%0], %1;" ::"l"(p), "h"(*reinterpret_cast<const uint16_t *>(&r)) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(p),
+                     "h"(*reinterpret_cast<const uint16_t *>(&r)), "r"((uint32_t)ok)
+                     : "memory");
     }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_vec(T *p, const Vec<T, W> &r)
+{
+    store_vec_if(p, true, r);
 }
 
 template <typename T, int W>

@@ -210,8 +210,8 @@ __device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool rota
 
 constexpr int kAppendWarps = 4;
 
-// One warp a task: token task / split, heads [part, part + 1) / split of its
-// passes of 512 / D heads.
+// One warp a task: a token (blockIdx.x) and one of the `split` parts (blockIdx.y) of
+// its passes of 512 / D heads.
 template <typename T, int D, bool VEC, bool INTER>
 __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const __grid_constant__ AppendArgs a)
 {
@@ -219,13 +219,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
     __shared__ float2 table[kAppendWarps][D / 2];
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ln = lane % LANES;
-    const int64_t task = (int64_t)blockIdx.x * kAppendWarps + warp;
-    if (task >= a.T * a.split) {
+    const int64_t t = (int64_t)blockIdx.x * kAppendWarps + warp;
+    const int part = blockIdx.y;
+    if (t >= a.T) {
         pdl_wait();
         return;
     }
-    const int64_t t = task / a.split;
-    const int part = (int)(task - t * a.split);
     // passes over the query heads, then the key heads, then the value heads
     const int nq = (a.Hq + PER - 1) / PER, nk = (a.Hkv + PER - 1) / PER, passes = nq + 2 * nk;
     const int pass0 = passes * part / a.split, pass1 = passes * (part + 1) / a.split;
@@ -260,12 +259,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
         const int h0 = p0 * PER + lane / LANES;
         const T *p = base + t * tok + h0 * head;
         Vec<T, 8> n0, n1;
-        auto fetch = [&](int h) {
-            if (h >= H) return;
+        auto fetch = [&](bool ok) {
             if constexpr (VEC) {
-                load_vec(p + o0, n0);
-                load_vec(p + o1, n1);
-            } else {
+                load_vec_if(p + o0, ok, n0);
+                load_vec_if(p + o1, ok, n1);
+            } else if (ok) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     n0.v[e] = p[o0 + e];
@@ -273,13 +271,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
                 }
             }
         };
-        fetch(h0);
+        fetch(h0 < H);
         for (int h = h0, i = p0; i < p1; ++i, h += PER) {
             float x[2][8];
             widen(n0, x[0]);
             widen(n1, x[1]);
             p += PER * head;
-            if (i + 1 < p1) fetch(h + PER);
+            fetch(i + 1 < p1 && h + PER < H);
             if (h < H) work(h, x);  // whole groups of lanes
         }
     };
@@ -520,14 +518,14 @@ extern "C" tm_status tm_kv4_append(const void *Q, int64_t qs_tok, int64_t qs_hea
     AppendArgs a = {Q, K, V, QO, qs_tok, qs_head, qos_tok, qos_head, ks_tok, ks_head, vs_tok, vs_head, pos, slots, turns,
                     reinterpret_cast<uint8_t *>(pool), pages * page, pb, T, page, Hq, Hkv, rot, (int)split, gain,
                     dev->status};
-    const int64_t blocks = (T * split + kAppendWarps - 1) / kAppendWarps;
-    if (blocks > INT32_MAX) return TM_ERR_INVALID_ARG;
+    const int64_t blocks = (T + kAppendWarps - 1) / kAppendWarps;
+    if (split > 65535) return TM_ERR_INVALID_ARG;
     const bool inter = (flags & TM_ROPE_INTERLEAVED) != 0;
     const void *kern = xtype == TM_F32   ? append_kernel<float>(D, vec, inter)
                        : xtype == TM_F16 ? append_kernel<__half>(D, vec, inter)
                                          : append_kernel<__nv_bfloat16>(D, vec, inter);
     void *args[] = {&a};
-    return launch_kernel(kern, dim3((unsigned)blocks), dim3(kAppendWarps * 32), args, 0, as_stream(stream),
+    return launch_kernel(kern, dim3((unsigned)blocks, (unsigned)split), dim3(kAppendWarps * 32), args, 0, as_stream(stream),
                          (flags & TM_PDL) != 0);
 }
 

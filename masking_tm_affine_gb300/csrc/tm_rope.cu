@@ -28,11 +28,11 @@ struct RopeArgs {
     const int64_t *pos;
     const uint64_t *turns;
     int64_t T;
-    int H, D, rot, split, rest;  // rest: whether dims from rot on are copied
+    int H, D, rot, heads, rest;  // heads of a task; whether dims from rot on are copied
     float gain, sign;
 };
 
-// One warp a task: token task / split, heads [part, part + 1) / split.
+// One warp a task: a token (blockIdx.x) and `heads` of its heads (blockIdx.y).
 template <typename T, int P, bool INTER>
 __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeArgs a)
 {
@@ -40,14 +40,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
     __shared__ float2 table[kRopeWarps][kChunk];
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t task = (int64_t)blockIdx.x * kRopeWarps + warp;
-    if (task >= a.T * a.split) {
+    const int64_t t = (int64_t)blockIdx.x * kRopeWarps + warp;
+    if (t >= a.T) {
         pdl_wait();
         return;
     }
-    const int64_t t = task / a.split;
-    const int part = (int)(task - t * a.split);
-    const int h0 = (int)((int64_t)a.H * part / a.split), h1 = (int)((int64_t)a.H * (part + 1) / a.split);
+    const int h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.H);
     const T *x = reinterpret_cast<const T *>(a.X) + t * a.xs_tok;
     T *y = reinterpret_cast<T *>(a.Y) + t * a.ys_tok;
     const int half = a.rot / 2, groups = half / P;
@@ -60,42 +58,52 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
         const int i = P * (g0 + gl);  // this lane's first pair
         const int o0 = INTER ? 2 * i : i, o1 = INTER ? o0 + P : o0 + half;
         // the first heads' loads go out before the sines
-        constexpr int U = 4;
-        Vec<T, P> va[U], vb[U];
-        auto fetch = [&](int h) {
+        constexpr int U = 2;  // heads a lane works on at a time, and has in flight behind them
+        Vec<T, P> va[2][U], vb[2][U];
+        float2 cs[P];
+        const int64_t xs = per * a.xs_head, ys = per * a.ys_head;
+        const T *xp = x + (h0 + hl) * a.xs_head + o0;
+        T *yp = y + (h0 + hl) * a.ys_head + o0;
+        int left = in ? h1 - h0 - hl : 0;  // heads from this lane's next on
+        auto fetch = [&](int left, Vec<T, P> (&fa)[U], Vec<T, P> (&fb)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int hh = h + u * per + hl;
-                if (in && hh < h1) {
-                    load_vec(x + hh * a.xs_head + o0, va[u]);
-                    load_vec(x + hh * a.xs_head + o1, vb[u]);
-                }
+                load_vec_if(xp, u * per < left, fa[u]);
+                load_vec_if(xp + (o1 - o0), u * per < left, fb[u]);
+                xp += xs;
             }
         };
-        fetch(h0);
+        auto turn = [&](const Vec<T, P> (&fa)[U], const Vec<T, P> (&fb)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float lo[P], hi[P];
+                widen(fa[u], lo);
+                widen(fb[u], hi);
+                rotate_pairs<P, INTER>(lo, hi, cs);
+                Vec<T, P> o;
+                narrow(lo, o);
+                store_vec_if(yp, u * per < left, o);
+                narrow(hi, o);
+                store_vec_if(yp + (o1 - o0), u * per < left, o);
+                yp += ys;
+            }
+            left -= U * per;
+        };
+        fetch(left, va[0], vb[0]);
         __syncwarp();
         for (int q = lane; q < gn * P; q += 32) table[warp][q] = pair_rotation(pos, a.turns[P * g0 + q], a.gain, a.sign);
         __syncwarp();
-        float2 cs[P];
 #pragma unroll
         for (int q = 0; q < P; ++q) cs[q] = table[warp][P * gl + q];
         if (!waited) pdl_wait();
         waited = true;
-        for (int h = h0; h < h1; h += U * per) {
-            if (h > h0) fetch(h);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int hh = h + u * per + hl;
-                if (in && hh < h1) {
-                    float lo[P], hi[P];
-                    widen(va[u], lo);
-                    widen(vb[u], hi);
-                    rotate_pairs<P, INTER>(lo, hi, cs);
-                    narrow(lo, va[u]);
-                    narrow(hi, vb[u]);
-                    store_vec(y + hh * a.ys_head + o0, va[u]);
-                    store_vec(y + hh * a.ys_head + o1, vb[u]);
-                }
+        const int rounds = (h1 - h0 + U * per - 1) / (U * per);
+        for (int i = 0; i < rounds; i += 2) {
+            fetch(i + 1 < rounds ? left - U * per : 0, va[1], vb[1]);
+            turn(va[0], vb[0]);
+            if (i + 1 < rounds) {
+                fetch(i + 2 < rounds ? left - U * per : 0, va[0], vb[0]);
+                turn(va[1], vb[1]);
             }
         }
     }
@@ -198,18 +206,20 @@ extern "C" tm_status tm_rope(const void *X, int64_t xs_tok, int64_t xs_head, voi
     const DevInfo *dev;
     tm_status st = device_info(&dev);
     if (st != TM_OK) return st;
-    // Tasks: about two rounds of the warps the GPU holds, each of some heads.
-    int64_t split = (64LL * dev->sms + T - 1) / T;
+    // Tasks: at least about two rounds of the warps the GPU holds, each of some heads.
+    int64_t split = (48LL * dev->sms + T - 1) / T;
     if (split > H) split = H;
-    if (T > (int64_t)INT32_MAX * kRopeWarps / split) return TM_ERR_INVALID_ARG;
-    const int64_t blocks = (T * split + kRopeWarps - 1) / kRopeWarps;
-    RopeArgs a = {X, Y, xs_tok, xs_head, ys_tok, ys_head, pos, turns, T, H, D, rot, (int)split, X != Y && rot < D, gain,
+    const int heads = (int)((H + split - 1) / split);
+    split = (H + heads - 1) / heads;
+    const int64_t blocks = (T + kRopeWarps - 1) / kRopeWarps;
+    if (blocks > INT32_MAX || split > 65535) return TM_ERR_INVALID_ARG;
+    RopeArgs a = {X, Y, xs_tok, xs_head, ys_tok, ys_head, pos, turns, T, H, D, rot, heads, X != Y && rot < D, gain,
                   (flags & TM_ROPE_INVERSE) ? -1.0f : 1.0f};
     const bool inter = (flags & TM_ROPE_INTERLEAVED) != 0;
     const void *k = xtype == TM_F32   ? rope_width<float>(P, inter)
                     : xtype == TM_F16 ? rope_width<__half>(P, inter)
                                       : rope_width<__nv_bfloat16>(P, inter);
     void *args[] = {&a};
-    return launch_kernel(k, dim3((unsigned)blocks), dim3(kRopeWarps * 32), args, 0, as_stream(stream),
+    return launch_kernel(k, dim3((unsigned)blocks, (unsigned)split), dim3(kRopeWarps * 32), args, 0, as_stream(stream),
                          (flags & TM_PDL) != 0);
 }

@@ -140,6 +140,57 @@ def test_norm_gradient(cuda, kind, shape, residual):
     close(dw, dww, 0.0, t, U * (M + 128) * (np.abs(dy64) * n).sum(0))
 
 
+# Rows enough for every block of the GPU to walk some (the form that copies rows ahead), with an odd
+# count, a gap between rows, short rows (several to a block) and long ones.
+MANY = [(4901, 1000, 1008), (2501, 4096, 4096), (1301, 8192, 8200), (641, 16384, 16384), (10001, 520, 520)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", MANY)
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_of_many_rows(cuda, kind, shape, residual):
+    t, (M, N, ld) = ref.TYPES[kind], shape
+    rng = np.random.default_rng(M + N)
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    make = lambda s: (torch.randn(M, ld, generator=gen, device="cuda") * s).to(t)  # noqa: E731
+    x, r, dy = make(1.0), make(3.0) if residual else None, make(1.0)
+    wkind = "f32" if residual else kind            # weights of another type too
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(N)).to(ref.TYPES[wkind]).cuda()
+    y, h = torch.full_like(x, 7.0), torch.full_like(x, 7.0) if residual else None
+    rstd = torch.zeros(M, device="cuda")
+    code = ref.CODE[kind]
+    tm.tm_rmsnorm(x, ld, r, ld, h, ld, w, M, N, EPS, y, ld, None, rstd, code, ref.CODE[wkind], code)
+    codes, sc = torch.zeros(M, ld, dtype=torch.uint8, device="cuda"), torch.zeros(M, -(-N // 64), device="cuda")
+    tm.tm_rmsnorm(x, ld, r, ld, None, ld, w, M, N, EPS, codes, ld, sc, None, code, ref.CODE[wkind], tm.TM_E4M3, 64)
+    codes1, sc1 = torch.zeros(M, ld, dtype=torch.uint8, device="cuda"), torch.zeros(M, 1, device="cuda")
+    tm.tm_rmsnorm(x, ld, r, ld, None, ld, w, M, N, EPS, codes1, ld, sc1, None, code, ref.CODE[wkind], tm.TM_E4M3, 0)
+    dx, dw = torch.full_like(x, 7.0), torch.zeros(N, dtype=ref.TYPES[wkind], device="cuda")
+    ws = tm.tm_rmsnorm_bwd_workspace_bytes(M, N)
+    scratch = torch.full((ws // 4,), float("nan"), device="cuda")
+    stream = h if residual else x
+    dr = r if residual else None
+    tm.tm_rmsnorm_bwd(dy, ld, stream, ld, w, rstd, dr, ld, dx, ld, dw, M, N, code, ref.CODE[wkind], scratch, ws)
+    tm.tm_check()
+    hw, sw, yw = ref.rmsnorm(ref.f64(x[:, :N]), ref.f64(r[:, :N]) if residual else None, ref.f64(w), EPS)
+    close(y[:, :N], yw, 64 * U, t)
+    close(rstd, sw, 62 * U, torch.float32)
+    if residual:
+        close(h[:, :N], hw, U, t)
+        assert bool((h[:, N:] == 7.0).all())
+    assert bool((y[:, N:] == 7.0).all()) and bool((dx[:, N:] == 7.0).all()) and not codes[:, N:].any()
+    check_e4m3(codes[:, :N].contiguous(), sc, yw, 64)
+    check_e4m3(codes1[:, :N].contiguous(), sc1, yw, 0)
+    s, h64, dy64, w64 = ref.f64(rstd), ref.f64(stream[:, :N]), ref.f64(dy[:, :N]), ref.f64(w)
+    dr64 = ref.f64(dr[:, :N]) if residual else None
+    dxw, dww = ref.rmsnorm_bwd(dy64, h64, w64, s, dr64)
+    n = np.abs(h64) * s[:, None]
+    gn = np.abs(dy64 * w64) * n
+    mean = gn.mean(1, keepdims=True)
+    extra = U * (8 * (s[:, None] * (np.abs(dy64 * w64) + n * mean) + (np.abs(dr64) if residual else 0)) + 112 * s[:, None] * n * mean)
+    close(dx[:, :N], dxw, 0.0, t, extra)
+    close(dw, dww, 0.0, ref.TYPES[wkind], U * (M + 128) * (np.abs(dy64) * n).sum(0))
+
+
 def test_norm_gradient_against_differences(cuda):
     # d/dx of sum(y * dy), by central differences of the forward definition in 64 bits
     rng = np.random.default_rng(2)
