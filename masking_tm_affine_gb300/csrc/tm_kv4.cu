@@ -120,12 +120,19 @@ __device__ __forceinline__ float vector_error(bool turn, float lo, float hi)
 
 // Bounds of a vector's fp32 errors: `err` is how far any of its values may be
 // off.  Of the step and the low:
+// (three roundings of the step: the difference, 1/15 and the product).
 struct Doubt {
     float step, low;
 };
 __device__ __forceinline__ Doubt doubt_of(float err, float s, float lo)
 {
-    return {err * (2.0f / 15.0f) + s * 0x1p-21f, err + fabsf(lo) * 0x1p-23f};
+    return {err * (2.0f / 15.0f) + s * 0x1.8p-23f, err + fabsf(lo) * 0x1p-24f};
+}
+__device__ __forceinline__ bool params_unsure(float err, float s, float lo)
+{
+    const Doubt u = doubt_of(err, s, lo);
+    return __half_as_ushort(held_half(s - u.step)) != __half_as_ushort(held_half(s + u.step)) ||
+           __half_as_ushort(held_half(lo - u.low)) != __half_as_ushort(held_half(lo + u.low));
 }
 
 // Value i (0 .. 15) of a lane in fp64, from the tensor.
@@ -168,23 +175,28 @@ __device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool rota
     float lo, hi;
     vector_extremes<LANES>(x, mask, lo, hi);
     const float err = vector_error(rotated, lo, hi);
-    uint32_t extreme = 0;  // the values that may be the minimum or the maximum
+    const float s = (hi - lo) * (1.0f / 15.0f);
+    __half step = held_half(s), low = held_half(lo);
+    if (params_unsure(err, s, lo)) {  // the same for every lane of the vector
+        uint32_t extreme = 0;  // the values that may be the minimum or the maximum
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (x[i / 8][i % 8] <= lo + 2 * err || x[i / 8][i % 8] >= hi - 2 * err) extreme |= 1u << i;
-    double dlo = INFINITY, dhi = -INFINITY;
-    for (; extreme; extreme &= extreme - 1) {
-        const double d = exact_value<T, INTER>(p, o0, o1, turn, pos, turns, gain, __ffs(extreme) - 1);
-        dlo = fmin(dlo, d);
-        dhi = fmax(dhi, d);
-    }
-    __syncwarp(mask);
+        for (int i = 0; i < 16; ++i)
+            if (x[i / 8][i % 8] <= lo + 2 * err || x[i / 8][i % 8] >= hi - 2 * err) extreme |= 1u << i;
+        double dlo = INFINITY, dhi = -INFINITY;
+        for (; extreme; extreme &= extreme - 1) {
+            const double d = exact_value<T, INTER>(p, o0, o1, turn, pos, turns, gain, __ffs(extreme) - 1);
+            dlo = fmin(dlo, d);
+            dhi = fmax(dhi, d);
+        }
+        __syncwarp(mask);
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) {
-        dlo = fmin(dlo, __shfl_xor_sync(mask, dlo, o));
-        dhi = fmax(dhi, __shfl_xor_sync(mask, dhi, o));
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            dlo = fmin(dlo, __shfl_xor_sync(mask, dlo, o));
+            dhi = fmax(dhi, __shfl_xor_sync(mask, dhi, o));
+        }
+        step = held_half_d((dhi - dlo) / 15.0);
+        low = held_half_d(dlo);
     }
-    const __half step = held_half_d((dhi - dlo) / 15.0), low = held_half_d(dlo);
     const float fs = __half2float(step), fl = __half2float(low);
     const float inv = fs > 0.0f ? 1.0f / fs : 0.0f;
     uint32_t word[2] = {0, 0}, close = 0;
@@ -232,6 +244,74 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
     const int half = a.rot / 2;
     const bool turned = ln < a.rot / 16;  // this lane's 16 dims are 8 pairs
     const int q0 = !turned || INTER ? 16 * ln : 8 * ln, q1 = !turned || INTER ? q0 + 8 : q0 + half;
+    // This lane's two runs of its head of a pass; false past the last head.
+    const int hl = lane / LANES, v0 = 16 * ln;
+    const T *q_base = reinterpret_cast<const T *>(a.Q) + t * a.qs_tok, *k_base = reinterpret_cast<const T *>(a.K) + t * a.ks_tok,
+            *v_base = reinterpret_cast<const T *>(a.V) + t * a.vs_tok;
+    auto source = [&](int pass, const T *&p0, const T *&p1) -> bool {
+        if (pass < nq) {
+            const int h = pass * PER + hl;
+            p0 = q_base + h * a.qs_head + q0;
+            p1 = p0 + (q1 - q0);
+            return h < a.Hq;
+        }
+        pass -= nq;
+        if (pass < nk) {
+            const int h = pass * PER + hl;
+            p0 = k_base + h * a.ks_head + q0;
+            p1 = p0 + (q1 - q0);
+            return h < a.Hkv;
+        }
+        const int h = (pass - nk) * PER + hl;
+        p0 = v_base + h * a.vs_head + v0;
+        p1 = p0 + 8;
+        return h < a.Hkv;
+    };
+    // Vectors of the next kDepth - 1 passes are on their way to shared memory (every lane
+    // copies and reads its own 2 x 8 values, so nothing has to be waited for but its own
+    // copies); off the 16-byte grid they are read when they are needed.
+    constexpr int kDepth = sizeof(T) == 2 ? 6 : 4, kParts = 8 * sizeof(T) / 16;  // 16-byte parts of a run
+    __shared__ __align__(16) uint4 ring[VEC ? kAppendWarps * kDepth * 2 * kParts * 32 : 1];
+    uint4 *mine = ring + (VEC ? warp * (kDepth * 2 * kParts * 32) + lane : 0);
+    auto copy = [&](int pass) {
+        if constexpr (VEC) {
+            const T *p0, *p1;
+            if (pass < pass1 && source(pass, p0, p1)) {
+                uint4 *d = mine + (pass - pass0) % kDepth * (2 * kParts * 32);
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d + i * 32)),
+                                 "l"(reinterpret_cast<const char *>(p0) + 16 * i)
+                                 : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d + (kParts + i) * 32)),
+                                 "l"(reinterpret_cast<const char *>(p1) + 16 * i)
+                                 : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    auto take = [&](int pass, float (&x)[2][8]) {
+        if constexpr (VEC) {
+            copy(pass + kDepth - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            const uint4 *d = mine + (pass - pass0) % kDepth * (2 * kParts * 32);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                Vec<T, 8> v;
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) reinterpret_cast<uint4 *>(&v)[i] = d[(u * kParts + i) * 32];
+                widen(v, x[u]);
+            }
+        } else {
+            const T *p0, *p1;
+            if (source(pass, p0, p1)) {
+                load8<T, false>(p0, x[0]);
+                load8<T, false>(p1, x[1]);
+            }
+        }
+    };
+    for (int i = 0; i < kDepth - 1; ++i) copy(pass0 + i);
     const int64_t slot = a.slots[t], pos = a.rot > 0 ? a.pos[t] : 0;
     for (int i = lane; i < half; i += 32) table[warp][i] = pair_rotation(pos, a.turns[i], a.gain, 1.0f);
     __syncwarp();
@@ -252,43 +332,6 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
     const int64_t head_bytes = (int64_t)(a.page / 16) * kv4_block_bytes(D);
     pdl_wait();
 
-    // Passes [p0, p1) of one tensor of H heads; every lane has its two runs in hand
-    // one pass ahead.
-    auto walk = [&](const T *base, int64_t tok, int64_t head, int H, int p0, int p1, int o0, int o1, auto work) {
-        if (p0 >= p1) return;
-        const int h0 = p0 * PER + lane / LANES;
-        const T *p = base + t * tok + h0 * head;
-        Vec<T, 8> n0, n1;
-        auto fetch = [&](bool ok) {
-            if constexpr (VEC) {
-                load_vec_if(p + o0, ok, n0);
-                load_vec_if(p + o1, ok, n1);
-            } else if (ok) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    n0.v[e] = p[o0 + e];
-                    n1.v[e] = p[o1 + e];
-                }
-            }
-        };
-        fetch(h0 < H);
-        for (int h = h0, i = p0; i < p1; ++i, h += PER) {
-            float x[2][8];
-            widen(n0, x[0]);
-            widen(n1, x[1]);
-            p += PER * head;
-            fetch(i + 1 < p1 && h + PER < H);
-            if (h < H) work(h, x);  // whole groups of lanes
-        }
-    };
-    walk(reinterpret_cast<const T *>(a.Q), a.qs_tok, a.qs_head, a.Hq, pass0, min(pass1, nq), q0, q1,
-         [&](int h, float (&x)[2][8]) {
-             if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
-             T *o = reinterpret_cast<T *>(a.QO) + t * a.qos_tok + h * a.qos_head;
-             store8<T, VEC>(o + q0, x[0]);
-             store8<T, VEC>(o + q1, x[1]);
-         });
-    if (!held) return;
     // Hold a vector and store it at its words of a block, its (step, low) at `at`.
     const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (lane / LANES * LANES);
     // True if fp32 could not decide all of it.
@@ -304,10 +347,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
             params = __halves2half2(__ushort_as_half(0x7fff), __ushort_as_half(0x7fff));
         } else {
             const float s = (hi - lo) * (1.0f / 15.0f);
-            const Doubt u = doubt_of(err, s, lo);
             const __half step = held_half(s), low = held_half(lo);
-            unsure = __half_as_ushort(held_half(s - u.step)) != __half_as_ushort(held_half(s + u.step)) ||
-                     __half_as_ushort(held_half(lo - u.low)) != __half_as_ushort(held_half(lo + u.low));
+            unsure = params_unsure(err, s, lo);
             const float fs = __half2float(step), fl = __half2float(low);
             // steps are 0 or at least 2^-24: the reciprocal is a normal number
             const float inv = fs > 0.0f ? rcp(fs) : 0.0f;
@@ -337,23 +378,44 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
         return __any_sync(mask, unsure);
     };
     uint32_t again_k = 0, again_v = 0;  // passes to go through again, from the first of this task
-    const int k0 = max(pass0 - nq, 0), k1 = min(pass1 - nq, nk), v0 = max(pass0 - nq - nk, 0), v1 = pass1 - nq - nk;
-    walk(reinterpret_cast<const T *>(a.K), a.ks_tok, a.ks_head, a.Hkv, k0, k1, q0, q1,
-         [&](int h, float (&x)[2][8]) {
-             if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
-             uint8_t *b = block + h * head_bytes;
-             if (hold(x, a.rot > 0, b + kv4_k_word(D, r, q0), b + kv4_k_word(D, r, q1), b + kv4_ks_off(D) + 4 * r))
-                 again_k |= 1u << (h / PER - k0);
-         });
-    walk(reinterpret_cast<const T *>(a.V), a.vs_tok, a.vs_head, a.Hkv, v0, v1, 16 * ln, 16 * ln + 8,
-         [&](int h, float (&x)[2][8]) {
-             uint8_t *b = block + h * head_bytes;
-             if (hold(x, false, b + kv4_v_word(D, r, 16 * ln), b + kv4_v_word(D, r, 16 * ln + 8), b + kv4_vs_off(D) + 4 * r))
-                 again_v |= 1u << (h / PER - v0);
-         });
+    const int k0 = max(pass0 - nq, 0), k1 = min(pass1 - nq, nk), w0 = max(pass0 - nq - nk, 0), w1 = pass1 - nq - nk;
+    float x[2][8];
+    for (int pass = pass0; pass < min(pass1, nq); ++pass) {
+        take(pass, x);
+        if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
+        const int h = pass * PER + hl;
+        if (h < a.Hq) {
+            T *o = reinterpret_cast<T *>(a.QO) + t * a.qos_tok + h * a.qos_head;
+            store8<T, VEC>(o + q0, x[0]);
+            store8<T, VEC>(o + q1, x[1]);
+        }
+    }
+    if (!held) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
+    for (int i = k0; i < k1; ++i) {
+        take(nq + i, x);
+        const int h = i * PER + hl;
+        if (h < a.Hkv) {  // whole groups of lanes
+            if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
+            uint8_t *b = block + h * head_bytes;
+            if (hold(x, a.rot > 0, b + kv4_k_word(D, r, q0), b + kv4_k_word(D, r, q1), b + kv4_ks_off(D) + 4 * r))
+                again_k |= 1u << (i - k0);
+        }
+    }
+    for (int i = w0; i < w1; ++i) {
+        take(nq + nk + i, x);
+        const int h = i * PER + hl;
+        if (h < a.Hkv) {
+            uint8_t *b = block + h * head_bytes;
+            if (hold(x, false, b + kv4_v_word(D, r, v0), b + kv4_v_word(D, r, v0 + 8), b + kv4_vs_off(D) + 4 * r))
+                again_v |= 1u << (i - w0);
+        }
+    }
     for (; again_k; again_k &= again_k - 1) {
-        const int h = (k0 + __ffs(again_k) - 1) * PER + lane / LANES;
-        const T *p = reinterpret_cast<const T *>(a.K) + t * a.ks_tok + h * a.ks_head;
+        const int h = (k0 + __ffs(again_k) - 1) * PER + hl;
+        const T *p = k_base + h * a.ks_head;
         const uint3 w = hold_exactly<T, D, VEC, INTER>(p, q0, q1, a.rot > 0, turned, pos, a.turns + 8 * ln, a.gain,
                                                        &table[warp][turned ? 8 * ln : 0]);
         uint8_t *b = block + h * head_bytes;
@@ -362,13 +424,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
         if (ln == 0) *reinterpret_cast<uint32_t *>(b + kv4_ks_off(D) + 4 * r) = w.z;
     }
     for (; again_v; again_v &= again_v - 1) {
-        const int h = (v0 + __ffs(again_v) - 1) * PER + lane / LANES;
-        const T *p = reinterpret_cast<const T *>(a.V) + t * a.vs_tok + h * a.vs_head;
-        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, 16 * ln, 16 * ln + 8, false, false, pos, a.turns, a.gain,
+        const int h = (w0 + __ffs(again_v) - 1) * PER + hl;
+        const T *p = v_base + h * a.vs_head;
+        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, v0, v0 + 8, false, false, pos, a.turns, a.gain,
                                                        &table[warp][0]);
         uint8_t *b = block + h * head_bytes;
-        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, 16 * ln)) = w.x;
-        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, 16 * ln + 8)) = w.y;
+        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, v0)) = w.x;
+        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, v0 + 8)) = w.y;
         if (ln == 0) *reinterpret_cast<uint32_t *>(b + kv4_vs_off(D) + 4 * r) = w.z;
     }
 }
