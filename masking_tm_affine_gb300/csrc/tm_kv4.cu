@@ -16,8 +16,9 @@
 // fp16 numbers.  One bound a vector finds those cases (a few vectors in a
 // thousand); after its heads a warp goes through those again, in a second routine
 // (out of the loop, whose registers a call in it would spill) that decides the values
-// concerned, and only those, by the same formula in fp64: fp64 runs at 1/64 of the fp32 rate
-// here, and deciding every value in it would take longer than the whole launch.
+// concerned, and only those, by the same formula in pairs of floats, good to 2^-44.
+// (fp64 runs at 1/64 of the fp32 rate here: one value took some 5 us, and the last
+// warp to meet one held the whole launch up: 47.0 against APPENDUS us.)
 #include "tm_host.h"
 
 #include "tm_kv4.cuh"
@@ -67,7 +68,6 @@ __device__ __forceinline__ void store8(T *p, const float (&f)[8])
 
 // fp16 of a value by way of fp32, clamped to fp16's range.
 __device__ __forceinline__ __half held_half(float x) { return __float2half_rn(fminf(fmaxf(x, -65504.0f), 65504.0f)); }
-__device__ __forceinline__ __half held_half_d(double x) { return held_half((float)x); }
 
 // Largest and smallest of three, NaN if any is.
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -108,14 +108,25 @@ __device__ __forceinline__ void vector_extremes(const float (&x)[2][8], unsigned
     }
 }
 
-// How far a rotated value may be off in fp32.  |cos|, |sin| are off by at most
-// 2.1e-7 (the argument's rounding pi 2^-25, sincospif's last place, the gain's
-// rounding), the products and the sum add 2^-23 of |a| + |b|: 3.3e-7 in all, below
-// 1.5 * 2^-22, and gain (|a| + |b|) is at most twice the larger of the vector's
-// rotated extremes.
-__device__ __forceinline__ float vector_error(bool turn, float lo, float hi)
+// How far any rotated value of a vector may be off in fp32, from the largest
+// |a| + |b| of its pairs.  |cos|, |sin| are off by at most 1.5e-7 (the argument's
+// rounding pi 2^-27, sincospif's last place, the gain's rounding), the products and
+// the sum add 2^-23 of |a| + |b|: 2.7e-7 in all, below 1.15 * 2^-22.
+template <int LANES>
+__device__ __forceinline__ float vector_error(float pair, float gain, unsigned mask)
 {
-    return turn ? fmaxf(fabsf(lo), fabsf(hi)) * 0x1.82p-21f : 0.0f;
+    return lanes_max(pair, LANES, mask) * fabsf(gain) * 0x1.28p-22f;
+}
+
+// The largest |a| + |b| of a lane's pairs, before they are turned.
+template <bool INTER>
+__device__ __forceinline__ float largest_pair(const float (&x)[2][8])
+{
+    float m[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        m[e] = INTER ? fabsf(x[e / 4][e % 4 * 2]) + fabsf(x[e / 4][e % 4 * 2 + 1]) : fabsf(x[0][e]) + fabsf(x[1][e]);
+    return fmaxf(max3(m[0], m[1], m[2]), max3(max3(m[3], m[4], m[5]), m[6], m[7]));
 }
 
 // Bounds of a vector's fp32 errors: `err` is how far any of its values may be
@@ -135,29 +146,107 @@ __device__ __forceinline__ bool params_unsure(float err, float s, float lo)
            __half_as_ushort(held_half(lo - u.low)) != __half_as_ushort(held_half(lo + u.low));
 }
 
-// Value i (0 .. 15) of a lane in fp64, from the tensor.
-template <typename T, bool INTER>
-__device__ __noinline__ double exact_value(const T *p, int o0, int o1, bool turn, int64_t pos, const uint64_t *turns,
-                                           float gain, int i)
+// ---------------------------------------------------------------- pairs of floats
+// h + l with |l| at most half the last place of h: 48 bits, from the error-free sum
+// (Knuth) and product (one fused multiply-add) of two floats.
+struct Pair {
+    float h, l;
+};
+
+__device__ __forceinline__ Pair sum_of(float a, float b)
 {
-    if (!turn) return (double)to_f(i < 8 ? p[o0 + i] : p[o1 + i - 8]);
+    const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+    return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t))};
+}
+__device__ __forceinline__ Pair product_of(float a, float b)
+{
+    const float p = __fmul_rn(a, b);
+    return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b)
+{
+    const Pair s = sum_of(a.h, b.h), t = sum_of(a.l, b.l), u = sum_of(s.h, __fadd_rn(s.l, t.h));
+    return sum_of(u.h, __fadd_rn(u.l, t.l));
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b)
+{
+    const Pair p = product_of(a.h, b.h);
+    return sum_of(p.h, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, p.l)));
+}
+__device__ __forceinline__ bool less(Pair a, Pair b) { return a.h < b.h || (a.h == b.h && a.l < b.l); }
+
+// cos and sin of a signed fraction of a turn (units of 2^-64), good to about 2^-44:
+// the nearest quarter turn comes off exactly, then Taylor's series over [-pi/4, pi/4],
+// its first terms in pairs, the others (below 2^-20 of the result) in floats.
+__device__ __forceinline__ void exact_rotation(int64_t fraction, Pair &c, Pair &s)
+{
+    const uint64_t f = (uint64_t)fraction, quarter = (f + (1ull << 61)) >> 62;
+    const int64_t r = (int64_t)(f - (quarter << 62));  // |r| <= 2^61
+    const float rh = (float)(int32_t)(r >> 32);
+    const int64_t rest = r - ((int64_t)(int32_t)rh << 32);  // |rest| < 2^38
+    const float rl = (float)(int32_t)(rest >> 8);
+    const Pair x = mul(sum_of(rh * 0x1p-32f, rl * 0x1p-56f), {0x1.921fb6p+2f, -0x1.777a5cp-23f});  // 2 pi
+    const Pair z = mul(x, x);
+    const float zh = z.h;
+    // sin x = x - x^3 (1/3! - z/5! + z^2/7! - z^3 (1/9! - z/11! + z^2/13!))
+    float t = fmaf(zh, fmaf(zh, 1.6059044e-10f, -2.5052108e-8f), 2.7557319e-6f);
+    Pair u = add({0x1.a01a02p-13f, -0x1.7f97fap-39f}, {-zh * t, 0.0f});
+    u = mul(z, u);
+    u = add({0x1.111112p-7f, -0x1.dddddep-32f}, {-u.h, -u.l});
+    u = mul(z, u);
+    u = add({0x1.555556p-3f, -0x1.555556p-28f}, {-u.h, -u.l});
+    u = mul(mul(x, z), u);
+    const Pair sn = add(x, {-u.h, -u.l});
+    // cos x = 1 - z (1/2 - z/4! + z^2/6! - z^3 (1/8! - z/10! + z^2/12! - z^3/14!))
+    t = fmaf(zh, fmaf(zh, fmaf(zh, -1.1470746e-11f, 2.0876757e-9f), -2.7557319e-7f), 2.4801587e-5f);
+    u = add({0x1.6c16c2p-10f, -0x1.27d27ep-35f}, {-zh * t, 0.0f});
+    u = mul(z, u);
+    u = add({0x1.555556p-5f, -0x1.555556p-30f}, {-u.h, -u.l});
+    u = mul(z, u);
+    u = add({0.5f, 0.0f}, {-u.h, -u.l});
+    u = mul(z, u);
+    const Pair cn = add({1.0f, 0.0f}, {-u.h, -u.l});
+    c = quarter & 1 ? Pair{-sn.h, -sn.l} : cn;
+    s = quarter & 1 ? cn : sn;
+    if (quarter & 2) {
+        c = {-c.h, -c.l};
+        s = {-s.h, -s.l};
+    }
+}
+
+// Value i (0 .. 15) of a lane to 2^-44 of its pair's size, from the tensor.
+template <typename T, bool INTER>
+__device__ __noinline__ Pair exact_value(const T *p, int o0, int o1, bool turn, int64_t pos, const uint64_t *turns,
+                                         float gain, int i)
+{
+    if (!turn) return {to_f(i < 8 ? p[o0 + i] : p[o1 + i - 8]), 0.0f};
     const int pair = INTER ? i / 2 : i % 8;
     const bool first = INTER ? i % 2 == 0 : i < 8;
     const float a = to_f(INTER ? (pair < 4 ? p[o0 + 2 * pair] : p[o1 + 2 * pair - 8]) : p[o0 + pair]);
     const float b = to_f(INTER ? (pair < 4 ? p[o0 + 2 * pair + 1] : p[o1 + 2 * pair - 7]) : p[o1 + pair]);
-    double s, c;
-    sincospi((double)turn_fraction(pos, turns[pair]) * 0x1p-63, &s, &c);
-    const double r = first ? (double)a * c - (double)b * s : (double)a * s + (double)b * c;
-    return r * (double)gain;
+    Pair c, s;
+    exact_rotation(turn_fraction(pos, turns[pair]), c, s);
+    const Pair r = first ? add(mul({a, 0.0f}, c), mul({-b, 0.0f}, s)) : add(mul({a, 0.0f}, s), mul({b, 0.0f}, c));
+    return mul(r, {gain, 0.0f});
 }
 
-__device__ __forceinline__ int exact_code(double x, float low, float step)
+// (x - low) / step to the nearest whole number in 0 .. 15, a tie to the even one:
+// k from floats is at most one off, and k step is exact.
+__device__ __forceinline__ int exact_code(Pair x, float low, float step)
 {
-    const double t = rint((x - (double)low) / (double)step);
-    return (int)fmin(fmax(t, 0.0), 15.0);
+    const Pair d = add(x, {-low, 0.0f});
+    float k = fminf(fmaxf(rintf(d.h / step), 0.0f), 15.0f);
+    const Pair r = add(d, {-k * step, 0.0f});
+    const Pair up = add(r, {-0.5f * step, 0.0f}), down = add(r, {0.5f * step, 0.0f});
+    const bool odd = (int)k & 1;
+    if (up.h > 0.0f || (up.h == 0.0f && odd))
+        k += 1.0f;
+    else if (down.h < 0.0f || (down.h == 0.0f && odd))
+        k -= 1.0f;
+    return (int)fminf(fmaxf(k, 0.0f), 15.0f);
 }
 
-// The slow path: two words of codes and (step, low), whatever is in doubt in fp64.
+// The slow path: two words of codes and (step, low), whatever is in doubt in pairs.
 // Called by all D/16 lanes of a vector without NaN or infinity.
 template <typename T, int D, bool VEC, bool INTER>
 __device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool rotated, bool turn, int64_t pos, const uint64_t *turns,
@@ -171,10 +260,10 @@ __device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool rota
     for (int e = 0; e < 8; ++e) cs[e] = turn ? table[e] : make_float2(1.0f, 0.0f);
     load8<T, VEC>(p + o0, x[0]);
     load8<T, VEC>(p + o1, x[1]);
+    float err = 0.0f, lo, hi;
+    if (rotated) err = vector_error<LANES>(turn ? largest_pair<INTER>(x) : 0.0f, gain, mask);
     if (turn) rotate_pairs<8, INTER>(x[0], x[1], cs);
-    float lo, hi;
     vector_extremes<LANES>(x, mask, lo, hi);
-    const float err = vector_error(rotated, lo, hi);
     const float s = (hi - lo) * (1.0f / 15.0f);
     __half step = held_half(s), low = held_half(lo);
     if (params_unsure(err, s, lo)) {  // the same for every lane of the vector
@@ -182,20 +271,25 @@ __device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool rota
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             if (x[i / 8][i % 8] <= lo + 2 * err || x[i / 8][i % 8] >= hi - 2 * err) extreme |= 1u << i;
-        double dlo = INFINITY, dhi = -INFINITY;
+        Pair least = {INFINITY, 0.0f}, most = {-INFINITY, 0.0f};
         for (; extreme; extreme &= extreme - 1) {
-            const double d = exact_value<T, INTER>(p, o0, o1, turn, pos, turns, gain, __ffs(extreme) - 1);
-            dlo = fmin(dlo, d);
-            dhi = fmax(dhi, d);
+            const Pair d = exact_value<T, INTER>(p, o0, o1, turn, pos, turns, gain, __ffs(extreme) - 1);
+            least = less(d, least) ? d : least;
+            most = less(most, d) ? d : most;
         }
         __syncwarp(mask);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) {
-            dlo = fmin(dlo, __shfl_xor_sync(mask, dlo, o));
-            dhi = fmax(dhi, __shfl_xor_sync(mask, dhi, o));
+            const Pair l = {__shfl_xor_sync(mask, least.h, o), __shfl_xor_sync(mask, least.l, o)};
+            const Pair m = {__shfl_xor_sync(mask, most.h, o), __shfl_xor_sync(mask, most.l, o)};
+            least = less(l, least) ? l : least;
+            most = less(most, m) ? m : most;
         }
-        step = held_half_d((dhi - dlo) / 15.0);
-        low = held_half_d(dlo);
+        // a fifteenth of the spread: the quotient of the first part, and what it leaves
+        const Pair d = add(most, {-least.h, -least.l});
+        const float q = d.h / 15.0f, rest = fmaf(-q, 15.0f, d.h) + d.l;
+        step = held_half(sum_of(q, rest * (1.0f / 15.0f)).h);
+        low = held_half(least.h);
     }
     const float fs = __half2float(step), fl = __half2float(low);
     const float inv = fs > 0.0f ? 1.0f / fs : 0.0f;
@@ -220,12 +314,12 @@ __device__ __noinline__ uint3 hold_exactly(const T *p, int o0, int o1, bool rota
     return make_uint3(word[0], word[1], *reinterpret_cast<const uint32_t *>(&params));
 }
 
-constexpr int kAppendWarps = 4;
+constexpr int kAppendWarps = 1;
 
 // One warp a task: a token (blockIdx.x) and one of the `split` parts (blockIdx.y) of
 // its passes of 512 / D heads.
 template <typename T, int D, bool VEC, bool INTER>
-__global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(kAppendWarps * 32, 24) kv4_append_kernel(const __grid_constant__ AppendArgs a)
 {
     constexpr int LANES = D / 16, PER = 32 / LANES;  // lanes a head, heads a pass
     __shared__ float2 table[kAppendWarps][D / 2];
@@ -245,7 +339,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
     const bool turned = ln < a.rot / 16;  // this lane's 16 dims are 8 pairs
     const int q0 = !turned || INTER ? 16 * ln : 8 * ln, q1 = !turned || INTER ? q0 + 8 : q0 + half;
     // This lane's two runs of its head of a pass; false past the last head.
-    const int hl = lane / LANES, v0 = 16 * ln;
+    const int hl = lane / LANES, v0 = 8 * ln, v1 = v0 + D / 2;  // (a warp's accesses stay contiguous)
     const T *q_base = reinterpret_cast<const T *>(a.Q) + t * a.qs_tok, *k_base = reinterpret_cast<const T *>(a.K) + t * a.ks_tok,
             *v_base = reinterpret_cast<const T *>(a.V) + t * a.vs_tok;
     auto source = [&](int pass, const T *&p0, const T *&p1) -> bool {
@@ -264,7 +358,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
         }
         const int h = (pass - nk) * PER + hl;
         p0 = v_base + h * a.vs_head + v0;
-        p1 = p0 + 8;
+        p1 = p0 + D / 2;
         return h < a.Hkv;
     };
     // Vectors of the next kDepth - 1 passes are on their way to shared memory (every lane
@@ -334,11 +428,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
 
     // Hold a vector and store it at its words of a block, its (step, low) at `at`.
     const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (lane / LANES * LANES);
-    // True if fp32 could not decide all of it.
-    auto hold = [&](float (&x)[2][8], bool turn, uint8_t *w0, uint8_t *w1, uint8_t *at) -> bool {
+    // True if fp32 could not decide all of it; err: how far any of its values may be off.
+    auto hold = [&](float (&x)[2][8], float err, uint8_t *w0, uint8_t *w1, uint8_t *at) -> bool {
         float lo, hi;
         vector_extremes<LANES>(x, mask, lo, hi);  // NaN if any value is
-        const float err = vector_error(turn, lo, hi);
         bool unsure = false;
         uint32_t word[2];
         __half2 params;
@@ -350,16 +443,15 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
             const __half step = held_half(s), low = held_half(lo);
             unsure = params_unsure(err, s, lo);
             const float fs = __half2float(step), fl = __half2float(low);
-            // steps are 0 or at least 2^-24: the reciprocal is a normal number
-            const float inv = fs > 0.0f ? rcp(fs) : 0.0f;
+            const float inv = fs > 0.0f ? 1.0f / fs : 0.0f;
             // t = (x - low) / step as 15 times a value cut to [0, 1]; adding 1.5 * 2^23
             // rounds it to a whole number, in the low bits of the sum
-            const float m15 = inv * (1.0f / 15.0f), c15 = -fl * m15, magic = 12582912.0f;
+            const float m15 = inv * (1.0f / 15.0f), magic = 12582912.0f;
             float off = 0.0f;  // the largest distance from a whole number
             word[0] = word[1] = 0;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float t15 = __saturatef(fmaf(x[i / 8][i % 8], m15, c15));
+                const float t15 = __saturatef((x[i / 8][i % 8] - fl) * m15);
                 const float sum = fmaf(t15, 15.0f, magic), whole = sum - magic;
                 off = fmaxf(off, fabsf(fmaf(t15, 15.0f, -whole)));
                 word[i / 8] += __float_as_uint(sum) << (i % 8 * 4);
@@ -367,9 +459,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
             word[0] -= 0x4b400000u * 0x11111111u;
             word[1] -= 0x4b400000u * 0x11111111u;
             params = __halves2half2(step, low);
-            // the values' error, five roundings of t up to 15 (the reciprocal counts two),
-            // and those of low / step
-            const float et = (err + fabsf(fl) * 0x1p-21f) * inv + 15.0f * 0x1.4p-22f;
+            // the values' error, and four roundings of t (the difference, 1 / step, 1/15, the
+            // product), which is at most 15
+            const float et = err * inv + 15.0f * 0x1p-22f;
             unsure = unsure || off + et >= 0.5f;
         }
         *reinterpret_cast<uint32_t *>(w0) = word[0];
@@ -398,9 +490,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
         take(nq + i, x);
         const int h = i * PER + hl;
         if (h < a.Hkv) {  // whole groups of lanes
+            float err = 0.0f;
+            if (a.rot > 0) err = vector_error<LANES>(turned ? largest_pair<INTER>(x) : 0.0f, a.gain, mask);
             if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
             uint8_t *b = block + h * head_bytes;
-            if (hold(x, a.rot > 0, b + kv4_k_word(D, r, q0), b + kv4_k_word(D, r, q1), b + kv4_ks_off(D) + 4 * r))
+            if (hold(x, err, b + kv4_k_word(D, r, q0), b + kv4_k_word(D, r, q1), b + kv4_ks_off(D) + 4 * r))
                 again_k |= 1u << (i - k0);
         }
     }
@@ -409,7 +503,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
         const int h = i * PER + hl;
         if (h < a.Hkv) {
             uint8_t *b = block + h * head_bytes;
-            if (hold(x, false, b + kv4_v_word(D, r, v0), b + kv4_v_word(D, r, v0 + 8), b + kv4_vs_off(D) + 4 * r))
+            if (hold(x, 0.0f, b + kv4_v_word(D, r, v0), b + kv4_v_word(D, r, v1), b + kv4_vs_off(D) + 4 * r))
                 again_v |= 1u << (i - w0);
         }
     }
@@ -426,11 +520,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const 
     for (; again_v; again_v &= again_v - 1) {
         const int h = (w0 + __ffs(again_v) - 1) * PER + hl;
         const T *p = v_base + h * a.vs_head;
-        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, v0, v0 + 8, false, false, pos, a.turns, a.gain,
+        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, v0, v1, false, false, pos, a.turns, a.gain,
                                                        &table[warp][0]);
         uint8_t *b = block + h * head_bytes;
         *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, v0)) = w.x;
-        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, v0 + 8)) = w.y;
+        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, v1)) = w.y;
         if (ln == 0) *reinterpret_cast<uint32_t *>(b + kv4_vs_off(D) + 4 * r) = w.z;
     }
 }
@@ -441,56 +535,67 @@ struct GatherArgs {
     void *K, *V;
     int64_t slots_in_pool, page_bytes, ks_tok, ks_head, vs_tok, vs_head, T;
     int page, Hkv;
-    FastDiv by_heads;
+    FastDiv by_heads, by_page;
     unsigned *status;
 };
 
-// Bound by HBM: D/2 + 4 bytes read and D elements written a vector.  A group of
-// D/16 lanes takes one (token, head), 16 values of K and 16 of V a lane.
+// Bound by HBM: D/2 + 4 bytes read and D elements written a vector.  A group of D/8
+// lanes takes a (token, head) item, 8 values of K and 8 of V a lane: a word read and a
+// 16-byte vector written each, contiguous over the lanes (16 values a lane wrote every
+// other 16 bytes at a time: 14.9 against GATHERUS us for 8192 tokens of 8 heads).  A
+// thread asks for all of its items' words before it works on the first.
+constexpr int kGatherItems = 4;
+
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__ GatherArgs a)
 {
-    constexpr int LANES = D / 16;
+    constexpr int LANES = D / 8, PER = 256 / LANES;
     pdl_trigger();
-    const int ln = threadIdx.x % LANES;
-    const int64_t item = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
-    if (item < a.T * a.Hkv) {
-        const int64_t t = item <= INT32_MAX ? (int64_t)fdiv((uint32_t)item, a.by_heads) : item / a.Hkv;
-        const int h = (int)(item - t * a.Hkv);
-        const int64_t slot = a.slots[t];
-        const bool held = slot >= 0 && slot < a.slots_in_pool;
-        if (!held && slot != -1 && ln == 0) atomicOr(a.status, kStatusIndex);
-        uint32_t kw[2] = {0, 0}, vw[2] = {0, 0};
-        float2 kp = {0.0f, 0.0f}, vp = {0.0f, 0.0f};
-        if (held) {
-            const int64_t pg = slot <= INT32_MAX ? (int64_t)((uint32_t)slot / (uint32_t)a.page) : slot / a.page;
-            const int at = (int)(slot - pg * a.page), r = at % 16;
-            const uint8_t *b = a.pool + pg * a.page_bytes + ((int64_t)h * (a.page / 16) + at / 16) * kv4_block_bytes(D);
+    const int d = threadIdx.x % LANES * 8;
+    const int64_t item0 = (int64_t)blockIdx.x * (PER * kGatherItems) + threadIdx.x / LANES;
+    uint32_t kw[kGatherItems], vw[kGatherItems], ks[kGatherItems], vs[kGatherItems];
+    int64_t tok[kGatherItems], slot[kGatherItems];
+    int head[kGatherItems];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                kw[u] = ld_nc_b32(b + kv4_k_word(D, r, 16 * ln + 8 * u));
-                vw[u] = ld_nc_b32(b + kv4_v_word(D, r, 16 * ln + 8 * u));
-            }
-            const uint32_t ks = ld_nc_b32(b + kv4_ks_off(D) + 4 * r), vs = ld_nc_b32(b + kv4_vs_off(D) + 4 * r);
-            kp = __half22float2(*reinterpret_cast<const __half2 *>(&ks));
-            vp = __half22float2(*reinterpret_cast<const __half2 *>(&vs));
-        }
-        pdl_wait();
+    for (int i = 0; i < kGatherItems; ++i) {
+        const int64_t item = item0 + i * PER;
+        const bool in = item < a.T * a.Hkv;
+        tok[i] = item <= INT32_MAX ? (int64_t)fdiv((uint32_t)item, a.by_heads) : item / a.Hkv;
+        head[i] = (int)(item - tok[i] * a.Hkv);
+        slot[i] = in ? a.slots[tok[i]] : -1;
+        tok[i] = in ? tok[i] : -1;
+    }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float k8[8], v8[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                k8[e] = fmaf((float)(kw[u] >> (4 * e) & 15u), kp.x, kp.y);
-                v8[e] = fmaf((float)(vw[u] >> (4 * e) & 15u), vp.x, vp.y);
-            }
-            if (a.K)
-                store8<T, VEC>(reinterpret_cast<T *>(a.K) + t * a.ks_tok + h * a.ks_head + 16 * ln + 8 * u, k8);
-            if (a.V)
-                store8<T, VEC>(reinterpret_cast<T *>(a.V) + t * a.vs_tok + h * a.vs_head + 16 * ln + 8 * u, v8);
+    for (int i = 0; i < kGatherItems; ++i) {
+        kw[i] = vw[i] = ks[i] = vs[i] = 0;  // slot -1: zeros
+        if (slot[i] >= 0 && slot[i] < a.slots_in_pool) {
+            const int64_t pg = slot[i] <= INT32_MAX ? (int64_t)fdiv((uint32_t)slot[i], a.by_page) : slot[i] / a.page;
+            const int at = (int)(slot[i] - pg * a.page), r = at % 16;
+            const uint8_t *b =
+                a.pool + pg * a.page_bytes + ((int64_t)head[i] * (a.page / 16) + at / 16) * kv4_block_bytes(D);
+            kw[i] = ld_nc_b32(b + kv4_k_word(D, r, d));
+            vw[i] = ld_nc_b32(b + kv4_v_word(D, r, d));
+            ks[i] = ld_nc_b32(b + kv4_ks_off(D) + 4 * r);
+            vs[i] = ld_nc_b32(b + kv4_vs_off(D) + 4 * r);
+        } else if (slot[i] != -1 && d == 0) {
+            atomicOr(a.status, kStatusIndex);
         }
     }
     pdl_wait();
+#pragma unroll
+    for (int i = 0; i < kGatherItems; ++i) {
+        if (tok[i] < 0) continue;
+        const float2 kp = __half22float2(*reinterpret_cast<const __half2 *>(&ks[i]));
+        const float2 vp = __half22float2(*reinterpret_cast<const __half2 *>(&vs[i]));
+        float k8[8], v8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            k8[e] = fmaf((float)(kw[i] >> (4 * e) & 15u), kp.x, kp.y);
+            v8[e] = fmaf((float)(vw[i] >> (4 * e) & 15u), vp.x, vp.y);
+        }
+        if (a.K) store8<T, VEC>(reinterpret_cast<T *>(a.K) + tok[i] * a.ks_tok + head[i] * a.ks_head + d, k8);
+        if (a.V) store8<T, VEC>(reinterpret_cast<T *>(a.V) + tok[i] * a.vs_tok + head[i] * a.vs_head + d, v8);
+    }
 }
 
 template <typename T, int D>
@@ -610,13 +715,13 @@ extern "C" tm_status tm_kv4_gather(const void *pool, int64_t pages, int32_t page
                sp = span_of(pool, pages * pb, 1, pages * pb, 1);
     if ((K && V && heads_meet(k, Hkv, v, Hkv, T, D, e)) || meets(sk, ss) || meets(sv, ss) || meets(sk, sp) || meets(sv, sp)) return TM_ERR_INVALID_ARG;
     const bool vec = (!K || heads_vec(k, e)) && (!V || heads_vec(v, e));
-    const int64_t per = 256 / (D / 16), blocks = (T * Hkv + per - 1) / per;
+    const int64_t per = 256 / (D / 8) * kGatherItems, blocks = (T * Hkv + per - 1) / per;
     if (blocks > INT32_MAX) return TM_ERR_INVALID_ARG;
     const DevInfo *dev;
     tm_status st = device_info(&dev);
     if (st != TM_OK) return st;
     GatherArgs a = {reinterpret_cast<const uint8_t *>(pool), slots, K, V, pages * page, pb, ks_tok, ks_head, vs_tok,
-                    vs_head, T, page, Hkv, make_fastdiv((uint32_t)Hkv), dev->status};
+                    vs_head, T, page, Hkv, make_fastdiv((uint32_t)Hkv), make_fastdiv((uint32_t)page), dev->status};
     const void *kern = xtype == TM_F32   ? gather_kernel<float>(D, vec)
                        : xtype == TM_F16 ? gather_kernel<__half>(D, vec)
                                          : gather_kernel<__nv_bfloat16>(D, vec);

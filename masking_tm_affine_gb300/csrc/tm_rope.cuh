@@ -4,8 +4,7 @@
 // p * turns_i in wrapping 64-bit integers is the exact fraction of a turn at
 // position p (for |p| up to 2^63; the only error is turns_i's own rounding,
 // p * 2^-65 turns).  Read as a signed number it is the angle in units of
-// 2^-63 * pi within [-pi, pi), and its upper half in units of 2^-31 * pi one
-// rounding away from sincospif's argument.
+// 2^-63 * pi within [-pi, pi).
 // fp32 angles formed as p * f_i would be off by 0.03 radians at p = 2^20.
 #pragma once
 
@@ -21,10 +20,16 @@ __device__ __forceinline__ int64_t turn_fraction(int64_t pos, uint64_t turns)
 // (cos, sin) * gain of a pair; sign -1 turns back.
 __device__ __forceinline__ float2 pair_rotation(int64_t pos, uint64_t turns, float gain, float sign)
 {
+    // The nearest quarter turn comes off exactly, in integers, so that what is rounded is
+    // at most an eighth of a turn.  The upper 32 bits are enough (2^-32 of a turn) and
+    // convert at full rate, 64 bits do not.
+    const uint32_t f = (uint32_t)((uint64_t)turn_fraction(pos, turns) >> 32);
+    const uint32_t quarter = (f + 0x20000000u) >> 30;
     float s, c;
-    // the upper 32 bits are enough (2^-32 of a turn) and convert at full rate, 64 bits do not
-    sincospif((float)(int32_t)(turn_fraction(pos, turns) >> 32) * 0x1p-31f, &s, &c);
-    return make_float2(c * gain, s * gain * sign);
+    sincospif((float)(int32_t)(f - (quarter << 30)) * 0x1p-31f, &s, &c);
+    const float u = quarter & 1 ? -s : c, v = quarter & 1 ? c : s;
+    const float g = quarter & 2 ? -gain : gain;
+    return make_float2(u * g, v * g * sign);
 }
 
 // A lane's P pairs: `lo` and `hi` hold its two vectors of P elements.  Half
