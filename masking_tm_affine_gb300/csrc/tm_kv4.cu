@@ -16,9 +16,8 @@
 // fp16 numbers.  One bound a vector finds those cases (a few vectors in a
 // thousand); after its heads a warp goes through those again, in a second routine
 // (out of the loop, whose registers a call in it would spill) that decides the values
-// concerned, and only those, by the same formula in pairs of floats, good to 2^-44.
-// (fp64 runs at 1/64 of the fp32 rate here: one value took some 5 us, and the last
-// warp to meet one held the whole launch up: 47.0 against APPENDUS us.)
+// concerned, and only those, by the same formula in pairs of floats, good to 2^-41
+// (fp64 runs at 1/64 of the fp32 rate here).
 #include "tm_host.h"
 
 #include "tm_kv4.cuh"
@@ -175,7 +174,7 @@ __device__ __forceinline__ Pair mul(Pair a, Pair b)
 }
 __device__ __forceinline__ bool less(Pair a, Pair b) { return a.h < b.h || (a.h == b.h && a.l < b.l); }
 
-// cos and sin of a signed fraction of a turn (units of 2^-64), good to about 2^-44:
+// cos and sin of a signed fraction of a turn (units of 2^-64), good to about 2^-41:
 // the nearest quarter turn comes off exactly, then Taylor's series over [-pi/4, pi/4],
 // its first terms in pairs, the others (below 2^-20 of the result) in floats.
 __device__ __forceinline__ void exact_rotation(int64_t fraction, Pair &c, Pair &s)
@@ -214,7 +213,7 @@ __device__ __forceinline__ void exact_rotation(int64_t fraction, Pair &c, Pair &
     }
 }
 
-// Value i (0 .. 15) of a lane to 2^-44 of its pair's size, from the tensor.
+// Value i (0 .. 15) of a lane to 2^-41 of its pair's size, from the tensor.
 template <typename T, bool INTER>
 __device__ __noinline__ Pair exact_value(const T *p, int o0, int o1, bool turn, int64_t pos, const uint64_t *turns,
                                          float gain, int i)
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 24) kv4_append_kernel(const
     // Vectors of the next kDepth - 1 passes are on their way to shared memory (every lane
     // copies and reads its own 2 x 8 values, so nothing has to be waited for but its own
     // copies); off the 16-byte grid they are read when they are needed.
-    constexpr int kDepth = sizeof(T) == 2 ? 6 : 4, kParts = 8 * sizeof(T) / 16;  // 16-byte parts of a run
+    constexpr int kDepth = 4, kParts = 8 * sizeof(T) / 16;  // 16-byte parts of a run
     __shared__ __align__(16) uint4 ring[VEC ? kAppendWarps * kDepth * 2 * kParts * 32 : 1];
     uint4 *mine = ring + (VEC ? warp * (kDepth * 2 * kParts * 32) + lane : 0);
     auto copy = [&](int pass) {
@@ -469,8 +468,6 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 24) kv4_append_kernel(const
         if (ln == 0) *reinterpret_cast<__half2 *>(at) = params;
         return __any_sync(mask, unsure);
     };
-    uint32_t again_k = 0, again_v = 0;  // passes to go through again, from the first of this task
-    const int k0 = max(pass0 - nq, 0), k1 = min(pass1 - nq, nk), w0 = max(pass0 - nq - nk, 0), w1 = pass1 - nq - nk;
     float x[2][8];
     for (int pass = pass0; pass < min(pass1, nq); ++pass) {
         take(pass, x);
@@ -486,46 +483,37 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 24) kv4_append_kernel(const
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
     }
-    for (int i = k0; i < k1; ++i) {
-        take(nq + i, x);
-        const int h = i * PER + hl;
+    // Keys and values in one loop: two would not fit the instruction cache together.
+    uint32_t again = 0;  // passes to go through again, from the first of keys or values
+    const int first = max(pass0, nq), kw0 = kv4_k_word(D, r, q0), kw1 = kv4_k_word(D, r, q1),
+              vw0 = kv4_v_word(D, r, v0), vw1 = kv4_v_word(D, r, v1);
+    for (int pass = first; pass < pass1; ++pass) {
+        take(pass, x);
+        const bool k = pass < nq + nk;
+        const int h = (pass - nq - (k ? 0 : nk)) * PER + hl;
         if (h < a.Hkv) {  // whole groups of lanes
             float err = 0.0f;
-            if (a.rot > 0) err = vector_error<LANES>(turned ? largest_pair<INTER>(x) : 0.0f, a.gain, mask);
-            if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
+            if (k && a.rot > 0) {
+                err = vector_error<LANES>(turned ? largest_pair<INTER>(x) : 0.0f, a.gain, mask);
+                if (turned) rotate_pairs<8, INTER>(x[0], x[1], cs);
+            }
             uint8_t *b = block + h * head_bytes;
-            if (hold(x, err, b + kv4_k_word(D, r, q0), b + kv4_k_word(D, r, q1), b + kv4_ks_off(D) + 4 * r))
-                again_k |= 1u << (i - k0);
+            if (hold(x, err, b + (k ? kw0 : vw0), b + (k ? kw1 : vw1), b + (k ? kv4_ks_off(D) : kv4_vs_off(D)) + 4 * r))
+                again |= 1u << (pass - first);
         }
     }
-    for (int i = w0; i < w1; ++i) {
-        take(nq + nk + i, x);
-        const int h = i * PER + hl;
-        if (h < a.Hkv) {
-            uint8_t *b = block + h * head_bytes;
-            if (hold(x, 0.0f, b + kv4_v_word(D, r, v0), b + kv4_v_word(D, r, v1), b + kv4_vs_off(D) + 4 * r))
-                again_v |= 1u << (i - w0);
-        }
-    }
-    for (; again_k; again_k &= again_k - 1) {
-        const int h = (k0 + __ffs(again_k) - 1) * PER + hl;
-        const T *p = k_base + h * a.ks_head;
-        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, q0, q1, a.rot > 0, turned, pos, a.turns + 8 * ln, a.gain,
-                                                       &table[warp][turned ? 8 * ln : 0]);
+    for (; again; again &= again - 1) {
+        const int pass = first + __ffs(again) - 1;
+        const bool k = pass < nq + nk;
+        const int h = (pass - nq - (k ? 0 : nk)) * PER + hl;
+        const T *p = k ? k_base + h * a.ks_head : v_base + h * a.vs_head;
+        const bool turn = k && turned;
+        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, k ? q0 : v0, k ? q1 : v1, k && a.rot > 0, turn, pos,
+                                                       a.turns + 8 * ln, a.gain, &table[warp][turn ? 8 * ln : 0]);
         uint8_t *b = block + h * head_bytes;
-        *reinterpret_cast<uint32_t *>(b + kv4_k_word(D, r, q0)) = w.x;
-        *reinterpret_cast<uint32_t *>(b + kv4_k_word(D, r, q1)) = w.y;
-        if (ln == 0) *reinterpret_cast<uint32_t *>(b + kv4_ks_off(D) + 4 * r) = w.z;
-    }
-    for (; again_v; again_v &= again_v - 1) {
-        const int h = (w0 + __ffs(again_v) - 1) * PER + hl;
-        const T *p = v_base + h * a.vs_head;
-        const uint3 w = hold_exactly<T, D, VEC, INTER>(p, v0, v1, false, false, pos, a.turns, a.gain,
-                                                       &table[warp][0]);
-        uint8_t *b = block + h * head_bytes;
-        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, v0)) = w.x;
-        *reinterpret_cast<uint32_t *>(b + kv4_v_word(D, r, v1)) = w.y;
-        if (ln == 0) *reinterpret_cast<uint32_t *>(b + kv4_vs_off(D) + 4 * r) = w.z;
+        *reinterpret_cast<uint32_t *>(b + (k ? kw0 : vw0)) = w.x;
+        *reinterpret_cast<uint32_t *>(b + (k ? kw1 : vw1)) = w.y;
+        if (ln == 0) *reinterpret_cast<uint32_t *>(b + (k ? kv4_ks_off(D) : kv4_vs_off(D)) + 4 * r) = w.z;
     }
 }
 
@@ -542,7 +530,7 @@ struct GatherArgs {
 // Bound by HBM: D/2 + 4 bytes read and D elements written a vector.  A group of D/8
 // lanes takes a (token, head) item, 8 values of K and 8 of V a lane: a word read and a
 // 16-byte vector written each, contiguous over the lanes (16 values a lane wrote every
-// other 16 bytes at a time: 14.9 against GATHERUS us for 8192 tokens of 8 heads).  A
+// other 16 bytes at a time: 14.9 against 12.4 us for 8192 tokens of 8 heads of 128).  A
 // thread asks for all of its items' words before it works on the first.
 constexpr int kGatherItems = 4;
 
