@@ -45,20 +45,13 @@
 // go in as two fp16 parts each (22 bits).
 #include <atomic>
 
-#include "tm_host.h"
-
-#include "tm_elem.cuh"
-#include "tm_kv4.cuh"
+#include "tm_kv4_attn.cuh"
 
 namespace libtm {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTile = 32;    // tokens a warp takes at a time: two cache blocks
-// p goes up to 2^kSlack, p stepV 2^E up to 2^kSlack 2^(kStepBits + 3) <= 2^15
-constexpr int kSlack = 8, kStepBits = 4;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLog2eF = 1.4426950408889634f;
+constexpr int kWarps = 4;              // a warp takes tiles of kTile tokens
+static_assert(kUnit % (kWarps * kTile) == 0, "a unit is whole tiles of every warp");
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
@@ -73,111 +66,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ float2 half2_at(const uint8_t *p)
-{
-    return __half22float2(*reinterpret_cast<const __half2 *>(p));
-}
-
-// The codes of two nibbles 16 bits apart as an fp16 pair, from the low nibble
-// position (even dims of a word) or the next one (odd dims).
-// Plain: the bits as they are, subnormal fp16: c 2^-24, or c 2^-20.
-__device__ __forceinline__ uint32_t plain_even(uint32_t x) { return x & 0x000f000fu; }
-__device__ __forceinline__ uint32_t plain_odd(uint32_t x) { return x & 0x00f000f0u; }
-
-// Centred: c - 8, or 16 (c - 8), normal numbers: the nibble joins the low bits of
-// 1024 and the subtraction is exact.  `bias` holds 1024 twice and comes from the
-// launch's arguments: as a constant it would share the one immediate an instruction
-// has with the mask, and cost an instruction more for each pair.
-__device__ __forceinline__ uint32_t centred(uint32_t x, uint16_t middle)
-{
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), __halves2half2(__ushort_as_half(middle), __ushort_as_half(middle)));
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t centred_even(uint32_t x, uint32_t bias) { return centred((x & 0x000f000fu) | bias, 0x6408); }  // 1032
-__device__ __forceinline__ uint32_t centred_odd(uint32_t x, uint32_t bias) { return centred((x & 0x00f000f0u) | bias, 0x6480); }   // 1152
-
-constexpr int kUnit = 256;             // tokens: two tiles a warp
-static_assert(kUnit % (kWarps * kTile) == 0, "a unit is whole tiles of every warp");
-constexpr int kMostBlocks = 608;       // 152 SMs x 4: what the workspace is sized for
-
-struct AttnArgs {
-    const void *Q;
-    void *O;
-    float *lse;
-    const uint8_t *pool;
-    const int32_t *table, *lens, *qstart;
-    float *part;      // [2 gridDim.x] slots of [ROWS][D] outputs and [ROWS][2] (maximum, sum)
-    int2 *job;        // [B][Hkv][row_tiles]: the first block an item lies in, and how many; or NULL
-    int64_t qs_tok, qs_head, os_tok, os_head, pages, page_bytes, ldt, Tq, max_len;
-    int B, Hq, Hkv, G, window, full, vec, max_q, blocks_per_page, row_tiles;
-    uint32_t bias;  // 1024 in both halves of an fp16 pair
-    float scale;
-    FastDiv by_page, by_group;  // cache blocks of a page, heads of a group
-    unsigned *status;
-};
-
-// What a sequence's queries are: their first row of Q, their count and the
-// cache's length, checked against the call's bounds.
-struct Seq {
-    int q0, n, len;
-};
-
-__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b, bool report)
-{
-    Seq s;
-    int q1;
-    if (a.qstart) {
-        s.q0 = a.qstart[b];
-        q1 = a.qstart[b + 1];
-    } else {
-        s.q0 = b;
-        q1 = b + 1;
-    }
-    s.len = a.lens[b];
-    if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || q1 - s.q0 > a.max_q || s.len < 0 || s.len > a.max_len) {
-        if (report) atomicOr(a.status, kStatusIndex);
-        s.n = 0;
-        s.len = 0;
-        return s;
-    }
-    s.n = q1 - s.q0;
-    return s;
-}
-
-// Keys a query at place t of its sequence sees: [lower, upper).
-__device__ __forceinline__ int upper(const AttnArgs &a, const Seq &s, int t)
-{
-    return a.full ? s.len : min(s.len, max(0, s.len - s.n + t + 1));
-}
-__device__ __forceinline__ int lower(const AttnArgs &a, const Seq &s, int t)
-{
-    return a.window > 0 ? max(0, s.len - s.n + t + 1 - a.window) : 0;
-}
-
-// Row tiles of a sequence, and the units each of its items counts (one at
-// least: an item that sees nothing still has its zeros to write).  With a
-// window every row tile counts as many units as the widest could need.
-struct Load {
-    int tiles, units;
-    __device__ __forceinline__ int total(int Hkv) const { return tiles * units * Hkv; }  // the host bounds the sum
-};
-
-__device__ __forceinline__ Load load_of(const AttnArgs &a, const Seq &s, int rows_of_tile)
-{
-    Load l;
-    l.tiles = (s.n * a.G + rows_of_tile - 1) / rows_of_tile;
-    int range = s.len;
-    if (a.window > 0) range = min(range, a.window + rows_of_tile / a.G + 1 + kTile);
-    l.units = max(1, (range + kUnit - 1) / kUnit);
-    return l;
 }
 
 template <int D>
@@ -235,51 +123,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
 
-    // ---- this block's run of units: [pos, stop), starting in sequence b, whose units
-    // start at base.  Every warp adds the sequences up for itself, 32 at a time.
-    int pos, stop, share, base = 0, b = 0;
-    Seq seq;
-    Load load;
-    {
-        auto lane_load = [&](int i, bool report, Seq &q) {
-            q = {0, 0, 0};
-            if (i < a.B) q = sequence(a, i, report);
-            return load_of(a, q, ROWS).total(a.Hkv);
-        };
-        int all = 0, mine = 0;
-        Seq q;
-        for (int b0 = 0; b0 < a.B; b0 += 32) all += mine = lane_load(b0 + lane, blockIdx.x == 0 && warp == 0, q);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        share = (all + (int)gridDim.x - 1) / (int)gridDim.x;
-        pos = min(share * (int)blockIdx.x, all);
-        stop = min(all, pos + share);
-        if (pos >= stop) {
-            pdl_wait();
-            return;
-        }
-        int before = 0;
-        for (;; b += 32) {
-            if (a.B > 32) mine = lane_load(b + lane, false, q);
-            int inc = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += x;
-            }
-            const int sum = __shfl_sync(0xffffffffu, inc, 31);
-            if (pos < before + sum) {
-                const int at = __ffs(__ballot_sync(0xffffffffu, pos < before + inc)) - 1;
-                b += at;
-                base = before + __shfl_sync(0xffffffffu, inc - mine, at);
-                seq.q0 = __shfl_sync(0xffffffffu, q.q0, at);
-                seq.n = __shfl_sync(0xffffffffu, q.n, at);
-                seq.len = __shfl_sync(0xffffffffu, q.len, at);
-                break;
-            }
-            before += sum;
-        }
-        load = load_of(a, seq, ROWS);
+    Run run;
+    if (!find_run(a, ROWS, warp == 0, run)) {
+        pdl_wait();
+        return;
     }
     const uint64_t policy = l2_evict_first_policy();
     const uint32_t bias = a.bias;
@@ -288,31 +135,18 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
     int fill = 0;        // stage of the next tile to copy
     bool alive = true;
 
-    while (pos < stop) {
-        // ---- the segment: units [unit0, unit0 + count) of an item
-        while (pos >= base + load.total(a.Hkv)) {
-            base += load.total(a.Hkv);
-            seq = sequence(a, ++b, false);
-            load = load_of(a, seq, ROWS);
-        }
-        const int item = (pos - base) / load.units, unit0 = pos - base - item * load.units;
-        const int kvh = item / load.tiles, tile = item - kvh * load.tiles;
-        const int count = min(load.units - unit0, stop - pos);
-        const bool whole = count == load.units;
-        // the blocks an item lies in, noted for the join by the block that ends it
-        if (a.job && unit0 + count == load.units && tid == 0) {
-            const int first = pos - unit0, c0 = first / share;
+    while (run.pos < run.stop) {
+        const Segment seg = next_segment(a, ROWS, run);
+        const Seq seq = run.seq;
+        const int kvh = seg.kvh, tile = seg.tile, rows = seg.rows, end = seg.end, c0 = seg.c0, b = run.b;
+        if (a.job && seg.last && tid == 0) {
             pdl_wait();
-            a.job[((int64_t)b * a.Hkv + kvh) * a.row_tiles + tile] = make_int2(c0, (int)blockIdx.x - c0 + 1);
+            note_job(a, run, seg);
         }
-        pos += count;
-        const int rows = min(ROWS, seq.n * a.G - tile * ROWS);
-        const int t_first = (int)fdiv(tile * ROWS, a.by_group), t_last = (int)fdiv(tile * ROWS + rows - 1, a.by_group);
-        const int begin = lower(a, seq, t_first) / kTile * kTile, end = upper(a, seq, t_last);
-        const int c0 = min(end, begin + unit0 * kUnit);
-        const int c1 = unit0 + count == load.units ? end : min(end, c0 + count * kUnit);
+        run.pos += seg.count;
         // Where every row of the tile sees every token: [safe0, safe1).
-        const int safe0 = lower(a, seq, t_last), safe1 = upper(a, seq, t_first);
+        const int safe0 = lower(a, seq, (int)fdiv(tile * ROWS + rows - 1, a.by_group));
+        const int safe1 = upper(a, seq, (int)fdiv(tile * ROWS, a.by_group));
 
         // ---- this lane's queries, asked for before the copies' page numbers
         Vec<T, 8> raw[NT][LD / 8];
@@ -338,7 +172,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         // ---- the copies: this warp's tiles are warp, warp + 4, ... of the segment.  Of each
         // 32 tiles a lane works out one's source (two blocks, which can lie in two
         // pages) and copies it when its turn comes.
-        const int tiles = (c1 - c0 + kTile - 1) / kTile;
+        const int tiles = (seg.c1 - c0 + kTile - 1) / kTile;
         const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
         const int32_t *trow = a.table + (int64_t)b * a.ldt;
         const uint8_t *src0 = nullptr, *src1 = nullptr;
@@ -759,9 +593,9 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
             }
             // dims of this part: 2 KP of every slice of 2 KS
             const int d = d2 / (2 * KP) * (2 * KS) + ps * 2 * KP + d2 % (2 * KP);
-            if (!whole) {
+            if (!seg.whole) {
                 // the first segment of a block starts inside an item or is slot 1's like any other
-                float *slot = a.part + (2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0)) * (ROWS * (D + 2));
+                float *slot = a.part + (2 * (int64_t)blockIdx.x + (seg.unit0 == 0 ? 1 : 0)) * (ROWS * (D + 2));
                 *reinterpret_cast<float2 *>(slot + row * D + d) = make_float2(v0, v1);
                 if (d == 0) *reinterpret_cast<float2 *>(slot + ROWS * D + row * 2) = make_float2(mm, ll);
             } else {
@@ -891,12 +725,22 @@ int pick_nt(int64_t rows, int D, bool f32)
     return rows > 8 && D != 256 && !f32 ? 2 : 1;
 }
 
-// Bytes of the partial slots and of the items' jobs, for any element type.
+// Bytes of the partial slots and of the items' jobs.  For any element type: the most.
 size_t attn_workspace(int32_t B, int32_t max_q, int32_t Hq, int32_t Hkv, int32_t D)
 {
     const int64_t rows = (int64_t)max_q * (Hq / Hkv);
-    const size_t slots = 2 * kMostBlocks * (size_t)(rows > 8 ? 16 : 8) * (D + 2) * sizeof(float);
+    size_t slots = 2 * kMostBlocks * (size_t)(rows > 8 ? 16 : 8) * (D + 2) * sizeof(float);
+    if (chunk_attn_fits(TM_BF16, rows, D) && chunk_attn_slots_bytes(D) > slots) slots = chunk_attn_slots_bytes(D);
     return slots + (size_t)B * Hkv * ((size_t)rows + 7) / 8 * sizeof(int2);
+}
+
+template <typename T, int D>
+tm_status join_items(AttnArgs &a, int rows_of_tile, int W, cudaStream_t s)
+{
+    const int64_t items = (int64_t)a.B * a.Hkv * a.row_tiles;
+    void *jargs[] = {(void *)&a, &rows_of_tile, &W};
+    return launch_dependent((const void *)kv4_join_kernel<T, D>, dim3((unsigned)(items * rows_of_tile / (8 / W))),
+                            dim3(256), jargs, 0, s);
 }
 
 template <typename T, int D, int NT>
@@ -916,11 +760,7 @@ tm_status launch_attn(AttnArgs &a, int dev, int sms, bool join, cudaStream_t s, 
     void *args[] = {(void *)&a};
     tm_status st = launch_kernel(k, dim3((unsigned)blocks), dim3(kWarps * 32), args, attn_smem<D>(), s, pdl);
     if (st != TM_OK || !join) return st;
-    const int64_t items = (int64_t)a.B * a.Hkv * a.row_tiles;
-    int rows_of_tile = NT * 8, W = items >= sms ? 1 : 8;
-    void *jargs[] = {(void *)&a, &rows_of_tile, &W};
-    return launch_dependent((const void *)kv4_join_kernel<T, D>, dim3((unsigned)(items * rows_of_tile / (8 / W))),
-                            dim3(256), jargs, 0, s);
+    return join_items<T, D>(a, NT * 8, (int64_t)a.B * a.Hkv * a.row_tiles >= sms ? 1 : 8, s);
 }
 
 template <typename T>
@@ -943,6 +783,14 @@ bool attn_shape_ok(int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_
 }
 
 }  // namespace
+
+tm_status launch_attn_join(int D, int32_t xtype, AttnArgs &a, int rows_of_tile, int W, cudaStream_t s)
+{
+    if (xtype == TM_F16) return D == 64 ? join_items<__half, 64>(a, rows_of_tile, W, s) : join_items<__half, 128>(a, rows_of_tile, W, s);
+    return D == 64 ? join_items<__nv_bfloat16, 64>(a, rows_of_tile, W, s)
+                   : join_items<__nv_bfloat16, 128>(a, rows_of_tile, W, s);
+}
+
 }  // namespace libtm
 
 using namespace libtm;
@@ -988,10 +836,12 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     for (const Span &s : ins)
         if (meets(so, s) || meets(sl, s) || meets(sw, s)) return TM_ERR_INVALID_ARG;
     if (meets(so, sl) || meets(so, sw) || meets(sl, sw)) return TM_ERR_INVALID_ARG;
-    const int nt = pick_nt((int64_t)max_q * (Hq / Hkv), D, e == 4);
-    const int64_t row_tiles = ((int64_t)max_q * (Hq / Hkv) + nt * 8 - 1) / (nt * 8);
+    const int64_t most_rows = (int64_t)max_q * (Hq / Hkv);
+    const bool chunk = chunk_attn_fits(xtype, most_rows, D);
+    const int nt = pick_nt(most_rows, D, e == 4), rows_of_tile = chunk ? kChunkRows : nt * 8;
+    const int64_t row_tiles = (most_rows + rows_of_tile - 1) / rows_of_tile;
     // the units of all items, and the join's grid, fit 31 bits (with room for a block's share)
-    if (row_tiles > (1 << 30) / 16 / ((int64_t)B * Hkv) ||
+    if (row_tiles > (1 << 30) / rows_of_tile / ((int64_t)B * Hkv) ||
         (max_len / kUnit + 2) > (1 << 30) / ((int64_t)B * Hkv * row_tiles))
         return TM_ERR_INVALID_ARG;
     const DevInfo *dev;
@@ -1006,7 +856,10 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.lens = lens;
     a.qstart = qstart;
     a.part = reinterpret_cast<float *>(workspace);
-    a.job = join ? reinterpret_cast<int2 *>(a.part + 2 * (size_t)kMostBlocks * nt * 8 * (D + 2)) : nullptr;
+    a.job = join ? reinterpret_cast<int2 *>(reinterpret_cast<char *>(workspace) +
+                                           (chunk ? chunk_attn_slots_bytes(D)
+                                                  : 2 * (size_t)kMostBlocks * nt * 8 * (D + 2) * sizeof(float)))
+                 : nullptr;
     a.qs_tok = qs_tok;
     a.qs_head = qs_head;
     a.os_tok = os_tok;
@@ -1038,6 +891,7 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     }
     cudaStream_t s = as_stream(stream);
     const bool pdl = (flags & TM_PDL) != 0;
+    if (chunk) return launch_chunk_attn(D, xtype, a, device, dev->sms, join, s, pdl);
     return xtype == TM_F32   ? launch_attn<float>(D, nt, a, device, dev->sms, join, s, pdl)
            : xtype == TM_F16 ? launch_attn<__half>(D, nt, a, device, dev->sms, join, s, pdl)
                              : launch_attn<__nv_bfloat16>(D, nt, a, device, dev->sms, join, s, pdl);

@@ -1,0 +1,221 @@
+// tm_kv4_attn.cuh -- what the two attention kernels over the 4-bit cache share:
+// the codes' fp16 forms, the call's arguments, and how the work is cut and found.
+#pragma once
+
+#include "tm_host.h"
+
+#include "tm_elem.cuh"
+#include "tm_kv4.cuh"
+
+namespace libtm {
+
+constexpr int kTile = 32;    // tokens: first tokens of a row tile are rounded down to it
+// p goes up to 2^kSlack, p stepV 2^E up to 2^kSlack 2^(kStepBits + 3) <= 2^15
+constexpr int kSlack = 8, kStepBits = 4;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2eF = 1.4426950408889634f;
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 half2_at(const uint8_t *p)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(p));
+}
+
+// The codes of two nibbles 16 bits apart as an fp16 pair, from the low nibble
+// position (even dims of a word) or the next one (odd dims).
+// Plain: the bits as they are, subnormal fp16: c 2^-24, or c 2^-20.
+__device__ __forceinline__ uint32_t plain_even(uint32_t x) { return x & 0x000f000fu; }
+__device__ __forceinline__ uint32_t plain_odd(uint32_t x) { return x & 0x00f000f0u; }
+
+// Centred: c - 8, or 16 (c - 8), normal numbers: the nibble joins the low bits of
+// 1024 and the subtraction is exact.  `bias` holds 1024 twice and comes from the
+// launch's arguments: as a constant it would share the one immediate an instruction
+// has with the mask, and cost an instruction more for each pair.
+__device__ __forceinline__ uint32_t centred(uint32_t x, uint16_t middle)
+{
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), __halves2half2(__ushort_as_half(middle), __ushort_as_half(middle)));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t centred_even(uint32_t x, uint32_t bias) { return centred((x & 0x000f000fu) | bias, 0x6408); }  // 1032
+__device__ __forceinline__ uint32_t centred_odd(uint32_t x, uint32_t bias) { return centred((x & 0x00f000f0u) | bias, 0x6480); }   // 1152
+
+constexpr int kUnit = 256;             // tokens
+constexpr int kMostBlocks = 608;       // 152 SMs x 4: what the workspace is sized for
+
+struct AttnArgs {
+    const void *Q;
+    void *O;
+    float *lse;
+    const uint8_t *pool;
+    const int32_t *table, *lens, *qstart;
+    float *part;      // [2 gridDim.x] slots of [ROWS][D] outputs and [ROWS][2] (maximum, sum)
+    int2 *job;        // [B][Hkv][row_tiles]: the first block an item lies in, and how many; or NULL
+    int64_t qs_tok, qs_head, os_tok, os_head, pages, page_bytes, ldt, Tq, max_len;
+    int B, Hq, Hkv, G, window, full, vec, max_q, blocks_per_page, row_tiles;
+    uint32_t bias;  // 1024 in both halves of an fp16 pair
+    float scale;
+    FastDiv by_page, by_group;  // cache blocks of a page, heads of a group
+    unsigned *status;
+};
+
+// What a sequence's queries are: their first row of Q, their count and the
+// cache's length, checked against the call's bounds.
+struct Seq {
+    int q0, n, len;
+};
+
+__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b, bool report)
+{
+    Seq s;
+    int q1;
+    if (a.qstart) {
+        s.q0 = a.qstart[b];
+        q1 = a.qstart[b + 1];
+    } else {
+        s.q0 = b;
+        q1 = b + 1;
+    }
+    s.len = a.lens[b];
+    if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || q1 - s.q0 > a.max_q || s.len < 0 || s.len > a.max_len) {
+        if (report) atomicOr(a.status, kStatusIndex);
+        s.n = 0;
+        s.len = 0;
+        return s;
+    }
+    s.n = q1 - s.q0;
+    return s;
+}
+
+// Keys a query at place t of its sequence sees: [lower, upper).
+__device__ __forceinline__ int upper(const AttnArgs &a, const Seq &s, int t)
+{
+    return a.full ? s.len : min(s.len, max(0, s.len - s.n + t + 1));
+}
+__device__ __forceinline__ int lower(const AttnArgs &a, const Seq &s, int t)
+{
+    return a.window > 0 ? max(0, s.len - s.n + t + 1 - a.window) : 0;
+}
+
+// Row tiles of a sequence, and the units each of its items counts (one at
+// least: an item that sees nothing still has its zeros to write).  With a
+// window every row tile counts as many units as the widest could need.
+struct Load {
+    int tiles, units;
+    __device__ __forceinline__ int total(int Hkv) const { return tiles * units * Hkv; }  // the host bounds the sum
+};
+
+__device__ __forceinline__ Load load_of(const AttnArgs &a, const Seq &s, int rows_of_tile)
+{
+    Load l;
+    l.tiles = (s.n * a.G + rows_of_tile - 1) / rows_of_tile;
+    int range = s.len;
+    if (a.window > 0) range = min(range, a.window + rows_of_tile / a.G + 1 + kTile);
+    l.units = max(1, (range + kUnit - 1) / kUnit);
+    return l;
+}
+
+// A block's run of units, [pos, stop) of all items' one after another; pos lies in
+// sequence b, whose units start at base.  `share` units a block.
+struct Run {
+    int pos, stop, share, base, b;
+    Seq seq;
+    Load load;
+};
+
+// Called by whole warps, each for itself: sequences are added up 32 at a time.
+// False if the block has nothing to do.
+__device__ __forceinline__ bool find_run(const AttnArgs &a, int rows_of_tile, bool report, Run &r)
+{
+    const int lane = threadIdx.x & 31;
+    auto lane_load = [&](int i, bool say, Seq &q) {
+        q = {0, 0, 0};
+        if (i < a.B) q = sequence(a, i, say);
+        return load_of(a, q, rows_of_tile).total(a.Hkv);
+    };
+    int all = 0, mine = 0;
+    Seq q;
+    for (int b0 = 0; b0 < a.B; b0 += 32) all += mine = lane_load(b0 + lane, report && blockIdx.x == 0, q);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    r.share = (all + (int)gridDim.x - 1) / (int)gridDim.x;
+    r.pos = min(r.share * (int)blockIdx.x, all);
+    r.stop = min(all, r.pos + r.share);
+    if (r.pos >= r.stop) return false;
+    int before = 0;
+    for (r.b = 0;; r.b += 32) {
+        if (a.B > 32) mine = lane_load(r.b + lane, false, q);
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        const int sum = __shfl_sync(0xffffffffu, inc, 31);
+        if (r.pos < before + sum) {
+            const int at = __ffs(__ballot_sync(0xffffffffu, r.pos < before + inc)) - 1;
+            r.b += at;
+            r.base = before + __shfl_sync(0xffffffffu, inc - mine, at);
+            r.seq.q0 = __shfl_sync(0xffffffffu, q.q0, at);
+            r.seq.n = __shfl_sync(0xffffffffu, q.n, at);
+            r.seq.len = __shfl_sync(0xffffffffu, q.len, at);
+            break;
+        }
+        before += sum;
+    }
+    r.load = load_of(a, r.seq, rows_of_tile);
+    return true;
+}
+
+// A segment of the run: units [unit0, unit0 + count) of an item, its tokens [c0, c1).
+struct Segment {
+    int unit0, count, kvh, tile, rows, begin, end, c0, c1;
+    bool whole, last;  // the whole item; its last unit among them
+};
+
+__device__ __forceinline__ Segment next_segment(const AttnArgs &a, int rows_of_tile, Run &r)
+{
+    while (r.pos >= r.base + r.load.total(a.Hkv)) {
+        r.base += r.load.total(a.Hkv);
+        r.seq = sequence(a, ++r.b, false);
+        r.load = load_of(a, r.seq, rows_of_tile);
+    }
+    Segment s;
+    const int item = (r.pos - r.base) / r.load.units;
+    s.unit0 = r.pos - r.base - item * r.load.units;
+    s.kvh = item / r.load.tiles;
+    s.tile = item - s.kvh * r.load.tiles;
+    s.count = min(r.load.units - s.unit0, r.stop - r.pos);
+    s.whole = s.count == r.load.units;
+    s.last = s.unit0 + s.count == r.load.units;
+    s.rows = min(rows_of_tile, r.seq.n * a.G - s.tile * rows_of_tile);
+    const int first = s.tile * rows_of_tile;
+    s.begin = lower(a, r.seq, (int)fdiv(first, a.by_group)) / kTile * kTile;
+    s.end = upper(a, r.seq, (int)fdiv(first + s.rows - 1, a.by_group));
+    s.c0 = min(s.end, s.begin + s.unit0 * kUnit);
+    s.c1 = s.last ? s.end : min(s.end, s.c0 + s.count * kUnit);
+    return s;
+}
+
+// The blocks an item lies in, noted for the join by the block that ends it (call it
+// before the run moves on).
+__device__ __forceinline__ void note_job(const AttnArgs &a, const Run &r, const Segment &s)
+{
+    const int c0 = (r.pos - s.unit0) / r.share;
+    a.job[((int64_t)r.b * a.Hkv + s.kvh) * a.row_tiles + s.tile] = make_int2(c0, (int)blockIdx.x - c0 + 1);
+}
+
+// The kernel for many query rows (tm_kv4_chunk.cu).
+tm_status launch_chunk_attn(int D, int32_t xtype, AttnArgs &a, int device, int sms, bool join, cudaStream_t s, bool pdl);
+bool chunk_attn_fits(int32_t xtype, int64_t rows, int D);
+size_t chunk_attn_slots_bytes(int D);
+constexpr int kChunkRows = 256;  // its row tile
+
+// The join of partial outputs (tm_kv4_attn.cu).
+tm_status launch_attn_join(int D, int32_t xtype, AttnArgs &a, int rows_of_tile, int W, cudaStream_t s);
+
+}  // namespace libtm

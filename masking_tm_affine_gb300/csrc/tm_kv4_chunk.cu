@@ -1,0 +1,735 @@
+// tm_kv4_chunk.cu -- attention over the 4-bit cache for many query rows (the chunks
+// of a prompt): the same mathematics as tm_kv4_attn.cu, on tcgen05.
+//
+// Bound by the tensor cores and, as closely, by the exponentials: 4 D flops and one
+// exponential for each (query row, token).  An item's row tile is 256 rows (queries x
+// the heads that share a KV head), two halves of 128, walked over 128 tokens at a time:
+//
+//   loader warp      bulk copies of the tile's eight cache blocks
+//   2 unpack warps   codes -> fp16 c - 8 in shared memory, K and V once for both halves;
+//                    the tokens' (step, low) as floats
+//   MMA thread       S = Q K^T   [128 rows, 128 tokens], both operands in shared memory
+//                    O += P V    [128 rows, D], P from tensor memory, 64 tokens at a time
+//   2 x 4 warps      a half each, a thread a row: S from tensor memory, softmax, P back
+//                    into the columns S came from; while one half is at it, the tensor
+//                    cores run the other's products
+//
+// Shared memory: Q and K are K-major, V is MN-major (a token's dims contiguous), all in
+// 128-byte swizzled panels of 64 dims; a word's eight dims lie in the order 0 4 1 5 2 6
+// 3 7, the order its nibbles come in (Q is written in the same order, O is read back
+// in it).  Tensor memory: S of both halves in columns 0 .. 255, O in 256 .. 511.
+//
+// A thread has a whole row, so its maximum and sums need no exchange.  The reference
+// maximum moves only where a logit passes it by 2^8 and the steps' exponent only past
+// a power of two well above it: O is then scaled in tensor memory, which almost
+// never happens after a segment's first tile.
+//
+// Every wait is bounded.  One that runs out sets the abort flag, which every role
+// looks at; outstanding copies and products are waited for before the block ends.
+#include <atomic>
+
+#include "tm_kv4_attn.cuh"
+
+namespace libtm {
+namespace {
+
+constexpr int kTok = 128;            // tokens of a tile
+constexpr int kHalf = 64;            // tokens of one step of the second product
+constexpr int kUnpackWarps = 2;
+constexpr int kThreads2 = 12 * 32;   // warps 0-7 softmax, 8-9 unpack, 10 MMA, 11 loader: 168 registers a thread
+constexpr int kRawStages = 2, kOpStages = 3, kParStages = 2;
+
+template <int D>
+struct ChunkSmem {
+    alignas(1024) uint8_t q[2][D / 64][128 * 128];           // [half][panel]: 128 rows of 128 bytes
+    alignas(1024) uint8_t op[kOpStages][D / 64 * 128 * 128];  // K tiles: panels as Q; V tiles: [8 tokens][panel]
+    alignas(128) uint8_t raw[kRawStages][kTok / 16 * kv4_block_bytes(D)];
+    alignas(16) float2 kpar[kParStages][kTok], vpar[kParStages][kTok];  // (step, low) of K; (step 2^E, low) of V
+    float unit, top[8];
+    int vexp[kParStages];
+    alignas(8) uint64_t raw_full[kRawStages], raw_free[kRawStages], op_full[kOpStages], op_free[kOpStages],
+        par_full[kParStages], par_free[kParStages], top_full, q_full, unit_full, s_full[2], p_full[2][2], o_done[2][2], done;
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ void bar_init(uint64_t *b, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+
+// Wait for a phase; false after the limit, or once any role has given up.
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *abort, unsigned *status)
+{
+    const uint32_t at = smem_u32(b);
+    if (mbar_try_wait(at, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(at, parity)) {
+        if (*abort) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *abort = 1;
+            atomicOr(status, kStatusTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+// A counter of a ring's uses: stage and the parity of its next completion.
+struct Turn {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t stages)
+    {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Shared-memory descriptors, 128-byte swizzle (layout 2), version 1.  K-major: groups
+// of 8 rows 1024 bytes apart.  MN-major: panels of 64 columns `panel` bytes apart,
+// groups of 8 rows of the other extent `group` bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t at)
+{
+    return (uint64_t)((at >> 4) & 0x3FFF) | (1ull << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t panel, uint32_t group)
+{
+    return (uint64_t)((at >> 4) & 0x3FFF) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(group >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+// Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B fp16 (0), B
+// MN-major (bit 16), N >> 3 at bit 17, M >> 4 at bit 24.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
+{
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t id, bool acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(id), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t db, uint32_t id, bool acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(db), "r"(id), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *b)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b))
+                 : "memory");
+}
+
+// 32 columns of this warp's 32 rows, a row a lane.
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Eight codes of a word as c - 8 in fp16, in the order 0 4 1 5 2 6 3 7.  Even
+// nibbles: 1024 + c less 1032; odd ones: (1024 + 16 c) / 16 less 72.  Exact.
+__device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t bias)
+{
+    const __half2 e0 = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));  // 1032
+    const __half2 sx = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));  // 1/16
+    const __half2 o0 = __halves2half2(__ushort_as_half(0xd480), __ushort_as_half(0xd480));  // -72
+    const uint32_t v = w >> 8;
+    const uint32_t a = (w & 0x000f000fu) | bias, b = (w & 0x00f000f0u) | bias;
+    const uint32_t c = (v & 0x000f000fu) | bias, d = (v & 0x00f000f0u) | bias;
+    const __half2 ha = __hsub2(*reinterpret_cast<const __half2 *>(&a), e0), hb = __hfma2(*reinterpret_cast<const __half2 *>(&b), sx, o0);
+    const __half2 hc = __hsub2(*reinterpret_cast<const __half2 *>(&c), e0), hd = __hfma2(*reinterpret_cast<const __half2 *>(&d), sx, o0);
+    return make_uint4(*reinterpret_cast<const uint32_t *>(&ha), *reinterpret_cast<const uint32_t *>(&hb),
+                      *reinterpret_cast<const uint32_t *>(&hc), *reinterpret_cast<const uint32_t *>(&hd));
+}
+
+__device__ __forceinline__ void st_shared(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_constant__ AttnArgs a)
+{
+    constexpr int BB = kv4_block_bytes(D), PANELS = D / 64;
+    constexpr uint32_t kS = 0, kO = 256;  // first columns of S and O in tensor memory
+    extern __shared__ __align__(1024) unsigned char raw_smem[];
+    using Smem = ChunkSmem<D>;
+    Smem &s = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Run run;
+    const bool work = find_run(a, kChunkRows, warp == 0, run);
+    if (!work) {  // the same for every warp
+        pdl_wait();
+        return;
+    }
+    if (warp == 10) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRawStages; ++i) {
+            bar_init(&s.raw_full[i], 1);
+            bar_init(&s.raw_free[i], kUnpackWarps * 32);
+        }
+        for (int i = 0; i < kOpStages; ++i) {
+            bar_init(&s.op_full[i], kUnpackWarps * 32);
+            bar_init(&s.op_free[i], 1);
+        }
+        for (int i = 0; i < kParStages; ++i) {
+            bar_init(&s.par_full[i], kUnpackWarps * 32);
+            bar_init(&s.par_free[i], 256);
+        }
+        bar_init(&s.top_full, 256);
+        bar_init(&s.q_full, 256);
+        bar_init(&s.unit_full, 256);
+        // [half of the rows][half of a tile's tokens]: each completes once a tile, so the
+        // parity of the tile's number tells a completion from the one before
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&s.s_full[i], 1);
+            for (int h = 0; h < 2; ++h) {
+                bar_init(&s.p_full[i][h], 128);
+                bar_init(&s.o_done[i][h], 1);
+            }
+        }
+        bar_init(&s.done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s.abort = 0;
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s.tmem;
+    volatile int *abort = &s.abort;
+    auto wait = [&](uint64_t *b, uint32_t parity) { return bar_wait(b, parity, abort, a.status); };
+
+    if (warp == 11) {
+        // ---------------- loader: lane i copies block i of a tile
+        Turn raw;
+        uint32_t issued = 0;
+        bool ok = true;
+        while (ok && run.pos < run.stop) {
+            const Segment g = next_segment(a, kChunkRows, run);
+            const int32_t *trow = a.table + (int64_t)run.b * a.ldt;
+            run.pos += g.count;
+            for (int tok = g.c0; tok < g.c1; tok += kTok) {
+                const int blk = tok / 16 + lane;
+                const bool in = lane < kTok / 16 && blk * 16 < g.end;
+                int page = 0, at = 0;
+                if (in) {
+                    const int e = (int)fdiv(blk, a.by_page);
+                    at = blk - e * a.blocks_per_page;
+                    page = trow[e];
+                    if (page < 0 || page >= a.pages) {
+                        atomicOr(a.status, kStatusIndex);
+                        page = 0;
+                    }
+                }
+                const unsigned who = __ballot_sync(0xffffffffu, in);
+                if (issued >= kRawStages && !wait(&s.raw_free[raw.stage], raw.phase ^ 1)) ok = false;
+                ok = __all_sync(0xffffffffu, ok) && !*abort;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&s.raw_full[raw.stage]);
+                if (lane == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                                 "r"((uint32_t)__popc(who) * BB)
+                                 : "memory");
+                __syncwarp();
+                if (in)
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                            smem_u32(s.raw[raw.stage]) + lane * BB),
+                        "l"(a.pool + page * a.page_bytes + ((int64_t)g.kvh * a.blocks_per_page + at) * BB), "r"(BB), "r"(bar)
+                        : "memory");
+                raw.next(kRawStages);
+                ++issued;
+            }
+        }
+        // nothing may still be landing when the block leaves
+        const uint32_t first = issued > kRawStages ? issued - kRawStages : 0;
+        for (uint32_t i = first; i < issued; ++i)
+            mbar_wait_bounded(smem_u32(&s.raw_full[i % kRawStages]), (i / kRawStages) & 1);
+    } else if (warp == 10) {
+        if (lane == 0) {
+            // ---------------- MMA issuer
+            constexpr uint32_t id_s = idesc_f16(128, kTok, false), id_o = idesc_f16(128, D, true);
+            Turn op;
+            uint32_t segs = 0, count = 0;  // segments with tokens, tiles
+            bool ok = true;
+            auto score = [&](int half, uint32_t stage) {
+                const uint32_t q = smem_u32(s.q[half][0]), k = smem_u32(s.op[stage]);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    mma_ss(tmem + kS + 128 * half, desc_k(q + (i / 4) * 16384 + (i % 4) * 32),
+                           desc_k(k + (i / 4) * 16384 + (i % 4) * 32), id_s, i > 0);
+                commit(&s.s_full[half]);
+            };
+            while (ok && run.pos < run.stop) {
+                const Segment g = next_segment(a, kChunkRows, run);
+                run.pos += g.count;
+                const int tiles = (g.c1 - g.c0 + kTok - 1) / kTok;
+                if (tiles == 0) continue;
+                if (!wait(&s.q_full, segs & 1)) break;
+                ++segs;
+                ok = wait(&s.op_full[op.stage], op.phase);
+                if (!ok) break;
+                fence_after();
+                score(0, op.stage);
+                score(1, op.stage);
+                commit(&s.op_free[op.stage]);
+                op.next(kOpStages);
+                for (int t = 0; ok && t < tiles; ++t, ++count) {
+                    const Turn v = op;
+                    op.next(kOpStages);
+                    const Turn k = op;  // the next tile's K
+                    for (int h = 0; ok && h < 2; ++h)
+                        for (int i = 0; ok && i < 2; ++i) {
+                            if (h == 0 && i == 0) ok = wait(&s.op_full[v.stage], v.phase);
+                            ok = ok && wait(&s.p_full[i][h], count & 1);
+                            if (!ok) break;
+                            fence_after();
+                            const uint32_t vs = smem_u32(s.op[v.stage]) + h * (kHalf / 8) * PANELS * 1024;
+#pragma unroll
+                            for (int x = 0; x < kHalf / 16; ++x)
+                                mma_ts(tmem + kO + 128 * i, tmem + kS + 128 * i + 32 * h + 8 * x,
+                                       desc_mn(vs + x * 2 * PANELS * 1024, 1024, PANELS * 1024), id_o, t > 0 || h > 0 || x > 0);
+                            commit(&s.o_done[i][h]);
+                            if (h == 1 && i == 1) commit(&s.op_free[v.stage]);
+                            if (h == 1 && t + 1 < tiles) {
+                                // S goes where this P came from: after the product that reads it
+                                if (i == 0) ok = wait(&s.op_full[k.stage], k.phase);
+                                ok = ok && wait(&s.o_done[i][1], count & 1);
+                                if (!ok) break;
+                                fence_after();
+                                score(i, k.stage);
+                                if (i == 1) commit(&s.op_free[k.stage]);
+                            }
+                        }
+                    if (t + 1 < tiles) op.next(kOpStages);
+                }
+            }
+            commit(&s.done);  // every product issued, also after an abort
+            if (!mbar_wait_bounded(smem_u32(&s.done), 0)) {
+                *abort = 1;
+                atomicOr(a.status, kStatusTimeout);
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------- unpack
+        const int t = threadIdx.x - 256, w = warp - 8;
+        const uint32_t bias = a.bias;
+        Turn raw, op, par;
+        uint32_t ops = 0, pars = 0, segs = 0;
+        bool ok = true;
+        auto wait_all = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+        while (ok && run.pos < run.stop) {
+            const Segment g = next_segment(a, kChunkRows, run);
+            run.pos += g.count;
+            if (g.c1 <= g.c0) continue;
+            int vexp = 0;
+            float vcap = 0.0f;
+            ok = wait_all(&s.unit_full, segs & 1);
+            ++segs;
+            if (!ok) break;
+            const float unit = *(volatile float *)&s.unit;
+            for (int tok = g.c0; ok && tok < g.c1; tok += kTok) {
+                ok = wait_all(&s.raw_full[raw.stage], raw.phase);
+                if (!ok) break;
+                const uint8_t *src = s.raw[raw.stage];
+                // ---- scales
+                float vmax = 0.0f;  // of the tile, by every warp for itself
+#pragma unroll
+                for (int x = 0; x < kTok / 32; ++x) {
+                    const int tt = x * 32 + lane;
+                    const float step = half2_at(src + (tt / 16) * BB + kv4_vs_off(D) + 4 * (tt % 16)).x;
+                    if (tok + tt < g.end && step < INFINITY) vmax = fmaxf(vmax, step);
+                }
+                vmax = lanes_max(vmax, 32);
+                if (vmax >= vcap) {
+                    vexp = vmax > 0.0f ? (int)(__float_as_uint(vmax) >> 23) - 127 : -33;  // 2^e <= vmax < 2^(e+1)
+                    vcap = ldexpf(1.0f, vexp + 3);
+                }
+                if (pars >= kParStages) ok = wait_all(&s.par_free[par.stage], par.phase ^ 1);
+                if (!ok) break;
+                const float vscale = ldexpf(1.0f, kStepBits - vexp);
+#pragma unroll
+                for (int x = 0; x < kTok; x += kUnpackWarps * 32) {
+                    const int tt = x + t;
+                    const uint8_t *blk = src + (tt / 16) * BB;
+                    float2 kp = half2_at(blk + kv4_ks_off(D) + 4 * (tt % 16)), vp = half2_at(blk + kv4_vs_off(D) + 4 * (tt % 16));
+                    if (tok + tt >= g.end) kp = vp = make_float2(0.0f, 0.0f);  // (its bytes are whatever the ring held)
+                    kp.y = fmaf(8.0f, kp.x, kp.y);                             // codes count from 8
+                    vp.y = fmaf(8.0f, vp.x, vp.y);
+                    if (!(vp.x < INFINITY)) vp = make_float2(0.0f, NAN);
+                    s.kpar[par.stage][tt] = make_float2(kp.x * unit, kp.y * unit);
+                    s.vpar[par.stage][tt] = make_float2(vp.x * vscale, vp.y);
+                }
+                if (t == 0) s.vexp[par.stage] = vexp;
+                bar_arrive(&s.par_full[par.stage]);
+                par.next(kParStages);
+                ++pars;
+                // ---- K: a lane takes a quarter of a token's row (lanes of equal quarter together:
+                // their stores then fall on different banks)
+                if (ops >= kOpStages) ok = wait_all(&s.op_free[op.stage], op.phase ^ 1);
+                if (!ok) break;
+                uint32_t dst = smem_u32(s.op[op.stage]);
+                {
+                    const int j = lane >> 3, gr = lane & 7;
+                    constexpr int LW = D / 32;  // words of a quarter row
+#pragma unroll 2
+                    for (int i = 0; i < kTok / 8 / kUnpackWarps; ++i) {
+                        const int row = w * (kTok / kUnpackWarps) + i * 8 + gr;
+                        const uint8_t *p = src + (row / 16) * BB + (row % 16) * (D / 2) + j * (D / 8);
+                        uint32_t c[LW];
+                        if constexpr (LW == 4)
+                            *reinterpret_cast<uint4 *>(c) = *reinterpret_cast<const uint4 *>(p);
+                        else
+                            *reinterpret_cast<uint2 *>(c) = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+                        for (int x = 0; x < LW; ++x) {
+                            const int chunk = j * LW + x;  // of 8 dims
+                            st_shared(dst + (chunk / 8) * 16384 + row * 128 + ((chunk % 8) ^ (row & 7)) * 16, unpack8(c[x], bias));
+                        }
+                    }
+                }
+                fence_async();
+                bar_arrive(&s.op_full[op.stage]);
+                op.next(kOpStages);
+                ++ops;
+                // ---- V: a lane takes a slice (D/8 dims) of a token pair
+                if (ops >= kOpStages) ok = wait_all(&s.op_free[op.stage], op.phase ^ 1);
+                if (!ok) break;
+                dst = smem_u32(s.op[op.stage]);
+                {
+                    const int r = lane & 7, pr = lane >> 3;
+                    constexpr int LW = D / 64;  // words a token has in a slice
+#pragma unroll 2
+                    for (int i = 0; i < kTok / 8 / kUnpackWarps; ++i) {
+                        const int pair = w * (kTok / 2 / kUnpackWarps) + i * 4 + pr;  // of 64
+                        const uint8_t *p = src + (pair / 8) * BB + kv4_v_off(D) + (pair % 8) * D + r * (D / 8);
+                        uint32_t c[2 * LW];
+                        if constexpr (LW == 2)
+                            *reinterpret_cast<uint4 *>(c) = *reinterpret_cast<const uint4 *>(p);
+                        else
+                            *reinterpret_cast<uint2 *>(c) = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+                        for (int x = 0; x < 2 * LW; ++x) {
+                            const int token = 2 * pair + x / LW, chunk = r * LW + x % LW;
+                            st_shared(dst + (token / 8) * (PANELS * 1024) + (chunk / 8) * 1024 + (token % 8) * 128 +
+                                          ((chunk % 8) ^ (token % 8)) * 16,
+                                      unpack8(c[x], bias));
+                        }
+                    }
+                }
+                bar_arrive(&s.raw_free[raw.stage]);
+                raw.next(kRawStages);
+                fence_async();
+                bar_arrive(&s.op_full[op.stage]);
+                op.next(kOpStages);
+                ++ops;
+            }
+        }
+    } else {
+        // ---------------- softmax: half i, thread r of it has row 128 i + r of the tile
+        const int i = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kS + 128 * i, to = tmem + lanes + kO + 128 * i;
+        Turn par;
+        uint32_t count = 0, segs = 0;  // tiles, segments with tokens
+        bool ok = true;
+        while (ok && run.pos < run.stop) {
+            const Segment g = next_segment(a, kChunkRows, run);
+            const Seq seq = run.seq;
+            if (a.job && g.last && threadIdx.x == 0) {
+                pdl_wait();
+                note_job(a, run, g);
+            }
+            run.pos += g.count;
+            const int row = 128 * i + r, full_row = g.tile * kChunkRows + row;
+            const bool live = row < g.rows;
+            const int t = live ? (int)fdiv(full_row, a.by_group) : 0, hq = g.kvh * a.G + full_row - t * a.G;
+            // ---- Q: this row, scaled by a power of two common to the tile, into shared memory
+            const T *qp = reinterpret_cast<const T *>(a.Q) + (int64_t)(seq.q0 + t) * a.qs_tok + (int64_t)hq * a.qs_head;
+            Vec<T, 8> v[D / 8];
+            float top = 0.0f;
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x) {
+                if (!live) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[x].v[e] = from_f<T>(0.0f);
+                } else if (a.vec) {
+                    load_vec(qp + 8 * x, v[x]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[x].v[e] = qp[8 * x + e];
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(v[x].v[e])));
+            const bool any = g.c1 > g.c0;
+            float qsum = 0.0f;
+            if (any) {
+            top = lanes_max(top, 32);
+            if (lane == 0) s.top[warp] = top;
+            bar_arrive(&s.top_full);
+            ok = wait(&s.top_full, segs & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ++segs;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) top = fmaxf(top, s.top[x]);
+            const int qe = max(-100, min((int)(__float_as_uint(top) >> 23) - 127, 127));
+            const float up = ldexpf(1.0f, 14 - qe);
+            if (threadIdx.x == 0) s.unit = a.scale * kLog2eF * ldexpf(1.0f, qe - 14);
+            bar_arrive(&s.unit_full);
+            {
+                const uint32_t dst = smem_u32(s.q[i][0]) + r * 128;
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x) {
+                    float f[8];
+                    widen(v[x], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f[e] *= up;
+                        qsum += f[e];
+                    }
+                    st_shared(dst + (x / 8) * 16384 + ((x % 8) ^ (r & 7)) * 16,
+                              make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
+                                         pack_half2(f[3], f[7])));
+                }
+            }
+            fence_async();
+            bar_arrive(&s.q_full);
+            // (s.top is written again only after this segment's products, which need every
+            // thread to have come here)
+            }
+
+            // ---- this row's keys [lo, hi), and where all of this warp's rows see all
+            const int lo = live ? lower(a, seq, t) : 0, hi = live ? upper(a, seq, t) : g.c1;
+            const int safe0 = __reduce_max_sync(0xffffffffu, lo), safe1 = __reduce_min_sync(0xffffffffu, hi);
+            float m = -INFINITY, l = 0.0f, lowsum = 0.0f;
+            int vexp = 0;
+            bool first = true;
+            for (int tok = g.c0; ok && tok < g.c1; tok += kTok) {
+                ok = wait(&s.s_full[i], count & 1) && wait(&s.par_full[par.stage], par.phase);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                fence_after();
+                const float4 *kpar = reinterpret_cast<const float4 *>(s.kpar[par.stage]);
+                const float4 *vpar = reinterpret_cast<const float4 *>(s.vpar[par.stage]);
+                const int e_new = s.vexp[par.stage];
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t acc[kHalf];
+                    tmem_load(ts + kHalf * h, acc);
+                    tmem_load(ts + kHalf * h + 32, acc + 32);
+                    tmem_load_wait();
+                    float y[kHalf], top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 2) {
+                        const float4 kp = kpar[(kHalf * h + c) / 2];
+                        y[c] = fmaf(__uint_as_float(acc[c]), kp.x, kp.y * qsum);
+                        y[c + 1] = fmaf(__uint_as_float(acc[c + 1]), kp.z, kp.w * qsum);
+                    }
+                    const int t0 = tok + kHalf * h;
+                    const bool masked = t0 < safe0 || t0 + kHalf > safe1;
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < kHalf; ++c)
+                            if (t0 + c < lo || t0 + c >= hi) y[c] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 2) top = fmaxf(top, fmaxf(y[c], y[c + 1]));
+                    const bool grow = top > m + kSlack;
+                    if (__any_sync(0xffffffffu, grow) || e_new != vexp) {
+                        const float mn = fmaxf(m, top);
+                        const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        lowsum *= f;
+                        if (!first) {
+                            // O is this warp's once the last step handed over is done
+                            ok = h ? wait(&s.o_done[i][0], count & 1) : wait(&s.o_done[i][1], (count - 1) & 1);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            fence_after();
+                            const float move = f * ldexpf(1.0f, vexp - e_new);
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_load(to + c, o);
+                                tmem_load_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * move);
+                                tmem_store(to + c, o);
+                            }
+                            tmem_store_wait();
+                        }
+                        vexp = e_new;
+                    }
+                    first = false;
+                    const float ref = m == -INFINITY ? 0.0f : m;
+                    uint32_t p[kHalf / 2];
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 2) {
+                        const float4 vp = vpar[(kHalf * h + c) / 2];
+                        const float p0 = ex2(y[c] - ref), p1 = ex2(y[c + 1] - ref);
+                        l += p0 + p1;
+                        if (masked) {  // a low that is NaN joins only the rows that see its token
+                            if (y[c] != -INFINITY) lowsum = fmaf(p0, vp.y, lowsum);
+                            if (y[c + 1] != -INFINITY) lowsum = fmaf(p1, vp.w, lowsum);
+                        } else {
+                            lowsum = fmaf(p0, vp.y, lowsum);
+                            lowsum = fmaf(p1, vp.w, lowsum);
+                        }
+                        p[c / 2] = pack_half2(p0 * vp.x, p1 * vp.z);
+                    }
+                    tmem_store(ts + 32 * h, p);
+                    tmem_store_wait();
+                    fence_before();
+                    bar_arrive(&s.p_full[i][h]);
+                }
+                if (!ok) break;
+                bar_arrive(&s.par_free[par.stage]);
+                par.next(kParStages);
+                ++count;
+            }
+            // ---- the segment's end
+            pdl_wait();
+            if (ok && any) {
+                ok = wait(&s.o_done[i][1], (count - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                fence_after();
+            }
+            if (!ok) break;
+            const float back = ldexpf(1.0f, vexp - kStepBits), inv = l == 0.0f ? 0.0f : 1.0f / l;
+            float *slot = a.part + (2 * (int64_t)blockIdx.x + (g.unit0 == 0 ? 1 : 0)) * (kChunkRows * (D + 2));
+            T *out = reinterpret_cast<T *>(a.O) + (int64_t)(seq.q0 + t) * a.os_tok + (int64_t)hq * a.os_head;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                if (any) {
+                    tmem_load(to + c, o);
+                    tmem_load_wait();
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float f[8];  // columns come in the order 0 4 1 5 2 6 3 7 of a word's dims
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int d = (e & 1) * 4 + (e >> 1);
+                        f[d] = any ? fmaf(__uint_as_float(o[8 * x + e]), back, lowsum) : 0.0f;
+                    }
+                    if (!live) continue;
+                    if (!g.whole) {
+                        float4 *q = reinterpret_cast<float4 *>(slot + row * D + c + 8 * x);
+                        q[0] = make_float4(f[0], f[1], f[2], f[3]);
+                        q[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] *= inv;
+                        Vec<T, 8> vo;
+                        narrow(f, vo);
+                        if (a.vec) {
+                            store_vec(out + c + 8 * x, vo);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) out[c + 8 * x + e] = vo.v[e];
+                        }
+                    }
+                }
+            }
+            if (live && !g.whole) *reinterpret_cast<float2 *>(slot + kChunkRows * D + row * 2) = make_float2(m, l);
+            if (live && g.whole && a.lse)
+                a.lse[(int64_t)(seq.q0 + t) * a.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            fence_before();  // the reads of O, before the next segment's P lets products write it
+        }
+    }
+    pdl_wait();
+    fence_before();
+    __syncthreads();
+    if (warp == 10) {
+        __syncwarp();
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <typename T, int D>
+tm_status launch_chunk(AttnArgs &a, int device, int sms, cudaStream_t s, bool pdl)
+{
+    const void *k = (const void *)kv4_chunk_kernel<T, D>;
+    constexpr size_t smem = sizeof(ChunkSmem<D>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static std::atomic<bool> ready[kMaxDevices];
+    if (!ready[device].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+            cudaGetLastError();
+            return TM_ERR_CUDA;
+        }
+        ready[device].store(true, std::memory_order_release);
+    }
+    void *args[] = {(void *)&a};
+    const unsigned blocks = (unsigned)(sms < kMostBlocks / 4 ? sms : kMostBlocks / 4);
+    return launch_kernel(k, dim3(blocks), dim3(kThreads2), args, smem, s, pdl);
+}
+
+}  // namespace
+
+bool chunk_attn_fits(int32_t xtype, int64_t rows, int D)
+{
+    return xtype != TM_F32 && (D == 64 || D == 128) && rows >= 128;
+}
+
+size_t chunk_attn_slots_bytes(int D) { return 2 * (size_t)(kMostBlocks / 4) * kChunkRows * (D + 2) * sizeof(float); }
+
+tm_status launch_chunk_attn(int D, int32_t xtype, AttnArgs &a, int device, int sms, bool join, cudaStream_t s, bool pdl)
+{
+    const tm_status st = xtype == TM_F16 ? (D == 64 ? launch_chunk<__half, 64>(a, device, sms, s, pdl)
+                                                    : launch_chunk<__half, 128>(a, device, sms, s, pdl))
+                                         : (D == 64 ? launch_chunk<__nv_bfloat16, 64>(a, device, sms, s, pdl)
+                                                    : launch_chunk<__nv_bfloat16, 128>(a, device, sms, s, pdl));
+    if (st != TM_OK || !join) return st;
+    return launch_attn_join(D, xtype, a, kChunkRows, 1, s);
+}
+
+}  // namespace libtm

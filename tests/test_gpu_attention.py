@@ -112,6 +112,100 @@ def test_several_queries(cuda, kind, D, window):
     c.check(window=window)
 
 
+# 128 query rows a KV head and more: the form for chunks of a prompt.
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,qn,Hq,Hkv,page", [
+    ([130], [128], 1, 1, 16), ([128], [128], 1, 1, 128), ([70], [32], 4, 1, 32), ([40], [40], 8, 2, 48),
+    ([300, 0, 129], [33, 5, 129], 4, 1, 16), ([1000, 260, 64], [70, 64, 64], 12, 3, 64), ([20, 500], [90, 1], 4, 2, 16)])
+def test_chunks(cuda, kind, D, lens, qn, Hq, Hkv, page):
+    c = Case(kind, lens, qn, Hq, Hkv, D, page)
+    c.run()
+    tm.tm_check()
+    c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [1, 50, 200])
+def test_chunks_with_a_window(cuda, D, window):
+    c = Case("bf16", [700, 150], [80, 150], 4, 2, D, 32)
+    c.run(window=window)
+    tm.tm_check()
+    c.check(window=window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_chunks_every_key_split_over_blocks(cuda, kind):
+    c = Case(kind, [5000], [64], 4, 1, 128, 64)
+    c.run(flags=tm.TM_ATTN_FULL)
+    tm.tm_check()
+    c.check(full=True)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_chunks_strides_and_gaps(cuda, shift):
+    c = Case("bf16", [260, 90], [80, 50], 6, 2, 64, 16, ld_gap=24, shift=shift)
+    c.run(lse=False)
+    tm.tm_check()
+    c.check(lse=False)
+    c.o[:, :c.Hq * c.D] = 9.0
+    assert bool((c.obuf == 9.0).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_chunks_scales_of_very_different_size(cuda, kind):
+    c = Case(kind, [900], [140], 2, 1, 128, 16)
+    rng = np.random.default_rng(3)
+    grow = 2.0 ** rng.integers(-8, 5, (c.pages * 16, 1, 1)).astype(np.float64)
+    v = rng.standard_normal((c.pages * 16, 1, 128)) * grow
+    c.pool = ref.empty_pool(c.pages, 1, 16, 128)
+    c.kk, c.vv = ref.append(c.pool, range(c.pages * 16), 16, c.kk, v)
+    c.q *= torch.from_numpy(2.0 ** rng.integers(-8, 3, (c.Tq, c.row))).to(c.t).cuda()
+    c.run()
+    tm.tm_check()
+    c.check()
+
+
+def test_chunks_not_finite_where_masked_and_where_seen(cuda):
+    c = Case("bf16", [200], [150], 2, 1, 64, 16, extra_pages=0)
+    order = [int(c.table[0][j // 16]) * 16 + j % 16 for j in range(208)]
+    nan = np.full((1, 64), np.nan)
+    kk, vv = c.kk.copy(), c.vv.copy()
+    for which in ("k", "v"):
+        for j in (190, 201, 207):     # seen by the last ten queries; past the end
+            at = order[j]
+            ref.append(c.pool, [at], 16, (nan if which == "k" else kk[at])[None], (nan if which == "v" else vv[at])[None])
+        c.run()
+        tm.tm_check()
+        o, l = ref.f64(c.o).reshape(150, 2, 64), ref.f64(c.lse)
+        w, lw, *_ = ref.attention(c.q64()[:140], kk, vv, c.table, [190], [0, 140], 16, c.scale)
+        assert np.isnan(o[140:]).all() and np.isnan(l[140:]).all() == (which == "k")
+        assert np.abs(o[:140] - w).max() < 0.05 and np.abs(l[:140] - lw).max() < 1e-3
+        ref.append(c.pool, [order[190]], 16, kk[order[190]][None], vv[order[190]][None])
+
+
+def test_chunks_bad_pages_and_lengths(cuda):
+    c = Case("bf16", [300, 280], [130, 130], 1, 1, 64, 16)
+    good = c.table.copy()
+    for at, page in ((3, c.pages), (0, -1)):
+        bad = good.copy()
+        bad[1, at] = page
+        c.run(table=bad)
+        with pytest.raises(tm.TmError) as e:
+            tm.tm_check()
+        assert e.value.status == tm.TM_ERR_INDEX
+    c.run(lens=[300, 301])
+    with pytest.raises(tm.TmError) as e:
+        tm.tm_check()
+    assert e.value.status == tm.TM_ERR_INDEX
+    c.run()
+    first, l = c.o.clone(), c.lse.clone()
+    c.run()
+    tm.tm_check()
+    c.check()
+    assert torch.equal(first, c.o) and torch.equal(l, c.lse)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_every_key(cuda, kind):
     c = Case(kind, [50, 33], [3, 40], 4, 4, 64, 16)
