@@ -627,10 +627,11 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 // every W-th partial with a running maximum of its own, a lane D/32 dims; then a row's
 // warps in order.  Items with few partials (many items) take a warp a row, few items
 // with many partials all eight.
-template <typename T, int D>
+// U: partials a warp has in flight.
+template <typename T, int D, int U>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ AttnArgs a, int rows_of_tile, int W)
 {
-    constexpr int E = D / 32, U = D == 256 ? 4 : 8;  // partials in flight
+    constexpr int E = D / 32;
     __shared__ float sums[8][D], stat[8][2];
     pdl_trigger();
     pdl_wait();
@@ -739,8 +740,8 @@ tm_status join_items(AttnArgs &a, int rows_of_tile, int W, cudaStream_t s)
 {
     const int64_t items = (int64_t)a.B * a.Hkv * a.row_tiles;
     void *jargs[] = {(void *)&a, &rows_of_tile, &W};
-    return launch_dependent((const void *)kv4_join_kernel<T, D>, dim3((unsigned)(items * rows_of_tile / (8 / W))),
-                            dim3(256), jargs, 0, s);
+    const void *k = W == 1 ? (const void *)kv4_join_kernel<T, D, 2> : (const void *)kv4_join_kernel<T, D, D == 256 ? 4 : 8>;
+    return launch_dependent(k, dim3((unsigned)(items * rows_of_tile / (8 / W))), dim3(256), jargs, 0, s);
 }
 
 template <typename T, int D, int NT>

@@ -47,6 +47,7 @@ struct ChunkSmem {
     alignas(16) float2 kpar[kParStages][kTok], vpar[kParStages][kTok];  // (step, low) of K; (step 2^E, low) of V
     float unit, top[8];
     int vexp[kParStages];
+    uint32_t vnan[kParStages][kTok / 32];  // tokens whose V is held as NaN
     alignas(8) uint64_t raw_full[kRawStages], raw_free[kRawStages], op_full[kOpStages], op_free[kOpStages],
         par_full[kParStages], par_free[kParStages], top_full, q_full, unit_full, s_full[2], p_full[2][2], o_done[2][2], done;
     uint32_t tmem;
@@ -190,7 +191,8 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
     constexpr uint32_t kS = 0, kO = 256;  // first columns of S and O in tensor memory
     extern __shared__ __align__(1024) unsigned char raw_smem[];
     using Smem = ChunkSmem<D>;
-    Smem &s = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    // (an offset, not a rounded address: the compiler has to see shared memory)
+    Smem &s = *reinterpret_cast<Smem *>(raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023));
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Run run;
@@ -397,7 +399,10 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                     if (tok + tt >= g.end) kp = vp = make_float2(0.0f, 0.0f);  // (its bytes are whatever the ring held)
                     kp.y = fmaf(8.0f, kp.x, kp.y);                             // codes count from 8
                     vp.y = fmaf(8.0f, vp.x, vp.y);
-                    if (!(vp.x < INFINITY)) vp = make_float2(0.0f, NAN);
+                    const bool bad = !(vp.x < INFINITY);
+                    if (bad) vp = make_float2(0.0f, 0.0f);
+                    const unsigned mask = __ballot_sync(0xffffffffu, bad);
+                    if (lane == 0) s.vnan[par.stage][tt / 32] = mask;
                     s.kpar[par.stage][tt] = make_float2(kp.x * unit, kp.y * unit);
                     s.vpar[par.stage][tt] = make_float2(vp.x * vscale, vp.y);
                 }
@@ -607,6 +612,12 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                         vexp = e_new;
                     }
                     first = false;
+                    // a token held as NaN makes the rows that see it NaN, and no others
+                    if ((s.vnan[par.stage][2 * h] | s.vnan[par.stage][2 * h + 1]) != 0) {
+#pragma unroll
+                        for (int c = 0; c < kHalf; ++c)
+                            if ((s.vnan[par.stage][2 * h + c / 32] >> (c % 32) & 1) && y[c] != -INFINITY) lowsum = NAN;
+                    }
                     const float ref = m == -INFINITY ? 0.0f : m;
                     uint32_t p[kHalf / 2];
 #pragma unroll
@@ -614,13 +625,8 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                         const float4 vp = vpar[(kHalf * h + c) / 2];
                         const float p0 = ex2(y[c] - ref), p1 = ex2(y[c + 1] - ref);
                         l += p0 + p1;
-                        if (masked) {  // a low that is NaN joins only the rows that see its token
-                            if (y[c] != -INFINITY) lowsum = fmaf(p0, vp.y, lowsum);
-                            if (y[c + 1] != -INFINITY) lowsum = fmaf(p1, vp.w, lowsum);
-                        } else {
-                            lowsum = fmaf(p0, vp.y, lowsum);
-                            lowsum = fmaf(p1, vp.w, lowsum);
-                        }
+                        lowsum = fmaf(p0, vp.y, lowsum);
+                        lowsum = fmaf(p1, vp.w, lowsum);
                         p[c / 2] = pack_half2(p0 * vp.x, p1 * vp.z);
                     }
                     tmem_store(ts + 32 * h, p);
