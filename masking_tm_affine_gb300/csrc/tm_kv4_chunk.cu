@@ -6,10 +6,10 @@
 // the heads that share a KV head), two halves of 128, walked over 128 tokens at a time:
 //
 //   loader warp      bulk copies of the tile's eight cache blocks
-//   2 unpack warps   codes -> fp16 c - 8 in shared memory, K and V once for both halves;
+//   4 unpack warps   codes -> fp16 c - 8 in shared memory, K and V once for both halves;
 //                    the tokens' (step, low) as floats
 //   MMA thread       S = Q K^T   [128 rows, 128 tokens], both operands in shared memory
-//                    O += P V    [128 rows, D], P from tensor memory, 64 tokens at a time
+//                    O += P V    [128 rows, D], P from tensor memory, 32 tokens at a time
 //   2 x 4 warps      a half each, a thread a row: S from tensor memory, softmax, P back
 //                    into the columns S came from; while one half is at it, the tensor
 //                    cores run the other's products
@@ -34,9 +34,13 @@ namespace libtm {
 namespace {
 
 constexpr int kTok = 128;            // tokens of a tile
-constexpr int kHalf = 64;            // tokens of one step of the second product
-constexpr int kUnpackWarps = 2;
-constexpr int kThreads2 = 12 * 32;   // warps 0-7 softmax, 8-9 unpack, 10 MMA, 11 loader: 168 registers a thread
+constexpr int kStep = 32, kSteps = kTok / kStep;  // tokens of one step of the second product
+constexpr int kUnpackWarps = 4;
+constexpr int kThreads2 = 16 * 32;   // warps 0-7 softmax, 8-11 unpack, 12 MMA, 13 loader (14, 15 idle)
+// Registers: 128 a thread at launch (all there are); the softmax warps, which hold 64
+// logits of a row, take what the others give: 2 x 168 + 2 x 88 = 4 x 128.
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
+static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "register shares");
 constexpr int kRawStages = 2, kOpStages = 3, kParStages = 2;
 
 template <int D>
@@ -49,7 +53,7 @@ struct ChunkSmem {
     int vexp[kParStages];
     uint32_t vnan[kParStages][kTok / 32];  // tokens whose V is held as NaN
     alignas(8) uint64_t raw_full[kRawStages], raw_free[kRawStages], op_full[kOpStages], op_free[kOpStages],
-        par_full[kParStages], par_free[kParStages], top_full, q_full, unit_full, s_full[2], p_full[2][2], o_done[2][2], done;
+        par_full[kParStages], par_free[kParStages], top_full, q_full, unit_full, s_full[2], p_full[2][kSteps], o_done[2][kSteps], done;
     uint32_t tmem;
     int abort;
 };
@@ -146,16 +150,21 @@ __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t *r)
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
-__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t *r)
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t *r)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         pdl_wait();
         return;
     }
-    if (warp == 10) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -221,11 +230,11 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         bar_init(&s.top_full, 256);
         bar_init(&s.q_full, 256);
         bar_init(&s.unit_full, 256);
-        // [half of the rows][half of a tile's tokens]: each completes once a tile, so the
+        // [half of the rows][step of a tile's tokens]: each completes once a tile, so the
         // parity of the tile's number tells a completion from the one before
         for (int i = 0; i < 2; ++i) {
             bar_init(&s.s_full[i], 1);
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < kSteps; ++h) {
                 bar_init(&s.p_full[i][h], 128);
                 bar_init(&s.o_done[i][h], 1);
             }
@@ -241,7 +250,11 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
     volatile int *abort = &s.abort;
     auto wait = [&](uint64_t *b, uint32_t parity) { return bar_wait(b, parity, abort, a.status); };
 
-    if (warp == 11) {
+    // Each split is taken in its own branch, so that the registers of either are known to
+    // the compiler all the way through it.
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 13) {
         // ---------------- loader: lane i copies block i of a tile
         Turn raw;
         uint32_t issued = 0;
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         const uint32_t first = issued > kRawStages ? issued - kRawStages : 0;
         for (uint32_t i = first; i < issued; ++i)
             mbar_wait_bounded(smem_u32(&s.raw_full[i % kRawStages]), (i / kRawStages) & 1);
-    } else if (warp == 10) {
+    } else if (warp == 12) {
         if (lane == 0) {
             // ---------------- MMA issuer
             constexpr uint32_t id_s = idesc_f16(128, kTok, false), id_o = idesc_f16(128, D, true);
@@ -321,23 +334,23 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                     const Turn v = op;
                     op.next(kOpStages);
                     const Turn k = op;  // the next tile's K
-                    for (int h = 0; ok && h < 2; ++h)
+                    for (int h = 0; ok && h < kSteps; ++h)
                         for (int i = 0; ok && i < 2; ++i) {
                             if (h == 0 && i == 0) ok = wait(&s.op_full[v.stage], v.phase);
                             ok = ok && wait(&s.p_full[i][h], count & 1);
                             if (!ok) break;
                             fence_after();
-                            const uint32_t vs = smem_u32(s.op[v.stage]) + h * (kHalf / 8) * PANELS * 1024;
+                            const uint32_t vs = smem_u32(s.op[v.stage]) + h * (kStep / 8) * PANELS * 1024;
 #pragma unroll
-                            for (int x = 0; x < kHalf / 16; ++x)
-                                mma_ts(tmem + kO + 128 * i, tmem + kS + 128 * i + 32 * h + 8 * x,
+                            for (int x = 0; x < kStep / 16; ++x)
+                                mma_ts(tmem + kO + 128 * i, tmem + kS + 128 * i + kStep / 2 * h + 8 * x,
                                        desc_mn(vs + x * 2 * PANELS * 1024, 1024, PANELS * 1024), id_o, t > 0 || h > 0 || x > 0);
                             commit(&s.o_done[i][h]);
-                            if (h == 1 && i == 1) commit(&s.op_free[v.stage]);
-                            if (h == 1 && t + 1 < tiles) {
+                            if (h == kSteps - 1 && i == 1) commit(&s.op_free[v.stage]);
+                            if (h == kSteps - 1 && t + 1 < tiles) {
                                 // S goes where this P came from: after the product that reads it
                                 if (i == 0) ok = wait(&s.op_full[k.stage], k.phase);
-                                ok = ok && wait(&s.o_done[i][1], count & 1);
+                                ok = ok && wait(&s.o_done[i][kSteps - 1], count & 1);
                                 if (!ok) break;
                                 fence_after();
                                 score(i, k.stage);
@@ -353,7 +366,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 atomicOr(a.status, kStatusTimeout);
             }
         }
-    } else if (warp >= 8) {
+    } else if (warp < 12) {
         // ---------------- unpack
         const int t = threadIdx.x - 256, w = warp - 8;
         const uint32_t bias = a.bias;
@@ -418,7 +431,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 {
                     const int j = lane >> 3, gr = lane & 7;
                     constexpr int LW = D / 32;  // words of a quarter row
-#pragma unroll 2
+#pragma unroll
                     for (int i = 0; i < kTok / 8 / kUnpackWarps; ++i) {
                         const int row = w * (kTok / kUnpackWarps) + i * 8 + gr;
                         const uint8_t *p = src + (row / 16) * BB + (row % 16) * (D / 2) + j * (D / 8);
@@ -445,7 +458,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 {
                     const int r = lane & 7, pr = lane >> 3;
                     constexpr int LW = D / 64;  // words a token has in a slice
-#pragma unroll 2
+#pragma unroll
                     for (int i = 0; i < kTok / 8 / kUnpackWarps; ++i) {
                         const int pair = w * (kTok / 2 / kUnpackWarps) + i * 4 + pr;  // of 64
                         const uint8_t *p = src + (pair / 8) * BB + kv4_v_off(D) + (pair % 8) * D + r * (D / 8);
@@ -471,7 +484,9 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 ++ops;
             }
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---------------- softmax: half i, thread r of it has row 128 i + r of the tile
         const int i = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -492,24 +507,25 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             const int t = live ? (int)fdiv(full_row, a.by_group) : 0, hq = g.kvh * a.G + full_row - t * a.G;
             // ---- Q: this row, scaled by a power of two common to the tile, into shared memory
             const T *qp = reinterpret_cast<const T *>(a.Q) + (int64_t)(seq.q0 + t) * a.qs_tok + (int64_t)hq * a.qs_head;
-            Vec<T, 8> v[D / 8];
-            float top = 0.0f;
-#pragma unroll
-            for (int x = 0; x < D / 8; ++x) {
+            auto load_q = [&](int x, Vec<T, 8> &v) {
                 if (!live) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[x].v[e] = from_f<T>(0.0f);
+                    for (int e = 0; e < 8; ++e) v.v[e] = from_f<T>(0.0f);
                 } else if (a.vec) {
-                    load_vec(qp + 8 * x, v[x]);
+                    v = *reinterpret_cast<const Vec<T, 8> *>(qp + 8 * x);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[x].v[e] = qp[8 * x + e];
+                    for (int e = 0; e < 8; ++e) v.v[e] = qp[8 * x + e];
                 }
+            };
+            float top = 0.0f;
+#pragma unroll 4
+            for (int x = 0; x < D / 8; ++x) {
+                Vec<T, 8> v;
+                load_q(x, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(v.v[e])));
             }
-#pragma unroll
-            for (int x = 0; x < D / 8; ++x)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(v[x].v[e])));
             const bool any = g.c1 > g.c0;
             float qsum = 0.0f;
             if (any) {
@@ -528,10 +544,12 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             bar_arrive(&s.unit_full);
             {
                 const uint32_t dst = smem_u32(s.q[i][0]) + r * 128;
-#pragma unroll
+#pragma unroll 4
                 for (int x = 0; x < D / 8; ++x) {
+                    Vec<T, 8> v;
                     float f[8];
-                    widen(v[x], f);
+                    load_q(x, v);  // (a second time: held, the row would take 64 registers)
+                    widen(v, f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         f[e] *= up;
@@ -562,30 +580,26 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 const float4 *kpar = reinterpret_cast<const float4 *>(s.kpar[par.stage]);
                 const float4 *vpar = reinterpret_cast<const float4 *>(s.vpar[par.stage]);
                 const int e_new = s.vexp[par.stage];
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t acc[kHalf];
-                    tmem_load(ts + kHalf * h, acc);
-                    tmem_load(ts + kHalf * h + 32, acc + 32);
-                    tmem_load_wait();
-                    float y[kHalf], top = -INFINITY;
+                const uint32_t nan0 = s.vnan[par.stage][0] | s.vnan[par.stage][1] | s.vnan[par.stage][2] | s.vnan[par.stage][3];
+                // One step: logits, the reference, probabilities back to tensor memory.  `acc`
+                // holds its columns of S.
+                auto step = [&](int h, uint32_t (&acc)[kStep]) {
+                    float y[kStep], top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 2) {
-                        const float4 kp = kpar[(kHalf * h + c) / 2];
+                    for (int c = 0; c < kStep; c += 2) {
+                        const float4 kp = kpar[(kStep * h + c) / 2];
                         y[c] = fmaf(__uint_as_float(acc[c]), kp.x, kp.y * qsum);
                         y[c + 1] = fmaf(__uint_as_float(acc[c + 1]), kp.z, kp.w * qsum);
                     }
-                    const int t0 = tok + kHalf * h;
-                    const bool masked = t0 < safe0 || t0 + kHalf > safe1;
-                    if (masked) {
+                    const int t0 = tok + kStep * h;
+                    if (t0 < safe0 || t0 + kStep > safe1) {
 #pragma unroll
-                        for (int c = 0; c < kHalf; ++c)
+                        for (int c = 0; c < kStep; ++c)
                             if (t0 + c < lo || t0 + c >= hi) y[c] = -INFINITY;
                     }
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 2) top = fmaxf(top, fmaxf(y[c], y[c + 1]));
-                    const bool grow = top > m + kSlack;
-                    if (__any_sync(0xffffffffu, grow) || e_new != vexp) {
+                    for (int c = 0; c < kStep; c += 2) top = fmaxf(top, fmaxf(y[c], y[c + 1]));
+                    if (__any_sync(0xffffffffu, top > m + kSlack) || e_new != vexp) {
                         const float mn = fmaxf(m, top);
                         const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
                         m = mn;
@@ -593,19 +607,19 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                         lowsum *= f;
                         if (!first) {
                             // O is this warp's once the last step handed over is done
-                            ok = h ? wait(&s.o_done[i][0], count & 1) : wait(&s.o_done[i][1], (count - 1) & 1);
+                            ok = h ? wait(&s.o_done[i][h - 1], count & 1) : wait(&s.o_done[i][kSteps - 1], (count - 1) & 1);
                             ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
+                            if (!ok) return;
                             fence_after();
                             const float move = f * ldexpf(1.0f, vexp - e_new);
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_load(to + c, o);
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_load16(to + c, o);
                                 tmem_load_wait();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * move);
-                                tmem_store(to + c, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * move);
+                                tmem_store16(to + c, o);
                             }
                             tmem_store_wait();
                         }
@@ -613,26 +627,33 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                     }
                     first = false;
                     // a token held as NaN makes the rows that see it NaN, and no others
-                    if ((s.vnan[par.stage][2 * h] | s.vnan[par.stage][2 * h + 1]) != 0) {
+                    if (nan0 != 0) {
 #pragma unroll
-                        for (int c = 0; c < kHalf; ++c)
-                            if ((s.vnan[par.stage][2 * h + c / 32] >> (c % 32) & 1) && y[c] != -INFINITY) lowsum = NAN;
+                        for (int c = 0; c < kStep; ++c)
+                            if ((s.vnan[par.stage][h] >> c & 1) && y[c] != -INFINITY) lowsum = NAN;
                     }
                     const float ref = m == -INFINITY ? 0.0f : m;
-                    uint32_t p[kHalf / 2];
+                    uint32_t p[kStep / 2];
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 2) {
-                        const float4 vp = vpar[(kHalf * h + c) / 2];
+                    for (int c = 0; c < kStep; c += 2) {
+                        const float4 vp = vpar[(kStep * h + c) / 2];
                         const float p0 = ex2(y[c] - ref), p1 = ex2(y[c + 1] - ref);
                         l += p0 + p1;
                         lowsum = fmaf(p0, vp.y, lowsum);
                         lowsum = fmaf(p1, vp.w, lowsum);
                         p[c / 2] = pack_half2(p0 * vp.x, p1 * vp.z);
                     }
-                    tmem_store(ts + 32 * h, p);
+                    tmem_store16(ts + kStep / 2 * h, p);
                     tmem_store_wait();
                     fence_before();
                     bar_arrive(&s.p_full[i][h]);
+                };
+#pragma unroll 1
+                for (int h = 0; ok && h < kSteps; ++h) {
+                    uint32_t acc[kStep];
+                    tmem_load(ts + kStep * h, acc);
+                    tmem_load_wait();
+                    step(h, acc);
                 }
                 if (!ok) break;
                 bar_arrive(&s.par_free[par.stage]);
@@ -642,7 +663,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             // ---- the segment's end
             pdl_wait();
             if (ok && any) {
-                ok = wait(&s.o_done[i][1], (count - 1) & 1);
+                ok = wait(&s.o_done[i][kSteps - 1], (count - 1) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 fence_after();
             }
@@ -693,7 +714,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
     pdl_wait();
     fence_before();
     __syncthreads();
-    if (warp == 10) {
+    if (warp == 12) {
         __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
