@@ -6,8 +6,8 @@
 // the heads that share a KV head), two halves of 128, walked over 128 tokens at a time:
 //
 //   loader warp      bulk copies of the tile's eight cache blocks
-//   4 unpack warps   codes -> fp16 c - 8 in shared memory, K and V once for both halves;
-//                    the tokens' (step, low) as floats
+//   4 unpack warps   codes -> fp16 in shared memory, once for both halves: K as the
+//                    whole numbers c, V as the values low + c step
 //   MMA thread       S = Q K^T   [128 rows, 128 tokens], both operands in shared memory
 //                    O += P V    [128 rows, D], P from tensor memory, 32 tokens at a time
 //   2 x 4 warps      a half each, a thread a row: S from tensor memory, softmax, P back
@@ -18,6 +18,14 @@
 // 128-byte swizzled panels of 64 dims; a word's eight dims lie in the order 0 4 1 5 2 6
 // 3 7, the order its nibbles come in (Q is written in the same order, O is read back
 // in it).  Tensor memory: S of both halves in columns 0 .. 255, O in 256 .. 511.
+//
+// K's scales stay outside its product, as in tm_kv4_attn.cu, so that logits keep fp32's
+// accuracy; a thread multiplies them in, one pair of fp16 numbers a token, read four
+// tokens at a time (every lane reads the same: shared memory returns 512 bytes for
+// 16, and with the scales of K and V as floats these reads alone took 4096 of a
+// tile's cycles).  V's are multiplied into its operand, which rounds each value to
+// fp16, off by 2^-11 of itself like the probabilities; the tile's exponent comes off
+// first, so that the rounding does not depend on V's size.
 //
 // A thread has a whole row, so its maximum and sums need no exchange.  The reference
 // maximum moves only where a logit passes it by 2^8 and the steps' exponent only past
@@ -48,12 +56,12 @@ struct ChunkSmem {
     alignas(1024) uint8_t q[2][D / 64][128 * 128];           // [half][panel]: 128 rows of 128 bytes
     alignas(1024) uint8_t op[kOpStages][D / 64 * 128 * 128];  // K tiles: panels as Q; V tiles: [8 tokens][panel]
     alignas(128) uint8_t raw[kRawStages][kTok / 16 * kv4_block_bytes(D)];
-    alignas(16) float2 kpar[kParStages][kTok], vpar[kParStages][kTok];  // (step, low) of K; (step 2^E, low) of V
-    float unit, top[8];
+    alignas(16) uint32_t kpar[kParStages][kTok];  // (step, low) of K
+    float top[8];
     int vexp[kParStages];
     uint32_t vnan[kParStages][kTok / 32];  // tokens whose V is held as NaN
     alignas(8) uint64_t raw_full[kRawStages], raw_free[kRawStages], op_full[kOpStages], op_free[kOpStages],
-        par_full[kParStages], par_free[kParStages], top_full, q_full, unit_full, s_full[2], p_full[2][kSteps], o_done[2][kSteps], done;
+        par_full[kParStages], par_free[kParStages], top_full, q_full, s_full[2], p_full[2][kSteps], o_done[2][kSteps], done;
     uint32_t tmem;
     int abort;
 };
@@ -172,20 +180,26 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Eight codes of a word as c - 8 in fp16, in the order 0 4 1 5 2 6 3 7.  Even
-// nibbles: 1024 + c less 1032; odd ones: (1024 + 16 c) / 16 less 72.  Exact.
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ uint32_t as_bits(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+
+// Eight codes of a word as whole numbers in fp16, in the order 0 4 1 5 2 6 3 7.  Even
+// nibbles: 1024 + c less 1024; odd ones: (1024 + 16 c) / 16 less 64.  Exact.
 __device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t bias)
 {
-    const __half2 e0 = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));  // 1032
-    const __half2 sx = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));  // 1/16
-    const __half2 o0 = __halves2half2(__ushort_as_half(0xd480), __ushort_as_half(0xd480));  // -72
+    const __half2 e0 = as_half2(0x64006400u), sx = as_half2(0x2c002c00u), o0 = as_half2(0xd400d400u);  // 1024, 1/16, -64
     const uint32_t v = w >> 8;
-    const uint32_t a = (w & 0x000f000fu) | bias, b = (w & 0x00f000f0u) | bias;
-    const uint32_t c = (v & 0x000f000fu) | bias, d = (v & 0x00f000f0u) | bias;
-    const __half2 ha = __hsub2(*reinterpret_cast<const __half2 *>(&a), e0), hb = __hfma2(*reinterpret_cast<const __half2 *>(&b), sx, o0);
-    const __half2 hc = __hsub2(*reinterpret_cast<const __half2 *>(&c), e0), hd = __hfma2(*reinterpret_cast<const __half2 *>(&d), sx, o0);
-    return make_uint4(*reinterpret_cast<const uint32_t *>(&ha), *reinterpret_cast<const uint32_t *>(&hb),
-                      *reinterpret_cast<const uint32_t *>(&hc), *reinterpret_cast<const uint32_t *>(&hd));
+    return make_uint4(as_bits(__hsub2(as_half2((w & 0x000f000fu) | bias), e0)),
+                      as_bits(__hfma2(as_half2((w & 0x00f000f0u) | bias), sx, o0)),
+                      as_bits(__hsub2(as_half2((v & 0x000f000fu) | bias), e0)),
+                      as_bits(__hfma2(as_half2((v & 0x00f000f0u) | bias), sx, o0)));
+}
+
+// The values they stand for, rounded once.
+__device__ __forceinline__ uint4 scaled8(uint4 c, __half2 step, __half2 low)
+{
+    return make_uint4(as_bits(__hfma2(as_half2(c.x), step, low)), as_bits(__hfma2(as_half2(c.y), step, low)),
+                      as_bits(__hfma2(as_half2(c.z), step, low)), as_bits(__hfma2(as_half2(c.w), step, low)));
 }
 
 __device__ __forceinline__ void st_shared(uint32_t at, uint4 v)
@@ -229,7 +243,6 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         }
         bar_init(&s.top_full, 256);
         bar_init(&s.q_full, 256);
-        bar_init(&s.unit_full, 256);
         // [half of the rows][step of a tile's tokens]: each completes once a tile, so the
         // parity of the tile's number tells a completion from the one before
         for (int i = 0; i < 2; ++i) {
@@ -371,7 +384,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         const int t = threadIdx.x - 256, w = warp - 8;
         const uint32_t bias = a.bias;
         Turn raw, op, par;
-        uint32_t ops = 0, pars = 0, segs = 0;
+        uint32_t ops = 0, pars = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
         while (ok && run.pos < run.stop) {
@@ -380,46 +393,37 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             if (g.c1 <= g.c0) continue;
             int vexp = 0;
             float vcap = 0.0f;
-            ok = wait_all(&s.unit_full, segs & 1);
-            ++segs;
-            if (!ok) break;
-            const float unit = *(volatile float *)&s.unit;
             for (int tok = g.c0; ok && tok < g.c1; tok += kTok) {
                 ok = wait_all(&s.raw_full[raw.stage], raw.phase);
                 if (!ok) break;
                 const uint8_t *src = s.raw[raw.stage];
-                // ---- scales
-                float vmax = 0.0f;  // of the tile, by every warp for itself
+                // ---- scales: V's largest magnitude in the tile, by every warp for itself
+                float vmax = 0.0f;
+                unsigned nans[kTok / 32];
 #pragma unroll
                 for (int x = 0; x < kTok / 32; ++x) {
                     const int tt = x * 32 + lane;
-                    const float step = half2_at(src + (tt / 16) * BB + kv4_vs_off(D) + 4 * (tt % 16)).x;
-                    if (tok + tt < g.end && step < INFINITY) vmax = fmaxf(vmax, step);
+                    const float2 vp = half2_at(src + (tt / 16) * BB + kv4_vs_off(D) + 4 * (tt % 16));
+                    const bool in = tok + tt < g.end, bad = in && !(vp.x < INFINITY);
+                    if (in && !bad) vmax = fmaxf(vmax, fmaxf(fabsf(vp.y), fabsf(fmaf(15.0f, vp.x, vp.y))));
+                    nans[x] = __ballot_sync(0xffffffffu, bad);
                 }
                 vmax = lanes_max(vmax, 32);
                 if (vmax >= vcap) {
-                    vexp = vmax > 0.0f ? (int)(__float_as_uint(vmax) >> 23) - 127 : -33;  // 2^e <= vmax < 2^(e+1)
+                    vexp = vmax > 0.0f ? (int)(__float_as_uint(vmax) >> 23) - 127 : -24;  // 2^e <= vmax < 2^(e+1)
                     vcap = ldexpf(1.0f, vexp + 3);
                 }
+                const float vscale = ldexpf(1.0f, -vexp);  // values below 8
                 if (pars >= kParStages) ok = wait_all(&s.par_free[par.stage], par.phase ^ 1);
                 if (!ok) break;
-                const float vscale = ldexpf(1.0f, kStepBits - vexp);
-#pragma unroll
-                for (int x = 0; x < kTok; x += kUnpackWarps * 32) {
-                    const int tt = x + t;
-                    const uint8_t *blk = src + (tt / 16) * BB;
-                    float2 kp = half2_at(blk + kv4_ks_off(D) + 4 * (tt % 16)), vp = half2_at(blk + kv4_vs_off(D) + 4 * (tt % 16));
-                    if (tok + tt >= g.end) kp = vp = make_float2(0.0f, 0.0f);  // (its bytes are whatever the ring held)
-                    kp.y = fmaf(8.0f, kp.x, kp.y);                             // codes count from 8
-                    vp.y = fmaf(8.0f, vp.x, vp.y);
-                    const bool bad = !(vp.x < INFINITY);
-                    if (bad) vp = make_float2(0.0f, 0.0f);
-                    const unsigned mask = __ballot_sync(0xffffffffu, bad);
-                    if (lane == 0) s.vnan[par.stage][tt / 32] = mask;
-                    s.kpar[par.stage][tt] = make_float2(kp.x * unit, kp.y * unit);
-                    s.vpar[par.stage][tt] = make_float2(vp.x * vscale, vp.y);
+                {
+                    const uint8_t *blk = src + (t / 16) * BB;
+                    // a token past the end has no scales (its bytes are whatever the ring held)
+                    s.kpar[par.stage][t] =
+                        tok + t < g.end ? *reinterpret_cast<const uint32_t *>(blk + kv4_ks_off(D) + 4 * (t % 16)) : 0u;
+                    if (t < kTok / 32) s.vnan[par.stage][t] = t == 0 ? nans[0] : t == 1 ? nans[1] : t == 2 ? nans[2] : nans[3];
+                    if (t == 0) s.vexp[par.stage] = vexp;
                 }
-                if (t == 0) s.vexp[par.stage] = vexp;
                 bar_arrive(&s.par_full[par.stage]);
                 par.next(kParStages);
                 ++pars;
@@ -468,11 +472,18 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                         else
                             *reinterpret_cast<uint2 *>(c) = *reinterpret_cast<const uint2 *>(p);
 #pragma unroll
-                        for (int x = 0; x < 2 * LW; ++x) {
-                            const int token = 2 * pair + x / LW, chunk = r * LW + x % LW;
-                            st_shared(dst + (token / 8) * (PANELS * 1024) + (chunk / 8) * 1024 + (token % 8) * 128 +
-                                          ((chunk % 8) ^ (token % 8)) * 16,
-                                      unpack8(c[x], bias));
+                        for (int o = 0; o < 2; ++o) {
+                            const int token = 2 * pair + o;
+                            float2 vp = half2_at(src + (token / 16) * BB + kv4_vs_off(D) + 4 * (token % 16));
+                            if (tok + token >= g.end || !(vp.x < INFINITY)) vp = make_float2(0.0f, 0.0f);
+                            const __half2 step = __float2half2_rn(vp.x * vscale), low = __float2half2_rn(vp.y * vscale);
+#pragma unroll
+                            for (int x = 0; x < LW; ++x) {
+                                const int chunk = r * LW + x;
+                                st_shared(dst + (token / 8) * (PANELS * 1024) + (chunk / 8) * 1024 + (token % 8) * 128 +
+                                              ((chunk % 8) ^ (token % 8)) * 16,
+                                          scaled8(unpack8(c[o * LW + x], bias), step, low));
+                            }
                         }
                     }
                 }
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(v.v[e])));
             }
             const bool any = g.c1 > g.c0;
-            float qsum = 0.0f;
+            float qsum = 0.0f, unit = 1.0f;  // logits in base 2 are z unit
             if (any) {
             top = lanes_max(top, 32);
             if (lane == 0) s.top[warp] = top;
@@ -539,9 +550,9 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
 #pragma unroll
             for (int x = 0; x < 8; ++x) top = fmaxf(top, s.top[x]);
             const int qe = max(-100, min((int)(__float_as_uint(top) >> 23) - 127, 127));
-            const float up = ldexpf(1.0f, 14 - qe);
-            if (threadIdx.x == 0) s.unit = a.scale * kLog2eF * ldexpf(1.0f, qe - 14);
-            bar_arrive(&s.unit_full);
+            // (a negative scale turns q's sign: z below then grows with the logit)
+            const float up = copysignf(ldexpf(1.0f, 14 - qe), a.scale);
+            unit = fmaxf(fabsf(a.scale) * kLog2eF * ldexpf(1.0f, qe - 14), 1e-37f);
             {
                 const uint32_t dst = smem_u32(s.q[i][0]) + r * 128;
 #pragma unroll 4
@@ -569,7 +580,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             // ---- this row's keys [lo, hi), and where all of this warp's rows see all
             const int lo = live ? lower(a, seq, t) : 0, hi = live ? upper(a, seq, t) : g.c1;
             const int safe0 = __reduce_max_sync(0xffffffffu, lo), safe1 = __reduce_min_sync(0xffffffffu, hi);
-            float m = -INFINITY, l = 0.0f, lowsum = 0.0f;
+            float m = -INFINITY, l = 0.0f, poison = 0.0f;  // reference, sum, what joins the outputs: 0 or NaN
             int vexp = 0;
             bool first = true;
             for (int tok = g.c0; ok && tok < g.c1; tok += kTok) {
@@ -577,34 +588,37 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after();
-                const float4 *kpar = reinterpret_cast<const float4 *>(s.kpar[par.stage]);
-                const float4 *vpar = reinterpret_cast<const float4 *>(s.vpar[par.stage]);
+                const uint4 *kpar = reinterpret_cast<const uint4 *>(s.kpar[par.stage]);
                 const int e_new = s.vexp[par.stage];
                 const uint32_t nan0 = s.vnan[par.stage][0] | s.vnan[par.stage][1] | s.vnan[par.stage][2] | s.vnan[par.stage][3];
                 // One step: logits, the reference, probabilities back to tensor memory.  `acc`
                 // holds its columns of S.
                 auto step = [&](int h, uint32_t (&acc)[kStep]) {
-                    float y[kStep], top = -INFINITY;
+                    float z[kStep], top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kStep; c += 2) {
-                        const float4 kp = kpar[(kStep * h + c) / 2];
-                        y[c] = fmaf(__uint_as_float(acc[c]), kp.x, kp.y * qsum);
-                        y[c + 1] = fmaf(__uint_as_float(acc[c + 1]), kp.z, kp.w * qsum);
+                    for (int c = 0; c < kStep; c += 4) {
+                        const uint4 kp = kpar[(kStep * h + c) / 4];
+                        const uint32_t w[4] = {kp.x, kp.y, kp.z, kp.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = __half22float2(as_half2(w[e]));
+                            z[c + e] = fmaf(__uint_as_float(acc[c + e]), f.x, f.y * qsum);
+                        }
                     }
                     const int t0 = tok + kStep * h;
                     if (t0 < safe0 || t0 + kStep > safe1) {
 #pragma unroll
                         for (int c = 0; c < kStep; ++c)
-                            if (t0 + c < lo || t0 + c >= hi) y[c] = -INFINITY;
+                            if (t0 + c < lo || t0 + c >= hi) z[c] = -INFINITY;
                     }
 #pragma unroll
-                    for (int c = 0; c < kStep; c += 2) top = fmaxf(top, fmaxf(y[c], y[c + 1]));
+                    for (int c = 0; c < kStep; c += 2) top = fmaxf(top, fmaxf(z[c], z[c + 1]));
+                    top *= unit;
                     if (__any_sync(0xffffffffu, top > m + kSlack) || e_new != vexp) {
                         const float mn = fmaxf(m, top);
                         const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
                         m = mn;
                         l *= f;
-                        lowsum *= f;
                         if (!first) {
                             // O is this warp's once the last step handed over is done
                             ok = h ? wait(&s.o_done[i][h - 1], count & 1) : wait(&s.o_done[i][kSteps - 1], (count - 1) & 1);
@@ -630,18 +644,15 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                     if (nan0 != 0) {
 #pragma unroll
                         for (int c = 0; c < kStep; ++c)
-                            if ((s.vnan[par.stage][h] >> c & 1) && y[c] != -INFINITY) lowsum = NAN;
+                            if ((s.vnan[par.stage][h] >> c & 1) && z[c] != -INFINITY) poison = NAN;
                     }
                     const float ref = m == -INFINITY ? 0.0f : m;
                     uint32_t p[kStep / 2];
 #pragma unroll
                     for (int c = 0; c < kStep; c += 2) {
-                        const float4 vp = vpar[(kStep * h + c) / 2];
-                        const float p0 = ex2(y[c] - ref), p1 = ex2(y[c + 1] - ref);
+                        const float p0 = ex2(fmaf(z[c], unit, -ref)), p1 = ex2(fmaf(z[c + 1], unit, -ref));
                         l += p0 + p1;
-                        lowsum = fmaf(p0, vp.y, lowsum);
-                        lowsum = fmaf(p1, vp.w, lowsum);
-                        p[c / 2] = pack_half2(p0 * vp.x, p1 * vp.z);
+                        p[c / 2] = pack_half2(p0, p1);
                     }
                     tmem_store16(ts + kStep / 2 * h, p);
                     tmem_store_wait();
@@ -668,7 +679,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 fence_after();
             }
             if (!ok) break;
-            const float back = ldexpf(1.0f, vexp - kStepBits), inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float back = ldexpf(1.0f, vexp), inv = l == 0.0f ? 0.0f : 1.0f / l;
             float *slot = a.part + (2 * (int64_t)blockIdx.x + (g.unit0 == 0 ? 1 : 0)) * (kChunkRows * (D + 2));
             T *out = reinterpret_cast<T *>(a.O) + (int64_t)(seq.q0 + t) * a.os_tok + (int64_t)hq * a.os_head;
 #pragma unroll 1
@@ -684,7 +695,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int d = (e & 1) * 4 + (e >> 1);
-                        f[d] = any ? fmaf(__uint_as_float(o[8 * x + e]), back, lowsum) : 0.0f;
+                        f[d] = any ? fmaf(__uint_as_float(o[8 * x + e]), back, poison) : 0.0f;
                     }
                     if (!live) continue;
                     if (!g.whole) {
