@@ -20,12 +20,10 @@
 // in it).  Tensor memory: S of both halves in columns 0 .. 255, O in 256 .. 511.
 //
 // K's scales stay outside its product, as in tm_kv4_attn.cu, so that logits keep fp32's
-// accuracy; a thread multiplies them in, one pair of fp16 numbers a token, read four
-// tokens at a time (every lane reads the same: shared memory returns 512 bytes for
-// 16, and with the scales of K and V as floats these reads alone took 4096 of a
-// tile's cycles).  V's are multiplied into its operand, which rounds each value to
-// fp16, off by 2^-11 of itself like the probabilities; the tile's exponent comes off
-// first, so that the rounding does not depend on V's size.
+// accuracy; a thread multiplies them in, two floats a token.  V's are multiplied into
+// its operand, which rounds each value to fp16, off by 2^-11 of itself like the
+// probabilities; the tile's exponent comes off first, so that the rounding does not
+// depend on V's size.
 //
 // A thread has a whole row, so its maximum and sums need no exchange.  The reference
 // maximum moves only where a logit passes it by 2^8 and the steps' exponent only past
@@ -56,7 +54,7 @@ struct ChunkSmem {
     alignas(1024) uint8_t q[2][D / 64][128 * 128];           // [half][panel]: 128 rows of 128 bytes
     alignas(1024) uint8_t op[kOpStages][D / 64 * 128 * 128];  // K tiles: panels as Q; V tiles: [8 tokens][panel]
     alignas(128) uint8_t raw[kRawStages][kTok / 16 * kv4_block_bytes(D)];
-    alignas(16) uint32_t kpar[kParStages][kTok];  // (step, low) of K
+    alignas(16) float2 kpar[kParStages][kTok];  // (step, low) of K
     float top[8];
     int vexp[kParStages];
     uint32_t vnan[kParStages][kTok / 32];  // tokens whose V is held as NaN
@@ -420,7 +418,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                     const uint8_t *blk = src + (t / 16) * BB;
                     // a token past the end has no scales (its bytes are whatever the ring held)
                     s.kpar[par.stage][t] =
-                        tok + t < g.end ? *reinterpret_cast<const uint32_t *>(blk + kv4_ks_off(D) + 4 * (t % 16)) : 0u;
+                        tok + t < g.end ? half2_at(blk + kv4_ks_off(D) + 4 * (t % 16)) : make_float2(0.0f, 0.0f);
                     if (t < kTok / 32) s.vnan[par.stage][t] = t == 0 ? nans[0] : t == 1 ? nans[1] : t == 2 ? nans[2] : nans[3];
                     if (t == 0) s.vexp[par.stage] = vexp;
                 }
@@ -588,7 +586,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after();
-                const uint4 *kpar = reinterpret_cast<const uint4 *>(s.kpar[par.stage]);
+                const float4 *kpar = reinterpret_cast<const float4 *>(s.kpar[par.stage]);
                 const int e_new = s.vexp[par.stage];
                 const uint32_t nan0 = s.vnan[par.stage][0] | s.vnan[par.stage][1] | s.vnan[par.stage][2] | s.vnan[par.stage][3];
                 // One step: logits, the reference, probabilities back to tensor memory.  `acc`
@@ -596,14 +594,10 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 auto step = [&](int h, uint32_t (&acc)[kStep]) {
                     float z[kStep], top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kStep; c += 4) {
-                        const uint4 kp = kpar[(kStep * h + c) / 4];
-                        const uint32_t w[4] = {kp.x, kp.y, kp.z, kp.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 f = __half22float2(as_half2(w[e]));
-                            z[c + e] = fmaf(__uint_as_float(acc[c + e]), f.x, f.y * qsum);
-                        }
+                    for (int c = 0; c < kStep; c += 2) {
+                        const float4 kp = kpar[(kStep * h + c) / 2];
+                        z[c] = fmaf(__uint_as_float(acc[c]), kp.x, kp.y * qsum);
+                        z[c + 1] = fmaf(__uint_as_float(acc[c + 1]), kp.z, kp.w * qsum);
                     }
                     const int t0 = tok + kStep * h;
                     if (t0 < safe0 || t0 + kStep > safe1) {
@@ -681,40 +675,66 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             if (!ok) break;
             const float back = ldexpf(1.0f, vexp), inv = l == 0.0f ? 0.0f : 1.0f / l;
             float *slot = a.part + (2 * (int64_t)blockIdx.x + (g.unit0 == 0 ? 1 : 0)) * (kChunkRows * (D + 2));
-            T *out = reinterpret_cast<T *>(a.O) + (int64_t)(seq.q0 + t) * a.os_tok + (int64_t)hq * a.os_head;
+            // O goes out through this warp's part of Q's shared memory (Q is done with, and is
+            // written again only after every thread has come to the next segment), D/2
+            // columns at a time, so that a warp writes whole rows.  The 16-byte pieces of row
+            // r lie at piece ^ (r & 7).
+            const uint32_t stage = smem_u32(s.q[i][0]) + (warp & 3) * (32 * (D / 2) * 4);
+            const float scale = g.whole ? back * inv : back, join = g.whole ? poison * inv : poison;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                if (any) {
-                    tmem_load(to + c, o);
-                    tmem_load_wait();
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float f[8];  // columns come in the order 0 4 1 5 2 6 3 7 of a word's dims
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int d = (e & 1) * 4 + (e >> 1);
-                        f[d] = any ? fmaf(__uint_as_float(o[8 * x + e]), back, poison) : 0.0f;
+            for (int c = 0; c < D; c += D / 2) {
+#pragma unroll 1
+                for (int cc = 0; cc < D / 2; cc += 32) {
+                    uint32_t o[32];
+                    if (any) {
+                        tmem_load(to + c + cc, o);
+                        tmem_load_wait();
                     }
-                    if (!live) continue;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float f[8];  // columns come in the order 0 4 1 5 2 6 3 7 of a word's dims
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[(e & 1) * 4 + (e >> 1)] = any ? fmaf(__uint_as_float(o[8 * x + e]), scale, join) : 0.0f;
+                        const int pc = (cc + 8 * x) / 4;
+                        const uint32_t at = stage + lane * (D / 2 * 4);
+                        st_shared(at + (pc ^ (lane & 7)) * 16, make_uint4(as_u(f[0]), as_u(f[1]), as_u(f[2]), as_u(f[3])));
+                        st_shared(at + ((pc + 1) ^ (lane & 7)) * 16, make_uint4(as_u(f[4]), as_u(f[5]), as_u(f[6]), as_u(f[7])));
+                    }
+                }
+                __syncwarp();
+                constexpr int kLanes = D / 2 / 8, kRowsIt = 32 / kLanes;  // 8 columns a lane
+                const int part = lane % kLanes;
+#pragma unroll 2
+                for (int x = 0; x < 32; x += kRowsIt) {
+                    const int rl = x + lane / kLanes, rw = 128 * i + (warp & 3) * 32 + rl;
+                    const uint32_t at = stage + rl * (D / 2 * 4);
+                    float f[8];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                     : "=f"(f[4 * y]), "=f"(f[4 * y + 1]), "=f"(f[4 * y + 2]), "=f"(f[4 * y + 3])
+                                     : "r"(at + ((2 * part + y) ^ (rl & 7)) * 16)
+                                     : "memory");
+                    if (rw >= g.rows) continue;
                     if (!g.whole) {
-                        float4 *q = reinterpret_cast<float4 *>(slot + row * D + c + 8 * x);
+                        float4 *q = reinterpret_cast<float4 *>(slot + rw * D + c + 8 * part);
                         q[0] = make_float4(f[0], f[1], f[2], f[3]);
                         q[1] = make_float4(f[4], f[5], f[6], f[7]);
                     } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] *= inv;
+                        const int fr = g.tile * kChunkRows + rw, tq = (int)fdiv(fr, a.by_group), hh = g.kvh * a.G + fr - tq * a.G;
+                        T *out = reinterpret_cast<T *>(a.O) + (int64_t)(seq.q0 + tq) * a.os_tok + (int64_t)hh * a.os_head + c + 8 * part;
                         Vec<T, 8> vo;
                         narrow(f, vo);
                         if (a.vec) {
-                            store_vec(out + c + 8 * x, vo);
+                            store_vec(out, vo);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) out[c + 8 * x + e] = vo.v[e];
+                            for (int e = 0; e < 8; ++e) out[e] = vo.v[e];
                         }
                     }
                 }
+                __syncwarp();
             }
             if (live && !g.whole) *reinterpret_cast<float2 *>(slot + kChunkRows * D + row * 2) = make_float2(m, l);
             if (live && g.whole && a.lse)
