@@ -59,7 +59,7 @@ struct ChunkSmem {
     int vexp[kParStages];
     uint32_t vnan[kParStages][kTok / 32];  // tokens whose V is held as NaN
     alignas(8) uint64_t raw_full[kRawStages], raw_free[kRawStages], op_full[kOpStages], op_free[kOpStages],
-        par_full[kParStages], par_free[kParStages], top_full, q_full, s_full[2], p_full[2][kSteps], o_done[2][kSteps], done;
+        par_full[kParStages], par_free[kParStages], top_full, q_full, s_full[2][2], p_full[2][kSteps], o_done[2][kSteps], done;
     uint32_t tmem;
     int abort;
 };
@@ -137,6 +137,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t db, uint
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(db), "r"(id), "r"((uint32_t)acc)
         : "memory");
+}
+// One lane of the warp, the same at every call.  (The compiler knows that code under
+// this has one active lane and keeps descriptors in uniform registers; under
+// `lane == 0` it moved them there for every product, 200 cycles each.)
+__device__ __forceinline__ bool elect()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e)::"memory");
+    return e != 0;
 }
 __device__ __forceinline__ void commit(uint64_t *b)
 {
@@ -233,7 +242,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         }
         for (int i = 0; i < kOpStages; ++i) {
             bar_init(&s.op_full[i], kUnpackWarps * 32);
-            bar_init(&s.op_free[i], 1);
+            bar_init(&s.op_free[i], 2);
         }
         for (int i = 0; i < kParStages; ++i) {
             bar_init(&s.par_full[i], kUnpackWarps * 32);
@@ -244,13 +253,14 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         // [half of the rows][step of a tile's tokens]: each completes once a tile, so the
         // parity of the tile's number tells a completion from the one before
         for (int i = 0; i < 2; ++i) {
-            bar_init(&s.s_full[i], 1);
+            bar_init(&s.s_full[i][0], 1);
+            bar_init(&s.s_full[i][1], 1);
             for (int h = 0; h < kSteps; ++h) {
                 bar_init(&s.p_full[i][h], 128);
                 bar_init(&s.o_done[i][h], 1);
             }
         }
-        bar_init(&s.done, 1);
+        bar_init(&s.done, 2);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s.abort = 0;
     }
@@ -312,70 +322,83 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         const uint32_t first = issued > kRawStages ? issued - kRawStages : 0;
         for (uint32_t i = first; i < issued; ++i)
             mbar_wait_bounded(smem_u32(&s.raw_full[i % kRawStages]), (i / kRawStages) & 1);
-    } else if (warp == 12) {
-        if (lane == 0) {
-            // ---------------- MMA issuer
-            constexpr uint32_t id_s = idesc_f16(128, kTok, false), id_o = idesc_f16(128, D, true);
-            Turn op;
-            uint32_t segs = 0, count = 0;  // segments with tokens, tiles
-            bool ok = true;
-            auto score = [&](int half, uint32_t stage) {
-                const uint32_t q = smem_u32(s.q[half][0]), k = smem_u32(s.op[stage]);
+    } else if (warp == 12 || warp == 14) {
+        // ---------------- MMA issuers, one for each half of the rows: the warp together, one lane
+        // of it issuing
+        const int i = __shfl_sync(0xffffffffu, (warp - 12) / 2, 0);
+        constexpr uint32_t id_s = idesc_f16(128, kTok / 2, false), id_o = idesc_f16(128, D, true);
+        const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0), acc_s = base + kS + 128 * i, acc_o = base + kO + 128 * i;
+        const uint64_t q = desc_k(smem_u32(s.q[i][0]));
+        const uint32_t ops = smem_u32(s.op[0]);
+        constexpr uint32_t kOpBytes = sizeof(s.op[0]);
+        auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(b, parity, abort, a.status)) != 0; };
+        Turn k;                        // the next K
+        uint32_t segs = 0, count = 0;  // segments with tokens, tiles
+        bool ok = true;
+        // S for the first or second 64 tokens of the tile whose K is at `at`
+        auto score = [&](int part, Turn at) {
+            const uint64_t kd = desc_k(ops + at.stage * kOpBytes + part * (kTok / 2 * 128));
+            if (elect()) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    mma_ss(tmem + kS + 128 * half, desc_k(q + (i / 4) * 16384 + (i % 4) * 32),
-                           desc_k(k + (i / 4) * 16384 + (i % 4) * 32), id_s, i > 0);
-                commit(&s.s_full[half]);
-            };
-            while (ok && run.pos < run.stop) {
-                const Segment g = next_segment(a, kChunkRows, run);
-                run.pos += g.count;
-                const int tiles = (g.c1 - g.c0 + kTok - 1) / kTok;
-                if (tiles == 0) continue;
-                if (!wait(&s.q_full, segs & 1)) break;
-                ++segs;
-                ok = wait(&s.op_full[op.stage], op.phase);
-                if (!ok) break;
-                fence_after();
-                score(0, op.stage);
-                score(1, op.stage);
-                commit(&s.op_free[op.stage]);
-                op.next(kOpStages);
-                for (int t = 0; ok && t < tiles; ++t, ++count) {
-                    const Turn v = op;
-                    op.next(kOpStages);
-                    const Turn k = op;  // the next tile's K
-                    for (int h = 0; ok && h < kSteps; ++h)
-                        for (int i = 0; ok && i < 2; ++i) {
-                            if (h == 0 && i == 0) ok = wait(&s.op_full[v.stage], v.phase);
-                            ok = ok && wait(&s.p_full[i][h], count & 1);
-                            if (!ok) break;
-                            fence_after();
-                            const uint32_t vs = smem_u32(s.op[v.stage]) + h * (kStep / 8) * PANELS * 1024;
+                for (int x = 0; x < D / 16; ++x)
+                    mma_ss(acc_s + 64 * part, q + (x / 4) * 1024 + (x % 4) * 2, kd + (x / 4) * 1024 + (x % 4) * 2, id_s, x > 0);
+                commit(&s.s_full[i][part]);
+                if (part == 1) commit(&s.op_free[at.stage]);
+            }
+        };
+        while (__any_sync(0xffffffffu, ok && run.pos < run.stop)) {
+            const Segment g = next_segment(a, kChunkRows, run);
+            run.pos += g.count;
+            const int tiles = __shfl_sync(0xffffffffu, (g.c1 - g.c0 + kTok - 1) / kTok, 0);
+            if (tiles == 0) continue;
+            ok = wait(&s.q_full, segs & 1) && wait(&s.op_full[k.stage], k.phase);
+            if (!ok) break;
+            ++segs;
+            fence_after();
+            score(0, k);
+            for (int t = 0; t < tiles; ++t, ++count) {
+                const Turn k0 = k;  // this tile's K
+                Turn v = k;
+                v.next(kOpStages);
+                k = v;
+                k.next(kOpStages);  // the next tile's
+                const uint64_t vd = desc_mn(ops + v.stage * kOpBytes, 1024, PANELS * 1024);
 #pragma unroll
-                            for (int x = 0; x < kStep / 16; ++x)
-                                mma_ts(tmem + kO + 128 * i, tmem + kS + 128 * i + kStep / 2 * h + 8 * x,
-                                       desc_mn(vs + x * 2 * PANELS * 1024, 1024, PANELS * 1024), id_o, t > 0 || h > 0 || x > 0);
-                            commit(&s.o_done[i][h]);
-                            if (h == kSteps - 1 && i == 1) commit(&s.op_free[v.stage]);
-                            if (h == kSteps - 1 && t + 1 < tiles) {
-                                // S goes where this P came from: after the product that reads it
-                                if (i == 0) ok = wait(&s.op_full[k.stage], k.phase);
-                                ok = ok && wait(&s.o_done[i][kSteps - 1], count & 1);
-                                if (!ok) break;
-                                fence_after();
-                                score(i, k.stage);
-                                if (i == 1) commit(&s.op_free[k.stage]);
-                            }
-                        }
-                    if (t + 1 < tiles) op.next(kOpStages);
+                for (int h = 0; h < kSteps; ++h) {
+                    // S is made half a tile ahead of the softmax, into the columns whose P is done
+                    // with: the second half of this tile, while the softmax is at the first, then the
+                    // first half of the next
+                    if (h == 0) {
+                        ok = t == 0 || wait(&s.o_done[i][kSteps - 1], (count - 1) & 1);
+                        if (!ok) break;
+                        fence_after();
+                        score(1, k0);
+                    } else if (h == 2 && t + 1 < tiles) {
+                        ok = wait(&s.op_full[k.stage], k.phase) && wait(&s.o_done[i][1], count & 1);
+                        if (!ok) break;
+                        fence_after();
+                        score(0, k);
+                    }
+                    if (h == 0) ok = ok && wait(&s.op_full[v.stage], v.phase);
+                    ok = ok && wait(&s.p_full[i][h], count & 1);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect()) {
+#pragma unroll
+                        for (int x = 0; x < kStep / 16; ++x)
+                            mma_ts(acc_o, acc_s + 64 * (h / 2) + kStep / 2 * (h % 2) + 8 * x, vd + (h * (kStep / 8) + 2 * x) * (PANELS * 64), id_o,
+                                   h > 0 || x > 0 || t > 0);
+                        commit(&s.o_done[i][h]);
+                        if (h == kSteps - 1) commit(&s.op_free[v.stage]);
+                    }
                 }
+                if (!ok) break;
             }
-            commit(&s.done);  // every product issued, also after an abort
-            if (!mbar_wait_bounded(smem_u32(&s.done), 0)) {
-                *abort = 1;
-                atomicOr(a.status, kStatusTimeout);
-            }
+        }
+        if (elect()) commit(&s.done);  // every product issued, also after an abort
+        if (!mbar_wait_bounded(smem_u32(&s.done), 0)) {
+            *abort = 1;
+            atomicOr(a.status, kStatusTimeout);
         }
     } else if (warp < 12) {
         // ---------------- unpack
@@ -582,10 +605,9 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             int vexp = 0;
             bool first = true;
             for (int tok = g.c0; ok && tok < g.c1; tok += kTok) {
-                ok = wait(&s.s_full[i], count & 1) && wait(&s.par_full[par.stage], par.phase);
+                ok = wait(&s.par_full[par.stage], par.phase);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                fence_after();
                 const float4 *kpar = reinterpret_cast<const float4 *>(s.kpar[par.stage]);
                 const int e_new = s.vexp[par.stage];
                 const uint32_t nan0 = s.vnan[par.stage][0] | s.vnan[par.stage][1] | s.vnan[par.stage][2] | s.vnan[par.stage][3];
@@ -648,13 +670,18 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                         l += p0 + p1;
                         p[c / 2] = pack_half2(p0, p1);
                     }
-                    tmem_store16(ts + kStep / 2 * h, p);
+                    tmem_store16(ts + 64 * (h / 2) + kStep / 2 * (h % 2), p);
                     tmem_store_wait();
                     fence_before();
                     bar_arrive(&s.p_full[i][h]);
                 };
 #pragma unroll 1
                 for (int h = 0; ok && h < kSteps; ++h) {
+                    if (h % 2 == 0) {
+                        ok = __all_sync(0xffffffffu, wait(&s.s_full[i][h / 2], count & 1));
+                        if (!ok) break;
+                        fence_after();
+                    }
                     uint32_t acc[kStep];
                     tmem_load(ts + kStep * h, acc);
                     tmem_load_wait();
