@@ -537,65 +537,84 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             const int row = 128 * i + r, full_row = g.tile * kChunkRows + row;
             const bool live = row < g.rows;
             const int t = live ? (int)fdiv(full_row, a.by_group) : 0, hq = g.kvh * a.G + full_row - t * a.G;
-            // ---- Q: this row, scaled by a power of two common to the tile, into shared memory
-            const T *qp = reinterpret_cast<const T *>(a.Q) + (int64_t)(seq.q0 + t) * a.qs_tok + (int64_t)hq * a.qs_head;
-            auto load_q = [&](int x, Vec<T, 8> &v) {
-                if (!live) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v.v[e] = from_f<T>(0.0f);
-                } else if (a.vec) {
-                    v = *reinterpret_cast<const Vec<T, 8> *>(qp + 8 * x);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v.v[e] = qp[8 * x + e];
-                }
-            };
-            float top = 0.0f;
-#pragma unroll 4
-            for (int x = 0; x < D / 8; ++x) {
-                Vec<T, 8> v;
-                load_q(x, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(v.v[e])));
-            }
+            // ---- Q into shared memory, a warp its own 32 rows; then a thread its row: scaled by a
+            // power of two common to the tile, in place
             const bool any = g.c1 > g.c0;
             float qsum = 0.0f, unit = 1.0f;  // logits in base 2 are z unit
+            const uint32_t rows_at = smem_u32(s.q[i][0]) + (warp & 3) * (32 * 128);
+            // the 16 bytes x of row rl of this warp's
+            auto piece = [&](int rl, int x) { return rows_at + rl * 128 + (x / 8) * 16384 + ((x % 8) ^ (rl & 7)) * 16; };
+            auto lds = [](uint32_t at, uint32_t *w) {
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(at)
+                             : "memory");
+            };
             if (any) {
-            top = lanes_max(top, 32);
-            if (lane == 0) s.top[warp] = top;
-            bar_arrive(&s.top_full);
-            ok = wait(&s.top_full, segs & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ++segs;
+                if (a.vec) {
+                    constexpr int kLanes = D / 8;
+                    const int x = lane % kLanes;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) top = fmaxf(top, s.top[x]);
-            const int qe = max(-100, min((int)(__float_as_uint(top) >> 23) - 127, 127));
-            // (a negative scale turns q's sign: z below then grows with the logit)
-            const float up = copysignf(ldexpf(1.0f, 14 - qe), a.scale);
-            unit = fmaxf(fabsf(a.scale) * kLog2eF * ldexpf(1.0f, qe - 14), 1e-37f);
-            {
-                const uint32_t dst = smem_u32(s.q[i][0]) + r * 128;
+                    for (int r0 = 0; r0 < 32; r0 += 32 / kLanes) {
+                        const int rl = r0 + lane / kLanes, rw = 128 * i + (warp & 3) * 32 + rl;
+                        const int fr = g.tile * kChunkRows + min(rw, g.rows - 1);
+                        const int tq = (int)fdiv(fr, a.by_group), hh = g.kvh * a.G + fr - tq * a.G;
+                        const T *p = reinterpret_cast<const T *>(a.Q) + (int64_t)(seq.q0 + tq) * a.qs_tok + (int64_t)hh * a.qs_head + 8 * x;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(piece(rl, x)), "l"(p), "r"(rw < g.rows ? 16 : 0)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    __syncwarp();
+                } else {
+                    const T *p = reinterpret_cast<const T *>(a.Q) + (int64_t)(seq.q0 + t) * a.qs_tok + (int64_t)hq * a.qs_head;
+#pragma unroll 1
+                    for (int x = 0; x < D / 8; ++x) {
+                        Vec<T, 8> v;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v.v[e] = live ? p[8 * x + e] : from_f<T>(0.0f);
+                        const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+                        st_shared(piece(lane, x), make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                }
+                float top = 0.0f;
+#pragma unroll 4
+                for (int x = 0; x < D / 8; ++x) {
+                    Vec<T, 8> v;
+                    lds(piece(lane, x), reinterpret_cast<uint32_t *>(&v));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(v.v[e])));
+                }
+                top = lanes_max(top, 32);
+                if (lane == 0) s.top[warp] = top;
+                bar_arrive(&s.top_full);
+                ok = wait(&s.top_full, segs & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++segs;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) top = fmaxf(top, s.top[x]);
+                const int qe = max(-100, min((int)(__float_as_uint(top) >> 23) - 127, 127));
+                // (a negative scale turns q's sign: z below then grows with the logit)
+                const float up = copysignf(ldexpf(1.0f, 14 - qe), a.scale);
+                unit = fmaxf(fabsf(a.scale) * kLog2eF * ldexpf(1.0f, qe - 14), 1e-37f);
 #pragma unroll 4
                 for (int x = 0; x < D / 8; ++x) {
                     Vec<T, 8> v;
                     float f[8];
-                    load_q(x, v);  // (a second time: held, the row would take 64 registers)
+                    lds(piece(lane, x), reinterpret_cast<uint32_t *>(&v));
                     widen(v, f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         f[e] *= up;
                         qsum += f[e];
                     }
-                    st_shared(dst + (x / 8) * 16384 + ((x % 8) ^ (r & 7)) * 16,
-                              make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
-                                         pack_half2(f[3], f[7])));
+                    st_shared(piece(lane, x), make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
+                                                         pack_half2(f[3], f[7])));
                 }
-            }
-            fence_async();
-            bar_arrive(&s.q_full);
-            // (s.top is written again only after this segment's products, which need every
-            // thread to have come here)
+                fence_async();
+                bar_arrive(&s.q_full);
+                // (s.top is written again only after this segment's products, which need every
+                // thread to have come here)
             }
 
             // ---- this row's keys [lo, hi), and where all of this warp's rows see all
@@ -702,11 +721,8 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             if (!ok) break;
             const float back = ldexpf(1.0f, vexp), inv = l == 0.0f ? 0.0f : 1.0f / l;
             float *slot = a.part + (2 * (int64_t)blockIdx.x + (g.unit0 == 0 ? 1 : 0)) * (kChunkRows * (D + 2));
-            // O goes out through this warp's part of Q's shared memory (Q is done with, and is
-            // written again only after every thread has come to the next segment), D/2
-            // columns at a time, so that a warp writes whole rows.  The 16-byte pieces of row
-            // r lie at piece ^ (r & 7).
-            const uint32_t stage = smem_u32(s.q[i][0]) + (warp & 3) * (32 * (D / 2) * 4);
+            // O goes out through this warp's rows of Q's shared memory (which the products are done
+            // with), D/2 columns at a time, so that a warp writes whole rows
             const float scale = g.whole ? back * inv : back, join = g.whole ? poison * inv : poison;
 #pragma unroll 1
             for (int c = 0; c < D; c += D / 2) {
@@ -723,10 +739,9 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             f[(e & 1) * 4 + (e >> 1)] = any ? fmaf(__uint_as_float(o[8 * x + e]), scale, join) : 0.0f;
-                        const int pc = (cc + 8 * x) / 4;
-                        const uint32_t at = stage + lane * (D / 2 * 4);
-                        st_shared(at + (pc ^ (lane & 7)) * 16, make_uint4(as_u(f[0]), as_u(f[1]), as_u(f[2]), as_u(f[3])));
-                        st_shared(at + ((pc + 1) ^ (lane & 7)) * 16, make_uint4(as_u(f[4]), as_u(f[5]), as_u(f[6]), as_u(f[7])));
+                        const int pc = cc / 4 + 2 * x;
+                        st_shared(piece(lane, pc), make_uint4(as_u(f[0]), as_u(f[1]), as_u(f[2]), as_u(f[3])));
+                        st_shared(piece(lane, pc + 1), make_uint4(as_u(f[4]), as_u(f[5]), as_u(f[6]), as_u(f[7])));
                     }
                 }
                 __syncwarp();
@@ -735,14 +750,9 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
 #pragma unroll 2
                 for (int x = 0; x < 32; x += kRowsIt) {
                     const int rl = x + lane / kLanes, rw = 128 * i + (warp & 3) * 32 + rl;
-                    const uint32_t at = stage + rl * (D / 2 * 4);
                     float f[8];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                     : "=f"(f[4 * y]), "=f"(f[4 * y + 1]), "=f"(f[4 * y + 2]), "=f"(f[4 * y + 3])
-                                     : "r"(at + ((2 * part + y) ^ (rl & 7)) * 16)
-                                     : "memory");
+                    lds(piece(rl, 2 * part), reinterpret_cast<uint32_t *>(f));
+                    lds(piece(rl, 2 * part + 1), reinterpret_cast<uint32_t *>(f + 4));
                     if (rw >= g.rows) continue;
                     if (!g.whole) {
                         float4 *q = reinterpret_cast<float4 *>(slot + rw * D + c + 8 * part);
