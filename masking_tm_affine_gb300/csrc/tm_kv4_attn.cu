@@ -627,18 +627,18 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 // every W-th partial with a running maximum of its own, a lane D/32 dims; then a row's
 // warps in order.  Items with few partials (many items) take a warp a row, few items
 // with many partials all eight.
-// U: partials a warp has in flight.
-template <typename T, int D, int U>
+// U: partials of a row a warp has in flight.  R: rows a warp has, all in flight (W = 1).
+template <typename T, int D, int U, int R>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ AttnArgs a, int rows_of_tile, int W)
 {
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, F = E < 4 ? E : 4;
     __shared__ float sums[8][D], stat[8][2];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows_here = 8 / W, sub = warp % W;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows_here = 8 / W * R, sub = warp % W;
     // blockIdx.x = ((b * Hkv + kvh) * row_tiles + tile) * (rows_of_tile / rows_here) + part
     const unsigned parts = rows_of_tile / rows_here, item = blockIdx.x / parts;
-    const int row = (int)(blockIdx.x - item * parts) * rows_here + warp / W;
+    const int row = (int)(blockIdx.x - item * parts) * rows_here + warp / W;  // and every 8th after it
     const int2 job = a.job[item];
     const unsigned bh = item / a.row_tiles;
     const int tile = (int)(item - bh * a.row_tiles), b = (int)(bh / a.Hkv), kvh = (int)(bh - b * a.Hkv);
@@ -649,74 +649,94 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ A
     const int stride = rows_of_tile * (D + 2);
     // partial p: the item's first block holds it in its slot 1, the others in slot 0
     const float *first = a.part + (int64_t)2 * job.x * stride;
-    float mm = -INFINITY, ll = 0.0f, v[E];
+    float mm[R], ll[R], v[R][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.0f;
+    for (int r = 0; r < R; ++r) {
+        mm[r] = -INFINITY;
+        ll[r] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[r][e] = 0.0f;
+    }
     for (int p0 = sub; p0 < n; p0 += U * W) {
-        float x[U][E];
-        float2 ms[U];
-        float top = mm;
+        Vec<float, F> x[R][U][E / F];
+        float2 ms[R][U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int p = p0 + u * W;
-            ms[u] = make_float2(-INFINITY, 0.0f);
+            const float *q = first + (int64_t)(p == 0 ? 1 : 2 * p) * stride;
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
-            if (p < n) {
-                const float *q = first + (int64_t)(p == 0 ? 1 : 2 * p) * stride;
-                ms[u] = *reinterpret_cast<const float2 *>(q + rows_of_tile * D + row * 2);
+            for (int r = 0; r < R; ++r) {
+                ms[r][u] = make_float2(-INFINITY, 0.0f);
+                if (p < n) ms[r][u] = *reinterpret_cast<const float2 *>(q + rows_of_tile * D + (row + 8 * r) * 2);
 #pragma unroll
-                for (int e = 0; e < E; e += 2)
-                    *reinterpret_cast<float2 *>(x[u] + e) = *reinterpret_cast<const float2 *>(q + row * D + lane * E + e);
+                for (int e = 0; e < E / F; ++e)
+                    if (p < n)
+                        x[r][u][e] = *reinterpret_cast<const Vec<float, F> *>(q + (row + 8 * r) * D + lane * E + e * F);
+                    else
+                        x[r][u][e] = {};
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) top = fmaxf(top, ms[u].x);
-        const float f0 = mm == -INFINITY ? 1.0f : ex2(mm - top);
-        ll *= f0;
+        for (int r = 0; r < R; ++r) {
+            float top = mm[r];
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= f0;
-        mm = top;
+            for (int u = 0; u < U; ++u) top = fmaxf(top, ms[r][u].x);
+            const float f0 = mm[r] == -INFINITY ? 1.0f : ex2(mm[r] - top);
+            ll[r] *= f0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const float f = ms[u].x == -INFINITY ? 1.0f : ex2(ms[u].x - mm);  // a share that saw nothing holds zeros
-            ll = fmaf(ms[u].y, f, ll);
+            for (int e = 0; e < E; ++e) v[r][e] *= f0;
+            mm[r] = top;
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = fmaf(x[u][e], f, v[e]);
+            for (int u = 0; u < U; ++u) {
+                const float f = ms[r][u].x == -INFINITY ? 1.0f : ex2(ms[r][u].x - top);  // a share that saw nothing holds zeros
+                ll[r] = fmaf(ms[r][u].y, f, ll[r]);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[r][e] = fmaf(x[r][u][e / F].v[e % F], f, v[r][e]);
+            }
         }
     }
-    if (W > 1) {
+    if (W > 1) {  // (R = 1)
 #pragma unroll
-        for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = v[e];
+        for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = v[0][e];
         if (lane == 0) {
-            stat[warp][0] = mm;
-            stat[warp][1] = ll;
+            stat[warp][0] = mm[0];
+            stat[warp][1] = ll[0];
         }
         __syncthreads();
         if (sub != 0) return;
-        float top = mm;
+        float top = mm[0];
         for (int w = 1; w < W; ++w) top = fmaxf(top, stat[warp + w][0]);
-        const float f0 = mm == -INFINITY ? 1.0f : ex2(mm - top);
-        ll *= f0;
+        const float f0 = mm[0] == -INFINITY ? 1.0f : ex2(mm[0] - top);
+        ll[0] *= f0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= f0;
+        for (int e = 0; e < E; ++e) v[0][e] *= f0;
         for (int w = 1; w < W; ++w) {
             const float mw = stat[warp + w][0], f = mw == -INFINITY ? 1.0f : ex2(mw - top);
-            ll = fmaf(stat[warp + w][1], f, ll);
+            ll[0] = fmaf(stat[warp + w][1], f, ll[0]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = fmaf(sums[warp + w][lane * E + e], f, v[e]);
+            for (int e = 0; e < E; ++e) v[0][e] = fmaf(sums[warp + w][lane * E + e], f, v[0][e]);
         }
-        mm = top;
+        mm[0] = top;
     }
-    const int full_row = tile * rows_of_tile + row;
-    if (full_row >= seq.n * a.G) return;
-    const int t = (int)fdiv(full_row, a.by_group), hq = kvh * a.G + full_row - t * a.G;
-    const int64_t q = (int64_t)(seq.q0 + t) * a.Hq + hq;
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-    T *out = reinterpret_cast<T *>(a.O) + (int64_t)(seq.q0 + t) * a.os_tok + hq * a.os_head + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = from_f<T>(v[e] * inv);
-    if (lane == 0 && a.lse) a.lse[q] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    for (int r = 0; r < R; ++r) {
+        const int full_row = tile * rows_of_tile + row + 8 * r;
+        if (full_row >= seq.n * a.G) return;
+        const int t = (int)fdiv(full_row, a.by_group), hq = kvh * a.G + full_row - t * a.G;
+        const int64_t q = (int64_t)(seq.q0 + t) * a.Hq + hq;
+        const float inv = ll[r] == 0.0f ? 0.0f : 1.0f / ll[r];
+        T *out = reinterpret_cast<T *>(a.O) + (int64_t)(seq.q0 + t) * a.os_tok + hq * a.os_head + lane * E;
+        if (a.vec && E * sizeof(T) <= 16) {
+            Vec<T, E> o;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o.v[e] = from_f<T>(v[r][e] * inv);
+            store_vec(out, o);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) out[e] = from_f<T>(v[r][e] * inv);
+        }
+        if (lane == 0 && a.lse) a.lse[q] = ll[r] == 0.0f ? -INFINITY : (mm[r] + log2f(ll[r])) * kLn2;
+    }
 }
 
 // Column tiles for a sequence's rows (its queries x the heads of a group).
@@ -736,12 +756,26 @@ size_t attn_workspace(int32_t B, int32_t max_q, int32_t Hq, int32_t Hkv, int32_t
 }
 
 template <typename T, int D>
-tm_status join_items(AttnArgs &a, int rows_of_tile, int W, cudaStream_t s)
+tm_status join_items(AttnArgs &a, int rows_of_tile, int sms, cudaStream_t s)
 {
     const int64_t items = (int64_t)a.B * a.Hkv * a.row_tiles;
+    int W = 1, rows = 1;  // warps of a row, rows of a warp
+    const void *k = (const void *)kv4_join_kernel<T, D, D == 256 ? 4 : 8, 1>;
+    if constexpr (sizeof(T) == 2 && D != 256) {
+        // An item has about sms / items + 1 partials.  256 rows a tile, D 128, the whole call:
+        // 64 items 87.7 us with four rows a warp, 90.5 with eight partials of one; 32 items
+        // 67.7 against 64.0; 16 items 55.9 against 45.4.
+        if (rows_of_tile == kChunkRows && 4 * items >= sms) {
+            k = (const void *)kv4_join_kernel<T, D, 2, 4>;
+            rows = 4;
+        }
+    }
+    if (rows_of_tile != kChunkRows) {
+        W = items >= sms ? 1 : 8;
+        if (W == 1) k = (const void *)kv4_join_kernel<T, D, 2, 1>;
+    }
     void *jargs[] = {(void *)&a, &rows_of_tile, &W};
-    const void *k = W == 1 ? (const void *)kv4_join_kernel<T, D, 2> : (const void *)kv4_join_kernel<T, D, D == 256 ? 4 : 8>;
-    return launch_dependent(k, dim3((unsigned)(items * rows_of_tile / (8 / W))), dim3(256), jargs, 0, s);
+    return launch_dependent(k, dim3((unsigned)(items * rows_of_tile / (8 / W * rows))), dim3(256), jargs, 0, s);
 }
 
 template <typename T, int D, int NT>
@@ -761,7 +795,7 @@ tm_status launch_attn(AttnArgs &a, int dev, int sms, bool join, cudaStream_t s, 
     void *args[] = {(void *)&a};
     tm_status st = launch_kernel(k, dim3((unsigned)blocks), dim3(kWarps * 32), args, attn_smem<D>(), s, pdl);
     if (st != TM_OK || !join) return st;
-    return join_items<T, D>(a, NT * 8, (int64_t)a.B * a.Hkv * a.row_tiles >= sms ? 1 : 8, s);
+    return join_items<T, D>(a, NT * 8, sms, s);
 }
 
 template <typename T>
@@ -785,11 +819,11 @@ bool attn_shape_ok(int32_t B, int64_t Tq, int32_t max_q, int64_t max_len, int32_
 
 }  // namespace
 
-tm_status launch_attn_join(int D, int32_t xtype, AttnArgs &a, int rows_of_tile, int W, cudaStream_t s)
+tm_status launch_chunk_join(int D, int32_t xtype, AttnArgs &a, int sms, cudaStream_t s)
 {
-    if (xtype == TM_F16) return D == 64 ? join_items<__half, 64>(a, rows_of_tile, W, s) : join_items<__half, 128>(a, rows_of_tile, W, s);
-    return D == 64 ? join_items<__nv_bfloat16, 64>(a, rows_of_tile, W, s)
-                   : join_items<__nv_bfloat16, 128>(a, rows_of_tile, W, s);
+    if (xtype == TM_F16) return D == 64 ? join_items<__half, 64>(a, kChunkRows, sms, s) : join_items<__half, 128>(a, kChunkRows, sms, s);
+    return D == 64 ? join_items<__nv_bfloat16, 64>(a, kChunkRows, sms, s)
+                   : join_items<__nv_bfloat16, 128>(a, kChunkRows, sms, s);
 }
 
 }  // namespace libtm

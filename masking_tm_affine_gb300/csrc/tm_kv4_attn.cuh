@@ -215,7 +215,7 @@ bool chunk_attn_fits(int32_t xtype, int64_t rows, int D);
 size_t chunk_attn_slots_bytes(int D);
 constexpr int kChunkRows = 256;  // its row tile
 
-// The join of partial outputs (tm_kv4_attn.cu).
-tm_status launch_attn_join(int D, int32_t xtype, AttnArgs &a, int rows_of_tile, int W, cudaStream_t s);
+// The join of its partial outputs (tm_kv4_attn.cu).
+tm_status launch_chunk_join(int D, int32_t xtype, AttnArgs &a, int sms, cudaStream_t s);
 
 }  // namespace libtm

@@ -44,7 +44,7 @@ constexpr int kStep = 32, kSteps = kTok / kStep;  // tokens of one step of the s
 constexpr int kUnpackWarps = 4;
 constexpr int kThreads2 = 16 * 32;   // warps 0-7 softmax, 8-11 unpack, 12 MMA, 13 loader (14, 15 idle)
 // Registers: 128 a thread at launch (all there are); the softmax warps, which hold 64
-// logits of a row, take what the others give: 2 x 168 + 2 x 88 = 4 x 128.
+// logits of a row, take what the others give: 2 x 152 + 2 x 104 = 4 x 128.
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "register shares");
 constexpr int kRawStages = 2, kOpStages = 3, kParStages = 2;
@@ -54,7 +54,7 @@ struct ChunkSmem {
     alignas(1024) uint8_t q[2][D / 64][128 * 128];           // [half][panel]: 128 rows of 128 bytes
     alignas(1024) uint8_t op[kOpStages][D / 64 * 128 * 128];  // K tiles: panels as Q; V tiles: [8 tokens][panel]
     alignas(128) uint8_t raw[kRawStages][kTok / 16 * kv4_block_bytes(D)];
-    alignas(16) float2 kpar[kParStages][kTok];  // (step, low) of K
+    alignas(16) float kpar[kParStages][kTok / 2][4];  // K's scales, two tokens at a time: steps, lows
     float top[8];
     int vexp[kParStages];
     uint32_t vnan[kParStages][kTok / 32];  // tokens whose V is held as NaN
@@ -165,6 +165,16 @@ __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t *r)
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
+// The loads' end, for registers that were named before it.
+__device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+          "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+          "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+          "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
 __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t *r)
 {
     asm volatile(
@@ -207,6 +217,38 @@ __device__ __forceinline__ uint4 scaled8(uint4 c, __half2 step, __half2 low)
 {
     return make_uint4(as_bits(__hfma2(as_half2(c.x), step, low)), as_bits(__hfma2(as_half2(c.y), step, low)),
                       as_bits(__hfma2(as_half2(c.z), step, low)), as_bits(__hfma2(as_half2(c.w), step, low)));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(uint64_t p)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 __device__ __forceinline__ void st_shared(uint32_t at, uint4 v)
@@ -440,8 +482,9 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 {
                     const uint8_t *blk = src + (t / 16) * BB;
                     // a token past the end has no scales (its bytes are whatever the ring held)
-                    s.kpar[par.stage][t] =
-                        tok + t < g.end ? half2_at(blk + kv4_ks_off(D) + 4 * (t % 16)) : make_float2(0.0f, 0.0f);
+                    const float2 kp = tok + t < g.end ? half2_at(blk + kv4_ks_off(D) + 4 * (t % 16)) : make_float2(0.0f, 0.0f);
+                    s.kpar[par.stage][t / 2][t % 2] = kp.x;
+                    s.kpar[par.stage][t / 2][2 + t % 2] = kp.y;
                     if (t < kTok / 32) s.vnan[par.stage][t] = t == 0 ? nans[0] : t == 1 ? nans[1] : t == 2 ? nans[2] : nans[3];
                     if (t == 0) s.vexp[par.stage] = vexp;
                 }
@@ -456,7 +499,8 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 {
                     const int j = lane >> 3, gr = lane & 7;
                     constexpr int LW = D / 32;  // words of a quarter row
-#pragma unroll
+                    // (rolled: the four roles' loops share the instruction caches)
+#pragma unroll 1
                     for (int i = 0; i < kTok / 8 / kUnpackWarps; ++i) {
                         const int row = w * (kTok / kUnpackWarps) + i * 8 + gr;
                         const uint8_t *p = src + (row / 16) * BB + (row % 16) * (D / 2) + j * (D / 8);
@@ -483,7 +527,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 {
                     const int r = lane & 7, pr = lane >> 3;
                     constexpr int LW = D / 64;  // words a token has in a slice
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < kTok / 8 / kUnpackWarps; ++i) {
                         const int pair = w * (kTok / 2 / kUnpackWarps) + i * 4 + pr;  // of 64
                         const uint8_t *p = src + (pair / 8) * BB + kv4_v_off(D) + (pair % 8) * D + r * (D / 8);
@@ -637,8 +681,10 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
 #pragma unroll
                     for (int c = 0; c < kStep; c += 2) {
                         const float4 kp = kpar[(kStep * h + c) / 2];
-                        z[c] = fmaf(__uint_as_float(acc[c]), kp.x, kp.y * qsum);
-                        z[c + 1] = fmaf(__uint_as_float(acc[c + 1]), kp.z, kp.w * qsum);
+                        const float2 zz = both(fma2(pair2(__uint_as_float(acc[c]), __uint_as_float(acc[c + 1])), pair2(kp.x, kp.y),
+                                                    mul2(pair2(kp.z, kp.w), pair2(qsum, qsum))));
+                        z[c] = zz.x;
+                        z[c + 1] = zz.y;
                     }
                     const int t0 = tok + kStep * h;
                     if (t0 < safe0 || t0 + kStep > safe1) {
@@ -683,12 +729,16 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                     }
                     const float ref = m == -INFINITY ? 0.0f : m;
                     uint32_t p[kStep / 2];
+                    uint64_t sum = 0;
 #pragma unroll
                     for (int c = 0; c < kStep; c += 2) {
-                        const float p0 = ex2(fmaf(z[c], unit, -ref)), p1 = ex2(fmaf(z[c + 1], unit, -ref));
-                        l += p0 + p1;
+                        const float2 x = both(fma2(pair2(z[c], z[c + 1]), pair2(unit, unit), pair2(-ref, -ref)));
+                        const float p0 = ex2(x.x), p1 = ex2(x.y);
+                        sum = add2(sum, pair2(p0, p1));
                         p[c / 2] = pack_half2(p0, p1);
                     }
+                    const float2 sums = both(sum);
+                    l += sums.x + sums.y;
                     tmem_store16(ts + 64 * (h / 2) + kStep / 2 * (h % 2), p);
                     tmem_store_wait();
                     fence_before();
@@ -824,7 +874,7 @@ tm_status launch_chunk_attn(int D, int32_t xtype, AttnArgs &a, int device, int s
                                          : (D == 64 ? launch_chunk<__nv_bfloat16, 64>(a, device, sms, s, pdl)
                                                     : launch_chunk<__nv_bfloat16, 128>(a, device, sms, s, pdl));
     if (st != TM_OK || !join) return st;
-    return launch_attn_join(D, xtype, a, kChunkRows, 1, s);
+    return launch_chunk_join(D, xtype, a, sms, s);
 }
 
 }  // namespace libtm
