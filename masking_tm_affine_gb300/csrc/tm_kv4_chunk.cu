@@ -1,18 +1,29 @@
 // tm_kv4_chunk.cu -- attention over the 4-bit cache for many query rows (the chunks
 // of a prompt): the same mathematics as tm_kv4_attn.cu, on tcgen05.
 //
-// Bound by the tensor cores and, as closely, by the exponentials: 4 D flops and one
-// exponential for each (query row, token).  An item's row tile is 256 rows (queries x
-// the heads that share a KV head), two halves of 128, walked over 128 tokens at a time:
+// The least it has to do is 4 D flops and one exponential for each (query row, token).
+// An item's row tile is 256 rows (queries x the heads that share a KV head), two
+// halves of 128, walked over 128 tokens at a time:
 //
 //   loader warp      bulk copies of the tile's eight cache blocks
 //   4 unpack warps   codes -> fp16 in shared memory, once for both halves: K as the
 //                    whole numbers c, V as the values low + c step
-//   MMA thread       S = Q K^T   [128 rows, 128 tokens], both operands in shared memory
-//                    O += P V    [128 rows, D], P from tensor memory, 32 tokens at a time
+//   2 MMA warps      a half each, so that neither waits for the other's softmax:
+//                    S = Q K^T  [128 rows, 64 tokens], both operands in shared memory,
+//                    half a tile ahead of the softmax;
+//                    O += P V   [128 rows, D], P from tensor memory, 32 tokens at a time
 //   2 x 4 warps      a half each, a thread a row: S from tensor memory, softmax, P back
-//                    into the columns S came from; while one half is at it, the tensor
-//                    cores run the other's products
+//                    into the columns S came from
+//
+// What bounds it: the softmax warps, two to a scheduler, by the latency of their chain
+// (read S, maximum, exponentials, write P): 256 queries on 2 sequences of 4 100 to 8 192
+// tokens, 32 heads on 8, D 128, bf16, the whole call 87.8 us, 70 of them this kernel's,
+// 60 of those its tiles, about 5800 cycles each, of which the products need 1024.  There
+// the tensor cores are 29% busy, the issue slots 40%, the exponential unit 14%.
+// 2048 queries on 8192 tokens: 352 us, 683 TFLOP/s.  On the way: one warp issuing both
+// halves' products in turn 109 us, and 117 with its code under `lane == 0`; S of a whole
+// tile made only after the tile before 107; the step's loop unrolled 118 (the roles'
+// code outgrows the instruction caches).
 //
 // Shared memory: Q and K are K-major, V is MN-major (a token's dims contiguous), all in
 // 128-byte swizzled panels of 64 dims; a word's eight dims lie in the order 0 4 1 5 2 6
@@ -42,9 +53,10 @@ namespace {
 constexpr int kTok = 128;            // tokens of a tile
 constexpr int kStep = 32, kSteps = kTok / kStep;  // tokens of one step of the second product
 constexpr int kUnpackWarps = 4;
-constexpr int kThreads2 = 16 * 32;   // warps 0-7 softmax, 8-11 unpack, 12 MMA, 13 loader (14, 15 idle)
-// Registers: 128 a thread at launch (all there are); the softmax warps, which hold 64
-// logits of a row, take what the others give: 2 x 152 + 2 x 104 = 4 x 128.
+constexpr int kThreads2 = 16 * 32;   // warps 0-7 softmax, 8-11 unpack, 12 and 14 MMA, 13 loader (15 idle)
+// Registers: 128 a thread at launch (all there are); the softmax warps, which hold a
+// step of S and P of a row, take what the others give: 2 x 168 + 2 x 88 = 4 x 128.
+// (152 and 104: 90.5 us for 88.5.)
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "register shares");
 constexpr int kRawStages = 2, kOpStages = 3, kParStages = 2;
@@ -138,9 +150,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t db, uint
         "r"(a), "l"(db), "r"(id), "r"((uint32_t)acc)
         : "memory");
 }
-// One lane of the warp, the same at every call.  (The compiler knows that code under
-// this has one active lane and keeps descriptors in uniform registers; under
-// `lane == 0` it moved them there for every product, 200 cycles each.)
+// One lane of the warp, the same at every call.  The compiler knows that code under
+// this has one active lane and can keep descriptors in uniform registers.
 __device__ __forceinline__ bool elect()
 {
     uint32_t e;
@@ -862,7 +873,11 @@ tm_status launch_chunk(AttnArgs &a, int device, int sms, cudaStream_t s, bool pd
 
 bool chunk_attn_fits(int32_t xtype, int64_t rows, int D)
 {
-    return xtype != TM_F32 && (D == 64 || D == 128) && rows >= 128;
+    // Whole calls, mma.sync kernel against this one, heads 4 to a KV head.  D 128, 64 rows:
+    // 2 sequences of 8192 tokens 35 / 39 us, 32 of 4096 148 / 195, one of 65536 88 / 105;
+    // 96 rows: 46 / 39, 213 / 196, 122 / 105.  D 64, 2 of 8192: 64 rows 27 / 37 us,
+    // 128 rows 37 / 35.
+    return xtype != TM_F32 && ((D == 128 && rows >= 96) || (D == 64 && rows >= 128));
 }
 
 size_t chunk_attn_slots_bytes(int D) { return 2 * (size_t)(kMostBlocks / 4) * kChunkRows * (D + 2) * sizeof(float); }
