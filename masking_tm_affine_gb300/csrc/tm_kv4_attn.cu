@@ -882,7 +882,7 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     const int64_t row_tiles = (most_rows + rows_of_tile - 1) / rows_of_tile;
     // the units of all items, and the join's grid, fit 31 bits (with room for a block's share)
     if (row_tiles > (1 << 30) / rows_of_tile / ((int64_t)B * Hkv) ||
-        (max_len / kUnit + 2) > (1 << 30) / ((int64_t)B * Hkv * row_tiles))
+        (max_len / kUnit + 4) > (1 << 30) / ((int64_t)B * Hkv * row_tiles))
         return TM_ERR_INVALID_ARG;
     const DevInfo *dev;
     tm_status st = device_info(&dev);
@@ -921,6 +921,16 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.by_group = make_fastdiv((uint32_t)a.G);
     a.max_q = max_q;
     a.row_tiles = (int)row_tiles;
+    // Row tiles by what they see, if the queries are a good part of the tokens and items have
+    // several units.  32 heads on 8, D 128, counting all alike / by what they see, us: 8192
+    // queries on 8192 tokens 1248 / 746, two of 4096 on 4096 585 / 401, 2048 on 8192 354 / 322,
+    // four of 1024 on 4096 321 / 306, four of 1024 on 1024 107 / 107; four of 512 on 4096 173 / 180,
+    // eight of 512 on 512 75 / 86.  (With more queries than tokens the tiles' ends would pass
+    // max_len, the bound above.)
+    a.tile_step = -1;
+    if (chunk && !a.full && window == 0 && kChunkRows % a.G == 0 && max_len > 4 * kUnit && max_q <= max_len &&
+        4 * (int64_t)max_q >= max_len)
+        for (a.tile_step = 0; a.G << a.tile_step < kChunkRows;) ++a.tile_step;  // kChunkRows / G, a power of two
     a.bias = 0x64006400u;
     a.scale = scale;
     a.status = dev->status;

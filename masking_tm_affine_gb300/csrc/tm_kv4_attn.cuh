@@ -44,7 +44,9 @@ __device__ __forceinline__ uint32_t centred(uint32_t x, uint16_t middle)
 __device__ __forceinline__ uint32_t centred_even(uint32_t x, uint32_t bias) { return centred((x & 0x000f000fu) | bias, 0x6408); }  // 1032
 __device__ __forceinline__ uint32_t centred_odd(uint32_t x, uint32_t bias) { return centred((x & 0x00f000f0u) | bias, 0x6480); }   // 1152
 
-constexpr int kUnit = 256;             // tokens
+constexpr int kUnitShift = 8, kUnit = 1 << kUnitShift;             // tokens of a unit of work
+constexpr int kChunkRows = 256;        // the chunk kernel's row tile
+static_assert(kChunkRows <= kUnit, "a tile's step is at most a unit");
 constexpr int kMostBlocks = 608;       // 152 SMs x 4: what the workspace is sized for
 
 struct AttnArgs {
@@ -57,6 +59,7 @@ struct AttnArgs {
     int2 *job;        // [B][Hkv][row_tiles]: the first block an item lies in, and how many; or NULL
     int64_t qs_tok, qs_head, os_tok, os_head, pages, page_bytes, ldt, Tq, max_len;
     int B, Hq, Hkv, G, window, full, vec, max_q, blocks_per_page, row_tiles;
+    int tile_step;  // chunk kernel, in log2: tokens a row tile sees more than the one before (-1: all count alike)
     uint32_t bias;  // 1024 in both halves of an fp16 pair
     float scale;
     FastDiv by_page, by_group;  // cache blocks of a page, heads of a group
@@ -103,19 +106,40 @@ __device__ __forceinline__ int lower(const AttnArgs &a, const Seq &s, int t)
 
 // Row tiles of a sequence, and the units each of its items counts (one at
 // least: an item that sees nothing still has its zeros to write).  With a
-// window every row tile counts as many units as the widest could need.
+// window every row tile counts as many units as the widest could need.  In the
+// chunk kernel, where the queries are a large part of the tokens, a causal item counts
+// what its last row sees, end + tile 2^step tokens, and one unit for its own start and
+// end: a prompt's first row tiles see next to nothing.
 struct Load {
-    int tiles, units;
-    __device__ __forceinline__ int total(int Hkv) const { return tiles * units * Hkv; }  // the host bounds the sum
+    int tiles, units, end, step, head;  // units: of every item, where step < 0; head: of a KV head's items
+    __device__ __forceinline__ int total(int Hkv) const { return head * Hkv; }  // the host bounds the sum
+    // Units of the first t row tiles, sum over k < t of 1 + ceil((end + k 2^step) / kUnit):
+    // with x = (end - 1) >> step and 2^r = kUnit / 2^step, a term is ((x + k) >> r) + 2.
+    __device__ __forceinline__ int before(int t) const
+    {
+        if (step < 0) return t * units;
+        const int r = kUnitShift - step, x = end - 1 >> step;
+        return (int)(below(x + t, r) - below(x, r)) + 2 * t;
+    }
+    // Sum over i < x of i >> r.
+    static __device__ __forceinline__ int64_t below(int64_t x, int r)
+    {
+        const int64_t m = x >> r;
+        return (m * (m - 1) / 2 << r) + m * (x - (m << r));
+    }
 };
 
 __device__ __forceinline__ Load load_of(const AttnArgs &a, const Seq &s, int rows_of_tile)
 {
     Load l;
+    const bool chunk = rows_of_tile == kChunkRows;
     l.tiles = (s.n * a.G + rows_of_tile - 1) / rows_of_tile;
+    l.step = chunk ? a.tile_step : -1;
+    l.end = l.step < 0 ? 1 : max(1, min(s.len, s.len - s.n + (1 << l.step)));
     int range = s.len;
     if (a.window > 0) range = min(range, a.window + rows_of_tile / a.G + 1 + kTile);
     l.units = max(1, (range + kUnit - 1) / kUnit);
+    l.head = l.before(l.tiles);
     return l;
 }
 
@@ -185,13 +209,26 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs &a, int rows_of_t
         r.load = load_of(a, r.seq, rows_of_tile);
     }
     Segment s;
-    const int item = (r.pos - r.base) / r.load.units;
-    s.unit0 = r.pos - r.base - item * r.load.units;
-    s.kvh = item / r.load.tiles;
-    s.tile = item - s.kvh * r.load.tiles;
-    s.count = min(r.load.units - s.unit0, r.stop - r.pos);
-    s.whole = s.count == r.load.units;
-    s.last = s.unit0 + s.count == r.load.units;
+    int units = r.load.units;
+    s.kvh = (r.pos - r.base) / r.load.head;
+    s.unit0 = r.pos - r.base - s.kvh * r.load.head;
+    if (r.load.step < 0) {
+        s.tile = s.unit0 / units;
+        s.unit0 -= s.tile * units;
+    } else {
+        int lo = 0, hi = r.load.tiles;  // before(lo) <= unit0 < before(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            (r.load.before(mid) <= s.unit0 ? lo : hi) = mid;
+        }
+        s.tile = lo;
+        const int first = r.load.before(lo);
+        units = r.load.before(lo + 1) - first;
+        s.unit0 -= first;
+    }
+    s.count = min(units - s.unit0, r.stop - r.pos);
+    s.whole = s.count == units;
+    s.last = s.unit0 + s.count == units;
     s.rows = min(rows_of_tile, r.seq.n * a.G - s.tile * rows_of_tile);
     const int first = s.tile * rows_of_tile;
     s.begin = lower(a, r.seq, (int)fdiv(first, a.by_group)) / kTile * kTile;
@@ -213,7 +250,6 @@ __device__ __forceinline__ void note_job(const AttnArgs &a, const Run &r, const 
 tm_status launch_chunk_attn(int D, int32_t xtype, AttnArgs &a, int device, int sms, bool join, cudaStream_t s, bool pdl);
 bool chunk_attn_fits(int32_t xtype, int64_t rows, int D);
 size_t chunk_attn_slots_bytes(int D);
-constexpr int kChunkRows = 256;  // its row tile
 
 // The join of its partial outputs (tm_kv4_attn.cu).
 tm_status launch_chunk_join(int D, int32_t xtype, AttnArgs &a, int sms, cudaStream_t s);

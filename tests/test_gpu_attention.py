@@ -125,6 +125,25 @@ def test_chunks(cuda, kind, D, lens, qn, Hq, Hkv, page):
     c.check()
 
 
+# Whole prompts and late chunks of several row tiles, which see more and more: every tile step (256 / heads
+# of a group, and a group that does not divide it), sequences beside them of one tile, of none, of fewer keys than
+# queries, and more queries than any sequence has tokens.
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,qn,Hq,Hkv,D,max_len", [
+    ([700], [700], 2, 2, 64, 700), ([700, 20, 0], [700, 20, 3], 2, 1, 64, 704), ([600, 257], [600, 130], 4, 1, 128, 600),
+    ([520, 0, 300], [300, 0, 300], 8, 1, 128, 520), ([129, 400, 1], [129, 65, 1], 16, 1, 64, 400),
+    ([300, 290], [300, 150], 6, 2, 128, 300), ([500, 9], [300, 400], 4, 2, 64, 500), ([260], [400], 4, 2, 64, 260),
+    ([257], [257], 1, 1, 128, 257), ([256, 255], [256, 255], 4, 1, 64, 256), ([1100], [1100], 2, 2, 64, 1100),
+    ([1500, 20, 0, 1030], [1500, 20, 3, 300], 4, 1, 128, 1504), ([1200, 1217], [400, 1200], 8, 1, 64, 1217),
+    ([1100], [1100], 16, 1, 64, 1100), ([2000, 700], [600, 700], 6, 2, 128, 2000), ([1056, 3], [1056, 40], 4, 4, 64, 1056),
+    ([1300, 1], [1300, 300], 2, 1, 128, 1312)])
+def test_chunks_of_several_row_tiles(cuda, kind, lens, qn, Hq, Hkv, D, max_len):
+    c = Case(kind, lens, qn, Hq, Hkv, D, 32)
+    c.run(max_len=max_len)
+    tm.tm_check()
+    c.check()
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("window", [1, 50, 200])
 def test_chunks_with_a_window(cuda, D, window):
