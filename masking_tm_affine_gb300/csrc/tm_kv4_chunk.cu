@@ -20,9 +20,10 @@
 // tokens, 32 heads on 8, D 128, bf16, the whole call 87.8 us, 70 of them this kernel's,
 // 60 of those its tiles, about 5800 cycles each, of which the products need 1024.  There
 // the tensor cores are 29% busy, the issue slots 40%, the exponential unit 14%.
-// 2048 queries on 8192 tokens: 322 us, 747 TFLOP/s; 8192 on 8192: 746 us, 737.  On the way: one warp issuing both
-// halves' products in turn 109 us, and 117 with its code under `lane == 0`; S of a whole
-// tile made only after the tile before 107; the step's loop unrolled 118 (the roles'
+// 2048 queries on 8192 tokens: 322 us, 747 TFLOP/s; 8192 on 8192: 746 us, 737.
+// On the way, the first of these calls: one warp issuing both halves' products in turn
+// 109 us, 124 with S made half a tile ahead; two warps, S of a tile made after the tile
+// before, 107, ahead 99; the softmax step's loop unrolled 118 instead of 89 (the roles'
 // code outgrows the instruction caches).
 //
 // Shared memory: Q and K are K-major, V is MN-major (a token's dims contiguous), all in
