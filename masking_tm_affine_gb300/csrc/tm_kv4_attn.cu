@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
     int vexp = 0;
     for (int i = 0; i < mine; ++i) {
         const int tok0 = c0 + (warp + i * kWarps) * kTile;
-        if (!mbar_wait_bounded(bar_s + 8 * stage, phase)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_s + 8 * stage, phase))) {  // a warp gives up together
             alive = false;
             break;
         }
@@ -650,6 +650,10 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ A
     const Seq seq = sequence(a, b, false);
     if (tile * rows_of_tile >= seq.n * a.G) return;  // not an item: its job was not noted
     const int n = job.y;
+    if (!job_in_grid(job.x, n, a.grid)) {
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
     if (n == 1) return;  // one block had the whole item and wrote its output
     const int stride = rows_of_tile * (D + 2);
     // partial p: the item's first block holds it in its slot 1, the others in slot 0
@@ -797,6 +801,7 @@ tm_status launch_attn(AttnArgs &a, int dev, int sms, bool join, cudaStream_t s, 
     }
     int64_t blocks = (int64_t)sms * blocks_per_sm<T, D, NT>();
     if (blocks > kMostBlocks) blocks = kMostBlocks;
+    a.grid = (int)blocks;
     void *args[] = {(void *)&a};
     tm_status st = launch_kernel(k, dim3((unsigned)blocks), dim3(kWarps * 32), args, attn_smem<D>(), s, pdl);
     if (st != TM_OK || !join) return st;

@@ -59,6 +59,7 @@ struct AttnArgs {
     int2 *job;        // [B][Hkv][row_tiles]: the first block an item lies in, and how many; or NULL
     int64_t qs_tok, qs_head, os_tok, os_head, pages, page_bytes, ldt, Tq, max_len;
     int B, Hq, Hkv, G, window, full, vec, max_q, blocks_per_page, row_tiles;
+    int grid;       // blocks of the attention's launch, the bound of a job's blocks
     int tile_step;  // chunk kernel, in log2: tokens a row tile sees more than the one before (-1: all count alike)
     uint32_t bias;  // 1024 in both halves of an fp16 pair
     float scale;
@@ -244,6 +245,13 @@ __device__ __forceinline__ void note_job(const AttnArgs &a, const Run &r, const 
 {
     const int c0 = (r.pos - s.unit0) / r.share;
     a.job[((int64_t)r.b * a.Hkv + s.kvh) * a.row_tiles + s.tile] = make_int2(c0, (int)blockIdx.x - c0 + 1);
+}
+
+// Whether a job names blocks of the launch.  A block that gave up on a wait has noted
+// nothing for the items after it: their jobs are whatever the workspace held.
+__host__ __device__ constexpr bool job_in_grid(int first, int count, int grid)
+{
+    return first >= 0 && count >= 1 && count <= grid && first <= grid - count;
 }
 
 // The kernel for many query rows (tm_kv4_chunk.cu).

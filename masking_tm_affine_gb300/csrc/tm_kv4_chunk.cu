@@ -865,8 +865,9 @@ tm_status launch_chunk(AttnArgs &a, int device, int sms, cudaStream_t s, bool pd
         }
         ready[device].store(true, std::memory_order_release);
     }
-    void *args[] = {(void *)&a};
     const unsigned blocks = (unsigned)(sms < kMostBlocks / 4 ? sms : kMostBlocks / 4);
+    a.grid = (int)blocks;
+    void *args[] = {(void *)&a};
     return launch_kernel(k, dim3(blocks), dim3(kThreads2), args, smem, s, pdl);
 }
 
