@@ -278,8 +278,9 @@ __global__ void __launch_bounds__(kNormLanes<EW, K>) rmsnorm_kernel(const __grid
 // ---------------------------------------------------------------- the ring of row copies
 // A stage holds `slots` rows of each of `tensors` tensors, row bytes each (a multiple
 // of 16).  The first slots * tensors threads issue a copy each; thread 0 announces
-// the bytes.  Waits are bounded: a stage that does not come marks the status word,
-// the block then copies and stores nothing more.
+// the bytes.  Waits are bounded: a warp whose stage does not come marks the status word
+// and stores nothing more.  A warp gives up together, and the threads that copy are one
+// warp (slots * tensors <= 8 * 3): the bytes announced for a stage are those copied.
 struct Ring {
     uint32_t data, bars;  // shared addresses
     uint32_t row_bytes, slots, tensors, stages;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(512) rmsnorm_ring_kernel(const __grid_constant
     uint32_t phase = 0;
     bool alive = true;
     for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < a.M; r0 += step) {
-        alive = alive && mbar_wait_bounded(g.bars + 8 * stage, phase);
+        alive = alive && __all_sync(0xffffffffu, mbar_wait_bounded(g.bars + 8 * stage, phase));
         const int64_t row = r0 + slot;
         const int left = row < a.M ? a.N - j0 : 0;
         float h[K][EW], ss;
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_ring_kernel(const __grid_cons
     for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < a.M; r0 += step, turn ^= 1) {
         const int64_t row = r0 + slot;
         const float s = row < a.M ? __ldg(a.rstd + row) : 0.0f;
-        alive = alive && mbar_wait_bounded(g.bars + 8 * stage, phase);
+        alive = alive && __all_sync(0xffffffffu, mbar_wait_bounded(g.bars + 8 * stage, phase));
         const int left = row < a.M ? a.N - j0 : 0;
         Vec<T, EW> vy[K], vh[K], vr[K];
         const uint32_t at = g.data + (stage * tensors * slots + slot) * g.row_bytes + j0 * (int)sizeof(T);
