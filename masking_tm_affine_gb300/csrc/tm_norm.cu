@@ -30,6 +30,8 @@
 
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "tm_elem.cuh"
 
 namespace libtm {
@@ -671,55 +673,91 @@ void pick_lanes(int64_t nv, int want, int least, int EW, bool grad, int *L, int 
     *K = k;
 }
 
+// A kernel instance and the dynamic shared memory its launches may ask for: its most over all
+// sizes, allowed once a device (the limit belongs to the instance, so a call that set its own
+// size could take it from under a call of another host thread).
+struct Instance {
+    const void *k;
+    int most;
+    mutable std::atomic<bool> ready[kMaxDevices];
+};
+
+constexpr int kRingBytes = 222 * 1024;
+
+template <auto KERNEL, int MOST = 0>
+const Instance *instance()
+{
+    static const Instance i = {(const void *)KERNEL, MOST, {}};
+    return &i;
+}
+
+tm_status allow_smem(const Instance &i)
+{
+    if (i.most == 0) return TM_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return TM_ERR_CUDA;
+    }
+    if (i.ready[dev].load(std::memory_order_acquire)) return TM_OK;
+    if (cudaFuncSetAttribute(i.k, cudaFuncAttributeMaxDynamicSharedMemorySize, i.most) != cudaSuccess) {
+        cudaGetLastError();
+        return TM_ERR_CUDA;
+    }
+    i.ready[dev].store(true, std::memory_order_release);
+    return TM_OK;
+}
+
 template <typename T, typename WT, int EW, bool E4M3>
-const void *norm_kernel(int K)
+const Instance *norm_kernel(int K)
 {
     if constexpr (EW == 1)
-        return K <= 8 ? (const void *)rmsnorm_kernel<T, WT, 1, 8, E4M3> : (const void *)rmsnorm_kernel<T, WT, 1, 32, E4M3>;
+        return K <= 8 ? instance<rmsnorm_kernel<T, WT, 1, 8, E4M3>>() : instance<rmsnorm_kernel<T, WT, 1, 32, E4M3>>();
     else
-        return K == 1   ? (const void *)rmsnorm_kernel<T, WT, EW, 1, E4M3>
-               : K == 2 ? (const void *)rmsnorm_kernel<T, WT, EW, 2, E4M3>
-               : K == 4 ? (const void *)rmsnorm_kernel<T, WT, EW, 4, E4M3>
-                        : (const void *)rmsnorm_kernel<T, WT, EW, 8, E4M3>;
+        return K == 1   ? instance<rmsnorm_kernel<T, WT, EW, 1, E4M3>>()
+               : K == 2 ? instance<rmsnorm_kernel<T, WT, EW, 2, E4M3>>()
+               : K == 4 ? instance<rmsnorm_kernel<T, WT, EW, 4, E4M3>>()
+                        : instance<rmsnorm_kernel<T, WT, EW, 8, E4M3>>();
 }
 
 template <typename T, typename WT, int EW>
-const void *norm_bwd_kernel(int K)
+const Instance *norm_bwd_kernel(int K)
 {
     if constexpr (EW == 1)
-        return K <= 8 ? (const void *)rmsnorm_bwd_kernel<T, WT, 1, 8> : (const void *)rmsnorm_bwd_kernel<T, WT, 1, 32>;
+        return K <= 8 ? instance<rmsnorm_bwd_kernel<T, WT, 1, 8>, kMaxCols * 4>()
+                      : instance<rmsnorm_bwd_kernel<T, WT, 1, 32>, kMaxCols * 4>();
     else
-        return K == 1   ? (const void *)rmsnorm_bwd_kernel<T, WT, EW, 1>
-               : K == 2 ? (const void *)rmsnorm_bwd_kernel<T, WT, EW, 2>
-               : K == 4 ? (const void *)rmsnorm_bwd_kernel<T, WT, EW, 4>
-                        : (const void *)rmsnorm_bwd_kernel<T, WT, EW, 8>;
+        return K == 1   ? instance<rmsnorm_bwd_kernel<T, WT, EW, 1>, kMaxCols * 4>()
+               : K == 2 ? instance<rmsnorm_bwd_kernel<T, WT, EW, 2>, kMaxCols * 4>()
+               : K == 4 ? instance<rmsnorm_bwd_kernel<T, WT, EW, 4>, kMaxCols * 4>()
+                        : instance<rmsnorm_bwd_kernel<T, WT, EW, 8>, kMaxCols * 4>();
 }
 
 template <typename T, typename WT>
-const void *norm_pick(bool vec, bool ring, bool e4, int K)
+const Instance *norm_pick(bool vec, bool ring, bool e4, int K)
 {
     constexpr int EW = 16 / sizeof(T);
     if (ring) {
         if (e4)
-            return K == 1   ? (const void *)rmsnorm_ring_kernel<T, WT, EW, 1, true>
-                   : K == 2 ? (const void *)rmsnorm_ring_kernel<T, WT, EW, 2, true>
-                            : (const void *)rmsnorm_ring_kernel<T, WT, EW, 4, true>;
-        return K == 1   ? (const void *)rmsnorm_ring_kernel<T, WT, EW, 1, false>
-               : K == 2 ? (const void *)rmsnorm_ring_kernel<T, WT, EW, 2, false>
-                        : (const void *)rmsnorm_ring_kernel<T, WT, EW, 4, false>;
+            return K == 1   ? instance<rmsnorm_ring_kernel<T, WT, EW, 1, true>, kRingBytes>()
+                   : K == 2 ? instance<rmsnorm_ring_kernel<T, WT, EW, 2, true>, kRingBytes>()
+                            : instance<rmsnorm_ring_kernel<T, WT, EW, 4, true>, kRingBytes>();
+        return K == 1   ? instance<rmsnorm_ring_kernel<T, WT, EW, 1, false>, kRingBytes>()
+               : K == 2 ? instance<rmsnorm_ring_kernel<T, WT, EW, 2, false>, kRingBytes>()
+                        : instance<rmsnorm_ring_kernel<T, WT, EW, 4, false>, kRingBytes>();
     }
     if (vec) return e4 ? norm_kernel<T, WT, EW, true>(K) : norm_kernel<T, WT, EW, false>(K);
     return e4 ? norm_kernel<T, WT, 1, true>(K) : norm_kernel<T, WT, 1, false>(K);
 }
 
 template <typename T, typename WT>
-const void *norm_bwd_pick(bool vec, bool ring, int K)
+const Instance *norm_bwd_pick(bool vec, bool ring, int K)
 {
     constexpr int EW = 16 / sizeof(T);
     if (ring)
-        return K == 1   ? (const void *)rmsnorm_bwd_ring_kernel<T, WT, EW, 1>
-               : K == 2 ? (const void *)rmsnorm_bwd_ring_kernel<T, WT, EW, 2>
-                        : (const void *)rmsnorm_bwd_ring_kernel<T, WT, EW, 4>;
+        return K == 1   ? instance<rmsnorm_bwd_ring_kernel<T, WT, EW, 1>, kRingBytes>()
+               : K == 2 ? instance<rmsnorm_bwd_ring_kernel<T, WT, EW, 2>, kRingBytes>()
+                        : instance<rmsnorm_bwd_ring_kernel<T, WT, EW, 4>, kRingBytes>();
     return vec ? norm_bwd_kernel<T, WT, EW>(K) : norm_bwd_kernel<T, WT, 1>(K);
 }
 
@@ -749,7 +787,7 @@ bool ring_plan(int64_t M, int64_t nv, int tensors, int want, int sms, RingPlan *
     p->threads = l < 256 ? 256 : l;
     const int64_t slots = p->threads / l, stage = slots * tensors * nv * 16;
     p->per_sm = stage * 2 <= 110 * 1024 ? 2 : 1;
-    const int64_t room = p->per_sm == 2 ? 110 * 1024 : 222 * 1024;
+    const int64_t room = p->per_sm == 2 ? 110 * 1024 : kRingBytes;
     p->stages = (int)(room / stage);
     if (p->stages < 2) return false;
     if (p->stages > kMostStages) p->stages = kMostStages;
@@ -759,16 +797,6 @@ bool ring_plan(int64_t M, int64_t nv, int tensors, int want, int sms, RingPlan *
     if (p->blocks < most) return false;
     p->blocks = most;
     return true;
-}
-
-tm_status allow_smem(const void *k, size_t bytes)
-{
-    if (bytes > 40 * 1024 &&
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
-        cudaGetLastError();
-        return TM_ERR_CUDA;
-    }
-    return TM_OK;
 }
 
 constexpr int64_t kBwdBlocks = 608;  // dw partial rows at most: 152 SMs x 4 blocks
@@ -867,16 +895,17 @@ extern "C" tm_status tm_rmsnorm(const void *X, int64_t ldx, const void *R, int64
     NormArgs a = {X, R, W, H, Y, scales, rstd, ldx, ldr, ldh, ldy, M, (int)N, L, group,
                   group == 32 ? 5 : group == 64 ? 6 : 7, eps, 1.0f / (float)N, dev->status};
     const bool wf = wtype == TM_F32;
-    const void *k = xtype == TM_F32 ? norm_pick<float, float>(vec, ring, e4, K)
-                    : xtype == TM_F16
-                        ? (wf ? norm_pick<__half, float>(vec, ring, e4, K) : norm_pick<__half, __half>(vec, ring, e4, K))
-                        : (wf ? norm_pick<__nv_bfloat16, float>(vec, ring, e4, K)
-                              : norm_pick<__nv_bfloat16, __nv_bfloat16>(vec, ring, e4, K));
+    const Instance *k =
+        xtype == TM_F32 ? norm_pick<float, float>(vec, ring, e4, K)
+        : xtype == TM_F16
+            ? (wf ? norm_pick<__half, float>(vec, ring, e4, K) : norm_pick<__half, __half>(vec, ring, e4, K))
+            : (wf ? norm_pick<__nv_bfloat16, float>(vec, ring, e4, K)
+                  : norm_pick<__nv_bfloat16, __nv_bfloat16>(vec, ring, e4, K));
     void *args[] = {&a, &rp.stages};
     const size_t smem = ring ? rp.smem : 0;
-    st = allow_smem(k, smem);
+    st = allow_smem(*k);
     if (st != TM_OK) return st;
-    return launch_kernel(k, dim3((unsigned)blocks), dim3(threads), args, smem, as_stream(stream), (flags & TM_PDL) != 0);
+    return launch_kernel(k->k, dim3((unsigned)blocks), dim3(threads), args, smem, as_stream(stream), (flags & TM_PDL) != 0);
 }
 
 extern "C" size_t tm_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t N)
@@ -933,17 +962,18 @@ extern "C" tm_status tm_rmsnorm_bwd(const void *DY, int64_t lddy, const void *H,
         NormBwdArgs a = {DY, H, W, DR, rstd, DX, DW ? reinterpret_cast<float *>(workspace) : nullptr,
                          lddy, ldh, lddr, lddx, M, (int)N, p.L, 1.0f / (float)N, dev->status};
         const bool wf = wtype == TM_F32;
-        const void *k = xtype == TM_F32 ? norm_bwd_pick<float, float>(vec, ring, p.K)
-                        : xtype == TM_F16 ? (wf ? norm_bwd_pick<__half, float>(vec, ring, p.K)
-                                                : norm_bwd_pick<__half, __half>(vec, ring, p.K))
-                                          : (wf ? norm_bwd_pick<__nv_bfloat16, float>(vec, ring, p.K)
-                                                : norm_bwd_pick<__nv_bfloat16, __nv_bfloat16>(vec, ring, p.K));
+        const Instance *k =
+            xtype == TM_F32 ? norm_bwd_pick<float, float>(vec, ring, p.K)
+            : xtype == TM_F16
+                ? (wf ? norm_bwd_pick<__half, float>(vec, ring, p.K) : norm_bwd_pick<__half, __half>(vec, ring, p.K))
+                : (wf ? norm_bwd_pick<__nv_bfloat16, float>(vec, ring, p.K)
+                      : norm_bwd_pick<__nv_bfloat16, __nv_bfloat16>(vec, ring, p.K));
         // the ring's stages hold [N] floats for the end: two rows of 2-byte elements or more
         const size_t smem = ring ? rp.smem : (size_t)N * sizeof(float);
-        st = allow_smem(k, smem);
+        st = allow_smem(*k);
         if (st != TM_OK) return st;
         void *args[] = {&a, &rp.stages};
-        st = launch_kernel(k, dim3((unsigned)p.blocks), dim3(p.threads), args, smem, s, (flags & TM_PDL) != 0);
+        st = launch_kernel(k->k, dim3((unsigned)p.blocks), dim3(p.threads), args, smem, s, (flags & TM_PDL) != 0);
         if (st != TM_OK) return st;
     }
     if (DW != nullptr) {
