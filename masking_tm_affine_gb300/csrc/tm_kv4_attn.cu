@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
     constexpr int ROWS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps][STAGES];
+    __shared__ float4 cols[kWarps][NT][4];  // factors of d and of K's low for two rows
 
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
@@ -222,26 +223,22 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         for (; issued < STAGES && issued < mine; ++issued) issue(issued);
 
     // ---- queries: lane (g, j) holds dims j D/4 .. of row g of each column tile, as the
-    // second operand of the first product.  Scaled by a power of two common to all
-    // rows, so that the largest lies in [2^14, 2^15): bf16's eight bits, and fp16's
-    // eleven down to 2^-28 of the largest, are kept whole.
+    // second operand of the first product.  Each row is scaled by a power of two of its
+    // own, so that its largest lies in [2^14, 2^15): bf16's eight bits, and fp16's
+    // eleven down to 2^-28 of the largest, are kept whole, and a row with an infinity or
+    // far larger than the others takes nothing from them.
     uint32_t qf[PARTS][NT][KS][2];
-    float qsum[NT];
-    float top = 0.0f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+        float top = 0.0f, sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < LD / 8; ++w)
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(raw[nt][w].v[e])));
-    top = lanes_max(top, 32);
-    // 2^qe: exponent of the largest, kept where 2^(14 - qe) and its inverse are normal
-    int qe = (int)(__float_as_uint(top) >> 23) - 127;
-    qe = max(-100, min(qe, 127));
-    const float up = ldexpf(1.0f, 14 - qe);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float sum = 0.0f;
+        top = lanes_max(top, 4);
+        // 2^qe: exponent of the largest, kept where 2^(14 - qe) and its inverse are normal
+        const int qe = max(-100, min((int)(__float_as_uint(top) >> 23) - 127, 127));
+        const float up = ldexpf(1.0f, 14 - qe);
 #pragma unroll
         for (int w = 0; w < LD / 8; ++w) {
             float f[8];
@@ -264,17 +261,16 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
                 }
             }
         }
-        qsum[nt] = lanes_sum(sum, 4);
+        // logits in base 2 are (acc stepK + lowK qsum) * unit, acc in units of 2^-24 where codes are subnormal
+        const float unit = a.scale * kLog2eF * ldexpf(1.0f, qe - 14), qsum = lanes_sum(sum, 4) * unit;
+        // of rows 2j and 2j + 1, this lane's accumulator columns (kept in shared memory: registers are
+        // what the loop lacks)
+        const float ku = SPLIT ? unit : unit * 0x1p24f;
+        const float4 col = make_float4(__shfl_sync(0xffffffffu, ku, 8 * j), __shfl_sync(0xffffffffu, ku, 8 * j + 4),
+                                       __shfl_sync(0xffffffffu, qsum, 8 * j), __shfl_sync(0xffffffffu, qsum, 8 * j + 4));
+        if (g == 0) cols[warp][nt][j] = col;
     }
-    // logits in base 2 are (acc stepK + lowK qsum) * unit, acc in units of 2^-24 where codes are subnormal
-    const float unit = a.scale * kLog2eF * ldexpf(1.0f, qe - 14);
-    float qs[NT][2];  // of this lane's accumulator columns, rows 2j and 2j + 1
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        qs[nt][0] = __shfl_sync(0xffffffffu, qsum[nt], 8 * j) * unit;
-        qs[nt][1] = __shfl_sync(0xffffffffu, qsum[nt], 8 * j + 4) * unit;
-    }
-    const float kunit = SPLIT ? unit : unit * 0x1p24f;
+    __syncwarp();
 
     // ---- running state: per column (2j, 2j + 1 of each tile); the maximum is the
     // warp's, the sums are this lane's share (its tokens)
@@ -360,16 +356,18 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
                 }
                 vp[q][0].y = fmaf(8.0f, vp[q][0].x, vp[q][0].y);
                 vp[q][1].y = fmaf(8.0f, vp[q][1].x, vp[q][1].y);
-                const float ks0 = kp0.x * kunit, ks1 = kp1.x * kunit;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float4 col = cols[warp][nt][j];
+                    const float ku[2] = {col.x, col.y}, qs[2] = {col.z, col.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float d = acc[q][0][nt][0][e] + acc[q][0][nt][1][e];
                         if constexpr (SPLIT)
                             d = fmaf(acc[q][PARTS - 1][nt][0][e] + acc[q][PARTS - 1][nt][1][e], 1.0f / 2048.0f, d);
-                        y[q][nt][e] = fmaf(d, e < 2 ? ks0 : ks1, (e < 2 ? kp0.y : kp1.y) * qs[nt][e & 1]);
+                        y[q][nt][e] = fmaf(d, (e < 2 ? kp0.x : kp1.x) * ku[e & 1], (e < 2 ? kp0.y : kp1.y) * qs[e & 1]);
                     }
+                }
             }
         }
         if (masked) {

@@ -68,11 +68,10 @@ struct ChunkSmem {
     alignas(1024) uint8_t op[kOpStages][D / 64 * 128 * 128];  // K tiles: panels as Q; V tiles: [8 tokens][panel]
     alignas(128) uint8_t raw[kRawStages][kTok / 16 * kv4_block_bytes(D)];
     alignas(16) float kpar[kParStages][kTok / 2][4];  // K's scales, two tokens at a time: steps, lows
-    float top[8];
     int vexp[kParStages];
     uint32_t vnan[kParStages][kTok / 32];  // tokens whose V is held as NaN
     alignas(8) uint64_t raw_full[kRawStages], raw_free[kRawStages], op_full[kOpStages], op_free[kOpStages],
-        par_full[kParStages], par_free[kParStages], top_full, q_full, s_full[2][2], p_full[2][kSteps], o_done[2][kSteps], done;
+        par_full[kParStages], par_free[kParStages], q_full, s_full[2][2], p_full[2][kSteps], o_done[2][kSteps], done;
     uint32_t tmem;
     int abort;
 };
@@ -302,7 +301,6 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             bar_init(&s.par_full[i], kUnpackWarps * 32);
             bar_init(&s.par_free[i], 256);
         }
-        bar_init(&s.top_full, 256);
         bar_init(&s.q_full, 256);
         // [half of the rows][step of a tile's tokens]: each completes once a tile, so the
         // parity of the tile's number tells a completion from the one before
@@ -580,7 +578,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + kS + 128 * i, to = tmem + lanes + kO + 128 * i;
         Turn par;
-        uint32_t count = 0, segs = 0;  // tiles, segments with tokens
+        uint32_t count = 0;  // tiles
         bool ok = true;
         while (ok && run.pos < run.stop) {
             const Segment g = next_segment(a, kChunkRows, run);
@@ -593,8 +591,8 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
             const int row = 128 * i + r, full_row = g.tile * kChunkRows + row;
             const bool live = row < g.rows;
             const int t = live ? (int)fdiv(full_row, a.by_group) : 0, hq = g.kvh * a.G + full_row - t * a.G;
-            // ---- Q into shared memory, a warp its own 32 rows; then a thread its row: scaled by a
-            // power of two common to the tile, in place
+            // ---- Q into shared memory, a warp its own 32 rows; then a thread its row: scaled in
+            // place by a power of two of its own (one row's infinity leaves the others as they are)
             const bool any = g.c1 > g.c0;
             float qsum = 0.0f, unit = 1.0f;  // logits in base 2 are z unit
             const uint32_t rows_at = smem_u32(s.q[i][0]) + (warp & 3) * (32 * 128);
@@ -640,15 +638,6 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(to_f(v.v[e])));
                 }
-                top = lanes_max(top, 32);
-                if (lane == 0) s.top[warp] = top;
-                bar_arrive(&s.top_full);
-                ok = wait(&s.top_full, segs & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                ++segs;
-#pragma unroll
-                for (int x = 0; x < 8; ++x) top = fmaxf(top, s.top[x]);
                 const int qe = max(-100, min((int)(__float_as_uint(top) >> 23) - 127, 127));
                 // (a negative scale turns q's sign: z below then grows with the logit)
                 const float up = copysignf(ldexpf(1.0f, 14 - qe), a.scale);
@@ -669,8 +658,6 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 }
                 fence_async();
                 bar_arrive(&s.q_full);
-                // (s.top is written again only after this segment's products, which need every
-                // thread to have come here)
             }
 
             // ---- this row's keys [lo, hi), and where all of this warp's rows see all

@@ -1,0 +1,71 @@
+"""tm_kv4_attention where one row, one size or one window could spoil others: the
+definition in 64 bits and the tolerances of test_gpu_attention.py."""
+import numpy as np
+import pytest
+import torch
+
+import block_ref as ref
+from masking_tm_affine_gb300 import tm
+from test_gpu_attention import KINDS, Case
+
+pytestmark = pytest.mark.gpu
+
+
+def check_rows(c, keep, window=0):
+    """Rows (query, head) where keep is true against the definition."""
+    q = c.q64()
+    q[~keep] = 0.0
+    o, l, size, vmax, seen = ref.attention(q, c.kk, c.vv, c.table, c.lens, c.qstart, c.page, c.scale, window)
+    delta = (c.D + 16) * 2.0 ** -23 * 3 * size
+    prob = 2.0 ** -11 if c.kind != "f32" else 2.0 ** -22
+    tol = ((2 * delta + 2.0 ** -21 + 2 * prob + seen / 16 * 2.0 ** -23) * vmax)[..., None]
+    r, a = ref.half_step(c.t)
+    got, lse = ref.f64(c.o)[:, :c.Hq * c.D].reshape(o.shape), ref.f64(c.lse)
+    err = np.abs(got - o) / (tol + r * (np.abs(o) + tol) + a)
+    assert np.all(err[keep] <= 1), err[keep].max()
+    live = keep & (seen > 0)
+    assert np.all(np.abs(lse[live] - l[live]) <= delta[live] + 2.0 ** -21 + 2.0 ** -22 * np.abs(l[live]))
+    return got
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv,qn", [(4, 1, [1, 1]), (8, 1, [2, 1]), (12, 2, [3, 2])])
+def test_an_infinite_query_spoils_its_own_row_only(cuda, kind, D, Hq, Hkv, qn):
+    c = Case(kind, [70, 300], qn, Hq, Hkv, D, 16)
+    keep = np.ones((c.Tq, Hq), dtype=bool)
+    for t, h, x in ((0, 1, np.inf), (c.Tq - 1, Hq - 1, -np.inf), (c.Tq - 1, 0, np.nan)):
+        c.q[t, h * D + 7] = float(x)
+        keep[t, h] = False
+    c.run()
+    tm.tm_check()
+    got = check_rows(c, keep)
+    assert np.isnan(got[~keep]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,qn,Hq,Hkv", [([400], [150], 2, 1), ([700, 90], [70, 64], 8, 2)])
+def test_an_infinite_query_spoils_its_own_row_only_in_chunks(cuda, kind, D, lens, qn, Hq, Hkv):
+    c = Case(kind, lens, qn, Hq, Hkv, D, 32)
+    keep = np.ones((c.Tq, Hq), dtype=bool)
+    for t, h, x in ((0, 0, np.inf), (c.Tq - 1, Hq - 1, -np.inf), (40, 1, np.nan)):
+        c.q[t, h * D + 7] = float(x)
+        keep[t, h] = False
+    c.run()
+    tm.tm_check()
+    got = check_rows(c, keep)
+    assert np.isnan(got[~keep]).all()
+
+
+# A row far above the others (its own softmax is one key's, and not looked at here).
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("qn,Hq,D", [([1], 4, 128), ([3], 8, 64), ([160], 2, 128)])
+def test_a_huge_query_takes_nothing_from_other_rows(cuda, kind, qn, Hq, D):
+    c = Case(kind, [260], qn, Hq, 1, D, 16)
+    keep = np.ones((c.Tq, Hq), dtype=bool)
+    c.q[0, D:2 * D] *= 2.0 ** 60
+    keep[0, 1] = False
+    c.run()
+    tm.tm_check()
+    check_rows(c, keep)
