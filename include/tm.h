@@ -443,7 +443,8 @@ tm_status tm_gemm(const float *A, int64_t lda, const float *B, int64_t ldb, floa
  *              run of that many columns (the last may be short),
  *              [M, ceil(N / group)].  scale = max|y| / 448 over its values (1
  *              where they are all 0), code = y * (448 / max|y|) rounded to
- *              nearest even
+ *              nearest even, for any max|y| > 0 (h * w is formed in fp32 and,
+ *              like the scale, loses bits below 2^-126)
  *   rstd       output [M] fp32, 1 / sqrt(mean h^2 + eps), for the gradient, or NULL
  * N <= 32768.  Overlaps other than those named are refused.
  * Errors: INVALID_ARG (also eps < 0 or NaN, scales without TM_E4M3 or missing

@@ -141,9 +141,28 @@ struct NormArgs {
 };
 
 // What maps a largest magnitude of `top` (of h w) to 448, and what a code of 1 then
-// stands for (s = 1 / rms).
-__device__ __forceinline__ float e4m3_factor(float top) { return top > 0.0f ? 448.0f / top : 1.0f; }
+// stands for (s = 1 / rms).  448 / top passes fp32's range below 2^-119: values of a group
+// below kTiny are lifted by 2^100 first (lift_tiny), and the factor is that of the lifted ones.
+constexpr float kTiny = 0x1p-100f, kLift = 0x1p100f;
+__device__ __forceinline__ float e4m3_factor(float top)
+{
+    return top > 0.0f ? 448.0f / (top < kTiny ? top * kLift : top) : 1.0f;
+}
 __device__ __forceinline__ float e4m3_scale(float top, float s) { return top > 0.0f ? top * s * (1.0f / 448.0f) : 1.0f; }
+
+// By whole warps: one vote a row, next to always with no such group.
+template <int EW, int K>
+__device__ __forceinline__ void lift_tiny(const float (&top)[K], float (&h)[K][EW])
+{
+    bool tiny = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k) tiny = tiny || (top[k] > 0.0f && top[k] < kTiny);
+    if (!__any_sync(0xffffffffu, tiny)) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < EW; ++e) h[k][e] *= top[k] < kTiny ? kLift : 1.0f;
+}
 
 // What follows a row's sum: 1 / rms, h, y.  `h` is overwritten.
 template <typename T, typename WT, int EW, int K, bool E4M3>
@@ -188,9 +207,8 @@ __device__ __forceinline__ void finish_row(const NormArgs &a, int64_t row, bool 
             for (int k = 0; k < K; ++k) t = fmaxf(t, top[k]);
             t = row_max(t, a.L, buf);
             if (live && ln == 0) a.scales[row] = e4m3_scale(t, s);
-            const float f = e4m3_factor(t);
 #pragma unroll
-            for (int k = 0; k < K; ++k) top[k] = f;
+            for (int k = 0; k < K; ++k) top[k] = t;
         } else {
             // a group is group / EW lanes of one k (EW > 1), or all 32 lanes of group / 32
             // consecutive k (EW = 1)
@@ -203,7 +221,6 @@ __device__ __forceinline__ void finish_row(const NormArgs &a, int64_t row, bool 
                     top[k] = lanes_max(top[k], lanes);
                     if (k * 32 * EW < left && (ln & (lanes - 1)) == 0)
                         scales[(j0 + k * 32 * EW) >> a.group_log] = e4m3_scale(top[k], s);
-                    top[k] = e4m3_factor(top[k]);
                 }
             } else {
                 float m[K];
@@ -217,14 +234,16 @@ __device__ __forceinline__ void finish_row(const NormArgs &a, int64_t row, bool 
                         if (q >> (a.group_log - 5) == k >> (a.group_log - 5)) t = fmaxf(t, m[q]);
                     const int j = j0 + k * 32;
                     if (k * 32 < left && (j & (a.group - 1)) == 0) scales[j >> a.group_log] = e4m3_scale(t, s);
-                    top[k] = e4m3_factor(t);
+                    top[k] = t;
                 }
             }
         }
+        lift_tiny<EW, K>(top, h);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            const float f = e4m3_factor(top[k]);
 #pragma unroll
-            for (int e = 0; e < EW; ++e) h[k][e] *= top[k];
+            for (int e = 0; e < EW; ++e) h[k][e] *= f;
             store_e4m3<EW>(out + k * 32 * EW, k * 32 * EW < left, h[k]);
         }
     }
