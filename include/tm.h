@@ -587,7 +587,7 @@ tm_status tm_kv4_gather(const void *pool, int64_t pages, int32_t page, const int
  * them), token j in page table[b*ldt + j / page]; its queries are rows
  * qstart[b] .. qstart[b+1] - 1 of Q, at positions lens[b] - n .. lens[b] - 1 (n
  * their count).  A query at position p sees keys j <= p, with window > 0 only
- * j > p - window, with TM_ATTN_FULL every key (window 0).  A query that sees
+ * j > p - window (window >= max_len hides nothing), with TM_ATTN_FULL every key (window 0).  A query that sees
  * none gets o = 0 and lse = -inf.  Query head h reads KV head h / (Hq / Hkv).
  *   Q, O       [Tq, Hq, D] as in tm_rope; O does not overlap Q
  *   lse        [Tq, Hq] fp32, or NULL

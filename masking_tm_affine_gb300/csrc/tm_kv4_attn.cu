@@ -916,7 +916,7 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.G = Hq / Hkv;
-    a.window = window;
+    a.window = window_of(window, max_len);
     a.full = (flags & TM_ATTN_FULL) ? 1 : 0;
     a.vec = heads_vec(q, e) && heads_vec(o, e) ? 1 : 0;
     a.blocks_per_page = page / 16;
@@ -931,7 +931,7 @@ extern "C" tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_
     // eight of 512 on 512 75 / 86.  (With more queries than tokens the tiles' ends would pass
     // max_len, the bound above.)
     a.tile_step = -1;
-    if (chunk && !a.full && window == 0 && kChunkRows % a.G == 0 && max_len > 4 * kUnit && max_q <= max_len &&
+    if (chunk && !a.full && a.window == 0 && kChunkRows % a.G == 0 && max_len > 4 * kUnit && max_q <= max_len &&
         4 * (int64_t)max_q >= max_len)
         for (a.tile_step = 0; a.G << a.tile_step < kChunkRows;) ++a.tile_step;  // kChunkRows / G, a power of two
     a.bias = 0x64006400u;

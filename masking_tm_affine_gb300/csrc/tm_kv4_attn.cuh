@@ -49,6 +49,10 @@ constexpr int kChunkRows = 256;        // the chunk kernel's row tile
 static_assert(kChunkRows <= kUnit, "a tile's step is at most a unit");
 constexpr int kMostBlocks = 608;       // 152 SMs x 4: what the workspace is sized for
 
+// The window the kernels take: 0 for one that hides nothing from any query.  A window
+// below max_len (at most 2^30) keeps their sums of lengths and windows within 32 bits.
+__host__ __device__ constexpr int window_of(int window, int64_t max_len) { return window >= max_len ? 0 : window; }
+
 struct AttnArgs {
     const void *Q;
     void *O;

@@ -69,3 +69,23 @@ def test_a_huge_query_takes_nothing_from_other_rows(cuda, kind, qn, Hq, D):
     c.run()
     tm.tm_check()
     check_rows(c, keep)
+
+
+# Windows that hide nothing, up to the largest an int32 holds, are no window: the same bits.  Long sequences (split
+# over blocks), fewer keys than queries, an empty sequence; both forms.
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,qn,Hq,Hkv,D", [
+    ([5000, 1, 1281], [1, 1, 1], 8, 2, 128), ([130, 40, 3, 64, 0], [40, 5, 7, 0, 2], 6, 2, 64), ([7], [12], 4, 2, 128),
+    ([300, 20, 129], [133, 90, 5], 4, 1, 128), ([1500, 900], [600, 900], 2, 1, 64)])
+def test_a_window_that_hides_nothing(cuda, kind, lens, qn, Hq, Hkv, D):
+    c = Case(kind, lens, qn, Hq, Hkv, D, 16)
+    c.run()
+    tm.tm_check()
+    o, lse = c.o.clone(), c.lse.clone()
+    c.check()
+    for window in (2 ** 31 - 1, 2 ** 31 - 40, 2 ** 31 - 300, 2 ** 30, max(lens) + 1, max(lens)):
+        c.o.fill_(9.0)
+        c.lse.fill_(9.0)
+        c.run(window=window)
+        tm.tm_check()
+        assert torch.equal(lse, c.lse) and torch.equal(o, c.o), window
