@@ -38,7 +38,10 @@
 // depend on V's size.
 //
 // A thread has a whole row, so its maximum and sums need no exchange.  The reference
-// maximum moves only where a logit passes it by 2^8 and the steps' exponent only past
+// lies 2^7 below the maximum that set it (probabilities go up from 2^7 in fp16, so that
+// those of 2^-21 and more of the maximum keep fp16's eleven bits, and what vanishes lies below 2^-32
+// of it: a long context holds 10^5 of them).  It moves only where a logit passes that
+// maximum by 2^8, and the steps' exponent only past
 // a power of two well above it: O is then scaled in tensor memory, which almost
 // never happens after a segment's first tile.
 //
@@ -60,6 +63,8 @@ constexpr int kThreads2 = 16 * 32;   // warps 0-7 softmax, 8-11 unpack, 12 and 1
 // (152 and 104: 90.5 us for 88.5.)
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "register shares");
+constexpr int kHead = 7;  // 2^(kHead + kSlack) is the largest probability, below fp16's 2^16
+static_assert(kHead + kSlack <= 15, "probabilities in fp16");
 constexpr int kRawStages = 2, kOpStages = 3, kParStages = 2;
 
 template <int D>
@@ -694,8 +699,8 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
 #pragma unroll
                     for (int c = 0; c < kStep; c += 2) top = fmaxf(top, fmaxf(z[c], z[c + 1]));
                     top *= unit;
-                    if (__any_sync(0xffffffffu, top > m + kSlack) || e_new != vexp) {
-                        const float mn = fmaxf(m, top);
+                    if (__any_sync(0xffffffffu, top > m + (kHead + kSlack)) || e_new != vexp) {
+                        const float mn = fmaxf(m, top - kHead);
                         const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
                         m = mn;
                         l *= f;

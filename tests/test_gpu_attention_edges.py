@@ -89,3 +89,54 @@ def test_a_window_that_hides_nothing(cuda, kind, lens, qn, Hq, Hkv, D):
         c.run(window=window)
         tm.tm_check()
         assert torch.equal(lse, c.lse) and torch.equal(o, c.o), window
+
+
+# One key far above all others, and its value zero: the output is what the others leave, each a probability of about
+# 2^-bits.  (Keys' and queries' parts of the tolerance are taken key by key.)  A probability is off by fp16's half step, or
+# below fp16's range by 2^-32 (chunks: 2^-25 behind a reference 2^7 down) of the value.
+def faint(c, bits, seed=0):
+    rng = np.random.default_rng(seed)
+    n, page, D = c.pages * c.page, c.page, c.D
+    q = 1.0 + 0.01 * rng.standard_normal((c.Tq, c.Hq * D))
+    c.q.copy_(torch.from_numpy(q).to(c.t))
+    k = 0.01 * rng.standard_normal((n, 1, D))
+    v = 1.0 + 0.1 * rng.random((n, 1, D))
+    v[:, :, 0] = -1.0                                   # lows far from the values: the codes carry them
+    first = int(c.table[0][0]) * page
+    k[first], v[first] = bits * np.log(2.0) / D ** 0.5, 0.0
+    c.pool = ref.empty_pool(c.pages, 1, page, D)
+    c.kk, c.vv = ref.append(c.pool, range(n), page, k, v)
+
+
+def check_faint(c, rel, absolute):
+    """`absolute`: what a key's share may lose whatever its size, as a share of the largest |v|."""
+    at = np.concatenate([p * c.page + np.arange(c.page) for p in c.table[0]])
+    q, got = c.q64(), ref.f64(c.o).reshape(c.Tq, c.Hq, c.D)
+    half, a = ref.half_step(c.t)
+    for t in range(c.Tq):
+        n = c.lens[0] - c.Tq + t + 1
+        k, v = c.kk[at[:n], 0], c.vv[at[:n], 0]
+        for h in range(c.Hq):
+            s = k @ q[t, h] * c.scale
+            size = np.abs(k) @ np.abs(q[t, h]) * c.scale
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            delta = (c.D + 16) * 2.0 ** -23 * 3 * (size + size[0]) + 2.0 ** -20
+            want, vmax = p @ v, np.abs(v).max()
+            assert np.abs(want).max() > 0
+            lim = (p * (delta + 2 * rel + n / 16 * 2.0 ** -23)) @ np.abs(v) + n * absolute * vmax
+            lim += half * (np.abs(want) + lim) + a
+            err = np.abs(got[t, h] - want) / lim
+            assert np.all(err <= 1), (t, h, err.max(), got[t, h, 1], want[1])
+            assert lim[1] < 0.5 * want[1]               # the check would see them vanish
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bits", [16, 26])
+def test_faint_keys_of_a_chunk(cuda, kind, D, bits):
+    c = Case(kind, [6000], [130], 1, 1, D, 16)
+    faint(c, bits)
+    c.run()
+    tm.tm_check()
+    check_faint(c, 2.0 ** -11, 2.0 ** -32)
