@@ -41,8 +41,10 @@
 //
 // P stepV is rounded to fp16 for the second product, scaled by a 2^E that keeps the
 // largest of them in range: off by at most 2^-11 of itself, errors that the sum over
-// tokens averages below the output's own rounding.  With fp32 tensors q and P stepV
-// go in as two fp16 parts each (22 bits).
+// tokens averages below the output's own rounding, or, for probabilities below 2^-18 of the
+// largest that the same warp meets, by 2^-29 of that (times the largest step: half of fp16's
+// smallest number).  With fp32 tensors q and P stepV go in as two fp16 parts each: 22 bits, those
+// of P stepV down to 2^-12 of the largest, and 2^-35 of it below that.
 //
 // Measured with the join, D 128, 8 KV heads: 64 sequences of 1000 to 8192 tokens, 32
 // heads, bf16, 78 us (321 MB, 60% of the copy rate); one of 131071, 64 heads, fp16, 43 us
@@ -108,6 +110,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
 {
     constexpr bool SPLIT = sizeof(T) == 4;     // two fp16 parts
     constexpr int PARTS = SPLIT ? 2 : 1;
+    // The reference lies 2^LEAD below the maximum that set it: what P stepV keeps of faint keys
+    // against how often a new maximum moves the state.  0 / 2 / 4 / 6 in fp32: 64 sequences 97.9 / 98.1 /
+    // 98.7 / 99.2 us, one of 131071 tokens 52.3 / 52.4 / 52.7 / 53.5.
+    constexpr int LEAD = SPLIT ? 6 : 0;
     constexpr int KS = D / 16;                 // steps of the first product = row tiles of the second
     constexpr int LD = D / 4;                  // dims of a row that a lane holds for the first product
     constexpr int STAGES = ring_stages<D>();
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
                     }
         }
         // The reference m moves only where a logit passes it by 2^kSlack, and the steps' cap
-        // only past three times a power of two: moving the running state costs half a
+        // only past eight times a power of two: moving the running state costs half a
         // tile's work, and following every new maximum of eight rows did so in two
         // tiles of three (attn of 131071 tokens: 44 against 33 us).
         bool grow = false;
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
                     float t = fmaxf(fmaxf(y[0][nt][c], y[0][nt][2 + c]), fmaxf(y[1][nt][c], y[1][nt][2 + c]));
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-                    const float mn = fmaxf(m[nt][c], t);
+                    const float mn = fmaxf(m[nt][c], t - LEAD);
                     const float f = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - mn);
                     m[nt][c] = mn;
                     l[nt][c] *= f;

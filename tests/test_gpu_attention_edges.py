@@ -108,13 +108,13 @@ def faint(c, bits, seed=0):
     c.kk, c.vv = ref.append(c.pool, range(n), page, k, v)
 
 
-def check_faint(c, rel, absolute):
-    """`absolute`: what a key's share may lose whatever its size, as a share of the largest |v|."""
+def check_faint(c, rel, absolute, rows, lossy):
+    """Row t sees rows[t] keys.  `absolute`: what a key's share may lose whatever its size, as a share of the largest |v|,
+    and of how many keys."""
     at = np.concatenate([p * c.page + np.arange(c.page) for p in c.table[0]])
     q, got = c.q64(), ref.f64(c.o).reshape(c.Tq, c.Hq, c.D)
     half, a = ref.half_step(c.t)
-    for t in range(c.Tq):
-        n = c.lens[0] - c.Tq + t + 1
+    for t, n in rows.items():
         k, v = c.kk[at[:n], 0], c.vv[at[:n], 0]
         for h in range(c.Hq):
             s = k @ q[t, h] * c.scale
@@ -124,7 +124,7 @@ def check_faint(c, rel, absolute):
             delta = (c.D + 16) * 2.0 ** -23 * 3 * (size + size[0]) + 2.0 ** -20
             want, vmax = p @ v, np.abs(v).max()
             assert np.abs(want).max() > 0
-            lim = (p * (delta + 2 * rel + n / 16 * 2.0 ** -23)) @ np.abs(v) + n * absolute * vmax
+            lim = (p * (delta + 2 * rel + n / 16 * 2.0 ** -23)) @ np.abs(v) + min(n, lossy) * absolute * vmax
             lim += half * (np.abs(want) + lim) + a
             err = np.abs(got[t, h] - want) / lim
             assert np.all(err <= 1), (t, h, err.max(), got[t, h, 1], want[1])
@@ -139,4 +139,22 @@ def test_faint_keys_of_a_chunk(cuda, kind, D, bits):
     faint(c, bits)
     c.run()
     tm.tm_check()
-    check_faint(c, 2.0 ** -11, 2.0 ** -32)
+    check_faint(c, 2.0 ** -11, 2.0 ** -32, {t: 6000 - 130 + t + 1 for t in range(130)}, 6000)
+
+
+# Single queries.  p * step goes in with the largest step at 2^4 to 2^7 (fp32: in two parts, behind a reference 2^6 down): a
+# key may lose half of fp16's smallest number there, 2^-29 (2^-35) of the largest step, times at most eight steps of
+# 2 |v| / 15 each: 2^-28 and 2^-34 of |v|.  Only keys of the strong key's own warp can: more sequences than blocks, so that
+# a block has most of one, and a quarter of the keys (in tiles of 32) are that warp's.
+@pytest.mark.parametrize("kind,bits", [("bf16", 22), ("f16", 22), ("f32", 22), ("f32", 31)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_faint_keys_of_single_queries(cuda, kind, bits, D):
+    n, B = 1500, 700
+    c = Case(kind, [n], [B], 1, 1, D, 16)
+    faint(c, bits)
+    c.lens, c.max_q, c.qstart = [n] * B, 1, list(range(B + 1))     # B sequences of one query over the same pages
+    c.table = np.repeat(c.table, B, axis=0)
+    c.run()
+    tm.tm_check()
+    bound = (2.0 ** -22, 2.0 ** -34) if kind == "f32" else (2.0 ** -11, 2.0 ** -28)
+    check_faint(c, *bound, {t: n for t in range(0, B, 5)}, n // 4 + 64)
