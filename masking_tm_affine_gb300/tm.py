@@ -138,8 +138,12 @@ def _stream(s) -> int | None:
     if s is None:
         torch = sys.modules.get("torch")
         if torch is not None and torch.cuda.is_initialized():
-            # what torch.cuda.current_stream().cuda_stream reads, without building a Stream object (3.8 us a call)
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            # what torch.cuda.current_stream().cuda_stream reads, without building a Stream object (3.8 us a
+            # call); those two are not torch's public functions, so a version may lack them
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+            if raw is None or device is None:
+                return torch.cuda.current_stream().cuda_stream
+            return raw(device())
         return None
     if isinstance(s, int):
         return s
