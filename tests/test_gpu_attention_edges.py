@@ -158,3 +158,21 @@ def test_faint_keys_of_single_queries(cuda, kind, bits, D):
     tm.tm_check()
     bound = (2.0 ** -22, 2.0 ** -34) if kind == "f32" else (2.0 ** -11, 2.0 ** -28)
     check_faint(c, *bound, {t: n for t in range(0, B, 5)}, n // 4 + 64)
+
+
+# Any real scale: negative, zero.
+@pytest.mark.parametrize("kind,qn,D", [("f32", [1, 3], 128), ("bf16", [1, 3], 64), ("f16", [90, 70], 128), ("bf16", [130, 5], 64)])
+@pytest.mark.parametrize("scale", [-0.125, 0.0, -0.0])
+def test_scales_of_either_sign(cuda, kind, qn, D, scale):
+    c = Case(kind, [300, 70], qn, 4, 2, D, 16)
+    c.scale = scale
+    c.run()
+    tm.tm_check()
+    o, l, size, vmax, seen = ref.attention(c.q64(), c.kk, c.vv, c.table, c.lens, c.qstart, c.page, scale)
+    delta = (D + 16) * 2.0 ** -23 * 3 * np.abs(size)
+    prob = 2.0 ** -11 if kind != "f32" else 2.0 ** -22
+    tol = ((2 * delta + 2.0 ** -21 + 2 * prob + seen / 16 * 2.0 ** -23) * vmax)[..., None]
+    r, a = ref.half_step(c.t)
+    got = ref.f64(c.o)[:, :c.Hq * D].reshape(o.shape)
+    assert np.all(np.abs(got - o) <= tol + r * (np.abs(o) + tol) + a)
+    assert np.all(np.abs(ref.f64(c.lse) - l)[seen > 0] <= (delta + 2.0 ** -21 + 2.0 ** -22 * np.abs(l))[seen > 0])
