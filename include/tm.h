@@ -497,7 +497,10 @@ tm_status tm_rmsnorm_bwd(const void *DY, int64_t lddy, const void *H, int64_t ld
  *                    by (n_i - low) / (high - low)
  *   TM_ROPE_BY_DIM   the same two ends, weighted linearly in the pair's index
  *                    between the (real) indices at which n_i = high and n_i = low,
- *                    rounded down and up to whole ones
+ *                    rounded down and up to whole ones and cut to 0 .. rot - 1
+ *                    (where both are the same, the upper one 0.001 on): the
+ *                    published by-dimension scaling, whose bounds results have to
+ *                    agree with
  * Host only.  Errors: INVALID_ARG (rot odd or < 2, base <= 1, factor < 1, and
  * for the last two orig <= 0 or not 0 < low < high), and TM_ROPE_BASE with rot 2.
  */
@@ -536,7 +539,8 @@ tm_status tm_rope(const void *X, int64_t xs_tok, int64_t xs_head, void *Y, int64
  * codes 0).  A vector with a NaN, an infinity or a spread beyond fp32's range is
  * held as NaN.  The codes are
  * those of this formula on the exactly rotated values: where fp32 cannot decide
- * a rounding, the kernel decides it in fp64.
+ * a rounding, the kernel decides it in pairs of floats, good to 2^-41 of a
+ * rotated pair's size.
  *
  * The pool is `pages` pages of `page` tokens (a multiple of 16), each
  * tm_kv4_page_bytes(Hkv, D, page) bytes: [Hkv][page / 16] blocks of 16 tokens,
@@ -587,21 +591,31 @@ tm_status tm_kv4_gather(const void *pool, int64_t pages, int32_t page, const int
  * them), token j in page table[b*ldt + j / page]; its queries are rows
  * qstart[b] .. qstart[b+1] - 1 of Q, at positions lens[b] - n .. lens[b] - 1 (n
  * their count).  A query at position p sees keys j <= p, with window > 0 only
- * j > p - window (window >= max_len hides nothing), with TM_ATTN_FULL every key (window 0).  A query that sees
- * none gets o = 0 and lse = -inf.  Query head h reads KV head h / (Hq / Hkv).
+ * j > p - window (one of max_len or more hides nothing), with TM_ATTN_FULL every
+ * key (window 0).  A query that sees none gets o = 0 and lse = -inf.  An
+ * infinity or NaN in a query, or a token held as NaN, makes the rows that have
+ * or see it NaN, and no others.  Query head h reads KV head h / (Hq / Hkv).
  *   Q, O       [Tq, Hq, D] as in tm_rope; O does not overlap Q
  *   lse        [Tq, Hq] fp32, or NULL
  *   pool, pages, page   the cache
  *   table, ldt device int32 [B, ldt]; lens device int32 [B], each at most max_len
  *   qstart     device int32 [B + 1], non-decreasing from 0 to Tq, or NULL: one
  *              query a sequence (Tq == B)
- *   max_q      no sequence has more queries (the grid is sized by it)
+ *   max_q      no sequence has more queries.  It decides which kernel takes the
+ *              call: from about 100 query rows a KV head (16-bit types, D 64 or
+ *              128) all its sequences are taken 256 rows at a time.  Single
+ *              queries beside a chunk then cost far more than in a call of their
+ *              own (one chunk of 256 and 63 single queries on up to 8192 tokens
+ *              490 us, as two calls 154): give them calls of their own
  *   max_len    no sequence has more tokens; table rows hold its pages.  It sets how
  *              the work is split, so a close bound is faster
  *   workspace  tm_kv4_attention_workspace_bytes(...) bytes, 16-byte aligned, in
  *              use until the call's kernels finish
- * Products run on the codes in fp16 on the tensor cores (fp32 queries as two
- * fp16 parts), sums in fp32; splits of a sequence are joined in a fixed order.
+ * Products run on the codes in fp16 on the tensor cores (fp32 queries and their
+ * probabilities as two fp16 parts), sums in fp32; splits of a sequence are
+ * joined in a fixed order.  With |v| the largest value that a row meets, a key of
+ * probability p adds at most 2^-10 p |v| to the output's error, or 2^-25 |v| times
+ * the row's largest p where that is more (fp32: 2^-22 and 2^-34).
  * Errors: INVALID_ARG, UNSUPPORTED_TILE (D, page), MISALIGNED, WORKSPACE, CUDA;
  *         INDEX (a page outside the pool, a length beyond max_len, a count beyond
  *         max_q or Tq) and TIMEOUT through tm_check.

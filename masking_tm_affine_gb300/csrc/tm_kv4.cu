@@ -459,8 +459,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 24) kv4_append_kernel(const
             word[0] -= 0x4b400000u * 0x11111111u;
             word[1] -= 0x4b400000u * 0x11111111u;
             params = __halves2half2(step, low);
-            // the values' error, and four roundings of t (the difference, 1 / step, 1/15, the
-            // product), which is at most 15
+            // the values' error, and what t, at most 14.5 where it matters, is off by: m15 by 2.54 2^-24
+            // of itself (three roundings, over every fp16 step), the difference by 2^-24, the cut
+            // value, below 1, by 2^-25: 14.5 * 3.54 + 15 / 2 of 2^-24, below 15 * 4
             const float et = err * inv + 15.0f * 0x1p-22f;
             unsure = unsure || off + et >= 0.5f;
         }

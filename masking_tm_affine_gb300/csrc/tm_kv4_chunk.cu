@@ -34,16 +34,17 @@
 // K's scales stay outside its product, as in tm_kv4_attn.cu, so that logits keep fp32's
 // accuracy; a thread multiplies them in, two floats a token.  V's are multiplied into
 // its operand, which rounds each value to fp16, off by 2^-11 of itself like the
-// probabilities; the tile's exponent comes off first, so that the rounding does not
-// depend on V's size.
+// probabilities; the exponent of the largest value so far comes off first, so that the
+// rounding does not depend on V's size (what lies 2^-14 and more below that value loses
+// bits: half of fp16's smallest number, 2^-25 of it).
 //
 // A thread has a whole row, so its maximum and sums need no exchange.  The reference
-// lies 2^7 below the maximum that set it (probabilities go up from 2^7 in fp16, so that
-// those of 2^-21 and more of the maximum keep fp16's eleven bits, and what vanishes lies below 2^-32
-// of it: a long context holds 10^5 of them).  It moves only where a logit passes that
-// maximum by 2^8, and the steps' exponent only past
-// a power of two well above it: O is then scaled in tensor memory, which almost
-// never happens after a segment's first tile.
+// lies 2^7 below the maximum that set it: probabilities go up from 2^7 in fp16, so that
+// those of 2^-21 and more of the maximum keep fp16's eleven bits, and what vanishes lies
+// below 2^-32 of it (a long context holds 10^5 of them).  It moves only where a logit
+// passes that maximum by 2^8, and V's exponent only past a power of two well above it: O
+// is then scaled in tensor memory, which almost never happens after a segment's first
+// tile.
 //
 // Every wait is bounded.  One that runs out sets the abort flag, which every role
 // looks at; outstanding copies and products are waited for before the block ends.
