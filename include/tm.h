@@ -613,9 +613,9 @@ tm_status tm_kv4_gather(const void *pool, int64_t pages, int32_t page, const int
  *              use until the call's kernels finish
  * Products run on the codes in fp16 on the tensor cores (fp32 queries and their
  * probabilities as two fp16 parts), sums in fp32; splits of a sequence are
- * joined in a fixed order.  With |v| the largest value that a row meets, a key of
- * probability p adds at most 2^-10 p |v| to the output's error, or 2^-25 |v| times
- * the row's largest p where that is more (fp32: 2^-22 and 2^-34).
+ * joined in a fixed order.  With |v| the largest value that the queries of its
+ * sequence see, a key of probability p adds at most 2^-10 p |v| to a row's error, or
+ * 2^-28 |v| times the row's largest p where that is more (fp32: 2^-22 and 2^-34).
  * Errors: INVALID_ARG, UNSUPPORTED_TILE (D, page), MISALIGNED, WORKSPACE, CUDA;
  *         INDEX (a page outside the pool, a length beyond max_len, a count beyond
  *         max_q or Tq) and TIMEOUT through tm_check.

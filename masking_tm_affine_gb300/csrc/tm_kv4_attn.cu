@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         // Where every row of the tile sees every token: [safe0, safe1).
         const int safe0 = lower(a, seq, (int)fdiv(tile * ROWS + rows - 1, a.by_group));
         const int safe1 = upper(a, seq, (int)fdiv(tile * ROWS, a.by_group));
+        const int first = lower(a, seq, (int)fdiv(tile * ROWS, a.by_group));  // nothing before it is seen
 
         // ---- this lane's queries, asked for before the copies' page numbers
         Vec<T, 8> raw[NT][LD / 8];
@@ -391,12 +392,13 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
                             if (tok < lo || tok >= hi) y[q][nt][2 * r + c] = -INFINITY;
                         }
                 }
-            // a token past the end has no scales (its bytes are whatever the page or the ring held)
+            // a token past the end has no scales (its bytes are whatever the page or the ring held),
+            // one before every row's window none that count
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    if (tok0 + 16 * q + 8 * r + g >= end) vp[q][r] = make_float2(0.0f, 0.0f);
+                    if (const int tok = tok0 + 16 * q + 8 * r + g; tok >= end || tok < first) vp[q][r] = make_float2(0.0f, 0.0f);
         }
         // A token held as NaN makes the rows that see it NaN, and no others: its scales
         // leave the sums (0 * NaN is not 0) and a NaN joins what is added to each output.

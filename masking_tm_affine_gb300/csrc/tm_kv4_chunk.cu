@@ -35,8 +35,9 @@
 // accuracy; a thread multiplies them in, two floats a token.  V's are multiplied into
 // its operand, which rounds each value to fp16, off by 2^-11 of itself like the
 // probabilities; the exponent of the largest value so far comes off first, so that the
-// rounding does not depend on V's size (what lies 2^-14 and more below that value loses
-// bits: half of fp16's smallest number, 2^-25 of it).
+// rounding does not depend on V's size.  That value may be a token's that a row does not
+// see: it goes in at 2^9 and more, so that what lies 2^20 below it (fp16's steps and lows reach
+// no further from 1) still keeps 2^-13 of itself.
 //
 // A thread has a whole row, so its maximum and sums need no exchange.  The reference
 // lies 2^7 below the maximum that set it: probabilities go up from 2^7 in fp16, so that
@@ -66,6 +67,7 @@ constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "register shares");
 constexpr int kHead = 7;  // 2^(kHead + kSlack) is the largest probability, below fp16's 2^16
 static_assert(kHead + kSlack <= 15, "probabilities in fp16");
+constexpr int kValueBits = 9;  // the largest value lies in [2^9, 2^12) of fp16's 2^16
 constexpr int kRawStages = 2, kOpStages = 3, kParStages = 2;
 
 template <int D>
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                     vexp = vmax > 0.0f ? (int)(__float_as_uint(vmax) >> 23) - 127 : -24;  // 2^e <= vmax < 2^(e+1)
                     vcap = ldexpf(1.0f, vexp + 3);
                 }
-                const float vscale = ldexpf(1.0f, -vexp);  // values below 8
+                const float vscale = ldexpf(1.0f, kValueBits - vexp);  // values below 2^(kValueBits + 3)
                 if (pars >= kParStages) ok = wait_all(&s.par_free[par.stage], par.phase ^ 1);
                 if (!ok) break;
                 {
@@ -774,7 +776,7 @@ __global__ void __launch_bounds__(kThreads2, 1) kv4_chunk_kernel(const __grid_co
                 fence_after();
             }
             if (!ok) break;
-            const float back = ldexpf(1.0f, vexp), inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float back = ldexpf(1.0f, vexp - kValueBits), inv = l == 0.0f ? 0.0f : 1.0f / l;
             float *slot = a.part + (2 * (int64_t)blockIdx.x + (g.unit0 == 0 ? 1 : 0)) * (kChunkRows * (D + 2));
             // O goes out through this warp's rows of Q's shared memory (which the products are done
             // with), D/2 columns at a time, so that a warp writes whole rows

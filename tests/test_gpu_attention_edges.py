@@ -176,3 +176,41 @@ def test_scales_of_either_sign(cuda, kind, qn, D, scale):
     got = ref.f64(c.o)[:, :c.Hq * D].reshape(o.shape)
     assert np.all(np.abs(got - o) <= tol + r * (np.abs(o) + tol) + a)
     assert np.all(np.abs(ref.f64(c.lse) - l)[seen > 0] <= (delta + 2.0 ** -21 + 2.0 ** -22 * np.abs(l))[seen > 0])
+
+
+# Tokens that a row does not see, their values as large as the cache holds: beyond the window of every row, and in chunks
+# ahead of a row too.  (Tolerances are by the values that the row sees.)
+def giants(c, tokens):
+    at = [int(c.table[0][j // c.page]) * c.page + j % c.page for j in tokens]
+    rng = np.random.default_rng(5)
+    big = 1e30 * np.sign(rng.standard_normal((len(at), c.vv.shape[1], c.D)))
+    c.kk[at], c.vv[at] = ref.append(c.pool, at, c.page, c.kk[at], big)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [100, 250])
+def test_giants_outside_the_window(cuda, kind, D, window):
+    c = Case(kind, [419], [1], 4, 2, D, 16)
+    giants(c, [419 - window - 1, 419 - window - 3])
+    c.run(window=window)
+    tm.tm_check()
+    got = check_rows(c, np.ones((1, 4), dtype=bool), window)
+    assert np.abs(got).max() < 10
+    # in the 2-norm, as test_gpu_attention.py has it: errors of different keys are independent
+    o = ref.attention(c.q64(), c.kk, c.vv, c.table, c.lens, c.qstart, c.page, c.scale, window)[0]
+    assert np.linalg.norm(got - o) <= {"f32": 1e-5, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[kind] * np.linalg.norm(o)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 180])
+def test_giants_that_a_row_of_a_chunk_does_not_see(cuda, kind, D, window):
+    c = Case(kind, [500], [150], 2, 1, D, 16)
+    giants(c, [490, 495] + ([150] if window else []))            # the first of them is seen from query 140 on
+    c.run(window=window)
+    tm.tm_check()
+    keep = np.zeros((150, 2), dtype=bool)
+    keep[:140] = True                                            # 150 is before each of their windows (350 - 180 + 1)
+    got = check_rows(c, keep, window)
+    assert np.abs(got[keep]).max() < 10
