@@ -48,7 +48,7 @@
 //
 // Measured with the join, D 128, 8 KV heads: 64 sequences of 1000 to 8192 tokens, 32
 // heads, bf16, 78 us (321 MB, 60% of the copy rate); one of 131071, 64 heads, fp16, 43 us
-// (143 MB, 49%; longer ones approach 77%).  Issue slots are 51 to 55% busy: a tile's chain of
+// (143 MB, 49%; longer ones approach 77%).  Issue slots are 54 to 58% busy: a tile's chain of
 // copy, products and softmax bounds it, and a fixed 10 us of start and join.
 #include <atomic>
 

@@ -17,14 +17,15 @@
 //
 // What bounds it: the softmax warps, two to a scheduler, by the latency of their chain
 // (read S, maximum, exponentials, write P): 256 queries on 2 sequences of 4 100 to 8 192
-// tokens, 32 heads on 8, D 128, bf16, the whole call 89 us, 71 of them this kernel's,
+// tokens, 32 heads on 8, D 128, bf16, the whole call 88 us, about 70 of them this kernel's,
 // 60 of those its tiles, about 5800 cycles each, of which the products need 1024.  There
-// the tensor cores are 29% busy, the issue slots 40%, the exponential unit 14%.
-// 2048 queries on 8192 tokens: 322 us, 747 TFLOP/s; 8192 on 8192: 746 us, 737.
+// the tensor cores are 28% busy, the issue slots 49%, the exponential unit 14%.
+// 2048 queries on 8192 tokens: 319 us, 755 TFLOP/s; 8192 on 8192: 745 us, 738.
 // On the way, the first of these calls: one warp issuing both halves' products in turn
 // 109 us, 124 with S made half a tile ahead; two warps, S of a tile made after the tile
 // before, 107, ahead 99; the softmax step's loop unrolled 118 instead of 89 (the roles'
-// code outgrows the instruction caches).
+// code outgrows the instruction caches); an exponent of Q common to the tile, which the
+// halves exchanged before the first product, 90.
 //
 // Shared memory: Q and K are K-major, V is MN-major (a token's dims contiguous), all in
 // 128-byte swizzled panels of 64 dims; a word's eight dims lie in the order 0 4 1 5 2 6

@@ -23,7 +23,7 @@
 // run of lanes of one warp (or, with single elements, of one lane's registers).
 // All sums are fp32, in a fixed order.
 //
-// Measured, bf16: 8192 x 8192 with a residual to e4m3 by 128 columns 84 us, 83% of the
+// Measured, bf16: 8192 x 8192 with a residual to e4m3 by 128 columns 82 us, 85% of the
 // rate of a copy of the same bytes; 8192 x 4096 with a residual, both directions, 97 us,
 // 81%; 32 x 4096 to e4m3 3.1 us on the device.
 #include "tm_host.h"
@@ -782,7 +782,9 @@ const Instance *norm_bwd_pick(bool vec, bool ring, int K)
 
 // The ring's shape for rows of nv vectors, `tensors` of them a row: 256 lanes a block
 // where a row needs no more, `want` vectors a lane, two blocks an SM (one if a row's
-// copies are too large), and as many stages as their shared memory holds.  False if
+// copies are too large), and as many stages as their shared memory holds.  (Registers are
+// not counted: a block of 512 threads of more than 64 fits an SM once, and the second
+// round of blocks follows the first.)  False if
 // the ring does not fit, or if there are fewer steps than blocks.  Measured (bf16 with
 // a residual, first form / ring, us): norm 8192 x 8192 122 / 91, 1024 x 8192 19.6 /
 // 14.6, 2048 x 4096 18.7 / 14.9, 8192 x 1024 17.3 / 15.0, 4096 x 1024 10.5 / 10.7;
