@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T, D, NT>())
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    __syncwarp();  // every lane copies and waits on these barriers
 
     Run run;
     if (!find_run(a, ROWS, warp == 0, run)) {
