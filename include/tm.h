@@ -631,6 +631,106 @@ tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_head, void 
                            tm_stream_t stream);
 
 /*
+ * Products on operands of 8 and 16 bits
+ * -------------------------------------
+ * Rows sorted by expert.  E experts share one call: expert e has rows starts[e] ..
+ * starts[e+1] - 1 of the T rows (device int32 [E + 1], non-decreasing, within 0 .. T),
+ * none, one or many.  Rows before starts[0] and from starts[E] on belong to nobody:
+ * they would produce stays as it was.  An expert whose borders fall or leave 0 .. T is taken as
+ * empty, and the next tm_check returns TM_ERR_INDEX.  starts == NULL with E == 1: one
+ * matrix for all rows.  E <= 1024.
+ * Operands that are multiplied start on 16-byte boundaries and have row strides
+ * of whole 16 bytes (tm_row_stride; any extents): MISALIGNED otherwise.  Outputs need
+ * only their element's alignment.  Sums are fp32; an output is rounded once.  A row's
+ * infinities and NaNs reach its own outputs and no others.
+ *
+ * tm_quant_e4m3 -- 8-bit floats with a scale for each run of 128 columns of `rows` rows
+ * (1: as tm_rmsnorm writes with group 128; 128: square blocks, for weights):
+ *   scale = max|x| / 448 over the block (1 where all are 0),  code = x * 448 / max|x|
+ * rounded to nearest even, decided on the exact quotient.  A block with an infinity or
+ * a NaN is held as NaN: codes 0x7F, scale NaN.
+ *   X, ldx     input [M, N] of xtype          Y, ldy   output codes [M, N], a byte each
+ *   scales     output [ceil(M / rows), ceil(N / 128)] fp32
+ * Errors: INVALID_ARG (also any overlap), UNSUPPORTED_TILE (rows), MISALIGNED, CUDA.
+ */
+tm_status tm_quant_e4m3(const void *X, int64_t ldx, int64_t M, int64_t N, void *Y, int64_t ldy, float *scales,
+                        int32_t rows, int32_t xtype, uint32_t flags, tm_stream_t stream);
+
+/*
+ * tm_gemm_e4m3 -- C = A B^T with both operands in 8 bits: for the rows t of expert e
+ *   C[t, n] = sum over blocks b of sa[t, b] sb[e, n / 128, b] * sum_{k in b} A[t, k] B[e, n, k].
+ *   A, lda     codes [M, K]; sa: group 128 [M, ceil(K / 128)], group 0 [M], as
+ *              tm_rmsnorm and tm_quant_e4m3 write them
+ *   B, ldb     codes [E, N, K] (rows n of all experts one after another); sb
+ *              [E, ceil(N / 128), ceil(K / 128)] from tm_quant_e4m3 with 128 rows
+ *              (expert by expert where N is no multiple of 128)
+ *   C, ldc     output [M, N] of ctype (TM_F32, TM_F16, TM_BF16); overlaps no input
+ * Products of codes are exact and summed in fp32 over a block of 128, and the blocks in
+ * fp32 after their scales: |error| <= (K + ceil(K / 128)) 2^-23 * sum |sa sb A B|.  The gradient of the
+ * rows is the same call with the transposed codes and scales of B.
+ * Errors: INVALID_ARG, UNSUPPORTED_TILE (group, E, extents beyond 2^31 - 513 or 2^30
+ *         tiles), MISALIGNED, CUDA; INDEX and TIMEOUT through tm_check.
+ */
+tm_status tm_gemm_e4m3(const void *A, int64_t lda, const float *sa, int32_t group, const void *B, int64_t ldb,
+                       const float *sb, void *C, int64_t ldc, const int32_t *starts, int32_t E, int64_t M, int64_t N,
+                       int64_t K, int32_t ctype, uint32_t flags, tm_stream_t stream);
+
+/*
+ * tm_gemm_experts -- products of 16-bit rows with their experts' matrices: Y[t, :] = W_e X[t, :].
+ *   X, ldx     [T, K] of xtype (TM_F16 or TM_BF16; fp32 products: tm_gemm)
+ *   W, ldw     [E, N, K] of xtype, rows n of all experts one after another
+ *   Y, ldy     output [T, N] of ytype (xtype or TM_F32); overlaps no input
+ * K == 0 gives zeros.  Errors: as tm_gemm_e4m3.
+ */
+tm_status tm_gemm_experts(const void *X, int64_t ldx, const void *W, int64_t ldw, void *Y, int64_t ldy,
+                          const int32_t *starts, int32_t E, int64_t T, int64_t N, int64_t K, int32_t xtype,
+                          int32_t ytype, uint32_t flags, tm_stream_t stream);
+
+/*
+ * tm_gemm_experts_bwd -- its gradients:
+ *   DX[t, :] = W_e^T DY[t, :],   DW_e = sum over the rows t of e of DY[t, :] X[t, :]^T.
+ *   DY, lddy   [T, N] of xtype    X, W as in the forward call (X only for DW, W only for DX)
+ *   DX, lddx   output [T, K] of xtype, or NULL
+ *   DW, lddw   output [E, N, K] of wtype (xtype or TM_F32), or NULL; zeros for an
+ *              expert without rows.  Rows that belong to nobody take no part, whatever they hold
+ * Errors: as tm_gemm_e4m3.
+ */
+tm_status tm_gemm_experts_bwd(const void *DY, int64_t lddy, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                              void *DX, int64_t lddx, void *DW, int64_t lddw, const int32_t *starts, int32_t E,
+                              int64_t T, int64_t N, int64_t K, int32_t xtype, int32_t wtype, uint32_t flags,
+                              tm_stream_t stream);
+
+/*
+ * Gradients clipped by their norm together: norm = sqrt(sum g^2) over any number of
+ * tensors, out = g * min(1, max_norm / (norm + eps)), rounded once to g's type.
+ *
+ * tm_clip_plan -- fills the HOST buffer plan (tm_clip_chunks(sizes, n) entries of
+ * TM_CLIP_CHUNK_BYTES) for n contiguous tensors: device pointers grads[i], outs[i]
+ * (grads[i] itself: in place; NULL, or outs NULL: only the norm), sizes[i]
+ * elements of types[i] (TM_F32, TM_F16, TM_BF16).  Copied to the device once (16-byte aligned), it
+ * serves every call while the tensors stay where they are.  No output may overlap another
+ * tensor's memory (checked against its own gradient only).  Host only.
+ * tm_clip_chunks returns -1 for bad arguments.
+ *
+ * tm_clip_grads -- one step:
+ *   plan, chunks   the device copy
+ *   max_norm   >= 0; infinity: no clipping.  With factor 1 a gradient in place is not written
+ *   norm       output, one fp32 on the device.  It is right wherever fp32 holds it: squares
+ *              beyond fp32's range are added in 64 bits.  A NaN or infinite gradient makes
+ *              it so; then out = g * NaN, or g * 0
+ *   workspace  tm_clip_workspace_bytes() bytes, 16-byte aligned, in use until the
+ *              call's kernels finish
+ * The same tensors give the same bits.  Errors: INVALID_ARG, MISALIGNED, WORKSPACE, CUDA.
+ */
+#define TM_CLIP_CHUNK_BYTES 32
+int64_t tm_clip_chunks(const int64_t *sizes, int32_t n);
+tm_status tm_clip_plan(void *plan, const void *const *grads, void *const *outs, const int64_t *sizes,
+                       const int32_t *types, int32_t n);
+size_t tm_clip_workspace_bytes(void);
+tm_status tm_clip_grads(const void *plan, int64_t chunks, float max_norm, float eps, float *norm, void *workspace,
+                        size_t ws_bytes, uint32_t flags, tm_stream_t stream);
+
+/*
  * tm_check -- synchronize `stream`, then read and clear this device's status
  * word.  Returns TM_ERR_BROKEN_PROMISE if a kernel's entry check found the
  * aligned promise broken (that kernel stored nothing), TM_ERR_MISALIGNED if it

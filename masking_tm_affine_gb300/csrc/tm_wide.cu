@@ -1,0 +1,403 @@
+// tm_wide.cu -- 16-bit products grouped by expert, for experts with many rows: the output,
+// the gradient of the rows and the gradient of the weights.
+//
+//   forward       y[t, n]    = sum_k x[t, k]  w_e[n, k]
+//   rows' gradient    dx[t, k]   = sum_n dy[t, n] w_e[n, k]
+//   weights' gradient dw_e[n, k] = sum_t dy[t, n] x[t, k]     over the rows t of expert e
+//
+// One kernel: out[c, r] = sum_s wide[c, s] tall[r, s], a tile 256 of r by up to 256 of c,
+// shared by a CTA pair (tcgen05 cta_group::2: each CTA stages its 128 of the tall operand
+// and half of the wide one, 32 KB a stage of 64 of the sum, six stages; two
+// accumulators of 256 columns, so that one tile's output overlaps the next tile's sum).
+// The tall operand (r) runs along the tensor memory's lanes and c along its columns, so
+// that a warp's 32 lanes hold 32 neighbours of an output row: outputs leave as coalesced
+// stores of 64 or 128 bytes with no way through shared memory, whatever their
+// alignment, and a row past an expert's end is one that is not stored.  Nothing is
+// transposed first: an operand whose summed extent is the outer one is read MN-major.
+//
+// The rows of an expert end anywhere.  Along c that costs nothing (the product's extent is
+// a multiple of 64 of rows, the others are not stored).  Where rows are summed (the
+// weights' gradient) a last stage of r < 64 rows runs ceil(r / 16) products, and a warp
+// clears the rows between r and the next 16 in both operands first: they are
+// the next expert's, or whatever lies there.
+#include <mutex>
+
+#include "tm_products.h"
+#include "tm_umma.cuh"
+
+namespace libtm {
+namespace {
+
+constexpr int kThreadsWide = 224;  // warp 0 copies, 1 products, 2-5 outputs, 6 clears rows
+constexpr int kStages = 6;
+constexpr uint32_t kHalf = 128 * 128;       // bytes of one operand a stage and CTA: 128 of its outer extent by 64 of the sum
+constexpr uint32_t kPanel = 64 * 128;       // MN-major: 64 of the outer extent by 64 of the sum
+constexpr uint32_t kStageBytes = 2 * kHalf;
+constexpr int kGroup = 8;                   // c tiles that run at the same time, for the sake of L2
+
+enum Mode { kForward = 0, kRows = 1, kWeights = 2 };
+
+struct WideArgs {
+    void *out;
+    int64_t ldo;
+    const int32_t *starts;
+    unsigned *status;
+    int otype, E, T;
+    int R, C;    // extents of r, and of c where c is not an expert's rows
+    int rtiles, ctiles;  // of 256 (ctiles: weights' gradient)
+    int steps;   // stages a tile (not of the weights' gradient)
+    uint32_t id;
+};
+
+struct WideSmem {
+    alignas(8) uint64_t full[kStages], empty[kStages], tail[kStages], acc_full[2], acc_empty[2], done;
+    uint32_t tmem;
+    int abort;
+    Experts x;
+};
+
+// A tile: expert, first of r and c, how many of c, the rows summed (weights' gradient).
+struct Tile {
+    int e, r0, c0, n, s0, steps, last;  // last: rows of the last stage, 64 if it is whole
+};
+
+template <int MODE>
+struct Walk {
+    const WideArgs &a;
+    const Experts &x;
+    int e = 0;
+    __device__ Walk(const WideArgs &args, const Experts &experts) : a(args), x(experts) {}
+    __device__ Tile at(int item)
+    {
+        Tile t;
+        int cts, local;
+        if constexpr (MODE == kWeights) {
+            const int per = a.rtiles * a.ctiles;
+            e = item / per;
+            local = item - e * per;
+            cts = a.ctiles;
+        } else {
+            while ((int64_t)x.before[e + 1] * a.rtiles <= item) ++e;
+            cts = x.before[e + 1] - x.before[e];
+            local = item - x.before[e] * a.rtiles;
+        }
+        // blocks of kGroup tiles of c; within one, c is the faster
+        const int block = local / (kGroup * a.rtiles), in = local - block * kGroup * a.rtiles;
+        const int wide = cts - block * kGroup < kGroup ? cts - block * kGroup : kGroup;
+        const int ct = block * kGroup + in % wide;
+        t.e = e;
+        t.r0 = in / wide * 256;
+        if constexpr (MODE == kWeights) {
+            t.c0 = ct * 256;
+            t.n = a.C - t.c0 < 256 ? a.C - t.c0 : 256;
+            t.s0 = x.first[e];
+            t.steps = (x.count[e] + 63) / 64;
+            t.last = x.count[e] - (t.steps - 1) * 64;
+        } else {
+            const int left = x.count[e] - ct * 256;
+            t.c0 = x.first[e] + ct * 256;
+            t.n = left < 256 ? left : 256;
+            t.s0 = 0;
+            t.steps = a.steps;
+            t.last = 64;
+        }
+        return t;
+    }
+};
+
+template <int MODE, typename O>
+__global__ void __launch_bounds__(kThreadsWide, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap mtall, const __grid_constant__ CUtensorMap mwide, const WideArgs a)
+{
+    constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeights;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    __shared__ WideSmem s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int unit = (int)(blockIdx.x >> 1), units = (int)(gridDim.x >> 1);
+
+    pdl_trigger();
+    if (warp == 1) acc_alloc<true>(&s.tmem, 512);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.full[i], 2);  // each CTA says what it copies, or that its last rows are cleared
+            mbar_init(&s.empty[i], 1);
+            mbar_init(&s.tail[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], 8);
+        }
+        mbar_init(&s.done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s.abort = 0;
+    }
+    experts_read(s.x, a.starts, a.E, a.T, 256, a.status);
+    acc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist
+    acc_fence_after();
+    const uint32_t tmem = s.tmem;
+    const int items = MODE == kWeights ? a.E * a.rtiles * a.ctiles : s.x.before[a.E] * a.rtiles;
+    Walk<MODE> walk(a, s.x);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            Turn t;
+            uint32_t used = 0, tails = 0;  // tails: slots whose last filling was counted on `tail`
+            uint32_t tail_parity = 0;
+            bool ok = true;
+            for (int item = unit; ok && item < items; item += units) {
+                const Tile w = walk.at(item);
+                const int r = w.r0 + (int)rank * 128;
+                // the wide operand's share of this CTA: half of the product's extent
+                const int half = B_MN ? 128 : (w.n + 63) / 64 * 32, c = w.c0 + (int)rank * half;
+                const uint32_t bytes = kHalf + (B_MN ? kHalf : (uint32_t)half * 128u);
+                for (int k = 0; k < w.steps; ++k) {
+                    if (used >= kStages && !role_wait<true>(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = smem_u32(ring) + t.slot * kStageBytes;
+                    const int k0 = w.s0 + k * 64;
+                    const bool cut = MODE == kWeights && k == w.steps - 1 && w.last % 16 != 0;
+                    if (cut) {
+                        if constexpr (MODE == kWeights) {
+                            const uint32_t bar = smem_u32(&s.tail[t.slot]);
+                            mbar_expect(&s.tail[t.slot], bytes);
+                            for (int p = 0; p < 2; ++p) {
+                                tma_load_2d(at + p * kPanel, &mtall, r + 64 * p, k0, bar);
+                                tma_load_2d(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
+                            }
+                            tails |= 1u << t.slot;
+                            tail_parity ^= 1u << t.slot;
+                        }
+                    } else {
+                        const uint32_t bar = cluster_addr(smem_u32(&s.full[t.slot]), 0);
+                        mbar_expect_cluster(bar, bytes);
+                        if constexpr (MODE == kWeights) {
+                            for (int p = 0; p < 2; ++p) {
+                                tma_load_2d_pair(at + p * kPanel, &mtall, r + 64 * p, k0, bar);
+                                tma_load_2d_pair(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
+                            }
+                        } else {
+                            if constexpr (A_MN) {
+                                for (int p = 0; p < 2; ++p) tma_load_3d_pair(at + p * kPanel, &mtall, r + 64 * p, k0, w.e, bar);
+                            } else {
+                                tma_load_3d_pair(at, &mtall, k0, r, w.e, bar);
+                            }
+                            for (int b = 0; b < half; b += 32)
+                                tma_load_2d_pair(at + kHalf + (uint32_t)b * 128u, &mwide, k0, c + b, bar);
+                        }
+                        tails &= ~(1u << t.slot);
+                    }
+                    ++used;
+                    t.next(kStages);
+                }
+            }
+            // nothing may still be landing when the pair leaves: the last filling of each slot
+            for (uint32_t i = 0; i < (uint32_t)kStages && i < used; ++i) {
+                if (tails >> i & 1u)
+                    mbar_wait_bounded(smem_u32(&s.tail[i]), (tail_parity >> i & 1u) ^ 1u);
+                if (rank == 0) mbar_wait_bounded(smem_u32(&s.full[i]), ((used - i + kStages - 1) / kStages - 1) & 1u);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            Turn t, acc;
+            uint32_t runs = 0;
+            bool ok = true;
+            for (int item = unit; ok && item < items; item += units) {
+                const Tile w = walk.at(item);
+                if (w.steps == 0) continue;
+                if (runs >= 2 && !role_wait<true>(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status)) break;
+                acc_fence_after();
+                ++runs;
+                const uint32_t id = a.id | ((B_MN ? 256u : (uint32_t)((w.n + 63) / 64 * 64)) >> 3) << 17;
+                const uint32_t d = tmem + acc.slot * 256;
+                for (int k = 0; k < w.steps; ++k) {
+                    if (!role_wait<true>(&s.full[t.slot], t.phase, &s.abort, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    acc_fence_after();
+                    const uint32_t at = smem_u32(ring) + t.slot * kStageBytes;
+                    const int js = MODE == kWeights && k == w.steps - 1 ? (w.last + 15) / 16 : 4;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (MODE != kWeights || j < js)
+                            umma<false, true>(d, A_MN ? operand_mn(at + j * 2048, kPanel) : operand_k(at + j * 32),
+                                              B_MN ? operand_mn(at + kHalf + j * 2048, kPanel) : operand_k(at + kHalf + j * 32),
+                                              id, j != 0 || k != 0);
+                    umma_done<true>(&s.empty[t.slot]);
+                    t.next(kStages);
+                }
+                if (ok) {
+                    umma_done<true>(&s.acc_full[acc.slot]);
+                    acc.next(2);
+                }
+            }
+            umma_done<true>(&s.done);
+            mbar_wait_bounded(smem_u32(&s.done), 0);
+        }
+    } else if (warp < 6) {
+        const int q = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        const uint32_t free0 = cluster_addr(smem_u32(&s.acc_empty[0]), 0), free1 = cluster_addr(smem_u32(&s.acc_empty[1]), 0);
+        O *out = reinterpret_cast<O *>(a.out);
+        Turn acc;
+        bool waited = false;
+        for (int item = unit; item < items; item += units) {
+            const Tile w = walk.at(item);
+            const int r = w.r0 + (int)rank * 128 + q * 32 + lane;
+            O *p = out + ((MODE == kWeights ? (int64_t)w.e * a.C : 0) + w.c0) * a.ldo + r;
+            if (w.steps > 0) {
+                if (!__all_sync(0xffffffffu, role_wait<true>(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status))) break;
+                acc_fence_after();
+            }
+            if (!waited) {
+                pdl_wait();
+                waited = true;
+            }
+#pragma unroll 1
+            for (int c0 = 0; c0 < w.n; c0 += 32) {
+                float v[32];
+                if (w.steps > 0) {
+                    acc_load32(lanes + acc.slot * 256 + c0, v);
+                    acc_load_wait(v);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    if (c0 + c < w.n && r < a.R) *p = from_f<O>(v[c]);
+                    p += a.ldo;
+                }
+            }
+            if (w.steps > 0) {
+                acc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc.slot ? free1 : free0);
+                acc.next(2);
+            }
+        }
+    } else if (MODE == kWeights) {
+        // rows past an expert's end, up to the next 16 of the sum, in the stage that holds its last rows
+        Turn t;
+        uint32_t parity = 0;
+        for (int item = unit; item < items; item += units) {
+            const Tile w = walk.at(item);
+            if (w.steps == 0) continue;
+            for (int k = 0; k + 1 < w.steps; ++k) t.next(kStages);
+            if (w.last % 16 != 0) {
+                if (!__all_sync(0xffffffffu, role_wait(&s.tail[t.slot], parity >> t.slot & 1u, &s.abort, a.status))) break;
+                parity ^= 1u << t.slot;
+                const uint32_t at = smem_u32(ring) + t.slot * kStageBytes;
+                const int upto = (w.last + 15) / 16 * 16;
+                // a row of the sum is 128 bytes in each of the four panels: 8 lanes a row, 4 panels at once
+                for (int row = w.last; row < upto; ++row)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at + (uint32_t)(lane >> 3) * kPanel +
+                                                                                (uint32_t)row * 128u + (uint32_t)(lane & 7) * 16u),
+                                 "r"(0)
+                                 : "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&s.full[t.slot]), 0));
+            }
+            t.next(kStages);
+        }
+    }
+    pdl_wait();
+    acc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the pair's products, copies and arrivals are over
+    if (warp == 1) {
+        __syncwarp();
+        acc_fence_after();
+        acc_free<true>(tmem, 512);
+    }
+}
+
+constexpr size_t kWideSmem = kStages * kStageBytes + 1024;
+
+template <int MODE, typename O>
+tm_status launch_wide(const CUtensorMap &tall, const CUtensorMap &wide, const WideArgs &a, int64_t items, const DevInfo &dev,
+                      cudaStream_t s, bool pdl)
+{
+    const void *k = (const void *)wide_kernel<MODE, O>;
+    static std::once_flag once[kMaxDevices];
+    static bool good[kMaxDevices];
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return TM_ERR_CUDA;
+    std::call_once(once[d], [&] {
+        good[d] = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWideSmem) == cudaSuccess;
+        if (!good[d]) cudaGetLastError();
+    });
+    if (!good[d]) return TM_ERR_CUDA;
+    const int64_t pairs = dev.sms / 2, units = items < pairs ? items : pairs;
+    void *args[] = {const_cast<CUtensorMap *>(&tall), const_cast<CUtensorMap *>(&wide), const_cast<WideArgs *>(&a)};
+    return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(kThreadsWide), args, kWideSmem, s, pdl, 2);
+}
+
+template <int MODE>
+tm_status launch_typed(const CUtensorMap &tall, const CUtensorMap &wide, const WideArgs &a, int64_t items, const DevInfo &dev,
+                       cudaStream_t s, bool pdl)
+{
+    if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
+    if (a.otype == TM_F32) return launch_wide<MODE, float>(tall, wide, a, items, dev, s, pdl);
+    if (a.otype == TM_F16) return launch_wide<MODE, __half>(tall, wide, a, items, dev, s, pdl);
+    return launch_wide<MODE, __nv_bfloat16>(tall, wide, a, items, dev, s, pdl);
+}
+
+int tiles256(int64_t n) { return (int)((n + 255) / 256); }
+
+}  // namespace
+
+tm_status wide_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
+{
+    WideArgs a = {};
+    a.out = p.out;
+    a.ldo = p.ldo;
+    a.starts = p.starts;
+    a.status = dev.status;
+    a.otype = p.otype;
+    a.E = p.E;
+    a.T = (int)p.T;
+    a.R = (int)p.F;
+    a.rtiles = tiles256(p.F);
+    a.steps = (int)((p.R + 63) / 64);
+    a.id = instruction(p.kind == kProductBF16 ? 1u : 0u, p.w_mn, false, 256, 0);
+    CUtensorMap tall, wide;
+    if (!rows_map(&tall, p.kind, p.w, p.w_mn ? p.F : p.R, p.w_mn ? p.R : p.F, p.ldw, p.E, p.w_mn ? 64 : 128) ||
+        !rows_map(&wide, p.kind, p.x, p.R, p.T, p.ldx, 0, 32))
+        return TM_ERR_CUDA;
+    const int64_t busy = p.E < p.T ? p.E : p.T, items = ((p.T + 255) / 256 + busy) * a.rtiles;
+    return p.w_mn ? launch_typed<kRows>(tall, wide, a, items, dev, s, pdl)
+                  : launch_typed<kForward>(tall, wide, a, items, dev, s, pdl);
+}
+
+tm_status wide_weights(ProductKind kind, const void *dy, int64_t lddy, const void *x, int64_t ldx, void *dw, int64_t lddw,
+                       int32_t wtype, const int32_t *starts, int32_t E, int64_t T, int64_t N, int64_t K, const DevInfo &dev,
+                       cudaStream_t s, bool pdl)
+{
+    WideArgs a = {};
+    a.out = dw;
+    a.ldo = lddw;
+    a.starts = starts;
+    a.status = dev.status;
+    a.otype = wtype;
+    a.E = E;
+    a.T = (int)T;
+    a.R = (int)K;
+    a.C = (int)N;
+    a.rtiles = tiles256(K);
+    a.ctiles = tiles256(N);
+    a.id = instruction(kind == kProductBF16 ? 1u : 0u, true, true, 256, 0);
+    CUtensorMap tall, wide;
+    if (!rows_map(&tall, kind, x, K, T, ldx, 0, 64) || !rows_map(&wide, kind, dy, N, T, lddy, 0, 64)) return TM_ERR_CUDA;
+    return launch_typed<kWeights>(tall, wide, a, (int64_t)E * a.rtiles * a.ctiles, dev, s, pdl);
+}
+
+}  // namespace libtm

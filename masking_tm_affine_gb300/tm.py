@@ -87,6 +87,15 @@ SIGNATURES = {
     "tm_kv4_attention_workspace_bytes": (_sz, [_i32, _i64, _i32, _i64, _i32, _i32, _i32]),
     "tm_kv4_attention": (_st, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _i64,
                                _i32, _i64, _i32, _i32, _i32, _f32, _i32, _i32, _vp, _sz, _u32, _vp]),
+    "tm_quant_e4m3": (_st, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i32, _i32, _u32, _vp]),
+    "tm_gemm_e4m3": (_st, [_vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _i32, _u32, _vp]),
+    "tm_gemm_experts": (_st, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _i32, _i32, _u32, _vp]),
+    "tm_gemm_experts_bwd": (_st, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _i64,
+                                  _i32, _i32, _u32, _vp]),
+    "tm_clip_chunks": (_i64, [_vp, _i32]),
+    "tm_clip_plan": (_st, [_vp, _vp, _vp, _vp, _vp, _i32]),
+    "tm_clip_workspace_bytes": (_sz, []),
+    "tm_clip_grads": (_st, [_vp, _i64, _f32, _f32, _vp, _vp, _sz, _u32, _vp]),
     "tm_check": (_st, [_vp]),
     "tm_tile_walk_probe": (_st, [_i64, _i32, _vp, _vp]),
     "tm_scale2d_unchecked": (_st, [_vp, _i64, _vp, _i64, _i64, _i64, _f32, _i32, _i32, _vp]),
@@ -338,6 +347,67 @@ def tm_kv4_attention(Q, qs_tok: int, qs_head: int, O, os_tok: int, os_head: int,
     _ok(load().tm_kv4_attention(_ptr(Q), qs_tok, qs_head, _ptr(O), os_tok, os_head, _ptr(lse), _ptr(pool), pages, page,
                                 _ptr(table), ldt, _ptr(lens), _ptr(qstart), B, Tq, max_q, max_len, Hq, Hkv, D, scale,
                                 window, xtype, _ptr(workspace), ws_bytes, flags, _stream(stream)), "tm_kv4_attention")
+
+
+def tm_quant_e4m3(X, ldx: int, M: int, N: int, Y, ldy: int, scales, rows: int = 1, xtype: int = TM_F32, flags: int = 0,
+                  stream=None) -> None:
+    """Codes of x in 8 bits, with a scale for each run of 128 columns of 1 or 128 rows."""
+    _ok(load().tm_quant_e4m3(_ptr(X), ldx, M, N, _ptr(Y), ldy, _ptr(scales), rows, xtype, flags, _stream(stream)),
+        "tm_quant_e4m3")
+
+
+def tm_gemm_e4m3(A, lda: int, sa, group: int, B, ldb: int, sb, C, ldc: int, starts, E: int, M: int, N: int, K: int,
+                 ctype: int = TM_F32, flags: int = 0, stream=None) -> None:
+    """C = A B^T of 8-bit operands with their scales, each row with its expert's matrix."""
+    _ok(load().tm_gemm_e4m3(_ptr(A), lda, _ptr(sa), group, _ptr(B), ldb, _ptr(sb), _ptr(C), ldc, _ptr(starts), E, M, N, K,
+                            ctype, flags, _stream(stream)), "tm_gemm_e4m3")
+
+
+def tm_gemm_experts(X, ldx: int, W, ldw: int, Y, ldy: int, starts, E: int, T: int, N: int, K: int, xtype: int = TM_BF16,
+                    ytype: int = TM_BF16, flags: int = 0, stream=None) -> None:
+    """Y[t] = W_e X[t] for the rows t of each expert e."""
+    _ok(load().tm_gemm_experts(_ptr(X), ldx, _ptr(W), ldw, _ptr(Y), ldy, _ptr(starts), E, T, N, K, xtype, ytype, flags,
+                               _stream(stream)), "tm_gemm_experts")
+
+
+def tm_gemm_experts_bwd(DY, lddy: int, X, ldx: int, W, ldw: int, DX, lddx: int, DW, lddw: int, starts, E: int, T: int,
+                        N: int, K: int, xtype: int = TM_BF16, wtype: int = TM_BF16, flags: int = 0, stream=None) -> None:
+    """DX[t] = W_e^T DY[t] and DW_e = sum over e's rows of DY[t] X[t]^T; either may be None."""
+    _ok(load().tm_gemm_experts_bwd(_ptr(DY), lddy, _ptr(X), ldx, _ptr(W), ldw, _ptr(DX), lddx, _ptr(DW), lddw,
+                                   _ptr(starts), E, T, N, K, xtype, wtype, flags, _stream(stream)), "tm_gemm_experts_bwd")
+
+
+TM_CLIP_CHUNK_BYTES = 32  # include/tm.h
+
+
+def tm_clip_chunks(sizes) -> int:
+    return int(load().tm_clip_chunks(ctypes.cast((_i64 * max(len(sizes), 1))(*sizes), _vp), len(sizes)))
+
+
+def tm_clip_plan(grads, outs, sizes, types):
+    """The table tm_clip_grads takes, as a torch byte tensor on the host, to be copied to the device.  ``outs`` may be
+    None (only the norm), and so may any of its entries; an entry that is its gradient is clipped in place."""
+    import torch
+    n = len(sizes)
+    if len(grads) != n or len(types) != n or (outs is not None and len(outs) != n):
+        raise TmError(TM_ERR_INVALID_ARG, "tm_clip_plan")
+    plan = torch.empty(max(tm_clip_chunks(sizes), 1) * TM_CLIP_CHUNK_BYTES, dtype=torch.uint8)
+    table = lambda t, v: ctypes.cast((t * max(n, 1))(*v), _vp)  # noqa: E731
+    _ok(load().tm_clip_plan(plan.data_ptr(), table(_vp, [_ptr(g) for g in grads]),
+                            None if outs is None else table(_vp, [_ptr(o) for o in outs]), table(_i64, sizes),
+                            table(_i32, types), n), "tm_clip_plan")
+    return plan
+
+
+def tm_clip_workspace_bytes() -> int:
+    return int(load().tm_clip_workspace_bytes())
+
+
+def tm_clip_grads(plan, chunks: int, max_norm: float, eps: float, norm, workspace, ws_bytes: int, flags: int = 0,
+                  stream=None) -> None:
+    """The norm of all gradients of the plan, and the gradients times min(1, max_norm / (norm + eps))."""
+    _ok(load().tm_clip_grads(_ptr(plan), chunks, max_norm, eps, _ptr(norm), _ptr(workspace), ws_bytes, flags,
+                             _stream(stream)), "tm_clip_grads")
 
 
 def tm_check(stream=None) -> None:
