@@ -170,5 +170,6 @@ extern "C" tm_status tm_gemm_e4m3(const void *A, int64_t lda, const float *sa, i
     p.sa = sa;
     p.sb = sb;
     p.group = group;
-    return thin_product(p, *dev, as_stream(stream), (flags & TM_PDL) != 0);
+    const bool pdl = (flags & TM_PDL) != 0;
+    return few_rows(p) ? thin_product(p, *dev, as_stream(stream), pdl) : wide8_product(p, *dev, as_stream(stream), pdl);
 }

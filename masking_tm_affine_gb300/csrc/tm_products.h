@@ -34,6 +34,9 @@ bool rows_map(CUtensorMap *m, ProductKind kind, const void *p, int64_t inner, in
 // Few rows an expert: tiles of 128 features and up to 128 rows, split along the sum.
 tm_status thin_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl);
 
+// 8 bits, many rows an expert: CTA pairs, tiles of 256 by 256.
+tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl);
+
 // 16 bits, many rows an expert: CTA pairs, tiles of 256 by 256.
 tm_status wide_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl);
 // dw [E][N][K] of wtype from dy [T][N] and x [T][K].

@@ -221,23 +221,24 @@ __global__ void __launch_bounds__(kThreadsThin, 1)
 #pragma unroll
                 for (int c = 0; c < BT; ++c) sum[c] = 0.0f;
                 const float *sb = a.sb + ((int64_t)w.e * a.ftiles + w.f0 / 128) * G;
-                // this warp's copy of the rows' factors, a step ahead
-                float nxt[BT / 32];
-                auto factors = [&](int k) {
-                    const float m = k < k1 ? sb[k] : 0.0f;
+                // this warp's copy of the rows' factors; the next block's are on their way meanwhile
+                float fa[BT / 32], fb = 0.0f;
+                auto fetch = [&](int k) {
+                    if (k >= k1) return;
+                    fb = __ldg(sb + k);
 #pragma unroll
                     for (int i = 0; i < BT / 32; ++i) {
                         const int t = i * 32 + lane;
                         const int64_t row = w.row + (t < w.n ? t : 0);
-                        nxt[i] = k < k1 && t < w.n ? m * a.sa[a.group ? row * G + k : row] : 0.0f;
+                        fa[i] = __ldg(a.sa + (a.group ? row * G + k : row));
                     }
                 };
-                factors(k0);
+                fetch(k0);
                 for (int k = k0; k < k1; ++k) {
                     float *factor = s.scale[q][k & 1];
 #pragma unroll
-                    for (int i = 0; i < BT / 32; ++i) factor[i * 32 + lane] = nxt[i];
-                    factors(k + 1);
+                    for (int i = 0; i < BT / 32; ++i) factor[i * 32 + lane] = fa[i] * fb;
+                    fetch(k + 1);
                     __syncwarp();
                     ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status));
                     if (!ok) break;

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                 const int half = B_MN ? 128 : (w.n + 63) / 64 * 32, c = w.c0 + (int)rank * half;
                 const uint32_t bytes = kHalf + (B_MN ? kHalf : (uint32_t)half * 128u);
                 for (int k = 0; k < w.steps; ++k) {
-                    if (used >= kStages && !role_wait<true>(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
+                    if (used >= kStages && !role_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
                         ok = false;
                         break;
                     }
@@ -211,13 +211,16 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
             for (int item = unit; ok && item < items; item += units) {
                 const Tile w = walk.at(item);
                 if (w.steps == 0) continue;
-                if (runs >= 2 && !role_wait<true>(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status)) break;
+                if (runs >= 2 && !role_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status)) break;
                 acc_fence_after();
                 ++runs;
                 const uint32_t id = a.id | ((B_MN ? 256u : (uint32_t)((w.n + 63) / 64 * 64)) >> 3) << 17;
                 const uint32_t d = tmem + acc.slot * 256;
                 for (int k = 0; k < w.steps; ++k) {
-                    if (!role_wait<true>(&s.full[t.slot], t.phase, &s.abort, a.status)) {
+                    // a cut stage's rows were cleared by the pair's threads; others are the copies' alone
+                    const bool cut = MODE == kWeights && k == w.steps - 1 && w.last % 16 != 0;
+                    if (!(cut ? role_wait<true>(&s.full[t.slot], t.phase, &s.abort, a.status)
+                              : role_wait(&s.full[t.slot], t.phase, &s.abort, a.status))) {
                         ok = false;
                         break;
                     }
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
             const int r = w.r0 + (int)rank * 128 + q * 32 + lane;
             O *p = out + ((MODE == kWeights ? (int64_t)w.e * a.C : 0) + w.c0) * a.ldo + r;
             if (w.steps > 0) {
-                if (!__all_sync(0xffffffffu, role_wait<true>(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status))) break;
+                if (!__all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status))) break;
                 acc_fence_after();
             }
             if (!waited) {
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
             if (w.steps > 0) {
                 acc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(acc.slot ? free1 : free0);
+                if (lane == 0) mbar_arrive_remote(acc.slot ? free1 : free0);
                 acc.next(2);
             }
         }

@@ -1,0 +1,341 @@
+// tm_wide8.cu -- the 8-bit product for experts with many rows:
+//
+//   c[t, n] = sum_b sa[t, b] sb[n / 128, b] * sum_{k in b} a[t, k] b[n, k]
+//
+// A CTA pair takes a tile of 256 rows t by 256 columns n; a stage of the ring is one block of
+// 128 of the sum, 16 KB of each operand a CTA.  Rows lie along the tensor memory's lanes
+// here: then a block's two scales are one factor a thread (its row's, times that of the 128
+// columns the thread holds), and adding a block is one packed fp32 operation for two
+// outputs.  The tensor cores make a block's sums in one accumulator of 256 columns while
+// eight warps read the other, multiply and add: 128 sums a thread, in registers.  That
+// addition is what the kernel must keep up with: 256 by 256 by 128 takes the tensor cores
+// about 512 cycles, and a CTA's share of it 128 x 256 reads and additions, 256 cycles each at best.
+//
+// Outputs leave through shared memory and TMA, so that the warps are back at the next
+// tile's sums early (16-bit outputs of whole warps' rows; others are stored directly).
+#include <mutex>
+
+#include "tm_products.h"
+#include "tm_umma.cuh"
+
+namespace libtm {
+namespace {
+
+constexpr int kThreads8 = 384;  // warp 0 copies, 1 products, 2-3 none, 4-11 sums and outputs
+constexpr int kStages8 = 4;
+constexpr uint32_t kHalf8 = 128 * 128;
+constexpr uint32_t kStage8 = 2 * kHalf8;
+constexpr int kGroup8 = 8;                 // row tiles that run at the same time, for the sake of L2
+constexpr uint32_t kOutWarp = 2 * 32 * 128;  // a warp's outputs on their way: 32 rows of two pieces of 128 bytes
+// 384 threads start with 168 registers each: 64512.  4 warps of 80 and 8 of 208 are 63488.
+constexpr int kFewRegs = 80, kManyRegs = 208;
+
+struct Wide8Args {
+    void *out;
+    int64_t ldo;
+    const int32_t *starts;
+    const float *sa, *sb;
+    unsigned *status;
+    int otype, E, T, N, ntiles, steps, group;
+    int by_copy;  // 16-bit outputs on a grid TMA can store to
+    uint32_t id;
+};
+
+struct Wide8Smem {
+    alignas(8) uint64_t full[kStages8], empty[kStages8], acc_full[2], acc_empty[2], done;
+    uint32_t tmem;
+    int abort;
+    Experts x;
+};
+
+struct Tile8 {
+    int e, row, n, n0;  // expert, first row and how many, first column
+};
+
+struct Walk8 {
+    const Wide8Args &a;
+    const Experts &x;
+    int e = 0;
+    __device__ Walk8(const Wide8Args &args, const Experts &experts) : a(args), x(experts) {}
+    __device__ Tile8 at(int item)
+    {
+        while ((int64_t)x.before[e + 1] * a.ntiles <= item) ++e;
+        const int tiles = x.before[e + 1] - x.before[e], local = item - x.before[e] * a.ntiles;
+        const int block = local / (kGroup8 * a.ntiles), in = local - block * kGroup8 * a.ntiles;
+        const int wide = tiles - block * kGroup8 < kGroup8 ? tiles - block * kGroup8 : kGroup8;
+        const int r = (block * kGroup8 + in % wide) * 256, left = x.count[e] - r;
+        return {e, x.first[e] + r, left < 256 ? left : 256, in / wide * 256};
+    }
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t v, uint64_t m)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(m));
+}
+
+__global__ void __launch_bounds__(kThreads8, 1)
+    wide8_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                 const __grid_constant__ CUtensorMap mc, const Wide8Args a)
+{
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *outs = ring + kStages8 * kStage8;
+    __shared__ Wide8Smem s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int unit = (int)(blockIdx.x >> 1), units = (int)(gridDim.x >> 1);
+
+    pdl_trigger();
+    if (warp == 1) acc_alloc<true>(&s.tmem, 512);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages8; ++i) {
+            mbar_init(&s.full[i], 2);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], 16);
+        }
+        mbar_init(&s.done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s.abort = 0;
+    }
+    experts_read(s.x, a.starts, a.E, a.T, 256, a.status);
+    acc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    acc_fence_after();
+    const uint32_t tmem = s.tmem;
+    const int items = s.x.before[a.E] * a.ntiles;
+    Walk8 walk(a, s.x);
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 0 && lane == 0) {
+            Turn t;
+            uint32_t used = 0;
+            bool ok = true;
+            for (int item = unit; ok && item < items; item += units) {
+                const Tile8 w = walk.at(item);
+                const int row = w.row + (int)rank * 128, n = w.n0 + (int)rank * 128;
+                for (int k = 0; k < a.steps; ++k) {
+                    if (used >= kStages8 && !role_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = smem_u32(ring) + t.slot * kStage8, bar = cluster_addr(smem_u32(&s.full[t.slot]), 0);
+                    mbar_expect_cluster(bar, kStage8);
+                    tma_load_2d_pair(at, &ma, k * 128, row, bar);
+                    tma_load_3d_pair(at + kHalf8, &mb, k * 128, n, w.e, bar);
+                    ++used;
+                    t.next(kStages8);
+                }
+            }
+            // nothing may still be landing when the pair leaves: the last filling of each slot
+            if (rank == 0)
+                for (uint32_t i = 0; i < (uint32_t)kStages8 && i < used; ++i)
+                    mbar_wait_bounded(smem_u32(&s.full[i]), ((used - i + kStages8 - 1) / kStages8 - 1) & 1u);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            Turn t, acc;
+            uint32_t runs = 0;
+            bool ok = true;
+            for (int item = unit; ok && item < items; item += units) {
+                for (int k = 0; k < a.steps; ++k) {
+                    if ((runs >= 2 && !role_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status)) ||
+                        !role_wait(&s.full[t.slot], t.phase, &s.abort, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    ++runs;
+                    acc_fence_after();
+                    const uint32_t at = smem_u32(ring) + t.slot * kStage8, d = tmem + acc.slot * 256;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) umma<true, true>(d, operand_k(at + j * 32), operand_k(at + kHalf8 + j * 32), a.id, j != 0);
+                    umma_done<true>(&s.empty[t.slot]);
+                    umma_done<true>(&s.acc_full[acc.slot]);
+                    t.next(kStages8);
+                    acc.next(2);
+                }
+            }
+            umma_done<true>(&s.done);
+            mbar_wait_bounded(smem_u32(&s.done), 0);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        const int q = warp & 3, half = (warp - 4) >> 2;  // lanes 32 q .., columns 128 half ..
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)half * 128;
+        const uint32_t free0 = cluster_addr(smem_u32(&s.acc_empty[0]), 0), free1 = cluster_addr(smem_u32(&s.acc_empty[1]), 0);
+        unsigned char *mine = outs + (warp - 4) * kOutWarp;
+        const int NB = (a.N + 127) / 128;
+        Turn acc;
+        bool waited = false, ok = true;
+        for (int item = unit; ok && item < items; item += units) {
+            const Tile8 w = walk.at(item);
+            const int r = (int)rank * 128 + q * 32 + lane;  // of the tile
+            const bool live = r < w.n;
+            const int64_t row = (int64_t)w.row + r;
+            const int n = w.n0 + half * 128;
+            const float *sa = a.sa + (live ? (a.group ? row * a.steps : row) : 0);
+            const float *sb = a.sb + ((int64_t)w.e * NB + (n < a.N ? n / 128 : 0)) * a.steps;
+            uint64_t sum[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sum[i] = 0;
+            // the next block's factors are on their way while this one is added
+            float fa = a.steps > 0 ? __ldg(sa) : 0.0f, fb = a.steps > 0 ? __ldg(sb) : 0.0f;
+            for (int k = 0; k < a.steps; ++k) {
+                const float f = fa * fb;
+                const uint64_t m = pack2(f, f);
+                if (k + 1 < a.steps) {
+                    fa = __ldg(sa + (a.group ? k + 1 : 0));
+                    fb = __ldg(sb + k + 1);
+                }
+                ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status));
+                if (!ok) break;
+                acc_fence_after();
+                const uint32_t at = lanes + acc.slot * 256;
+                float v0[32], v1[32];
+                auto add = [&](const float(&v)[32], int c) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) fma2(sum[c / 2 + i], pack2(v[2 * i], v[2 * i + 1]), m);
+                };
+                acc_load32(at, v0);
+                acc_load_wait(v0);
+                acc_load32(at + 32, v1);
+                add(v0, 0);
+                acc_load_wait(v1);
+                acc_load32(at + 64, v0);
+                add(v1, 32);
+                acc_load_wait(v0);
+                acc_load32(at + 96, v1);
+                add(v0, 64);
+                acc_load_wait(v1);
+                acc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(acc.slot ? free1 : free0);
+                add(v1, 96);
+                acc.next(2);
+            }
+            if (!ok) break;
+            if (!waited) {
+                pdl_wait();
+                waited = true;
+            }
+            if (n >= a.N) continue;
+            if (a.by_copy && __all_sync(0xffffffffu, live)) {
+                // 32 rows of 128 values: two pieces of 128 bytes a row, in the copy's swizzle
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float lo, hi;
+                        unpack2(sum[4 * i + j], lo, hi);
+                        if (a.otype == TM_F16)
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(hi), "f"(lo));
+                        else
+                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(hi), "f"(lo));
+                    }
+                    const uint32_t at = smem_u32(mine) + (uint32_t)(i >> 3) * (kOutWarp / 2) + (uint32_t)lane * 128u +
+                                        (uint32_t)(((i & 7) ^ (lane & 7)) * 16);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+                                 : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    const int y = w.row + (int)rank * 128 + q * 32;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        if (n + 64 * p < a.N)
+                            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&mc),
+                                         "r"(n + 64 * p), "r"(y), "r"(smem_u32(mine) + (uint32_t)p * (kOutWarp / 2))
+                                         : "memory");
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            } else if (live) {
+                const int64_t at = row * a.ldo + n;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    float v[2];
+                    unpack2(sum[i], v[0], v[1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (n + 2 * i + j < a.N) {
+                            if (a.otype == TM_F32)
+                                reinterpret_cast<float *>(a.out)[at + 2 * i + j] = v[j];
+                            else if (a.otype == TM_F16)
+                                reinterpret_cast<__half *>(a.out)[at + 2 * i + j] = __float2half_rn(v[j]);
+                            else
+                                reinterpret_cast<__nv_bfloat16 *>(a.out)[at + 2 * i + j] = __float2bfloat16_rn(v[j]);
+                        }
+                }
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+    pdl_wait();
+    acc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        acc_fence_after();
+        acc_free<true>(tmem, 512);
+    }
+}
+
+constexpr size_t kWide8Smem = kStages8 * kStage8 + 8 * kOutWarp + 1024;
+
+}  // namespace
+
+tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
+{
+    const void *k = (const void *)wide8_kernel;
+    static std::once_flag once[kMaxDevices];
+    static bool good[kMaxDevices];
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return TM_ERR_CUDA;
+    std::call_once(once[d], [&] {
+        good[d] = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWide8Smem) == cudaSuccess;
+        if (!good[d]) cudaGetLastError();
+    });
+    if (!good[d]) return TM_ERR_CUDA;
+    Wide8Args a = {};
+    a.out = p.out;
+    a.ldo = p.ldo;
+    a.starts = p.starts;
+    a.sa = p.sa;
+    a.sb = p.sb;
+    a.status = dev.status;
+    a.otype = p.otype;
+    a.E = p.E;
+    a.T = (int)p.T;
+    a.N = (int)p.F;
+    a.ntiles = (int)((p.F + 255) / 256);
+    a.steps = (int)((p.R + 127) / 128);
+    a.group = p.group;
+    a.id = instruction(0, false, false, 256, 256);
+    // TMA clips what it stores at whole 16 bytes: N must end on them
+    a.by_copy = p.otype != TM_F32 && aligned_to(p.out, 16) && p.ldo % 8 == 0 && p.F % 8 == 0;
+    CUtensorMap ma, mb, mc;
+    if (!rows_map(&ma, p.kind, p.x, p.R, p.T, p.ldx, 0, 128) || !rows_map(&mb, p.kind, p.w, p.R, p.F, p.ldw, p.E, 128)) return TM_ERR_CUDA;
+    if (a.by_copy ? !rows_map(&mc, kProductF16, p.out, p.F, p.T, p.ldo, 0, 32) : (mc = ma, false)) return TM_ERR_CUDA;
+    const int64_t busy = p.E < p.T ? p.E : p.T, items = ((p.T + 255) / 256 + busy) * a.ntiles, pairs = dev.sms / 2;
+    if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
+    const int64_t units = items < pairs ? items : pairs;
+    void *args[] = {&ma, &mb, &mc, &a};
+    return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(kThreads8), args, kWide8Smem, s, pdl, 2);
+}
+
+}  // namespace libtm
