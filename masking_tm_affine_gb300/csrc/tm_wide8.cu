@@ -27,8 +27,8 @@ constexpr uint32_t kHalf8 = 128 * 128;
 constexpr uint32_t kStage8 = 2 * kHalf8;
 constexpr int kGroup8 = 8;                 // row tiles that run at the same time, for the sake of L2
 constexpr uint32_t kOutWarp = 2 * 32 * 128;  // a warp's outputs on their way: 32 rows of two pieces of 128 bytes
-// 384 threads start with 168 registers each: 64512.  4 warps of 80 and 8 of 208 are 63488.
-constexpr int kFewRegs = 80, kManyRegs = 208;
+// 384 threads start with 168 registers each: 64512.  4 warps of 96 and 8 of 200 are 63488.
+constexpr int kFewRegs = 96, kManyRegs = 200;
 
 struct Wide8Args {
     void *out;
@@ -75,9 +75,25 @@ __device__ __forceinline__ uint64_t pack2(float a, float b)
     return r;
 }
 __device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t v, uint64_t m)
+
+// sum += m * 32 columns of the accumulator, two columns an operation.  One statement: the
+// values pass from the read to the additions in registers that nothing else names, which
+// saves the moves that separate statements took (8192 x 8192 x 4096: 255 us, so 234).
+__device__ __forceinline__ void add_columns(uint32_t at, uint64_t *s, uint64_t m)
 {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(m));
+#define TM_ADD(I, A, B) "mov.b64 p, {t" #A ", t" #B "};\n\tfma.rn.f32x2 %" #I ", p, %17, %" #I ";\n\t"
+    asm volatile(
+        "{\n\t.reg .b32 t<32>;\n\t.reg .b64 p;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, t16, "
+        "t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t" TM_ADD(0, 0, 1) TM_ADD(1, 2, 3) TM_ADD(2, 4, 5) TM_ADD(3, 6, 7) TM_ADD(4, 8, 9)
+            TM_ADD(5, 10, 11) TM_ADD(6, 12, 13) TM_ADD(7, 14, 15) TM_ADD(8, 16, 17) TM_ADD(9, 18, 19) TM_ADD(10, 20, 21)
+                TM_ADD(11, 22, 23) TM_ADD(12, 24, 25) TM_ADD(13, 26, 27) TM_ADD(14, 28, 29) TM_ADD(15, 30, 31) "}"
+        : "+l"(s[0]), "+l"(s[1]), "+l"(s[2]), "+l"(s[3]), "+l"(s[4]), "+l"(s[5]), "+l"(s[6]), "+l"(s[7]), "+l"(s[8]),
+          "+l"(s[9]), "+l"(s[10]), "+l"(s[11]), "+l"(s[12]), "+l"(s[13]), "+l"(s[14]), "+l"(s[15])
+        : "r"(at), "l"(m)
+        : "memory");
+#undef TM_ADD
 }
 
 __global__ void __launch_bounds__(kThreads8, 1)
@@ -201,26 +217,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 if (!ok) break;
                 acc_fence_after();
                 const uint32_t at = lanes + acc.slot * 256;
-                float v0[32], v1[32];
-                auto add = [&](const float(&v)[32], int c) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) fma2(sum[c / 2 + i], pack2(v[2 * i], v[2 * i + 1]), m);
-                };
-                acc_load32(at, v0);
-                acc_load_wait(v0);
-                acc_load32(at + 32, v1);
-                add(v0, 0);
-                acc_load_wait(v1);
-                acc_load32(at + 64, v0);
-                add(v1, 32);
-                acc_load_wait(v0);
-                acc_load32(at + 96, v1);
-                add(v0, 64);
-                acc_load_wait(v1);
+                for (int c = 0; c < 4; ++c) add_columns(at + 32 * c, sum + 16 * c, m);
                 acc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(acc.slot ? free1 : free0);
-                add(v1, 96);
                 acc.next(2);
             }
             if (!ok) break;
