@@ -651,7 +651,8 @@ tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_head, void 
  * a NaN is held as NaN: codes 0x7F, scale NaN.
  *   X, ldx     input [M, N] of xtype          Y, ldy   output codes [M, N], a byte each
  *   scales     output [ceil(M / rows), ceil(N / 128)] fp32
- * Errors: INVALID_ARG (also any overlap), UNSUPPORTED_TILE (rows), MISALIGNED, CUDA.
+ * Errors: INVALID_ARG (also any overlap), UNSUPPORTED_TILE (rows, more than 2^30 blocks or columns),
+ *         MISALIGNED, CUDA.
  */
 tm_status tm_quant_e4m3(const void *X, int64_t ldx, int64_t M, int64_t N, void *Y, int64_t ldy, float *scales,
                         int32_t rows, int32_t xtype, uint32_t flags, tm_stream_t stream);

@@ -4,12 +4,17 @@
 //   top = max |x| over the block,  scale = top / 448,  code = nearest e4m3 to x * 448 / top
 //
 // Each value is read once and stays in registers between the block's maximum and its codes,
-// so memory bounds it: 2 or 4 bytes in, 1 out.
+// so memory bounds it: 2 or 4 bytes in, 1 out.  At 16 bits that leaves about 11 lanes'
+// instructions a value on an SM, so the maximum is taken two values at a time on their bits.
 //
-// Codes are those of the exact quotient.  In 16 bits quotients often lie exactly on a border
-// between two codes, where an error of the last place of q = x * (448 / top) decides wrongly.
-// So a value whose q is within 4 places of a border is decided in 64 bits: |x| * 448
-// against border * top, both exact there.  Few values take that way.
+// Codes are those of the exact quotient, which q = x * (448 / top) misses by up to 2^-23 of
+// itself: wrong where a border between two codes lies between them.
+//   16-bit x.  x and top have at most 11 significant bits and a border 5, so x * 448 and border *
+//   top are integers below 2^17 on one scale: a quotient lies on a border or at least
+//   2^-17 of itself away.  q is rounded to 21 bits: that puts one that belongs on a border back
+//   on it, where the conversion takes the even code, and moves no other across.
+//   fp32 x.  A q within 4 places of a border is decided in 64 bits: |x| * 448 against
+//   border * top, both exact there.  Few values take that way.
 #include "tm_host.h"
 #include "tm_elem.cuh"
 
@@ -22,29 +27,32 @@ constexpr int kQuantThreads = 256;
 struct Factor {
     float top, by, lift;
 };
+__device__ __forceinline__ float lift_of(float top) { return top < 0x1p-60f ? 0x1p64f : 1.0f; }
 __device__ __forceinline__ Factor factor_of(float top)
 {
     Factor f;
-    f.lift = top < 8.6736174e-19f ? 1.8446744e19f : 1.0f;
+    f.lift = lift_of(top);
     f.top = top * f.lift;
     f.by = top > 0.0f ? __fdiv_rn(448.0f, f.top) : 0.0f;
     return f;
 }
 
-// x * 448 / top, moved off a border (or onto it, where the quotient lies on it) if fp32 cannot tell its side.
-__device__ __forceinline__ float quotient(float x, const Factor &f)
+__device__ __forceinline__ float near21(float q) { return as_f((as_u(q) + 4u) & ~7u); }
+
+// fp32: how far q is from a border, at least; 0 .. 8 within 4 places.  Below 2^-6 codes are
+// multiples of 2^-9: 2^-6 more, and they are spaced as at 2^-6.
+__device__ __forceinline__ uint32_t places(float q)
 {
-    const float z = fabsf(x) * f.lift, q = z * f.by;
-    // below 2^-6 codes are multiples of 2^-9: 2^-6 more, and they are spaced as at 2^-6
-    const float y = q < 0.015625f ? q + 0.015625f : q;
-    const uint32_t u = as_u(y);
-    float r = q;
-    if (((u & 0xFFFFFu) - 0x7FFFCu) <= 8u) {
-        const float edge = as_f((u & 0xFFF00000u) | 0x80000u), m = q < 0.015625f ? edge - 0.015625f : edge;
-        const double a = (double)z * 448.0, b = (double)m * (double)f.top;
-        r = a > b ? m * (1.0f + 0x1p-18f) : a < b ? m * (1.0f - 0x1p-18f) : m;
-    }
-    return copysignf(r, x);
+    const float y = fabsf(q) < 0.015625f ? fabsf(q) + 0.015625f : q;
+    return (as_u(y) & 0xFFFFFu) - 0x7FFFCu;
+}
+// q moved off the border that it is close to, to its side of it (or onto it, where the quotient lies on it).
+__device__ __noinline__ float decided(float x, float q, Factor f)
+{
+    const float p = fabsf(q), z = fabsf(x) * f.lift, y = p < 0.015625f ? p + 0.015625f : p;
+    const float edge = as_f((as_u(y) & 0xFFF00000u) | 0x80000u), m = p < 0.015625f ? edge - 0.015625f : edge;
+    const double a = (double)z * 448.0, b = (double)m * (double)f.top;
+    return copysignf(a > b ? m * (1.0f + 0x1p-18f) : a < b ? m * (1.0f - 0x1p-18f) : m, x);
 }
 
 __device__ __forceinline__ uint32_t codes2(float lo, float hi)
@@ -54,24 +62,63 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi)
     return r;
 }
 
-// The maximum of magnitudes; an infinity or NaN makes it infinite.
-__device__ __forceinline__ float join(float top, float x)
+// The largest magnitude as the bits of T, which grow with it; two halves at once in 16 bits.
+template <typename T, int W>
+__device__ __forceinline__ uint32_t join(uint32_t top, const Vec<T, W> &r)
 {
-    const float m = fabsf(x);
-    return fmaxf(top, m == m ? m : INFINITY);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) top = max(top, as_u(r.v[e]) & 0x7FFFFFFFu);
+    } else if constexpr (W == 1) {
+        top = max(top, (uint32_t)(*reinterpret_cast<const uint16_t *>(&r) & 0x7FFFu));
+    } else {
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(&r);
+#pragma unroll
+        for (int e = 0; e < W / 2; ++e) top = __vmaxu2(top, u[e] & 0x7FFF7FFFu);
+    }
+    return top;
+}
+// The maximum over `lanes` lanes, as fp32; infinite or NaN where any value is.
+template <typename T>
+__device__ __forceinline__ float joined(uint32_t top, int lanes)
+{
+    if constexpr (sizeof(T) == 2) top = max(top & 0xFFFFu, top >> 16);
+    for (int o = lanes >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if constexpr (sizeof(T) == 4)
+        return as_f(top);
+    else {
+        const uint16_t h = (uint16_t)top;
+        return to_f(*reinterpret_cast<const T *>(&h));
+    }
 }
 
-template <int W>
-__device__ __forceinline__ void put_codes(uint8_t *p, bool ok, const float (&v)[W], const Factor &f, bool finite)
+template <typename T, int W>
+__device__ __forceinline__ void put_codes(uint8_t *p, bool ok, const Vec<T, W> &r, const Factor &f, bool finite)
 {
+    float v[W], q[W];
+    widen(r, v);
+    uint32_t close = ~0u;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        q[e] = v[e] * f.lift * f.by;
+        if constexpr (sizeof(T) == 2)
+            q[e] = near21(q[e]);
+        else
+            close = min(close, places(q[e]));
+    }
+    if constexpr (sizeof(T) == 4)
+        if (close <= 8u) {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (places(q[e]) <= 8u) q[e] = decided(v[e], q[e], f);
+        }
     if constexpr (W == 1) {
-        if (ok) *p = finite ? (uint8_t)codes2(quotient(v[0], f), 0.0f) : (uint8_t)0x7F;
+        if (ok) *p = finite ? (uint8_t)codes2(q[0], 0.0f) : (uint8_t)0x7F;
     } else {
         uint32_t w[W / 4];
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
-            w[i] = codes2(quotient(v[4 * i], f), quotient(v[4 * i + 1], f)) |
-                   codes2(quotient(v[4 * i + 2], f), quotient(v[4 * i + 3], f)) << 16;
+            w[i] = codes2(q[4 * i], q[4 * i + 1]) | codes2(q[4 * i + 2], q[4 * i + 3]) << 16;
             if (!finite) w[i] = 0x7F7F7F7Fu;
         }
         if (ok) {
@@ -83,12 +130,15 @@ __device__ __forceinline__ void put_codes(uint8_t *p, bool ok, const float (&v)[
     }
 }
 
+__device__ __forceinline__ float scale_of(float top, bool finite) { return !finite ? NAN : top > 0.0f ? __fdiv_rn(top, 448.0f) : 1.0f; }
+
 struct QuantArgs {
     const void *x;
     uint8_t *y;
     float *scales;
-    int64_t ldx, ldy, M, N, cols;  // cols: runs of 128 columns
-    int64_t tasks;
+    int64_t ldx, ldy, M, N;
+    int tasks, cols;  // cols: runs of 128 columns
+    FastDiv by_cols;
 };
 
 // One row's runs: L lanes a run, U runs a thread, neighbours in the flat order of all runs.
@@ -99,94 +149,89 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows(const QuantArgs a)
     constexpr int kRuns = kQuantThreads / L;
     pdl_trigger();
     const int lane = threadIdx.x % L;
-    const int64_t first = (int64_t)blockIdx.x * kRuns * U + threadIdx.x / L;
+    const int first = (int)blockIdx.x * kRuns * U + (int)threadIdx.x / L;
     Vec<T, W> raw[U][P];
-    int64_t row[U], col[U];
+    int row[U], col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t run = first + u * kRuns;
+        const int run = first + u * kRuns;
         const bool live = run < a.tasks;
-        row[u] = live ? run / a.cols : a.M;
+        row[u] = live ? (int)fdiv((uint32_t)run, a.by_cols) : -1;
         col[u] = live ? (run - row[u] * a.cols) * 128 + lane * W : 0;
 #pragma unroll
         for (int p = 0; p < P; ++p)
             load_vec_if(reinterpret_cast<const T *>(a.x) + (live ? row[u] * a.ldx + col[u] + p * 32 : 0),
                         live && col[u] + p * 32 < a.N, raw[u][p]);
     }
+    // two divisions a lane for its U runs together: lane u of a run's lanes takes run u's
+    float tops[U], mine = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int p = 0; p < P; ++p) bits = join(bits, raw[u][p]);
+        tops[u] = joined<T>(bits, L);
+        if (lane == u) mine = tops[u];
+    }
+    const Factor own = factor_of(mine);
+    const float scale = scale_of(mine, mine <= 3.402823466e38f);
     pdl_wait();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float v[P][W], top = 0.0f;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            widen(raw[u][p], v[p]);
-#pragma unroll
-            for (int e = 0; e < W; ++e) top = join(top, v[p][e]);
-        }
-        top = lanes_max(top, L);
-        const bool finite = top <= 3.402823466e38f, live = row[u] < a.M;
-        const Factor f = factor_of(top);
-        if (live && lane == 0)
-            a.scales[row[u] * a.cols + col[u] / 128] = !finite ? NAN : top > 0.0f ? __fdiv_rn(top, 448.0f) : 1.0f;
+        const bool live = row[u] >= 0;
+        const Factor f = {tops[u] * lift_of(tops[u]), __shfl_sync(0xffffffffu, own.by, u, L), lift_of(tops[u])};
+        if (live && lane == u) a.scales[(int64_t)row[u] * a.cols + col[u] / 128] = scale;
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            put_codes<W>(a.y + (live ? row[u] * a.ldy + col[u] + p * 32 : 0), live && col[u] + p * 32 < a.N, v[p], f, finite);
+            put_codes(a.y + (live ? row[u] * a.ldy + col[u] + p * 32 : 0), live && col[u] + p * 32 < a.N, raw[u][p], f,
+                      tops[u] <= 3.402823466e38f);
     }
 }
 
 // A block of 128 by 128 values a CTA, 64 a thread.
 template <typename T, int W>
-__global__ void __launch_bounds__(kQuantThreads, 2) quant_blocks(const QuantArgs a)
+__global__ void __launch_bounds__(kQuantThreads, W == 1 ? 2 : 3) quant_blocks(const QuantArgs a)
 {
     constexpr int L = W == 1 ? 32 : 128 / W, P = W == 1 ? 4 : 1, R = kQuantThreads / L, I = 128 / R;
     __shared__ float tops[kQuantThreads / 32];
     pdl_trigger();
     const int lane = threadIdx.x % L, r0 = threadIdx.x / L;
-    for (int64_t b = blockIdx.x; b < a.tasks; b += gridDim.x) {
-        const int64_t br = b / a.cols, bc = b - br * a.cols, col = bc * 128 + lane * W;
-        Vec<T, W> raw[I][P];
+    const int br = (int)fdiv(blockIdx.x, a.by_cols), bc = (int)blockIdx.x - br * a.cols, col = bc * 128 + lane * W;
+    Vec<T, W> raw[I][P];
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            const int64_t row = br * 128 + r0 + i * R;
+    for (int i = 0; i < I; ++i) {
+        const int64_t row = (int64_t)br * 128 + r0 + i * R;
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const bool ok = row < a.M && col + p * 32 < a.N;
-                load_vec_if(reinterpret_cast<const T *>(a.x) + (ok ? row * a.ldx + col + p * 32 : 0), ok, raw[i][p]);
-            }
-        }
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < I; ++i)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                float v[W];
-                widen(raw[i][p], v);
-#pragma unroll
-                for (int e = 0; e < W; ++e) top = join(top, v[e]);
-            }
-        top = lanes_max(top, 32);
-        if ((threadIdx.x & 31) == 0) tops[threadIdx.x / 32] = top;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kQuantThreads / 32; ++i) top = fmaxf(top, tops[i]);
-        __syncthreads();  // read, before the next block's
-        const bool finite = top <= 3.402823466e38f;
-        const Factor f = factor_of(top);
-        pdl_wait();
-        if (threadIdx.x == 0) a.scales[b] = !finite ? NAN : top > 0.0f ? __fdiv_rn(top, 448.0f) : 1.0f;
-#pragma unroll
-        for (int i = 0; i < I; ++i) {
-            const int64_t row = br * 128 + r0 + i * R;
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const bool ok = row < a.M && col + p * 32 < a.N;
-                float v[W];
-                widen(raw[i][p], v);
-                put_codes<W>(a.y + (ok ? row * a.ldy + col + p * 32 : 0), ok, v, f, finite);
-            }
+        for (int p = 0; p < P; ++p) {
+            const bool ok = row < a.M && col + p * 32 < a.N;
+            load_vec_if(reinterpret_cast<const T *>(a.x) + (ok ? row * a.ldx + col + p * 32 : 0), ok, raw[i][p]);
         }
     }
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) bits = join(bits, raw[i][p]);
+    float top = joined<T>(bits, 32);
+    // a NaN loses against a number in fmaxf: it counts as an infinity
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x / 32] = top <= 3.402823466e38f ? top : INFINITY;
+    __syncthreads();
+    top = tops[0];
+#pragma unroll
+    for (int i = 1; i < kQuantThreads / 32; ++i) top = fmaxf(top, tops[i]);
+    const bool finite = top <= 3.402823466e38f;
+    const Factor f = factor_of(top);
     pdl_wait();
+    if (threadIdx.x == 0) a.scales[blockIdx.x] = scale_of(top, finite);
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        const int64_t row = (int64_t)br * 128 + r0 + i * R;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const bool ok = row < a.M && col + p * 32 < a.N;
+            put_codes(a.y + (ok ? row * a.ldy + col + p * 32 : 0), ok, raw[i][p], f, finite);
+        }
+    }
 }
 
 template <typename T, int W>
@@ -194,10 +239,9 @@ tm_status launch_quant(const QuantArgs &a, int32_t rows, cudaStream_t s, bool pd
 {
     void *args[] = {const_cast<QuantArgs *>(&a)};
     if (rows == 128)
-        return launch_kernel((const void *)quant_blocks<T, W>, dim3(flat_grid(a.tasks)), dim3(kQuantThreads), args, 0, s, pdl);
+        return launch_kernel((const void *)quant_blocks<T, W>, dim3((unsigned)a.tasks), dim3(kQuantThreads), args, 0, s, pdl);
     constexpr int U = W == 1 ? 2 : 4, kRuns = kQuantThreads / (W == 1 ? 32 : 128 / W);
-    const int64_t blocks = (a.tasks + kRuns * U - 1) / (kRuns * U);
-    if (blocks > INT32_MAX) return TM_ERR_UNSUPPORTED_TILE;
+    const int blocks = (a.tasks + kRuns * U - 1) / (kRuns * U);
     return launch_kernel((const void *)quant_rows<T, W, U>, dim3((unsigned)blocks), dim3(kQuantThreads), args, 0, s, pdl);
 }
 
@@ -221,12 +265,13 @@ extern "C" tm_status tm_quant_e4m3(const void *X, int64_t ldx, int64_t M, int64_
     if (M > 0 && N > 0 && scales == nullptr) return TM_ERR_INVALID_ARG;
     if (rows != 1 && rows != 128) return TM_ERR_UNSUPPORTED_TILE;
     if (!aligned_to(X, (uintptr_t)e) || !aligned_to(scales, 4)) return TM_ERR_MISALIGNED;
-    QuantArgs a = {X, reinterpret_cast<uint8_t *>(Y), scales, ldx, ldy, M, N, (N + 127) / 128, 0};
-    const int64_t bands = (M + rows - 1) / rows;
-    a.tasks = bands * a.cols;
-    const Span x = span_of(X, ldx, M, N, e), y = span_of(Y, ldy, M, N, 1), sc = span_of(scales, a.cols, bands, a.cols, 4);
+    const int64_t bands = (M + rows - 1) / rows, cols = (N + 127) / 128;
+    const Span x = span_of(X, ldx, M, N, e), y = span_of(Y, ldy, M, N, 1), sc = span_of(scales, cols, bands, cols, 4);
     if (meets(x, y) || meets(x, sc) || meets(y, sc)) return TM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return TM_OK;
+    if (N > (1 << 30) || bands > (1 << 30) / cols) return TM_ERR_UNSUPPORTED_TILE;
+    const QuantArgs a = {X, reinterpret_cast<uint8_t *>(Y), scales, ldx, ldy, M, N, (int)(bands * cols), (int)cols,
+                         make_fastdiv((uint32_t)cols)};
     const int w = 16 / e;
     const bool vec = aligned_to(X, 16) && aligned_to(Y, (uintptr_t)w) && ldx % w == 0 && ldy % w == 0 && N % w == 0;
     const bool pdl = (flags & TM_PDL) != 0;
