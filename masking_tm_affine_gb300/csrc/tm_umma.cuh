@@ -88,6 +88,10 @@ struct Turn {
 };
 
 // ---------------------------------------------------------------- copies
+__device__ __forceinline__ void tensormap_prefetch(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
     asm volatile(
@@ -95,12 +99,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar,
+                                                 uint64_t policy)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}],"
+        " [%5], %6;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
         : "memory");
 }
 // Into this CTA's memory, counted on a barrier of either CTA of the pair.
@@ -238,9 +243,18 @@ struct Experts {
 // All threads of the block; ends with a __syncthreads.
 __device__ __forceinline__ void experts_read(Experts &x, const int32_t *starts, int E, int T, int tile, unsigned *status)
 {
+    if (starts == nullptr) {  // one expert
+        if (threadIdx.x == 0) {
+            x.first[0] = x.before[0] = 0;
+            x.count[0] = T;
+            x.before[1] = T / tile + (T % tile != 0);
+        }
+        __syncthreads();
+        return;
+    }
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        x.first[e] = starts == nullptr ? 0 : starts[e];
-        x.count[e] = starts == nullptr ? T : starts[e + 1];  // the upper border, until the scan below
+        x.first[e] = starts[e];
+        x.count[e] = starts[e + 1];  // the upper border, until the scan below
     }
     __syncthreads();
     if (threadIdx.x < 32) {
