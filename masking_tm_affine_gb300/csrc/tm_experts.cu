@@ -30,8 +30,19 @@ const void *base_of(const void *p, int64_t elements, const void *out)
     return elements > 0 ? p : reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(15));
 }
 
-// Kernels.  Up to 128 rows an expert the weights' bytes bound the call.
-bool few_rows(const Product &p) { return p.T <= 128 * (int64_t)p.E; }
+// Which kernel.  Tiles of 128 by 32 or 128, of which a sum can be cut into several, up to 32 rows an
+// expert (where the weights' bytes bound the call) or while tiles of 256 by 256 would leave two
+// thirds of the SMs without work; in 8 bits such a tile of 128 rows is slower, and only taken for one of them.
+//   64 experts of 2048 x 2048, 16 bits: 32 rows each 105 us either way, 64 rows 119 us thin and 107 wide
+//   64 of 2048 x 4096, 8 bits: 32 rows 109 and 129 us, 64 rows 158 and 130
+//   one of 4096 x 4096, 16 bits: 128 rows 25 and 29 us, 256 rows 29 and 35, 512 rows 37 and 35;
+//   8 bits: 128 rows 21 and 25, 256 rows 37 and 25
+bool few_rows(const Product &p, const DevInfo &dev)
+{
+    if (p.T <= 32 * (int64_t)p.E) return true;
+    const int64_t busy = p.E < p.T ? p.E : p.T, rows = (p.T + 255) / 256, tiles = (rows > busy ? rows : busy) * ((p.F + 255) / 256);
+    return tiles * 6 <= dev.sms && (p.kind != kProductE4M3 || p.T <= 128 * (int64_t)p.E);
+}
 
 }  // namespace
 }  // namespace libtm
@@ -72,7 +83,7 @@ extern "C" tm_status tm_gemm_experts(const void *X, int64_t ldx, const void *W, 
     p.F = N;
     p.R = K;
     const bool pdl = (flags & TM_PDL) != 0;
-    return few_rows(p) ? thin_product(p, *dev, as_stream(stream), pdl) : wide_product(p, *dev, as_stream(stream), pdl);
+    return few_rows(p, *dev) ? thin_product(p, *dev, as_stream(stream), pdl) : wide_product(p, *dev, as_stream(stream), pdl);
 }
 
 extern "C" tm_status tm_gemm_experts_bwd(const void *DY, int64_t lddy, const void *X, int64_t ldx, const void *W, int64_t ldw,
@@ -121,7 +132,7 @@ extern "C" tm_status tm_gemm_experts_bwd(const void *DY, int64_t lddy, const voi
         p.T = T;
         p.F = K;
         p.R = N;
-        st = few_rows(p) ? thin_product(p, *dev, as_stream(stream), pdl) : wide_product(p, *dev, as_stream(stream), pdl);
+        st = few_rows(p, *dev) ? thin_product(p, *dev, as_stream(stream), pdl) : wide_product(p, *dev, as_stream(stream), pdl);
         if (st != TM_OK) return st;
     }
     if (weights)
@@ -171,5 +182,5 @@ extern "C" tm_status tm_gemm_e4m3(const void *A, int64_t lda, const float *sa, i
     p.sb = sb;
     p.group = group;
     const bool pdl = (flags & TM_PDL) != 0;
-    return few_rows(p) ? thin_product(p, *dev, as_stream(stream), pdl) : wide8_product(p, *dev, as_stream(stream), pdl);
+    return few_rows(p, *dev) ? thin_product(p, *dev, as_stream(stream), pdl) : wide8_product(p, *dev, as_stream(stream), pdl);
 }

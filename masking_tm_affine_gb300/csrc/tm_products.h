@@ -31,6 +31,10 @@ struct Product {
 // swizzle, zeros outside; with E > 0 of E matrices of `rows` rows.
 bool rows_map(CUtensorMap *m, ProductKind kind, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E, int box);
 
+// The same seen as panels of 64 columns (16-bit; `inner` a multiple of 64): boxes of two panels of
+// 64 rows, one behind the other in shared memory, in one copy.  Coordinates: 0, row, panel, matrix.
+bool panels_map(CUtensorMap *m, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E);
+
 // Few rows an expert: tiles of 128 features and up to 128 rows, split along the sum.
 tm_status thin_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl);
 

@@ -3,7 +3,7 @@
 // What bounds it is reading each busy expert's weights once.  So the weights are the
 // tall operand: a tile is 128 features by up to BT rows of x, the rows along N of the
 // tensor cores' product, where an extent is any multiple of 16 (a tile of 5 rows costs
-// 16, and copies 16).  TMA fills a ring of stages of 16 KB of weights.  A CTA has one tile and two or
+// 16).  TMA fills a ring of stages of 16 KB of weights.  A CTA has one tile and two or
 // three CTAs share an SM, so that one's start and end hide behind the others' copies and a free SM takes the next
 // tile: CTAs that stay, one an SM with all of its memory, read at 5.3 TB/s.
 // Few tiles are cut along the sum over a cluster of S CTAs: each
@@ -34,6 +34,19 @@ bool rows_map(CUtensorMap *m, ProductKind kind, const void *p, int64_t inner, in
     return encode(m, kind == kProductE4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, E > 0 ? 3 : 2,
                   const_cast<void *>(p), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool panels_map(CUtensorMap *m, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E)
+{
+    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(inner / 64), (cuuint64_t)(E > 0 ? E : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)(ld * 2), 128, (cuuint64_t)(ld * 2 * rows)};
+    const cuuint32_t boxes[4] = {64, 64, 2, 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    auto encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(p), dims, strides, boxes, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -128,7 +141,8 @@ __device__ __forceinline__ void find_tile(S &s, const ThinArgs &a, int tile, int
 
 template <bool F8, bool MN, int BT>
 __global__ void __launch_bounds__(kThreadsThin)
-    thin_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, const ThinArgs a, const int S)
+    thin_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mx_all,
+                const ThinArgs a, const int S)
 {
     constexpr uint32_t kStage = kTall + BT * 128;
     constexpr uint32_t kStagesT = (uint32_t)thin_stages(BT);
@@ -186,20 +200,25 @@ __global__ void __launch_bounds__(kThreadsThin)
 
     if (warp == 0) {
         if (lane == 0 && n > 0) {
-            const uint32_t boxes = (uint32_t)(n + 15) / 16;
+            // few copies a stage: rows in boxes of 32, or all 128 in one
+            const bool whole = BT > 32 && n > 96;
+            const uint32_t boxes = whole ? 4 : (uint32_t)(n + 31) / 32;
             Turn t;
             uint32_t used = 0;
             for (int k = k0; k < k1; ++k) {
                 if (used >= kStagesT && !role_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) break;
                 const uint32_t bar = smem_u32(&s.full[t.slot]), at = smem_u32(ring) + t.slot * kStage;
-                mbar_expect(&s.full[t.slot], kTall + boxes * 2048u);
+                mbar_expect(&s.full[t.slot], kTall + boxes * 4096u);
                 if constexpr (MN) {
                     tma_load_3d_hint(at, &mw, f0, k * kStep, e, bar, pol);
                     tma_load_3d_hint(at + kTall / 2, &mw, f0 + 64, k * kStep, e, bar, pol);
                 } else {
                     tma_load_3d_hint(at, &mw, k * kStep, f0, e, bar, pol);
                 }
-                for (uint32_t b = 0; b < boxes; ++b) tma_load_2d(at + kTall + b * 2048u, &mx, k * kStep, row0 + 16 * (int)b, bar);
+                if (whole)
+                    tma_load_2d(at + kTall, &mx_all, k * kStep, row0, bar);
+                else
+                    for (uint32_t b = 0; b < boxes; ++b) tma_load_2d(at + kTall + b * 4096u, &mx, k * kStep, row0 + 32 * (int)b, bar);
                 ++used;
                 t.next(kStagesT);
             }
@@ -402,11 +421,11 @@ tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool
     // 21.5 us, 2 18.6, 4 15.0, 8 14.8; 128 rows: 35.8, 35.6, 25.0, 47.6
     int S = 1;
     while (S < 4 && tiles * S <= (int64_t)dev.sms && a.steps >= 4 * S) S *= 2;
-    CUtensorMap mw, mx;
+    CUtensorMap mw, mx, mx_all;
     if (!rows_map(&mw, p.kind, p.w, MN ? p.F : p.R, MN ? p.R : p.F, p.ldw, p.E, MN ? 64 : 128) ||
-        !rows_map(&mx, p.kind, p.x, p.R, p.T, p.ldx, 0, 16))
+        !rows_map(&mx, p.kind, p.x, p.R, p.T, p.ldx, 0, 32) || !rows_map(&mx_all, p.kind, p.x, p.R, p.T, p.ldx, 0, BT))
         return TM_ERR_CUDA;
-    void *args[] = {&mw, &mx, &a, &S};
+    void *args[] = {&mw, &mx, &mx_all, &a, &S};
     return launch_kernel(k, dim3((unsigned)(most * S)), dim3(kThreadsThin), args, kRing, s, pdl, (unsigned)S);
 }
 

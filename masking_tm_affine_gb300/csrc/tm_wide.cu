@@ -1,7 +1,7 @@
 // tm_wide.cu -- 16-bit products grouped by expert, for experts with many rows: the output,
 // the gradient of the rows and the gradient of the weights.
 //
-//   forward       y[t, n]    = sum_k x[t, k]  w_e[n, k]
+//   forward           y[t, n]    = sum_k x[t, k]  w_e[n, k]
 //   rows' gradient    dx[t, k]   = sum_n dy[t, n] w_e[n, k]
 //   weights' gradient dw_e[n, k] = sum_t dy[t, n] x[t, k]     over the rows t of expert e
 //
@@ -13,7 +13,9 @@
 // that a warp's 32 lanes hold 32 neighbours of an output row: outputs leave as coalesced
 // stores of 64 or 128 bytes with no way through shared memory, whatever their
 // alignment, and a row past an expert's end is one that is not stored.  Nothing is
-// transposed first: an operand whose summed extent is the outer one is read MN-major.
+// transposed first: an operand whose summed extent is the outer one is read MN-major.  A stage
+// comes in as few copies as there can be, one of 16 KB an operand where the extents allow it:
+// with four of 4 KB the copies bound the kernel (8192 x 4096 x 4096: 182 us, with one 156).
 //
 // The rows of an expert end anywhere.  Along c that costs nothing (the product's extent is
 // a multiple of 64 of rows, the others are not stored).  Where rows are summed (the
@@ -46,6 +48,7 @@ struct WideArgs {
     int R, C;    // extents of r, and of c where c is not an expert's rows
     int rtiles, ctiles;  // of 256 (ctiles: weights' gradient)
     int steps;   // stages a tile (not of the weights' gradient)
+    int tall_panels, wide_panels;  // MN-major operands whose two panels come in one copy
     uint32_t id;
 };
 
@@ -107,7 +110,8 @@ struct Walk {
 
 template <int MODE, typename O>
 __global__ void __launch_bounds__(kThreadsWide, 1)
-    wide_kernel(const __grid_constant__ CUtensorMap mtall, const __grid_constant__ CUtensorMap mwide, const WideArgs a)
+    wide_kernel(const __grid_constant__ CUtensorMap mtall, const __grid_constant__ CUtensorMap mwide,
+                const __grid_constant__ CUtensorMap mwide_all, const WideArgs a)
 {
     constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeights;
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -166,10 +170,14 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                         if constexpr (MODE == kWeights) {
                             const uint32_t bar = smem_u32(&s.tail[t.slot]);
                             mbar_expect(&s.tail[t.slot], bytes);
-                            for (int p = 0; p < 2; ++p) {
-                                tma_load_2d(at + p * kPanel, &mtall, r + 64 * p, k0, bar);
-                                tma_load_2d(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
-                            }
+                            if (a.tall_panels)
+                                tma_load_4d(at, &mtall, 0, k0, r / 64, 0, bar);
+                            else
+                                for (int p = 0; p < 2; ++p) tma_load_2d(at + p * kPanel, &mtall, r + 64 * p, k0, bar);
+                            if (a.wide_panels)
+                                tma_load_4d(at + kHalf, &mwide, 0, k0, c / 64, 0, bar);
+                            else
+                                for (int p = 0; p < 2; ++p) tma_load_2d(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
                             tails |= 1u << t.slot;
                             tail_parity ^= 1u << t.slot;
                         }
@@ -177,18 +185,28 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                         const uint32_t bar = cluster_addr(smem_u32(&s.full[t.slot]), 0);
                         mbar_expect_cluster(bar, bytes);
                         if constexpr (MODE == kWeights) {
-                            for (int p = 0; p < 2; ++p) {
-                                tma_load_2d_pair(at + p * kPanel, &mtall, r + 64 * p, k0, bar);
-                                tma_load_2d_pair(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
-                            }
+                            if (a.tall_panels)
+                                tma_load_4d_pair(at, &mtall, 0, k0, r / 64, 0, bar);
+                            else
+                                for (int p = 0; p < 2; ++p) tma_load_2d_pair(at + p * kPanel, &mtall, r + 64 * p, k0, bar);
+                            if (a.wide_panels)
+                                tma_load_4d_pair(at + kHalf, &mwide, 0, k0, c / 64, 0, bar);
+                            else
+                                for (int p = 0; p < 2; ++p) tma_load_2d_pair(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
                         } else {
                             if constexpr (A_MN) {
-                                for (int p = 0; p < 2; ++p) tma_load_3d_pair(at + p * kPanel, &mtall, r + 64 * p, k0, w.e, bar);
+                                if (a.tall_panels)
+                                    tma_load_4d_pair(at, &mtall, 0, k0, r / 64, w.e, bar);
+                                else
+                                    for (int p = 0; p < 2; ++p) tma_load_3d_pair(at + p * kPanel, &mtall, r + 64 * p, k0, w.e, bar);
                             } else {
                                 tma_load_3d_pair(at, &mtall, k0, r, w.e, bar);
                             }
-                            for (int b = 0; b < half; b += 32)
-                                tma_load_2d_pair(at + kHalf + (uint32_t)b * 128u, &mwide, k0, c + b, bar);
+                            if (half == 128)
+                                tma_load_2d_pair(at + kHalf, &mwide_all, k0, c, bar);
+                            else
+                                for (int b = 0; b < half; b += 32)
+                                    tma_load_2d_pair(at + kHalf + (uint32_t)b * 128u, &mwide, k0, c + b, bar);
                         }
                         tails &= ~(1u << t.slot);
                     }
@@ -326,7 +344,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
 constexpr size_t kWideSmem = kStages * kStageBytes + 1024;
 
 template <int MODE, typename O>
-tm_status launch_wide(const CUtensorMap &tall, const CUtensorMap &wide, const WideArgs &a, int64_t items, const DevInfo &dev,
+tm_status launch_wide(const CUtensorMap &tall, const CUtensorMap &wide, const CUtensorMap &all, const WideArgs &a, int64_t items, const DevInfo &dev,
                       cudaStream_t s, bool pdl)
 {
     const void *k = (const void *)wide_kernel<MODE, O>;
@@ -340,18 +358,19 @@ tm_status launch_wide(const CUtensorMap &tall, const CUtensorMap &wide, const Wi
     });
     if (!good[d]) return TM_ERR_CUDA;
     const int64_t pairs = dev.sms / 2, units = items < pairs ? items : pairs;
-    void *args[] = {const_cast<CUtensorMap *>(&tall), const_cast<CUtensorMap *>(&wide), const_cast<WideArgs *>(&a)};
+    void *args[] = {const_cast<CUtensorMap *>(&tall), const_cast<CUtensorMap *>(&wide), const_cast<CUtensorMap *>(&all),
+                    const_cast<WideArgs *>(&a)};
     return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(kThreadsWide), args, kWideSmem, s, pdl, 2);
 }
 
 template <int MODE>
-tm_status launch_typed(const CUtensorMap &tall, const CUtensorMap &wide, const WideArgs &a, int64_t items, const DevInfo &dev,
+tm_status launch_typed(const CUtensorMap &tall, const CUtensorMap &wide, const CUtensorMap &all, const WideArgs &a, int64_t items, const DevInfo &dev,
                        cudaStream_t s, bool pdl)
 {
     if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
-    if (a.otype == TM_F32) return launch_wide<MODE, float>(tall, wide, a, items, dev, s, pdl);
-    if (a.otype == TM_F16) return launch_wide<MODE, __half>(tall, wide, a, items, dev, s, pdl);
-    return launch_wide<MODE, __nv_bfloat16>(tall, wide, a, items, dev, s, pdl);
+    if (a.otype == TM_F32) return launch_wide<MODE, float>(tall, wide, all, a, items, dev, s, pdl);
+    if (a.otype == TM_F16) return launch_wide<MODE, __half>(tall, wide, all, a, items, dev, s, pdl);
+    return launch_wide<MODE, __nv_bfloat16>(tall, wide, all, a, items, dev, s, pdl);
 }
 
 int tiles256(int64_t n) { return (int)((n + 255) / 256); }
@@ -372,13 +391,15 @@ tm_status wide_product(const Product &p, const DevInfo &dev, cudaStream_t s, boo
     a.rtiles = tiles256(p.F);
     a.steps = (int)((p.R + 63) / 64);
     a.id = instruction(p.kind == kProductBF16 ? 1u : 0u, p.w_mn, false, 256, 0);
-    CUtensorMap tall, wide;
-    if (!rows_map(&tall, p.kind, p.w, p.w_mn ? p.F : p.R, p.w_mn ? p.R : p.F, p.ldw, p.E, p.w_mn ? 64 : 128) ||
-        !rows_map(&wide, p.kind, p.x, p.R, p.T, p.ldx, 0, 32))
+    a.tall_panels = p.w_mn && p.F % 64 == 0 && p.R > 0;
+    CUtensorMap tall, wide, all;
+    if (a.tall_panels ? !panels_map(&tall, p.w, p.F, p.R, p.ldw, p.E)
+                      : !rows_map(&tall, p.kind, p.w, p.w_mn ? p.F : p.R, p.w_mn ? p.R : p.F, p.ldw, p.E, p.w_mn ? 64 : 128))
         return TM_ERR_CUDA;
+    if (!rows_map(&wide, p.kind, p.x, p.R, p.T, p.ldx, 0, 32) || !rows_map(&all, p.kind, p.x, p.R, p.T, p.ldx, 0, 128)) return TM_ERR_CUDA;
     const int64_t busy = p.E < p.T ? p.E : p.T, items = ((p.T + 255) / 256 + busy) * a.rtiles;
-    return p.w_mn ? launch_typed<kRows>(tall, wide, a, items, dev, s, pdl)
-                  : launch_typed<kForward>(tall, wide, a, items, dev, s, pdl);
+    return p.w_mn ? launch_typed<kRows>(tall, wide, all, a, items, dev, s, pdl)
+                  : launch_typed<kForward>(tall, wide, all, a, items, dev, s, pdl);
 }
 
 tm_status wide_weights(ProductKind kind, const void *dy, int64_t lddy, const void *x, int64_t ldx, void *dw, int64_t lddw,
@@ -398,9 +419,12 @@ tm_status wide_weights(ProductKind kind, const void *dy, int64_t lddy, const voi
     a.rtiles = tiles256(K);
     a.ctiles = tiles256(N);
     a.id = instruction(kind == kProductBF16 ? 1u : 0u, true, true, 256, 0);
+    a.tall_panels = K % 64 == 0 && T > 0;
+    a.wide_panels = N % 64 == 0 && T > 0;
     CUtensorMap tall, wide;
-    if (!rows_map(&tall, kind, x, K, T, ldx, 0, 64) || !rows_map(&wide, kind, dy, N, T, lddy, 0, 64)) return TM_ERR_CUDA;
-    return launch_typed<kWeights>(tall, wide, a, (int64_t)E * a.rtiles * a.ctiles, dev, s, pdl);
+    if (a.tall_panels ? !panels_map(&tall, x, K, T, ldx, 0) : !rows_map(&tall, kind, x, K, T, ldx, 0, 64)) return TM_ERR_CUDA;
+    if (a.wide_panels ? !panels_map(&wide, dy, N, T, lddy, 0) : !rows_map(&wide, kind, dy, N, T, lddy, 0, 64)) return TM_ERR_CUDA;
+    return launch_typed<kWeights>(tall, wide, wide, a, (int64_t)E * a.rtiles * a.ctiles, dev, s, pdl);
 }
 
 }  // namespace libtm
