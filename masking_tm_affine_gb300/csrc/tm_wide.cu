@@ -30,7 +30,7 @@
 namespace libtm {
 namespace {
 
-constexpr int kThreadsWide = 224;  // warp 0 copies, 1 products, 2-5 outputs, 6 clears rows
+constexpr int kThreadsWide = 352;  // warp 0 copies, 1 products, 2-9 outputs, 10 clears rows
 constexpr int kStages = 6;
 constexpr uint32_t kHalf = 128 * 128;       // bytes of one operand a stage and CTA: 128 of its outer extent by 64 of the sum
 constexpr uint32_t kPanel = 64 * 128;       // MN-major: 64 of the outer extent by 64 of the sum
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.acc_full[i], 1);
-            mbar_init(&s.acc_empty[i], 8);
+            mbar_init(&s.acc_empty[i], 16);
         }
         mbar_init(&s.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -262,8 +262,9 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
             umma_done<true>(&s.done);
             mbar_wait_bounded(smem_u32(&s.done), 0);
         }
-    } else if (warp < 6) {
-        const int q = warp & 3;
+    } else if (warp < 10) {
+        // two warps a 32 lanes: one takes the even runs of 32 columns, the other the odd
+        const int q = warp & 3, odd = (warp - 2) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t free0 = cluster_addr(smem_u32(&s.acc_empty[0]), 0), free1 = cluster_addr(smem_u32(&s.acc_empty[1]), 0);
         O *out = reinterpret_cast<O *>(a.out);
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
         for (int item = unit; item < items; item += units) {
             const Tile w = walk.at(item);
             const int r = w.r0 + (int)rank * 128 + q * 32 + lane;
-            O *p = out + ((MODE == kWeights ? (int64_t)w.e * a.C : 0) + w.c0) * a.ldo + r;
+            O *const first = out + ((MODE == kWeights ? (int64_t)w.e * a.C : 0) + w.c0) * a.ldo + r;
             if (w.steps > 0) {
                 if (!__all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status))) break;
                 acc_fence_after();
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                 waited = true;
             }
 #pragma unroll 1
-            for (int c0 = 0; c0 < w.n; c0 += 32) {
+            for (int c0 = 32 * odd; c0 < w.n; c0 += 64) {
                 float v[32];
                 if (w.steps > 0) {
                     acc_load32(lanes + acc.slot * 256 + c0, v);
@@ -291,10 +292,21 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
 #pragma unroll
                     for (int c = 0; c < 32; ++c) v[c] = 0.0f;
                 }
+                O *p = first + c0 * a.ldo;
+                if (c0 + 32 <= w.n) {
+                    if (r < a.R) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    if (c0 + c < w.n && r < a.R) *p = from_f<O>(v[c]);
-                    p += a.ldo;
+                        for (int c = 0; c < 32; ++c) {
+                            *p = from_f<O>(v[c]);
+                            p += a.ldo;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (c0 + c < w.n && r < a.R) *p = from_f<O>(v[c]);
+                        p += a.ldo;
+                    }
                 }
             }
             if (w.steps > 0) {
