@@ -11,9 +11,11 @@
 // which adds them in rank order and stores: one launch, no workspace, the same bits
 // every time.
 //
-// Sums.  16-bit operands: the accumulator stays in tensor memory, fp32.  e4m3: one
-// accumulator for each 128 of the sum, read out, multiplied by both scales and added in
-// fp32 registers while the next ones are made.
+// Sums.  16-bit operands to 16-bit outputs: the accumulator stays in tensor memory, fp32.  To
+// fp32 outputs: the tensor cores' additions lose up to 2^-23 of the sum each, always towards zero, so a
+// sum leaves them after kRunSums of it and is added in registers, rounded to nearest (over 8192 rows of a
+// weights' gradient: 2.5e-6 of the result without, 2e-7 with).  e4m3: one accumulator for each 128 of the
+// sum, read out, multiplied by both scales and added in fp32 registers while the next ones are made.
 #include <mutex>
 
 #include "tm_products.h"
@@ -52,8 +54,7 @@ bool panels_map(CUtensorMap *m, const void *p, int64_t inner, int64_t rows, int6
 
 namespace {
 
-constexpr int kThreadsThin = 192;  // warp 0 copies, warp 1 products, warps 2-5 outputs
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 6;
 constexpr uint32_t kTall = 128 * 128;  // bytes of weights a stage
 
 struct ThinArgs {
@@ -68,19 +69,29 @@ struct ThinArgs {
     uint32_t id;  // the instruction without its N
 };
 
-// Accumulators: one of a tile (16 bits); e4m3 takes a new one every block.
-template <bool F8, int BT>
-__host__ __device__ constexpr int thin_accs() { return !F8 ? 1 : BT <= 32 ? 4 : 2; }
-// Three CTAs an SM with tiles of 32 rows, two with 128: stages of 20 and 32 KB.
-__host__ __device__ constexpr int thin_stages(int) { return 3; }
+// The forms.  F8: e4m3; SUMS: sums leave the tensor cores in runs (always with F8).
+template <bool F8, bool SUMS, int BT>
+struct Thin {
+    static constexpr int kOutWarps = BT <= 32 ? 4 : 8;  // behind warp 0, which copies, and warp 1, which multiplies
+    static constexpr int kThreads = 64 + 32 * kOutWarps;
+    static constexpr int kCols = BT * 4 / kOutWarps;    // columns of an output warp
+    // Three CTAs an SM with tiles of 32 rows, two with 128, stages of 20 and 32 KB; one where 64 sums a
+    // thread take its registers.
+    static constexpr int kCtas = BT <= 32 ? 3 : SUMS ? 1 : 2;
+    static constexpr int kStages = kCtas == 1 ? 6 : 3;
+    static constexpr int kRun = F8 ? 1 : kRunSums / 64;  // stages a run
+    // accumulators: one of a tile, or several that take turns over its runs
+    static constexpr int kAccs = !SUMS ? 1 : BT <= 32 ? 4 : 2;
+};
 
-template <bool F8, int BT>
+template <bool F8, bool SUMS, int BT>
 struct ThinSmem {
+    using F = Thin<F8, SUMS, BT>;
     alignas(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[4], acc_empty[4], inbox, done;
     uint32_t tmem;
     int abort;
     int e, row, n;  // the tile: expert, first row, how many (0: none)
-    alignas(16) float scale[4][2][F8 ? BT : 4];  // each output warp's own
+    alignas(16) float scale[F::kOutWarps][2][F8 ? F::kCols : 4];  // each output warp's own
     int starts[kMaxExperts + 1];
 };
 
@@ -139,15 +150,16 @@ __device__ __forceinline__ void find_tile(S &s, const ThinArgs &a, int tile, int
     __syncwarp();
 }
 
-template <bool F8, bool MN, int BT>
-__global__ void __launch_bounds__(kThreadsThin)
+template <bool F8, bool SUMS, bool MN, int BT>
+__global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
     thin_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mx_all,
                 const ThinArgs a, const int S)
 {
     constexpr uint32_t kStage = kTall + BT * 128;
-    constexpr uint32_t kStagesT = (uint32_t)thin_stages(BT);
+    using F = Thin<F8, SUMS, BT>;
+    constexpr uint32_t kStagesT = (uint32_t)F::kStages;
     constexpr int kStep = F8 ? 128 : 64;  // elements of the sum a stage
-    constexpr int kAccs = thin_accs<F8, BT>();
+    constexpr int kAccs = F::kAccs, kRun = F::kRun, CW = F::kCols;
     // weights are read once, or by a few tiles at about the same time: they are the first L2 gives up, not
     // lines still to be written back (32 experts of 2048 x 4096 in 16 bits, 64 rows: 63.5 us without, 55.6 with)
     const uint64_t pol = l2_evict_first_policy();
@@ -157,7 +169,7 @@ __global__ void __launch_bounds__(kThreadsThin)
     // the ring's place once every CTA of the cluster is done with its own
     float *inbox = reinterpret_cast<float *>(ring);
     static_assert(BT * 128 * 4 <= kStagesT * kStage, "inbox");
-    __shared__ ThinSmem<F8, BT> s;
+    __shared__ ThinSmem<F8, SUMS, BT> s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_rank() : 0;
     const int item = (int)blockIdx.x / S;
@@ -175,7 +187,7 @@ __global__ void __launch_bounds__(kThreadsThin)
         }
         for (int i = 0; i < kAccs; ++i) {
             mbar_init(&s.acc_full[i], 1);
-            mbar_init(&s.acc_empty[i], 4);
+            mbar_init(&s.acc_empty[i], F::kOutWarps);
         }
         mbar_init(&s.done, 1);
         mbar_init(&s.inbox, 1);
@@ -183,7 +195,7 @@ __global__ void __launch_bounds__(kThreadsThin)
         s.abort = 0;
     }
     if (a.starts != nullptr) {
-        for (int e = threadIdx.x; e <= a.E; e += kThreadsThin) s.starts[e] = a.starts[e];
+        for (int e = threadIdx.x; e <= a.E; e += F::kThreads) s.starts[e] = a.starts[e];
         __syncthreads();
     }
     if (warp == 0) find_tile(s, a, tile, BT);
@@ -193,32 +205,36 @@ __global__ void __launch_bounds__(kThreadsThin)
     acc_fence_after();
     const int e = s.e, row0 = s.row, n = s.n;
     const uint32_t tmem = s.tmem;
-    const int q = warp & 3, f = f0 + q * 32 + lane;
+    // an output warp: 32 features, CW columns from cb on
+    const int q = warp & 3, f = f0 + q * 32 + lane, part = (warp - 2) >> 2, cb = part * CW;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     bool ok = true;
-    float sum[F8 ? BT : 1];  // e4m3: of the output warps
+    float sum[SUMS ? CW : 1];
 
     if (warp == 0) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             // few copies a stage: rows in boxes of 32, or all 128 in one
             const bool whole = BT > 32 && n > 96;
             const uint32_t boxes = whole ? 4 : (uint32_t)(n + 31) / 32;
             Turn t;
             uint32_t used = 0;
             for (int k = k0; k < k1; ++k) {
-                if (used >= kStagesT && !role_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) break;
+                if (used >= kStagesT && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) break;
                 const uint32_t bar = smem_u32(&s.full[t.slot]), at = smem_u32(ring) + t.slot * kStage;
-                mbar_expect(&s.full[t.slot], kTall + boxes * 4096u);
-                if constexpr (MN) {
-                    tma_load_3d_hint(at, &mw, f0, k * kStep, e, bar, pol);
-                    tma_load_3d_hint(at + kTall / 2, &mw, f0 + 64, k * kStep, e, bar, pol);
-                } else {
-                    tma_load_3d_hint(at, &mw, k * kStep, f0, e, bar, pol);
+                if (elect()) {
+                    mbar_expect(&s.full[t.slot], kTall + boxes * 4096u);
+                    if constexpr (MN) {
+                        tma_load_3d_hint(at, &mw, f0, k * kStep, e, bar, pol);
+                        tma_load_3d_hint(at + kTall / 2, &mw, f0 + 64, k * kStep, e, bar, pol);
+                    } else {
+                        tma_load_3d_hint(at, &mw, k * kStep, f0, e, bar, pol);
+                    }
+                    if (whole)
+                        tma_load_2d(at + kTall, &mx_all, k * kStep, row0, bar);
+                    else
+                        for (uint32_t b = 0; b < boxes; ++b) tma_load_2d(at + kTall + b * 4096u, &mx, k * kStep, row0 + 32 * (int)b, bar);
                 }
-                if (whole)
-                    tma_load_2d(at + kTall, &mx_all, k * kStep, row0, bar);
-                else
-                    for (uint32_t b = 0; b < boxes; ++b) tma_load_2d(at + kTall + b * 4096u, &mx, k * kStep, row0 + 32 * (int)b, bar);
+                __syncwarp();
                 ++used;
                 t.next(kStagesT);
             }
@@ -227,71 +243,90 @@ __global__ void __launch_bounds__(kThreadsThin)
                 mbar_wait_bounded(smem_u32(&s.full[i]), ((used - i + kStagesT - 1) / kStagesT - 1) & 1u);
         }
     } else if (warp == 1) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             const uint32_t id = a.id | ((uint32_t)((n + 15) / 16 * 2) << 17);
             Turn t, acc;
+            int in_run = 0;
+            uint32_t runs = 0;
             for (int k = k0; k < k1; ++k) {
-                if (F8 && k - k0 >= kAccs && !role_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status)) break;
-                if (!role_wait(&s.full[t.slot], t.phase, &s.abort, a.status)) break;
+                if (SUMS && in_run == 0 && runs >= (uint32_t)kAccs &&
+                    !warp_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status))
+                    break;
+                if (!warp_wait(&s.full[t.slot], t.phase, &s.abort, a.status)) break;
                 acc_fence_after();
                 const uint32_t at = smem_u32(ring) + t.slot * kStage, d = tmem + acc.slot * BT;
+                ++in_run;
+                const bool end = (SUMS && in_run == kRun) || k + 1 == k1;
+                if (elect()) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    umma<F8, false>(d, MN ? operand_mn(at + j * 2048, kTall / 2) : operand_k(at + j * 32),
-                                    operand_k(at + kTall + j * 32), id, j != 0 || (!F8 && k != k0));
-                umma_done<false>(&s.empty[t.slot]);
+                    for (int j = 0; j < 4; ++j)
+                        umma<F8, false>(d, MN ? operand_mn(at + j * 2048, kTall / 2) : operand_k(at + j * 32),
+                                        operand_k(at + kTall + j * 32), id, j != 0 || in_run != 1);
+                    umma_done<false>(&s.empty[t.slot]);
+                    if (end) umma_done<false>(&s.acc_full[acc.slot]);
+                }
+                __syncwarp();
                 t.next(kStagesT);
-                if (F8 || k + 1 == k1) {
-                    umma_done<false>(&s.acc_full[acc.slot]);
+                if (end) {
                     acc.next(kAccs);
+                    in_run = 0;
+                    ++runs;
                 }
             }
             // every product issued has completed before the tensor memory is given back
-            umma_done<false>(&s.done);
+            if (elect()) umma_done<false>(&s.done);
+            __syncwarp();
             mbar_wait_bounded(smem_u32(&s.done), 0);
         }
     } else if (n > 0) {
-        if constexpr (F8) {
-            const int G = a.steps;  // scales of a row
+        if constexpr (SUMS) {
 #pragma unroll
-            for (int c = 0; c < BT; ++c) sum[c] = 0.0f;
-            const float *sb = a.sb + ((int64_t)e * a.ftiles + f0 / 128) * G;
-            // this warp's copy of the rows' factors; the next block's are on their way meanwhile
-            float fa[BT / 32], fb = 0.0f;
+            for (int c = 0; c < CW; ++c) sum[c] = 0.0f;
+            // e4m3: this warp's copy of the rows' factors; the next block's are on their way meanwhile
+            const int G = a.steps;  // scales of a row
+            const float *sb = F8 ? a.sb + ((int64_t)e * a.ftiles + f0 / 128) * G : nullptr;
+            float fa[CW / 32], fb = 0.0f;
             auto fetch = [&](int k) {
-                if (k >= k1) return;
+                if (!F8 || k >= k1) return;
                 fb = __ldg(sb + k);
 #pragma unroll
-                for (int i = 0; i < BT / 32; ++i) {
-                    const int t = i * 32 + lane;
+                for (int i = 0; i < CW / 32; ++i) {
+                    const int t = cb + i * 32 + lane;
                     const int64_t row = row0 + (t < n ? t : 0);
                     fa[i] = __ldg(a.sa + (a.group ? row * G + k : row));
                 }
             };
             Turn acc;
             fetch(k0);
-            for (int k = k0; k < k1; ++k) {
-                float *factor = s.scale[q][k & 1];
+            for (int k = k0; k < k1; k += kRun) {
+                float *factor = s.scale[warp - 2][k & 1];
+                if constexpr (F8) {
 #pragma unroll
-                for (int i = 0; i < BT / 32; ++i) factor[i * 32 + lane] = fa[i] * fb;
-                fetch(k + 1);
-                __syncwarp();
+                    for (int i = 0; i < CW / 32; ++i) factor[i * 32 + lane] = fa[i] * fb;
+                    fetch(k + 1);
+                    __syncwarp();
+                }
                 ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status));
                 if (!ok) break;
                 acc_fence_after();
 #pragma unroll
-                for (int c0 = 0; c0 < BT; c0 += 32) {
-                    if (c0 < n) {
+                for (int c0 = 0; c0 < CW; c0 += 32) {
+                    if (cb + c0 < n) {
                         float v[32];
-                        acc_load32(lanes + acc.slot * BT + c0, v);
+                        acc_load32(lanes + acc.slot * BT + cb + c0, v);
                         acc_load_wait(v);
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
-                            const float4 m = *reinterpret_cast<const float4 *>(factor + c0 + c);
-                            sum[c0 + c] = __fmaf_rn(v[c], m.x, sum[c0 + c]);
-                            sum[c0 + c + 1] = __fmaf_rn(v[c + 1], m.y, sum[c0 + c + 1]);
-                            sum[c0 + c + 2] = __fmaf_rn(v[c + 2], m.z, sum[c0 + c + 2]);
-                            sum[c0 + c + 3] = __fmaf_rn(v[c + 3], m.w, sum[c0 + c + 3]);
+                            if constexpr (F8) {
+                                const float4 m = *reinterpret_cast<const float4 *>(factor + c0 + c);
+                                sum[c0 + c] = __fmaf_rn(v[c], m.x, sum[c0 + c]);
+                                sum[c0 + c + 1] = __fmaf_rn(v[c + 1], m.y, sum[c0 + c + 1]);
+                                sum[c0 + c + 2] = __fmaf_rn(v[c + 2], m.z, sum[c0 + c + 2]);
+                                sum[c0 + c + 3] = __fmaf_rn(v[c + 3], m.w, sum[c0 + c + 3]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) sum[c0 + c + i] += v[c + i];
+                            }
                         }
                     }
                 }
@@ -318,12 +353,13 @@ __global__ void __launch_bounds__(kThreadsThin)
         pdl_wait();
         if (ok) {
 #pragma unroll
-            for (int c0 = 0; c0 < BT; c0 += 32) {
+            for (int i0 = 0; i0 < CW; i0 += 32) {
+                const int c0 = cb + i0;
                 if (c0 >= n) break;
                 float v[32];
-                if constexpr (F8) {
+                if constexpr (SUMS) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = sum[c0 + c];
+                    for (int c = 0; c < 32; ++c) v[c] = sum[i0 + c];
                 } else if (k0 < k1) {
                     acc_load32(lanes + c0, v);
                     acc_load_wait(v);
@@ -357,7 +393,7 @@ __global__ void __launch_bounds__(kThreadsThin)
                 }
             }
             if (S > 1 && __all_sync(0xffffffffu, role_wait<true>(&s.inbox, 0, &s.abort, a.status)))
-                for (int c = 0; c < own; c += 4) {
+                for (int c = 4 * part; c < own; c += F::kOutWarps) {
                     float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
                     for (int r = 0; r < S; ++r) {
                         const float4 u = *reinterpret_cast<const float4 *>(inbox + (((r * 4 + q) * (BT / S / 4) + c / 4) * 32 + lane) * 4);
@@ -382,13 +418,14 @@ __global__ void __launch_bounds__(kThreadsThin)
     }
 }
 
-template <bool F8, bool MN, int BT>
+template <bool F8, bool SUMS, bool MN, int BT>
 tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
 {
-    constexpr int kCtas = BT <= 32 ? 3 : 2;  // an SM
-    constexpr size_t kRing = thin_stages(BT) * (kTall + BT * 128) + 1024;
-    static_assert(kCtas * (kRing + sizeof(ThinSmem<F8, BT>) + 1024) <= 228 * 1024, "shared memory");
-    const void *k = (const void *)thin_kernel<F8, MN, BT>;
+    using F = Thin<F8, SUMS, BT>;
+    constexpr size_t kRing = F::kStages * (kTall + BT * 128) + 1024;
+    static_assert(F::kCtas * (kRing + sizeof(ThinSmem<F8, SUMS, BT>) + 1024) <= 228 * 1024, "shared memory");
+    static_assert(F::kCtas * F::kAccs * BT <= 512, "tensor memory");
+    const void *k = (const void *)thin_kernel<F8, SUMS, MN, BT>;
     static std::once_flag once[kMaxDevices];
     static bool good[kMaxDevices];
     int d = 0;
@@ -426,7 +463,7 @@ tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool
         !rows_map(&mx, p.kind, p.x, p.R, p.T, p.ldx, 0, 32) || !rows_map(&mx_all, p.kind, p.x, p.R, p.T, p.ldx, 0, BT))
         return TM_ERR_CUDA;
     void *args[] = {&mw, &mx, &mx_all, &a, &S};
-    return launch_kernel(k, dim3((unsigned)(most * S)), dim3(kThreadsThin), args, kRing, s, pdl, (unsigned)S);
+    return launch_kernel(k, dim3((unsigned)(most * S)), dim3(F::kThreads), args, kRing, s, pdl, (unsigned)S);
 }
 
 }  // namespace
@@ -435,9 +472,12 @@ tm_status thin_product(const Product &p, const DevInfo &dev, cudaStream_t s, boo
 {
     const bool few = p.T <= 32 * (int64_t)p.E;
     if (p.kind == kProductE4M3)
-        return few ? launch_thin<true, false, 32>(p, dev, s, pdl) : launch_thin<true, false, 128>(p, dev, s, pdl);
-    if (p.w_mn) return few ? launch_thin<false, true, 32>(p, dev, s, pdl) : launch_thin<false, true, 128>(p, dev, s, pdl);
-    return few ? launch_thin<false, false, 32>(p, dev, s, pdl) : launch_thin<false, false, 128>(p, dev, s, pdl);
+        return few ? launch_thin<true, true, false, 32>(p, dev, s, pdl) : launch_thin<true, true, false, 128>(p, dev, s, pdl);
+    if (p.w_mn)  // always to 16 bits
+        return few ? launch_thin<false, false, true, 32>(p, dev, s, pdl) : launch_thin<false, false, true, 128>(p, dev, s, pdl);
+    if (p.otype == TM_F32)
+        return few ? launch_thin<false, true, false, 32>(p, dev, s, pdl) : launch_thin<false, true, false, 128>(p, dev, s, pdl);
+    return few ? launch_thin<false, false, false, 32>(p, dev, s, pdl) : launch_thin<false, false, false, 128>(p, dev, s, pdl);
 }
 
 }  // namespace libtm

@@ -75,6 +75,23 @@ __device__ __forceinline__ bool role_wait(uint64_t *b, uint32_t parity, int *abo
     return true;
 }
 
+// The same by a whole warp, which goes on or gives up together.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, int *abort_flag, unsigned *status)
+{
+    return __all_sync(0xffffffffu, role_wait<CLUSTER>(b, parity, abort_flag, status)) != 0;
+}
+
+// One lane of a converged warp, the same every time.  Warps that copy or multiply stay together and elect:
+// the instructions' operands then live in uniform registers (by a lane in a branch of its own each
+// stage cost the 16-bit products a tenth of their time).
+__device__ __forceinline__ bool elect()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e)::"memory");
+    return e != 0;
+}
+
 // Place in a ring of barriers: the slot, and the parity of the phase to wait for.
 struct Turn {
     uint32_t slot = 0, phase = 0;
@@ -246,6 +263,38 @@ __device__ __forceinline__ void acc_load_wait(float (&r)[32])
 }
 __device__ __forceinline__ void acc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void acc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Pairs of fp32 values in one register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+
+// sum += m * 32 columns of the accumulator, two columns an operation.  One statement: the
+// values pass from the read to the additions in registers that nothing else names, which
+// saves the moves that separate statements took (8192 x 8192 x 4096: 255 us, so 234).
+__device__ __forceinline__ void add_columns(uint32_t at, uint64_t *s, uint64_t m)
+{
+#define TM_ADD(I, A, B) "mov.b64 p, {t" #A ", t" #B "};\n\tfma.rn.f32x2 %" #I ", p, %17, %" #I ";\n\t"
+    asm volatile(
+        "{\n\t.reg .b32 t<32>;\n\t.reg .b64 p;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, t16, "
+        "t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t" TM_ADD(0, 0, 1) TM_ADD(1, 2, 3) TM_ADD(2, 4, 5) TM_ADD(3, 6, 7) TM_ADD(4, 8, 9)
+            TM_ADD(5, 10, 11) TM_ADD(6, 12, 13) TM_ADD(7, 14, 15) TM_ADD(8, 16, 17) TM_ADD(9, 18, 19) TM_ADD(10, 20, 21)
+                TM_ADD(11, 22, 23) TM_ADD(12, 24, 25) TM_ADD(13, 26, 27) TM_ADD(14, 28, 29) TM_ADD(15, 30, 31) "}"
+        : "+l"(s[0]), "+l"(s[1]), "+l"(s[2]), "+l"(s[3]), "+l"(s[4]), "+l"(s[5]), "+l"(s[6]), "+l"(s[7]), "+l"(s[8]),
+          "+l"(s[9]), "+l"(s[10]), "+l"(s[11]), "+l"(s[12]), "+l"(s[13]), "+l"(s[14]), "+l"(s[15])
+        : "r"(at), "l"(m)
+        : "memory");
+#undef TM_ADD
+}
+
+// 16-bit operands to fp32 outputs: how much of a sum the tensor cores add before it leaves them.
+constexpr int kRunSums = 512;
 
 // ---------------------------------------------------------------- rows of the experts
 constexpr int kMaxExperts = 1024;

@@ -30,7 +30,16 @@
 namespace libtm {
 namespace {
 
-constexpr int kThreadsWide = 352;  // warp 0 copies, 1 products, 2-9 outputs, 10 clears rows
+// Warp 0 copies, 1 multiplies, 8 warps make outputs, one clears rows.  fp32 outputs: sums leave the tensor
+// cores every kRunSums and are added in registers (tm_thin.cu says why), 128 a thread of the output warps,
+// which so are whole warpgroups and take registers from the others: 4 warps of 96 and 8 of 200 are
+// 63488, of the 64512 that 384 threads of 168 start with.
+template <bool SUMS>
+struct Warps {
+    static constexpr int kOut = SUMS ? 4 : 2, kClear = SUMS ? 2 : 10, kThreads = SUMS ? 384 : 352;
+};
+constexpr int kFewRegs = 96, kManyRegs = 200;
+constexpr int kRun = kRunSums / 64;  // stages
 constexpr int kStages = 6;
 constexpr uint32_t kHalf = 128 * 128;       // bytes of one operand a stage and CTA: 128 of its outer extent by 64 of the sum
 constexpr uint32_t kPanel = 64 * 128;       // MN-major: 64 of the outer extent by 64 of the sum
@@ -109,11 +118,12 @@ struct Walk {
 };
 
 template <int MODE, typename O>
-__global__ void __launch_bounds__(kThreadsWide, 1)
+__global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap mtall, const __grid_constant__ CUtensorMap mwide,
                 const __grid_constant__ CUtensorMap mwide_all, const WideArgs a)
 {
-    constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeights;
+    constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeights, SUMS = sizeof(O) == 4;
+    using Ws = Warps<SUMS>;
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     __shared__ WideSmem s;
@@ -146,8 +156,13 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
     const int items = MODE == kWeights ? a.E * a.rtiles * a.ctiles : s.x.before[a.E] * a.rtiles;
     Walk<MODE> walk(a, s.x);
 
+    // in the branches themselves: behind one of its own the compiler counts on the smaller share everywhere
+    auto fewer_registers = [] {
+        if constexpr (SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    };
     if (warp == 0) {
-        if (lane == 0) {
+        fewer_registers();
+        {
             Turn t;
             uint32_t used = 0, tails = 0;  // tails: slots whose last filling was counted on `tail`
             uint32_t tail_parity = 0;
@@ -159,7 +174,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                 const int half = B_MN ? 128 : (w.n + 63) / 64 * 32, c = w.c0 + (int)rank * half;
                 const uint32_t bytes = kHalf + (B_MN ? kHalf : (uint32_t)half * 128u);
                 for (int k = 0; k < w.steps; ++k) {
-                    if (used >= kStages && !role_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
+                    if (used >= kStages && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
                         ok = false;
                         break;
                     }
@@ -167,6 +182,14 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                     const int k0 = w.s0 + k * 64;
                     const bool cut = MODE == kWeights && k == w.steps - 1 && w.last % 16 != 0;
                     if (cut) {
+                        tails |= 1u << t.slot;
+                        tail_parity ^= 1u << t.slot;
+                    } else {
+                        tails &= ~(1u << t.slot);
+                    }
+                    if (!elect()) {
+                        // the others wait below
+                    } else if (cut) {
                         if constexpr (MODE == kWeights) {
                             const uint32_t bar = smem_u32(&s.tail[t.slot]);
                             mbar_expect(&s.tail[t.slot], bytes);
@@ -178,8 +201,6 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                                 tma_load_4d(at + kHalf, &mwide, 0, k0, c / 64, 0, bar);
                             else
                                 for (int p = 0; p < 2; ++p) tma_load_2d(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
-                            tails |= 1u << t.slot;
-                            tail_parity ^= 1u << t.slot;
                         }
                     } else {
                         const uint32_t bar = cluster_addr(smem_u32(&s.full[t.slot]), 0);
@@ -208,8 +229,8 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                                 for (int b = 0; b < half; b += 32)
                                     tma_load_2d_pair(at + kHalf + (uint32_t)b * 128u, &mwide, k0, c + b, bar);
                         }
-                        tails &= ~(1u << t.slot);
                     }
+                    __syncwarp();
                     ++used;
                     t.next(kStages);
                 }
@@ -222,49 +243,55 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        fewer_registers();
+        if (rank == 0) {
             Turn t, acc;
             uint32_t runs = 0;
             bool ok = true;
             for (int item = unit; ok && item < items; item += units) {
                 const Tile w = walk.at(item);
-                if (w.steps == 0) continue;
-                if (runs >= 2 && !role_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status)) break;
-                acc_fence_after();
-                ++runs;
                 const uint32_t id = a.id | ((B_MN ? 256u : (uint32_t)((w.n + 63) / 64 * 64)) >> 3) << 17;
-                const uint32_t d = tmem + acc.slot * 256;
-                for (int k = 0; k < w.steps; ++k) {
-                    // a cut stage's rows were cleared by the pair's threads; others are the copies' alone
-                    const bool cut = MODE == kWeights && k == w.steps - 1 && w.last % 16 != 0;
-                    if (!(cut ? role_wait<true>(&s.full[t.slot], t.phase, &s.abort, a.status)
-                              : role_wait(&s.full[t.slot], t.phase, &s.abort, a.status))) {
-                        ok = false;
-                        break;
-                    }
-                    acc_fence_after();
-                    const uint32_t at = smem_u32(ring) + t.slot * kStageBytes;
-                    const int js = MODE == kWeights && k == w.steps - 1 ? (w.last + 15) / 16 : 4;
+                for (int k = 0; ok && k < w.steps;) {
+                    // a run of the sum into the next accumulator: all of it, or kRun stages
+                    const int end = SUMS && w.steps - k > kRun ? k + kRun : w.steps;
+                    ok = runs < 2 || warp_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status);
+                    const uint32_t d = tmem + acc.slot * 256;
+                    bool add = false;
+                    for (; ok && k < end; ++k) {
+                        // a cut stage's rows were cleared by the pair's threads; others are the copies' alone
+                        const bool last = MODE == kWeights && k == w.steps - 1;
+                        ok = last && w.last % 16 != 0 ? warp_wait<true>(&s.full[t.slot], t.phase, &s.abort, a.status)
+                                                      : warp_wait(&s.full[t.slot], t.phase, &s.abort, a.status);
+                        if (!ok) break;
+                        acc_fence_after();
+                        const uint32_t at = smem_u32(ring) + t.slot * kStageBytes;
+                        const int js = last ? (w.last + 15) / 16 : 4;
+                        if (elect()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (MODE != kWeights || j < js)
-                            umma<false, true>(d, A_MN ? operand_mn(at + j * 2048, kPanel) : operand_k(at + j * 32),
-                                              B_MN ? operand_mn(at + kHalf + j * 2048, kPanel) : operand_k(at + kHalf + j * 32),
-                                              id, j != 0 || k != 0);
-                    umma_done<true>(&s.empty[t.slot]);
-                    t.next(kStages);
-                }
-                if (ok) {
-                    umma_done<true>(&s.acc_full[acc.slot]);
+                            for (int j = 0; j < 4; ++j)
+                                if (MODE != kWeights || j < js)
+                                    umma<false, true>(d, A_MN ? operand_mn(at + j * 2048, kPanel) : operand_k(at + j * 32),
+                                                      B_MN ? operand_mn(at + kHalf + j * 2048, kPanel) : operand_k(at + kHalf + j * 32),
+                                                      id, j != 0 || add);
+                            umma_done<true>(&s.empty[t.slot]);
+                            if (k + 1 == end) umma_done<true>(&s.acc_full[acc.slot]);
+                        }
+                        __syncwarp();
+                        add = true;
+                        t.next(kStages);
+                    }
                     acc.next(2);
+                    ++runs;
                 }
             }
-            umma_done<true>(&s.done);
+            if (elect()) umma_done<true>(&s.done);
+            __syncwarp();
             mbar_wait_bounded(smem_u32(&s.done), 0);
         }
-    } else if (warp < 10) {
+    } else if (warp >= Ws::kOut && warp < Ws::kOut + 8) {
+        if constexpr (SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         // two warps a 32 lanes: one takes the even runs of 32 columns, the other the odd
-        const int q = warp & 3, odd = (warp - 2) >> 2;
+        const int q = warp & 3, odd = (warp - Ws::kOut) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t free0 = cluster_addr(smem_u32(&s.acc_empty[0]), 0), free1 = cluster_addr(smem_u32(&s.acc_empty[1]), 0);
         O *out = reinterpret_cast<O *>(a.out);
@@ -274,24 +301,19 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
             const Tile w = walk.at(item);
             const int r = w.r0 + (int)rank * 128 + q * 32 + lane;
             O *const first = out + ((MODE == kWeights ? (int64_t)w.e * a.C : 0) + w.c0) * a.ldo + r;
-            if (w.steps > 0) {
-                if (!__all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status))) break;
+            bool ok = true;
+            auto ready = [&] {
+                ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status));
                 acc_fence_after();
-            }
-            if (!waited) {
-                pdl_wait();
-                waited = true;
-            }
-#pragma unroll 1
-            for (int c0 = 32 * odd; c0 < w.n; c0 += 64) {
-                float v[32];
-                if (w.steps > 0) {
-                    acc_load32(lanes + acc.slot * 256 + c0, v);
-                    acc_load_wait(v);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-                }
+                return ok;
+            };
+            auto give_back = [&] {
+                acc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(acc.slot ? free1 : free0);
+                acc.next(2);
+            };
+            auto store = [&](const float(&v)[32], int c0) {
                 O *p = first + c0 * a.ldo;
                 if (c0 + 32 <= w.n) {
                     if (r < a.R) {
@@ -308,19 +330,53 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
                         p += a.ldo;
                     }
                 }
-            }
-            if (w.steps > 0) {
-                acc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(acc.slot ? free1 : free0);
-                acc.next(2);
+            };
+            if constexpr (SUMS) {
+                uint64_t sum[64];  // runs of 32 columns, pairs of them
+#pragma unroll
+                for (int i = 0; i < 64; ++i) sum[i] = 0;
+                const uint64_t one = pack2(1.0f, 1.0f);
+                for (int k = 0; k < w.steps && ready(); k += kRun) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) add_columns(lanes + acc.slot * 256 + 32 * odd + 64 * i, sum + 16 * i, one);
+                    give_back();
+                }
+                if (!ok) break;
+                if (!waited) pdl_wait();
+                waited = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (32 * odd + 64 * i < w.n) {
+                        float v[32];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) unpack2(sum[16 * i + c], v[2 * c], v[2 * c + 1]);
+                        store(v, 32 * odd + 64 * i);
+                    }
+            } else {
+                if (w.steps > 0 && !ready()) break;
+                if (!waited) pdl_wait();
+                waited = true;
+#pragma unroll 1
+                for (int c0 = 32 * odd; c0 < w.n; c0 += 64) {
+                    float v[32];
+                    if (w.steps > 0) {
+                        acc_load32(lanes + acc.slot * 256 + c0, v);
+                        acc_load_wait(v);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+                    }
+                    store(v, c0);
+                }
+                if (w.steps > 0) give_back();
             }
         }
-    } else if (MODE == kWeights) {
+    } else {
+        fewer_registers();
         // rows past an expert's end, up to the next 16 of the sum, in the stage that holds its last rows
         Turn t;
         uint32_t parity = 0;
-        for (int item = unit; item < items; item += units) {
+        for (int item = unit; MODE == kWeights && warp == Ws::kClear && item < items; item += units) {
             const Tile w = walk.at(item);
             if (w.steps == 0) continue;
             for (int k = 0; k + 1 < w.steps; ++k) t.next(kStages);
@@ -372,7 +428,7 @@ tm_status launch_wide(const CUtensorMap &tall, const CUtensorMap &wide, const CU
     const int64_t pairs = dev.sms / 2, units = items < pairs ? items : pairs;
     void *args[] = {const_cast<CUtensorMap *>(&tall), const_cast<CUtensorMap *>(&wide), const_cast<CUtensorMap *>(&all),
                     const_cast<WideArgs *>(&a)};
-    return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(kThreadsWide), args, kWideSmem, s, pdl, 2);
+    return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(Warps<sizeof(O) == 4>::kThreads), args, kWideSmem, s, pdl, 2);
 }
 
 template <int MODE>
@@ -380,7 +436,8 @@ tm_status launch_typed(const CUtensorMap &tall, const CUtensorMap &wide, const C
                        cudaStream_t s, bool pdl)
 {
     if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
-    if (a.otype == TM_F32) return launch_wide<MODE, float>(tall, wide, all, a, items, dev, s, pdl);
+    if constexpr (MODE != kRows)  // always to 16 bits
+        if (a.otype == TM_F32) return launch_wide<MODE, float>(tall, wide, all, a, items, dev, s, pdl);
     if (a.otype == TM_F16) return launch_wide<MODE, __half>(tall, wide, all, a, items, dev, s, pdl);
     return launch_wide<MODE, __nv_bfloat16>(tall, wide, all, a, items, dev, s, pdl);
 }

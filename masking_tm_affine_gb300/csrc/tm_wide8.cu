@@ -68,34 +68,6 @@ struct Walk8 {
     }
 };
 
-__device__ __forceinline__ uint64_t pack2(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-
-// sum += m * 32 columns of the accumulator, two columns an operation.  One statement: the
-// values pass from the read to the additions in registers that nothing else names, which
-// saves the moves that separate statements took (8192 x 8192 x 4096: 255 us, so 234).
-__device__ __forceinline__ void add_columns(uint32_t at, uint64_t *s, uint64_t m)
-{
-#define TM_ADD(I, A, B) "mov.b64 p, {t" #A ", t" #B "};\n\tfma.rn.f32x2 %" #I ", p, %17, %" #I ";\n\t"
-    asm volatile(
-        "{\n\t.reg .b32 t<32>;\n\t.reg .b64 p;\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, t16, "
-        "t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t" TM_ADD(0, 0, 1) TM_ADD(1, 2, 3) TM_ADD(2, 4, 5) TM_ADD(3, 6, 7) TM_ADD(4, 8, 9)
-            TM_ADD(5, 10, 11) TM_ADD(6, 12, 13) TM_ADD(7, 14, 15) TM_ADD(8, 16, 17) TM_ADD(9, 18, 19) TM_ADD(10, 20, 21)
-                TM_ADD(11, 22, 23) TM_ADD(12, 24, 25) TM_ADD(13, 26, 27) TM_ADD(14, 28, 29) TM_ADD(15, 30, 31) "}"
-        : "+l"(s[0]), "+l"(s[1]), "+l"(s[2]), "+l"(s[3]), "+l"(s[4]), "+l"(s[5]), "+l"(s[6]), "+l"(s[7]), "+l"(s[8]),
-          "+l"(s[9]), "+l"(s[10]), "+l"(s[11]), "+l"(s[12]), "+l"(s[13]), "+l"(s[14]), "+l"(s[15])
-        : "r"(at), "l"(m)
-        : "memory");
-#undef TM_ADD
-}
-
 __global__ void __launch_bounds__(kThreads8, 1)
     wide8_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const __grid_constant__ CUtensorMap mc, const Wide8Args a)
@@ -134,7 +106,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             Turn t;
             uint32_t used = 0;
             bool ok = true;
@@ -142,14 +114,17 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const Tile8 w = walk.at(item);
                 const int row = w.row + (int)rank * 128, n = w.n0 + (int)rank * 128;
                 for (int k = 0; k < a.steps; ++k) {
-                    if (used >= kStages8 && !role_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
+                    if (used >= kStages8 && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
                         ok = false;
                         break;
                     }
                     const uint32_t at = smem_u32(ring) + t.slot * kStage8, bar = cluster_addr(smem_u32(&s.full[t.slot]), 0);
-                    mbar_expect_cluster(bar, kStage8);
-                    tma_load_2d_pair(at, &ma, k * 128, row, bar);
-                    tma_load_3d_pair(at + kHalf8, &mb, k * 128, n, w.e, bar);
+                    if (elect()) {
+                        mbar_expect_cluster(bar, kStage8);
+                        tma_load_2d_pair(at, &ma, k * 128, row, bar);
+                        tma_load_3d_pair(at + kHalf8, &mb, k * 128, n, w.e, bar);
+                    }
+                    __syncwarp();
                     ++used;
                     t.next(kStages8);
                 }
@@ -158,29 +133,34 @@ __global__ void __launch_bounds__(kThreads8, 1)
             if (rank == 0)
                 for (uint32_t i = 0; i < (uint32_t)kStages8 && i < used; ++i)
                     mbar_wait_bounded(smem_u32(&s.full[i]), ((used - i + kStages8 - 1) / kStages8 - 1) & 1u);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             Turn t, acc;
             uint32_t runs = 0;
             bool ok = true;
             for (int item = unit; ok && item < items; item += units) {
                 for (int k = 0; k < a.steps; ++k) {
-                    if ((runs >= 2 && !role_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status)) ||
-                        !role_wait(&s.full[t.slot], t.phase, &s.abort, a.status)) {
+                    if ((runs >= 2 && !warp_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status)) ||
+                        !warp_wait(&s.full[t.slot], t.phase, &s.abort, a.status)) {
                         ok = false;
                         break;
                     }
                     ++runs;
                     acc_fence_after();
                     const uint32_t at = smem_u32(ring) + t.slot * kStage8, d = tmem + acc.slot * 256;
+                    if (elect()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) umma<true, true>(d, operand_k(at + j * 32), operand_k(at + kHalf8 + j * 32), a.id, j != 0);
-                    umma_done<true>(&s.empty[t.slot]);
-                    umma_done<true>(&s.acc_full[acc.slot]);
+                        for (int j = 0; j < 4; ++j)
+                            umma<true, true>(d, operand_k(at + j * 32), operand_k(at + kHalf8 + j * 32), a.id, j != 0);
+                        umma_done<true>(&s.empty[t.slot]);
+                        umma_done<true>(&s.acc_full[acc.slot]);
+                    }
+                    __syncwarp();
                     t.next(kStages8);
                     acc.next(2);
                 }
             }
-            umma_done<true>(&s.done);
+            if (elect()) umma_done<true>(&s.done);
+            __syncwarp();
             mbar_wait_bounded(smem_u32(&s.done), 0);
         }
         __syncwarp();

@@ -3,9 +3,10 @@ quantisation and of gradient clipping, and the tolerances of their tests.
 
 Sums.  Products of two 16-bit (or two e4m3) values are exact in fp32.  The tensor
 cores' additions are taken as fp32 with truncation, 2^-23 of the partial sum each, and
-a partial sum is at most S = sum |a b|: K of them for 16 bits, at most 128 a block for e4m3,
-whose blocks then take one rounding of the scales' product, one of the addition (2^-24
-each), and up to 8 parts of a split sum one more each.
+a partial sum is at most S = sum |a b|: K of them for 16 bits (to fp32 outputs 512 a
+run, and one rounding a run), at most 128 a block for e4m3, whose blocks then take one
+rounding of the scales' product, one of the addition (2^-24 each), and up to 8 parts of a
+split sum one more each.
 """
 import numpy as np
 import torch
@@ -32,8 +33,8 @@ def rows(x, ld, fill=float("nan")):
     return out.cuda()
 
 
-def sum_bound(K):
-    return (K + 9) * ULP
+def sum_bound(K, out):
+    return ((K if out != torch.float32 else min(K, 512) + -(-K // 512)) + 9) * ULP
 
 
 def block_bound(K):

@@ -58,7 +58,7 @@ class Case:
         want, size = ref.forward(self.x64, self.w64, self.starts)
         got = y.double().cpu().numpy()
         assert np.all(got[~self.mine] == 7.0) and np.all(got[:, self.N:] == 7.0)
-        ref.check(got[self.mine, :self.N], want[self.mine], size[self.mine], 0 if self.ints else ref.sum_bound(self.K),
+        ref.check(got[self.mine, :self.N], want[self.mine], size[self.mine], 0 if self.ints else ref.sum_bound(self.K, TYPES[ytype]),
                   TYPES[ytype], "y")
 
     def check_backward(self, dx, dw, wtype):
@@ -66,12 +66,12 @@ class Case:
         if dx is not None:
             got = dx.double().cpu().numpy()
             assert np.all(got[~self.mine] == 7.0) and np.all(got[:, self.K:] == 7.0)
-            ref.check(got[self.mine, :self.K], wx[self.mine], sx[self.mine], 0 if self.ints else ref.sum_bound(self.N), self.t, "dx")
+            ref.check(got[self.mine, :self.K], wx[self.mine], sx[self.mine], 0 if self.ints else ref.sum_bound(self.N, self.t), self.t, "dx")
         if dw is not None:
             got = dw.double().cpu().numpy()
             assert np.all(got[:, self.K:] == 7.0)
             got = got[:, :self.K].reshape(self.E, self.N, self.K)
-            ref.check(got, ww, sw, 0 if self.ints else ref.sum_bound(max(1, self.T)), TYPES[wtype], "dw")
+            ref.check(got, ww, sw, 0 if self.ints else ref.sum_bound(max(1, self.T), TYPES[wtype]), TYPES[wtype], "dw")
 
     def check_all(self, out="f32", **kw):
         y = self.forward(out, **kw)
@@ -100,6 +100,11 @@ def test_integers_are_exact(cuda, counts, N, K):
 def test_values(cuda, counts, N, K, kind, out):
     c = Case(counts, N, K, kind, seed=K)
     c.check_all(kind if out == "same" else "f32")
+
+
+@pytest.mark.parametrize("counts,N,K", [([20], 136, 6000), ([600], 72, 5000), ([5000, 3000], 200, 136)])
+def test_long_sums_to_32_bits(cuda, counts, N, K):
+    Case(counts, N, K, "bf16", seed=K).check_all("f32")
 
 
 @pytest.mark.parametrize("counts", [[3, 0, 30], [290, 0, 300, 45]])
