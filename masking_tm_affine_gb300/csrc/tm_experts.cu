@@ -30,18 +30,20 @@ const void *base_of(const void *p, int64_t elements, const void *out)
     return elements > 0 ? p : reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(out) & ~uintptr_t(15));
 }
 
-// Which kernel.  Tiles of 128 by 32 or 128, of which a sum can be cut into several, up to 32 rows an
-// expert (where the weights' bytes bound the call) or while tiles of 256 by 256 would leave two
-// thirds of the SMs without work; in 8 bits such a tile of 128 rows is slower, and only taken for one of them.
+// Which kernel.  Tiles of 128 by 32 or 128, whose sums can be cut over a cluster, up to 32 rows an expert
+// (where the weights' bytes bound the call), or for long sums while tiles of 256 by 256 would leave most
+// SMs without work; in 8 bits such a tile of 128 rows is slower, and taken only for one of them.
 //   64 experts of 2048 x 2048, 16 bits: 32 rows each 105 us either way, 64 rows 119 us thin and 107 wide
 //   64 of 2048 x 4096, 8 bits: 32 rows 109 and 129 us, 64 rows 158 and 130
-//   one of 4096 x 4096, 16 bits: 128 rows 25 and 29 us, 256 rows 29 and 35, 512 rows 37 and 35;
-//   8 bits: 128 rows 21 and 25, 256 rows 37 and 25
+//   one of 4096 x 4096, 16 bits: 128 rows 22 and 28 us, 256 rows 27 and 29, 512 rows 31 and 29;
+//   8 bits: 128 rows 20 and 24, 256 rows 33 and 24
+//   short sums, 16 bits: 5 experts of 520 x 1000, 200 rows each: 18 and 16 us, their rows' gradient 22 and 14
 bool few_rows(const Product &p, const DevInfo &dev)
 {
     if (p.T <= 32 * (int64_t)p.E) return true;
     const int64_t busy = p.E < p.T ? p.E : p.T, rows = (p.T + 255) / 256, tiles = (rows > busy ? rows : busy) * ((p.F + 255) / 256);
-    return tiles * 6 <= dev.sms && (p.kind != kProductE4M3 || p.T <= 128 * (int64_t)p.E);
+    const bool f8 = p.kind == kProductE4M3;
+    return tiles * 6 <= dev.sms && p.R >= 32 * (f8 ? 128 : 64) && (!f8 || p.T <= 128 * (int64_t)p.E);
 }
 
 }  // namespace
