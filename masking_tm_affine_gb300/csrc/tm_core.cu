@@ -133,6 +133,14 @@ __global__ void __launch_bounds__(kThreads) read_probe_fixed_kernel(const float 
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
+    // The driver's call wants a context of the calling thread, which a thread has after its first
+    // runtime call that needs one -- perhaps the launch below this.
+    static thread_local bool bound = false;
+    if (!bound) {
+        int dev = 0;
+        bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+        if (!bound) cudaGetLastError();
+    }
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::call_once(once, [] {
