@@ -24,6 +24,22 @@ bool on_grid(const void *p, int64_t ld, int64_t rows, int64_t inner, int e)
 
 bool span_fits(int64_t ld, int64_t rows, int e) { return ld < (int64_t(1) << 36) && (rows == 0 || ld <= (int64_t(1) << 56) / rows / e); }
 
+// Whether two sets of rows share a byte: not where both are columns of one tensor, one beside the other.
+struct Rows {
+    const void *p;
+    int64_t ld, rows, cols;
+    int e;
+};
+bool rows_meet(const Rows &a, const Rows &b)
+{
+    const Span x = span_of(a.p, a.ld, a.rows, a.cols, a.e), y = span_of(b.p, b.ld, b.rows, b.cols, b.e);
+    if (!meets(x, y)) return false;
+    const int64_t row = a.ld * a.e;
+    if (row != b.ld * b.e) return true;
+    const int64_t d = x.lo <= y.lo ? (int64_t)(y.lo - x.lo) % row : (row - (int64_t)(x.lo - y.lo) % row) % row;
+    return d < a.cols * a.e || d + b.cols * b.e > row;
+}
+
 // Nothing of an operand without elements is read, but its map wants an address.
 const void *base_of(const void *p, int64_t elements, const void *out)
 {
@@ -63,9 +79,8 @@ extern "C" tm_status tm_gemm_experts(const void *X, int64_t ldx, const void *W, 
     if (!span_fits(ldx, T, 2) || !span_fits(ldw, (int64_t)E * N, 2)) return TM_ERR_INVALID_ARG;
     const int eo = elem_bytes(ytype);
     if (!on_grid(X, ldx, T, K, 2) || !on_grid(W, ldw, (int64_t)E * N, K, 2) || !aligned_to(Y, (uintptr_t)eo)) return TM_ERR_MISALIGNED;
-    const Span y = span_of(Y, ldy, T, N, eo);
-    if (meets(y, span_of(X, ldx, T, K, 2)) || meets(y, span_of(W, ldw, (int64_t)E * N, K, 2)) ||
-        (starts != nullptr && meets(y, span_of(starts, E + 1, 1, E + 1, 4))))
+    const Rows y = {Y, ldy, T, N, eo};
+    if (rows_meet(y, {X, ldx, T, K, 2}) || rows_meet(y, {W, ldw, (int64_t)E * N, K, 2}) || rows_meet(y, {starts, E + 1, 1, E + 1, 4}))
         return TM_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return TM_OK;
     const DevInfo *dev;
@@ -107,12 +122,11 @@ extern "C" tm_status tm_gemm_experts_bwd(const void *DY, int64_t lddy, const voi
     if (!on_grid(DY, lddy, T, N, 2) || (DX != nullptr && (!on_grid(W, ldw, EN, K, 2) || !aligned_to(DX, 2))) ||
         (DW != nullptr && (!on_grid(X, ldx, T, K, 2) || !aligned_to(DW, (uintptr_t)ew))))
         return TM_ERR_MISALIGNED;
-    const Span dx = DX ? span_of(DX, lddx, T, K, 2) : Span{0, 0}, dw = DW ? span_of(DW, lddw, EN, K, ew) : Span{0, 0};
-    const Span in[] = {span_of(DY, lddy, T, N, 2), DW ? span_of(X, ldx, T, K, 2) : Span{0, 0},
-                       DX ? span_of(W, ldw, EN, K, 2) : Span{0, 0}, starts ? span_of(starts, E + 1, 1, E + 1, 4) : Span{0, 0}};
-    for (const Span &i : in)
-        if (meets(dx, i) || meets(dw, i)) return TM_ERR_INVALID_ARG;
-    if (meets(dx, dw)) return TM_ERR_INVALID_ARG;
+    const Rows dx = {DX, lddx, T, K, 2}, dw = {DW, lddw, EN, K, ew};
+    const Rows in[] = {{DY, lddy, T, N, 2}, {DW ? X : nullptr, ldx, T, K, 2}, {DX ? W : nullptr, ldw, EN, K, 2}, {starts, E + 1, 1, E + 1, 4}};
+    for (const Rows &i : in)
+        if (rows_meet(dx, i) || rows_meet(dw, i)) return TM_ERR_INVALID_ARG;
+    if (rows_meet(dx, dw)) return TM_ERR_INVALID_ARG;
     if (!rows && !weights) return TM_OK;
     const DevInfo *dev;
     if ((st = device_info(&dev)) != TM_OK) return st;
@@ -159,9 +173,9 @@ extern "C" tm_status tm_gemm_e4m3(const void *A, int64_t lda, const float *sa, i
     if (!on_grid(A, lda, M, K, 1) || !on_grid(B, ldb, EN, K, 1) || !aligned_to(C, (uintptr_t)ec) || !aligned_to(sa, 4) ||
         !aligned_to(sb, 4))
         return TM_ERR_MISALIGNED;
-    const Span c = span_of(C, ldc, M, N, ec);
-    if (meets(c, span_of(A, lda, M, K, 1)) || meets(c, span_of(B, ldb, EN, K, 1)) || meets(c, span_of(sa, sacols, M, sacols, 4)) ||
-        meets(c, span_of(sb, NB * KB, E, NB * KB, 4)) || (starts != nullptr && meets(c, span_of(starts, E + 1, 1, E + 1, 4))))
+    const Rows c = {C, ldc, M, N, ec};
+    if (rows_meet(c, {A, lda, M, K, 1}) || rows_meet(c, {B, ldb, EN, K, 1}) || rows_meet(c, {sa, sacols, M, sacols, 4}) ||
+        rows_meet(c, {sb, NB * KB, E, NB * KB, 4}) || rows_meet(c, {starts, E + 1, 1, E + 1, 4}))
         return TM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return TM_OK;
     const DevInfo *dev;

@@ -177,7 +177,6 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
     const int tile = item / a.ftiles, f0 = (item - tile * a.ftiles) * 128;
     const int k0 = (int)((int64_t)a.steps * rank / S), k1 = (int)((int64_t)a.steps * (rank + 1) / S);
 
-    pdl_trigger();
     if (threadIdx.x == 0) {
         tensormap_prefetch(&mw);
         tensormap_prefetch(&mx);
@@ -203,6 +202,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
     acc_fence_before();
     __syncthreads();
     acc_fence_after();
+    pdl_trigger();  // only now: a dependent's CTA could take the tensor memory that this one waits for
     const int e = s.e, row0 = s.row, n = s.n;
     const uint32_t tmem = s.tmem;
     // an output warp: 32 features, CW columns from cb on

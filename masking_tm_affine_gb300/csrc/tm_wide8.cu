@@ -80,7 +80,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const uint32_t rank = cluster_rank();
     const int unit = (int)(blockIdx.x >> 1), units = (int)(gridDim.x >> 1);
 
-    pdl_trigger();
     if (warp == 1) acc_alloc<true>(&s.tmem, 512);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages8; ++i) {
@@ -100,6 +99,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     __syncthreads();
     cluster_sync();
     acc_fence_after();
+    pdl_trigger();  // only now: a dependent's CTA could take the tensor memory that this one waits for
     const uint32_t tmem = s.tmem;
     const int items = s.x.before[a.E] * a.ntiles;
     Walk8 walk(a, s.x);

@@ -62,7 +62,9 @@ def fwd(x=A, ldx=64, w=B, ldw=64, y=C, ldy=40, starts=W, E=2, T=8, N=40, K=64, x
     (INVALID, dict(ldw=63)), (INVALID, dict(ldy=39)), (INVALID, dict(x=None)), (INVALID, dict(w=None)), (INVALID, dict(y=None)),
     (MIS, dict(x=A + 2)), (MIS, dict(ldx=68)), (MIS, dict(w=B + 8)), (MIS, dict(ldw=67)), (MIS, dict(y=C + 1)),
     (MIS, dict(yt=0, y=C + 2)), (INVALID, dict(y=A)), (INVALID, dict(y=B)), (INVALID, dict(y=W)), (OK, dict(T=0)),
-    (OK, dict(N=0, w=None))])
+    # columns of the rows' own tensor: beside them, or over their ends
+    (INVALID, dict(ldx=128, y=A + 126, ldy=128)), (INVALID, dict(ldx=128, y=A + 178, ldy=128)), (INVALID, dict(ldx=128, y=A + 128, ldy=120)),
+    (INVALID, dict(ldx=128, y=A - 78, ldy=128)), (OK, dict(N=0, w=None))])
 def test_forward_refusals(want, kw):
     assert fwd(**kw) == want
 
