@@ -27,9 +27,13 @@ struct Product {
     int32_t group;
 };
 
-// A map of rows of `inner` elements in boxes 128 bytes wide and `box` rows high, 128-byte
+// A map of rows of `inner` elements of e bytes in boxes 128 bytes wide and `box` rows high, 128-byte
 // swizzle, zeros outside; with E > 0 of E matrices of `rows` rows.
-bool rows_map(CUtensorMap *m, ProductKind kind, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E, int box);
+bool rows_map_of(CUtensorMap *m, int e, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E, int box);
+inline bool rows_map(CUtensorMap *m, ProductKind kind, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E, int box)
+{
+    return rows_map_of(m, kind == kProductE4M3 ? 1 : 2, p, inner, rows, ld, E, box);
+}
 
 // The same seen as panels of 64 columns (16-bit; `inner` a multiple of 64): boxes of two panels of
 // 64 rows, one behind the other in shared memory, in one copy.  Coordinates: 0, row, panel, matrix.

@@ -23,9 +23,8 @@
 
 namespace libtm {
 
-bool rows_map(CUtensorMap *m, ProductKind kind, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E, int box)
+bool rows_map_of(CUtensorMap *m, int e, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E, int box)
 {
-    const int e = kind == kProductE4M3 ? 1 : 2;
     if (inner <= 0 || rows <= 0) inner = rows = 1, ld = 16;  // nothing to read: a map that no tile asks for
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)(E > 0 ? E : 1)};
     const cuuint64_t strides[2] = {(cuuint64_t)(ld * e), (cuuint64_t)(ld * e * rows)};
@@ -33,7 +32,7 @@ bool rows_map(CUtensorMap *m, ProductKind kind, const void *p, int64_t inner, in
     const cuuint32_t steps[3] = {1, 1, 1};
     auto encode = tensor_map_encoder();
     if (encode == nullptr) return false;
-    return encode(m, kind == kProductE4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, E > 0 ? 3 : 2,
+    return encode(m, e == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : e == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, E > 0 ? 3 : 2,
                   const_cast<void *>(p), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -11,8 +11,9 @@
 // addition is what the kernel must keep up with: 256 by 256 by 128 takes the tensor cores
 // about 512 cycles, and a CTA's share of it 128 x 256 reads and additions, 256 cycles each at best.
 //
-// Outputs leave through shared memory and TMA, so that the warps are back at the next
-// tile's sums early (16-bit outputs of whole warps' rows; others are stored directly).
+// Outputs leave through shared memory: whole warps' rows by TMA, so that the warps are back
+// at the next tile's sums early; rows that another expert's follow, or outputs off TMA's 16-byte
+// grid, by rows (stored by each thread from its own registers, 1001 rows of 1000 columns in fp32 took 15 us).
 #include <mutex>
 
 #include "tm_products.h"
@@ -27,8 +28,8 @@ constexpr uint32_t kHalf8 = 128 * 128;
 constexpr uint32_t kStage8 = 2 * kHalf8;
 constexpr int kGroup8 = 8;                 // row tiles that run at the same time, for the sake of L2
 constexpr uint32_t kOutWarp = 2 * 32 * 128;  // a warp's outputs on their way: 32 rows of two pieces of 128 bytes
-// 384 threads start with 168 registers each: 64512.  4 warps of 96 and 8 of 200 are 63488.
-constexpr int kFewRegs = 96, kManyRegs = 200;
+// 384 threads start with 168 registers each: 64512.  4 warps of 120 and 8 of 184 are 62464.
+constexpr int kFewRegs = 120, kManyRegs = 184;
 
 struct Wide8Args {
     void *out;
@@ -36,8 +37,8 @@ struct Wide8Args {
     const int32_t *starts;
     const float *sa, *sb;
     unsigned *status;
-    int otype, E, T, N, ntiles, steps, group;
-    int by_copy;  // 16-bit outputs on a grid TMA can store to
+    int E, T, N, ntiles, steps, group;
+    int by_copy;  // outputs on a grid TMA can store to
     uint32_t id;
 };
 
@@ -68,6 +69,22 @@ struct Walk8 {
     }
 };
 
+// Staged rows to where another expert's rows follow, or off the copies' grid: row by row, neighbours by
+// neighbours.  Out of line: what the sums' loop has for registers is not to depend on it.
+template <int E>
+__device__ __noinline__ void rows_out(const unsigned char *staged, void *out, int64_t ldo, int rows, int cols)
+{
+    for (int i = 0; i < rows; ++i)
+        for (int c = threadIdx.x & 31; c < 256 / E && c < cols; c += 32) {
+            const unsigned char *from = staged + (c * E >> 7) * (kOutWarp / 2) + i * 128 + ((c * E >> 4 & 7) ^ (i & 7)) * 16 + (c * E & 15);
+            if constexpr (E == 4)
+                reinterpret_cast<uint32_t *>(out)[i * ldo + c] = *reinterpret_cast<const uint32_t *>(from);
+            else
+                reinterpret_cast<uint16_t *>(out)[i * ldo + c] = *reinterpret_cast<const uint16_t *>(from);
+        }
+}
+
+template <typename O>
 __global__ void __launch_bounds__(kThreads8, 1)
     wide8_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const __grid_constant__ CUtensorMap mc, const Wide8Args a)
@@ -210,10 +227,58 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 waited = true;
             }
             if (n >= a.N) continue;
-            if (a.by_copy && __all_sync(0xffffffffu, live)) {
-                // 32 rows of 128 values: two pieces of 128 bytes a row, in the copy's swizzle
+            // the warp's 32 rows go through its staging rows of 256 bytes, two pieces of 128 in the copy's
+            // swizzle: 128 columns in 16 bits, 64 in fp32
+            const int row0 = w.row + (int)rank * 128 + q * 32, rows = w.n - ((int)rank * 128 + q * 32);
+            auto room = [&] {  // the last copy has read the staging rows
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
+            };
+            auto put = [&](int i, const uint32_t(&u)[4]) {  // 16 bytes, the i-th of the lane's row
+                const uint32_t at = smem_u32(mine) + (uint32_t)(i >> 3) * (kOutWarp / 2) + (uint32_t)lane * 128u +
+                                    (uint32_t)(((i & 7) ^ (lane & 7)) * 16);
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+            };
+            auto out = [&](int first) {  // columns first .. from the staging rows
+                constexpr int e = sizeof(O);
+                if (a.by_copy && rows >= 32) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+                            if (first + p * (128 / e) < a.N)
+                                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&mc),
+                                             "r"(first + p * (128 / e)), "r"(row0), "r"(smem_u32(mine) + (uint32_t)p * (kOutWarp / 2))
+                                             : "memory");
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    __syncwarp();
+                    return;
+                }
+                __syncwarp();
+                rows_out<sizeof(O)>(mine, reinterpret_cast<O *>(a.out) + (int64_t)row0 * a.ldo + first, a.ldo, rows < 32 ? rows : 32,
+                                    a.N - first);
+                __syncwarp();
+            };
+            if (rows <= 0) continue;
+            if constexpr (sizeof(O) == 4) {
+#pragma unroll
+                for (int half64 = 0; half64 < 2; ++half64) {
+                    if (n + 64 * half64 >= a.N) break;
+                    room();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float v[4];
+                        unpack2(sum[32 * half64 + 2 * i], v[0], v[1]);
+                        unpack2(sum[32 * half64 + 2 * i + 1], v[2], v[3]);
+                        const uint32_t u[4] = {as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])};
+                        put(i, u);
+                    }
+                    out(n + 64 * half64);
+                }
+            } else {
+                room();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     uint32_t u[4];
@@ -221,45 +286,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     for (int j = 0; j < 4; ++j) {
                         float lo, hi;
                         unpack2(sum[4 * i + j], lo, hi);
-                        if (a.otype == TM_F16)
+                        if constexpr (std::is_same<O, __half>::value)
                             asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(hi), "f"(lo));
                         else
                             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(hi), "f"(lo));
                     }
-                    const uint32_t at = smem_u32(mine) + (uint32_t)(i >> 3) * (kOutWarp / 2) + (uint32_t)lane * 128u +
-                                        (uint32_t)(((i & 7) ^ (lane & 7)) * 16);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
-                                 : "memory");
+                    put(i, u);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    const int y = w.row + (int)rank * 128 + q * 32;
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        if (n + 64 * p < a.N)
-                            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&mc),
-                                         "r"(n + 64 * p), "r"(y), "r"(smem_u32(mine) + (uint32_t)p * (kOutWarp / 2))
-                                         : "memory");
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                }
-            } else if (live) {
-                const int64_t at = row * a.ldo + n;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    float v[2];
-                    unpack2(sum[i], v[0], v[1]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (n + 2 * i + j < a.N) {
-                            if (a.otype == TM_F32)
-                                reinterpret_cast<float *>(a.out)[at + 2 * i + j] = v[j];
-                            else if (a.otype == TM_F16)
-                                reinterpret_cast<__half *>(a.out)[at + 2 * i + j] = __float2half_rn(v[j]);
-                            else
-                                reinterpret_cast<__nv_bfloat16 *>(a.out)[at + 2 * i + j] = __float2bfloat16_rn(v[j]);
-                        }
-                }
+                out(n);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -278,11 +312,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
 constexpr size_t kWide8Smem = kStages8 * kStage8 + 8 * kOutWarp + 1024;
 
-}  // namespace
-
-tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
+template <typename O>
+tm_status launch_wide8(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const Wide8Args &a, int64_t units,
+                       cudaStream_t s, bool pdl)
 {
-    const void *k = (const void *)wide8_kernel;
+    const void *k = (const void *)wide8_kernel<O>;
     static std::once_flag once[kMaxDevices];
     static bool good[kMaxDevices];
     int d = 0;
@@ -292,6 +326,15 @@ tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bo
         if (!good[d]) cudaGetLastError();
     });
     if (!good[d]) return TM_ERR_CUDA;
+    void *args[] = {const_cast<CUtensorMap *>(&ma), const_cast<CUtensorMap *>(&mb), const_cast<CUtensorMap *>(&mc),
+                    const_cast<Wide8Args *>(&a)};
+    return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(kThreads8), args, kWide8Smem, s, pdl, 2);
+}
+
+}  // namespace
+
+tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
+{
     Wide8Args a = {};
     a.out = p.out;
     a.ldo = p.ldo;
@@ -299,7 +342,6 @@ tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bo
     a.sa = p.sa;
     a.sb = p.sb;
     a.status = dev.status;
-    a.otype = p.otype;
     a.E = p.E;
     a.T = (int)p.T;
     a.N = (int)p.F;
@@ -308,15 +350,17 @@ tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bo
     a.group = p.group;
     a.id = instruction(0, false, false, 256, 256);
     // TMA clips what it stores at whole 16 bytes: N must end on them
-    a.by_copy = p.otype != TM_F32 && aligned_to(p.out, 16) && p.ldo % 8 == 0 && p.F % 8 == 0;
+    const int eo = elem_bytes(p.otype), grid = 16 / eo;
+    a.by_copy = aligned_to(p.out, 16) && p.ldo % grid == 0 && p.F % grid == 0;
     CUtensorMap ma, mb, mc;
     if (!rows_map(&ma, p.kind, p.x, p.R, p.T, p.ldx, 0, 128) || !rows_map(&mb, p.kind, p.w, p.R, p.F, p.ldw, p.E, 128)) return TM_ERR_CUDA;
-    if (a.by_copy ? !rows_map(&mc, kProductF16, p.out, p.F, p.T, p.ldo, 0, 32) : (mc = ma, false)) return TM_ERR_CUDA;
+    if (a.by_copy ? !rows_map_of(&mc, eo, p.out, p.F, p.T, p.ldo, 0, 32) : (mc = ma, false)) return TM_ERR_CUDA;
     const int64_t busy = p.E < p.T ? p.E : p.T, items = ((p.T + 255) / 256 + busy) * a.ntiles, pairs = dev.sms / 2;
     if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
     const int64_t units = items < pairs ? items : pairs;
-    void *args[] = {&ma, &mb, &mc, &a};
-    return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(kThreads8), args, kWide8Smem, s, pdl, 2);
+    if (p.otype == TM_F32) return launch_wide8<float>(ma, mb, mc, a, units, s, pdl);
+    if (p.otype == TM_F16) return launch_wide8<__half>(ma, mb, mc, a, units, s, pdl);
+    return launch_wide8<__nv_bfloat16>(ma, mb, mc, a, units, s, pdl);
 }
 
 }  // namespace libtm
