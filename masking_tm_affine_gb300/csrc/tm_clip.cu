@@ -19,8 +19,8 @@ namespace libtm {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kChunk = 16384;
-constexpr int kClipBlocks = 8;     // blocks an SM: the most that are resident
+constexpr int kChunk = 8192;       // 32 elements a thread, all read together
+constexpr int kClipBlocks = 4;     // blocks an SM: the most that are resident
 constexpr int kMostBlocks = 4096;  // sums a workspace holds
 
 struct Chunk {
@@ -73,7 +73,7 @@ __device__ __forceinline__ double square(const float (&v)[W])
 template <typename T>
 __device__ __forceinline__ double chunk_sum(const Chunk &c)
 {
-    constexpr int W = 16 / sizeof(T), U = 4;
+    constexpr int W = 16 / sizeof(T), U = 32 / W;
     const T *p = reinterpret_cast<const T *>(c.src);
     double sum = 0.0;
     if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
@@ -121,13 +121,16 @@ __device__ __forceinline__ double block_sum(double x, double *shared)
     return x;
 }
 
-__global__ void __launch_bounds__(kClipThreads) clip_sums(const ClipArgs a)
+__global__ void __launch_bounds__(kClipThreads, kClipBlocks) clip_sums(const ClipArgs a)
 {
     __shared__ double shared[kClipThreads / 32];
     pdl_trigger();
     double sum = 0.0;
+    Chunk next = {};
+    if (blockIdx.x < a.chunks) next = chunk_at(a.plan, blockIdx.x);
     for (int64_t i = blockIdx.x; i < a.chunks; i += gridDim.x) {
-        const Chunk c = chunk_at(a.plan, i);
+        const Chunk c = next;
+        if (i + gridDim.x < a.chunks) next = chunk_at(a.plan, i + gridDim.x);
         sum += c.type == TM_F32 ? chunk_sum<float>(c) : c.type == TM_F16 ? chunk_sum<__half>(c) : chunk_sum<__nv_bfloat16>(c);
     }
     sum = block_sum(sum, shared);
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kClipThreads) clip_sums(const ClipArgs a)
 template <typename T>
 __device__ __forceinline__ void chunk_scale(const Chunk &c, float f)
 {
-    constexpr int W = 16 / sizeof(T), U = 4;
+    constexpr int W = 16 / sizeof(T), U = 32 / W;
     const T *p = reinterpret_cast<const T *>(c.src);
     T *q = reinterpret_cast<T *>(c.dst);
     if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15) == 0) {
@@ -167,10 +170,12 @@ __device__ __forceinline__ void chunk_scale(const Chunk &c, float f)
     }
 }
 
-__global__ void __launch_bounds__(kClipThreads) clip_scale(const ClipArgs a)
+__global__ void __launch_bounds__(kClipThreads, kClipBlocks) clip_scale(const ClipArgs a)
 {
     __shared__ double shared[kClipThreads / 32];
     pdl_trigger();
+    Chunk next = {};
+    if (a.chunks > blockIdx.x) next = chunk_at(a.plan, a.chunks - 1 - blockIdx.x);
     pdl_wait();  // the sums
     double sum = 0.0;
     for (int i = threadIdx.x; i < a.blocks; i += kClipThreads) sum += __ldcg(a.sums + i);
@@ -180,7 +185,8 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale(const ClipArgs a)
     const double ratio = (double)a.max_norm / (norm + (double)a.eps);
     const float f = isinf(a.max_norm) || ratio >= 1.0 ? 1.0f : (float)ratio;
     for (int64_t i = a.chunks - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
-        const Chunk c = chunk_at(a.plan, i);
+        const Chunk c = next;
+        if (i >= gridDim.x) next = chunk_at(a.plan, i - gridDim.x);
         if (c.dst == nullptr || (f == 1.0f && c.dst == c.src)) continue;
         if (c.type == TM_F32)
             chunk_scale<float>(c, f);

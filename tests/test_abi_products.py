@@ -85,15 +85,20 @@ def test_backward_refusals(want, kw):
 
 
 def test_clip_plan():
-    sizes = [0, 1, 16384, 16385, 70000]
-    assert tm.tm_clip_chunks(sizes) == 0 + 1 + 1 + 2 + 5 and tm.tm_clip_chunks([]) == 0 and tm.tm_clip_chunks([-1]) == -1
-    g = [None, A, B, C, W]
-    p = tm.tm_clip_plan(g, [None, None, B, S, X], sizes, [0, 2, 1, 0, 2])
-    rows = p.view(torch.int64).view(-1, 4).tolist()
-    assert p.numel() == 9 * tm.TM_CLIP_CHUNK_BYTES
-    at = [(r[0], r[1], r[2] & 0xFFFFFFFF, r[2] >> 32) for r in rows]
-    assert at[:4] == [(A, 0, 1, 2), (B, B, 16384, 1), (C, S, 16384, 0), (C + 65536, S + 65536, 1, 0)]
-    assert at[4] == (W, X, 16384, 2) and at[8] == (W + 4 * 32768, X + 4 * 32768, 70000 - 65536, 2)
+    sizes, types = [0, 1, 16384, 16385, 70000], [0, 2, 1, 0, 2]
+    grads, outs = [None, A, B, C, W], [None, None, B, S, X]
+    assert tm.tm_clip_chunks([]) == tm.tm_clip_chunks([0, 0]) == 0 and tm.tm_clip_chunks([-1]) == -1 and tm.tm_clip_chunks([1]) == 1
+    rows = tm.tm_clip_plan(grads, outs, sizes, types).view(torch.int64).view(-1, 4).tolist()
+    assert len(rows) == tm.tm_clip_chunks(sizes)
+    rows = [(r[0], r[1], r[2] & 0xFFFFFFFF, r[2] >> 32) for r in rows]
+    for g, o, n, t in zip(grads, outs, sizes, types):      # each tensor's chunks follow one another and cover it
+        e, at = (4, 2, 2)[t], 0
+        while at < n:
+            src, dst, count, kind = rows.pop(0)
+            assert (src, dst, kind) == (g + at * e, 0 if o is None else o + at * e, t) and 0 < count <= n - at
+            assert at % 8 == 0                             # whole 16-byte vectors from the tensor's start
+            at += count
+    assert not rows
     assert tm.tm_clip_plan([A], None, [5], [0]).view(torch.int64).tolist()[1] == 0
 
 
