@@ -201,16 +201,16 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
 #undef TM_UMMA
 }
 
-// Arrive on `b` (in both CTAs of a pair) once every product issued so far by this
-// thread has completed.
+// Arrive on `b` (in both CTAs of a pair, whose ranks are the bits of `ranks`) once every
+// product issued so far by this thread has completed.
 template <bool PAIR>
-__device__ __forceinline__ void umma_done(uint64_t *b)
+__device__ __forceinline__ void umma_done(uint64_t *b, uint32_t ranks = 3)
 {
     if constexpr (PAIR)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
                 smem_u32(b)),
-            "h"((uint16_t)3)
+            "h"((uint16_t)ranks)
             : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b))
@@ -295,6 +295,40 @@ __device__ __forceinline__ void add_columns(uint32_t at, uint64_t *s, uint64_t m
 
 // 16-bit operands to fp32 outputs: how much of a sum the tensor cores add before it leaves them.
 constexpr int kRunSums = 512;
+
+// ---------------------------------------------------------------- joins
+// A tile's sum cut over the pairs of a cluster: each output warp pushes its runs of 32 columns to
+// the CTA (of its own rank in the pair) whose pair owns them, into [pair][8 warps][4 / S runs][8][32 lanes] x
+// 16 bytes, 128 KB in the rings' place.  The owner adds them in the order of the pairs.
+__device__ __forceinline__ uint32_t join_slot(int pair, int warp, int run, int S, int lane)
+{
+    return (uint32_t)(((pair * 8 + warp) * (4 / S) + run % (4 / S)) * 8 * 32 + lane) * 16u;
+}
+__device__ __forceinline__ void join_push(const float (&v)[32], uint32_t inbox, uint64_t *bar, int pair, int warp, int run, int S,
+                                          uint32_t rank)
+{
+    const uint32_t to = (uint32_t)(run / (4 / S)) * 2u + rank, lane = threadIdx.x & 31u;
+    const uint32_t dst = cluster_addr(inbox + join_slot(pair, warp, run, S, (int)lane), to), b = cluster_addr(smem_u32(bar), to);
+#pragma unroll
+    for (int c = 0; c < 32; c += 4)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                         dst + (uint32_t)c * 128u),
+                     "r"(as_u(v[c])), "r"(as_u(v[c + 1])), "r"(as_u(v[c + 2])), "r"(as_u(v[c + 3])), "r"(b)
+                     : "memory");
+}
+__device__ __forceinline__ void join_sum(float (&v)[32], const unsigned char *inbox, int warp, int run, int S)
+{
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+    for (int pair = 0; pair < S; ++pair) {
+        const unsigned char *from = inbox + join_slot(pair, warp, run, S, (int)(threadIdx.x & 31u));
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(from + c * 128);
+            v[c] += u.x, v[c + 1] += u.y, v[c + 2] += u.z, v[c + 3] += u.w;
+        }
+    }
+}
 
 // ---------------------------------------------------------------- rows of the experts
 constexpr int kMaxExperts = 1024;

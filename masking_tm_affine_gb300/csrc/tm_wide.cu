@@ -62,7 +62,7 @@ struct WideArgs {
 };
 
 struct WideSmem {
-    alignas(8) uint64_t full[kStages], empty[kStages], tail[kStages], acc_full[2], acc_empty[2], done;
+    alignas(8) uint64_t full[kStages], empty[kStages], tail[kStages], acc_full[2], acc_empty[2], done, inbox;
     uint32_t tmem;
     int abort;
     Experts x;
@@ -71,14 +71,16 @@ struct WideSmem {
 // A tile: expert, first of r and c, how many of c, the rows summed (weights' gradient).
 struct Tile {
     int e, r0, c0, n, s0, steps, last;  // last: rows of the last stage, 64 if it is whole
+    int kb, ke;                         // this pair's stages
 };
 
 template <int MODE>
 struct Walk {
     const WideArgs &a;
     const Experts &x;
+    const int pair, S;  // of the S pairs that share a tile's sum
     int e = 0;
-    __device__ Walk(const WideArgs &args, const Experts &experts) : a(args), x(experts) {}
+    __device__ Walk(const WideArgs &args, const Experts &experts, int p, int pairs) : a(args), x(experts), pair(p), S(pairs) {}
     __device__ Tile at(int item)
     {
         Tile t;
@@ -113,14 +115,17 @@ struct Walk {
             t.steps = a.steps;
             t.last = 64;
         }
+        t.kb = S == 1 ? 0 : t.steps * pair / S;
+        t.ke = S == 1 ? t.steps : t.steps * (pair + 1) / S;
         return t;
     }
 };
 
-template <int MODE, typename O>
+// SPLIT (weights' gradient): a cluster of S pairs (2 or 4) has one tile, each pair its part of the sum.
+template <int MODE, typename O, bool SPLIT>
 __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap mtall, const __grid_constant__ CUtensorMap mwide,
-                const __grid_constant__ CUtensorMap mwide_all, const WideArgs a)
+                const __grid_constant__ CUtensorMap mwide_all, const WideArgs a, const int pairs)
 {
     constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeights, SUMS = sizeof(O) == 4;
     using Ws = Warps<SUMS>;
@@ -128,8 +133,9 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
     unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     __shared__ WideSmem s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int unit = (int)(blockIdx.x >> 1), units = (int)(gridDim.x >> 1);
+    const int S = SPLIT ? pairs : 1;
+    const uint32_t rank = cluster_rank() & 1u, even = SPLIT ? cluster_rank() & ~1u : 0u;  // in the pair; its even CTA
+    const int pair = (int)even / 2, unit = (int)blockIdx.x / (2 * S), units = (int)gridDim.x / (2 * S);
 
     if (warp == 1) acc_alloc<true>(&s.tmem, 512);
     if (threadIdx.x == 0) {
@@ -143,6 +149,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
             mbar_init(&s.acc_empty[i], 16);
         }
         mbar_init(&s.done, 1);
+        mbar_init(&s.inbox, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s.abort = 0;
     }
@@ -154,7 +161,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
     pdl_trigger();  // only now: a dependent's CTA could take the tensor memory that this one waits for
     const uint32_t tmem = s.tmem;
     const int items = MODE == kWeights ? a.E * a.rtiles * a.ctiles : s.x.before[a.E] * a.rtiles;
-    Walk<MODE> walk(a, s.x);
+    Walk<MODE> walk(a, s.x, pair, S);
 
     // in the branches themselves: behind one of its own the compiler counts on the smaller share everywhere
     auto fewer_registers = [] {
@@ -173,7 +180,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                 // the wide operand's share of this CTA: half of the product's extent
                 const int half = B_MN ? 128 : (w.n + 63) / 64 * 32, c = w.c0 + (int)rank * half;
                 const uint32_t bytes = kHalf + (B_MN ? kHalf : (uint32_t)half * 128u);
-                for (int k = 0; k < w.steps; ++k) {
+                for (int k = w.kb; k < w.ke; ++k) {
                     if (used >= kStages && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
                         ok = false;
                         break;
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                                 for (int p = 0; p < 2; ++p) tma_load_2d(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
                         }
                     } else {
-                        const uint32_t bar = cluster_addr(smem_u32(&s.full[t.slot]), 0);
+                        const uint32_t bar = cluster_addr(smem_u32(&s.full[t.slot]), even);
                         mbar_expect_cluster(bar, bytes);
                         if constexpr (MODE == kWeights) {
                             if (a.tall_panels)
@@ -251,9 +258,9 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
             for (int item = unit; ok && item < items; item += units) {
                 const Tile w = walk.at(item);
                 const uint32_t id = a.id | ((B_MN ? 256u : (uint32_t)((w.n + 63) / 64 * 64)) >> 3) << 17;
-                for (int k = 0; ok && k < w.steps;) {
+                for (int k = w.kb; ok && k < w.ke;) {
                     // a run of the sum into the next accumulator: all of it, or kRun stages
-                    const int end = SUMS && w.steps - k > kRun ? k + kRun : w.steps;
+                    const int end = SUMS && w.ke - k > kRun ? k + kRun : w.ke;
                     ok = runs < 2 || warp_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status);
                     const uint32_t d = tmem + acc.slot * 256;
                     bool add = false;
@@ -273,8 +280,8 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                                     umma<false, true>(d, A_MN ? operand_mn(at + j * 2048, kPanel) : operand_k(at + j * 32),
                                                       B_MN ? operand_mn(at + kHalf + j * 2048, kPanel) : operand_k(at + kHalf + j * 32),
                                                       id, j != 0 || add);
-                            umma_done<true>(&s.empty[t.slot]);
-                            if (k + 1 == end) umma_done<true>(&s.acc_full[acc.slot]);
+                            umma_done<true>(&s.empty[t.slot], 3u << even);
+                            if (k + 1 == end) umma_done<true>(&s.acc_full[acc.slot], 3u << even);
                         }
                         __syncwarp();
                         add = true;
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                     ++runs;
                 }
             }
-            if (elect()) umma_done<true>(&s.done);
+            if (elect()) umma_done<true>(&s.done, 3u << even);
             __syncwarp();
             mbar_wait_bounded(smem_u32(&s.done), 0);
         }
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
         // two warps a 32 lanes: one takes the even runs of 32 columns, the other the odd
         const int q = warp & 3, odd = (warp - Ws::kOut) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-        const uint32_t free0 = cluster_addr(smem_u32(&s.acc_empty[0]), 0), free1 = cluster_addr(smem_u32(&s.acc_empty[1]), 0);
+        const uint32_t free0 = cluster_addr(smem_u32(&s.acc_empty[0]), even), free1 = cluster_addr(smem_u32(&s.acc_empty[1]), even);
         O *out = reinterpret_cast<O *>(a.out);
         Turn acc;
         bool waited = false;
@@ -331,15 +338,50 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                     }
                 }
             };
+            // SPLIT: the parts of the sum meet; get(i, v): this pair's columns 32 odd + 64 i on
+            auto join = [&](auto get) {
+                const int own = pair * (4 / S), mine = warp - Ws::kOut;
+                if (warp == Ws::kOut && lane == 0) {
+                    uint32_t runs = 0;
+                    for (int i = 0; i < 4 / S; ++i) runs += (64 * (own + i) < w.n) + (64 * (own + i) + 32 < w.n);
+                    mbar_expect(&s.inbox, runs * (uint32_t)S * 16384u);
+                }
+                __syncwarp();
+                cluster_sync();  // every ring is done with, every inbox ready
+                if (!ok) return;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (32 * odd + 64 * i < w.n) {
+                        float v[32];
+                        get(i, v);
+                        join_push(v, smem_u32(ring), &s.inbox, pair, mine, i, S, rank);
+                    }
+                ok = __all_sync(0xffffffffu, role_wait<true>(&s.inbox, 0, &s.abort, a.status));
+                if (!ok) return;
+                pdl_wait();
+                for (int i = own; i < own + 4 / S; ++i)
+                    if (32 * odd + 64 * i < w.n) {
+                        float v[32];
+                        join_sum(v, ring, mine, i, S);
+                        store(v, 32 * odd + 64 * i);
+                    }
+            };
             if constexpr (SUMS) {
                 uint64_t sum[64];  // runs of 32 columns, pairs of them
 #pragma unroll
                 for (int i = 0; i < 64; ++i) sum[i] = 0;
                 const uint64_t one = pack2(1.0f, 1.0f);
-                for (int k = 0; k < w.steps && ready(); k += kRun) {
+                for (int k = w.kb; k < w.ke && ready(); k += kRun) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) add_columns(lanes + acc.slot * 256 + 32 * odd + 64 * i, sum + 16 * i, one);
                     give_back();
+                }
+                if constexpr (SPLIT) {
+                    join([&](int i, float(&v)[32]) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) unpack2(sum[16 * i + c], v[2 * c], v[2 * c + 1]);
+                    });
+                    break;
                 }
                 if (!ok) break;
                 if (!waited) pdl_wait();
@@ -353,6 +395,19 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                         store(v, 32 * odd + 64 * i);
                     }
             } else {
+                if constexpr (SPLIT) {
+                    if (w.kb < w.ke) ready();
+                    join([&](int i, float(&v)[32]) {
+                        if (w.kb < w.ke) {
+                            acc_load32(lanes + 32 * odd + 64 * i, v);
+                            acc_load_wait(v);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+                        }
+                    });
+                    break;
+                }
                 if (w.steps > 0 && !ready()) break;
                 if (!waited) pdl_wait();
                 waited = true;
@@ -378,9 +433,9 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
         uint32_t parity = 0;
         for (int item = unit; MODE == kWeights && warp == Ws::kClear && item < items; item += units) {
             const Tile w = walk.at(item);
-            if (w.steps == 0) continue;
-            for (int k = 0; k + 1 < w.steps; ++k) t.next(kStages);
-            if (w.last % 16 != 0) {
+            if (w.kb == w.ke) continue;
+            for (int k = w.kb; k + 1 < w.ke; ++k) t.next(kStages);
+            if (w.last % 16 != 0 && w.ke == w.steps) {
                 if (!__all_sync(0xffffffffu, role_wait(&s.tail[t.slot], parity >> t.slot & 1u, &s.abort, a.status))) break;
                 parity ^= 1u << t.slot;
                 const uint32_t at = smem_u32(ring) + t.slot * kStageBytes;
@@ -393,11 +448,13 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                                  : "memory");
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&s.full[t.slot]), 0));
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&s.full[t.slot]), even));
             }
             t.next(kStages);
         }
     }
+    __syncwarp();
+    if (SPLIT && unit < items && !(warp >= Ws::kOut && warp < Ws::kOut + 8)) cluster_sync();  // the joins' own
     pdl_wait();
     acc_fence_before();
     __syncthreads();
@@ -411,35 +468,87 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
 
 constexpr size_t kWideSmem = kStages * kStageBytes + 1024;
 
-template <int MODE, typename O>
-tm_status launch_wide(const CUtensorMap &tall, const CUtensorMap &wide, const CUtensorMap &all, const WideArgs &a, int64_t items, const DevInfo &dev,
-                      cudaStream_t s, bool pdl)
+// One instance of the kernel on a device: its shared memory allowed, and how many clusters of 2 and
+// 4 pairs can be there at once.
+struct Instance {
+    std::once_flag once;
+    bool good;
+    int fit2, fit4;
+};
+
+template <int MODE, typename O, bool SPLIT>
+tm_status instance(const Instance **out)
 {
-    const void *k = (const void *)wide_kernel<MODE, O>;
-    static std::once_flag once[kMaxDevices];
-    static bool good[kMaxDevices];
+    static Instance each[kMaxDevices];
+    const void *k = (const void *)wide_kernel<MODE, O, SPLIT>;
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return TM_ERR_CUDA;
-    std::call_once(once[d], [&] {
-        good[d] = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWideSmem) == cudaSuccess;
-        if (!good[d]) cudaGetLastError();
+    Instance &i = each[d];
+    std::call_once(i.once, [&] {
+        i.good = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWideSmem) == cudaSuccess;
+        i.fit2 = i.fit4 = 0;
+        for (int S = 2; i.good && SPLIT && S <= 4; S *= 2) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 * S);
+            cfg.blockDim = dim3(Warps<sizeof(O) == 4>::kThreads);
+            cfg.dynamicSmemBytes = kWideSmem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)(2 * S);
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(S == 2 ? &i.fit2 : &i.fit4, k, &cfg) != cudaSuccess) (S == 2 ? i.fit2 : i.fit4) = 0;
+        }
+        cudaGetLastError();
     });
-    if (!good[d]) return TM_ERR_CUDA;
-    const int64_t pairs = dev.sms / 2, units = items < pairs ? items : pairs;
+    *out = &i;
+    return i.good ? TM_OK : TM_ERR_CUDA;
+}
+
+template <int MODE, typename O, bool SPLIT>
+tm_status launch_pairs(const CUtensorMap &tall, const CUtensorMap &wide, const CUtensorMap &all, const WideArgs &a, int S, int64_t units,
+                       cudaStream_t s, bool pdl)
+{
+    const Instance *i;
+    const tm_status st = instance<MODE, O, SPLIT>(&i);
+    if (st != TM_OK) return st;
     void *args[] = {const_cast<CUtensorMap *>(&tall), const_cast<CUtensorMap *>(&wide), const_cast<CUtensorMap *>(&all),
-                    const_cast<WideArgs *>(&a)};
-    return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(Warps<sizeof(O) == 4>::kThreads), args, kWideSmem, s, pdl, 2);
+                    const_cast<WideArgs *>(&a), &S};
+    return launch_kernel((const void *)wide_kernel<MODE, O, SPLIT>, dim3((unsigned)(2 * S * units)),
+                         dim3(Warps<sizeof(O) == 4>::kThreads), args, kWideSmem, s, pdl, (unsigned)(2 * S));
+}
+
+// steps: stages of an average sum (weights' gradient).  Few long sums are shared by pairs while all the
+// clusters are there at once: a join costs about 5 us, a stage 0.27.  One expert of 1024 x 1024 in fp32,
+// 2048 rows: 15.6 us a pair a tile, 16.0 two; 4096 rows: 24.0, 20.2; 8192 rows: 40.8, 28.5.  Of 512 x 520, four
+// pairs a tile: 2048 rows 15.2, 4096 rows 17.3, 8192 rows 21.6 us.  The other products with as few
+// tiles and sums as long go to the small tiles (tm_experts.cu).
+template <int MODE, typename O>
+tm_status launch_wide(const CUtensorMap &tall, const CUtensorMap &wide, const CUtensorMap &all, const WideArgs &a, int64_t items,
+                      int64_t steps, const DevInfo &dev, cudaStream_t s, bool pdl)
+{
+    if constexpr (MODE == kWeights)
+        if (steps >= 32) {
+            const Instance *i;
+            const tm_status st = instance<MODE, O, true>(&i);
+            if (st != TM_OK) return st;
+            const int S = items <= i->fit4 ? 4 : items <= i->fit2 && steps >= 48 ? 2 : 1;
+            if (S > 1) return launch_pairs<MODE, O, true>(tall, wide, all, a, S, items, s, pdl);
+        }
+    const int64_t pairs = dev.sms / 2;
+    return launch_pairs<MODE, O, false>(tall, wide, all, a, 1, items < pairs ? items : pairs, s, pdl);
 }
 
 template <int MODE>
-tm_status launch_typed(const CUtensorMap &tall, const CUtensorMap &wide, const CUtensorMap &all, const WideArgs &a, int64_t items, const DevInfo &dev,
-                       cudaStream_t s, bool pdl)
+tm_status launch_typed(const CUtensorMap &tall, const CUtensorMap &wide, const CUtensorMap &all, const WideArgs &a, int64_t items,
+                       int64_t steps, const DevInfo &dev, cudaStream_t s, bool pdl)
 {
     if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
     if constexpr (MODE != kRows)  // always to 16 bits
-        if (a.otype == TM_F32) return launch_wide<MODE, float>(tall, wide, all, a, items, dev, s, pdl);
-    if (a.otype == TM_F16) return launch_wide<MODE, __half>(tall, wide, all, a, items, dev, s, pdl);
-    return launch_wide<MODE, __nv_bfloat16>(tall, wide, all, a, items, dev, s, pdl);
+        if (a.otype == TM_F32) return launch_wide<MODE, float>(tall, wide, all, a, items, steps, dev, s, pdl);
+    if (a.otype == TM_F16) return launch_wide<MODE, __half>(tall, wide, all, a, items, steps, dev, s, pdl);
+    return launch_wide<MODE, __nv_bfloat16>(tall, wide, all, a, items, steps, dev, s, pdl);
 }
 
 int tiles256(int64_t n) { return (int)((n + 255) / 256); }
@@ -467,8 +576,8 @@ tm_status wide_product(const Product &p, const DevInfo &dev, cudaStream_t s, boo
         return TM_ERR_CUDA;
     if (!rows_map(&wide, p.kind, p.x, p.R, p.T, p.ldx, 0, 32) || !rows_map(&all, p.kind, p.x, p.R, p.T, p.ldx, 0, 128)) return TM_ERR_CUDA;
     const int64_t busy = p.E < p.T ? p.E : p.T, items = ((p.T + 255) / 256 + busy) * a.rtiles;
-    return p.w_mn ? launch_typed<kRows>(tall, wide, all, a, items, dev, s, pdl)
-                  : launch_typed<kForward>(tall, wide, all, a, items, dev, s, pdl);
+    return p.w_mn ? launch_typed<kRows>(tall, wide, all, a, items, a.steps, dev, s, pdl)
+                  : launch_typed<kForward>(tall, wide, all, a, items, a.steps, dev, s, pdl);
 }
 
 tm_status wide_weights(ProductKind kind, const void *dy, int64_t lddy, const void *x, int64_t ldx, void *dw, int64_t lddw,
@@ -493,7 +602,7 @@ tm_status wide_weights(ProductKind kind, const void *dy, int64_t lddy, const voi
     CUtensorMap tall, wide;
     if (a.tall_panels ? !panels_map(&tall, x, K, T, ldx, 0) : !rows_map(&tall, kind, x, K, T, ldx, 0, 64)) return TM_ERR_CUDA;
     if (a.wide_panels ? !panels_map(&wide, dy, N, T, lddy, 0) : !rows_map(&wide, kind, dy, N, T, lddy, 0, 64)) return TM_ERR_CUDA;
-    return launch_typed<kWeights>(tall, wide, wide, a, (int64_t)E * a.rtiles * a.ctiles, dev, s, pdl);
+    return launch_typed<kWeights>(tall, wide, wide, a, (int64_t)E * a.rtiles * a.ctiles, T / 64 / E, dev, s, pdl);
 }
 
 }  // namespace libtm

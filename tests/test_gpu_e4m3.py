@@ -168,6 +168,21 @@ def test_values(cuda, counts, N, K, out, group):
     c.check(got, out)
 
 
+# few tiles with long sums
+@pytest.mark.parametrize("counts,N,K", [([300], 264, 4100), ([300], 264, 2000), ([700, 240], 130, 3333), ([513], 72, 8000), ([250, 0, 300], 1000, 4100)])
+@pytest.mark.parametrize("out,group", [("bf16", 128), ("f32", 0)])
+def test_few_long_sums(cuda, counts, N, K, out, group):
+    c = Case(counts, N, K, group, seed=N, ints=True, behind=3)
+    got = c.run("f32")
+    tm.tm_check()
+    c.check(got)
+    c = Case(counts, N, K, group, seed=N)
+    got, again = c.run(out, ldc=N + 8), c.run(out, ldc=N + 8)
+    tm.tm_check()
+    c.check(got, out)
+    assert torch.equal(got, again)
+
+
 def test_one_matrix_without_borders(cuda):
     for T in (9, 600):
         c = Case([T], 192, 320, ints=True, starts=False)

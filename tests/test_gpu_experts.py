@@ -123,6 +123,21 @@ def test_sums_over_any_number_of_rows(cuda, n):
     Case([n], 72, 136, "f16", seed=n, ints=True, behind=64, before=3).check_all("f32")
 
 
+# few tiles with long sums: forward (long K), rows' gradient (long N), weights' gradient (many rows, shared by pairs of SMs)
+@pytest.mark.parametrize("counts,N,K", [([600], 264, 2000), ([600], 264, 4100), ([700, 40], 130, 3333), ([600], 3400, 264),
+                                        ([4000], 264, 130), ([9001], 72, 520), ([3000, 0, 1700], 130, 136), ([513], 72, 6000),
+                                        ([3500], 1000, 1000), ([0, 6003], 257, 300)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_few_long_sums(cuda, counts, N, K, out):
+    Case(counts, N, K, "bf16", seed=N, ints=True, behind=3).check_all(out)
+    c = Case(counts, N, K, "bf16", seed=N)
+    c.check_all(out)
+    y, (dx, dw) = c.forward(out), c.backward(out)
+    again, (dx2, dw2) = c.forward(out), c.backward(out)
+    tm.tm_check()
+    assert torch.equal(y, again) and torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
 def test_one_matrix_without_borders(cuda):
     for T in (9, 600):
         Case([T], 192, 320, "bf16", ints=True, starts=False).check_all("f32")
