@@ -667,8 +667,10 @@ tm_status tm_quant_e4m3(const void *X, int64_t ldx, int64_t M, int64_t N, void *
  *              (expert by expert where N is no multiple of 128)
  *   C, ldc     output [M, N] of ctype (TM_F32, TM_F16, TM_BF16); overlaps no input
  * Products of codes are exact and summed in fp32 over a block of 128, and the blocks in
- * fp32 after their scales: |error| <= (K + ceil(K / 128)) 2^-23 * sum |sa sb A B|.  The gradient of the
- * rows is the same call with the transposed codes and scales of B.
+ * fp32 after their scales: |error| <= (128 + ceil(K / 128) + 9) 2^-23 * sum |sa sb A B|, plus the
+ * output's own rounding.  The two scales of a block are multiplied first, in fp32 (below
+ * 2^-126 that product loses bits).  The gradient of the rows is the same call with
+ * the transposed codes and scales of B.
  * Errors: INVALID_ARG, UNSUPPORTED_TILE (group, E, extents beyond 2^31 - 513 or 2^30
  *         tiles), MISALIGNED, CUDA; INDEX and TIMEOUT through tm_check.
  */
@@ -717,7 +719,8 @@ tm_status tm_gemm_experts_bwd(const void *DY, int64_t lddy, const void *X, int64
  *
  * tm_clip_grads -- one step:
  *   plan, chunks   the device copy
- *   max_norm   >= 0; infinity: no clipping.  With factor 1 a gradient in place is not written
+ *   max_norm   >= 0; infinity: no clipping, and none where norm + eps is 0.  With factor 1 a
+ *              gradient in place is not written
  *   norm       output, one fp32 on the device.  It is right wherever fp32 holds it: squares
  *              beyond fp32's range are added in 64 bits.  A NaN or infinite gradient makes
  *              it so; then out = g * NaN, or g * 0

@@ -181,9 +181,9 @@ __global__ void __launch_bounds__(kClipThreads, kClipBlocks) clip_scale(const Cl
     for (int i = threadIdx.x; i < a.blocks; i += kClipThreads) sum += __ldcg(a.sums + i);
     const double norm = sqrt(block_sum(sum, shared));
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-    // a NaN stays one
-    const double ratio = (double)a.max_norm / (norm + (double)a.eps);
-    const float f = isinf(a.max_norm) || ratio >= 1.0 ? 1.0f : (float)ratio;
+    // a NaN stays one; nothing at all is not clipped
+    const double size = norm + (double)a.eps, ratio = (double)a.max_norm / size;
+    const float f = isinf(a.max_norm) || size == 0.0 || ratio >= 1.0 ? 1.0f : (float)ratio;
     for (int64_t i = a.chunks - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
         const Chunk c = next;
         if (i >= gridDim.x) next = chunk_at(a.plan, i - gridDim.x);

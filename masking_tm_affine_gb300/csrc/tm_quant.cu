@@ -23,18 +23,22 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 
-// A block's factor 448 / top.  Tops below 2^-60 are lifted by 2^64 (exactly), with their values.
+// A block's factor 448 / top.  It passes fp32's range below tops of 2^-119: values of a block whose top is
+// below 2^-100 are raised by 2^64 first, which is exact in their own type (fp16 has none as small).
 struct Factor {
-    float top, by, lift;
+    float top, by;
 };
-__device__ __forceinline__ float lift_of(float top) { return top < 0x1p-60f ? 0x1p64f : 1.0f; }
+constexpr float kSmall = 0x1p-100f, kRaise = 0x1p64f;
 __device__ __forceinline__ Factor factor_of(float top)
 {
-    Factor f;
-    f.lift = lift_of(top);
-    f.top = top * f.lift;
-    f.by = top > 0.0f ? __fdiv_rn(448.0f, f.top) : 0.0f;
-    return f;
+    const float t = top < kSmall ? top * kRaise : top;
+    return {t, top > 0.0f ? __fdiv_rn(448.0f, t) : 0.0f};
+}
+template <typename T, int W>
+__device__ __forceinline__ void raise(Vec<T, W> &r)
+{
+#pragma unroll
+    for (int e = 0; e < W; ++e) r.v[e] = from_f<T>(to_f(r.v[e]) * kRaise);
 }
 
 __device__ __forceinline__ float near21(float q) { return as_f((as_u(q) + 4u) & ~7u); }
@@ -49,7 +53,7 @@ __device__ __forceinline__ uint32_t places(float q)
 // q moved off the border that it is close to, to its side of it (or onto it, where the quotient lies on it).
 __device__ __noinline__ float decided(float x, float q, Factor f)
 {
-    const float p = fabsf(q), z = fabsf(x) * f.lift, y = p < 0.015625f ? p + 0.015625f : p;
+    const float p = fabsf(q), z = fabsf(x), y = p < 0.015625f ? p + 0.015625f : p;
     const float edge = as_f((as_u(y) & 0xFFF00000u) | 0x80000u), m = p < 0.015625f ? edge - 0.015625f : edge;
     const double a = (double)z * 448.0, b = (double)m * (double)f.top;
     return copysignf(a > b ? m * (1.0f + 0x1p-18f) : a < b ? m * (1.0f - 0x1p-18f) : m, x);
@@ -92,6 +96,20 @@ __device__ __forceinline__ float joined(uint32_t top, int lanes)
     }
 }
 
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <typename T, int W>
 __device__ __forceinline__ void put_codes(uint8_t *p, bool ok, const Vec<T, W> &r, const Factor &f, bool finite)
 {
@@ -99,8 +117,13 @@ __device__ __forceinline__ void put_codes(uint8_t *p, bool ok, const Vec<T, W> &
     widen(r, v);
     uint32_t close = ~0u;
 #pragma unroll
+    for (int e = 0; e + 1 < W; e += 2) {
+        const uint64_t p = mul2(pack2(v[e], v[e + 1]), pack2(f.by, f.by));
+        unpack2(p, q[e], q[e + 1]);
+    }
+    if constexpr (W == 1) q[0] = v[0] * f.by;
+#pragma unroll
     for (int e = 0; e < W; ++e) {
-        q[e] = v[e] * f.lift * f.by;
         if constexpr (sizeof(T) == 2)
             q[e] = near21(q[e]);
         else
@@ -179,7 +202,10 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows(const QuantArgs a)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const bool live = row[u] >= 0;
-        const Factor f = {tops[u] * lift_of(tops[u]), __shfl_sync(0xffffffffu, own.by, u, L), lift_of(tops[u])};
+        const Factor f = {tops[u] < kSmall ? tops[u] * kRaise : tops[u], __shfl_sync(0xffffffffu, own.by, u, L)};
+        if (tops[u] < kSmall)
+#pragma unroll
+            for (int p = 0; p < P; ++p) raise(raw[u][p]);
         if (live && lane == u) a.scales[(int64_t)row[u] * a.cols + col[u] / 128] = scale;
 #pragma unroll
         for (int p = 0; p < P; ++p)
@@ -190,7 +216,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows(const QuantArgs a)
 
 // A block of 128 by 128 values a CTA, 64 a thread.
 template <typename T, int W>
-__global__ void __launch_bounds__(kQuantThreads, W == 1 ? 2 : 3) quant_blocks(const QuantArgs a)
+__global__ void __launch_bounds__(kQuantThreads, W == 1 ? 2 : sizeof(T) == 2 ? 5 : 3) quant_blocks(const QuantArgs a)
 {
     constexpr int L = W == 1 ? 32 : 128 / W, P = W == 1 ? 4 : 1, R = kQuantThreads / L, I = 128 / R;
     __shared__ float tops[kQuantThreads / 32];
@@ -221,6 +247,11 @@ __global__ void __launch_bounds__(kQuantThreads, W == 1 ? 2 : 3) quant_blocks(co
     for (int i = 1; i < kQuantThreads / 32; ++i) top = fmaxf(top, tops[i]);
     const bool finite = top <= 3.402823466e38f;
     const Factor f = factor_of(top);
+    if (top < kSmall)
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int p = 0; p < P; ++p) raise(raw[i][p]);
     pdl_wait();
     if (threadIdx.x == 0) a.scales[blockIdx.x] = scale_of(top, finite);
 #pragma unroll

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
                 acc.next(kAccs);
             }
         } else if (k0 < k1) {
-            ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[0], 0, &s.abort, a.status));
+            ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[0], 0, &s.abort, a.status, k1 - k0));
             acc_fence_after();
         }
     }

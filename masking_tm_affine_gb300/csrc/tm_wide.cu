@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
             O *const first = out + ((MODE == kWeights ? (int64_t)w.e * a.C : 0) + w.c0) * a.ldo + r;
             bool ok = true;
             auto ready = [&] {
-                ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status));
+                ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status, SUMS ? 0 : w.steps));
                 acc_fence_after();
                 return ok;
             };

@@ -109,6 +109,10 @@ def test_nothing_and_zeros(cuda):
     c.run(1.0, 0.0)     # max_norm / 0: no clipping
     tm.tm_check()
     assert float(c.norm) == 0.0 and not c.outs[0][:5000].any()
+    c = Clip([torch.zeros(70, device="cuda")])
+    c.run(0.0, 0.0)     # 0 / 0
+    tm.tm_check()
+    assert float(c.norm) == 0.0 and not c.outs[0][:70].any()
     c = Clip(tensors([5000], ["f32"]))
     c.run(0.0)
     tm.tm_check()

@@ -176,8 +176,10 @@ def test_empty_extents(cuda):
         dx, dw = torch.full((T, 40), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((80, 24), 7.0, device="cuda")
         tm.tm_gemm_experts_bwd(None, 0, None, 0, None, 40, dx, 40, None, 0, st, 2, T, 0, 40)
         tm.tm_gemm_experts_bwd(None, 40, None, 24, None, 24, None, 0, dw, 24, ref.starts_of([0, 0]), 2, 0, 40, 24, 2, 0)
+        one = torch.full((80, 24), 7.0, dtype=torch.bfloat16, device="cuda")
+        tm.tm_gemm_experts_bwd(None, 80, None, 24, None, 24, None, 0, one, 24, None, 1, 0, 80, 24)
         tm.tm_check()
-        assert not y.any() and not dx.any() and not dw.any()
+        assert not y.any() and not dx.any() and not dw.any() and not one.any()
 
 
 def test_borders_out_of_range(cuda):

@@ -140,6 +140,50 @@ def test_two_graphs_of_one_expert_list_at_once(cuda):
         assert all(torch.equal(o[i], plain[i]) for i in (1, 6, 7))
 
 
+FIRST = """
+import sys, torch
+sys.path.insert(0, %r)
+from masking_tm_affine_gb300 import tm
+T, N, K, E = %d, 136, 264, 2
+x, w = torch.randint(-3, 4, (T, K)).bfloat16().cuda(), torch.randint(-3, 4, (E, N, K)).bfloat16().cuda()
+y, dx = torch.zeros(T, N, device="cuda"), torch.zeros(T, K, device="cuda").bfloat16()
+dw, q, sc = torch.zeros(E, N, K, device="cuda"), torch.zeros(T, 272, dtype=torch.uint8, device="cuda"), torch.zeros(T, 3, device="cuda")
+b, sb, z = torch.full((N, 272), 0x38, dtype=torch.uint8, device="cuda"), torch.ones(2, 3, device="cuda"), torch.zeros(T, N, device="cuda")
+st = torch.tensor([0, T // 3, T], dtype=torch.int32, device="cuda")
+norm, ws = torch.zeros(1, device="cuda"), torch.zeros(tm.tm_clip_workspace_bytes(), dtype=torch.uint8, device="cuda")
+plan = tm.tm_clip_plan([x], None, [T * K], [2]).cuda()
+torch.cuda.synchronize()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(g, stream=s):
+    tm.tm_gemm_experts(x, K, w, K, y, N, st, E, T, N, K, 2, 0)
+    tm.tm_gemm_experts_bwd(x, K, x, K, w.view(E, K, N), N, dx, N, None, 0, st, E, T, K, N)
+    tm.tm_gemm_experts_bwd(w.view(-1)[:T * N], N, x, K, None, 0, None, 0, dw, K, st, E, T, N, K, 2, 0)
+    tm.tm_quant_e4m3(x, K, T, K, q, 272, sc, 1, 2)
+    tm.tm_gemm_e4m3(q, 272, sc, 128, b, 272, sb, z, N, None, 1, T, N, K)
+    tm.tm_clip_grads(plan, tm.tm_clip_chunks([T * K]), 1.0, 0.0, norm, ws, ws.numel())
+g.replay()
+tm.tm_check(s)
+torch.cuda.synchronize()
+for e, at in ((0, slice(0, T // 3)), (1, slice(T // 3, T))):
+    assert torch.equal(y[at].double(), x[at].double() @ w[e].double().T)
+v = q[:, :K].view(torch.float8_e4m3fn).double() * sc.double().repeat_interleave(128, 1)[:, :K]
+assert float((z.double() - v.sum(1, keepdim=True)).abs().max()) <= 2.0 ** -10 * float(v.abs().sum(1).max())
+assert abs(float(norm) - float(x.double().norm())) <= 2.0 ** -19 * float(norm) and dx.any() and dw.any()
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("T", [40, 900])
+def test_a_process_whose_first_calls_are_captured(cuda, T):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    # (w has room for the T rows of the weights' gradient: E * N * K elements)
+    r = subprocess.run([sys.executable, "-c", FIRST % (root, min(T, 2 * 264))], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
 # ------------------------------------------------------------------ experts
 @pytest.mark.parametrize("E,per", [(1024, 1), (1000, 3), (300, 70), (257, 40)])
 def test_many_experts(cuda, E, per):
