@@ -53,7 +53,7 @@ bool panels_map(CUtensorMap *m, const void *p, int64_t inner, int64_t rows, int6
 
 namespace {
 
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 10;
 constexpr uint32_t kTall = 128 * 128;  // bytes of weights a stage
 
 struct ThinArgs {
@@ -64,6 +64,7 @@ struct ThinArgs {
     unsigned *status;
     int otype, E, T, F, ftiles;
     int steps;   // stages a tile: 128 bytes of the sum each
+    int stages;  // of the ring
     int group;
     uint32_t id;  // the instruction without its N
 };
@@ -77,7 +78,9 @@ struct Thin {
     // Three CTAs an SM with tiles of 32 rows, two with 128, stages of 20 and 32 KB; one where 64 sums a
     // thread take its registers.
     static constexpr int kCtas = BT <= 32 ? 3 : SUMS ? 1 : 2;
-    static constexpr int kStages = kCtas == 1 ? 6 : 3;
+    // Stages of the ring, by how many CTAs an SM there are: a tile alone there has all of the memory (16 rows
+    // by 2048 x 8192 in 16 bits, cold: 18.5 us with 3 stages, 16.0 with 10; 4096 x 4096 14.1 and 13.4)
+    static constexpr int stages(int ctas) { return BT <= 32 ? (ctas <= 1 ? 10 : ctas == 2 ? 5 : 3) : ctas <= 1 || kCtas == 1 ? 6 : 3; }
     static constexpr int kRun = F8 ? 1 : kRunSums / 64;  // stages a run
     // accumulators: one of a tile, or several that take turns over its runs
     static constexpr int kAccs = !SUMS ? 1 : BT <= 32 ? 4 : 2;
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
 {
     constexpr uint32_t kStage = kTall + BT * 128;
     using F = Thin<F8, SUMS, BT>;
-    constexpr uint32_t kStagesT = (uint32_t)F::kStages;
+    const uint32_t stages = (uint32_t)a.stages;
     constexpr int kStep = F8 ? 128 : 64;  // elements of the sum a stage
     constexpr int kAccs = F::kAccs, kRun = F::kRun, CW = F::kCols;
     // weights are read once, or by a few tiles at about the same time: they are the first L2 gives up, not
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
     // with S > 1: [S][4 warps][BT / S / 4][32 lanes][4 rows] partial sums of the rows this CTA owns, in
     // the ring's place once every CTA of the cluster is done with its own
     float *inbox = reinterpret_cast<float *>(ring);
-    static_assert(BT * 128 * 4 <= kStagesT * kStage, "inbox");
+    static_assert(BT * 128 * 4 <= 3 * kStage, "inbox");
     __shared__ ThinSmem<F8, SUMS, BT> s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_rank() : 0;
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
     if (threadIdx.x == 0) {
         tensormap_prefetch(&mw);
         tensormap_prefetch(&mx);
-        for (int i = 0; i < (int)kStagesT; ++i) {
+        for (int i = 0; i < a.stages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
         }
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
             Turn t;
             uint32_t used = 0;
             for (int k = k0; k < k1; ++k) {
-                if (used >= kStagesT && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) break;
+                if (used >= stages && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) break;
                 const uint32_t bar = smem_u32(&s.full[t.slot]), at = smem_u32(ring) + t.slot * kStage;
                 if (elect()) {
                     mbar_expect(&s.full[t.slot], kTall + boxes * 4096u);
@@ -235,11 +238,11 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
                 }
                 __syncwarp();
                 ++used;
-                t.next(kStagesT);
+                t.next(stages);
             }
             // nothing may still be landing when the CTA leaves: the last filling of each slot
-            for (uint32_t i = 0; i < kStagesT && i < used; ++i)
-                mbar_wait_bounded(smem_u32(&s.full[i]), ((used - i + kStagesT - 1) / kStagesT - 1) & 1u);
+            for (uint32_t i = 0; i < stages && i < used; ++i)
+                mbar_wait_bounded(smem_u32(&s.full[i]), ((used - i + stages - 1) / stages - 1) & 1u);
         }
     } else if (warp == 1) {
         if (n > 0) {
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
                     if (end) umma_done<false>(&s.acc_full[acc.slot]);
                 }
                 __syncwarp();
-                t.next(kStagesT);
+                t.next(stages);
                 if (end) {
                     acc.next(kAccs);
                     in_run = 0;
@@ -421,8 +424,10 @@ template <bool F8, bool SUMS, bool MN, int BT>
 tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
 {
     using F = Thin<F8, SUMS, BT>;
-    constexpr size_t kRing = F::kStages * (kTall + BT * 128) + 1024;
-    static_assert(F::kCtas * (kRing + sizeof(ThinSmem<F8, SUMS, BT>) + 1024) <= 228 * 1024, "shared memory");
+    constexpr size_t kStage = kTall + BT * 128;
+    static_assert(F::stages(1) * kStage + 1024 + sizeof(ThinSmem<F8, SUMS, BT>) <= 227 * 1024 && F::stages(1) <= kMaxStages, "shared memory");
+    static_assert(F::kCtas == 1 || F::kCtas * (F::stages(F::kCtas) * kStage + sizeof(ThinSmem<F8, SUMS, BT>) + 2048) <= 228 * 1024,
+                  "shared memory");
     static_assert(F::kCtas * F::kAccs * BT <= 512, "tensor memory");
     const void *k = (const void *)thin_kernel<F8, SUMS, MN, BT>;
     static std::once_flag once[kMaxDevices];
@@ -430,7 +435,8 @@ tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return TM_ERR_CUDA;
     std::call_once(once[d], [&] {
-        good[d] = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRing) == cudaSuccess;
+        good[d] = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(F::stages(1) * kStage + 1024)) == cudaSuccess;
         if (!good[d]) cudaGetLastError();
     });
     if (!good[d]) return TM_ERR_CUDA;
@@ -457,12 +463,13 @@ tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool
     // 21.5 us, 2 18.6, 4 15.0, 8 14.8; 128 rows: 35.8, 35.6, 25.0, 47.6
     int S = 1;
     while (S < 4 && tiles * S <= (int64_t)dev.sms && a.steps >= 4 * S) S *= 2;
+    a.stages = F::stages((int)(most * S > 3 * (int64_t)dev.sms ? 3 : (most * S + dev.sms - 1) / dev.sms));
     CUtensorMap mw, mx, mx_all;
     if (!rows_map(&mw, p.kind, p.w, MN ? p.F : p.R, MN ? p.R : p.F, p.ldw, p.E, MN ? 64 : 128) ||
         !rows_map(&mx, p.kind, p.x, p.R, p.T, p.ldx, 0, 32) || !rows_map(&mx_all, p.kind, p.x, p.R, p.T, p.ldx, 0, BT))
         return TM_ERR_CUDA;
     void *args[] = {&mw, &mx, &mx_all, &a, &S};
-    return launch_kernel(k, dim3((unsigned)(most * S)), dim3(F::kThreads), args, kRing, s, pdl, (unsigned)S);
+    return launch_kernel(k, dim3((unsigned)(most * S)), dim3(F::kThreads), args, a.stages * kStage + 1024, s, pdl, (unsigned)S);
 }
 
 }  // namespace
