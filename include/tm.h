@@ -66,7 +66,7 @@ typedef enum tm_status {
     TM_ERR_CUDA = 5,             /* a CUDA runtime call or kernel launch failed */
     TM_ERR_WORKSPACE = 6,        /* workspace NULL, too small or misaligned (colsum: 16 bytes, gemm: 1024) */
     TM_ERR_TIMEOUT = 7,          /* a bounded device-side wait gave up (reported by tm_check) */
-    TM_ERR_INDEX = 8             /* a page, slot or length read on the device is out of range (reported by tm_check) */
+    TM_ERR_INDEX = 8             /* a page, slot, length or expert's border read on the device is out of range (reported by tm_check) */
 } tm_status;
 
 /* A cudaStream_t, passed as an opaque pointer; NULL = legacy default stream. */
@@ -643,6 +643,7 @@ tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_head, void 
  * of whole 16 bytes (tm_row_stride; any extents): MISALIGNED otherwise.  Outputs need
  * only their element's alignment.  Sums are fp32; an output is rounded once.  A row's
  * infinities and NaNs reach its own outputs and no others.
+ * Flags: TM_PDL.
  *
  * tm_quant_e4m3 -- 8-bit floats with a scale for each run of 128 columns of `rows` rows
  * (1: as tm_rmsnorm writes with group 128; 128: square blocks, for weights):
@@ -741,7 +742,7 @@ tm_status tm_clip_grads(const void *plan, int64_t chunks, float max_norm, float 
  * word.  Returns TM_ERR_BROKEN_PROMISE if a kernel's entry check found the
  * aligned promise broken (that kernel stored nothing), TM_ERR_MISALIGNED if it
  * found a misaligned pointer or ld, TM_ERR_TIMEOUT if a bounded wait gave up,
- * TM_ERR_INDEX if a kernel met a page, slot or length out of range,
+ * TM_ERR_INDEX if a kernel met a page, slot, length or expert's border out of range,
  * TM_ERR_CUDA if the stream reports a CUDA error, else TM_OK.
  */
 tm_status tm_check(tm_stream_t stream);
