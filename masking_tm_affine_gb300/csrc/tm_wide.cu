@@ -56,6 +56,7 @@ struct WideArgs {
     int otype, E, T;
     int R, C;    // extents of r, and of c where c is not an expert's rows
     int rtiles, ctiles;  // of 256 (ctiles: weights' gradient)
+    FastDiv by_block, by_expert;  // kGroup * rtiles; rtiles * ctiles
     int steps;   // stages a tile (not of the weights' gradient)
     int tall_panels, wide_panels;  // MN-major operands whose two panels come in one copy
     uint32_t id;
@@ -87,7 +88,7 @@ struct Walk {
         int cts, local;
         if constexpr (MODE == kWeights) {
             const int per = a.rtiles * a.ctiles;
-            e = item / per;
+            e = (int)fdiv((uint32_t)item, a.by_expert);
             local = item - e * per;
             cts = a.ctiles;
         } else {
@@ -96,11 +97,11 @@ struct Walk {
             local = item - x.before[e] * a.rtiles;
         }
         // blocks of kGroup tiles of c; within one, c is the faster
-        const int block = local / (kGroup * a.rtiles), in = local - block * kGroup * a.rtiles;
+        const int block = (int)fdiv((uint32_t)local, a.by_block), in = local - block * kGroup * a.rtiles;
         const int wide = cts - block * kGroup < kGroup ? cts - block * kGroup : kGroup;
-        const int ct = block * kGroup + in % wide;
+        const int rt = wide == kGroup ? in / kGroup : in / wide, ct = block * kGroup + in - rt * wide;
         t.e = e;
-        t.r0 = in / wide * 256;
+        t.r0 = rt * 256;
         if constexpr (MODE == kWeights) {
             t.c0 = ct * 256;
             t.n = a.C - t.c0 < 256 ? a.C - t.c0 : 256;
@@ -411,19 +412,30 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                 if (w.steps > 0 && !ready()) break;
                 if (!waited) pdl_wait();
                 waited = true;
+                if (w.steps > 0) {
+                    // the next run on its way while one is stored
+                    const uint32_t at = lanes + acc.slot * 256;
+                    float v0[32], v1[32];
+                    acc_load32(at + 32 * odd, v0);
 #pragma unroll 1
-                for (int c0 = 32 * odd; c0 < w.n; c0 += 64) {
-                    float v[32];
-                    if (w.steps > 0) {
-                        acc_load32(lanes + acc.slot * 256 + c0, v);
-                        acc_load_wait(v);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+                    for (int c0 = 32 * odd; c0 < w.n; c0 += 128) {
+                        acc_load_wait(v0);
+                        if (c0 + 64 < w.n) acc_load32(at + c0 + 64, v1);
+                        store(v0, c0);
+                        if (c0 + 64 >= w.n) break;
+                        acc_load_wait(v1);
+                        if (c0 + 128 < w.n) acc_load32(at + c0 + 128, v0);
+                        store(v1, c0 + 64);
                     }
-                    store(v, c0);
+                    acc_load_wait(v0);
+                    give_back();
+                } else {
+                    float v[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+#pragma unroll 1
+                    for (int c0 = 32 * odd; c0 < w.n; c0 += 64) store(v, c0);
                 }
-                if (w.steps > 0) give_back();
             }
         }
     } else {
@@ -567,6 +579,7 @@ tm_status wide_product(const Product &p, const DevInfo &dev, cudaStream_t s, boo
     a.T = (int)p.T;
     a.R = (int)p.F;
     a.rtiles = tiles256(p.F);
+    a.by_block = a.by_expert = make_fastdiv((uint32_t)(kGroup * a.rtiles));
     a.steps = (int)((p.R + 63) / 64);
     a.id = instruction(p.kind == kProductBF16 ? 1u : 0u, p.w_mn, false, 256, 0);
     a.tall_panels = p.w_mn && p.F % 64 == 0 && p.R > 0;
@@ -596,6 +609,8 @@ tm_status wide_weights(ProductKind kind, const void *dy, int64_t lddy, const voi
     a.C = (int)N;
     a.rtiles = tiles256(K);
     a.ctiles = tiles256(N);
+    a.by_block = make_fastdiv((uint32_t)(kGroup * a.rtiles));
+    a.by_expert = make_fastdiv((uint32_t)((int64_t)a.rtiles * a.ctiles < (1 << 30) ? a.rtiles * a.ctiles : 1));  // more tiles are refused
     a.id = instruction(kind == kProductBF16 ? 1u : 0u, true, true, 256, 0);
     a.tall_panels = K % 64 == 0 && T > 0;
     a.wide_panels = N % 64 == 0 && T > 0;
