@@ -199,6 +199,16 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // depends on, which keeps a chain of dependent launches in stream order.
 __device__ __forceinline__ uint32_t as_u(float f) { return __float_as_uint(f); }
 
+// ---------------------------------------------------------------- pairs
+// Two fp32 values in one register pair, for the operations that take two at a time.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+
 // ---------------------------------------------------------------- tile walk
 // The split of a loop over a runtime extent K in steps of T into whole tiles
 // (no mask) and at most one masked remainder tile ("Slicing, bounds and

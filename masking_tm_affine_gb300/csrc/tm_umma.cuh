@@ -265,15 +265,6 @@ __device__ __forceinline__ void acc_load_wait(float (&r)[32])
 __device__ __forceinline__ void acc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void acc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Pairs of fp32 values in one register pair.
-__device__ __forceinline__ uint64_t pack2(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-
 // sum += m * 32 columns of the accumulator, two columns an operation.  One statement: the
 // values pass from the read to the additions in registers that nothing else names, which
 // saves the moves that separate statements took (8192 x 8192 x 4096: 255 us, so 234).
