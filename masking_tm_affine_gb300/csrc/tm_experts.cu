@@ -47,19 +47,17 @@ const void *base_of(const void *p, int64_t elements, const void *out)
 }
 
 // Which kernel.  Tiles of 128 by 32 or 128, whose sums can be cut over a cluster, up to 32 rows an expert
-// (where the weights' bytes bound the call), or for long sums while tiles of 256 by 256 would leave most
-// SMs without work; in 8 bits such a tile of 128 rows is slower, and taken only for one of them.
+// (where the weights' bytes bound the call), or for long sums while there are so few of those tiles that four CTAs can
+// share each sum.
 //   64 experts of 2048 x 2048, 16 bits: 32 rows each 105 us either way, 64 rows 119 us thin and 107 wide
 //   64 of 2048 x 4096, 8 bits: 32 rows 109 and 129 us, 64 rows 158 and 130
-//   one of 4096 x 4096, 16 bits: 128 rows 22 and 28 us, 256 rows 27 and 29, 512 rows 31 and 29;
-//   8 bits: 128 rows 20 and 24, 256 rows 33 and 24
-//   short sums, 16 bits: 5 experts of 520 x 1000, 200 rows each: 18 and 16 us, their rows' gradient 22 and 14
+//   sums over four CTAs, one of 512 x 4096, 16 bits: 400 rows 18.5 us thin and 22.6 wide; of 256 x 8192, 8 bits,
+//   1000 rows 24.6 and 29.7; over two, of 4096 x 4096, 16 bits, 256 rows: 26.6 and 24.6
+//   short ones, 16 bits, 100 rows of 1024 x 1024: 14.3 and 12.3
 bool few_rows(const Product &p, const DevInfo &dev)
 {
     if (p.T <= 32 * (int64_t)p.E) return true;
-    const int64_t busy = p.E < p.T ? p.E : p.T, rows = (p.T + 255) / 256, tiles = (rows > busy ? rows : busy) * ((p.F + 255) / 256);
-    const bool f8 = p.kind == kProductE4M3;
-    return tiles * 6 <= dev.sms && p.R >= 32 * (f8 ? 128 : 64) && (!f8 || p.T <= 128 * (int64_t)p.E);
+    return tiles_of(p, 128) * ((p.F + 127) / 128) * 4 <= dev.sms && p.R >= 2048;
 }
 
 }  // namespace

@@ -27,6 +27,9 @@ struct Product {
     int32_t group;
 };
 
+// Row tiles to expect: the experts' borders, which are not known here, cut half a tile each.
+inline int64_t tiles_of(const Product &p, int rows) { return (p.T + rows - 1) / rows + (p.E < p.T ? p.E : p.T) / 2; }
+
 // A map of rows of `inner` elements of e bytes in boxes 128 bytes wide and `box` rows high, 128-byte
 // swizzle, zeros outside; with E > 0 of E matrices of `rows` rows.
 bool rows_map_of(CUtensorMap *m, int e, const void *p, int64_t inner, int64_t rows, int64_t ld, int64_t E, int box);

@@ -55,7 +55,8 @@ struct WideArgs {
     unsigned *status;
     int otype, E, T;
     int R, C;    // extents of r, and of c where c is not an expert's rows
-    int rtiles, ctiles;  // of 256 (ctiles: weights' gradient)
+    int rtiles, ctiles;  // of 256 of r, of `width` of c (ctiles: weights' gradient)
+    int width;           // of a tile along c: 256, 128 or 64
     FastDiv by_block, by_expert;  // kGroup * rtiles; rtiles * ctiles
     int steps;   // stages a tile (not of the weights' gradient)
     int tall_panels, wide_panels;  // MN-major operands whose two panels come in one copy
@@ -103,15 +104,15 @@ struct Walk {
         t.e = e;
         t.r0 = rt * 256;
         if constexpr (MODE == kWeights) {
-            t.c0 = ct * 256;
-            t.n = a.C - t.c0 < 256 ? a.C - t.c0 : 256;
+            t.c0 = ct * a.width;
+            t.n = a.C - t.c0 < a.width ? a.C - t.c0 : a.width;
             t.s0 = x.first[e];
             t.steps = (x.count[e] + 63) / 64;
             t.last = x.count[e] - (t.steps - 1) * 64;
         } else {
-            const int left = x.count[e] - ct * 256;
-            t.c0 = x.first[e] + ct * 256;
-            t.n = left < 256 ? left : 256;
+            const int left = x.count[e] - ct * a.width;
+            t.c0 = x.first[e] + ct * a.width;
+            t.n = left < a.width ? left : a.width;
             t.s0 = 0;
             t.steps = a.steps;
             t.last = 64;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s.abort = 0;
     }
-    experts_read(s.x, a.starts, a.E, a.T, 256, a.status);
+    experts_read(s.x, a.starts, a.E, a.T, a.width, a.status);
     acc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist
@@ -179,8 +180,8 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                 const Tile w = walk.at(item);
                 const int r = w.r0 + (int)rank * 128;
                 // the wide operand's share of this CTA: half of the product's extent
-                const int half = B_MN ? 128 : (w.n + 63) / 64 * 32, c = w.c0 + (int)rank * half;
-                const uint32_t bytes = kHalf + (B_MN ? kHalf : (uint32_t)half * 128u);
+                const int half = B_MN ? a.width / 2 : (w.n + 63) / 64 * 32, c = w.c0 + (int)rank * half;
+                const uint32_t bytes = kHalf + (uint32_t)half * 128u;
                 for (int k = w.kb; k < w.ke; ++k) {
                     if (used >= kStages && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
                         ok = false;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                             if (a.wide_panels)
                                 tma_load_4d(at + kHalf, &mwide, 0, k0, c / 64, 0, bar);
                             else
-                                for (int p = 0; p < 2; ++p) tma_load_2d(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
+                                for (int p = 0; p < half / 64; ++p) tma_load_2d(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
                         }
                     } else {
                         const uint32_t bar = cluster_addr(smem_u32(&s.full[t.slot]), even);
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                             if (a.wide_panels)
                                 tma_load_4d_pair(at + kHalf, &mwide, 0, k0, c / 64, 0, bar);
                             else
-                                for (int p = 0; p < 2; ++p) tma_load_2d_pair(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
+                                for (int p = 0; p < half / 64; ++p) tma_load_2d_pair(at + kHalf + p * kPanel, &mwide, c + 64 * p, k0, bar);
                         } else {
                             if constexpr (A_MN) {
                                 if (a.tall_panels)
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                             } else {
                                 tma_load_3d_pair(at, &mtall, k0, r, w.e, bar);
                             }
-                            if (half == 128)
+                            if (half == a.width / 2)
                                 tma_load_2d_pair(at + kHalf, &mwide_all, k0, c, bar);
                             else
                                 for (int b = 0; b < half; b += 32)
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
             bool ok = true;
             for (int item = unit; ok && item < items; item += units) {
                 const Tile w = walk.at(item);
-                const uint32_t id = a.id | ((B_MN ? 256u : (uint32_t)((w.n + 63) / 64 * 64)) >> 3) << 17;
+                const uint32_t id = a.id | ((B_MN ? (uint32_t)a.width : (uint32_t)((w.n + 63) / 64 * 64)) >> 3) << 17;
                 for (int k = w.kb; ok && k < w.ke;) {
                     // a run of the sum into the next accumulator: all of it, or kRun stages
                     const int end = SUMS && w.ke - k > kRun ? k + kRun : w.ke;
@@ -374,7 +375,8 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                 const uint64_t one = pack2(1.0f, 1.0f);
                 for (int k = w.kb; k < w.ke && ready(); k += kRun) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) add_columns(lanes + acc.slot * 256 + 32 * odd + 64 * i, sum + 16 * i, one);
+                    for (int i = 0; i < 4; ++i)
+                        if (64 * i < a.width) add_columns(lanes + acc.slot * 256 + 32 * odd + 64 * i, sum + 16 * i, one);
                     give_back();
                 }
                 if constexpr (SPLIT) {
@@ -565,6 +567,17 @@ tm_status launch_typed(const CUtensorMap &tall, const CUtensorMap &wide, const C
 
 int tiles256(int64_t n) { return (int)((n + 255) / 256); }
 
+// The width of a tile along c: 128 or 64 where all such tiles run at once, on SMs that would have nothing to do; more
+// of them would only read more.  16 bits, cold: 5 experts of 520 x 1000, 200 rows each, forward 16.4 us with 256 and 14.3 with
+// 128; 512 x 512, 1000 rows, 12.3 and with 64 10.7.
+template <typename F>
+int width_of(F tiles, int least, const DevInfo &dev)
+{
+    int w = 256;
+    while (w > least && tiles(w / 2) <= dev.sms / 2) w /= 2;
+    return w;
+}
+
 }  // namespace
 
 tm_status wide_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
@@ -579,6 +592,9 @@ tm_status wide_product(const Product &p, const DevInfo &dev, cudaStream_t s, boo
     a.T = (int)p.T;
     a.R = (int)p.F;
     a.rtiles = tiles256(p.F);
+    const int64_t busy = p.E < p.T ? p.E : p.T;
+    auto tiles = [&](int w) { return ((p.T + w - 1) / w + busy) * a.rtiles; };
+    a.width = width_of([&](int w) { return tiles_of(p, w) * a.rtiles; }, 64, dev);
     a.by_block = a.by_expert = make_fastdiv((uint32_t)(kGroup * a.rtiles));
     a.steps = (int)((p.R + 63) / 64);
     a.id = instruction(p.kind == kProductBF16 ? 1u : 0u, p.w_mn, false, 256, 0);
@@ -587,10 +603,9 @@ tm_status wide_product(const Product &p, const DevInfo &dev, cudaStream_t s, boo
     if (a.tall_panels ? !panels_map(&tall, p.w, p.F, p.R, p.ldw, p.E)
                       : !rows_map(&tall, p.kind, p.w, p.w_mn ? p.F : p.R, p.w_mn ? p.R : p.F, p.ldw, p.E, p.w_mn ? 64 : 128))
         return TM_ERR_CUDA;
-    if (!rows_map(&wide, p.kind, p.x, p.R, p.T, p.ldx, 0, 32) || !rows_map(&all, p.kind, p.x, p.R, p.T, p.ldx, 0, 128)) return TM_ERR_CUDA;
-    const int64_t busy = p.E < p.T ? p.E : p.T, items = ((p.T + 255) / 256 + busy) * a.rtiles;
-    return p.w_mn ? launch_typed<kRows>(tall, wide, all, a, items, a.steps, dev, s, pdl)
-                  : launch_typed<kForward>(tall, wide, all, a, items, a.steps, dev, s, pdl);
+    if (!rows_map(&wide, p.kind, p.x, p.R, p.T, p.ldx, 0, 32) || !rows_map(&all, p.kind, p.x, p.R, p.T, p.ldx, 0, a.width / 2)) return TM_ERR_CUDA;
+    return p.w_mn ? launch_typed<kRows>(tall, wide, all, a, tiles(a.width), a.steps, dev, s, pdl)
+                  : launch_typed<kForward>(tall, wide, all, a, tiles(a.width), a.steps, dev, s, pdl);
 }
 
 tm_status wide_weights(ProductKind kind, const void *dy, int64_t lddy, const void *x, int64_t ldx, void *dw, int64_t lddw,
@@ -608,12 +623,14 @@ tm_status wide_weights(ProductKind kind, const void *dy, int64_t lddy, const voi
     a.R = (int)K;
     a.C = (int)N;
     a.rtiles = tiles256(K);
-    a.ctiles = tiles256(N);
+    // long sums are shared by pairs instead (one of 1024 x 512, 3000 rows: 20.8 us, narrow 24.6)
+    a.width = T / 64 / E >= 32 ? 256 : width_of([&](int w) { return (int64_t)E * a.rtiles * ((N + w - 1) / w); }, 128, dev);
+    a.ctiles = (int)((N + a.width - 1) / a.width);
     a.by_block = make_fastdiv((uint32_t)(kGroup * a.rtiles));
     a.by_expert = make_fastdiv((uint32_t)((int64_t)a.rtiles * a.ctiles < (1 << 30) ? a.rtiles * a.ctiles : 1));  // more tiles are refused
     a.id = instruction(kind == kProductBF16 ? 1u : 0u, true, true, 256, 0);
     a.tall_panels = K % 64 == 0 && T > 0;
-    a.wide_panels = N % 64 == 0 && T > 0;
+    a.wide_panels = N % 64 == 0 && T > 0 && a.width == 256;  // two panels a CTA
     CUtensorMap tall, wide;
     if (a.tall_panels ? !panels_map(&tall, x, K, T, ldx, 0) : !rows_map(&tall, kind, x, K, T, ldx, 0, 64)) return TM_ERR_CUDA;
     if (a.wide_panels ? !panels_map(&wide, dy, N, T, lddy, 0) : !rows_map(&wide, kind, dy, N, T, lddy, 0, 64)) return TM_ERR_CUDA;

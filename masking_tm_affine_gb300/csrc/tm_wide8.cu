@@ -2,7 +2,7 @@
 //
 //   c[t, n] = sum_b sa[t, b] sb[n / 128, b] * sum_{k in b} a[t, k] b[n, k]
 //
-// A CTA pair takes a tile of 256 rows t by 256 columns n; a stage of the ring is one block of
+// A CTA pair takes a tile of 256 rows t by 256 columns n (128 where that leaves SMs without a tile); a stage of the ring is one block of
 // 128 of the sum, 16 KB of each operand a CTA.  Rows lie along the tensor memory's lanes
 // here: then a block's two scales are one factor a thread (its row's, times that of the 128
 // columns the thread holds), and adding a block is one packed fp32 operation for two
@@ -53,6 +53,7 @@ struct Tile8 {
     int e, row, n, n0;  // expert, first row and how many, first column
 };
 
+template <int NT>
 struct Walk8 {
     const Wide8Args &a;
     const Experts &x;
@@ -65,7 +66,7 @@ struct Walk8 {
         const int block = local / (kGroup8 * a.ntiles), in = local - block * kGroup8 * a.ntiles;
         const int wide = tiles - block * kGroup8 < kGroup8 ? tiles - block * kGroup8 : kGroup8;
         const int r = (block * kGroup8 + in % wide) * 256, left = x.count[e] - r;
-        return {e, x.first[e] + r, left < 256 ? left : 256, in / wide * 256};
+        return {e, x.first[e] + r, left < 256 ? left : 256, in / wide * NT};
     }
 };
 
@@ -84,7 +85,8 @@ __device__ __noinline__ void rows_out(const unsigned char *staged, void *out, in
         }
 }
 
-template <typename O>
+// NT: columns of a tile, 256 or 128.
+template <typename O, int NT>
 __global__ void __launch_bounds__(kThreads8, 1)
     wide8_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const __grid_constant__ CUtensorMap mc, const Wide8Args a)
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     pdl_trigger();  // only now: a dependent's CTA could take the tensor memory that this one waits for
     const uint32_t tmem = s.tmem;
     const int items = s.x.before[a.E] * a.ntiles;
-    Walk8 walk(a, s.x);
+    Walk8<NT> walk(a, s.x);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             bool ok = true;
             for (int item = unit; ok && item < items; item += units) {
                 const Tile8 w = walk.at(item);
-                const int row = w.row + (int)rank * 128, n = w.n0 + (int)rank * 128;
+                const int row = w.row + (int)rank * 128, n = w.n0 + (int)rank * (NT / 2);
                 for (int k = 0; k < a.steps; ++k) {
                     if (used >= kStages8 && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
                         ok = false;
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                     const uint32_t at = smem_u32(ring) + t.slot * kStage8, bar = cluster_addr(smem_u32(&s.full[t.slot]), 0);
                     if (elect()) {
-                        mbar_expect_cluster(bar, kStage8);
+                        mbar_expect_cluster(bar, kHalf8 + NT / 2 * 128);
                         tma_load_2d_pair(at, &ma, k * 128, row, bar);
                         tma_load_3d_pair(at + kHalf8, &mb, k * 128, n, w.e, bar);
                     }
@@ -183,8 +185,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
-        const int q = warp & 3, half = (warp - 4) >> 2;  // lanes 32 q .., columns 128 half ..
-        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)half * 128;
+        constexpr int CW = NT / 2;  // columns of a warp
+        const int q = warp & 3, half = (warp - 4) >> 2;  // lanes 32 q .., columns CW half ..
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * CW);
         const uint32_t free0 = cluster_addr(smem_u32(&s.acc_empty[0]), 0), free1 = cluster_addr(smem_u32(&s.acc_empty[1]), 0);
         unsigned char *mine = outs + (warp - 4) * kOutWarp;
         const int NB = (a.N + 127) / 128;
@@ -195,12 +198,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const int r = (int)rank * 128 + q * 32 + lane;  // of the tile
             const bool live = r < w.n;
             const int64_t row = (int64_t)w.row + r;
-            const int n = w.n0 + half * 128;
+            const int n = w.n0 + half * CW;
             const float *sa = a.sa + (live ? (a.group ? row * a.steps : row) : 0);
             const float *sb = a.sb + ((int64_t)w.e * NB + (n < a.N ? n / 128 : 0)) * a.steps;
-            uint64_t sum[64];
+            uint64_t sum[CW / 2];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) sum[i] = 0;
+            for (int i = 0; i < CW / 2; ++i) sum[i] = 0;
             // the next block's factors are on their way while this one is added
             float fa = a.steps > 0 ? __ldg(sa) : 0.0f, fb = a.steps > 0 ? __ldg(sb) : 0.0f;
             for (int k = 0; k < a.steps; ++k) {
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 acc_fence_after();
                 const uint32_t at = lanes + acc.slot * 256;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) add_columns(at + 32 * c, sum + 16 * c, m);
+                for (int c = 0; c < CW / 32; ++c) add_columns(at + 32 * c, sum + 16 * c, m);
                 acc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(acc.slot ? free1 : free0);
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     __syncwarp();
                     if (lane == 0) {
 #pragma unroll
-                        for (int p = 0; p < 2; ++p)
+                        for (int p = 0; p < (CW * e > 128 ? 2 : 1); ++p)
                             if (first + p * (128 / e) < a.N)
                                 asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&mc),
                                              "r"(first + p * (128 / e)), "r"(row0), "r"(smem_u32(mine) + (uint32_t)p * (kOutWarp / 2))
@@ -258,13 +261,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 }
                 __syncwarp();
                 rows_out<sizeof(O)>(mine, reinterpret_cast<O *>(a.out) + (int64_t)row0 * a.ldo + first, a.ldo, rows < 32 ? rows : 32,
-                                    a.N - first);
+                                    a.N - first < CW ? a.N - first : CW);
                 __syncwarp();
             };
             if (rows <= 0) continue;
             if constexpr (sizeof(O) == 4) {
 #pragma unroll
-                for (int half64 = 0; half64 < 2; ++half64) {
+                for (int half64 = 0; half64 < CW / 64; ++half64) {
                     if (n + 64 * half64 >= a.N) break;
                     room();
 #pragma unroll
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             } else {
                 room();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < CW / 8; ++i) {
                     uint32_t u[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -312,11 +315,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
 constexpr size_t kWide8Smem = kStages8 * kStage8 + 8 * kOutWarp + 1024;
 
-template <typename O>
-tm_status launch_wide8(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const Wide8Args &a, int64_t units,
+template <typename O, int NT>
+tm_status launch_wide8_as(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const Wide8Args &a, int64_t units,
                        cudaStream_t s, bool pdl)
 {
-    const void *k = (const void *)wide8_kernel<O>;
+    const void *k = (const void *)wide8_kernel<O, NT>;
     static std::once_flag once[kMaxDevices];
     static bool good[kMaxDevices];
     int d = 0;
@@ -329,6 +332,13 @@ tm_status launch_wide8(const CUtensorMap &ma, const CUtensorMap &mb, const CUten
     void *args[] = {const_cast<CUtensorMap *>(&ma), const_cast<CUtensorMap *>(&mb), const_cast<CUtensorMap *>(&mc),
                     const_cast<Wide8Args *>(&a)};
     return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(kThreads8), args, kWide8Smem, s, pdl, 2);
+}
+
+template <typename O>
+tm_status launch_wide8(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const Wide8Args &a, int nt, int64_t units,
+                       cudaStream_t s, bool pdl)
+{
+    return nt == 256 ? launch_wide8_as<O, 256>(ma, mb, mc, a, units, s, pdl) : launch_wide8_as<O, 128>(ma, mb, mc, a, units, s, pdl);
 }
 
 }  // namespace
@@ -345,22 +355,26 @@ tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bo
     a.E = p.E;
     a.T = (int)p.T;
     a.N = (int)p.F;
-    a.ntiles = (int)((p.F + 255) / 256);
+    const int64_t busy = p.E < p.T ? p.E : p.T, rtiles = (p.T + 255) / 256 + busy, pairs = dev.sms / 2;
+    // narrow tiles where all of them run at once, on SMs that would have nothing to do (one of 4096 x 4096, 512 rows:
+    // 24.6 us with 256 and 20.5 with 128; 1000 rows of 2048 x 7168: 34.8 and 28.7)
+    const int nt = tiles_of(p, 256) * ((p.F + 127) / 128) <= pairs ? 128 : 256;
+    a.ntiles = (int)((p.F + nt - 1) / nt);
     a.steps = (int)((p.R + 127) / 128);
     a.group = p.group;
-    a.id = instruction(0, false, false, 256, 256);
+    a.id = instruction(0, false, false, 256, (uint32_t)nt);
     // TMA clips what it stores at whole 16 bytes: N must end on them
     const int eo = elem_bytes(p.otype), grid = 16 / eo;
     a.by_copy = aligned_to(p.out, 16) && p.ldo % grid == 0 && p.F % grid == 0;
     CUtensorMap ma, mb, mc;
-    if (!rows_map(&ma, p.kind, p.x, p.R, p.T, p.ldx, 0, 128) || !rows_map(&mb, p.kind, p.w, p.R, p.F, p.ldw, p.E, 128)) return TM_ERR_CUDA;
+    if (!rows_map(&ma, p.kind, p.x, p.R, p.T, p.ldx, 0, 128) || !rows_map(&mb, p.kind, p.w, p.R, p.F, p.ldw, p.E, nt / 2)) return TM_ERR_CUDA;
     if (a.by_copy ? !rows_map_of(&mc, eo, p.out, p.F, p.T, p.ldo, 0, 32) : (mc = ma, false)) return TM_ERR_CUDA;
-    const int64_t busy = p.E < p.T ? p.E : p.T, items = ((p.T + 255) / 256 + busy) * a.ntiles, pairs = dev.sms / 2;
+    const int64_t items = rtiles * a.ntiles;
     if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
     const int64_t units = items < pairs ? items : pairs;
-    if (p.otype == TM_F32) return launch_wide8<float>(ma, mb, mc, a, units, s, pdl);
-    if (p.otype == TM_F16) return launch_wide8<__half>(ma, mb, mc, a, units, s, pdl);
-    return launch_wide8<__nv_bfloat16>(ma, mb, mc, a, units, s, pdl);
+    if (p.otype == TM_F32) return launch_wide8<float>(ma, mb, mc, a, nt, units, s, pdl);
+    if (p.otype == TM_F16) return launch_wide8<__half>(ma, mb, mc, a, nt, units, s, pdl);
+    return launch_wide8<__nv_bfloat16>(ma, mb, mc, a, nt, units, s, pdl);
 }
 
 }  // namespace libtm
