@@ -11,8 +11,10 @@
 // itself: wrong where a border between two codes lies between them.
 //   16-bit x.  x and top have at most 11 significant bits and a border 5, so x * 448 and border *
 //   top are integers below 2^17 on one scale: a quotient lies on a border or at least
-//   2^-17 of itself away.  q is rounded to 21 bits: that puts one that belongs on a border back
-//   on it, where the conversion takes the even code, and moves no other across.
+//   2^-17 of itself away.  q is made too large by 2^-21 of itself, by way of the factor (all
+//   roundings together are 3 * 2^-24 at most), and its last 4 bits, up to 2^-19, are cut: that puts
+//   one that belongs on a border back on it, where the conversion takes the even code, and moves
+//   no other across.
 //   fp32 x.  A q within 4 places of a border is decided in 64 bits: |x| * 448 against
 //   border * top, both exact there.  Few values take that way.
 #include "tm_host.h"
@@ -28,11 +30,14 @@ constexpr int kQuantThreads = 256;
 struct Factor {
     float top, by;
 };
+template <typename T>
+constexpr float kMore = sizeof(T) == 2 ? 1.0f + 0x1p-21f : 1.0f;
 constexpr float kSmall = 0x1p-100f, kRaise = 0x1p64f;
+template <typename T>
 __device__ __forceinline__ Factor factor_of(float top)
 {
     const float t = top < kSmall ? top * kRaise : top;
-    return {t, top > 0.0f ? __fdiv_rn(448.0f, t) : 0.0f};
+    return {t, top > 0.0f ? __fdiv_rn(448.0f, t) * kMore<T> : 0.0f};
 }
 template <typename T, int W>
 __device__ __forceinline__ void raise(Vec<T, W> &r)
@@ -41,7 +46,7 @@ __device__ __forceinline__ void raise(Vec<T, W> &r)
     for (int e = 0; e < W; ++e) r.v[e] = from_f<T>(to_f(r.v[e]) * kRaise);
 }
 
-__device__ __forceinline__ float near21(float q) { return as_f((as_u(q) + 4u) & ~7u); }
+__device__ __forceinline__ float cut(float q) { return as_f(as_u(q) & ~15u); }
 
 // fp32: how far q is from a border, at least; 0 .. 8 within 4 places.  Below 2^-6 codes are
 // multiples of 2^-9: 2^-6 more, and they are spaced as at 2^-6.
@@ -118,7 +123,7 @@ __device__ __forceinline__ void put_codes(uint8_t *p, bool ok, const Vec<T, W> &
 #pragma unroll
     for (int e = 0; e < W; ++e) {
         if constexpr (sizeof(T) == 2)
-            q[e] = near21(q[e]);
+            q[e] = cut(q[e]);
         else
             close = min(close, places(q[e]));
     }
@@ -157,54 +162,36 @@ struct QuantArgs {
     FastDiv by_cols;
 };
 
-// One row's runs: L lanes a run, U runs a thread, neighbours in the flat order of all runs.
-template <typename T, int W, int U>
+// One row's runs, neighbours in the flat order of all runs: 32 values a thread in four vectors, so that a
+// run's maximum takes few exchanges between lanes and its address is found once (8192 x 8192 in 16 bits 36 us, 81 % of
+// a copy's rate; 8 values a thread of four runs, 48).
+template <typename T, int W>
 __global__ void __launch_bounds__(kQuantThreads) quant_rows(const QuantArgs a)
 {
-    constexpr int L = W == 1 ? 32 : 128 / W, P = W == 1 ? 4 : 1;  // lanes a run; vectors a lane
-    constexpr int kRuns = kQuantThreads / L;
+    constexpr int L = 32 / W, P = 4;  // lanes a run; vectors a lane
     pdl_trigger();
-    const int lane = threadIdx.x % L;
-    const int first = (int)blockIdx.x * kRuns * U + (int)threadIdx.x / L;
-    Vec<T, W> raw[U][P];
-    int row[U], col[U];
+    const int lane = threadIdx.x % L, run = (int)blockIdx.x * (kQuantThreads / L) + (int)threadIdx.x / L;
+    const bool live = run < a.tasks;
+    const int row = live ? (int)fdiv((uint32_t)run, a.by_cols) : 0;
+    const int64_t col = live ? (int64_t)(run - row * a.cols) * 128 + lane * W : a.N;
+    const T *x = reinterpret_cast<const T *>(a.x) + (live ? row * a.ldx + col : 0);
+    Vec<T, W> raw[P];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int run = first + u * kRuns;
-        const bool live = run < a.tasks;
-        row[u] = live ? (int)fdiv((uint32_t)run, a.by_cols) : -1;
-        col[u] = live ? (run - row[u] * a.cols) * 128 + lane * W : 0;
+    for (int p = 0; p < P; ++p) load_vec_if(x + p * 32, col + p * 32 < a.N, raw[p]);
+    uint32_t bits = 0;
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-            load_vec_if(reinterpret_cast<const T *>(a.x) + (live ? row[u] * a.ldx + col[u] + p * 32 : 0),
-                        live && col[u] + p * 32 < a.N, raw[u][p]);
-    }
-    // two divisions a lane for its U runs together: lane u of a run's lanes takes run u's
-    float tops[U], mine = 0.0f;
+    for (int p = 0; p < P; ++p) bits = join(bits, raw[p]);
+    const float top = joined<T>(bits, L);
+    const bool finite = top <= 3.402823466e38f;
+    const Factor f = factor_of<T>(top);
+    if (top < kSmall)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int p = 0; p < P; ++p) bits = join(bits, raw[u][p]);
-        tops[u] = joined<T>(bits, L);
-        if (lane == u) mine = tops[u];
-    }
-    const Factor own = factor_of(mine);
-    const float scale = scale_of(mine, mine <= 3.402823466e38f);
+        for (int p = 0; p < P; ++p) raise(raw[p]);
     pdl_wait();
+    if (live && lane == 0) a.scales[run] = scale_of(top, finite);
+    uint8_t *y = a.y + (live ? row * a.ldy + col : 0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const bool live = row[u] >= 0;
-        const Factor f = {tops[u] < kSmall ? tops[u] * kRaise : tops[u], __shfl_sync(0xffffffffu, own.by, u, L)};
-        if (tops[u] < kSmall)
-#pragma unroll
-            for (int p = 0; p < P; ++p) raise(raw[u][p]);
-        if (live && lane == u) a.scales[(int64_t)row[u] * a.cols + col[u] / 128] = scale;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-            put_codes(a.y + (live ? row[u] * a.ldy + col[u] + p * 32 : 0), live && col[u] + p * 32 < a.N, raw[u][p], f,
-                      tops[u] <= 3.402823466e38f);
-    }
+    for (int p = 0; p < P; ++p) put_codes(y + p * 32, col + p * 32 < a.N, raw[p], f, finite);
 }
 
 // A block of 128 by 128 values a CTA, 64 a thread.
@@ -239,7 +226,7 @@ __global__ void __launch_bounds__(kQuantThreads, W == 1 ? 2 : sizeof(T) == 2 ? 5
 #pragma unroll
     for (int i = 1; i < kQuantThreads / 32; ++i) top = fmaxf(top, tops[i]);
     const bool finite = top <= 3.402823466e38f;
-    const Factor f = factor_of(top);
+    const Factor f = factor_of<T>(top);
     if (top < kSmall)
 #pragma unroll
         for (int i = 0; i < I; ++i)
@@ -264,9 +251,8 @@ tm_status launch_quant(const QuantArgs &a, int32_t rows, cudaStream_t s, bool pd
     void *args[] = {const_cast<QuantArgs *>(&a)};
     if (rows == 128)
         return launch_kernel((const void *)quant_blocks<T, W>, dim3((unsigned)a.tasks), dim3(kQuantThreads), args, 0, s, pdl);
-    constexpr int U = W == 1 ? 2 : 4, kRuns = kQuantThreads / (W == 1 ? 32 : 128 / W);
-    const int blocks = (a.tasks + kRuns * U - 1) / (kRuns * U);
-    return launch_kernel((const void *)quant_rows<T, W, U>, dim3((unsigned)blocks), dim3(kQuantThreads), args, 0, s, pdl);
+    constexpr int kRuns = kQuantThreads / (32 / W);
+    return launch_kernel((const void *)quant_rows<T, W>, dim3((unsigned)((a.tasks + kRuns - 1) / kRuns)), dim3(kQuantThreads), args, 0, s, pdl);
 }
 
 template <typename T>
