@@ -2,8 +2,9 @@
 //
 //   c[t, n] = sum_b sa[t, b] sb[n / 128, b] * sum_{k in b} a[t, k] b[n, k]
 //
-// A CTA pair takes a tile of 256 rows t by 256 columns n (128 where that leaves SMs without a tile); a stage of the ring is one block of
-// 128 of the sum, 16 KB of each operand a CTA.  Rows lie along the tensor memory's lanes
+// A CTA pair takes a tile of 256 rows t by 256 columns n (128 where that leaves SMs without a tile), or a CTA
+// one of 128 by 128 where experts have few rows; a stage of the ring is one block of 128 of the sum, up to 16 KB of
+// each operand a CTA.  Rows lie along the tensor memory's lanes
 // here: then a block's two scales are one factor a thread (its row's, times that of the 128
 // columns the thread holds), and adding a block is one packed fp32 operation for two
 // outputs.  The tensor cores make a block's sums in one accumulator of 256 columns while
@@ -53,7 +54,7 @@ struct Tile8 {
     int e, row, n, n0;  // expert, first row and how many, first column
 };
 
-template <int NT>
+template <int RT, int NT>
 struct Walk8 {
     const Wide8Args &a;
     const Experts &x;
@@ -65,28 +66,39 @@ struct Walk8 {
         const int tiles = x.before[e + 1] - x.before[e], local = item - x.before[e] * a.ntiles;
         const int block = local / (kGroup8 * a.ntiles), in = local - block * kGroup8 * a.ntiles;
         const int wide = tiles - block * kGroup8 < kGroup8 ? tiles - block * kGroup8 : kGroup8;
-        const int r = (block * kGroup8 + in % wide) * 256, left = x.count[e] - r;
-        return {e, x.first[e] + r, left < 256 ? left : 256, in / wide * NT};
+        const int r = (block * kGroup8 + in % wide) * RT, left = x.count[e] - r;
+        return {e, x.first[e] + r, left < RT ? left : RT, in / wide * NT};
     }
 };
 
-// Staged rows to where another expert's rows follow, or off the copies' grid: row by row, neighbours by
-// neighbours.  Out of line: what the sums' loop has for registers is not to depend on it.
+// Staged rows to where another expert's rows follow, or off the copies' grid: two rows of 256 bytes at once on
+// the grid, else row by row, neighbours by neighbours.  Out of line: what the sums' loop has for registers is not to depend
+// on it.  (64 experts of 2048 x 4096 with 47 rows each, element by element: 152 us, so 131.)
 template <int E>
-__device__ __noinline__ void rows_out(const unsigned char *staged, void *out, int64_t ldo, int rows, int cols)
+__device__ __noinline__ void rows_out(const unsigned char *staged, void *out, int64_t ldo, int rows, int cols, bool on_grid)
 {
-    for (int i = 0; i < rows; ++i)
-        for (int c = threadIdx.x & 31; c < 256 / E && c < cols; c += 32) {
-            const unsigned char *from = staged + (c * E >> 7) * (kOutWarp / 2) + i * 128 + ((c * E >> 4 & 7) ^ (i & 7)) * 16 + (c * E & 15);
+    auto from = [&](int i, int at) { return staged + (at >> 7) * (kOutWarp / 2) + i * 128 + ((at >> 4 & 7) ^ (i & 7)) * 16 + (at & 15); };
+    const int lane = threadIdx.x & 31;
+    if (on_grid) {
+        const int at = (lane & 15) * 16;
+        if (at >= cols * E) return;
+#pragma unroll 2
+        for (int i = lane >> 4; i < rows; i += 2)
+            *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(out) + i * ldo * E + at) = *reinterpret_cast<const uint4 *>(from(i, at));
+        return;
+    }
+    for (int c = lane; c < 256 / E && c < cols; c += 32)
+#pragma unroll 2
+        for (int i = 0; i < rows; ++i) {
             if constexpr (E == 4)
-                reinterpret_cast<uint32_t *>(out)[i * ldo + c] = *reinterpret_cast<const uint32_t *>(from);
+                reinterpret_cast<uint32_t *>(out)[i * ldo + c] = *reinterpret_cast<const uint32_t *>(from(i, c * E));
             else
-                reinterpret_cast<uint16_t *>(out)[i * ldo + c] = *reinterpret_cast<const uint16_t *>(from);
+                reinterpret_cast<uint16_t *>(out)[i * ldo + c] = *reinterpret_cast<const uint16_t *>(from(i, c * E));
         }
 }
 
-// NT: columns of a tile, 256 or 128.
-template <typename O, int NT>
+// NT: columns of a tile, 256 or 128.  PAIR: two CTAs a tile of 256 rows; else one a tile of 128 (by 128).
+template <typename O, int NT, bool PAIR>
 __global__ void __launch_bounds__(kThreads8, 1)
     wide8_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const __grid_constant__ CUtensorMap mc, const Wide8Args a)
@@ -96,42 +108,46 @@ __global__ void __launch_bounds__(kThreads8, 1)
     unsigned char *outs = ring + kStages8 * kStage8;
     __shared__ Wide8Smem s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int unit = (int)(blockIdx.x >> 1), units = (int)(gridDim.x >> 1);
+    static_assert(PAIR || NT == 128, "a stage holds 128 rows of each operand");
+    constexpr int C = PAIR ? 2 : 1, BR = NT / C;  // CTAs a tile; a CTA's rows of b
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const int unit = (int)blockIdx.x / C, units = (int)gridDim.x / C;
 
-    if (warp == 1) acc_alloc<true>(&s.tmem, 512);
+    if (warp == 1) acc_alloc<PAIR>(&s.tmem, 512);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages8; ++i) {
-            mbar_init(&s.full[i], 2);
+            mbar_init(&s.full[i], C);
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.acc_full[i], 1);
-            mbar_init(&s.acc_empty[i], 16);
+            mbar_init(&s.acc_empty[i], 8 * C);
         }
         mbar_init(&s.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s.abort = 0;
     }
-    experts_read(s.x, a.starts, a.E, a.T, 256, a.status);
+    experts_read(s.x, a.starts, a.E, a.T, 128 * C, a.status);
     acc_fence_before();
     __syncthreads();
-    cluster_sync();
+    if constexpr (PAIR) cluster_sync();
     acc_fence_after();
     pdl_trigger();  // only now: a dependent's CTA could take the tensor memory that this one waits for
     const uint32_t tmem = s.tmem;
     const int items = s.x.before[a.E] * a.ntiles;
-    Walk8<NT> walk(a, s.x);
+    Walk8<128 * C, NT> walk(a, s.x);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (warp == 0) {
+            // one row tile an expert: its weights are read once
+            const uint64_t pol = PAIR ? 0 : l2_evict_first_policy();
             Turn t;
             uint32_t used = 0;
             bool ok = true;
             for (int item = unit; ok && item < items; item += units) {
                 const Tile8 w = walk.at(item);
-                const int row = w.row + (int)rank * 128, n = w.n0 + (int)rank * (NT / 2);
+                const int row = w.row + (int)rank * 128, n = w.n0 + (int)rank * BR;
                 for (int k = 0; k < a.steps; ++k) {
                     if (used >= kStages8 && !warp_wait(&s.empty[t.slot], t.phase ^ 1u, &s.abort, a.status)) {
                         ok = false;
@@ -139,9 +155,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                     const uint32_t at = smem_u32(ring) + t.slot * kStage8, bar = cluster_addr(smem_u32(&s.full[t.slot]), 0);
                     if (elect()) {
-                        mbar_expect_cluster(bar, kHalf8 + NT / 2 * 128);
-                        tma_load_2d_pair(at, &ma, k * 128, row, bar);
-                        tma_load_3d_pair(at + kHalf8, &mb, k * 128, n, w.e, bar);
+                        mbar_expect_cluster(bar, kHalf8 + BR * 128);
+                        if constexpr (PAIR) {
+                            tma_load_2d_pair(at, &ma, k * 128, row, bar);
+                            tma_load_3d_pair(at + kHalf8, &mb, k * 128, n, w.e, bar);
+                        } else {
+                            tma_load_2d(at, &ma, k * 128, row, smem_u32(&s.full[t.slot]));
+                            tma_load_3d_hint(at + kHalf8, &mb, k * 128, n, w.e, smem_u32(&s.full[t.slot]), pol);
+                        }
                     }
                     __syncwarp();
                     ++used;
@@ -169,16 +190,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     if (elect()) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            umma<true, true>(d, operand_k(at + j * 32), operand_k(at + kHalf8 + j * 32), a.id, j != 0);
-                        umma_done<true>(&s.empty[t.slot]);
-                        umma_done<true>(&s.acc_full[acc.slot]);
+                            umma<true, PAIR>(d, operand_k(at + j * 32), operand_k(at + kHalf8 + j * 32), a.id, j != 0);
+                        umma_done<PAIR>(&s.empty[t.slot]);
+                        umma_done<PAIR>(&s.acc_full[acc.slot]);
                     }
                     __syncwarp();
                     t.next(kStages8);
                     acc.next(2);
                 }
             }
-            if (elect()) umma_done<true>(&s.done);
+            if (elect()) umma_done<PAIR>(&s.done);
             __syncwarp();
             mbar_wait_bounded(smem_u32(&s.done), 0);
         }
@@ -261,7 +282,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 }
                 __syncwarp();
                 rows_out<sizeof(O)>(mine, reinterpret_cast<O *>(a.out) + (int64_t)row0 * a.ldo + first, a.ldo, rows < 32 ? rows : 32,
-                                    a.N - first < CW ? a.N - first : CW);
+                                    a.N - first < CW ? a.N - first : CW, a.by_copy != 0);
                 __syncwarp();
             };
             if (rows <= 0) continue;
@@ -305,21 +326,21 @@ __global__ void __launch_bounds__(kThreads8, 1)
     pdl_wait();
     acc_fence_before();
     __syncthreads();
-    cluster_sync();
+    if constexpr (PAIR) cluster_sync();
     if (warp == 1) {
         __syncwarp();
         acc_fence_after();
-        acc_free<true>(tmem, 512);
+        acc_free<PAIR>(tmem, 512);
     }
 }
 
 constexpr size_t kWide8Smem = kStages8 * kStage8 + 8 * kOutWarp + 1024;
 
-template <typename O, int NT>
+template <typename O, int NT, bool PAIR>
 tm_status launch_wide8_as(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const Wide8Args &a, int64_t units,
                        cudaStream_t s, bool pdl)
 {
-    const void *k = (const void *)wide8_kernel<O, NT>;
+    const void *k = (const void *)wide8_kernel<O, NT, PAIR>;
     static std::once_flag once[kMaxDevices];
     static bool good[kMaxDevices];
     int d = 0;
@@ -331,14 +352,15 @@ tm_status launch_wide8_as(const CUtensorMap &ma, const CUtensorMap &mb, const CU
     if (!good[d]) return TM_ERR_CUDA;
     void *args[] = {const_cast<CUtensorMap *>(&ma), const_cast<CUtensorMap *>(&mb), const_cast<CUtensorMap *>(&mc),
                     const_cast<Wide8Args *>(&a)};
-    return launch_kernel(k, dim3((unsigned)(2 * units)), dim3(kThreads8), args, kWide8Smem, s, pdl, 2);
+    return launch_kernel(k, dim3((unsigned)(units * (PAIR ? 2 : 1))), dim3(kThreads8), args, kWide8Smem, s, pdl, PAIR ? 2 : 1);
 }
 
 template <typename O>
-tm_status launch_wide8(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const Wide8Args &a, int nt, int64_t units,
+tm_status launch_wide8(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const Wide8Args &a, int nt, bool pair, int64_t units,
                        cudaStream_t s, bool pdl)
 {
-    return nt == 256 ? launch_wide8_as<O, 256>(ma, mb, mc, a, units, s, pdl) : launch_wide8_as<O, 128>(ma, mb, mc, a, units, s, pdl);
+    if (!pair) return launch_wide8_as<O, 128, false>(ma, mb, mc, a, units, s, pdl);
+    return nt == 256 ? launch_wide8_as<O, 256, true>(ma, mb, mc, a, units, s, pdl) : launch_wide8_as<O, 128, true>(ma, mb, mc, a, units, s, pdl);
 }
 
 }  // namespace
@@ -355,26 +377,29 @@ tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bo
     a.E = p.E;
     a.T = (int)p.T;
     a.N = (int)p.F;
-    const int64_t busy = p.E < p.T ? p.E : p.T, rtiles = (p.T + 255) / 256 + busy, pairs = dev.sms / 2;
-    // narrow tiles where all of them run at once, on SMs that would have nothing to do (one of 4096 x 4096, 512 rows:
-    // 24.6 us with 256 and 20.5 with 128; 1000 rows of 2048 x 7168: 34.8 and 28.7)
-    const int nt = tiles_of(p, 256) * ((p.F + 127) / 128) <= pairs ? 128 : 256;
+    // a tile a CTA where experts have 128 rows on average (64 experts of 2048 x 4096, 64 rows each: 129 us by pairs,
+    // 111 so; 8 of 4096 x 4096, 100 rows each: 47 and 37; 64 of 2048 x 2048 with uneven rows, 128 on average: 75 and 80).  Else narrow tiles where all of them run at once, on SMs that would have nothing to do (one of
+    // 4096 x 4096, 512 rows: 24.6 us with 256 columns and 20.5 with 128; 1000 rows of 2048 x 7168: 34.8 and 28.7).
+    const bool pair = p.T > 128 * (int64_t)p.E;
+    const int64_t busy = p.E < p.T ? p.E : p.T, rt = pair ? 256 : 128, rtiles = (p.T + rt - 1) / rt + busy;
+    const int64_t at_once = pair ? dev.sms / 2 : dev.sms;
+    const int nt = !pair || tiles_of(p, 256) * ((p.F + 127) / 128) <= at_once ? 128 : 256;
     a.ntiles = (int)((p.F + nt - 1) / nt);
     a.steps = (int)((p.R + 127) / 128);
     a.group = p.group;
-    a.id = instruction(0, false, false, 256, (uint32_t)nt);
+    a.id = instruction(0, false, false, (uint32_t)rt, (uint32_t)nt);
     // TMA clips what it stores at whole 16 bytes: N must end on them
     const int eo = elem_bytes(p.otype), grid = 16 / eo;
     a.by_copy = aligned_to(p.out, 16) && p.ldo % grid == 0 && p.F % grid == 0;
     CUtensorMap ma, mb, mc;
-    if (!rows_map(&ma, p.kind, p.x, p.R, p.T, p.ldx, 0, 128) || !rows_map(&mb, p.kind, p.w, p.R, p.F, p.ldw, p.E, nt / 2)) return TM_ERR_CUDA;
+    if (!rows_map(&ma, p.kind, p.x, p.R, p.T, p.ldx, 0, 128) || !rows_map(&mb, p.kind, p.w, p.R, p.F, p.ldw, p.E, pair ? nt / 2 : nt)) return TM_ERR_CUDA;
     if (a.by_copy ? !rows_map_of(&mc, eo, p.out, p.F, p.T, p.ldo, 0, 32) : (mc = ma, false)) return TM_ERR_CUDA;
     const int64_t items = rtiles * a.ntiles;
     if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
-    const int64_t units = items < pairs ? items : pairs;
-    if (p.otype == TM_F32) return launch_wide8<float>(ma, mb, mc, a, nt, units, s, pdl);
-    if (p.otype == TM_F16) return launch_wide8<__half>(ma, mb, mc, a, nt, units, s, pdl);
-    return launch_wide8<__nv_bfloat16>(ma, mb, mc, a, nt, units, s, pdl);
+    const int64_t units = items < at_once ? items : at_once;
+    if (p.otype == TM_F32) return launch_wide8<float>(ma, mb, mc, a, nt, pair, units, s, pdl);
+    if (p.otype == TM_F16) return launch_wide8<__half>(ma, mb, mc, a, nt, pair, units, s, pdl);
+    return launch_wide8<__nv_bfloat16>(ma, mb, mc, a, nt, pair, units, s, pdl);
 }
 
 }  // namespace libtm

@@ -1,5 +1,5 @@
-"""The products by expert at sizes that take tiles of each width (64, 128 and 256 along the narrow extent), among them calls
-with more tiles than SMs hold at once and tiles that end after one row or one column."""
+"""The products by expert at sizes that take tiles of each width (64, 128 and 256 along the narrow extent; in 8 bits also
+of 128 by 128), among them calls with more tiles than SMs hold at once and tiles that end after one row or one column."""
 import pytest
 import torch
 
@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 # rows of each expert, N, K
 SHAPES = [([900, 800, 333, 5, 0, 700], 1000, 330), ([900, 800, 333, 5, 0, 700], 500, 330), ([129] * 50, 200, 72), ([65] * 60, 256, 136),
           ([33] * 70, 130, 264), ([257] * 48, 100, 200), ([64, 65, 63, 1, 129, 128, 127], 257, 129), ([3000], 264, 1000),
-          ([1025], 1025, 512), ([255, 257, 513], 72, 1032), ([2000, 1, 2000], 260, 64)]
+          ([1025], 1025, 512), ([255, 257, 513], 72, 1032), ([2000, 1, 2000], 260, 64), ([127, 0, 0, 300, 40, 1], 1000, 136),
+          ([100] * 20, 1100, 200), ([34, 128, 0, 129, 1], 136, 1160)]
 
 
 @pytest.mark.parametrize("counts,N,K", SHAPES)
