@@ -6,6 +6,7 @@
 // Each value is read once and stays in registers between the block's maximum and its codes,
 // so memory bounds it: 2 or 4 bytes in, 1 out.  At 16 bits that leaves about 11 lanes'
 // instructions a value on an SM, so the maximum is taken two values at a time on their bits.
+// 8192 x 8192 in 16 bits: 34 us by blocks and by rows, 87 % of a copy's rate.
 //
 // Codes are those of the exact quotient, which q = x * (448 / top) misses by up to 2^-23 of
 // itself: wrong where a border between two codes lies between them.
@@ -163,8 +164,8 @@ struct QuantArgs {
 };
 
 // One row's runs, neighbours in the flat order of all runs: 32 values a thread in four vectors, so that a
-// run's maximum takes few exchanges between lanes and its address is found once (8192 x 8192 in 16 bits 36 us, 81 % of
-// a copy's rate; 8 values a thread of four runs, 48).
+// run's maximum takes few exchanges between lanes and its address is found once (8192 x 8192 in 16 bits, cold: 36 us; 8
+// values a thread of each of four runs, 48).
 template <typename T, int W>
 __global__ void __launch_bounds__(kQuantThreads) quant_rows(const QuantArgs a)
 {

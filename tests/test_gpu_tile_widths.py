@@ -1,5 +1,6 @@
 """The products by expert at sizes that take tiles of each width (64, 128 and 256 along the narrow extent; in 8 bits also
 of 128 by 128), among them calls with more tiles than SMs hold at once and tiles that end after one row or one column."""
+import numpy as np
 import pytest
 import torch
 
@@ -44,3 +45,60 @@ def test_sums_on_both_sides_of_a_rule(cuda, counts, K):
     tm.tm_check()
     c.check(y, "f32")
     assert torch.equal(y, again)
+
+
+# the kernel and its tiles are chosen from T and E alone: any borders must do, also where they move between a graph's replays
+SPREADS = [[100, 100, 100, 100, 100, 100], [600, 0, 0, 0, 0, 0], [0, 0, 0, 0, 1, 599], [1, 2, 4, 8, 16, 569], [0, 300, 0, 300, 0, 0]]
+
+
+@pytest.mark.parametrize("N,K", [(1000, 264), (136, 1032)])
+def test_borders_move_under_a_graph(cuda, N, K):
+    c, c8 = Case(SPREADS[0], N, K, "bf16", seed=1, ints=True), Case8(SPREADS[0], N, K, 128, seed=2, ints=True)
+    # scales of one, so that no expert's own enter the oracle's operands wrongly when rows change hands
+    c8.sa.fill_(1.0), c8.sb.fill_(1.0)
+    plain = lambda t, ld: t.view(torch.float8_e4m3fn).float().double().cpu().numpy().reshape(-1, ld)[:, :K]  # noqa: E731
+    c8.a64, c8.b64 = plain(c8.a, c8.ld), plain(c8.b, c8.ld).reshape(6, N, K)
+    st = torch.cuda.Stream()
+    out = [torch.empty(600, N, device="cuda"), torch.empty(600, N, device="cuda"), torch.empty(600, K, device="cuda").bfloat16(),
+           torch.empty(6 * N, K, device="cuda")]
+    torch.cuda.synchronize()
+    s = st.cuda_stream
+
+    def run(flags):
+        tm.tm_gemm_experts(c.x, c.ldk, c.w, c.ldk, out[0], N, c.d_starts, 6, 600, N, K, 2, 0, flags, s)
+        tm.tm_gemm_e4m3(c8.a, c8.ld, c8.sa, 128, c8.b, c8.ld, c8.sb, out[1], N, c.d_starts, 6, 600, N, K, 0, flags, s)
+        tm.tm_gemm_experts_bwd(c.dy, c.ldn, c.x, c.ldk, c.w, c.ldk, out[2], K, out[3], K, c.d_starts, 6, 600, N, K, 2, 0, flags, s)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st):
+        with torch.cuda.graph(graph, stream=st):
+            run(0)
+            run(tm.TM_PDL)
+    for spread in SPREADS:
+        starts = np.concatenate([[0], np.cumsum(spread)])
+        c.starts = c8.starts = [int(v) for v in starts]
+        with torch.cuda.stream(st):
+            c.d_starts.copy_(torch.tensor(starts, dtype=torch.int32))
+            for o in out:
+                o.fill_(float("nan"))
+            graph.replay()
+        st.synchronize()
+        tm.tm_check(st)
+        c.check_forward(out[0], "f32")
+        c8.check(out[1])
+        c.check_backward(out[2], out[3], "f32")
+
+
+@pytest.mark.parametrize("counts,N,K", [([100] * 20, 1100, 200), ([257] * 48, 100, 200), ([700], 256, 2200)])
+def test_overlapped_calls(cuda, counts, N, K):
+    c, c8, st = Case(counts, N, K, "bf16", seed=4), Case8(counts, N, K, 128, seed=5), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    runs = []
+    with torch.cuda.stream(st):
+        first = c.forward("f32", stream=st), c8.run("f32", stream=st), *c.backward("f32", stream=st)
+        for _ in range(4):
+            runs.append((c.forward("f32", flags=tm.TM_PDL, stream=st), c8.run("f32", flags=tm.TM_PDL, stream=st),
+                         *c.backward("f32", flags=tm.TM_PDL, stream=st)))
+    tm.tm_check(st)
+    for r in runs:
+        assert all(torch.equal(a, b) for a, b in zip(first, r))
