@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from masking_tm_affine_gb300 import tm
-from test_gpu_e4m3 import Case as Case8
+from test_gpu_e4m3 import TYPES, Case as Case8, check_quant, quant
 from test_gpu_experts import Case
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +102,17 @@ def test_overlapped_calls(cuda, counts, N, K):
     tm.tm_check(st)
     for r in runs:
         assert all(torch.equal(a, b) for a, b in zip(first, r))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("N,ldx,ldy,x0,y0", [(260, 260, 260, 0, 0), (260, 264, 268, 4, 4), (264, 264, 264, 4, 0), (264, 268, 264, 0, 0),
+                                             (264, 264, 264, 0, 4), (264, 264, 265, 0, 0), (262, 264, 264, 0, 0), (262, 262, 262, 2, 6),
+                                             (264, 264, 264, 2, 2), (2, 2, 2, 0, 0), (4, 4, 4, 0, 0)])
+def test_quantisation_in_vectors_of_each_width(cuda, kind, rows, N, ldx, ldy, x0, y0):
+    g = torch.Generator().manual_seed(N + ldx)
+    flat = torch.full((131 * ldx + x0,), float("nan")).to(TYPES[kind])
+    x = flat[x0:].view(131, ldx)
+    x[:, :N] = torch.randn(131, N, generator=g).to(TYPES[kind])
+    x = flat.cuda()[x0:].view(131, ldx)[:, :N]
+    check_quant(x, *quant(x, kind, rows, ldy, y0), rows)
