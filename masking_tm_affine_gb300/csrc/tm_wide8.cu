@@ -380,8 +380,9 @@ tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bo
     a.N = (int)p.F;
     // a tile a CTA where experts have 128 rows on average (64 experts of 2048 x 4096, 64 rows each: 129 us by pairs,
     // 111 so; 8 of 4096 x 4096, 100 rows each: 47 and 37; 64 of 2048 x 2048 with uneven rows, 128 on average: 75
-    // and 80; all 8192 rows one expert's: 43 and 55).  Else narrow tiles where all of them run at once, on SMs that would have nothing to do (one of
-    // 4096 x 4096, 512 rows: 24.6 us with 256 columns and 20.5 with 128; 1000 rows of 2048 x 7168: 34.8 and 28.7).
+    // and 80; all 8192 rows one expert's: 43 and 55).  Else narrow tiles where all of them run at once, on SMs that
+    // would have nothing to do (one of 4096 x 4096, 512 rows: 24.6 us with 256 columns and 20.5 with 128; 1000 rows of
+    // 2048 x 7168: 34.8 and 28.7).
     const bool pair = p.T > 128 * (int64_t)p.E;
     const int64_t busy = p.E < p.T ? p.E : p.T, rt = pair ? 256 : 128, rtiles = (p.T + rt - 1) / rt + busy;
     const int64_t at_once = pair ? dev.sms / 2 : dev.sms;
@@ -394,7 +395,9 @@ tm_status wide8_product(const Product &p, const DevInfo &dev, cudaStream_t s, bo
     const int eo = elem_bytes(p.otype), grid = 16 / eo;
     a.by_copy = aligned_to(p.out, 16) && p.ldo % grid == 0 && p.F % grid == 0;
     CUtensorMap ma, mb, mc;
-    if (!rows_map(&ma, p.kind, p.x, p.R, p.T, p.ldx, 0, 128) || !rows_map(&mb, p.kind, p.w, p.R, p.F, p.ldw, p.E, pair ? nt / 2 : nt)) return TM_ERR_CUDA;
+    if (!rows_map(&ma, p.kind, p.x, p.R, p.T, p.ldx, 0, 128) ||
+        !rows_map(&mb, p.kind, p.w, p.R, p.F, p.ldw, p.E, pair ? nt / 2 : nt))
+        return TM_ERR_CUDA;
     if (a.by_copy ? !rows_map_of(&mc, eo, p.out, p.F, p.T, p.ldo, 0, 32) : (mc = ma, false)) return TM_ERR_CUDA;
     const int64_t items = rtiles * a.ntiles;
     if (items > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
