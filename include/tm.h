@@ -684,9 +684,9 @@ tm_status tm_gemm_e4m3(const void *A, int64_t lda, const float *sa, int32_t grou
  *   X, ldx     [T, K] of xtype (TM_F16 or TM_BF16; fp32 products: tm_gemm)
  *   W, ldw     [E, N, K] of xtype, rows n of all experts one after another
  *   Y, ldy     output [T, N] of ytype (xtype or TM_F32); overlaps no input
- * K == 0 gives zeros.  Sums to fp32 outputs leave the tensor cores every 512 of K and
- * are added rounded to nearest: |error| <= (512 + K / 512 + 9) 2^-23 * sum |x w|; to 16 bits they
- * stay there, (K + 9) 2^-23, far below the output's own rounding.  Errors: as tm_gemm_e4m3.
+ * K == 0 gives zeros.  Sums leave the tensor cores every 512 of K and are added rounded to
+ * nearest: |error| <= (512 + K / 512 + 9) 2^-23 * sum |x w|, plus the output's own rounding.
+ * Errors: as tm_gemm_e4m3.
  */
 tm_status tm_gemm_experts(const void *X, int64_t ldx, const void *W, int64_t ldw, void *Y, int64_t ldy,
                           const int32_t *starts, int32_t E, int64_t T, int64_t N, int64_t K, int32_t xtype,
@@ -699,6 +699,7 @@ tm_status tm_gemm_experts(const void *X, int64_t ldx, const void *W, int64_t ldw
  *   DX, lddx   output [T, K] of xtype, or NULL
  *   DW, lddw   output [E, N, K] of wtype (xtype or TM_F32), or NULL; zeros for an
  *              expert without rows.  Rows that belong to nobody take no part, whatever they hold
+ * Sums as in the forward call, over N (DX) and over the expert's rows (DW) instead of K.
  * Errors: as tm_gemm_e4m3.
  */
 tm_status tm_gemm_experts_bwd(const void *DY, int64_t lddy, const void *X, int64_t ldx, const void *W, int64_t ldw,

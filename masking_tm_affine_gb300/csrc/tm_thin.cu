@@ -11,10 +11,10 @@
 // which adds them in rank order and stores: one launch, no workspace, the same bits
 // every time.  256 rows over 48 experts of 2048 x 4096 in 8 bits: 67 us, 6.0 TB/s; 64 rows over 24 in 16 bits: 47 us, 5.8.
 //
-// Sums.  16-bit operands to 16-bit outputs: the accumulator stays in tensor memory, fp32.  To
-// fp32 outputs: the tensor cores' additions lose up to 2^-23 of the sum each, always towards zero, so a
-// sum leaves them after kRunSums of it and is added in registers, rounded to nearest (over 8192 rows of a
-// weights' gradient: 2.5e-6 of the result without, 2e-7 with).  e4m3: one accumulator for each 128 of the
+// Sums.  The tensor cores' additions lose up to 2^-23 of the sum each, always towards zero, so a
+// sum of 16-bit products leaves them after kRunSums of it and is added in registers, rounded to nearest (over
+// 8192 rows of a weights' gradient: 2.5e-6 of the result without, 2e-7 with; 131072 terms of one sign
+// lose 4e-4 of their sum without, nearly an output's rounding to fp16, and 3e-6 with).  e4m3: one accumulator for each 128 of the
 // sum, read out, multiplied by both scales and added in fp32 registers while the next ones are made.
 #include <mutex>
 
@@ -69,26 +69,24 @@ struct ThinArgs {
     uint32_t id;  // the instruction without its N
 };
 
-// The forms.  F8: e4m3; SUMS: sums leave the tensor cores in runs (always with F8).
-template <bool F8, bool SUMS, int BT>
+// The forms.  F8: e4m3.
+template <bool F8, int BT>
 struct Thin {
     static constexpr int kOutWarps = BT <= 32 ? 4 : 8;  // behind warp 0, which copies, and warp 1, which multiplies
     static constexpr int kThreads = 64 + 32 * kOutWarps;
     static constexpr int kCols = BT * 4 / kOutWarps;    // columns of an output warp
-    // Three CTAs an SM with tiles of 32 rows, two with 128, stages of 20 and 32 KB; one where 64 sums a
-    // thread take its registers.
-    static constexpr int kCtas = BT <= 32 ? 3 : SUMS ? 1 : 2;
+    // Three CTAs an SM with tiles of 32 rows, stages of 20 KB; one with 128, stages of 32 KB and 64 sums a thread.
+    static constexpr int kCtas = BT <= 32 ? 3 : 1;
     // Stages of the ring, by how many CTAs an SM there are: a tile alone there has all of the memory (16 rows
     // by 2048 x 8192 in 16 bits, cold: 18.5 us with 3 stages, 16.0 with 10; 4096 x 4096 14.1 and 13.4)
-    static constexpr int stages(int ctas) { return BT <= 32 ? (ctas <= 1 ? 10 : ctas == 2 ? 5 : 3) : ctas <= 1 || kCtas == 1 ? 6 : 3; }
+    static constexpr int stages(int ctas) { return BT > 32 ? 6 : ctas <= 1 ? 10 : ctas == 2 ? 5 : 3; }
     static constexpr int kRun = F8 ? 1 : kRunSums / 64;  // stages a run
-    // accumulators: one of a tile, or several that take turns over its runs
-    static constexpr int kAccs = !SUMS ? 1 : BT <= 32 ? 4 : 2;
+    static constexpr int kAccs = BT <= 32 ? 4 : 2;  // accumulators that take turns over a tile's runs
 };
 
-template <bool F8, bool SUMS, int BT>
+template <bool F8, int BT>
 struct ThinSmem {
-    using F = Thin<F8, SUMS, BT>;
+    using F = Thin<F8, BT>;
     alignas(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[4], acc_empty[4], inbox, done;
     uint32_t tmem;
     int abort;
@@ -152,13 +150,13 @@ __device__ __forceinline__ void find_tile(S &s, const ThinArgs &a, int tile, int
     __syncwarp();
 }
 
-template <bool F8, bool SUMS, bool MN, int BT>
-__global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
+template <bool F8, bool MN, int BT>
+__global__ void __launch_bounds__(Thin<F8, BT>::kThreads)
     thin_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mx_all,
                 const ThinArgs a, const int S)
 {
     constexpr uint32_t kStage = kTall + BT * 128;
-    using F = Thin<F8, SUMS, BT>;
+    using F = Thin<F8, BT>;
     const uint32_t stages = (uint32_t)a.stages;
     constexpr int kStep = F8 ? 128 : 64;  // elements of the sum a stage
     constexpr int kAccs = F::kAccs, kRun = F::kRun, CW = F::kCols;
@@ -171,7 +169,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
     // the ring's place once every CTA of the cluster is done with its own
     float *inbox = reinterpret_cast<float *>(ring);
     static_assert(BT * 128 * 4 <= 3 * kStage, "inbox");
-    __shared__ ThinSmem<F8, SUMS, BT> s;
+    __shared__ ThinSmem<F8, BT> s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_rank() : 0;
     const int item = (int)blockIdx.x / S;
@@ -211,7 +209,7 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
     const int q = warp & 3, f = f0 + q * 32 + lane, part = (warp - 2) >> 2, cb = part * CW;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     bool ok = true;
-    float sum[SUMS ? CW : 1];
+    float sum[CW];
 
     if (warp == 0) {
         if (n > 0) {
@@ -251,14 +249,14 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
             int in_run = 0;
             uint32_t runs = 0;
             for (int k = k0; k < k1; ++k) {
-                if (SUMS && in_run == 0 && runs >= (uint32_t)kAccs &&
+                if (in_run == 0 && runs >= (uint32_t)kAccs &&
                     !warp_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status))
                     break;
                 if (!warp_wait(&s.full[t.slot], t.phase, &s.abort, a.status)) break;
                 acc_fence_after();
                 const uint32_t at = smem_u32(ring) + t.slot * kStage, d = tmem + acc.slot * BT;
                 ++in_run;
-                const bool end = (SUMS && in_run == kRun) || k + 1 == k1;
+                const bool end = in_run == kRun || k + 1 == k1;
                 if (elect()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -281,65 +279,60 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
             mbar_wait_bounded(smem_u32(&s.done), 0);
         }
     } else if (n > 0) {
-        if constexpr (SUMS) {
 #pragma unroll
-            for (int c = 0; c < CW; ++c) sum[c] = 0.0f;
-            // e4m3: this warp's copy of the rows' factors; the next block's are on their way meanwhile
-            const int G = a.steps;  // scales of a row
-            const float *sb = F8 ? a.sb + ((int64_t)e * a.ftiles + f0 / 128) * G : nullptr;
-            float fa[CW / 32], fb = 0.0f;
-            auto fetch = [&](int k) {
-                if (!F8 || k >= k1) return;
-                fb = __ldg(sb + k);
+        for (int c = 0; c < CW; ++c) sum[c] = 0.0f;
+        // e4m3: this warp's copy of the rows' factors; the next block's are on their way meanwhile
+        const int G = a.steps;  // scales of a row
+        const float *sb = F8 ? a.sb + ((int64_t)e * a.ftiles + f0 / 128) * G : nullptr;
+        float fa[CW / 32], fb = 0.0f;
+        auto fetch = [&](int k) {
+            if (!F8 || k >= k1) return;
+            fb = __ldg(sb + k);
 #pragma unroll
-                for (int i = 0; i < CW / 32; ++i) {
-                    const int t = cb + i * 32 + lane;
-                    const int64_t row = row0 + (t < n ? t : 0);
-                    fa[i] = __ldg(a.sa + (a.group ? row * G + k : row));
-                }
-            };
-            Turn acc;
-            fetch(k0);
-            for (int k = k0; k < k1; k += kRun) {
-                float *factor = s.scale[warp - 2][k & 1];
-                if constexpr (F8) {
+            for (int i = 0; i < CW / 32; ++i) {
+                const int t = cb + i * 32 + lane;
+                const int64_t row = row0 + (t < n ? t : 0);
+                fa[i] = __ldg(a.sa + (a.group ? row * G + k : row));
+            }
+        };
+        Turn acc;
+        fetch(k0);
+        for (int k = k0; k < k1; k += kRun) {
+            float *factor = s.scale[warp - 2][k & 1];
+            if constexpr (F8) {
 #pragma unroll
-                    for (int i = 0; i < CW / 32; ++i) factor[i * 32 + lane] = fa[i] * fb;
-                    fetch(k + 1);
-                    __syncwarp();
-                }
-                ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status));
-                if (!ok) break;
-                acc_fence_after();
+                for (int i = 0; i < CW / 32; ++i) factor[i * 32 + lane] = fa[i] * fb;
+                fetch(k + 1);
+                __syncwarp();
+            }
+            ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status));
+            if (!ok) break;
+            acc_fence_after();
 #pragma unroll
-                for (int c0 = 0; c0 < CW; c0 += 32) {
-                    if (cb + c0 < n) {
-                        float v[32];
-                        acc_load32(lanes + acc.slot * BT + cb + c0, v);
-                        acc_load_wait(v);
+            for (int c0 = 0; c0 < CW; c0 += 32) {
+                if (cb + c0 < n) {
+                    float v[32];
+                    acc_load32(lanes + acc.slot * BT + cb + c0, v);
+                    acc_load_wait(v);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            if constexpr (F8) {
-                                const float4 m = *reinterpret_cast<const float4 *>(factor + c0 + c);
-                                sum[c0 + c] = __fmaf_rn(v[c], m.x, sum[c0 + c]);
-                                sum[c0 + c + 1] = __fmaf_rn(v[c + 1], m.y, sum[c0 + c + 1]);
-                                sum[c0 + c + 2] = __fmaf_rn(v[c + 2], m.z, sum[c0 + c + 2]);
-                                sum[c0 + c + 3] = __fmaf_rn(v[c + 3], m.w, sum[c0 + c + 3]);
-                            } else {
+                    for (int c = 0; c < 32; c += 4) {
+                        if constexpr (F8) {
+                            const float4 m = *reinterpret_cast<const float4 *>(factor + c0 + c);
+                            sum[c0 + c] = __fmaf_rn(v[c], m.x, sum[c0 + c]);
+                            sum[c0 + c + 1] = __fmaf_rn(v[c + 1], m.y, sum[c0 + c + 1]);
+                            sum[c0 + c + 2] = __fmaf_rn(v[c + 2], m.z, sum[c0 + c + 2]);
+                            sum[c0 + c + 3] = __fmaf_rn(v[c + 3], m.w, sum[c0 + c + 3]);
+                        } else {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) sum[c0 + c + i] += v[c + i];
-                            }
+                            for (int i = 0; i < 4; ++i) sum[c0 + c + i] += v[c + i];
                         }
                     }
                 }
-                acc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.acc_empty[acc.slot]);
-                acc.next(kAccs);
             }
-        } else if (k0 < k1) {
-            ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[0], 0, &s.abort, a.status, k1 - k0));
-            acc_fence_after();
+            acc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.acc_empty[acc.slot]);
+            acc.next(kAccs);
         }
     }
     __syncwarp();
@@ -359,16 +352,8 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
                 const int c0 = cb + i0;
                 if (c0 >= n) break;
                 float v[32];
-                if constexpr (SUMS) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = sum[i0 + c];
-                } else if (k0 < k1) {
-                    acc_load32(lanes + c0, v);
-                    acc_load_wait(v);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-                }
+                for (int c = 0; c < 32; ++c) v[c] = sum[i0 + c];
                 if (S == 1) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
@@ -420,16 +405,16 @@ __global__ void __launch_bounds__(Thin<F8, SUMS, BT>::kThreads)
     }
 }
 
-template <bool F8, bool SUMS, bool MN, int BT>
+template <bool F8, bool MN, int BT>
 tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
 {
-    using F = Thin<F8, SUMS, BT>;
+    using F = Thin<F8, BT>;
     constexpr size_t kStage = kTall + BT * 128;
-    static_assert(F::stages(1) * kStage + 1024 + sizeof(ThinSmem<F8, SUMS, BT>) <= 227 * 1024 && F::stages(1) <= kMaxStages, "shared memory");
-    static_assert(F::kCtas == 1 || F::kCtas * (F::stages(F::kCtas) * kStage + sizeof(ThinSmem<F8, SUMS, BT>) + 2048) <= 228 * 1024,
+    static_assert(F::stages(1) * kStage + 1024 + sizeof(ThinSmem<F8, BT>) <= 227 * 1024 && F::stages(1) <= kMaxStages, "shared memory");
+    static_assert(F::kCtas == 1 || F::kCtas * (F::stages(F::kCtas) * kStage + sizeof(ThinSmem<F8, BT>) + 2048) <= 228 * 1024,
                   "shared memory");
     static_assert(F::kCtas * F::kAccs * BT <= 512, "tensor memory");
-    const void *k = (const void *)thin_kernel<F8, SUMS, MN, BT>;
+    const void *k = (const void *)thin_kernel<F8, MN, BT>;
     static std::once_flag once[kMaxDevices];
     static bool good[kMaxDevices];
     int d = 0;
@@ -477,13 +462,9 @@ tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool
 tm_status thin_product(const Product &p, const DevInfo &dev, cudaStream_t s, bool pdl)
 {
     const bool few = p.T <= 32 * (int64_t)p.E;
-    if (p.kind == kProductE4M3)
-        return few ? launch_thin<true, true, false, 32>(p, dev, s, pdl) : launch_thin<true, true, false, 128>(p, dev, s, pdl);
-    if (p.w_mn)  // always to 16 bits
-        return few ? launch_thin<false, false, true, 32>(p, dev, s, pdl) : launch_thin<false, false, true, 128>(p, dev, s, pdl);
-    if (p.otype == TM_F32)
-        return few ? launch_thin<false, true, false, 32>(p, dev, s, pdl) : launch_thin<false, true, false, 128>(p, dev, s, pdl);
-    return few ? launch_thin<false, false, false, 32>(p, dev, s, pdl) : launch_thin<false, false, false, 128>(p, dev, s, pdl);
+    if (p.kind == kProductE4M3) return few ? launch_thin<true, false, 32>(p, dev, s, pdl) : launch_thin<true, false, 128>(p, dev, s, pdl);
+    if (p.w_mn) return few ? launch_thin<false, true, 32>(p, dev, s, pdl) : launch_thin<false, true, 128>(p, dev, s, pdl);
+    return few ? launch_thin<false, false, 32>(p, dev, s, pdl) : launch_thin<false, false, 128>(p, dev, s, pdl);
 }
 
 }  // namespace libtm

@@ -56,10 +56,9 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 }
 
 // Wait for a phase of `b`.  False after the limit, or once any role of this CTA has
-// given up; the first to give up records it.  Whoever waits for a whole sum allows 40000
-// cycles more for each of its stages, which take some hundreds.
+// given up; the first to give up records it.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool role_wait(uint64_t *b, uint32_t parity, int *abort_flag, unsigned *status, int stages = 0)
+__device__ __forceinline__ bool role_wait(uint64_t *b, uint32_t parity, int *abort_flag, unsigned *status)
 {
     const uint32_t bar = smem_u32(b);
     auto look = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
@@ -67,7 +66,7 @@ __device__ __forceinline__ bool role_wait(uint64_t *b, uint32_t parity, int *abo
     const long long t0 = clock64();
     while (!look()) {
         if (*(volatile const int *)abort_flag != 0) return false;
-        if (clock64() - t0 > kWaitCycles + 40000LL * stages) {
+        if (clock64() - t0 > kWaitCycles) {
             atomicOr(status, kStatusTimeout);
             *(volatile int *)abort_flag = 1;
             return false;
@@ -285,7 +284,7 @@ __device__ __forceinline__ void add_columns(uint32_t at, uint64_t *s, uint64_t m
 #undef TM_ADD
 }
 
-// 16-bit operands to fp32 outputs: how much of a sum the tensor cores add before it leaves them.
+// 16-bit operands: how much of a sum the tensor cores add before it leaves them.
 constexpr int kRunSums = 512;
 
 // ---------------------------------------------------------------- joins

@@ -8,7 +8,7 @@
 // One kernel: out[c, r] = sum_s wide[c, s] tall[r, s], a tile 256 of r by up to 256 of c,
 // shared by a CTA pair (tcgen05 cta_group::2: each CTA stages its 128 of the tall operand
 // and half of the wide one, 32 KB a stage of 64 of the sum, six stages; two
-// accumulators of 256 columns, so that one tile's output overlaps the next tile's sum).
+// accumulators of 256 columns, so that one run's addition and one tile's output overlap the next one's products).
 // The tall operand (r) runs along the tensor memory's lanes and c along its columns, so
 // that a warp's 32 lanes hold 32 neighbours of an output row: outputs leave as coalesced
 // stores of 64 or 128 bytes with no way through shared memory, whatever their
@@ -31,14 +31,13 @@
 namespace libtm {
 namespace {
 
-// Warp 0 copies, 1 multiplies, 8 warps make outputs, one clears rows.  fp32 outputs: sums leave the tensor
+// Warp 0 copies, 1 multiplies, 2 clears rows, 4 to 11 make outputs.  Sums leave the tensor
 // cores every kRunSums and are added in registers (tm_thin.cu says why), 128 a thread of the output warps,
 // which so are whole warpgroups and take registers from the others: 4 warps of 96 and 8 of 200 are
-// 63488, of the 64512 that 384 threads of 168 start with.
-template <bool SUMS>
-struct Warps {
-    static constexpr int kOut = SUMS ? 4 : 2, kClear = SUMS ? 2 : 10, kThreads = SUMS ? 384 : 352;
-};
+// 63488, of the 64512 that 384 threads of 168 start with.  To 16 bits, cold, against sums that stay in the
+// tensor cores: 8192 x 4096 x 4096 146 us either way, its gradients 146 and 164 (146 and 163); weights' gradient of
+// 64 experts of 2048 x 2048, 128 rows each, 110 (107), 32 rows each 105 (101).
+constexpr int kWideThreads = 384, kClear = 2, kOut = 4;
 constexpr int kFewRegs = 96, kManyRegs = 200;
 constexpr int kRun = kRunSums / 64;  // stages
 constexpr int kStages = 6;
@@ -126,12 +125,11 @@ struct Walk {
 
 // SPLIT (weights' gradient): a cluster of S pairs (2 or 4) has one tile, each pair its part of the sum.
 template <int MODE, typename O, bool SPLIT>
-__global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
+__global__ void __launch_bounds__(kWideThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap mtall, const __grid_constant__ CUtensorMap mwide,
                 const __grid_constant__ CUtensorMap mwide_all, const WideArgs a, const int pairs)
 {
-    constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeights, SUMS = sizeof(O) == 4;
-    using Ws = Warps<SUMS>;
+    constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeights;
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     __shared__ WideSmem s;
@@ -167,9 +165,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
     Walk<MODE> walk(a, s.x, pair, S);
 
     // in the branches themselves: behind one of its own the compiler counts on the smaller share everywhere
-    auto fewer_registers = [] {
-        if constexpr (SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-    };
+    auto fewer_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs)); };
     if (warp == 0) {
         fewer_registers();
         {
@@ -262,8 +258,8 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                 const Tile w = walk.at(item);
                 const uint32_t id = a.id | ((B_MN ? (uint32_t)a.width : (uint32_t)((w.n + 63) / 64 * 64)) >> 3) << 17;
                 for (int k = w.kb; ok && k < w.ke;) {
-                    // a run of the sum into the next accumulator: all of it, or kRun stages
-                    const int end = SUMS && w.ke - k > kRun ? k + kRun : w.ke;
+                    // a run of the sum into the next accumulator
+                    const int end = w.ke - k > kRun ? k + kRun : w.ke;
                     ok = runs < 2 || warp_wait(&s.acc_empty[acc.slot], acc.phase ^ 1u, &s.abort, a.status);
                     const uint32_t d = tmem + acc.slot * 256;
                     bool add = false;
@@ -298,10 +294,10 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
             __syncwarp();
             mbar_wait_bounded(smem_u32(&s.done), 0);
         }
-    } else if (warp >= Ws::kOut && warp < Ws::kOut + 8) {
-        if constexpr (SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    } else if (warp >= kOut) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         // two warps a 32 lanes: one takes the even runs of 32 columns, the other the odd
-        const int q = warp & 3, odd = (warp - Ws::kOut) >> 2;
+        const int q = warp & 3, odd = (warp - kOut) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t free0 = cluster_addr(smem_u32(&s.acc_empty[0]), even), free1 = cluster_addr(smem_u32(&s.acc_empty[1]), even);
         O *out = reinterpret_cast<O *>(a.out);
@@ -313,7 +309,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
             O *const first = out + ((MODE == kWeights ? (int64_t)w.e * a.C : 0) + w.c0) * a.ldo + r;
             bool ok = true;
             auto ready = [&] {
-                ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status, SUMS ? 0 : w.steps));
+                ok = __all_sync(0xffffffffu, role_wait(&s.acc_full[acc.slot], acc.phase, &s.abort, a.status));
                 acc_fence_after();
                 return ok;
             };
@@ -341,17 +337,30 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                     }
                 }
             };
-            // SPLIT: the parts of the sum meet; get(i, v): this pair's columns 32 odd + 64 i on
-            auto join = [&](auto get) {
-                const int own = pair * (4 / S), mine = warp - Ws::kOut;
-                if (warp == Ws::kOut && lane == 0) {
+            uint64_t sum[64];  // runs of 32 columns, pairs of them
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sum[i] = 0;
+            auto get = [&](int i, float(&v)[32]) {  // columns 32 odd + 64 i on
+#pragma unroll
+                for (int c = 0; c < 16; ++c) unpack2(sum[16 * i + c], v[2 * c], v[2 * c + 1]);
+            };
+            const uint64_t one = pack2(1.0f, 1.0f);
+            for (int k = w.kb; k < w.ke && ready(); k += kRun) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (64 * i < a.width) add_columns(lanes + acc.slot * 256 + 32 * odd + 64 * i, sum + 16 * i, one);
+                give_back();
+            }
+            if constexpr (SPLIT) {  // the parts of the sum meet
+                const int own = pair * (4 / S), mine = warp - kOut;
+                if (warp == kOut && lane == 0) {
                     uint32_t runs = 0;
                     for (int i = 0; i < 4 / S; ++i) runs += (64 * (own + i) < w.n) + (64 * (own + i) + 32 < w.n);
                     mbar_expect(&s.inbox, runs * (uint32_t)S * 16384u);
                 }
                 __syncwarp();
                 cluster_sync();  // every ring is done with, every inbox ready
-                if (!ok) return;
+                if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (32 * odd + 64 * i < w.n) {
@@ -360,7 +369,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                         join_push(v, smem_u32(ring), &s.inbox, pair, mine, i, S, rank);
                     }
                 ok = __all_sync(0xffffffffu, role_wait<true>(&s.inbox, 0, &s.abort, a.status));
-                if (!ok) return;
+                if (!ok) break;
                 pdl_wait();
                 for (int i = own; i < own + 4 / S; ++i)
                     if (32 * odd + 64 * i < w.n) {
@@ -368,85 +377,25 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
                         join_sum(v, ring, mine, i, S);
                         store(v, 32 * odd + 64 * i);
                     }
-            };
-            if constexpr (SUMS) {
-                uint64_t sum[64];  // runs of 32 columns, pairs of them
-#pragma unroll
-                for (int i = 0; i < 64; ++i) sum[i] = 0;
-                const uint64_t one = pack2(1.0f, 1.0f);
-                for (int k = w.kb; k < w.ke && ready(); k += kRun) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (64 * i < a.width) add_columns(lanes + acc.slot * 256 + 32 * odd + 64 * i, sum + 16 * i, one);
-                    give_back();
-                }
-                if constexpr (SPLIT) {
-                    join([&](int i, float(&v)[32]) {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) unpack2(sum[16 * i + c], v[2 * c], v[2 * c + 1]);
-                    });
-                    break;
-                }
-                if (!ok) break;
-                if (!waited) pdl_wait();
-                waited = true;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (32 * odd + 64 * i < w.n) {
-                        float v[32];
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) unpack2(sum[16 * i + c], v[2 * c], v[2 * c + 1]);
-                        store(v, 32 * odd + 64 * i);
-                    }
-            } else {
-                if constexpr (SPLIT) {
-                    if (w.kb < w.ke) ready();
-                    join([&](int i, float(&v)[32]) {
-                        if (w.kb < w.ke) {
-                            acc_load32(lanes + 32 * odd + 64 * i, v);
-                            acc_load_wait(v);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-                        }
-                    });
-                    break;
-                }
-                if (w.steps > 0 && !ready()) break;
-                if (!waited) pdl_wait();
-                waited = true;
-                if (w.steps > 0) {
-                    // the next run on its way while one is stored
-                    const uint32_t at = lanes + acc.slot * 256;
-                    float v0[32], v1[32];
-                    acc_load32(at + 32 * odd, v0);
-#pragma unroll 1
-                    for (int c0 = 32 * odd; c0 < w.n; c0 += 128) {
-                        acc_load_wait(v0);
-                        if (c0 + 64 < w.n) acc_load32(at + c0 + 64, v1);
-                        store(v0, c0);
-                        if (c0 + 64 >= w.n) break;
-                        acc_load_wait(v1);
-                        if (c0 + 128 < w.n) acc_load32(at + c0 + 128, v0);
-                        store(v1, c0 + 64);
-                    }
-                    acc_load_wait(v0);
-                    give_back();
-                } else {
-                    float v[32];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-#pragma unroll 1
-                    for (int c0 = 32 * odd; c0 < w.n; c0 += 64) store(v, c0);
-                }
+                break;
             }
+            if (!ok) break;
+            if (!waited) pdl_wait();
+            waited = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (32 * odd + 64 * i < w.n) {
+                    float v[32];
+                    get(i, v);
+                    store(v, 32 * odd + 64 * i);
+                }
         }
     } else {
         fewer_registers();
         // rows past an expert's end, up to the next 16 of the sum, in the stage that holds its last rows
         Turn t;
         uint32_t parity = 0;
-        for (int item = unit; MODE == kWeights && warp == Ws::kClear && item < items; item += units) {
+        for (int item = unit; MODE == kWeights && warp == kClear && item < items; item += units) {
             const Tile w = walk.at(item);
             if (w.kb == w.ke) continue;
             for (int k = w.kb; k + 1 < w.ke; ++k) t.next(kStages);
@@ -469,7 +418,7 @@ __global__ void __launch_bounds__(Warps<sizeof(O) == 4>::kThreads, 1)
         }
     }
     __syncwarp();
-    if (SPLIT && unit < items && !(warp >= Ws::kOut && warp < Ws::kOut + 8)) cluster_sync();  // the joins' own
+    if (SPLIT && unit < items && warp < kOut) cluster_sync();  // the joins' own
     pdl_wait();
     acc_fence_before();
     __syncthreads();
@@ -505,7 +454,7 @@ tm_status instance(const Instance **out)
         for (int S = 2; i.good && SPLIT && S <= 4; S *= 2) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(2 * S);
-            cfg.blockDim = dim3(Warps<sizeof(O) == 4>::kThreads);
+            cfg.blockDim = dim3(kWideThreads);
             cfg.dynamicSmemBytes = kWideSmem;
             cudaLaunchAttribute attr;
             attr.id = cudaLaunchAttributeClusterDimension;
@@ -531,7 +480,7 @@ tm_status launch_pairs(const CUtensorMap &tall, const CUtensorMap &wide, const C
     void *args[] = {const_cast<CUtensorMap *>(&tall), const_cast<CUtensorMap *>(&wide), const_cast<CUtensorMap *>(&all),
                     const_cast<WideArgs *>(&a), &S};
     return launch_kernel((const void *)wide_kernel<MODE, O, SPLIT>, dim3((unsigned)(2 * S * units)),
-                         dim3(Warps<sizeof(O) == 4>::kThreads), args, kWideSmem, s, pdl, (unsigned)(2 * S));
+                         dim3(kWideThreads), args, kWideSmem, s, pdl, (unsigned)(2 * S));
 }
 
 // steps: stages of an average sum (weights' gradient).  Few long sums are shared by pairs while all the
