@@ -131,28 +131,39 @@ __global__ void __launch_bounds__(kThreads) read_probe_fixed_kernel(const float 
 
 }  // namespace
 
+namespace {
+
+// A driver call looked up through the runtime; nullptr where there is none.
+template <typename F>
+F driver_call(const char *name, unsigned version)
+{
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+        return reinterpret_cast<F>(p);
+    cudaGetLastError();
+    return nullptr;
+}
+
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
-    // The driver's call wants a context of the calling thread, which a thread has after its first
-    // runtime call that needs one -- perhaps the launch below this.
-    static thread_local bool bound = false;
-    if (!bound) {
-        int dev = 0;
-        bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
-        if (!bound) cudaGetLastError();
-    }
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static PFN_cuCtxGetCurrent_v4000 current = nullptr;
     std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        else
-            cudaGetLastError();
+        fn = driver_call<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled", 12000);
+        current = driver_call<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent", 4000);
     });
+    // The driver's call wants a context of the calling thread.  A thread whose first call needs one may
+    // have none yet; one that the caller made current stays.
+    CUcontext ctx = nullptr;
+    if (current == nullptr || current(&ctx) != CUDA_SUCCESS || ctx == nullptr) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) cudaGetLastError();
+    }
     return fn;
 }
 
