@@ -246,3 +246,18 @@ def test_the_same_bits_every_time_and_from_a_graph(cuda, counts):
     graph.replay()
     torch.cuda.synchronize()
     assert bool((outs[0] == 3.0).all()) and not outs[2].any()
+
+
+@pytest.mark.parametrize("T", [4, 900])
+def test_rows_that_hold_an_infinity_or_a_nan(cuda, T):
+    # an infinity times a weight, or times 0; the rest of such a row's sum is finite
+    c = Case([T // 2, T - T // 2], 136, 200, "bf16", seed=1, ints=True)
+    c.x[0, 3], c.dy[0, 5], c.x[T - 1, 3], c.dy[T - 1, 5] = float("inf"), float("-inf"), float("nan"), float("nan")
+    y, (dx, _) = c.forward("f32"), c.backward("f32", weights=False)
+    tm.tm_check()
+    for got, sign, w in ((y, 1.0, c.w64[0, :, 3]), (dx, -1.0, c.w64[0, 5])):
+        got = got.double().cpu().numpy()
+        assert (w == 0).any() and (w != 0).any()
+        assert np.isnan(got[0][w == 0]).all()
+        assert np.array_equal(got[0][w != 0], sign * np.sign(w[w != 0]) * np.inf)
+        assert np.isnan(got[T - 1]).all()
