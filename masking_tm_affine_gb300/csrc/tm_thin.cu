@@ -443,7 +443,7 @@ tm_status launch_thin(const Product &p, const DevInfo &dev, cudaStream_t s, bool
     // tiles: at least one for each expert that has rows (how many have is not known here), and no more than `most`
     const int64_t busy = p.E < p.T ? p.E : p.T, rt = (p.T + BT - 1) / BT;
     const int64_t tiles = (rt > busy ? rt : busy) * a.ftiles, most = (p.starts == nullptr ? rt : rt + busy) * a.ftiles;
-    if (most > (1 << 28)) return TM_ERR_UNSUPPORTED_TILE;
+    if (most > (1 << 30)) return TM_ERR_UNSUPPORTED_TILE;
     // S CTAs a tile, up to two an SM in all.  32 tiles of a 4096 x 4096 matrix in 8 bits, 16 rows: S 1
     // 21.5 us, 2 18.6, 4 15.0, 8 14.8; 128 rows: 35.8, 35.6, 25.0, 47.6
     int S = 1;

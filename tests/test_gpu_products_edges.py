@@ -320,3 +320,17 @@ def test_clipping_past_2_to_31_elements(cuda):
     assert abs(float(norm) - want) <= 18 * 2.0 ** -24 * want
     for i in (0, 1 << 31, n - 1):
         assert abs(float(t[i]) - (3.0 if i == n - 1 else 2.0 ** -10) / want) <= 2.0 ** -8 * 3.0 / want
+
+
+def test_as_many_tiles_as_are_allowed(cuda):
+    # few rows an expert, and more than 2^28 tiles of 128 columns: 2^30 is the limit
+    E, N = 16, 2_040_000_000
+    if torch.cuda.mem_get_info()[0] < 80e9:
+        pytest.skip("64 GB of outputs")
+    y = torch.empty(E, N, dtype=torch.bfloat16, device="cuda")
+    y[0].fill_(7.0)
+    y[1:, ::4_000_000] = 7.0
+    starts = torch.tensor([0] * E + [1], dtype=torch.int32, device="cuda")     # one row, the last expert's
+    tm.tm_gemm_experts(None, 0, None, 0, y, N, starts, E, E, N, 0)             # the sum of nothing
+    tm.tm_check()
+    assert not y[0].any() and bool((y[1:, ::4_000_000] == 7.0).all())
