@@ -636,8 +636,8 @@ tm_status tm_kv4_attention(const void *Q, int64_t qs_tok, int64_t qs_head, void 
  * Rows sorted by expert.  E experts share one call: expert e has rows starts[e] ..
  * starts[e+1] - 1 of the T rows (device int32 [E + 1], non-decreasing, within 0 .. T),
  * none, one or many.  Rows before starts[0] and from starts[E] on belong to nobody:
- * they would produce stays as it was.  An expert whose borders fall or leave 0 .. T is taken as
- * empty, and the next tm_check returns TM_ERR_INDEX.  starts == NULL with E == 1: one
+ * the output rows they would produce stay as they were.  An expert whose borders fall, leave
+ * 0 .. T or lie before an earlier one is taken as empty, and the next tm_check returns TM_ERR_INDEX.  starts == NULL with E == 1: one
  * matrix for all rows.  E <= 1024.
  * Operands that are multiplied start on 16-byte boundaries and have row strides
  * of whole 16 bytes (tm_row_stride; any extents): MISALIGNED otherwise.  Outputs need
