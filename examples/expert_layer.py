@@ -122,6 +122,16 @@ def serve(T=24, H=512, F=640, E=8, k=2, steps=3, seed=0, dev="cuda"):
 
 
 # ------------------------------------------------------------------ trained in 16 bits
+def first_derivatives(backward):
+    """A backward pass that cannot be differentiated itself, and so refuses to be part of a graph (create_graph=True).
+    Marked once_differentiable it would be cut off without an error where torch.autograd.grad is given its inputs."""
+    def run(ctx, *grads):
+        if torch.is_grad_enabled():
+            raise RuntimeError("only first derivatives: call it without create_graph")
+        return backward(ctx, *grads)
+    return run
+
+
 class Experts(torch.autograd.Function):
     """rows [T, K], matrices [E, N, K], borders -> [T, N]"""
 
@@ -134,11 +144,12 @@ class Experts(torch.autograd.Function):
         return y
 
     @staticmethod
+    @first_derivatives
     def backward(ctx, dy):
         x, w, starts = ctx.saved_tensors
         (E, N, K), T = w.shape, x.shape[0]
         dy = dy.contiguous()
-        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        dx, dw = (torch.empty_like(t) if need else None for t, need in zip((x, w), ctx.needs_input_grad))
         tm.tm_gemm_experts_bwd(dy, N, x, K, w, K, dx, K, dw, K, starts, E, T, N, K, CODE, CODE)
         return dx, dw, None
 
@@ -153,14 +164,15 @@ class Norm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @first_derivatives
     def backward(ctx, dy):
         x, w, rstd = ctx.saved_tensors
         T, H = x.shape
-        dy, dx, dw = dy.contiguous(), torch.empty_like(x), torch.empty_like(w)
+        dy, dx, dw = dy.contiguous(), torch.empty_like(x), torch.empty_like(w) if ctx.needs_input_grad[1] else None
         need = tm.tm_rmsnorm_bwd_workspace_bytes(T, H)
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
         tm.tm_rmsnorm_bwd(dy, H, x, H, w, rstd, None, 0, dx, H, dw, T, H, CODE, CODE, ws, need)
-        return dx, dw
+        return dx if ctx.needs_input_grad[0] else None, dw
 
 
 class Clip:

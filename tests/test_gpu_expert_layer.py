@@ -40,3 +40,44 @@ def test_gradients_and_their_clipping(layer, T, H, F, E, k):
         factor = min(1.0, max_norm / (float(total) + 1e-6))
         for g, w in zip(grads, wide):
             assert float((g.double() - factor * w).norm()) <= 16 * 2.0 ** -9 * factor * float(w.norm())
+
+
+def test_second_derivatives_are_refused(layer):
+    # a gradient of a gradient has terms that these functions do not make: an error, not a wrong number
+    x = torch.randn(6, 64, device="cuda").bfloat16().requires_grad_()
+    w = torch.randn(2, 64, 64, device="cuda").bfloat16().requires_grad_()
+    n = torch.ones(64, device="cuda").bfloat16().requires_grad_()
+    starts = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    for y, leaves in ((layer.Experts.apply(x, w, starts), (x, w)), (layer.Norm.apply(x, n), (x, n))):
+        with pytest.raises(RuntimeError):
+            first = torch.autograd.grad((y.float() ** 2).sum(), leaves, create_graph=True)
+            penalty = sum(g.float().pow(2).sum() for g in first) + sum(t.float().pow(2).sum() for t in leaves)
+            torch.autograd.grad(penalty, leaves)
+
+
+def test_only_the_gradients_that_are_asked_for(layer, monkeypatch):
+    x, w = torch.randn(6, 64, device="cuda").bfloat16(), torch.randn(2, 64, 64, device="cuda").bfloat16()
+    starts = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    made, call = [], layer.tm.tm_gemm_experts_bwd
+
+    def spy(*a):
+        made.append((a[6] is not None, a[8] is not None))
+        return call(*a)
+    monkeypatch.setattr(layer.tm, "tm_gemm_experts_bwd", spy)
+    grads = []
+    for rows, weights in ((True, True), (True, False), (False, True)):
+        leaves = [t.clone().requires_grad_(need) for t, need in ((x, rows), (w, weights))]
+        layer.Experts.apply(*leaves, starts).float().sum().backward()
+        grads.append([t.grad for t in leaves])
+        assert made[-1] == (rows, weights)
+    assert grads[1][1] is None and grads[2][0] is None
+    assert torch.equal(grads[0][0], grads[1][0]) and torch.equal(grads[0][1], grads[2][1])
+    made.clear()
+    norm, back = [], layer.tm.tm_rmsnorm_bwd
+    monkeypatch.setattr(layer.tm, "tm_rmsnorm_bwd", lambda *a: (norm.append(a[10] is not None), back(*a))[1])
+    for weights in (True, False):
+        g, n = x.clone().requires_grad_(), torch.ones(64, device="cuda").bfloat16().requires_grad_(weights)
+        layer.Norm.apply(g, n).float().sum().backward()
+        assert norm[-1] is weights and (n.grad is not None) is weights
+        grads.append(g.grad)
+    assert torch.equal(grads[-1], grads[-2])
