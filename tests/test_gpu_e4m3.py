@@ -258,3 +258,51 @@ def test_norm_quantise_multiply(cuda):
     n = x.double() / (x.double().pow(2).mean(1, keepdim=True) + 1e-5).sqrt()
     full = n @ w1.double().T @ w2.double().T
     assert float((y.double() - full).norm() / full.norm()) < 4 * 2.0 ** -4
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("shape", [(128, 768), (40, 767), (130, 770)])
+def test_small_blocks_of_bf16(cuda, rows, shape):
+    # tops below 2^-100, where 448 / top nears or passes fp32's range, down to bf16's least value
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(*shape, generator=g)
+    for j, s in enumerate((2.0 ** -133, 2.0 ** -126, 2.0 ** -119, 2.0 ** -110, 2.0 ** -102, 2.0 ** -99)):
+        x[:, 128 * j:128 * j + 128] *= s
+    x = x.bfloat16().cuda()
+    check_quant(x, *quant(x, "bf16", rows), rows)
+
+
+@pytest.mark.parametrize("counts,N,K", [([5, 0, 9], 264, 200), ([300, 77, 150], 384, 260), ([200], 130, 1000)])
+def test_gradient_of_the_rows(cuda, counts, N, K):
+    # y = x W^T in 8 bits has dx = dy W: the same product with the transposed codes and scales of W
+    E, T = len(counts), sum(counts)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    w, dy = (torch.randn(*s, generator=g, device="cuda").bfloat16() for s in ((E, N, K), (T, N)))
+    KB, NB, ldk, ldn = -(-K // 128), -(-N // 128), ref.padded(K, 1), ref.padded(N, 1)
+    q, sb = torch.zeros(E, N, ldk, dtype=torch.uint8, device="cuda"), torch.empty(E, NB, KB, device="cuda")
+    for e in range(E):
+        tm.tm_quant_e4m3(w[e], K, N, K, q[e], ldk, sb[e], 128, tm.TM_BF16)
+    qt = torch.zeros(E, K, ldn, dtype=torch.uint8, device="cuda")
+    qt[..., :N] = q[..., :K].transpose(1, 2)
+    st = sb.transpose(1, 2).contiguous()
+    a, sa = torch.zeros(T, ldn, dtype=torch.uint8, device="cuda"), torch.empty(T, NB, device="cuda")
+    tm.tm_quant_e4m3(dy, N, T, N, a, ldn, sa, 1, tm.TM_BF16)
+    dx, starts = torch.full((T, K), 7.0, device="cuda"), [sum(counts[:e]) for e in range(E + 1)]
+    tm.tm_gemm_e4m3(a, ldn, sa, 128, qt, ldn, st, dx, K, ref.starts_of(counts), E, T, K, N)
+    tm.tm_check()
+    value = lambda c, s, n, b: c[..., :n].contiguous().view(E4M3).double().cpu().numpy() * ref.stretched(  # noqa: E731
+        s.double().cpu().numpy(), c.shape[-2], n, b)
+    wv, dv = value(q, sb, K, 128), value(a, sa, N, 1)
+    want, size = ref.forward(dv, wv.transpose(0, 2, 1), starts)
+    ref.check(dx, want, size, ref.block_bound(N), torch.float32)
+    # codes are within 2^-4 of their values, or 2^-10 of a code where they are smallest: x 2^-4 + top / 448 2^-10
+    err = lambda v, t: np.abs(v) * 2.0 ** -4 + t * 2.0 ** -10 / 448  # noqa: E731
+    w64, d64 = w.double().cpu().numpy(), dy.double().cpu().numpy()
+    top_w = ref.stretched(sb.double().cpu().numpy(), N, K, 128) * 448
+    top_d = ref.stretched(sa.double().cpu().numpy(), T, N, 1) * 448
+    assert np.all(np.abs(wv - w64) <= err(w64, top_w) * (1 + 1e-6)) and np.all(np.abs(dv - d64) <= err(d64, top_d) * (1 + 1e-6))
+    full, _ = ref.forward(d64, w64.transpose(0, 2, 1), starts)
+    sizes, _ = ref.forward(np.abs(d64) + err(d64, top_d), (np.abs(w64) + err(w64, top_w)).transpose(0, 2, 1), starts)
+    plain, _ = ref.forward(np.abs(d64), np.abs(w64).transpose(0, 2, 1), starts)
+    got = dx.double().cpu().numpy()
+    assert np.all(np.abs(got - full) <= sizes - plain + ref.block_bound(N) * sizes + 2.0 ** -24 * np.abs(full))
