@@ -709,7 +709,8 @@ tm_status tm_gemm_experts_bwd(const void *DY, int64_t lddy, const void *X, int64
 
 /*
  * Gradients clipped by their norm together: norm = sqrt(sum g^2) over any number of
- * tensors, out = g * min(1, max_norm / (norm + eps)), rounded once to g's type.
+ * tensors, out = g * min(1, max_norm / (norm + eps)): the factor rounded to fp32 (it loses
+ * bits below 2^-126), the product to g's type.
  *
  * tm_clip_plan -- fills the HOST buffer plan (tm_clip_chunks(sizes, n) entries of
  * TM_CLIP_CHUNK_BYTES) for n contiguous tensors: device pointers grads[i], outs[i]
@@ -721,11 +722,11 @@ tm_status tm_gemm_experts_bwd(const void *DY, int64_t lddy, const void *X, int64
  *
  * tm_clip_grads -- one step:
  *   plan, chunks   the device copy
- *   max_norm   >= 0; infinity: no clipping, and none where norm + eps is 0.  With factor 1 a
- *              gradient in place is not written
+ *   max_norm   >= 0; infinity: no clipping whatever the norm is, a NaN too, and none where
+ *              norm + eps is 0.  With factor 1 a gradient in place is not written
  *   norm       output, one fp32 on the device.  It is right wherever fp32 holds it: squares
  *              beyond fp32's range are added in 64 bits.  A NaN or infinite gradient makes
- *              it so; then out = g * NaN, or g * 0
+ *              it so; then, with a finite max_norm, out = g * NaN, or g * 0
  *   workspace  tm_clip_workspace_bytes() bytes, 16-byte aligned, in use until the
  *              call's kernels finish
  * The same tensors give the same bits.  Errors: INVALID_ARG, MISALIGNED, WORKSPACE, CUDA.

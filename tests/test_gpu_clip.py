@@ -161,3 +161,18 @@ def test_many_tensors_the_same_bits_and_a_graph(cuda):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(c.norm, norm) and all(torch.equal(a[:n], b[:n]) for a, b, n in zip(c.outs, outs, c.sizes))
+
+
+@pytest.mark.parametrize("outs", ["new", "place"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_no_clipping_whatever_the_norm_is(cuda, outs, bad):
+    # an infinite max_norm comes first: the gradients stay as they are, and the norm tells what they hold
+    t = tensors([40000, 300], ["f32", "bf16"])
+    t[1][7] = bad
+    c = Clip(t, outs)
+    c.run(float("inf"))
+    tm.tm_check()
+    assert str(float(c.norm)) == str(bad)
+    for o, b, n in zip(c.outs, c.before, c.sizes):
+        kept = torch.isnan(b) if math.isnan(bad) else torch.zeros_like(b, dtype=torch.bool)
+        assert bool((torch.isnan(o[:n]) == torch.isnan(b)).all()) and torch.equal(o[:n][~kept], b[~kept])
