@@ -670,7 +670,7 @@ tm_status tm_quant_e4m3(const void *X, int64_t ldx, int64_t M, int64_t N, void *
  * Products of codes are exact and summed in fp32 over a block of 128, and the blocks in
  * fp32 after their scales: |error| <= (128 + ceil(K / 128) + 9) 2^-23 * sum |sa sb A B|, plus the
  * output's own rounding.  The two scales of a block are multiplied first, in fp32 (below
- * 2^-126 that product loses bits).  The gradient of the rows is the same call with
+ * 2^-126 that product loses bits, from 2^128 on it is infinite).  The gradient of the rows is the same call with
  * the transposed codes and scales of B.
  * Errors: INVALID_ARG, UNSUPPORTED_TILE (group, E, extents beyond 2^31 - 513 or 2^30
  *         tiles), MISALIGNED, CUDA; INDEX and TIMEOUT through tm_check.

@@ -13,6 +13,9 @@
 // sum in 64 bits.  Where such a part leaves 2^-80 .. 2^100 (squares below it lose
 // bits, above it nears infinity) it is made again in 64 bits, so that a norm is right for
 // any gradients whose norm fp32 holds, however small or large.
+//
+// A gradient off 16 bytes, or whose output is, goes element by element, and one square at a time joins in 64
+// bits (300 M elements in 16 bits to another buffer: 288 us, all odd 2080, only the outputs 1030; in 32 bits 563, 2140, 1190).
 #include "tm_host.h"
 #include "tm_elem.cuh"
 
@@ -208,7 +211,8 @@ __device__ __forceinline__ void scale(const Chunk &c, float f)
         chunk_scale<__nv_bfloat16>(c, f);
 }
 
-// The factor and the norm, of the whole sum.  A NaN stays one; nothing at all is not clipped.
+// The factor and the norm, of the whole sum.  An infinite max_norm or nothing at all: no clipping; else a NaN
+// stays one.
 __device__ __forceinline__ float clip_factor(double sum, const ClipArgs &a, float *norm)
 {
     const double root = sqrt(sum), size = root + (double)a.eps, ratio = (double)a.max_norm / size;
